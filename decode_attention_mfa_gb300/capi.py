@@ -19,7 +19,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "mfa.h")
 MFA_OK = 0
 STATUS_NAMES = {0: "MFA_OK", 1: "MFA_ERR_INVALID_ARG", 2: "MFA_ERR_UNSUPPORTED", 3: "MFA_ERR_CUDA",
                 4: "MFA_ERR_WORKSPACE", 5: "MFA_ERR_DEVICE_PAGE", 6: "MFA_ERR_DEVICE_CAPACITY",
-                7: "MFA_ERR_DEVICE_TIMEOUT"}
+                7: "MFA_ERR_DEVICE_TIMEOUT", 8: "MFA_ERR_DEVICE_NO_PAGES"}
 HEADS, HEAD_DIM, PAGE_SIZE, MAX_BATCH, MAX_QUERY_TOKENS = 64, 256, 64, 1024, 8
 
 _lock = threading.Lock()
@@ -38,6 +38,7 @@ class Plan(ctypes.Structure):
 
 
 _P, _I, _F, _Z, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_uint64
+_I64 = ctypes.c_int64
 _SIGNATURES = {
     "mfa_plan_decode": ([_I, _I, _I, ctypes.POINTER(Plan)], _I),
     "mfa_decode_workspace_bytes": ([_I, _I], _Z),
@@ -58,6 +59,10 @@ _SIGNATURES = {
     "mfa_decode_attention_blocks": ([_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _F, _I, _I, _I, _I, _P, _Z, _P], _I),
     "mfa_decode_attention_blocks_fp8": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _F, _I, _I, _I, _I, _P, _Z,
                                          _P], _I),
+    "mfa_kv_append_slots": ([_P, _P, _I64, _I64, _P, _I, _P, _P, _I, _P, _P], _I),
+    "mfa_kv_append_slots_fp8": ([_P, _P, _I64, _I64, _P, _I, _P, _P, _P, _P, _I, _P, _P], _I),
+    "mfa_reserve_pages": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P], _I),
+    "mfa_release_pages": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P], _I),
     "mfa_check_device_errors": ([_P, _I, _P], _I),
     "mfa_set_wait_budget_ns": ([_U64], None),
     "mfa_selftest_wait_timeout": ([_P, _U64, _P], _I),
@@ -268,6 +273,38 @@ def mfa_decode_attention_blocks_fp8(q, k_cache, v_cache, k_scale, v_scale, page_
                                                   _ptr(n_blocks), max_blocks, _ptr(out), _ptr(lse), float(scale),
                                                   batch, max_pages, num_pages, max_len_hint, _ptr(workspace),
                                                   workspace_bytes, _stream(stream)))
+
+
+def mfa_reserve_pages(n_new, seq_lens, page_table, free_pages, n_free, batch, max_pages, num_pages, max_new,
+                      new_starts, slot_map, seq_lens_out, n_free_out, workspace, stream=None):
+    """Pages, page-table entries and token slots for a step's new tokens; see include/mfa.h.
+    slot_map int64 [max_new], new_starts int32 [batch + 1]; seq_lens_out / n_free_out may be seq_lens / n_free."""
+    _check(load().mfa_reserve_pages(_ptr(n_new), _ptr(seq_lens), _ptr(page_table), _ptr(free_pages), _ptr(n_free),
+                                    batch, max_pages, num_pages, max_new, _ptr(new_starts), _ptr(slot_map),
+                                    _ptr(seq_lens_out), _ptr(n_free_out), _ptr(workspace), _stream(stream)))
+
+
+def mfa_release_pages(finished, keep_pages, seq_lens, page_table, free_pages, n_free, batch, max_pages, num_pages,
+                      seq_lens_out, n_free_out, workspace, stream=None):
+    """Pages of finished requests back to the free stack; keep_pages None keeps none."""
+    _check(load().mfa_release_pages(_ptr(finished), _ptr(keep_pages), _ptr(seq_lens), _ptr(page_table),
+                                    _ptr(free_pages), _ptr(n_free), batch, max_pages, num_pages, _ptr(seq_lens_out),
+                                    _ptr(n_free_out), _ptr(workspace), _stream(stream)))
+
+
+def mfa_kv_append_slots(k_new, v_new, k_stride, v_stride, slot_map, n_rows, k_cache, v_cache, num_pages, workspace,
+                        stream=None):
+    """Rows to the slots of slot_map (int64, negative: skipped); strides in elements."""
+    _check(load().mfa_kv_append_slots(_ptr(k_new), _ptr(v_new), k_stride, v_stride, _ptr(slot_map), n_rows,
+                                      _ptr(k_cache), _ptr(v_cache), num_pages, _ptr(workspace), _stream(stream)))
+
+
+def mfa_kv_append_slots_fp8(k_new, v_new, k_stride, v_stride, slot_map, n_rows, k_cache, v_cache, k_scale, v_scale,
+                            num_pages, workspace, stream=None):
+    """The same into an E4M3 cache with per-token fp32 scales."""
+    _check(load().mfa_kv_append_slots_fp8(_ptr(k_new), _ptr(v_new), k_stride, v_stride, _ptr(slot_map), n_rows,
+                                          _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), num_pages,
+                                          _ptr(workspace), _stream(stream)))
 
 
 def mfa_check_device_errors(workspace, clear: bool = True, stream=None):

@@ -162,7 +162,61 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
   if (threadIdx.x == 0) p.seq_lens[b] = start + p.n_new;
 }
 
+// Rows scattered to the slots of a slot map: one warp per row of K or of V, kRows
+// such items a warp, all of whose loads are in flight before the first store. No
+// row depends on another, so the call is bound by latency for a decode step's
+// rows and by memory bandwidth for a prefill's (read 1 KB, write 1 KB or 520 B a
+// token).
+constexpr int kSlotThreads = 128;
+template <int kRows>
+__global__ void __launch_bounds__(kSlotThreads) kv_append_slots_kernel(const AppendSlotsParams p) {
+  const int lane = threadIdx.x & 31;
+  const long long items = 2ll * p.n_rows;  // item i: row i / 2, K (even) or V (odd)
+  const long long i0 = ((long long)blockIdx.x * (kSlotThreads / 32) + (threadIdx.x >> 5)) * kRows;
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  uint4 row[kRows];
+  long long slot[kRows];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const long long i = i0 + j, r = i >> 1;
+    slot[j] = -1;
+    if (i < items) {
+      slot[j] = __ldcg(reinterpret_cast<const long long*>(p.slot_map) + r);
+      const uint16_t* src = (i & 1) ? p.v_new + r * p.v_stride : p.k_new + r * p.k_stride;
+      row[j] = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    if (slot[j] < 0) continue;  // a padded row
+    if (slot[j] >= (long long)p.num_pages * kPageSize) {
+      if (lane == 0) raise_error(p.err, MFA_DEVERR_PAGE);
+      continue;
+    }
+    const bool is_v = (i0 + j) & 1;
+    if (p.fmt == kKvE4M3) {
+      quantise_row_e4m3(row[j], static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * kHeadDim,
+                        (is_v ? p.v_scale : p.k_scale) + slot[j], lane);
+    } else {
+      uint16_t* dst = static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * kHeadDim;
+      reinterpret_cast<uint4*>(dst)[lane] = row[j];
+    }
+  }
+}
+
+template <int kRows>
+cudaError_t launch_slots(const AppendSlotsParams& p, cudaStream_t stream) {
+  const long long warps = (2ll * p.n_rows + kRows - 1) / kRows;
+  const unsigned grid = (unsigned)((warps + kSlotThreads / 32 - 1) / (kSlotThreads / 32));
+  return launch_pdl(kv_append_slots_kernel<kRows>, dim3(grid), dim3(kSlotThreads), 0, stream, p);
+}
+
 }  // namespace
+
+cudaError_t launch_kv_append_slots(const AppendSlotsParams& p, cudaStream_t stream) {
+  return launch_slots<1>(p, stream);
+}
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {
   return launch_pdl(kv_append_kernel, dim3(p.B), dim3(kAppendThreads), 0, stream, p);

@@ -498,6 +498,137 @@ mfa_status_t mfa_decode_attention_fp4(const void* q, const void* k_cache, const 
                        0, 1);
 }
 
+namespace {
+mfa_status_t append_slots_common(const void* k_new, const void* v_new, long long k_stride, long long v_stride,
+                                 const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache, float* k_scale,
+                                 float* v_scale, int fmt, int num_pages, void* workspace, void* stream) {
+  if (!k_new || !v_new || !slot_map || !k_cache || !v_cache) return fail(MFA_ERR_INVALID_ARG, "null pointer argument");
+  if (fmt != kKvBf16 && (!k_scale || !v_scale)) return fail(MFA_ERR_INVALID_ARG, "null scale pointer");
+  if (fmt != kKvBf16 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))) return fail(MFA_ERR_INVALID_ARG, "misaligned scales");
+  if (n_rows < 0) return fail(MFA_ERR_INVALID_ARG, "negative n_rows");
+  if (num_pages < 1) return fail(MFA_ERR_INVALID_ARG, "num_pages must be >= 1");
+  if (k_stride < 0 || v_stride < 0 || k_stride % 8 || v_stride % 8)
+    return fail(MFA_ERR_INVALID_ARG, "row strides must be multiples of 8 elements, not negative");
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(slot_map, 8))
+    return fail(MFA_ERR_INVALID_ARG, "misaligned pointer (rows and caches need 16 bytes, the slot map 8)");
+  if (!workspace || !aligned(workspace, 256))
+    return fail(MFA_ERR_WORKSPACE, "workspace missing or not 256-byte aligned");
+  const mfa_status_t st = current_device(nullptr, nullptr);
+  if (st != MFA_OK) return st;
+  if (n_rows == 0) return MFA_OK;
+  AppendSlotsParams p{};
+  p.k_new = static_cast<const uint16_t*>(k_new);
+  p.v_new = static_cast<const uint16_t*>(v_new);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.slot_map = slot_map;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.err = static_cast<uint32_t*>(workspace);
+  p.n_rows = n_rows;
+  p.num_pages = num_pages;
+  p.fmt = fmt;
+  const cudaError_t e = launch_kv_append_slots(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_append_slots launch");
+  return MFA_OK;
+}
+
+// Checks that the reserve and release calls share; an output that replaces an
+// input is the same array, and not one that overlaps it.
+mfa_status_t check_page_tables(const int32_t* seq_lens, const int32_t* page_table, const int32_t* free_pages,
+                               const int32_t* n_free, const int32_t* seq_lens_out, const int32_t* n_free_out, int batch,
+                               int max_pages, int num_pages, const void* workspace) {
+  if (!seq_lens || !page_table || !free_pages || !n_free || !seq_lens_out || !n_free_out)
+    return fail(MFA_ERR_INVALID_ARG, "null pointer argument");
+  if (batch < 1 || batch > kMaxBatch) return fail(MFA_ERR_INVALID_ARG, "batch %d outside [1, %d]", batch, kMaxBatch);
+  if (max_pages < 1 || num_pages < 1) return fail(MFA_ERR_INVALID_ARG, "max_pages and num_pages must be >= 1");
+  if ((long long)max_pages * kPageSize > 0x7fffffffLL) return fail(MFA_ERR_INVALID_ARG, "max_pages too large");
+  for (const int32_t* q : {seq_lens, page_table, free_pages, n_free, seq_lens_out, n_free_out})
+    if (!aligned(q, 4)) return fail(MFA_ERR_INVALID_ARG, "misaligned pointer (4 bytes needed)");
+  const uintptr_t a = reinterpret_cast<uintptr_t>(seq_lens), b = reinterpret_cast<uintptr_t>(seq_lens_out);
+  const uintptr_t span = (uintptr_t)batch * sizeof(int32_t);
+  if (a != b && a < b + span && b < a + span)
+    return fail(MFA_ERR_INVALID_ARG, "seq_lens_out overlaps seq_lens without being the same array");
+  if (!workspace || !aligned(workspace, 256))
+    return fail(MFA_ERR_WORKSPACE, "workspace missing or not 256-byte aligned");
+  return MFA_OK;
+}
+
+PageTableParams make_page_table_params(const int32_t* seq_lens, int32_t* page_table, int32_t* free_pages,
+                                       const int32_t* n_free, int32_t* seq_lens_out, int32_t* n_free_out, int batch,
+                                       int max_pages, int num_pages, void* workspace) {
+  PageTableParams p{};
+  p.seq_lens = seq_lens;
+  p.page_table = page_table;
+  p.free_pages = free_pages;
+  p.n_free = n_free;
+  p.seq_lens_out = seq_lens_out;
+  p.n_free_out = n_free_out;
+  p.err = static_cast<uint32_t*>(workspace);
+  p.counter = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kTableCounterOffset);
+  p.B = batch;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  return p;
+}
+}  // namespace
+
+mfa_status_t mfa_kv_append_slots(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                 const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache, int num_pages,
+                                 void* workspace, void* stream) {
+  return append_slots_common(k_new, v_new, k_stride, v_stride, slot_map, n_rows, k_cache, v_cache, nullptr, nullptr,
+                             kKvBf16, num_pages, workspace, stream);
+}
+
+mfa_status_t mfa_kv_append_slots_fp8(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                     const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache,
+                                     float* k_scale, float* v_scale, int num_pages, void* workspace, void* stream) {
+  return append_slots_common(k_new, v_new, k_stride, v_stride, slot_map, n_rows, k_cache, v_cache, k_scale, v_scale,
+                             kKvE4M3, num_pages, workspace, stream);
+}
+
+mfa_status_t mfa_reserve_pages(const int32_t* n_new, const int32_t* seq_lens, int32_t* page_table,
+                               const int32_t* free_pages, const int32_t* n_free, int batch, int max_pages,
+                               int num_pages, int max_new, int32_t* new_starts, int64_t* slot_map,
+                               int32_t* seq_lens_out, int32_t* n_free_out, void* workspace, void* stream) {
+  if (!n_new || !new_starts || !slot_map) return fail(MFA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(n_new, 4) || !aligned(new_starts, 4) || !aligned(slot_map, 8))
+    return fail(MFA_ERR_INVALID_ARG, "misaligned pointer (the slot map needs 8 bytes)");
+  if (max_new < 0) return fail(MFA_ERR_INVALID_ARG, "negative max_new");
+  mfa_status_t st = check_page_tables(seq_lens, page_table, free_pages, n_free, seq_lens_out, n_free_out, batch,
+                                      max_pages, num_pages, workspace);
+  if (st != MFA_OK || (st = current_device(nullptr, nullptr)) != MFA_OK) return st;
+  PageTableParams p = make_page_table_params(seq_lens, page_table, const_cast<int32_t*>(free_pages), n_free,
+                                             seq_lens_out, n_free_out, batch, max_pages, num_pages, workspace);
+  p.n_new = n_new;
+  p.new_starts = new_starts;
+  p.slot_map = slot_map;
+  p.max_new = max_new;
+  const cudaError_t e = launch_reserve_pages(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "reserve_pages launch");
+  return MFA_OK;
+}
+
+mfa_status_t mfa_release_pages(const int32_t* finished, const int32_t* keep_pages, const int32_t* seq_lens,
+                               const int32_t* page_table, int32_t* free_pages, const int32_t* n_free, int batch,
+                               int max_pages, int num_pages, int32_t* seq_lens_out, int32_t* n_free_out,
+                               void* workspace, void* stream) {
+  if (!finished) return fail(MFA_ERR_INVALID_ARG, "null pointer argument");
+  if (!aligned(finished, 4) || !aligned(keep_pages, 4)) return fail(MFA_ERR_INVALID_ARG, "misaligned pointer (4 bytes needed)");
+  mfa_status_t st = check_page_tables(seq_lens, page_table, free_pages, n_free, seq_lens_out, n_free_out, batch,
+                                      max_pages, num_pages, workspace);
+  if (st != MFA_OK || (st = current_device(nullptr, nullptr)) != MFA_OK) return st;
+  PageTableParams p = make_page_table_params(seq_lens, const_cast<int32_t*>(page_table), free_pages, n_free,
+                                             seq_lens_out, n_free_out, batch, max_pages, num_pages, workspace);
+  p.finished = finished;
+  p.keep_pages = keep_pages;
+  const cudaError_t e = launch_release_pages(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "release_pages launch");
+  return MFA_OK;
+}
+
 // Query-path workspace for up to `cap` rows: header (arrival counters at bytes 128-255) |
 // y fp32 [cap * rank] | h bf16 [cap * rank] | ssq fp32 [rank/128 * cap].
 // A call with batch B <= cap uses the first B * rank floats of y, which it leaves zero, so y is zero on
@@ -653,6 +784,7 @@ mfa_status_t mfa_check_device_errors(void* workspace, int clear, void* stream) {
   }
   if (word & MFA_DEVERR_PAGE) return fail(MFA_ERR_DEVICE_PAGE, "device error word 0x%x", word);
   if (word & MFA_DEVERR_CAPACITY) return fail(MFA_ERR_DEVICE_CAPACITY, "device error word 0x%x", word);
+  if (word & MFA_DEVERR_NO_PAGES) return fail(MFA_ERR_DEVICE_NO_PAGES, "device error word 0x%x", word);
   if (word & MFA_DEVERR_TIMEOUT) return fail(MFA_ERR_DEVICE_TIMEOUT, "device error word 0x%x", word);
   return MFA_OK;
 }
@@ -688,6 +820,7 @@ const char* mfa_status_string(mfa_status_t status) {
     case MFA_ERR_DEVICE_PAGE: return "MFA_ERR_DEVICE_PAGE";
     case MFA_ERR_DEVICE_CAPACITY: return "MFA_ERR_DEVICE_CAPACITY";
     case MFA_ERR_DEVICE_TIMEOUT: return "MFA_ERR_DEVICE_TIMEOUT";
+    case MFA_ERR_DEVICE_NO_PAGES: return "MFA_ERR_DEVICE_NO_PAGES";
   }
   return "MFA_ERR_UNKNOWN";
 }

@@ -58,6 +58,40 @@ struct AppendParams {
   int fmt;                // kKvBf16, kKvE4M3 or kKvE2M1
 };
 
+// Rows scattered to cache slots (slot = page * 64 + row of the page; negative: no row).
+struct AppendSlotsParams {
+  const uint16_t* k_new;  // row i at k_new + i * k_stride (bf16 bits)
+  const uint16_t* v_new;
+  long long k_stride, v_stride;
+  const int64_t* slot_map;  // [n_rows]
+  void* k_cache;
+  void* v_cache;
+  float* k_scale;  // E4M3 only
+  float* v_scale;
+  uint32_t* err;
+  int n_rows, num_pages;
+  int fmt;  // kKvBf16 or kKvE4M3
+};
+
+// Pages taken from or given back to the stack of free page ids.
+constexpr size_t kTableCounterOffset = 64;  // header byte of the arrival counter (zero between calls)
+struct PageTableParams {
+  const int32_t* n_new;       // [B] tokens that arrive (reserve)
+  const int32_t* finished;    // [B] non-zero: the request ended (release)
+  const int32_t* keep_pages;  // [B] pages a released request keeps (release; null: none)
+  const int32_t* seq_lens;    // [B]
+  int32_t* page_table;        // [B][max_pages]
+  int32_t* free_pages;        // [num_pages] stack, top at n_free - 1
+  const int32_t* n_free;
+  int32_t* new_starts;        // [B + 1]
+  int64_t* slot_map;          // [max_new]
+  int32_t* seq_lens_out;      // [B], may be seq_lens
+  int32_t* n_free_out;        // may be n_free
+  uint32_t* err;
+  uint32_t* counter;
+  int B, max_pages, num_pages, max_new;
+};
+
 struct DecodeParams {
   const uint16_t* q;       // [B][64][256] bf16 bits
   const void* k_cache;     // [num_pages][64][256] bf16 bits or E4M3 codes
@@ -145,6 +179,9 @@ inline cudaError_t ensure_dynamic_smem(void (*kernel)(KArgs...), size_t bytes, i
 
 // Kernel launchers (each returns the launch's cudaError_t).
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv_append_slots(const AppendSlotsParams& p, cudaStream_t stream);
+cudaError_t launch_reserve_pages(const PageTableParams& p, cudaStream_t stream);
+cudaError_t launch_release_pages(const PageTableParams& p, cudaStream_t stream);
 cudaError_t launch_decode_split_tc(const DecodeParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
                                    const CUtensorMap& q_map, cudaStream_t stream);
 cudaError_t launch_decode_split_tc_fp8(const DecodeParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map,

@@ -73,13 +73,15 @@ typedef enum {
   MFA_ERR_WORKSPACE = 4,        /* workspace missing or smaller than required */
   MFA_ERR_DEVICE_PAGE = 5,      /* device saw a page id outside [0, num_pages) */
   MFA_ERR_DEVICE_CAPACITY = 6,  /* device saw a length beyond max_pages * 64 */
-  MFA_ERR_DEVICE_TIMEOUT = 7    /* a pipeline wait inside a kernel gave up */
+  MFA_ERR_DEVICE_TIMEOUT = 7,   /* a pipeline wait inside a kernel gave up */
+  MFA_ERR_DEVICE_NO_PAGES = 8   /* mfa_reserve_pages ran out of free pages */
 } mfa_status_t;
 
 /* Error-word bits (the first uint32 of the workspace). */
 #define MFA_DEVERR_PAGE 0x1u
 #define MFA_DEVERR_CAPACITY 0x2u
 #define MFA_DEVERR_TIMEOUT 0x4u
+#define MFA_DEVERR_NO_PAGES 0x8u
 
 /* Static description of how a decode call splits its work.
  * Host only; needs no GPU. */
@@ -139,6 +141,84 @@ mfa_status_t mfa_kv_append_fp8(const void* k_new, const void* v_new, int n_new,
                                const int32_t* page_table, int32_t* seq_lens,
                                int batch, int max_pages, int num_pages,
                                void* workspace, void* stream);
+
+/* Paged-cache bookkeeping on the device: the page tables of the requests, a
+ * stack of free page ids, and the slot of every token of a step, so that a
+ * serving loop (also one replayed as a CUDA graph) needs no lengths or page ids
+ * on the host.
+ *   free_pages: [device] int32 [num_pages]; the stack holds free_pages[0 ..
+ *               *n_free), its top is the last of them.
+ * A step runs mfa_reserve_pages, mfa_kv_append_slots, an attention call, and
+ * mfa_release_pages when requests have ended.
+ *
+ * mfa_reserve_pages: request b holds seq_lens[b] tokens in its first
+ * ceil(seq_lens[b] / 64) pages, and n_new[b] >= 0 tokens arrive for it. In
+ * request order, each takes the pages that it lacks from the top of the stack
+ * and enters them in its page_table row behind those it holds. Writes
+ *   new_starts   [device] int32 [batch + 1]: sums of n_new, so that token t of
+ *                request b is row new_starts[b] + t of the step's rows (at
+ *                most 2^31 - 1);
+ *   slot_map     [device] int64 [max_new]: for each row its slot, page * 64 +
+ *                row in the page; -1 for rows past the last;
+ *   seq_lens_out [device] int32 [batch]: seq_lens[b] + n_new[b];
+ *   n_free_out   [device] int32: pages left on the stack.
+ * seq_lens_out may be seq_lens and n_free_out may be n_free (the same array);
+ * other arrays do not overlap. The rows' contents are written by
+ * mfa_kv_append_slots. A request that cannot be served is left as it is: its
+ * rows get slot -1, its length and table row do not change. That is one with a
+ * negative length or count, with more than max_pages * 64 tokens, or with rows
+ * past max_new (MFA_DEVERR_CAPACITY), and one whose pages, with those that the
+ * requests before it need, are more than the stack holds (MFA_DEVERR_NO_PAGES;
+ * requests that need no page are still served). A page id outside
+ * [0, num_pages) in the table or on the stack sets MFA_DEVERR_PAGE, and its
+ * tokens get slot -1.
+ *
+ * mfa_release_pages: each request with finished[b] != 0 gives its pages behind
+ * the first keep_pages[b] (null: 0; pages that others share are kept) back to
+ * the stack, in request and page order. seq_lens_out[b] = min(seq_lens[b],
+ * 64 * keep_pages[b]) for it and seq_lens[b] for the others; table rows are not
+ * changed. A request with a bad length or a negative keep_pages[b], and one
+ * whose pages do not fit into free_pages, is left as it is
+ * (MFA_DEVERR_CAPACITY); a page id outside [0, num_pages) sets MFA_DEVERR_PAGE.
+ *
+ * workspace: [device] any workspace initialised by mfa_workspace_init (only its
+ * 256-byte header is used); calls that share one must not overlap on the GPU.
+ * Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers, batch outside
+ * [1, MFA_MAX_BATCH], max_pages < 1, num_pages < 1, max_new < 0, overlapping
+ * lengths), MFA_ERR_WORKSPACE. */
+mfa_status_t mfa_reserve_pages(const int32_t* n_new, const int32_t* seq_lens, int32_t* page_table,
+                               const int32_t* free_pages, const int32_t* n_free,
+                               int batch, int max_pages, int num_pages, int max_new,
+                               int32_t* new_starts, int64_t* slot_map,
+                               int32_t* seq_lens_out, int32_t* n_free_out,
+                               void* workspace, void* stream);
+mfa_status_t mfa_release_pages(const int32_t* finished, const int32_t* keep_pages, const int32_t* seq_lens,
+                               const int32_t* page_table, int32_t* free_pages, const int32_t* n_free,
+                               int batch, int max_pages, int num_pages,
+                               int32_t* seq_lens_out, int32_t* n_free_out,
+                               void* workspace, void* stream);
+
+/* KV append by slots, for steps whose requests bring different numbers of
+ * tokens: row i of K (k_new + i * k_stride, 256 bf16) and of V goes to slot
+ * slot_map[i] of the paged cache, i.e. row slot % 64 of page slot / 64. Lengths
+ * are not touched. Rows with a negative slot are skipped (padding); a slot of
+ * num_pages * 64 or more is skipped and sets MFA_DEVERR_PAGE. The slots are
+ * distinct.
+ *   k_new, v_new: [device] bf16, 16-byte aligned; k_stride, v_stride: elements
+ *     from one row to the next, multiples of 8, so that K and V may be columns
+ *     of one projection's output;
+ *   slot_map: [device] int64 [n_rows], as mfa_reserve_pages writes it.
+ * mfa_kv_append_slots_fp8 quantises each row as mfa_kv_append_fp8 does (the
+ * same codes and scales). workspace: any workspace (only its error word is
+ * used). Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers,
+ * n_rows < 0, num_pages < 1, bad strides), MFA_ERR_WORKSPACE. */
+mfa_status_t mfa_kv_append_slots(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                 const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache,
+                                 int num_pages, void* workspace, void* stream);
+mfa_status_t mfa_kv_append_slots_fp8(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                     const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache,
+                                     float* k_scale, float* v_scale, int num_pages,
+                                     void* workspace, void* stream);
 
 /* MFA decode attention over a bf16 paged cache (formula at the top of this
  * file). q, out, lse, caches, page_table, seq_lens: [device], layouts above.
@@ -349,7 +429,7 @@ mfa_status_t mfa_decode_attention_noalloc(const void* q, const void* k_cache, co
                                           uint32_t* device_error_word, void* stream);
 
 /* Synchronise `stream`, read the workspace error word and return the first
- * device fault it records (MFA_ERR_DEVICE_PAGE, _CAPACITY, _TIMEOUT) or MFA_OK.
+ * device fault it records (MFA_ERR_DEVICE_PAGE, _CAPACITY, _NO_PAGES, _TIMEOUT) or MFA_OK.
  * `clear` != 0 resets the word afterwards. This call blocks the host. */
 mfa_status_t mfa_check_device_errors(void* workspace, int clear, void* stream);
 
