@@ -124,6 +124,33 @@ struct DecodeParams {
   // (i + b) * q_groups + r, holding q_per_cta tokens.
   int q_per_cta, q_groups;
   uint64_t wait_budget_ns;
+  // Shared prefix (null: none): sequence b's first skip[b] pages are left out of the split (its table row, length and
+  // partition start behind them); its partial results over them are parts[b].y rows of [64 heads] from row parts[b].x
+  // on, kPrefixTileSeqs apart, of pre_o / pre_lse, which the combine merges with the split's.
+  const int32_t* skip;
+  const int2* parts;
+  const float* pre_o;    // [rows][64][256]
+  const float* pre_lse;  // [rows][64]
+  int pre_pairs;         // at most this many partial results a sequence
+};
+
+// Shared-prefix kernel: row tiles of kPrefixTileSeqs sequences, units of 128 keys.
+constexpr int kPrefixTileSeqs = 4;
+// Units charged per row tile that a pair of CTAs works on, besides its keys: loading Q and writing the partial result.
+constexpr int kPrefixPieceUnits = 2;
+struct PrefixParams {
+  const int32_t* group_starts;  // [n_groups + 1]
+  const int32_t* prefix_pages;  // [n_groups]
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  float* part_o;                // [(pair + row tile)][4 sequences][64 heads][256]
+  float* part_lse;
+  int32_t* skip;                // [B], written: see DecodeParams
+  int2* parts;
+  uint32_t* err;
+  float scale;
+  int B, n_groups, max_pages, num_pages, pairs;
+  uint64_t wait_budget_ns;
 };
 
 // Launch with programmatic stream serialisation (the kernel calls
@@ -195,6 +222,8 @@ size_t decode_split_tc_fp8_smem_bytes(int B);
 cudaError_t launch_decode_split_tc_mtp(const DecodeParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
                                        const CUtensorMap& q_map, cudaStream_t stream);
 size_t decode_split_tc_mtp_smem_bytes(int B);
+cudaError_t launch_decode_prefix_tc(const PrefixParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                    const CUtensorMap& q_map, cudaStream_t stream);
 
 // Host-side services of mfa_api.cu for other entry points of the library.
 void set_last_error_message(const char* msg);

@@ -315,6 +315,39 @@ mfa_status_t mfa_query_lowrank(const void* x, const void* w_down, const void* ga
                                int batch, int d_model, int rank, int n_out, float eps,
                                void* workspace, size_t workspace_bytes, void* stream);
 
+/* Decode attention for a batch whose sequences share prefixes (bf16 cache): the
+ * attention of mfa_decode_attention, with the same inputs, outputs and values,
+ * in which the pages that the sequences of a group have in common are read once
+ * for the group, as one matrix product over all its queries.
+ *   group_starts: [device] int32 [n_groups + 1], non-decreasing: group g is the
+ *                 sequences group_starts[g] .. group_starts[g + 1] - 1. Sequences
+ *                 in no group have no shared prefix.
+ *   prefix_pages: [device] int32 [n_groups]: the first prefix_pages[g] entries of
+ *                 the page-table rows of group g are the same pages, full of the
+ *                 prefix's 64 * prefix_pages[g] tokens (0: nothing is shared);
+ *                 they may be fewer than the pages really shared.
+ * seq_lens count the prefix. A sequence that holds fewer tokens than its
+ * group's prefix (0 for an empty slot of the batch), and a group with fewer than
+ * two others, are read through their own table rows alone, as by
+ * mfa_decode_attention.
+ * max_prefix_hint, max_suffix_hint: expected maxima of 64 * prefix_pages[g] and
+ * of the tokens behind the prefix; they size the grids only.
+ * workspace: at least mfa_decode_prefix_workspace_bytes(batch, n_groups,
+ * max_prefix_hint, max_suffix_hint) bytes (0 for a bad argument), initialised
+ * once by mfa_workspace_init; calls that share it must not overlap on the GPU.
+ * Device errors, besides those of mfa_decode_attention: MFA_DEVERR_CAPACITY for
+ * group_starts that decrease or leave [0, batch] and for prefix_pages outside
+ * [0, max_pages] (clamped). Host errors: MFA_ERR_INVALID_ARG also for n_groups
+ * outside [1, batch], negative hints, and batch * max_pages above 2^31 - 1. */
+size_t mfa_decode_prefix_workspace_bytes(int batch, int n_groups, int max_prefix_hint, int max_suffix_hint);
+mfa_status_t mfa_decode_attention_prefix(const void* q, const void* k_cache, const void* v_cache,
+                                         const int32_t* page_table, const int32_t* seq_lens,
+                                         const int32_t* group_starts, const int32_t* prefix_pages, int n_groups,
+                                         void* out, float* lse, float scale,
+                                         int batch, int max_pages, int num_pages,
+                                         int max_prefix_hint, int max_suffix_hint,
+                                         void* workspace, size_t workspace_bytes, void* stream);
+
 /* Multi-token (MTP) decode over a paged cache ("Step-3 is Large yet
  * Affordable", section 5.2: with multi-token prediction a decode step carries
  * extra predicted tokens that read the same KV cache, which raises the

@@ -1,0 +1,293 @@
+"""Shared-prefix decode attention (mfa_decode_attention_prefix*) against the definition in 64 bits.
+
+Tolerances, from the roundings on the way: each weight enters the second product as bf16, off by at most 2^-8 of
+itself, so an output is off by at most 2^-8 of the weighted mean of |v|, which is at most the largest |v|; the output is
+rounded to bf16, off by at most 2^-8 of itself; the fp32 sums of 256 products and the exponentials add less than 2^-12 of
+either. On an E4M3 cache the queries (2^-18.8 of the largest) and the weights (two terms: 2^-8) are held less exactly
+than that by no more than another 2^-8 of the largest |v|. The LSE is off by the logits' fp32 sums, 2^-15 of
+scale * sum |q k| (about 10 here), below 1e-3."""
+import numpy as np
+import pytest
+import torch
+
+from decode_attention_mfa_gb300 import capi
+
+pytestmark = pytest.mark.gpu
+PAGE, HEADS, DIM = 64, 64, 256
+SCALE = 1.0 / 16.0
+LSE_ABS = 1e-3
+
+
+class Batch:
+    """Groups (first sequence, sequences, prefix pages) of a batch and its sequences' lengths, on the device."""
+
+    def __init__(self, sizes, pages, lens, fp8=False, seed=0, starts=None, spare_cols=1):
+        rng = np.random.default_rng(seed)
+        self.B, self.fp8 = len(lens), fp8
+        self.starts = np.concatenate([[0], np.cumsum(sizes)]) if starts is None else np.asarray(starts)
+        self.pages, self.lens = np.asarray(pages), np.asarray(lens)
+        shared = np.zeros(self.B, np.int64)
+        group = np.full(self.B, -1)
+        for g, n in enumerate(self.pages):
+            shared[self.starts[g]:self.starts[g + 1]] = n
+            group[self.starts[g]:self.starts[g + 1]] = g
+        own = np.maximum(0, -(-self.lens // PAGE) - shared)
+        total = int(self.pages.sum() + own.sum()) + 3
+        order = rng.permutation(total)
+        self.table = np.full((self.B, max(1, int((shared + own).max())) + spare_cols), -1, np.int32)
+        at = int(self.pages.sum())
+        first = np.concatenate([[0], np.cumsum(self.pages)])
+        for b in range(self.B):
+            if group[b] >= 0:
+                self.table[b, :shared[b]] = order[first[group[b]]:first[group[b]] + shared[b]]
+            self.table[b, shared[b]:shared[b] + own[b]] = order[at:at + own[b]]
+            at += own[b]
+        gen = torch.Generator(device="cuda").manual_seed(seed + 1)
+        self.num_pages = total
+        self.q = torch.randn((self.B, HEADS, DIM), generator=gen, device="cuda").bfloat16()
+        rows = [torch.randn((total, PAGE, DIM), generator=gen, device="cuda").bfloat16() for _ in range(2)]
+        # rows that no sequence holds are poisoned: a stale row is never read
+        used = np.zeros((total, PAGE), bool)
+        for b in range(self.B):
+            n = int(self.lens[b])
+            for j in range(-(-n // PAGE)):
+                used[self.table[b, j], :min(PAGE, n - j * PAGE)] = True
+        self.unused = torch.from_numpy(~used).cuda()
+        self.scales = []
+        if fp8:
+            self.cache = []
+            for x in rows:
+                x = x.float() * torch.exp(0.5 * torch.randn((total, PAGE, 1), generator=gen, device="cuda"))
+                s = x.abs().amax(-1) / 448.0
+                codes = (x / s.unsqueeze(-1)).to(torch.float8_e4m3fn).view(torch.uint8)
+                codes[self.unused] = 0x7F
+                s[self.unused] = float("nan")
+                self.cache.append(codes)
+                self.scales.append(s)
+        else:
+            for x in rows:
+                x[self.unused] = float("nan")
+            self.cache = rows
+        i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a)).int().cuda()  # noqa: E731
+        self.d = dict(table=i32(self.table), lens=i32(self.lens), starts=i32(self.starts), pages=i32(self.pages))
+        self.out = torch.full((self.B, HEADS, DIM), 7.0, dtype=torch.bfloat16, device="cuda")
+        self.lse = torch.full((self.B, HEADS), 7.0, device="cuda")
+        self.hints = (int(self.pages.max()) * PAGE, int(max(1, (self.lens - shared * PAGE).max())))
+        self.ws = None
+
+    def workspace(self, hints=None):
+        n = capi.mfa_decode_prefix_workspace_bytes(self.B, len(self.pages), *(hints or self.hints))
+        self.ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+        capi.mfa_workspace_init(self.ws, n)
+        self.ws[256:] = 0xFF  # what the scratch holds between calls is not used: NaN floats, page counts of -1
+        torch.cuda.synchronize()
+
+    def call(self, scale=SCALE, hints=None, stream=None):
+        if self.ws is None:
+            self.workspace(hints)
+        fn = capi.mfa_decode_attention_prefix_fp8 if self.fp8 else capi.mfa_decode_attention_prefix
+        fn(self.q, *self.cache, *self.scales, self.d["table"], self.d["lens"], self.d["starts"], self.d["pages"],
+           len(self.pages), self.out, self.lse, scale, self.B, self.table.shape[1], self.num_pages, *(hints or self.hints),
+           self.ws, self.ws.numel(), stream)
+
+    def reference(self, b, scale=SCALE):
+        n = int(self.lens[b])
+        ids = torch.from_numpy(self.table[b, :-(-n // PAGE)]).long().cuda()
+        rows = []
+        for i, c in enumerate(self.cache):
+            if self.fp8:
+                x = c[ids].view(torch.float8_e4m3fn).double() * self.scales[i][ids].double().unsqueeze(-1)
+            else:
+                x = c[ids].double()
+            rows.append(x.reshape(-1, DIM)[:n])
+        logits = self.q[b].double() @ rows[0].T * scale
+        lse = torch.logsumexp(logits, 1)
+        return torch.exp(logits - lse[:, None]) @ rows[1], lse, rows[1].abs().max()
+
+    def check(self, scale=SCALE, which=None):
+        capi.mfa_check_device_errors(self.ws)
+        for b in range(self.B) if which is None else which:
+            if self.lens[b] == 0:
+                assert (self.out[b] == 0).all() and torch.isneginf(self.lse[b]).all()
+                continue
+            out, lse, top = self.reference(b, scale)
+            got = self.out[b].double()
+            bound = 2 ** -8 * ((2 if self.fp8 else 1) * top + out.abs()) + 2 ** -12 * top
+            assert torch.isfinite(got).all(), b
+            assert ((got - out).abs() <= bound).all(), (b, float((got - out).abs().max()), float(bound.min()))
+            assert float((got - out).norm() / out.norm()) <= 5e-3 * (2 if self.fp8 else 1), b
+            assert float((self.lse[b].double() - lse).abs().max()) <= LSE_ABS, b
+
+    def run(self, **kw):
+        self.call(**kw)
+        self.check(kw.get("scale", SCALE))
+        return self
+
+
+def lens_of(sizes, pages, suffix, seed=0):
+    rng = np.random.default_rng(seed)
+    return np.concatenate([p * PAGE + rng.integers(0, suffix + 1, n) for n, p in zip(sizes, pages)]).astype(np.int64)
+
+
+KV = pytest.mark.parametrize("fp8", [False])
+
+
+@KV
+@pytest.mark.parametrize("n,pages", [(2, 1), (2, 2), (4, 2), (4, 3), (3, 4), (5, 5), (8, 16), (9, 7), (17, 31), (64, 64), (6, 400)])
+def test_one_group(n, pages, fp8):
+    Batch([n], [pages], lens_of([n], [pages], 150, n), fp8, seed=n).run()
+
+
+@KV
+@pytest.mark.parametrize("suffix", [0, 1, 64, 65])
+def test_suffix_lengths(suffix, fp8):
+    """No token behind the prefix, one, a whole page, one more."""
+    Batch([6], [9], np.full(6, 9 * PAGE + suffix), fp8).run()
+
+
+@KV
+def test_groups_of_every_kind(fp8):
+    """Odd sizes, a group of one, one without shared pages, one whose prefix is a single page."""
+    sizes, pages = [7, 1, 19, 3, 2, 4], [5, 9, 40, 0, 1, 2]
+    Batch(sizes, pages, lens_of(sizes, pages, 700, 4), fp8, seed=9).run()
+
+
+@KV
+def test_many_small_groups(fp8):
+    """More row tiles than pairs of CTAs: pairs work through several pieces each."""
+    rng = np.random.default_rng(1)
+    sizes, pages = rng.integers(1, 6, 130).tolist(), rng.integers(1, 12, 130).tolist()
+    Batch(sizes, pages, lens_of(sizes, pages, 90, 4), fp8, seed=3).run()
+
+
+@KV
+def test_sequences_that_end_inside_the_prefix_and_empty_slots(fp8):
+    """They see their own tokens and nothing else, wherever in the group they stand; a group left with one whole prefix
+    is read through its own rows."""
+    sizes, pages = [5, 4, 6, 2], [6, 10, 3, 8]
+    lens = lens_of(sizes, pages, 100, 5)
+    lens[0], lens[2], lens[4] = 0, 1, 6 * PAGE - 1   # the first of its group among them
+    lens[5:8] = 65, 0, 640 - 64                      # one of four holds the prefix
+    lens[9:15] = 0                                   # none does
+    lens[15], lens[16] = 8 * PAGE, 8 * PAGE + 1
+    Batch(sizes, pages, lens, fp8, seed=5).run()
+
+
+@KV
+def test_all_empty_and_single(fp8):
+    Batch([4], [3], np.zeros(4, np.int64), fp8).run()
+    Batch([1], [3], np.array([200]), fp8).run()
+    Batch([1], [0], np.array([1]), fp8).run()
+
+
+@KV
+def test_sequences_outside_the_groups(fp8):
+    lens = np.array([10, 300, 5 * PAGE + 3, 5 * PAGE, 6 * PAGE, 77, 0, 128])
+    Batch(None, [5], lens, fp8, starts=[2, 5]).run()
+
+
+@KV
+def test_shared_pages_beyond_the_prefix_and_long_rows(fp8):
+    """prefix_pages may be fewer than the pages really shared; table rows may be longer than needed."""
+    b = Batch([4], [12], lens_of([4], [12], 40, 1), fp8, spare_cols=33)
+    b.d["pages"].fill_(5)
+    b.run()
+
+
+@KV
+@pytest.mark.parametrize("hints", [(0, 0), (64, 64), (1 << 20, 1 << 20)])
+def test_hints_size_the_grids_only(hints, fp8):
+    sizes, pages = [6, 5], [30, 4]
+    Batch(sizes, pages, lens_of(sizes, pages, 400, 8), fp8).run(hints=hints)
+
+
+@KV
+@pytest.mark.parametrize("scale", [-SCALE, 0.0, 0.5])
+def test_scales(scale, fp8):
+    sizes, pages = [6, 3], [7, 4]
+    Batch(sizes, pages, lens_of(sizes, pages, 100, 8), fp8).run(scale=scale)
+
+
+@KV
+def test_moving_maximum(fp8):
+    """Logits that grow along the prefix (the reference maximum moves at every unit) and fall again in the suffix."""
+    b = Batch([5], [40], lens_of([5], [40], 200, 3), fp8)
+    gain = torch.zeros(b.num_pages, device="cuda")
+    ids = torch.from_numpy(b.table[0, :40]).long().cuda()
+    gain[ids] = torch.linspace(0.0, 6.0, 40, device="cuda")
+    if fp8:
+        b.scales[0] *= (0.2 + gain).unsqueeze(-1)
+    else:
+        b.cache[0].copy_((b.cache[0].float() * (0.2 + gain).view(-1, 1, 1)).bfloat16())
+    # the logits reach about 8 * 4 * sqrt(256) / 16: the LSE's bound grows with them
+    b.call()
+    capi.mfa_check_device_errors(b.ws)
+    for i in range(5):
+        out, lse, top = b.reference(i)
+        assert ((b.out[i].double() - out).abs() <= 2 ** -7 * (2 if fp8 else 1) * top).all()
+        assert float((b.lse[i].double() - lse).abs().max()) <= 1e-2
+
+
+@KV
+def test_whole_batch_of_1024(fp8):
+    """The largest batch, in groups of four and one large group."""
+    sizes = [4] * 100 + [200] + [2] * 212
+    pages = [2] * 100 + [3] + [1] * 212
+    b = Batch(sizes, pages, lens_of(sizes, pages, 70, 8), fp8)
+    b.call()
+    b.check(which=range(0, 1024, 7))
+
+
+@KV
+def test_bad_groups_and_pages_are_reported(fp8):
+    """Group starts that decrease or leave the batch, page counts out of range and bad page ids set the error word;
+    sequences that they do not concern keep their values."""
+    sizes, pages = [4, 4, 4], [4, 3, 2]
+    lens = lens_of(sizes, pages, 100, 2)
+    b = Batch(sizes, pages, lens, fp8)
+    for starts, counts in (([0, 4, 2, 12], [4, 3, 2]), ([-3, 4, 8, 90], [4, 3, 2]), ([0, 4, 8, 12], [4, 3, 1 << 30])):
+        b.d["starts"].copy_(torch.tensor(starts))
+        b.d["pages"].copy_(torch.tensor(counts))
+        b.call()
+        with pytest.raises(capi.MFAError) as e:
+            capi.mfa_check_device_errors(b.ws)
+        assert e.value.status == 6
+        b.check(which=range(4))
+    b = Batch(sizes, pages, lens, fp8)
+    b.table[5, 0] = b.num_pages + 7
+    b.table[4, 1] = -2
+    b.d["table"].copy_(torch.from_numpy(b.table))
+    b.call()
+    with pytest.raises(capi.MFAError) as e:
+        capi.mfa_check_device_errors(b.ws)
+    assert e.value.status == 5
+    b.check(which=list(range(4)) + list(range(8, 12)))
+
+
+@KV
+def test_captured_and_replayed_with_new_lengths_and_groups(fp8):
+    """One graph, replayed on another stream with other lengths and groups of the same batch; two graphs share one
+    workspace in turn; every replay gives what a direct call gives, bit for bit."""
+    sizes, pages = [6, 6], [20, 10]
+    a = Batch(sizes, pages, lens_of(sizes, pages, 300, 2), fp8)
+    a.run()
+    first = a.out.clone(), a.lse.clone()
+    stream = torch.cuda.Stream()
+    graphs = []
+    with torch.cuda.stream(stream):
+        for _ in range(2):
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g, stream=stream):
+                a.call()
+            graphs.append(g)
+        for g in graphs * 2:
+            a.out.zero_()
+            g.replay()
+            stream.synchronize()
+            assert torch.equal(a.out, first[0]) and torch.equal(a.lse, first[1])
+        a.lens = np.maximum(0, a.lens - np.arange(12) * 37)
+        a.d["lens"].copy_(torch.from_numpy(a.lens))
+        a.d["pages"].copy_(torch.tensor([13, 0]))
+        graphs[0].replay()
+        stream.synchronize()
+        a.check()
