@@ -61,6 +61,8 @@ _SIGNATURES = {
                                          _P], _I),
     "mfa_decode_prefix_workspace_bytes": ([_I, _I, _I, _I], _Z),
     "mfa_decode_attention_prefix": ([_P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _F, _I, _I, _I, _I, _I, _P, _Z, _P], _I),
+    "mfa_decode_attention_prefix_fp8": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _F, _I, _I, _I, _I, _I, _P,
+                                         _Z, _P], _I),
     "mfa_kv_append_slots": ([_P, _P, _I64, _I64, _P, _I, _P, _P, _I, _P, _P], _I),
     "mfa_kv_append_slots_fp8": ([_P, _P, _I64, _I64, _P, _I, _P, _P, _P, _P, _I, _P, _P], _I),
     "mfa_reserve_pages": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P], _I),
@@ -293,6 +295,17 @@ def mfa_decode_attention_prefix(q, k_cache, v_cache, page_table, seq_lens, group
                                               _ptr(group_starts), _ptr(prefix_pages), n_groups, _ptr(out), _ptr(lse),
                                               float(scale), batch, max_pages, num_pages, max_prefix_hint,
                                               max_suffix_hint, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def mfa_decode_attention_prefix_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, group_starts,
+                                    prefix_pages, n_groups, out, lse, scale, batch, max_pages, num_pages,
+                                    max_prefix_hint, max_suffix_hint, workspace, workspace_bytes, stream=None):
+    """The same over an E4M3 cache with per-token fp32 scales."""
+    _check(load().mfa_decode_attention_prefix_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                                  _ptr(page_table), _ptr(seq_lens), _ptr(group_starts),
+                                                  _ptr(prefix_pages), n_groups, _ptr(out), _ptr(lse), float(scale),
+                                                  batch, max_pages, num_pages, max_prefix_hint, max_suffix_hint,
+                                                  _ptr(workspace), workspace_bytes, _stream(stream)))
 
 
 def mfa_reserve_pages(n_new, seq_lens, page_table, free_pages, n_free, batch, max_pages, num_pages, max_new,

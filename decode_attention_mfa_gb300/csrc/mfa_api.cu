@@ -456,6 +456,8 @@ mfa_status_t prefix_common(const void* q, const void* k_cache, const void* v_cac
   g.prefix_pages = prefix_pages;
   g.page_table = page_table;
   g.seq_lens = seq_lens;
+  g.k_scale = k_scale;
+  g.v_scale = v_scale;
   g.part_o = reinterpret_cast<float*>(ws + w.pre_o);
   g.part_lse = reinterpret_cast<float*>(ws + w.pre_lse);
   g.skip = reinterpret_cast<int32_t*>(ws + w.skip);
@@ -472,13 +474,14 @@ mfa_status_t prefix_common(const void* q, const void* k_cache, const void* v_cac
   CUtensorMap kmap, vmap, qmap;
   const uint64_t rows = (uint64_t)num_pages * kPageSize;
   if ((st = encode_rows_bf16(&qmap, q, (uint64_t)batch * kHeads)) != MFA_OK ||
-      (st = encode_rows_bf16(&kmap, k_cache, rows)) != MFA_OK || (st = encode_rows_bf16(&vmap, v_cache, rows)) != MFA_OK)
+      (st = fp8 ? encode_rows_e4m3(&kmap, k_cache, rows) : encode_rows_bf16(&kmap, k_cache, rows)) != MFA_OK ||
+      (st = fp8 ? encode_rows_e4m3(&vmap, v_cache, rows) : encode_rows_bf16(&vmap, v_cache, rows)) != MFA_OK)
     return st;
   cudaError_t e = launch_decode_prefix_tc(g, kmap, vmap, qmap, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode prefix launch");
   if (g_prof_start && (e = cudaEventRecordWithFlags(g_prof_start, s, cudaEventRecordExternal)) != cudaSuccess)
     return cuda_fail(e, "profile event record");
-  e = launch_decode_split_tc(p, kmap, vmap, qmap, s);
+  e = fp8 ? launch_decode_split_tc_fp8(p, kmap, vmap, qmap, s) : launch_decode_split_tc(p, kmap, vmap, qmap, s);
   if (e != cudaSuccess) return cuda_fail(e, "decode split launch");
   if (g_prof_stop && (e = cudaEventRecordWithFlags(g_prof_stop, s, cudaEventRecordExternal)) != cudaSuccess)
     return cuda_fail(e, "profile event record");
@@ -549,6 +552,18 @@ mfa_status_t mfa_decode_attention_prefix(const void* q, const void* k_cache, con
                                          int max_prefix_hint, int max_suffix_hint, void* workspace,
                                          size_t workspace_bytes, void* stream) {
   return prefix_common(q, k_cache, v_cache, nullptr, nullptr, false, page_table, seq_lens, group_starts, prefix_pages,
+                       n_groups, out, lse, scale, batch, max_pages, num_pages, max_prefix_hint, max_suffix_hint,
+                       workspace, workspace_bytes, stream);
+}
+
+mfa_status_t mfa_decode_attention_prefix_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                             const float* k_scale, const float* v_scale, const int32_t* page_table,
+                                             const int32_t* seq_lens, const int32_t* group_starts,
+                                             const int32_t* prefix_pages, int n_groups, void* out, float* lse,
+                                             float scale, int batch, int max_pages, int num_pages,
+                                             int max_prefix_hint, int max_suffix_hint, void* workspace,
+                                             size_t workspace_bytes, void* stream) {
+  return prefix_common(q, k_cache, v_cache, k_scale, v_scale, true, page_table, seq_lens, group_starts, prefix_pages,
                        n_groups, out, lse, scale, batch, max_pages, num_pages, max_prefix_hint, max_suffix_hint,
                        workspace, workspace_bytes, stream);
 }

@@ -143,6 +143,8 @@ struct PrefixParams {
   const int32_t* prefix_pages;  // [n_groups]
   const int32_t* page_table;
   const int32_t* seq_lens;
+  const float* k_scale;         // [num_pages][64] (null: bf16 cache)
+  const float* v_scale;
   float* part_o;                // [(pair + row tile)][4 sequences][64 heads][256]
   float* part_lse;
   int32_t* skip;                // [B], written: see DecodeParams

@@ -348,6 +348,21 @@ mfa_status_t mfa_decode_attention_prefix(const void* q, const void* k_cache, con
                                          int max_prefix_hint, int max_suffix_hint,
                                          void* workspace, size_t workspace_bytes, void* stream);
 
+/* The same over an E4M3 cache with per-token fp32 scales (k_scale, v_scale
+ * [num_pages][64], [device], 16-byte aligned): the attention of
+ * mfa_decode_attention_fp8. Over the prefix, q enters the 8-bit products as two
+ * E4M3 terms under a power of two per head, and the weights times the V scales
+ * as two E4M3 terms (about 2^-8 relative). Everything else as
+ * mfa_decode_attention_prefix. */
+mfa_status_t mfa_decode_attention_prefix_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                             const float* k_scale, const float* v_scale,
+                                             const int32_t* page_table, const int32_t* seq_lens,
+                                             const int32_t* group_starts, const int32_t* prefix_pages, int n_groups,
+                                             void* out, float* lse, float scale,
+                                             int batch, int max_pages, int num_pages,
+                                             int max_prefix_hint, int max_suffix_hint,
+                                             void* workspace, size_t workspace_bytes, void* stream);
+
 /* Multi-token (MTP) decode over a paged cache ("Step-3 is Large yet
  * Affordable", section 5.2: with multi-token prediction a decode step carries
  * extra predicted tokens that read the same KV cache, which raises the

@@ -129,7 +129,7 @@ def lens_of(sizes, pages, suffix, seed=0):
     return np.concatenate([p * PAGE + rng.integers(0, suffix + 1, n) for n, p in zip(sizes, pages)]).astype(np.int64)
 
 
-KV = pytest.mark.parametrize("fp8", [False])
+KV = pytest.mark.parametrize("fp8", [False, True])
 
 
 @KV
