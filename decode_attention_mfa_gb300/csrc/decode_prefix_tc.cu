@@ -1,34 +1,41 @@
-// decode_prefix_tc.cu -- the shared-prefix part of decode attention: the
-// queries of all the sequences of a group against the group's prefix, whose
-// pages are read once for four sequences at a time instead of once for each.
+// decode_prefix_tc.cu -- decode attention for a batch whose sequences share
+// prefixes: the pages of a group's prefix are read once for four sequences at a
+// time instead of once for each, and in the same kernel every sequence reads
+// what it holds behind its prefix.
 //
 // A group's queries form one matrix of 64 n rows (64 heads, n sequences), and
 //     S = Q K^T,  P = exp2(scale log2(e) S - m),  O = P V,  l = P 1
 // over the prefix is ordinary matrix work: 4 * 64 * 256 flops a sequence and
 // key, against 1 KB (bf16) a key for the whole group, so from about five
-// sequences on the tensor cores bound it and not memory. What a sequence has
-// behind the prefix is left to the split kernel, and the LSE combine joins both
-// by their log-sum-exps.
+// sequences on the tensor cores bound it and not memory. The tokens behind the
+// prefix are bound by memory. Both are row tiles of one line of work, so that some SMs
+// stream while others compute; the LSE combine joins a sequence's parts.
 //
-// Tile: a cluster of two CTAs works on 256 rows (four sequences, two a CTA)
-// against 128 keys (two pages) with tcgen05 MMAs of cta_group::2: each CTA
-// holds the Q rows of its two sequences, one of the two K pages and half of
-// V's dimensions, and both halves feed the pair's MMAs. Against one CTA with
-// 128 rows this halves what every SM reads from L2 (128 KB in 2048 tensor
-// cycles, which L2 cannot serve to 152 SMs) and what the MMAs read from shared
-// memory for B. TMEM holds S twice (2 x 128 columns, P overwrites S in place as
-// 64 columns of bf16 pairs, and is the A operand of P V from there) and O (256
-// columns): all of it.
+// Tile: a cluster of two CTAs works on 256 rows (four sequences of a group, two
+// a CTA; one sequence for its own tokens) against units of 128 keys (two pages)
+// with tcgen05 MMAs of cta_group::2: each CTA holds the Q rows of its
+// sequences, one of the two K pages and half of V's dimensions, and both halves
+// feed the pair's MMAs. Against one CTA with 128 rows this halves what every SM
+// reads from L2 (128 KB in 2048 tensor cycles, which L2 cannot serve to 152
+// SMs) and what the MMAs read from shared memory for B. A sequence's own tokens
+// use a quarter of the rows, but then a unit still takes the tensor cores less
+// time (2048 cycles for a pair) than HBM at its share of the bandwidth (128 KB).
+// TMEM holds S twice (2 x 128 columns; P overwrites S in place and is the A
+// operand of P V from there) and O (256 columns): all of it.
 //
-// Work split: the row tiles of all groups, one after the other, form a line of
-// units (one unit = one tile of 128 keys, and kPieceUnits for every tile's Q load and
-// partial result); each pair takes an equal range of it (stream-K) and writes
-// a normalised partial result and its LSE per row tile that it holds units of.
+// Work split: the row tiles, one after the other, form a line of units
+// (kPrefixPieceUnits more for every tile: its Q load and partial result); each
+// pair takes an equal range of it (stream-K) and writes a normalised partial
+// result and its LSE per row tile that it holds units of.
 //
-// Warp roles: warps 0-3 softmax (thread = row = TMEM lane: no exchange between
-// threads; the reference maximum moves only when a row exceeds it by 2^8, then
-// O is rescaled), warp 4 producer (TMA, each CTA its own halves, completing on
-// the leader's barriers), warp 5 MMA issue (the leader's only).
+// Warp roles:
+//   warps 0-7  softmax: thread = row = TMEM lane; warp w and w + 4 share 32
+//              rows, 64 keys of a unit each, and agree on the reference maximum, which moves
+//              only when a row exceeds it by 2^8 (then O is rescaled).
+//   warp 8     producer (TMA, each CTA its own halves, completing on the leader's barriers).
+//   warp 9     MMA issue (one thread of the leader) and TMEM allocation.
+//   warp 10    the rows behind a sequence's last token in V, zeroed up to the
+//              end of an MMA's 16 (E4M3: 32) keys: 0 * NaN of a stale row would poison P V.
 // Every wait is bounded (the wait budget), as in the split kernel.
 //
 // E4M3 cache: both products are 8-bit MMAs (kind::f8f6f4) on the raw codes. Q
@@ -46,53 +53,65 @@
 namespace mfa {
 namespace {
 
-constexpr int kThreads = 192;
-constexpr int kSoftmaxWarps = 4, kProducerWarp = 4, kMmaWarp = 5;
+constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kTailWarp = 10;
+constexpr int kThreads = 352;
 // Ring of 16 KB granules. bf16: half of a K page (128 dims), or 128 dims of a V page; E4M3: a K page, or 128 dims of
 // two V pages.
 template <bool kFp8>
 __host__ __device__ constexpr int slots() { return kFp8 ? 8 : 9; }
+constexpr int kMaxSlots = 9;
 constexpr int kGranule = 16384;
+constexpr int kUnitKeys = 2 * kPageSize;
 constexpr int kScaleSlots = 4;         // E4M3: 128 K scales and 128 V scales a unit
 constexpr int kScaleBytes = 1024;
+constexpr int kTails = 4;              // partial last units in flight: fewer fit the ring
 constexpr int kQBytes = 65536;         // 128 rows x 256 dims, four 64-dim blocks of [128 rows x 128 B]
+constexpr int kSeqQBytes = 32768;      // one sequence's rows
 constexpr int kTmemCols = 512, kTmemO = 256, kSCols = 128;
-constexpr int kTileRows = 256;         // of the pair, 128 a CTA
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kTop = 8.0f;           // log2 units: P (E4M3: P * v_scale) stays below 2^8 between moves of the reference
 // Where a move leaves the largest of them: 2^0, and 2^5 for E4M3, whose small weights then lie above its smallest steps.
 template <bool kFp8>
 __host__ __device__ constexpr float headroom() { return kFp8 ? 3.0f : kTop; }
-static_assert(kTileRows == kPrefixTileSeqs * kHeads, "rows of a row tile");
+// Keys of one MMA of P V.
+template <bool kFp8>
+__host__ __device__ constexpr int key_step() { return kFp8 ? 32 : 16; }
+static_assert(kPrefixTileSeqs * kHeads == 256, "rows of a row tile");
 
-constexpr int kMaxSlots = 9;
 enum Bar {
   Full = 0,                  // [slots] leader: both CTAs' halves landed
   Empty = Full + kMaxSlots,  // [slots] both: the MMAs reading the granule are done
   QFull = Empty + kMaxSlots, // bf16: leader; E4M3: both, each its own rows
   QReady,                    // E4M3, leader: Q split into terms, one arrival per softmax warp of the pair
   QEmpty,                    // both
-  SFull,                    // [2] both
-  PFull = SFull + 2,        // [2] leader: one arrival per softmax warp of the pair
-  PvDone = PFull + 2,       // [2] both: P V of even and odd units
-  OFree = PvDone + 2,                   // leader: O has been read, one arrival per softmax warp of the pair
-  Drain,                    // leader
-  ScFull,                   // [kScaleSlots] E4M3, both
-  ScEmpty = ScFull + kScaleSlots,  // one arrival per softmax warp of the CTA
-  kBars = ScEmpty + kScaleSlots
+  SFull,                     // [2] both
+  PFull = SFull + 2,         // [2] leader: one arrival per softmax warp of the pair
+  PvDone = PFull + 2,        // [2] both: P V of even and odd units
+  OFree = PvDone + 2,        // leader: O has been read, one arrival per softmax warp of the pair
+  Drain,                     // leader
+  ScFull,                    // [kScaleSlots] E4M3, both
+  ScEmpty = ScFull + kScaleSlots,   // [kScaleSlots] one arrival per softmax warp of the CTA
+  TailFull = ScEmpty + kScaleSlots, // [kTails] both: this CTA's V of a partial last unit landed
+  TailReady = TailFull + kTails,    // [kTails] leader: its rows behind the last token are zero, one arrival a CTA
+  kBars = TailReady + kTails
 };
 
-// Groups as every CTA sees them. Sizes and indices of sequences and tiles fit
-// 16 bits (at most 1024 sequences).
+// The line of work as every CTA sees it. Indices of sequences and tiles fit 16 bits (at most 1024 sequences).
 struct PlanSmem {
-  int32_t cost[kMaxBatch + 1];    // units before group g
-  int32_t pages[kMaxBatch];       // prefix pages
-  uint16_t b0[kMaxBatch + 2];     // first sequence
-  uint16_t lead[kMaxBatch];       // the sequence whose table row gives the prefix pages; kUnshared: not shared
-  uint16_t tile[kMaxBatch + 2];   // row tiles before group g
+  int32_t cost[kMaxBatch + 1];   // units of the prefix tiles of the groups before g; [n_groups]: of all
+  int32_t own[kMaxBatch + 1];    // units of the own tokens of the sequences before b
+  uint16_t b0[kMaxBatch + 2];    // first sequence of group g
+  uint16_t lead[kMaxBatch];      // the sequence whose table row gives the prefix pages, | kOdd; kUnshared: not shared
+  uint16_t tile[kMaxBatch + 2];  // prefix tiles of the groups before g
+  uint16_t tail[kMaxBatch];      // keys in the last unit of b's own tokens (0: it has none), | kBehind
 };
-constexpr uint16_t kUnshared = 0xFFFF;
+constexpr uint16_t kOdd = 0x8000;       // the prefix has an odd number of pages
+constexpr uint16_t kUnshared = 0x7FFF;
+constexpr uint16_t kBehind = 0x8000;    // b's own tokens begin behind its group's prefix
+struct PlanScratch {
+  int32_t count[kMaxBatch], lead[kMaxBatch], pages[kMaxBatch], len[kMaxBatch], group[kMaxBatch];
+};
 
 template <bool kFp8>
 struct Smem {
@@ -100,12 +119,13 @@ struct Smem {
   static constexpr uint32_t q = slots<kFp8>() * kGranule;
   static constexpr uint32_t scales = q + kQBytes;
   static constexpr uint32_t plan = scales + (kFp8 ? kScaleSlots * kScaleBytes : 0);
-  static constexpr uint32_t bars = (plan + (uint32_t)sizeof(PlanSmem) + 7) & ~7u;
-  static constexpr uint32_t misc = bars + 8 * kBars;
-  static constexpr uint32_t total = misc + 16;
+  static constexpr uint32_t red = (plan + (uint32_t)sizeof(PlanSmem) + 15) & ~15u;  // [2][128] exchange of the row halves
+  static constexpr uint32_t bars = red + 2 * 128 * 4;
+  static constexpr uint32_t misc = bars + 8 * kBars;  // TMEM base, abort flag, granules of the tails
+  static constexpr uint32_t total = misc + 8 + 4 * kTails;
 };
 static_assert(Smem<false>::total + 1024 <= 227 * 1024 && Smem<true>::total + 1024 <= 227 * 1024, "shared memory");
-static_assert(slots<true>() * kGranule >= 2 * 4 * kMaxBatch, "the plan's scratch lies in the ring");
+static_assert(slots<true>() * kGranule >= (int)sizeof(PlanScratch), "the plan's scratch lies in the ring");
 
 // ---------------------------------------------------------------- cluster pair
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -223,29 +243,42 @@ __device__ __forceinline__ int last_at_most(const T* a, int n, int x) {
   }
   return lo;
 }
-__device__ __forceinline__ int units_of(int pages) { return (pages + 1) / 2; }
+__device__ __forceinline__ int warp_inclusive_sum(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+__device__ __forceinline__ int tiles_of_group(const PlanSmem& s, int g) {
+  return (s.b0[g + 1] - s.b0[g] + kPrefixTileSeqs - 1) / kPrefixTileSeqs;
+}
+// Pages of a shared group's prefix.
+__device__ __forceinline__ int pages_of_group(const PlanSmem& s, int g) {
+  const int units = (s.cost[g + 1] - s.cost[g]) / tiles_of_group(s, g) - kPrefixPieceUnits;
+  return 2 * units - ((s.lead[g] & kOdd) ? 1 : 0);
+}
 
 // A group shares its prefix if at least two of its sequences hold all of it;
-// a sequence that ends inside it (or an empty slot of the batch) is left to the
-// split kernel as a whole, so that no row of the shared product has a mask and
-// nothing behind its last token is ever read for it. All threads; ends with a
-// barrier. t: 2 * kMaxBatch ints of scratch.
-__device__ void build_plan(const PrefixParams& p, PlanSmem& s, int32_t* t, uint32_t* err) {
-  const int n = p.n_groups;
-  int32_t* cnt = t;
-  int32_t* lead = t + kMaxBatch;
+// a sequence that ends inside it (or an empty slot of the batch) is read on its
+// own, so that no row of a shared product has a mask and nothing behind its
+// last token is ever read for it. All threads; ends with a barrier.
+__device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, uint32_t* err) {
+  const int n = p.n_groups, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   for (int g = threadIdx.x; g < n; g += kThreads) {
     int pages = __ldcg(p.prefix_pages + g);
     if (pages < 0 || pages > p.max_pages) {
       raise_error(err, MFA_DEVERR_CAPACITY);
       pages = pages < 0 ? 0 : p.max_pages;
     }
-    s.pages[g] = pages;
-    cnt[g] = 0;
-    lead[g] = kMaxBatch;
+    t.pages[g] = pages;
+    t.count[g] = 0;
+    t.lead[g] = kMaxBatch;
   }
-  if (threadIdx.x < 32) {  // starts, made non-decreasing within [0, B]: no sequence lies in two groups
-    const int lane = threadIdx.x;
+  for (int b = threadIdx.x; b < p.B; b += kThreads)
+    t.len[b] = clamp_len(__ldcg(p.seq_lens + b), p.max_pages * kPageSize, err);
+  if (warp == kThreads / 32 - 1) {  // starts, made non-decreasing within [0, B]: no sequence lies in two groups
     int top = 0;
     for (int g0 = 0; g0 <= n; g0 += 32) {
       const int g = g0 + lane;
@@ -265,41 +298,59 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, int32_t* t, uint3
     }
   }
   __syncthreads();
-  const int b_end = s.b0[n];
-  for (int b = s.b0[0] + (int)threadIdx.x; b < b_end; b += kThreads) {
-    const int g = last_at_most(s.b0, n + 1, b), pages = s.pages[g];
-    if (pages > 0 && __ldcg(p.seq_lens + b) >= pages * kPageSize) {
-      atomicAdd(cnt + g, 1);
-      atomicMin(lead + g, b);
+  for (int b = threadIdx.x; b < p.B; b += kThreads) {
+    int of = -1;
+    if (b >= s.b0[0] && b < s.b0[n]) {
+      const int g = last_at_most(s.b0, n + 1, b), pages = t.pages[g];
+      if (pages > 0 && t.len[b] >= pages * kPageSize) {
+        of = g;
+        atomicAdd(&t.count[g], 1);
+        atomicMin(&t.lead[g], b);
+      }
     }
+    t.group[b] = of;
   }
   __syncthreads();
-  if (threadIdx.x < 32) {
-    const int lane = threadIdx.x;
+  if (warp == 0) {
     int units = 0, tiles = 0;
     for (int g0 = 0; g0 < n; g0 += 32) {
       const int g = g0 + lane;
-      const bool shared = g < n && cnt[g] >= 2;
-      const int nt = shared ? (s.b0[g + 1] - s.b0[g] + kPrefixTileSeqs - 1) / kPrefixTileSeqs : 0;
-      const int nu = shared ? nt * (units_of(s.pages[g]) + kPrefixPieceUnits) : 0;
-      int x = nu, y = nt;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int a = __shfl_up_sync(0xffffffffu, x, o), b = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) {
-          x += a;
-          y += b;
-        }
-      }
+      const bool shared = g < n && t.count[g] >= 2;
+      const int nt = shared ? tiles_of_group(s, g) : 0;
+      const int nu = shared ? nt * ((t.pages[g] + 1) / 2 + kPrefixPieceUnits) : 0;
+      const int x = warp_inclusive_sum(nu, lane), y = warp_inclusive_sum(nt, lane);
       if (g < n) {
         s.cost[g] = units + x - nu;
         s.tile[g] = (uint16_t)(tiles + y - nt);
-        s.lead[g] = shared ? (uint16_t)lead[g] : kUnshared;
+        s.lead[g] = shared ? (uint16_t)(t.lead[g] | ((t.pages[g] & 1) ? kOdd : 0)) : kUnshared;
       }
       units += __shfl_sync(0xffffffffu, x, 31);
       tiles += __shfl_sync(0xffffffffu, y, 31);
     }
     if (lane == 0) s.cost[n] = units;
+  } else if (warp == 1) {
+    int units = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const int b = b0 + lane;
+      int rest = 0, u = 0;
+      uint16_t behind = 0;
+      if (b < p.B) {
+        const int g = t.group[b];
+        rest = t.len[b];
+        if (g >= 0 && t.count[g] >= 2) {
+          rest -= t.pages[g] * kPageSize;
+          behind = kBehind;
+        }
+        u = rest > 0 ? (rest + kUnitKeys - 1) / kUnitKeys + kPrefixPieceUnits : 0;
+      }
+      const int x = warp_inclusive_sum(u, lane);
+      if (b < p.B) {
+        s.own[b] = units + x - u;
+        s.tail[b] = (uint16_t)((rest > 0 ? (rest - 1) % kUnitKeys + 1 : 0) | behind);
+      }
+      units += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s.own[p.B] = units;
   }
   fence_proxy_async_smem();  // the scratch is TMA's from here on
   __syncthreads();
@@ -308,43 +359,65 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, int32_t* t, uint3
 // Pairs that have work: with fewer units than pairs, every range holds one.
 __device__ __forceinline__ int busy_pairs(const PrefixParams& p, int units) { return min(p.pairs, max(units, 1)); }
 
-// What the later kernels of the call need to know of each sequence: the pages
-// they skip, and where its partial results over the prefix are.
+// Where the combine finds each sequence's partial results.
 __device__ void publish_plan(const PrefixParams& p, const PlanSmem& s) {
-  const int n = p.n_groups, C = s.cost[n], W = busy_pairs(p, C);
+  const int n = p.n_groups, C1 = s.cost[n], C = C1 + s.own[p.B], W = busy_pairs(p, C);
   for (int b = blockIdx.x * kThreads + threadIdx.x; b < p.B; b += gridDim.x * kThreads) {
-    int skip = 0;
-    int2 parts = make_int2(0, 0);
-    if (b >= s.b0[0] && b < s.b0[n]) {
-      const int g = last_at_most(s.b0, n + 1, b), pages = s.pages[g];
-      if (s.lead[g] != kUnshared && __ldcg(p.seq_lens + b) >= pages * kPageSize) {
-        const int u = units_of(pages), j = b - s.b0[g], i = j / kPrefixTileSeqs;
-        const long long x0 = (long long)s.cost[g] + (long long)i * (u + kPrefixPieceUnits) + kPrefixPieceUnits;
-        const int w0 = cta_of_cost(x0, C, W), w1 = cta_of_cost(x0 + u - 1, C, W);
-        skip = pages;
-        parts = make_int2((w0 + s.tile[g] + i) * kPrefixTileSeqs + j % kPrefixTileSeqs, w1 - w0 + 1);
-      }
+    int4 parts = make_int4(0, 0, 0, 0);
+    if (s.tail[b] & kBehind) {
+      const int g = last_at_most(s.b0, n + 1, b), j = b - s.b0[g], i = j / kPrefixTileSeqs;
+      const int len = (s.cost[g + 1] - s.cost[g]) / tiles_of_group(s, g);  // units of one tile
+      const long long x = s.cost[g] + (long long)i * len;
+      const int w = cta_of_cost(x + kPrefixPieceUnits, C, W);
+      parts.x = (w + s.tile[g] + i) * kPrefixTileSeqs + j % kPrefixTileSeqs;
+      parts.y = cta_of_cost(x + len - 1, C, W) - w + 1;
     }
-    p.skip[b] = skip;
+    if (s.tail[b] & ~kBehind) {
+      const int w = cta_of_cost((long long)C1 + s.own[b] + kPrefixPieceUnits, C, W);
+      parts.z = p.own_row0 + w + b;
+      parts.w = cta_of_cost((long long)C1 + s.own[b + 1] - 1, C, W) - w + 1;
+    }
     p.parts[b] = parts;
   }
 }
 
 // A pair's pieces, in order: units [u0, u1) of one row tile.
 struct Piece {
-  int g, i;        // group, row tile of the group
-  int u0, u1;      // units
-  int pages;       // pages of the prefix
-  long long x;     // line position behind the tile
+  const int32_t* pages;  // page-table entries of the tile's keys
+  int b, seqs;           // first sequence, sequences (1 to kPrefixTileSeqs)
+  int keys;              // keys of the tile
+  int u0, u1;            // units
+  int row;               // partial result of its first sequence
+  bool own;              // a sequence's own tokens
+  long long x;           // line position behind the tile
 };
-__device__ __forceinline__ bool next_piece(const PlanSmem& s, int n, long long hi, Piece& q) {
+__device__ __forceinline__ bool next_piece(const PrefixParams& p, const PlanSmem& s, int pair, long long hi, Piece& q) {
+  const int n = p.n_groups, C1 = s.cost[n];
   while (q.x < hi) {
-    q.g = last_at_most(s.cost, n, (int)q.x);
-    q.pages = s.pages[q.g];
-    const int len = units_of(q.pages) + kPrefixPieceUnits;
-    const int local = (int)q.x - s.cost[q.g];
-    q.i = local / len;
-    const long long first = (long long)s.cost[q.g] + (long long)q.i * len;
+    long long first;
+    int len;
+    q.own = q.x >= C1;
+    if (!q.own) {
+      const int g = last_at_most(s.cost, n, (int)q.x), lead = s.lead[g] & ~kOdd;
+      len = (s.cost[g + 1] - s.cost[g]) / tiles_of_group(s, g);
+      const int i = ((int)q.x - s.cost[g]) / len;
+      first = s.cost[g] + (long long)i * len;
+      q.b = s.b0[g] + i * kPrefixTileSeqs;
+      q.seqs = min(kPrefixTileSeqs, s.b0[g + 1] - q.b);
+      q.keys = (len - kPrefixPieceUnits) * kUnitKeys - ((s.lead[g] & kOdd) ? kPageSize : 0);
+      q.pages = p.page_table + (size_t)lead * p.max_pages;
+      q.row = (pair + s.tile[g] + i) * kPrefixTileSeqs;
+    } else {
+      const int b = last_at_most(s.own, p.B, (int)(q.x - C1)), tail = s.tail[b];
+      len = s.own[b + 1] - s.own[b];
+      first = (long long)C1 + s.own[b];
+      q.b = b;
+      q.seqs = 1;
+      q.keys = (len - kPrefixPieceUnits - 1) * kUnitKeys + (tail & ~kBehind);
+      q.pages = p.page_table + (size_t)b * p.max_pages;
+      if (tail & kBehind) q.pages += pages_of_group(s, last_at_most(s.b0, n + 1, b));
+      q.row = p.own_row0 + pair + b;
+    }
     q.u0 = max(0, (int)(q.x - first) - kPrefixPieceUnits);
     q.u1 = (int)min((long long)len, hi - first) - kPrefixPieceUnits;
     q.x = first + len;
@@ -352,11 +425,14 @@ __device__ __forceinline__ bool next_piece(const PlanSmem& s, int n, long long h
   }
   return false;
 }
-__device__ __forceinline__ int pages_in_unit(const Piece& q, int u) { return 2 * u + 1 < q.pages ? 2 : 1; }
+__device__ __forceinline__ int keys_in_unit(const Piece& q, int u) { return min(kUnitKeys, q.keys - u * kUnitKeys); }
+// A last unit whose last MMA of P V reaches behind the sequence's last token.
+template <bool kFp8>
+__device__ __forceinline__ bool is_tail(const Piece& q, int valid) { return q.own && valid % key_step<kFp8>() != 0; }
 
 // ---------------------------------------------------------------- producer
-// Page ids of the prefix: a window of 64 held by the warp (32 ahead of need).
-struct PrefixPages {
+// Page ids of a tile: a window of 64 held by the warp (32 ahead of need).
+struct TilePages {
   const int32_t* row;
   int end, base, a, b;
   __device__ int fetch(int pg, const PrefixParams& p) const {
@@ -384,13 +460,13 @@ struct PrefixPages {
 
 template <bool kFp8>
 __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                              const CUtensorMap* qmap, const Ctx& cx, const PlanSmem& s, long long lo, long long hi) {
-  const int lane = threadIdx.x & 31;
+                              const CUtensorMap* qmap, const Ctx& cx, const PlanSmem& s, int pair, long long lo,
+                              long long hi, volatile uint32_t* tail_granule) {
   constexpr int kSlots = slots<kFp8>();
   using Sm = Smem<kFp8>;
-  const int r = (int)cx.rank;
-  const uint64_t pol = policy_evict_normal();
-  uint32_t cc = 0, pieces = 0, units = 0;
+  const int lane = threadIdx.x & 31, r = (int)cx.rank;
+  const uint64_t pol_shared = policy_evict_normal(), pol_own = policy_evict_first();
+  uint32_t cc = 0, pieces = 0, units = 0, tails = 0;
   // The next granule: its address, and the leader's barrier of it, on which the leader announces `bytes` of both CTAs.
   auto next_slot = [&](uint32_t bytes, uint32_t& dst, uint32_t& bar) -> bool {
     const uint32_t slot = cc % kSlots, n = cc / kSlots;
@@ -402,11 +478,12 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
     return true;
   };
   // K of one unit: this CTA's page (page r of the two); bf16: in two granules of 128 dims
-  auto load_k = [&](int pa, int pb) -> bool {
+  auto load_k = [&](int pa, int pb, uint64_t pol) -> bool {
     const int page = r == 0 ? pa : pb;
+    const uint32_t bytes = pb >= 0 ? 2 * kGranule : kGranule;
+    uint32_t dst, bar;
     if constexpr (kFp8) {
-      uint32_t dst, bar;
-      if (!next_slot(pb >= 0 ? 2 * kGranule : kGranule, dst, bar)) return false;
+      if (!next_slot(bytes, dst, bar)) return false;
       if (lane == 0 && page >= 0) {
         tma_load_2d_pair(dst, kmap, 0, page * kPageSize, bar, pol);
         tma_load_2d_pair(dst + 8192, kmap, 128, page * kPageSize, bar, pol);
@@ -426,36 +503,48 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
           bulk_load(sc + 512 + kPageScales, p.v_scale + (size_t)pb * kPageSize, kPageScales, sb);
         }
       }
-      return true;
-    }
-    for (int h = 0; h < 2; ++h) {
-      uint32_t dst, bar;
-      if (!next_slot(pb >= 0 ? 2 * kGranule : kGranule, dst, bar)) return false;
-      if (lane == 0 && page >= 0) {
-        tma_load_2d_pair(dst, kmap, h * 128, page * kPageSize, bar, pol);
-        tma_load_2d_pair(dst + 8192, kmap, h * 128 + 64, page * kPageSize, bar, pol);
+    } else {
+      for (int h = 0; h < 2; ++h) {
+        if (!next_slot(bytes, dst, bar)) return false;
+        if (lane == 0 && page >= 0) {
+          tma_load_2d_pair(dst, kmap, h * 128, page * kPageSize, bar, pol);
+          tma_load_2d_pair(dst + 8192, kmap, h * 128 + 64, page * kPageSize, bar, pol);
+        }
       }
     }
     return true;
   };
-  // V of one unit: this CTA's 128 dims of each page; bf16: a granule a page
-  auto load_v = [&](int pa, int pb) -> bool {
+  // V of one unit: this CTA's 128 dims of each page; bf16: a granule a page. The granule with the last page of a tail
+  // lands on this CTA's own barrier, for the warp that zeroes its rows.
+  auto load_v = [&](int pa, int pb, bool tail, uint64_t pol) -> bool {
+    uint32_t dst, bar;
+    auto to_tail = [&](uint32_t bytes) {
+      const uint32_t t = tails++ % kTails;
+      bar = cx.bar(TailFull + t);
+      if (lane == 0) {
+        tail_granule[t] = dst;
+        mbar_arrive_expect_tx(bar, bytes);
+      }
+    };
     if constexpr (kFp8) {
-      uint32_t dst, bar;
-      if (!next_slot(pb >= 0 ? 2 * kGranule : kGranule, dst, bar)) return false;
+      const uint32_t bytes = pb >= 0 ? kGranule : kGranule / 2;
+      if (!next_slot(tail ? 0 : 2 * bytes, dst, bar)) return false;
+      if (tail) to_tail(bytes);
       if (lane == 0) {
         tma_load_2d_pair(dst, vmap, r * 128, pa * kPageSize, bar, pol);
         if (pb >= 0) tma_load_2d_pair(dst + 8192, vmap, r * 128, pb * kPageSize, bar, pol);
       }
-      return true;
-    }
-    for (int i = 0; i < (pb >= 0 ? 2 : 1); ++i) {
-      uint32_t dst, bar;
-      if (!next_slot(2 * kGranule, dst, bar)) return false;
-      const int page = i ? pb : pa;
-      if (lane == 0) {
-        tma_load_2d_pair(dst, vmap, r * 128, page * kPageSize, bar, pol);
-        tma_load_2d_pair(dst + 8192, vmap, r * 128 + 64, page * kPageSize, bar, pol);
+    } else {
+      const int np = pb >= 0 ? 2 : 1;
+      for (int i = 0; i < np; ++i) {
+        const bool last = tail && i == np - 1;
+        if (!next_slot(last ? 0 : 2 * kGranule, dst, bar)) return false;
+        if (last) to_tail(kGranule);
+        const int page = i ? pb : pa;
+        if (lane == 0) {
+          tma_load_2d_pair(dst, vmap, r * 128, page * kPageSize, bar, pol);
+          tma_load_2d_pair(dst + 8192, vmap, r * 128 + 64, page * kPageSize, bar, pol);
+        }
       }
     }
     return true;
@@ -463,72 +552,111 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
   Piece q;
   q.x = lo;
   int va = -1, vb = -1;  // the unit whose V is still to be loaded: V trails K by a unit, as the MMAs use them
-  bool good = true;
-  while (good && next_piece(s, p.n_groups, hi, q)) {
-    PrefixPages ids;
-    ids.row = p.page_table + (size_t)s.lead[q.g] * p.max_pages;
-    ids.end = min(q.pages, 2 * q.u1);
+  bool vtail = false, good = true;
+  uint64_t vpol = pol_own;
+  while (good && next_piece(p, s, pair, hi, q)) {
+    TilePages ids;
+    ids.row = q.pages;
+    ids.end = min((q.keys + kPageSize - 1) / kPageSize, 2 * q.u1);
     ids.start(2 * q.u0, p, lane);
+    const uint64_t pol = q.own ? pol_own : pol_shared;
     good = cx.wait_warp(QEmpty, (pieces & 1) ^ 1);
     if (!good) break;
     if (lane == 0) {
-      const int row0 = (s.b0[q.g] + q.i * kPrefixTileSeqs + 2 * r) * kHeads;  // rows past the batch read zeros
+      const int here = min(2, max(0, q.seqs - 2 * r));  // this CTA's sequences
       if (kFp8)
-        mbar_arrive_expect_tx(cx.bar(QFull), kQBytes);
+        mbar_arrive_expect_tx(cx.bar(QFull), here * kSeqQBytes);
       else if (r == 0)
-        mbar_arrive_expect_tx(cx.bar(QFull), 2 * kQBytes);
+        mbar_arrive_expect_tx(cx.bar(QFull), q.seqs * kSeqQBytes);
       const uint32_t bar = kFp8 ? cx.bar(QFull) : cx.leader_bar(QFull);
       for (int d = 0; d < 4; ++d)
-        for (int h = 0; h < 2; ++h)
-          tma_load_2d_pair(cx.base + Sm::q + d * 16384 + h * 8192, qmap, d * 64, row0 + h * 64, bar, pol);
+        for (int h = 0; h < here; ++h)
+          tma_load_2d_pair(cx.base + Sm::q + d * 16384 + h * 8192, qmap, d * 64, (q.b + 2 * r + h) * kHeads, bar, pol_shared);
     }
     ++pieces;
     for (int u = q.u0; good && u < q.u1; ++u) {
+      const int valid = keys_in_unit(q, u);
       const int pa = ids.get(2 * u, p, lane);
-      const int pb = pages_in_unit(q, u) == 2 ? ids.get(2 * u + 1, p, lane) : -1;
-      good = load_k(pa, pb);
-      if (good && va >= 0) good = load_v(va, vb);
+      const int pb = valid > kPageSize ? ids.get(2 * u + 1, p, lane) : -1;
+      good = load_k(pa, pb, pol);
+      if (good && va >= 0) good = load_v(va, vb, vtail, vpol);
       va = pa;
       vb = pb;
+      vtail = is_tail<kFp8>(q, valid);
+      vpol = pol;
     }
     if (kFp8 && good) {  // E4M3: the next row tile's Q is split only behind this one's last P V
-      good = load_v(va, vb);
+      good = load_v(va, vb, vtail, vpol);
       va = -1;
     }
   }
-  if (good && va >= 0) good = load_v(va, vb);
+  if (good && va >= 0) good = load_v(va, vb, vtail, vpol);
   // Every copy of both CTAs must land before either leaves: the leader's barriers tell, and the other CTA stays
-  // until the cluster's last barrier.
-  if (kFp8 && lane == 0) {
-    for (uint32_t k = (units > (uint32_t)kScaleSlots ? units - kScaleSlots : 0); k < units; ++k)
-      (void)mbar_wait(cx.bar(ScFull + k % kScaleSlots), (k / kScaleSlots) & 1, cx.budget, nullptr, p.err);
-    if (pieces) (void)mbar_wait(cx.bar(QFull), (pieces - 1) & 1, cx.budget, nullptr, p.err);
-  }
-  if (r == 0 && lane == 0) {
-    for (uint32_t k = (cc > (uint32_t)kSlots ? cc - kSlots : 0); k < cc; ++k)
-      (void)mbar_wait(cx.bar(Full + k % kSlots), (k / kSlots) & 1, cx.budget, nullptr, p.err);
-    if (!kFp8 && pieces) (void)mbar_wait(cx.bar(QFull), (pieces - 1) & 1, cx.budget, nullptr, p.err);
+  // until the cluster's last barrier (the copies of a tail are waited for where its rows are zeroed).
+  if (lane == 0) {
+    if constexpr (kFp8) {
+      for (uint32_t k = (units > (uint32_t)kScaleSlots ? units - kScaleSlots : 0); k < units; ++k)
+        (void)mbar_wait(cx.bar(ScFull + k % kScaleSlots), (k / kScaleSlots) & 1, cx.budget, nullptr, p.err);
+    }
+    if (pieces && (kFp8 || r == 0)) (void)mbar_wait(cx.bar(QFull), (pieces - 1) & 1, cx.budget, nullptr, p.err);
+    if (r == 0)
+      for (uint32_t k = (cc > (uint32_t)kSlots ? cc - kSlots : 0); k < cc; ++k)
+        (void)mbar_wait(cx.bar(Full + k % kSlots), (k / kSlots) & 1, cx.budget, nullptr, p.err);
   }
   __syncwarp();
 }
 
+// ---------------------------------------------------------------- rows behind the last token
+template <bool kFp8>
+__device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, long long lo, long long hi,
+                          volatile uint32_t* tail_granule) {
+  const int lane = threadIdx.x & 31;
+  uint32_t tails = 0;
+  Piece q;
+  q.x = lo;
+  while (next_piece(p, s, pair, hi, q)) {
+    const int valid = keys_in_unit(q, q.u1 - 1);
+    if (!is_tail<kFp8>(q, valid)) continue;
+    const uint32_t t = tails % kTails;
+    if (!cx.wait_warp(TailFull + t, (tails / kTails) & 1)) return;
+    ++tails;
+    // rows of 128 B: of one page and two 64-dim chunks (bf16), of one 128-dim chunk and two pages (E4M3)
+    constexpr int kChunks = kFp8 ? 1 : 2, kStep = key_step<kFp8>();
+    const uint32_t base = tail_granule[t] + (kFp8 ? (uint32_t)(valid / kPageSize) * 8192u : 0u);
+    const int row = valid % kPageSize, rows = kStep - valid % kStep;
+    for (int i = lane; i < rows * 8 * kChunks; i += 32) {
+      const uint32_t at = base + (i / (rows * 8)) * 8192 + row * 128 + (i % (rows * 8)) * 16;
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_cluster(cx.leader_bar(TailReady + t));
+  }
+}
+
 // ---------------------------------------------------------------- MMA issue (one thread of the leader)
 template <bool kFp8>
-__device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, long long lo, long long hi,
+__device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, long long lo, long long hi,
                          uint32_t tmem) {
-  constexpr uint32_t idesc_s = idesc_f16(256, kSCols, 1, 0, 0);  // A = Q, B = K, both K-major
-  constexpr uint32_t idesc_o = idesc_f16(256, kHeadDim, 1, 0, 1);  // A = P (TMEM), B = V (dim-major)
-  constexpr uint32_t idesc_s8 = idesc_f16(256, kSCols, 0, 0, 0), idesc_o8 = idesc_f16(256, kHeadDim, 0, 0, 1);  // E4M3
+  constexpr uint32_t idesc_s = idesc_f16(256, kSCols, kFp8 ? 0 : 1, 0, 0);    // A = Q, B = K, both K-major (E4M3: format 0)
+  constexpr uint32_t idesc_o = idesc_f16(256, kHeadDim, kFp8 ? 0 : 1, 0, 1);  // A = P (TMEM), B = V (dim-major)
   constexpr int kSlots = slots<kFp8>();
   using Sm = Smem<kFp8>;
-  uint32_t cc = 0, pieces = 0, s_cnt = 0, p_cnt = 0;
+  uint32_t cc = 0, pieces = 0, s_cnt = 0, p_cnt = 0, tails = 0;
+  auto granule = [&](uint32_t& addr) -> bool {
+    const uint32_t slot = cc % kSlots;
+    if (!cx.wait(Full + slot, (cc / kSlots) & 1)) return false;
+    tc_fence_after();
+    addr = cx.base + Sm::ring + slot * kGranule;
+    return true;
+  };
+  auto granule_done = [&]() { tc_commit_pair(cx.bar(Empty + cc++ % kSlots)); };
   auto do_s = [&]() -> bool {
     const uint32_t d = tmem + (s_cnt & 1) * kSCols;  // its last reader, P V of two units ago, was issued before
+    const uint32_t qa = cx.base + Sm::q;
+    uint32_t kb;
     if constexpr (kFp8) {
-      const uint32_t slot = cc % kSlots;
-      if (!cx.wait(Full + slot, (cc / kSlots) & 1)) return false;
-      tc_fence_after();
-      const uint32_t kb = cx.base + Sm::ring + slot * kGranule, qa = cx.base + Sm::q;
+      if (!granule(kb)) return false;
 #pragma unroll
       for (int t = 0; t < 2; ++t)  // Q's terms
 #pragma unroll
@@ -536,88 +664,83 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             tc_mma_pair_f8(d, smem_desc_sw128(qa + t * 32768 + h * 16384 + kk * 32, 16, 1024),
-                           smem_desc_sw128(kb + h * 8192 + kk * 32, 16, 1024), idesc_s8, (t | h | kk) != 0);
-      tc_commit_pair(cx.bar(Empty + slot));
-      ++cc;
-    }
-    for (int h = 0; !kFp8 && h < 2; ++h) {
-      const uint32_t slot = cc % kSlots;
-      if (!cx.wait(Full + slot, (cc / kSlots) & 1)) return false;
-      tc_fence_after();
-      const uint32_t kb = cx.base + Sm::ring + slot * kGranule;
+                           smem_desc_sw128(kb + h * 8192 + kk * 32, 16, 1024), idesc_s, (t | h | kk) != 0);
+      granule_done();
+    } else {
+      for (int h = 0; h < 2; ++h) {
+        if (!granule(kb)) return false;
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const uint32_t qa = cx.base + Sm::q + (2 * h + e) * 16384;
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_pair(d, smem_desc_sw128(qa + kk * 32, 16, 1024), smem_desc_sw128(kb + e * 8192 + kk * 32, 16, 1024),
-                      idesc_s, (h | e | kk) != 0);
+          for (int kk = 0; kk < 4; ++kk)
+            tc_mma_pair(d, smem_desc_sw128(qa + (2 * h + e) * 16384 + kk * 32, 16, 1024),
+                        smem_desc_sw128(kb + e * 8192 + kk * 32, 16, 1024), idesc_s, (h | e | kk) != 0);
+        granule_done();
       }
-      tc_commit_pair(cx.bar(Empty + slot));
-      ++cc;
     }
     tc_commit_pair(cx.bar(SFull + (s_cnt & 1)));
     ++s_cnt;
     return true;
   };
-  auto do_pv = [&](int np, bool first, uint32_t piece) -> bool {
-    const uint32_t buf = p_cnt & 1;
-    if (first && !cx.wait_pair(OFree, (piece & 1) ^ 1)) return false;
+  // P V of a unit of `valid` keys: as many MMAs as hold one
+  struct Unit {
+    int valid;
+    bool tail, first;
+    uint32_t piece;
+  };
+  auto do_pv = [&](const Unit& v) -> bool {
+    constexpr int kStep = key_step<kFp8>(), kSteps = kPageSize / kStep;
+    const uint32_t buf = p_cnt & 1, a = tmem + buf * kSCols, d = tmem + kTmemO;
+    if (v.first && !cx.wait_pair(OFree, (v.piece & 1) ^ 1)) return false;
     if (!cx.wait_pair(PFull + buf, (p_cnt >> 1) & 1)) return false;
-    if constexpr (kFp8) {
-      const uint32_t slot = cc % kSlots;
-      if (!cx.wait(Full + slot, (cc / kSlots) & 1)) return false;
-      tc_fence_after();
-      const uint32_t vb = cx.base + Sm::ring + slot * kGranule;
-      for (int i = 0; i < np; ++i)
-#pragma unroll
+    const int np = v.valid > kPageSize ? 2 : 1;
+    uint32_t vb = 0;
+    if (kFp8 && !granule(vb)) return false;
+    for (int i = 0; i < np; ++i) {
+      if (!kFp8 && !granule(vb)) return false;
+      if (v.tail && i == (kFp8 ? 0 : np - 1)) {
+        if (!cx.wait_pair(TailReady + tails % kTails, (tails / kTails) & 1)) return false;
+        ++tails;
+        tc_fence_after();
+      }
+      const int steps = min(kSteps, (v.valid - i * kPageSize + kStep - 1) / kStep);
+      if constexpr (kFp8) {
         for (int t = 0; t < 2; ++t)  // P's terms
-#pragma unroll
-          for (int kk = 0; kk < 2; ++kk)
-            tc_mma_pair_f8_tmem_a(tmem + kTmemO, tmem + buf * kSCols + t * 32 + i * 16 + kk * 8,
-                                  smem_desc_sw128(vb + i * 8192 + kk * 4096, 16, 1024), idesc_o8,
-                                  !(first && (i | t | kk) == 0));
-      tc_commit_pair(cx.bar(Empty + slot));
-      ++cc;
+          for (int kk = 0; kk < steps; ++kk)
+            tc_mma_pair_f8_tmem_a(d, a + t * 32 + i * 16 + kk * 8, smem_desc_sw128(vb + i * 8192 + kk * 4096, 16, 1024),
+                                  idesc_o, !(v.first && (i | t | kk) == 0));
+      } else {
+        for (int kk = 0; kk < steps; ++kk)
+          tc_mma_pair_tmem_a(d, a + i * 32 + kk * 8, smem_desc_sw128(vb + kk * 2048, 8192, 1024), idesc_o,
+                             !(v.first && (i | kk) == 0));
+        granule_done();
+      }
     }
-    for (int i = 0; !kFp8 && i < np; ++i) {
-      const uint32_t slot = cc % kSlots;
-      if (!cx.wait(Full + slot, (cc / kSlots) & 1)) return false;
-      tc_fence_after();
-      const uint32_t vb = cx.base + Sm::ring + slot * kGranule;
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        tc_mma_pair_tmem_a(tmem + kTmemO, tmem + buf * kSCols + i * 32 + kk * 8, smem_desc_sw128(vb + kk * 2048, 8192, 1024),
-                           idesc_o, !(first && i == 0 && kk == 0));
-      tc_commit_pair(cx.bar(Empty + slot));
-      ++cc;
-    }
+    if (kFp8) granule_done();
     tc_commit_pair(cx.bar(PvDone + buf));
     ++p_cnt;
     return true;
   };
   Piece q;
   q.x = lo;
-  int pend = 0;  // pages of the unit whose P V is still to be issued (0: none)
-  bool pend_first = false, good = true;
-  uint32_t pend_piece = 0;
-  while (good && next_piece(s, p.n_groups, hi, q)) {
+  Unit pend{0, false, false, 0};  // the unit whose P V is still to be issued (valid = 0: none)
+  bool good = true;
+  while (good && next_piece(p, s, pair, hi, q)) {
     good = kFp8 ? cx.wait_pair(QReady, pieces & 1) : cx.wait(QFull, pieces & 1);
     for (int u = q.u0; good && u < q.u1; ++u) {
       good = do_s();
       if (good && u == q.u1 - 1) tc_commit_pair(cx.bar(QEmpty));
-      if (good && pend) good = do_pv(pend, pend_first, pend_piece);
-      pend = pages_in_unit(q, u);
-      pend_first = u == q.u0;
-      pend_piece = pieces;
+      if (good && pend.valid) good = do_pv(pend);
+      const int valid = keys_in_unit(q, u);
+      pend = Unit{valid, is_tail<kFp8>(q, valid), u == q.u0, pieces};
     }
     if (kFp8 && good) {  // the softmax warps split the next Q once they have read this O
-      good = do_pv(pend, pend_first, pend_piece);
-      pend = 0;
+      good = do_pv(pend);
+      pend.valid = 0;
     }
     ++pieces;
   }
-  if (good && pend) (void)do_pv(pend, pend_first, pend_piece);
+  if (good && pend.valid) (void)do_pv(pend);
   tc_commit_pair(cx.bar(Drain));  // every MMA is done before TMEM is given back
   (void)mbar_wait(cx.bar(Drain), 0, cx.budget, nullptr, p.err);
 }
@@ -632,11 +755,35 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-// 32 lanes x 8 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]),
-               "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
+      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 // 32 bytes at once: a whole sector of one row a thread.
 __device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
@@ -644,29 +791,49 @@ __device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
 }
+// Barriers of the two warps that share 32 rows, and of all softmax warps.
+__device__ __forceinline__ void barrier_rows(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
+__device__ __forceinline__ bool barrier_rows_or(int quad, bool pred) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, 64, q;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(r)
+      : "r"((uint32_t)pred), "r"(1 + quad)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void barrier_softmax() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 
-// ---- E4M3: this thread's row of Q (four 64-dim blocks of [128 rows x 128 B], 128-byte swizzle) becomes, in place, two
-// E4M3 terms of Q * 2^e ([term][128-dim half][128 rows x 128 B]): t1 rounds the scaled value, t2 the rest, which is
-// exact unless it falls below the E4M3 normal range (2^-18.8 of the row's largest |q|). 2^e is the largest power of two
-// that keeps the row within the E4M3 maximum, 448. Returns 2^-e. All 128 threads.
-__device__ __noinline__ float split_q_row(uint32_t q_addr, int row) {
-  auto ld = [](uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-  };
-  uint4 v[32];  // 8 dims each
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+
+// E4M3: the bf16 Q of this CTA's 128 rows (four 64-dim blocks of [128 rows x 128 B], 128-byte swizzle) becomes, in
+// place, two E4M3 terms of Q * 2^e ([term][128-dim half][128 rows x 128 B]): t1 rounds the scaled value, t2 the rest,
+// which is exact unless it falls below the E4M3 normal range (2^-18.8 of the row's largest |q|). 2^e is the largest
+// power of two that keeps the row within the E4M3 maximum, 448. Thread (row, half) takes 128 dims of its row. All
+// softmax threads; red: their exchange. Returns 2^-e.
+__device__ __noinline__ float split_q(uint32_t q_addr, float* red, int row, int half) {
+  uint4 v[16];  // 8 dims each
 #pragma unroll
-  for (int j = 0; j < 32; ++j) v[j] = ld(q_addr + (j >> 3) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4));
-  asm volatile("bar.sync 1, 128;" ::: "memory");  // every row is in registers
+  for (int j = 0; j < 16; ++j)
+    v[j] = ld_shared_v4(q_addr + (2 * half + (j >> 3)) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4));
   float top = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 32; ++j) {
+  for (int j = 0; j < 16; ++j) {
     const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
   }
+  red[half * 128 + row] = top;
+  barrier_softmax();  // every row is in registers: the terms may overwrite it
+  top = fmaxf(red[row], red[128 + row]);
   int e = 0;
   if (top > 0.0f && top <= 3.0e38f) {
     const uint32_t bits = __float_as_uint(top);
@@ -675,7 +842,7 @@ __device__ __noinline__ float split_q_row(uint32_t q_addr, int row) {
   }
   const float up = __uint_as_float((uint32_t)(e + 127) << 23);
 #pragma unroll
-  for (int o = 0; o < 16; ++o) {  // 16 dims
+  for (int o = 0; o < 8; ++o) {  // 16 dims
     uint32_t t1[4], t2[4];
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
@@ -697,49 +864,56 @@ __device__ __noinline__ float split_q_row(uint32_t q_addr, int row) {
         t2[2 * u + i] = b;
       }
     }
-    const uint32_t at = q_addr + (o >> 3) * 16384 + row * 128 + (((o & 7) ^ (row & 7)) << 4);
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(t1[0]), "r"(t1[1]), "r"(t1[2]), "r"(t1[3]) : "memory");
-    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + 32768), "r"(t2[0]), "r"(t2[1]), "r"(t2[2]), "r"(t2[3]) : "memory");
+    const uint32_t at = q_addr + half * 16384 + row * 128 + ((o ^ (row & 7)) << 4);
+    st_shared_v4(at, t1);
+    st_shared_v4(at + 32768, t2);
   }
   fence_proxy_async_smem();
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
-// Two weights (times their V scales, at most 2^8) as two E4M3 terms each: c1 rounds them, c2 the rest, formed in f16
-// (c1 is exact in f16, and so is the difference).
-__device__ __forceinline__ void split_p2(float a, float b, uint32_t& c1, uint32_t& c2) {
-  const __half2 x = __floats2half2_rn(a, b);
-  const __nv_fp8x2_storage_t t1 = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3);
-  const __half2_raw d1 = __nv_cvt_fp8x2_to_halfraw2(t1, __NV_E4M3);
-  const __half2 rest = __hsub2(x, *reinterpret_cast<const __half2*>(&d1));
-  c1 = t1;
+// Two weights (times their V scales, in [0, 2^8]) as two E4M3 terms each. The first is their f16 value rounded to the
+// three mantissa bits of E4M3, in f16 by integer arithmetic on both halves (conversions are the scarce instruction
+// here: two of them a pair instead of three); the second rounds the rest. Below 2^-6, where E4M3 has fewer bits, the
+// first conversion rounds once more: an error of 2^-10 at most, 2^-15 of the unit's largest weight.
+__device__ __forceinline__ void split_p2(float2 x, uint32_t& c1, uint32_t& c2) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  const uint32_t bits = (*reinterpret_cast<const uint32_t*>(&h) + 0x00400040u) & 0xFF80FF80u;
+  __half2_raw r1;
+  r1.x = (unsigned short)bits;
+  r1.y = (unsigned short)(bits >> 16);
+  const __half2 rest = __hsub2(h, *reinterpret_cast<const __half2*>(&bits));
+  c1 = __nv_cvt_halfraw2_to_fp8x2(r1, __NV_SATFINITE, __NV_E4M3);
   c2 = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, __NV_E4M3);
 }
 
 template <bool kFp8>
-__device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, long long lo, long long hi,
-                             uint32_t tmem, int pair, const uint8_t* gbase) {
-  const int row = threadIdx.x & 127, lane = row & 31;
-  uint32_t pieces = 0;
-  const uint32_t lanes = (uint32_t)(row & ~31) << 16;
+__device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, long long lo,
+                             long long hi, uint32_t tmem, uint8_t* gbase) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
+  const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   const float c2 = p.scale * kLog2e;
+  const bool neg = p.scale < 0.0f;  // the smallest product then makes the largest logit
   const uint32_t p_full = cx.leader_bar(PFull), o_free = cx.leader_bar(OFree);
-  uint32_t cnt = 0;  // units so far
+  float* red = reinterpret_cast<float*>(gbase + Smem<kFp8>::red);
+  uint32_t cnt = 0, pieces = 0;  // units, pieces so far
   // P V of the unit before `cnt`. S of that unit is done, and with it every MMA issued before it, P V of two units
   // earlier (the last on the same barrier) among them: the parity is exact.
   auto wait_pv = [&]() -> bool { return cx.wait_warp(PvDone + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1); };
   Piece q;
   q.x = lo;
-  while (next_piece(s, p.n_groups, hi, q)) {
-    const int j = 2 * (int)cx.rank + (row >> 6);  // sequence of the row tile (the same for the whole warp)
-    const bool mine = s.b0[q.g] + q.i * kPrefixTileSeqs + j < s.b0[q.g + 1];
-    float m = -INFINITY, l = 0.0f;  // reference maximum (log2 units) and this row's denominator
-    float mul = c2;                 // of this row's products: the softmax scale, and 2^-e of its Q terms
+  while (next_piece(p, s, pair, hi, q)) {
+    const int j = 2 * (int)cx.rank + (quad >> 1);  // sequence of the row tile
+    const bool mine = j < q.seqs;
+    float m = -INFINITY, l = 0.0f;  // the row's reference (log2 units), and this thread's share of its denominator
+    float mul = c2;                 // of the row's products: the softmax scale, and 2^-e of its Q terms
     if constexpr (kFp8) {
       if (!cx.wait_warp(QFull, pieces & 1)) return;
-      mul *= split_q_row(cx.base + Smem<kFp8>::q, row);
+      mul *= split_q(cx.base + Smem<kFp8>::q, red, row, half);
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(cx.leader_bar(QReady));
+      barrier_rows(quad);  // red is free again
       ++pieces;
     }
     for (int u = q.u0; u < q.u1; ++u, ++cnt) {
@@ -750,58 +924,64 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       if (!cx.wait_warp(SFull + buf, (cnt >> 1) & 1)) return;
       tc_fence_after();
       if (mine) {
-        const bool both = pages_in_unit(q, u) == 2;
-        float x[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(ts + 32 * c, x + 32 * c);
-        tc_wait_ld();
+        const int valid = keys_in_unit(q, u), cols = min(64, valid - 64 * half);  // this thread's keys (none: <= 0)
+        float2 x[32];
+        tmem_ld32(ts + 64 * half, reinterpret_cast<float*>(x));
+        tmem_ld32(ts + 64 * half + 32, reinterpret_cast<float*>(x) + 32);
         float lift = 0.0f;  // E4M3: log2 of the unit's largest V scale
         if constexpr (kFp8) {
-          // products times the K scales; an absent page's scales are not there either
-#pragma unroll
-          for (int c = 0; c < 128; c += 4) {
-            if (c == 64 && !both) break;
-            const float4 k4 = reinterpret_cast<const float4*>(sc)[c / 4];
-            x[c] *= k4.x;
-            x[c + 1] *= k4.y;
-            x[c + 2] *= k4.z;
-            x[c + 3] *= k4.w;
+          float4 v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
+          if (4 * lane + 3 >= valid) {  // scales behind the last key are stale
+            if (4 * lane >= valid) v4.x = 0.0f;
+            if (4 * lane + 1 >= valid) v4.y = 0.0f;
+            if (4 * lane + 2 >= valid) v4.z = 0.0f;
+            v4.w = 0.0f;
           }
-          float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (both || lane < 16) v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
           const float most = fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w)));
           lift = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-          lift = fmaxf(log2f(lift), -90.0f);  // so that p stays far from 2^128 whatever the scales are
+          lift = fmaxf(__log2f(lift), -90.0f);  // so that p stays far from 2^128 whatever the scales are
         }
-        // the largest logit of the unit (of one page: the other half of S is not of this prefix); a negative scale
-        // makes it of the smallest product
+        tc_wait_ld();
+        if constexpr (kFp8) {  // products times the K scales
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float4 k4 = reinterpret_cast<const float4*>(sc + 64 * half)[c / 2];
+            x[c] = mul2(x[c], make_float2(k4.x, k4.y));
+            x[c + 1] = mul2(x[c + 1], make_float2(k4.z, k4.w));
+          }
+        }
+        if (cols < 64) {  // behind the last key: out of the maximum, and weights of 0 below
+          const float out = neg ? 3.0e38f : -3.0e38f;
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            if (2 * c >= cols) x[c].x = out;
+            if (2 * c + 1 >= cols) x[c].y = out;
+          }
+        }
         float top[4];
-        if (mul >= 0.0f) {
+        if (!neg) {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) top[c & 3] = c < 4 ? x[c] : fmaxf(top[c & 3], x[c]);
-          if (both)
-#pragma unroll
-            for (int c = 64; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], x[c]);
+          for (int c = 0; c < 32; ++c) top[c & 3] = c < 4 ? fmaxf(x[c].x, x[c].y) : max3(top[c & 3], x[c].x, x[c].y);
         } else {
 #pragma unroll
-          for (int c = 0; c < 64; ++c) top[c & 3] = c < 4 ? -x[c] : fmaxf(top[c & 3], -x[c]);
-          if (both)
-#pragma unroll
-            for (int c = 64; c < 128; ++c) top[c & 3] = fmaxf(top[c & 3], -x[c]);
+          for (int c = 0; c < 32; ++c) top[c & 3] = c < 4 ? fmaxf(-x[c].x, -x[c].y) : max3(top[c & 3], -x[c].x, -x[c].y);
         }
         float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(mul);
-        big += lift - (kTop - headroom<kFp8>());
-        if (__any_sync(0xffffffffu, big > m + headroom<kFp8>() || u == q.u0)) {
-          const float m_new = fmaxf(m, big);
+        big = cols > 0 ? big + (lift - (kTop - headroom<kFp8>())) : -INFINITY;
+        // the barrier also lets P overwrite the columns that the other warp has read
+        if (barrier_rows_or(quad, big > m + headroom<kFp8>() || u == q.u0)) {
+          red[half * 128 + row] = big;
+          barrier_rows(quad);
+          const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));
           const float alpha = u == q.u0 || m == m_new ? 1.0f : ex2_approx(m - m_new);
           m = m_new;
           l *= alpha;
           if (u != q.u0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-            // O holds the units before this one: their last P V is done when its phase is
+            // O holds the units before this one; each of the two warps scales half of its columns
             if (!wait_pv()) return;
             tc_fence_after();
 #pragma unroll 1
-            for (int c = 0; c < kHeadDim; c += 32) {
+            for (int c = 128 * half; c < 128 * half + 128; c += 32) {
               float o[32];
               tmem_ld32(tmem + lanes + kTmemO + c, o);
               tc_wait_ld();
@@ -812,35 +992,49 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           }
         }
         const float ref = m == -INFINITY ? 0.0f : m;  // only infinite logits so far: weights of 0
-        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          if (c == 2 && !both) break;
-          uint32_t w[16];
+        for (int c = 0; c < 32; ++c) {
+          x[c] = fma2(x[c], mul_2, ref_2);
+          x[c].x = ex2_approx(x[c].x);
+          x[c].y = ex2_approx(x[c].y);
+        }
+        if (cols < 64) {
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            float a = ex2_approx(fmaf(x[32 * c + 2 * k], mul, -ref));
-            float b = ex2_approx(fmaf(x[32 * c + 2 * k + 1], mul, -ref));
-            sum[(2 * k) & 3] += a;
-            sum[(2 * k + 1) & 3] += b;
-            if constexpr (kFp8) {  // words 0-7: first terms of 32 keys, 8-15: second ones
-              const float2 v2 = reinterpret_cast<const float2*>(sc + 128)[16 * c + k];
-              uint32_t c1, c2;
-              split_p2(a * v2.x, b * v2.y, c1, c2);
-              w[k >> 1] = k & 1 ? w[k >> 1] | c1 << 16 : c1;
-              w[8 + (k >> 1)] = k & 1 ? w[8 + (k >> 1)] | c2 << 16 : c2;
-            } else {
-              w[k] = pack_bf16(a, b);  // the A operand is 16 bits: half a step, 2^-8, of each weight
-            }
-          }
-          if constexpr (kFp8) {
-            tmem_st8(ts + 8 * c, w);
-            tmem_st8(ts + 32 + 8 * c, w + 8);
-          } else {
-            tmem_st16(ts + 16 * c, reinterpret_cast<const float*>(w));
+          for (int c = 0; c < 32; ++c) {
+            if (2 * c >= cols) x[c].x = 0.0f;
+            if (2 * c + 1 >= cols) x[c].y = 0.0f;
           }
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        float2 sum[2] = {x[0], x[1]};
+#pragma unroll
+        for (int c = 2; c < 32; ++c) sum[c & 1] = add2(sum[c & 1], x[c]);
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        uint32_t w[32];
+        if constexpr (kFp8) {  // words 0-15: first terms of the 64 keys, 16-31: second ones
+#pragma unroll
+          for (int c = 0; c < 32; c += 2) {
+            const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + 64 * half)[c / 2];
+            float2 a = mul2(x[c], make_float2(v4.x, v4.y)), b = mul2(x[c + 1], make_float2(v4.z, v4.w));
+            if (cols < 64) {  // a stale scale may be NaN
+              if (2 * c >= cols) a.x = 0.0f;
+              if (2 * c + 1 >= cols) a.y = 0.0f;
+              if (2 * c + 2 >= cols) b.x = 0.0f;
+              if (2 * c + 3 >= cols) b.y = 0.0f;
+            }
+            uint32_t a1, a2, b1, b2;
+            split_p2(a, a1, a2);
+            split_p2(b, b1, b2);
+            w[c / 2] = a1 | b1 << 16;
+            w[16 + c / 2] = a2 | b2 << 16;
+          }
+          tmem_st16(ts + 16 * half, reinterpret_cast<const float*>(w));
+          tmem_st16(ts + 32 + 16 * half, reinterpret_cast<const float*>(w + 16));
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c) w[c] = pack_bf16(x[c].x, x[c].y);  // the A operand is 16 bits: half a step, 2^-8, of each weight
+          tmem_st32(ts + 32 * half, reinterpret_cast<const float*>(w));
+        }
         tc_wait_st();
       }
       tc_fence_before();
@@ -850,15 +1044,18 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
         if (kFp8) mbar_arrive(cx.bar(ScEmpty + sc_slot));
       }
     }
-    // ---- the piece's partial result: O / l and its LSE
+    // ---- the piece's partial result: O / l and its LSE, 128 dims a thread
     if (!wait_pv()) return;
     tc_fence_after();
     if (mine) {
-      const size_t at = ((size_t)(pair + s.tile[q.g] + q.i) * kPrefixTileSeqs + j) * kHeads + (row & 63);
+      red[half * 128 + row] = l;
+      barrier_rows(quad);
+      l += red[(half ^ 1) * 128 + row];
+      const size_t at = (size_t)(q.row + (q.own ? 0 : j)) * kHeads + (row & 63);
       const float inv = 1.0f / l;
       float* dst = p.part_o + at * kHeadDim;
 #pragma unroll 1
-      for (int c = 0; c < kHeadDim; c += 32) {
+      for (int c = 128 * half; c < 128 * half + 128; c += 32) {
         float o[32];
         tmem_ld32(tmem + lanes + kTmemO + c, o);
         tc_wait_ld();
@@ -867,7 +1064,8 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
 #pragma unroll
         for (int k = 0; k < 32; k += 8) st_global_v8(dst + c + k, o + k);
       }
-      p.part_lse[at] = (m + log2f(l)) * kLn2;
+      if (half == 0) p.part_lse[at] = (m + log2f(l)) * kLn2;
+      barrier_rows(quad);  // red is free again
     }
     tc_fence_before();
     __syncwarp();
@@ -879,20 +1077,23 @@ template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     decode_prefix_tc_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
+  using Sm = Smem<kFp8>;
   extern __shared__ __align__(1024) uint8_t dyn_smem[];
   const uint32_t raw = smem_u32(dyn_smem);
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* gbase = dyn_smem + (base - raw);
-  PlanSmem& plan = *reinterpret_cast<PlanSmem*>(gbase + Smem<kFp8>::plan);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Smem<kFp8>::misc);
-  int* abort_flag = reinterpret_cast<int*>(gbase + Smem<kFp8>::misc + 4);
+  PlanSmem& plan = *reinterpret_cast<PlanSmem*>(gbase + Sm::plan);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Sm::misc);
+  int* abort_flag = reinterpret_cast<int*>(gbase + Sm::misc + 4);
+  volatile uint32_t* tail_granule = reinterpret_cast<uint32_t*>(gbase + Sm::misc + 8);
   const int warp = threadIdx.x >> 5;
-  Ctx cx{base, base + Smem<kFp8>::bars, cta_rank(), abort_flag, p.err, p.wait_budget_ns};
+  Ctx cx{base, base + Sm::bars, cta_rank(), abort_flag, p.err, p.wait_budget_ns};
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool of_pair = i == PFull || i == PFull + 1 || i == OFree || i == QReady;
-      mbar_init(cx.bar(i), of_pair ? 2 * kSoftmaxWarps : i >= ScEmpty ? kSoftmaxWarps : 1);
+      const bool of_pair = i == PFull || i == PFull + 1 || i == OFree || i == QReady;  // every softmax warp of both CTAs
+      const bool of_cta = i >= ScEmpty && i < ScEmpty + kScaleSlots;                   // of this one
+      mbar_init(cx.bar(i), of_pair ? 2 * kSoftmaxWarps : of_cta ? kSoftmaxWarps : i >= TailReady ? 2 : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -903,7 +1104,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefetch_tensormap(&qmap);
   }
   if (warp == kMmaWarp) {
-    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + Smem<kFp8>::misc),
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + Sm::misc),
                  "n"(kTmemCols)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
@@ -911,20 +1112,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  build_plan(p, plan, reinterpret_cast<int32_t*>(gbase + Smem<kFp8>::ring), blockIdx.x == 0 ? p.err : nullptr);
+  build_plan(p, plan, *reinterpret_cast<PlanScratch*>(gbase + Sm::ring), blockIdx.x == 0 ? p.err : nullptr);
   publish_plan(p, plan);
   cluster_sync();  // the other CTA's barriers are initialised, its scratch is done with
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int units = plan.cost[p.n_groups], W = busy_pairs(p, units), pair = blockIdx.x >> 1;
+  const int units = plan.cost[p.n_groups] + plan.own[p.B], W = busy_pairs(p, units), pair = blockIdx.x >> 1;
   const long long lo = pair < W ? cta_cost_lo(pair, units, W) : 0, hi = pair < W ? cta_cost_lo(pair + 1, units, W) : 0;
 
   if (warp < kSoftmaxWarps) {
-    softmax_role<kFp8>(p, cx, plan, lo, hi, tmem, pair, gbase);
+    softmax_role<kFp8>(p, cx, plan, pair, lo, hi, tmem, gbase);
   } else if (warp == kProducerWarp) {
-    producer_role<kFp8>(p, &kmap, &vmap, &qmap, cx, plan, lo, hi);
+    producer_role<kFp8>(p, &kmap, &vmap, &qmap, cx, plan, pair, lo, hi, tail_granule);
+  } else if (warp == kTailWarp) {
+    tail_role<kFp8>(p, cx, plan, pair, lo, hi, tail_granule);
   } else if (cx.rank == 0 && (threadIdx.x & 31) == 0) {
-    mma_role<kFp8>(p, cx, plan, lo, hi, tmem);
+    mma_role<kFp8>(p, cx, plan, pair, lo, hi, tmem);
   }
   __syncwarp();
   tc_fence_before();
@@ -934,9 +1137,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
 }
 
-}  // namespace
-
-namespace {
 template <bool kFp8>
 cudaError_t launch_prefix(const PrefixParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const CUtensorMap& qmap, cudaStream_t stream) {

@@ -268,10 +268,6 @@ __device__ __forceinline__ float ex2_approx(float x) {
 struct Seg {
   int b, pg0, pg1, len;
 };
-// The page-table row of a sequence, from the first page that the split works on.
-__device__ __forceinline__ const int32_t* page_row(const DecodeParams& p, int b) {
-  return p.page_table + (size_t)b * p.max_pages + (p.skip ? __ldcg(p.skip + b) : 0);
-}
 __device__ __forceinline__ bool seg_first(const int* s_cost, int B, long long lo, long long hi, Seg& s) {
   if (lo >= hi) return false;
   s.b = seq_of_cost(s_cost, B, lo) - 1;
@@ -598,7 +594,7 @@ __device__ void producer_role(const DecodeParams& p, const CUtensorMap* kmap, co
   while (ok && seg_next(s_cost, s_len, p.B, p.piece_cost, lo, hi, s)) {
     if (*cx.abort) break;
     PageIds ids;
-    ids.row = page_row(p, s.b);
+    ids.row = p.page_table + (size_t)s.b * p.max_pages;
     ids.pg1 = s.pg1;
     if (!gather && !kGather8) ids.start(s.pg0, p, lane);
     BlockRows blk;
@@ -747,7 +743,7 @@ __device__ void producer_v_role(const DecodeParams& p, const CUtensorMap* vmap, 
   while (good && ok && seg_next(s_cost, s_len, p.B, p.piece_cost, lo, hi, s)) {
     if (*cx.abort) break;
     PageIds ids;
-    ids.row = page_row(p, s.b);
+    ids.row = p.page_table + (size_t)s.b * p.max_pages;
     ids.pg1 = s.pg1;
     ids.start(s.pg0, p, lane);
     for (int pg = s.pg0; good && pg < s.pg1; ++pg) {
@@ -789,7 +785,7 @@ __device__ void vref_role(const DecodeParams& p, const Ctx& cx, const int* s_cos
     if (*cx.abort) break;
     const uint32_t slot = piece & 1, n = piece >> 1;
     // lane i takes page g + i of each group of 32: its 64 scales in 16 vector loads
-    const int32_t* row = page_row(p, s.b);
+    const int32_t* row = p.page_table + (size_t)s.b * p.max_pages;
     float mx = 0.0f;
     if constexpr (kGather8) {
       // block gather: the piece's virtual blocks [8 pg0, 8 pg1) -- the selected blocks, then the block of the
@@ -1673,7 +1669,7 @@ __global__ void __launch_bounds__(Cfg<kFp8, kMtp>::kThreads)
   pdl_launch_dependents();  // the combine kernel may be scheduled now (its prologue reads seq_lens); it
                             // waits for this grid before it reads the partials
   build_cost_prefix(p.seq_lens, p.B, p.max_pages * kPageSize, p.err, p.piece_cost, s_len, s_cost, p.n_blocks,
-                    p.max_blocks, p.skip);  // ends with a barrier
+                    p.max_blocks);  // ends with a barrier
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const long long units = s_cost[p.B];  // total cost units

@@ -62,8 +62,7 @@ __host__ __device__ constexpr int chunk_bytes() { return kH == 8 ? 48 * 1024 : 3
 
 // At most 64 registers a thread and about 36 KB of shared memory, so four CTAs share an SM (608 on 152
 // SMs), which holds the whole grid of batches up to 64 sequences in one wave.
-// kPrefix: the partial results over a shared prefix are merged as well, behind the split's.
-template <int kH, bool kPrefix>
+template <int kH>
 __global__ void __launch_bounds__(kCombineThreads, 4) lse_combine_kernel(DecodeParams p) {
   using Sh = CombineShape<kH>;
   constexpr int kPartBytes = kH * 1024;            // the kH heads' rows of one partial
@@ -72,7 +71,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) lse_combine_kernel(DecodeP
   extern __shared__ __align__(128) uint8_t smem_raw[];
   int* s_len = reinterpret_cast<int*>(smem_raw + kChunkBytes);
   int* s_cost = s_len + p.B;
-  float* s_w = reinterpret_cast<float*>(s_cost + p.B + 1);  // [kH][G] normalised weights (with a prefix: [kH][G + pairs])
+  float* s_w = reinterpret_cast<float*>(s_cost + p.B + 1);  // [kH][G] normalised weights
   __shared__ float s_lse[kH];
   __shared__ float4 s_acc[Sh::kSubsets > 1 ? kCombineThreads * Sh::kVec : 1];
   __shared__ __align__(8) uint64_t s_bar;
@@ -87,7 +86,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) lse_combine_kernel(DecodeP
   }
   // seq_lens is final before the split kernel starts; the partials are not (ends with a barrier)
   build_cost_prefix(p.seq_lens, p.B, p.max_pages * kPageSize, nullptr, p.piece_cost, s_len, s_cost, p.n_blocks,
-                    p.max_blocks, kPrefix ? p.skip : nullptr);
+                    p.max_blocks);
   const int nq = p.n_query;
   const int b = blockIdx.y / nq, tq = blockIdx.y % nq;  // sequence, query token
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -99,13 +98,10 @@ __global__ void __launch_bounds__(kCombineThreads, 4) lse_combine_kernel(DecodeP
   // at position t, and range c's partial of it is row ((c + b) * q_groups + grp) * q_per_cta + t
   const int P = p.q_groups, kq = p.q_per_cta, grp = tq / kq, t = tq % kq;
   const int G = p.grid / P;
-  const int stride_w = kPrefix ? G + p.pre_pairs : G;
   const long long C = s_cost[p.B];
   const int np = pages_of_len(s_len[b]);
   uint16_t* out = p.out + ((size_t)blockIdx.y * kHeads + h) * kHeadDim;
-  const int2 pre = kPrefix ? __ldcg(p.parts + b) : make_int2(0, 0);
-  // empty sequence, or a token that sees no position
-  if (kPrefix ? np == 0 && pre.y == 0 : np == 0 || s_len[b] - (nq - 1 - tq) <= 0) {
+  if (np == 0 || s_len[b] - (nq - 1 - tq) <= 0) {  // empty sequence, or a token that sees no position
     if (sub == 0) {
 #pragma unroll
       for (int v = 0; v < Sh::kVec; ++v) reinterpret_cast<uint2*>(out)[dt * Sh::kVec + v] = make_uint2(0u, 0u);
@@ -116,14 +112,10 @@ __global__ void __launch_bounds__(kCombineThreads, 4) lse_combine_kernel(DecodeP
   // the CTAs holding the first and the last page of b; every CTA between
   // them with a non-empty range holds a piece of b
   const long long first = (long long)s_cost[b] + p.piece_cost;
-  const bool split = !kPrefix || np > 0;  // with a prefix, nothing may be left for the split
-  const int c_first = split ? cta_of_cost(first, C, G) : 0;
-  const int n_split = split ? cta_of_cost(first + np - 1, C, G) - c_first + 1 : 0;
-  const int n = n_split + pre.y;
+  const int c_first = cta_of_cost(first, C, G);
+  const int n = cta_of_cost(first + np - 1, C, G) - c_first + 1;
   // the kH heads' rows of range c_first + i's partial (kH KB, contiguous)
   auto part_rows = [&](int i) -> const float* {
-    if (kPrefix && i >= n_split)
-      return p.pre_o + ((size_t)(pre.x + (i - n_split) * kPrefixTileSeqs) * kHeads + h0) * kHeadDim;
     return p.part_o + ((((size_t)(c_first + i + b) * P + grp) * kq + t) * kHeads + h0) * kHeadDim;
   };
   // round k brings partials [k kChunk, min(n, (k + 1) kChunk)); a slot of an empty range holds stale data
@@ -141,16 +133,13 @@ __global__ void __launch_bounds__(kCombineThreads, 4) lse_combine_kernel(DecodeP
   if (warp == 0) issue_round(0);
   if (warp < kH) {
     const int hh = h0 + warp;
-    float* w = s_w + warp * stride_w;
+    float* w = s_w + warp * G;
     float mx = -INFINITY;
     for (int i = lane; i < n; i += 32) {
       const int c = c_first + i;
-      float v;
-      if (kPrefix && i >= n_split)
-        v = __ldcg(p.pre_lse + (size_t)(pre.x + (i - n_split) * kPrefixTileSeqs) * kHeads + hh);
-      else
-        v = cta_range_nonempty(c, C, G) ? __ldcg(p.part_lse + ((((size_t)(c + b) * P + grp) * kq + t) * kHeads + hh))
-                                        : -INFINITY;
+      const float v =
+          cta_range_nonempty(c, C, G) ? __ldcg(p.part_lse + ((((size_t)(c + b) * P + grp) * kq + t) * kHeads + hh))
+                                      : -INFINITY;
       w[i] = v;
       mx = fmaxf(mx, v);
     }
@@ -170,7 +159,7 @@ __global__ void __launch_bounds__(kCombineThreads, 4) lse_combine_kernel(DecodeP
   }
   __syncthreads();
 
-  const float* w = s_w + hl * stride_w;
+  const float* w = s_w + hl * G;
   float4 acc[Sh::kVec];
 #pragma unroll
   for (int v = 0; v < Sh::kVec; ++v) acc[v] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -226,18 +215,14 @@ __global__ void __launch_bounds__(kCombineThreads, 4) lse_combine_kernel(DecodeP
   }
 }
 
-template <int kH, bool kPrefix>
-cudaError_t launch_combine(const DecodeParams& p, cudaStream_t stream) {
-  dim3 grid(kHeads / kH, p.B * p.n_query);
-  const size_t smem = chunk_bytes<kH>() + sizeof(int) * (2 * (size_t)p.B + 1) + sizeof(float) * (size_t)kH * (p.grid + p.pre_pairs);
-  static int configured[kTrackedDevices] = {};
-  const cudaError_t e = ensure_dynamic_smem(lse_combine_kernel<kH, kPrefix>, smem, configured);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(lse_combine_kernel<kH, kPrefix>, grid, dim3(kCombineThreads), smem, stream, p);
-}
 template <int kH>
 cudaError_t launch_kh(const DecodeParams& p, cudaStream_t stream) {
-  return p.parts ? launch_combine<kH, true>(p, stream) : launch_combine<kH, false>(p, stream);
+  dim3 grid(kHeads / kH, p.B * p.n_query);
+  const size_t smem = chunk_bytes<kH>() + sizeof(int) * (2 * (size_t)p.B + 1) + sizeof(float) * (size_t)kH * p.grid;
+  static int configured[kTrackedDevices] = {};
+  const cudaError_t e = ensure_dynamic_smem(lse_combine_kernel<kH>, smem, configured);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(lse_combine_kernel<kH>, grid, dim3(kCombineThreads), smem, stream, p);
 }
 
 }  // namespace

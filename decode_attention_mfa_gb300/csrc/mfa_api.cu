@@ -395,27 +395,26 @@ mfa_status_t decode_common(const void* q, const void* k_cache, const void* v_cac
 }
 
 // ------------------------------------------------------------ shared prefix
-// Workspace: [header][split partials][prefix partials O, LSE][skip][parts].
+// Workspace: [header][partial O][partial LSE][parts].
 struct PrefixPlan {
-  mfa_plan_t split;
-  int pairs;
-  size_t pre_o, pre_lse, skip, parts, total;  // byte offsets
+  int pairs, own_row0;
+  size_t part_o, part_lse, parts, total;  // byte offsets
 };
 void fill_prefix_plan(int batch, int n_groups, int max_prefix_hint, int max_suffix_hint, int num_sms, PrefixPlan* w) {
-  fill_plan(batch, max_suffix_hint, num_sms, &w->split);
-  // at least two units of 128 keys a pair for the expected lengths, one pair per two SMs at most
-  const long long tiles_hint = (batch + kPrefixTileSeqs - 1) / kPrefixTileSeqs;
-  const long long units = tiles_hint * ((max_prefix_hint + 2ll * kPageSize - 1) / (2 * kPageSize));
-  w->pairs = (int)std::max(1ll, std::min((long long)(num_sms / 2), (units + 1) / 2));
-  // row tiles: every shared group has two sequences or more, and leaves at most one tile partly filled
-  const int tiles = std::min(batch / 2, (batch + (kPrefixTileSeqs - 1) * n_groups) / kPrefixTileSeqs);
-  const size_t slots = (size_t)(w->pairs + std::max(tiles, 1) - 1) * kPrefixTileSeqs;
+  // one pair of CTAs per two SMs, fewer when the expected lengths are less than kUnitsPerPair units of 128 keys a pair
+  constexpr long long kUnitsPerPair = 1;
+  auto units = [](long long tiles, long long tokens) { return tiles * ((tokens + 2 * kPageSize - 1) / (2 * kPageSize)); };
+  const long long work = units((batch + kPrefixTileSeqs - 1) / kPrefixTileSeqs, max_prefix_hint) + units(batch, max_suffix_hint);
+  w->pairs = (int)std::max(1ll, std::min((long long)(num_sms / 2), (work + kUnitsPerPair - 1) / kUnitsPerPair));
+  // tiles of prefixes: every shared group has two sequences or more, and leaves at most one tile partly filled
+  const int tiles = std::min(batch / 2, (int)((batch + (kPrefixTileSeqs - 1ll) * n_groups) / kPrefixTileSeqs));
+  w->own_row0 = (w->pairs + tiles) * kPrefixTileSeqs;
+  const size_t rows = (size_t)w->own_row0 + w->pairs + batch;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  w->pre_o = up(w->split.workspace_bytes);
-  w->pre_lse = w->pre_o + slots * kPartialOBytes;
-  w->skip = up(w->pre_lse + slots * kPartialLseBytes);
-  w->parts = up(w->skip + (size_t)batch * sizeof(int32_t));
-  w->total = up(w->parts + (size_t)batch * sizeof(int2));
+  w->part_o = kWsHeaderBytes;
+  w->part_lse = w->part_o + rows * kPartialOBytes;
+  w->parts = w->part_lse + up(rows * kPartialLseBytes);
+  w->total = w->parts + up((size_t)batch * sizeof(int4));
 }
 
 mfa_status_t prefix_common(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
@@ -431,45 +430,38 @@ mfa_status_t prefix_common(const void* q, const void* k_cache, const void* v_cac
   if (fp8 && (!k_scale || !v_scale)) return fail(MFA_ERR_INVALID_ARG, "null scale pointer");
   if (fp8 && (!aligned(k_scale, 16) || !aligned(v_scale, 16)))
     return fail(MFA_ERR_INVALID_ARG, "misaligned scales (16 bytes needed)");
-  DeviceInfo info;
-  mfa_status_t st = current_device(nullptr, &info);
-  if (st != MFA_OK) return st;
   mfa_plan_t plan;
-  st = check_decode_args(q, k_cache, v_cache, page_table, seq_lens, out, lse, batch, max_pages, num_pages,
-                         max_suffix_hint, workspace, workspace_bytes, info.num_sms, &plan);
+  mfa_status_t st = check_decode_args(q, k_cache, v_cache, page_table, seq_lens, out, lse, batch, max_pages, num_pages,
+                                      max_suffix_hint, workspace, (size_t)-1, 1, &plan);
   if (st != MFA_OK) return st;
+  DeviceInfo info;
+  if ((st = current_device(nullptr, &info)) != MFA_OK) return st;
   PrefixPlan w;
   fill_prefix_plan(batch, n_groups, max_prefix_hint, max_suffix_hint, info.num_sms, &w);
   if (workspace_bytes < w.total)
     return fail(MFA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, w.total);
   char* ws = static_cast<char*>(workspace);
-  DecodeParams p = make_decode_params(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, out, lse, scale,
-                                      batch, max_pages, num_pages, workspace, plan);
-  p.piece_cost = fp8 ? kPieceCostPagesFp8 : kPieceCostPages;
-  p.skip = reinterpret_cast<const int32_t*>(ws + w.skip);
-  p.parts = reinterpret_cast<const int2*>(ws + w.parts);
-  p.pre_o = reinterpret_cast<const float*>(ws + w.pre_o);
-  p.pre_lse = reinterpret_cast<const float*>(ws + w.pre_lse);
-  p.pre_pairs = w.pairs;
-  PrefixParams g{};
-  g.group_starts = group_starts;
-  g.prefix_pages = prefix_pages;
-  g.page_table = page_table;
-  g.seq_lens = seq_lens;
-  g.k_scale = k_scale;
-  g.v_scale = v_scale;
-  g.part_o = reinterpret_cast<float*>(ws + w.pre_o);
-  g.part_lse = reinterpret_cast<float*>(ws + w.pre_lse);
-  g.skip = reinterpret_cast<int32_t*>(ws + w.skip);
-  g.parts = reinterpret_cast<int2*>(ws + w.parts);
-  g.err = p.err;
-  g.scale = scale;
-  g.B = batch;
-  g.n_groups = n_groups;
-  g.max_pages = max_pages;
-  g.num_pages = num_pages;
-  g.pairs = w.pairs;
-  g.wait_budget_ns = p.wait_budget_ns;
+  PrefixParams p{};
+  p.group_starts = group_starts;
+  p.prefix_pages = prefix_pages;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  p.own_row0 = w.own_row0;
+  p.parts = reinterpret_cast<int4*>(ws + w.parts);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.err = reinterpret_cast<uint32_t*>(ws);
+  p.scale = scale;
+  p.B = batch;
+  p.n_groups = n_groups;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.pairs = w.pairs;
+  p.wait_budget_ns = g_wait_budget_ns.load(std::memory_order_relaxed);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   CUtensorMap kmap, vmap, qmap;
   const uint64_t rows = (uint64_t)num_pages * kPageSize;
@@ -477,16 +469,13 @@ mfa_status_t prefix_common(const void* q, const void* k_cache, const void* v_cac
       (st = fp8 ? encode_rows_e4m3(&kmap, k_cache, rows) : encode_rows_bf16(&kmap, k_cache, rows)) != MFA_OK ||
       (st = fp8 ? encode_rows_e4m3(&vmap, v_cache, rows) : encode_rows_bf16(&vmap, v_cache, rows)) != MFA_OK)
     return st;
-  cudaError_t e = launch_decode_prefix_tc(g, kmap, vmap, qmap, s);
-  if (e != cudaSuccess) return cuda_fail(e, "decode prefix launch");
+  cudaError_t e;
   if (g_prof_start && (e = cudaEventRecordWithFlags(g_prof_start, s, cudaEventRecordExternal)) != cudaSuccess)
     return cuda_fail(e, "profile event record");
-  e = fp8 ? launch_decode_split_tc_fp8(p, kmap, vmap, qmap, s) : launch_decode_split_tc(p, kmap, vmap, qmap, s);
-  if (e != cudaSuccess) return cuda_fail(e, "decode split launch");
+  if ((e = launch_decode_prefix_tc(p, kmap, vmap, qmap, s)) != cudaSuccess) return cuda_fail(e, "decode prefix launch");
   if (g_prof_stop && (e = cudaEventRecordWithFlags(g_prof_stop, s, cudaEventRecordExternal)) != cudaSuccess)
     return cuda_fail(e, "profile event record");
-  e = launch_lse_combine(p, s);
-  if (e != cudaSuccess) return cuda_fail(e, "lse combine launch");
+  if ((e = launch_prefix_combine(p, s)) != cudaSuccess) return cuda_fail(e, "prefix combine launch");
   return MFA_OK;
 }
 
@@ -535,10 +524,9 @@ size_t mfa_decode_mtp_workspace_bytes(int batch, int n_query, int max_len_hint) 
 }
 
 size_t mfa_decode_prefix_workspace_bytes(int batch, int n_groups, int max_prefix_hint, int max_suffix_hint) {
-  mfa_plan_t plan;
   DeviceInfo info;
-  if (n_groups < 1 || n_groups > batch || max_prefix_hint < 0 ||
-      mfa_plan_decode(batch, max_suffix_hint, 0, &plan) != MFA_OK || current_device(nullptr, &info) != MFA_OK)
+  if (batch < 1 || batch > kMaxBatch || n_groups < 1 || n_groups > batch || max_prefix_hint < 0 || max_suffix_hint < 0 ||
+      current_device(nullptr, &info) != MFA_OK)
     return 0;
   PrefixPlan w;
   fill_prefix_plan(batch, n_groups, max_prefix_hint, max_suffix_hint, info.num_sms, &w);

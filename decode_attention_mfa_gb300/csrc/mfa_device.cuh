@@ -74,10 +74,9 @@ __device__ __forceinline__ int virtual_len(int len, int nb) {
 __device__ __forceinline__ void build_cost_prefix(const int32_t* __restrict__ seq_lens, int B,
                                                   int cap_tokens, uint32_t* err, int piece_cost, int* s_len,
                                                   int* s_cost, const int32_t* n_blocks = nullptr,
-                                                  int max_blocks = 0, const int32_t* skip = nullptr) {
+                                                  int max_blocks = 0) {
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    int len = clamp_len(__ldg(seq_lens + b), cap_tokens, err);
-    if (skip) len -= __ldcg(skip + b) * kPageSize;  // shared prefix: never more pages than the sequence holds
+    const int len = clamp_len(__ldg(seq_lens + b), cap_tokens, err);
     s_len[b] = n_blocks ? virtual_len(len, selected_blocks(len, n_blocks, b, max_blocks, err)) : len;
   }
   __syncthreads();

@@ -124,19 +124,12 @@ struct DecodeParams {
   // (i + b) * q_groups + r, holding q_per_cta tokens.
   int q_per_cta, q_groups;
   uint64_t wait_budget_ns;
-  // Shared prefix (null: none): sequence b's first skip[b] pages are left out of the split (its table row, length and
-  // partition start behind them); its partial results over them are parts[b].y rows of [64 heads] from row parts[b].x
-  // on, kPrefixTileSeqs apart, of pre_o / pre_lse, which the combine merges with the split's.
-  const int32_t* skip;
-  const int2* parts;
-  const float* pre_o;    // [rows][64][256]
-  const float* pre_lse;  // [rows][64]
-  int pre_pairs;         // at most this many partial results a sequence
 };
 
-// Shared-prefix kernel: row tiles of kPrefixTileSeqs sequences, units of 128 keys.
+// Shared-prefix decode. The work is a line of row tiles: of each group that shares a prefix, kPrefixTileSeqs sequences
+// against the prefix, then each sequence against what it holds behind it (all of it, where nothing is shared). Units of
+// a tile: its keys by 128, plus kPrefixPieceUnits for loading Q and writing the partial result of each piece of it.
 constexpr int kPrefixTileSeqs = 4;
-// Units charged per row tile that a pair of CTAs works on, besides its keys: loading Q and writing the partial result.
 constexpr int kPrefixPieceUnits = 2;
 struct PrefixParams {
   const int32_t* group_starts;  // [n_groups + 1]
@@ -145,10 +138,14 @@ struct PrefixParams {
   const int32_t* seq_lens;
   const float* k_scale;         // [num_pages][64] (null: bf16 cache)
   const float* v_scale;
-  float* part_o;                // [(pair + row tile)][4 sequences][64 heads][256]
+  // partial results, rows of [64 heads][256] (and [64] LSEs): row 4 (pair + i) + s for sequence s of the i-th tile of a
+  // prefix, then, from row own_row0 on, row pair + b for sequence b's own tokens
+  float* part_o;
   float* part_lse;
-  int32_t* skip;                // [B], written: see DecodeParams
-  int2* parts;
+  int own_row0;
+  int4* parts;                  // [B]: first row and number of b's partial results over its prefix (kPrefixTileSeqs apart) and of its own
+  uint16_t* out;                // [B][64][256] bf16 bits
+  float* lse;                   // [B][64]
   uint32_t* err;
   float scale;
   int B, n_groups, max_pages, num_pages, pairs;
@@ -226,6 +223,7 @@ cudaError_t launch_decode_split_tc_mtp(const DecodeParams& p, const CUtensorMap&
 size_t decode_split_tc_mtp_smem_bytes(int B);
 cudaError_t launch_decode_prefix_tc(const PrefixParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
                                     const CUtensorMap& q_map, cudaStream_t stream);
+cudaError_t launch_prefix_combine(const PrefixParams& p, cudaStream_t stream);
 
 // Host-side services of mfa_api.cu for other entry points of the library.
 void set_last_error_message(const char* msg);
