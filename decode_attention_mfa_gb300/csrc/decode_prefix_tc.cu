@@ -55,16 +55,15 @@ namespace {
 
 constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kTailWarp = 10;
 constexpr int kThreads = 352;
-// Ring of 16 KB granules. bf16: half of a K page (128 dims), or 128 dims of a V page; E4M3: a K page, or 128 dims of
-// two V pages.
+// Two K and two V slots, of even and odd units, one CTA's half of a unit each: K one page of 256 dims, V 128 dims of two
+// pages (each page's half at kHalf). A K slot is free when S of its unit is done, a V slot when P V is, which the
+// softmax warps are told anyway: the issuing thread commits twice a unit. (With a ring of 16 KB granules it waited
+// four times and committed six times a unit, and a unit took 3600 cycles instead of XXXX.)
 template <bool kFp8>
-__host__ __device__ constexpr int slots() { return kFp8 ? 8 : 9; }
-constexpr int kMaxSlots = 9;
-constexpr int kGranule = 16384;
+__host__ __device__ constexpr uint32_t slot_bytes() { return kFp8 ? 16384 : 32768; }
 constexpr int kUnitKeys = 2 * kPageSize;
 constexpr int kScaleSlots = 4;         // E4M3: 128 K scales and 128 V scales a unit
 constexpr int kScaleBytes = 1024;
-constexpr int kTails = 4;              // partial last units in flight: fewer fit the ring
 constexpr int kQBytes = 65536;         // 128 rows x 256 dims, four 64-dim blocks of [128 rows x 128 B]
 constexpr int kSeqQBytes = 32768;      // one sequence's rows
 constexpr int kTmemCols = 512, kTmemO = 256, kSCols = 128;
@@ -80,21 +79,20 @@ __host__ __device__ constexpr int key_step() { return kFp8 ? 32 : 16; }
 static_assert(kPrefixTileSeqs * kHeads == 256, "rows of a row tile");
 
 enum Bar {
-  Full = 0,                  // [slots] leader: both CTAs' halves landed
-  Empty = Full + kMaxSlots,  // [slots] both: the MMAs reading the granule are done
-  QFull = Empty + kMaxSlots, // bf16: leader; E4M3: both, each its own rows
+  KFull = 0,                 // [2] leader: both CTAs' halves landed
+  VFull = KFull + 2,         // [2] leader
+  QFull = VFull + 2,         // bf16: leader; E4M3: both, each its own rows
   QReady,                    // E4M3, leader: Q split into terms, one arrival per softmax warp of the pair
-  QEmpty,                    // both
-  SFull,                     // [2] both
+  SFull,                     // [2] both: S of even and odd units
   PFull = SFull + 2,         // [2] leader: one arrival per softmax warp of the pair
   PvDone = PFull + 2,        // [2] both: P V of even and odd units
   OFree = PvDone + 2,        // leader: O has been read, one arrival per softmax warp of the pair
   Drain,                     // leader
   ScFull,                    // [kScaleSlots] E4M3, both
   ScEmpty = ScFull + kScaleSlots,   // [kScaleSlots] one arrival per softmax warp of the CTA
-  TailFull = ScEmpty + kScaleSlots, // [kTails] both: this CTA's V of a partial last unit landed
-  TailReady = TailFull + kTails,    // [kTails] leader: its rows behind the last token are zero, one arrival a CTA
-  kBars = TailReady + kTails
+  TailFull = ScEmpty + kScaleSlots, // [2] both: this CTA's V of a partial last unit landed (by V slot)
+  TailReady = TailFull + 2,         // [2] leader: its rows behind the last token are zero, one arrival a CTA
+  kBars = TailReady + 2
 };
 
 // The line of work as every CTA sees it. Indices of sequences and tiles fit 16 bits (at most 1024 sequences).
@@ -115,17 +113,18 @@ struct PlanScratch {
 
 template <bool kFp8>
 struct Smem {
-  static constexpr uint32_t ring = 0;
-  static constexpr uint32_t q = slots<kFp8>() * kGranule;
+  static constexpr uint32_t k = 0;
+  static constexpr uint32_t v = k + 2 * slot_bytes<kFp8>();
+  static constexpr uint32_t q = v + 2 * slot_bytes<kFp8>();
   static constexpr uint32_t scales = q + kQBytes;
   static constexpr uint32_t plan = scales + (kFp8 ? kScaleSlots * kScaleBytes : 0);
   static constexpr uint32_t red = (plan + (uint32_t)sizeof(PlanSmem) + 15) & ~15u;  // [2][128] exchange of the row halves
   static constexpr uint32_t bars = red + 2 * 128 * 4;
-  static constexpr uint32_t misc = bars + 8 * kBars;  // TMEM base, abort flag, granules of the tails
-  static constexpr uint32_t total = misc + 8 + 4 * kTails;
+  static constexpr uint32_t misc = bars + 8 * kBars;  // TMEM base, abort flag
+  static constexpr uint32_t total = misc + 8;
 };
 static_assert(Smem<false>::total + 1024 <= 227 * 1024 && Smem<true>::total + 1024 <= 227 * 1024, "shared memory");
-static_assert(slots<true>() * kGranule >= (int)sizeof(PlanScratch), "the plan's scratch lies in the ring");
+static_assert(4 * slot_bytes<true>() >= sizeof(PlanScratch), "the plan's scratch lies in the K and V slots");
 
 // ---------------------------------------------------------------- cluster pair
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -141,6 +140,13 @@ __device__ __forceinline__ uint32_t map_to_leader(uint32_t addr) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Arrival on a barrier of the other CTA. What it announces lies in tensor memory, which the tcgen05 fences order, so no
+// release at cluster scope is needed: that one waits for all of the thread's memory operations (a unit took 3800
+// cycles with it).
+__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+// The same behind writes to shared memory that the other CTA's MMAs read.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -461,39 +467,32 @@ struct TilePages {
 template <bool kFp8>
 __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
                               const CUtensorMap* qmap, const Ctx& cx, const PlanSmem& s, int pair, long long lo,
-                              long long hi, volatile uint32_t* tail_granule) {
-  constexpr int kSlots = slots<kFp8>();
+                              long long hi) {
   using Sm = Smem<kFp8>;
+  constexpr uint32_t kSlot = slot_bytes<kFp8>(), kPage = kSlot / 2;
+  constexpr int kCols = kFp8 ? 128 : 64;  // columns of a copy: 128 bytes
   const int lane = threadIdx.x & 31, r = (int)cx.rank;
   const uint64_t pol_shared = policy_evict_normal(), pol_own = policy_evict_first();
-  uint32_t cc = 0, pieces = 0, units = 0, tails = 0;
-  // The next granule: its address, and the leader's barrier of it, on which the leader announces `bytes` of both CTAs.
-  auto next_slot = [&](uint32_t bytes, uint32_t& dst, uint32_t& bar) -> bool {
-    const uint32_t slot = cc % kSlots, n = cc / kSlots;
-    if (!cx.wait_warp(Empty + slot, (n & 1) ^ 1)) return false;
-    dst = cx.base + Sm::ring + slot * kGranule;
-    bar = cx.leader_bar(Full + slot);
-    if (lane == 0 && r == 0) mbar_arrive_expect_tx(cx.bar(Full + slot), bytes);
-    ++cc;
-    return true;
-  };
-  // K of one unit: this CTA's page (page r of the two); bf16: in two granules of 128 dims
-  auto load_k = [&](int pa, int pb, uint64_t pol) -> bool {
+  uint32_t pieces = 0, tails[2] = {0, 0};
+  // K of unit `n` (and its scales): this CTA's page, page r of the two, on the leader's barrier, on which the leader
+  // announces the bytes of both CTAs
+  auto load_k = [&](uint32_t n, int pa, int pb, uint64_t pol) -> bool {
+    const uint32_t slot = n & 1;
+    if (n >= 2 && !cx.wait_warp(SFull + slot, ((n >> 1) & 1) ^ 1)) return false;
     const int page = r == 0 ? pa : pb;
-    const uint32_t bytes = pb >= 0 ? 2 * kGranule : kGranule;
-    uint32_t dst, bar;
-    if constexpr (kFp8) {
-      if (!next_slot(bytes, dst, bar)) return false;
-      if (lane == 0 && page >= 0) {
-        tma_load_2d_pair(dst, kmap, 0, page * kPageSize, bar, pol);
-        tma_load_2d_pair(dst + 8192, kmap, 128, page * kPageSize, bar, pol);
-      }
-      // the scales of all the unit's keys, for this CTA's rows
-      const uint32_t slot = units % kScaleSlots;
-      if (!cx.wait_warp(ScEmpty + slot, ((units / kScaleSlots) & 1) ^ 1)) return false;
-      ++units;
+    if (lane == 0) {
+      const uint32_t dst = cx.base + Sm::k + slot * kSlot, bar = cx.leader_bar(KFull + slot);
+      if (r == 0) mbar_arrive_expect_tx(cx.bar(KFull + slot), pb >= 0 ? 2 * kSlot : kSlot);
+      if (page >= 0)
+#pragma unroll
+        for (int d = 0; d < kHeadDim / kCols; ++d)
+          tma_load_2d_pair(dst + d * 8192, kmap, d * kCols, page * kPageSize, bar, pol);
+    }
+    if constexpr (kFp8) {  // the scales of all the unit's keys, for this CTA's rows
+      const uint32_t sc_slot = n % kScaleSlots;
+      if (!cx.wait_warp(ScEmpty + sc_slot, ((n / kScaleSlots) & 1) ^ 1)) return false;
       if (lane == 0) {
-        const uint32_t sc = cx.base + Sm::scales + slot * kScaleBytes, sb = cx.bar(ScFull + slot);
+        const uint32_t sc = cx.base + Sm::scales + sc_slot * kScaleBytes, sb = cx.bar(ScFull + sc_slot);
         constexpr uint32_t kPageScales = kPageSize * sizeof(float);
         mbar_arrive_expect_tx(sb, (pb >= 0 ? 4 : 2) * kPageScales);
         bulk_load(sc, p.k_scale + (size_t)pa * kPageSize, kPageScales, sb);
@@ -503,55 +502,31 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
           bulk_load(sc + 512 + kPageScales, p.v_scale + (size_t)pb * kPageSize, kPageScales, sb);
         }
       }
-    } else {
-      for (int h = 0; h < 2; ++h) {
-        if (!next_slot(bytes, dst, bar)) return false;
-        if (lane == 0 && page >= 0) {
-          tma_load_2d_pair(dst, kmap, h * 128, page * kPageSize, bar, pol);
-          tma_load_2d_pair(dst + 8192, kmap, h * 128 + 64, page * kPageSize, bar, pol);
-        }
-      }
     }
     return true;
   };
-  // V of one unit: this CTA's 128 dims of each page; bf16: a granule a page. The granule with the last page of a tail
-  // lands on this CTA's own barrier, for the warp that zeroes its rows.
-  auto load_v = [&](int pa, int pb, bool tail, uint64_t pol) -> bool {
-    uint32_t dst, bar;
-    auto to_tail = [&](uint32_t bytes) {
-      const uint32_t t = tails++ % kTails;
-      bar = cx.bar(TailFull + t);
-      if (lane == 0) {
-        tail_granule[t] = dst;
-        mbar_arrive_expect_tx(bar, bytes);
-      }
-    };
-    if constexpr (kFp8) {
-      const uint32_t bytes = pb >= 0 ? kGranule : kGranule / 2;
-      if (!next_slot(tail ? 0 : 2 * bytes, dst, bar)) return false;
-      if (tail) to_tail(bytes);
-      if (lane == 0) {
-        tma_load_2d_pair(dst, vmap, r * 128, pa * kPageSize, bar, pol);
-        if (pb >= 0) tma_load_2d_pair(dst + 8192, vmap, r * 128, pb * kPageSize, bar, pol);
-      }
-    } else {
-      const int np = pb >= 0 ? 2 : 1;
-      for (int i = 0; i < np; ++i) {
-        const bool last = tail && i == np - 1;
-        if (!next_slot(last ? 0 : 2 * kGranule, dst, bar)) return false;
-        if (last) to_tail(kGranule);
-        const int page = i ? pb : pa;
-        if (lane == 0) {
-          tma_load_2d_pair(dst, vmap, r * 128, page * kPageSize, bar, pol);
-          tma_load_2d_pair(dst + 8192, vmap, r * 128 + 64, page * kPageSize, bar, pol);
-        }
-      }
+  // V of unit `n`: this CTA's 128 dims of each page. That of a tail lands on this CTA's own barrier, for the warp that
+  // zeroes its rows.
+  auto load_v = [&](uint32_t n, int pa, int pb, bool tail, uint64_t pol) -> bool {
+    const uint32_t slot = n & 1;
+    if (n >= 2 && !cx.wait_warp(PvDone + slot, ((n >> 1) & 1) ^ 1)) return false;
+    if (lane == 0) {
+      const uint32_t dst = cx.base + Sm::v + slot * kSlot, bytes = pb >= 0 ? kSlot : kPage;
+      if (r == 0) mbar_arrive_expect_tx(cx.bar(VFull + slot), tail ? 0 : 2 * bytes);
+      if (tail) mbar_arrive_expect_tx(cx.bar(TailFull + slot), bytes);
+      const uint32_t bar = tail ? cx.bar(TailFull + slot) : cx.leader_bar(VFull + slot);
+      for (int i = 0; i < (pb >= 0 ? 2 : 1); ++i)
+#pragma unroll
+        for (int d = 0; d < 128 / kCols; ++d)
+          tma_load_2d_pair(dst + i * kPage + d * 8192, vmap, r * 128 + d * kCols, (i ? pb : pa) * kPageSize, bar, pol);
     }
+    tails[slot] += tail;
     return true;
   };
   Piece q;
   q.x = lo;
-  int va = -1, vb = -1;  // the unit whose V is still to be loaded: V trails K by a unit, as the MMAs use them
+  uint32_t cnt = 0;      // units whose K has been loaded
+  int va = -1, vb = -1;  // the last of them: its V is still to be loaded (V trails K by a unit, as the MMAs use them)
   bool vtail = false, good = true;
   uint64_t vpol = pol_own;
   while (good && next_piece(p, s, pair, hi, q)) {
@@ -560,7 +535,8 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
     ids.end = min((q.keys + kPageSize - 1) / kPageSize, 2 * q.u1);
     ids.start(2 * q.u0, p, lane);
     const uint64_t pol = q.own ? pol_own : pol_shared;
-    good = cx.wait_warp(QEmpty, (pieces & 1) ^ 1);
+    // Q may be replaced once S of every unit so far is done
+    good = cnt == 0 || cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1);
     if (!good) break;
     if (lane == 0) {
       const int here = min(2, max(0, q.seqs - 2 * r));  // this CTA's sequences
@@ -578,59 +554,61 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
       const int valid = keys_in_unit(q, u);
       const int pa = ids.get(2 * u, p, lane);
       const int pb = valid > kPageSize ? ids.get(2 * u + 1, p, lane) : -1;
-      good = load_k(pa, pb, pol);
-      if (good && va >= 0) good = load_v(va, vb, vtail, vpol);
+      good = load_k(cnt, pa, pb, pol);
+      if (good && va >= 0) good = load_v(cnt - 1, va, vb, vtail, vpol);
+      ++cnt;
       va = pa;
       vb = pb;
       vtail = is_tail<kFp8>(q, valid);
       vpol = pol;
     }
     if (kFp8 && good) {  // E4M3: the next row tile's Q is split only behind this one's last P V
-      good = load_v(va, vb, vtail, vpol);
+      good = load_v(cnt - 1, va, vb, vtail, vpol);
       va = -1;
     }
   }
-  if (good && va >= 0) good = load_v(va, vb, vtail, vpol);
-  // Every copy of both CTAs must land before either leaves: the leader's barriers tell, and the other CTA stays
-  // until the cluster's last barrier (the copies of a tail are waited for where its rows are zeroed).
+  if (good && va >= 0) good = load_v(cnt - 1, va, vb, vtail, vpol);
+  // Every copy of both CTAs must land before either leaves: this CTA's barriers and the leader's tell, and the other CTA
+  // stays until the cluster's last barrier.
   if (lane == 0) {
-    if constexpr (kFp8) {
-      for (uint32_t k = (units > (uint32_t)kScaleSlots ? units - kScaleSlots : 0); k < units; ++k)
-        (void)mbar_wait(cx.bar(ScFull + k % kScaleSlots), (k / kScaleSlots) & 1, cx.budget, nullptr, p.err);
+    for (uint32_t k = cnt > 2 ? cnt - 2 : 0; k < cnt; ++k) {
+      if (r == 0) (void)mbar_wait(cx.bar(KFull + (k & 1)), (k >> 1) & 1, cx.budget, nullptr, p.err);
+      if (r == 0 && (good || k + 1 < cnt)) (void)mbar_wait(cx.bar(VFull + (k & 1)), (k >> 1) & 1, cx.budget, nullptr, p.err);
     }
+    for (int i = 0; i < 2; ++i)
+      if (tails[i]) (void)mbar_wait(cx.bar(TailFull + i), (tails[i] - 1) & 1, cx.budget, nullptr, p.err);
+    if constexpr (kFp8)
+      for (uint32_t k = cnt > (uint32_t)kScaleSlots ? cnt - kScaleSlots : 0; k < cnt; ++k)
+        (void)mbar_wait(cx.bar(ScFull + k % kScaleSlots), (k / kScaleSlots) & 1, cx.budget, nullptr, p.err);
     if (pieces && (kFp8 || r == 0)) (void)mbar_wait(cx.bar(QFull), (pieces - 1) & 1, cx.budget, nullptr, p.err);
-    if (r == 0)
-      for (uint32_t k = (cc > (uint32_t)kSlots ? cc - kSlots : 0); k < cc; ++k)
-        (void)mbar_wait(cx.bar(Full + k % kSlots), (k / kSlots) & 1, cx.budget, nullptr, p.err);
   }
   __syncwarp();
 }
 
 // ---------------------------------------------------------------- rows behind the last token
 template <bool kFp8>
-__device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, long long lo, long long hi,
-                          volatile uint32_t* tail_granule) {
+__device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, long long lo, long long hi) {
+  constexpr int kStep = key_step<kFp8>(), kChunks = kFp8 ? 1 : 2;  // 128 B chunks of a V row half: 128 or 64 dims
   const int lane = threadIdx.x & 31;
-  uint32_t tails = 0;
+  uint32_t cnt = 0, tails[2] = {0, 0};
   Piece q;
   q.x = lo;
   while (next_piece(p, s, pair, hi, q)) {
+    cnt += q.u1 - q.u0;
     const int valid = keys_in_unit(q, q.u1 - 1);
     if (!is_tail<kFp8>(q, valid)) continue;
-    const uint32_t t = tails % kTails;
-    if (!cx.wait_warp(TailFull + t, (tails / kTails) & 1)) return;
-    ++tails;
-    // rows of 128 B: of one page and two 64-dim chunks (bf16), of one 128-dim chunk and two pages (E4M3)
-    constexpr int kChunks = kFp8 ? 1 : 2, kStep = key_step<kFp8>();
-    const uint32_t base = tail_granule[t] + (kFp8 ? (uint32_t)(valid / kPageSize) * 8192u : 0u);
-    const int row = valid % kPageSize, rows = kStep - valid % kStep;
-    for (int i = lane; i < rows * 8 * kChunks; i += 32) {
-      const uint32_t at = base + (i / (rows * 8)) * 8192 + row * 128 + (i % (rows * 8)) * 16;
+    const uint32_t slot = (cnt - 1) & 1;
+    if (!cx.wait_warp(TailFull + slot, tails[slot] & 1)) return;
+    ++tails[slot];
+    const uint32_t base = cx.base + Smem<kFp8>::v + slot * slot_bytes<kFp8>() + (valid / kPageSize) * (slot_bytes<kFp8>() / 2);
+    const int row = valid % kPageSize, words = (kStep - valid % kStep) * 8;  // 16 B words of a chunk's rows
+    for (int i = lane; i < words * kChunks; i += 32) {
+      const uint32_t at = base + (i / words) * 8192 + row * 128 + (i % words) * 16;
       asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
     }
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(cx.leader_bar(TailReady + t));
+    if (lane == 0) mbar_arrive_cluster(cx.leader_bar(TailReady + slot));
   }
 }
 
@@ -640,45 +618,36 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
                          uint32_t tmem) {
   constexpr uint32_t idesc_s = idesc_f16(256, kSCols, kFp8 ? 0 : 1, 0, 0);    // A = Q, B = K, both K-major (E4M3: format 0)
   constexpr uint32_t idesc_o = idesc_f16(256, kHeadDim, kFp8 ? 0 : 1, 0, 1);  // A = P (TMEM), B = V (dim-major)
-  constexpr int kSlots = slots<kFp8>();
   using Sm = Smem<kFp8>;
-  uint32_t cc = 0, pieces = 0, s_cnt = 0, p_cnt = 0, tails = 0;
-  auto granule = [&](uint32_t& addr) -> bool {
-    const uint32_t slot = cc % kSlots;
-    if (!cx.wait(Full + slot, (cc / kSlots) & 1)) return false;
-    tc_fence_after();
-    addr = cx.base + Sm::ring + slot * kGranule;
-    return true;
-  };
-  auto granule_done = [&]() { tc_commit_pair(cx.bar(Empty + cc++ % kSlots)); };
+  uint32_t pieces = 0, s_cnt = 0, p_cnt = 0, tails[2] = {0, 0};
+  // Descriptors of the operands' first blocks; a block `bytes` further on has bytes / 16 more in the address field, which
+  // holds every shared address without a carry.
+  auto ahead = [](uint64_t desc, uint32_t bytes) -> uint64_t { return desc + (bytes >> 4); };
+  const uint64_t q_desc = smem_desc_sw128(cx.base + Sm::q, 16, 1024);
+  const uint64_t k_desc0 = smem_desc_sw128(cx.base + Sm::k, 16, 1024);
+  const uint64_t v_desc0 = smem_desc_sw128(cx.base + Sm::v, kFp8 ? 16 : 8192, 1024);
   auto do_s = [&]() -> bool {
-    const uint32_t d = tmem + (s_cnt & 1) * kSCols;  // its last reader, P V of two units ago, was issued before
-    const uint32_t qa = cx.base + Sm::q;
-    uint32_t kb;
+    const uint32_t buf = s_cnt & 1, d = tmem + buf * kSCols;  // its last reader, P V of two units ago, was issued before
+    if (!cx.wait(KFull + buf, (s_cnt >> 1) & 1)) return false;
+    tc_fence_after();
+    const uint64_t k_desc = ahead(k_desc0, buf * slot_bytes<kFp8>());
     if constexpr (kFp8) {
-      if (!granule(kb)) return false;
 #pragma unroll
       for (int t = 0; t < 2; ++t)  // Q's terms
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
-            tc_mma_pair_f8(d, smem_desc_sw128(qa + t * 32768 + h * 16384 + kk * 32, 16, 1024),
-                           smem_desc_sw128(kb + h * 8192 + kk * 32, 16, 1024), idesc_s, (t | h | kk) != 0);
-      granule_done();
+            tc_mma_pair_f8(d, ahead(q_desc, t * 32768 + h * 16384 + kk * 32), ahead(k_desc, h * 8192 + kk * 32), idesc_s,
+                           (t | h | kk) != 0);
     } else {
-      for (int h = 0; h < 2; ++h) {
-        if (!granule(kb)) return false;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_pair(d, smem_desc_sw128(qa + (2 * h + e) * 16384 + kk * 32, 16, 1024),
-                        smem_desc_sw128(kb + e * 8192 + kk * 32, 16, 1024), idesc_s, (h | e | kk) != 0);
-        granule_done();
-      }
+        for (int kk = 0; kk < 4; ++kk)
+          tc_mma_pair(d, ahead(q_desc, e * 16384 + kk * 32), ahead(k_desc, e * 8192 + kk * 32), idesc_s, (e | kk) != 0);
     }
-    tc_commit_pair(cx.bar(SFull + (s_cnt & 1)));
+    tc_commit_pair(cx.bar(SFull + buf));
     ++s_cnt;
     return true;
   };
@@ -691,32 +660,32 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
   auto do_pv = [&](const Unit& v) -> bool {
     constexpr int kStep = key_step<kFp8>(), kSteps = kPageSize / kStep;
     const uint32_t buf = p_cnt & 1, a = tmem + buf * kSCols, d = tmem + kTmemO;
-    if (v.first && !cx.wait_pair(OFree, (v.piece & 1) ^ 1)) return false;
-    if (!cx.wait_pair(PFull + buf, (p_cnt >> 1) & 1)) return false;
-    const int np = v.valid > kPageSize ? 2 : 1;
-    uint32_t vb = 0;
-    if (kFp8 && !granule(vb)) return false;
-    for (int i = 0; i < np; ++i) {
-      if (!kFp8 && !granule(vb)) return false;
-      if (v.tail && i == (kFp8 ? 0 : np - 1)) {
-        if (!cx.wait_pair(TailReady + tails % kTails, (tails / kTails) & 1)) return false;
-        ++tails;
-        tc_fence_after();
-      }
-      const int steps = min(kSteps, (v.valid - i * kPageSize + kStep - 1) / kStep);
-      if constexpr (kFp8) {
-        for (int t = 0; t < 2; ++t)  // P's terms
-          for (int kk = 0; kk < steps; ++kk)
-            tc_mma_pair_f8_tmem_a(d, a + t * 32 + i * 16 + kk * 8, smem_desc_sw128(vb + i * 8192 + kk * 4096, 16, 1024),
-                                  idesc_o, !(v.first && (i | t | kk) == 0));
-      } else {
-        for (int kk = 0; kk < steps; ++kk)
-          tc_mma_pair_tmem_a(d, a + i * 32 + kk * 8, smem_desc_sw128(vb + kk * 2048, 8192, 1024), idesc_o,
-                             !(v.first && (i | kk) == 0));
-        granule_done();
-      }
+    if (v.first && !cx.wait(OFree, (v.piece & 1) ^ 1)) return false;
+    if (!cx.wait(VFull + buf, (p_cnt >> 1) & 1)) return false;
+    if (v.tail && !cx.wait_pair(TailReady + buf, tails[buf]++ & 1)) return false;
+    if (!cx.wait(PFull + buf, (p_cnt >> 1) & 1)) return false;
+    tc_fence_after();
+    const uint64_t v_desc = ahead(v_desc0, buf * slot_bytes<kFp8>());
+    auto mma = [&](int i, int t, int kk) {  // page i, term t of P (E4M3), step kk
+      if constexpr (kFp8)
+        tc_mma_pair_f8_tmem_a(d, a + t * 32 + i * 16 + kk * 8, ahead(v_desc, i * 8192 + kk * 4096), idesc_o,
+                              (i | t | kk) != 0 || !v.first);
+      else
+        tc_mma_pair_tmem_a(d, a + i * 32 + kk * 8, ahead(v_desc, i * 16384 + kk * 2048), idesc_o, (i | kk) != 0 || !v.first);
+    };
+    constexpr int kTerms = kFp8 ? 2 : 1;
+    if (v.valid == kUnitKeys) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+          for (int kk = 0; kk < kSteps; ++kk) mma(i, t, kk);
+    } else {
+      for (int i = 0; i * kPageSize < v.valid; ++i)
+        for (int t = 0; t < kTerms; ++t)
+          for (int kk = 0; kk < min(kSteps, (v.valid - i * kPageSize + kStep - 1) / kStep); ++kk) mma(i, t, kk);
     }
-    if (kFp8) granule_done();
     tc_commit_pair(cx.bar(PvDone + buf));
     ++p_cnt;
     return true;
@@ -729,7 +698,6 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
     good = kFp8 ? cx.wait_pair(QReady, pieces & 1) : cx.wait(QFull, pieces & 1);
     for (int u = q.u0; good && u < q.u1; ++u) {
       good = do_s();
-      if (good && u == q.u1 - 1) tc_commit_pair(cx.bar(QEmpty));
       if (good && pend.valid) good = do_pv(pend);
       const int valid = keys_in_unit(q, u);
       pend = Unit{valid, is_tail<kFp8>(q, valid), u == q.u0, pieces};
@@ -1040,7 +1008,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       tc_fence_before();
       __syncwarp();
       if (lane == 0) {
-        mbar_arrive_cluster(p_full + 8 * buf);
+        mbar_arrive_pair(p_full + 8 * buf);
         if (kFp8) mbar_arrive(cx.bar(ScEmpty + sc_slot));
       }
     }
@@ -1069,7 +1037,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     }
     tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(o_free);
+    if (lane == 0) mbar_arrive_pair(o_free);
   }
 }
 
@@ -1085,7 +1053,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   PlanSmem& plan = *reinterpret_cast<PlanSmem*>(gbase + Sm::plan);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Sm::misc);
   int* abort_flag = reinterpret_cast<int*>(gbase + Sm::misc + 4);
-  volatile uint32_t* tail_granule = reinterpret_cast<uint32_t*>(gbase + Sm::misc + 8);
   const int warp = threadIdx.x >> 5;
   Ctx cx{base, base + Sm::bars, cta_rank(), abort_flag, p.err, p.wait_budget_ns};
 
@@ -1112,7 +1079,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   pdl_wait_prior_grid();
   pdl_launch_dependents();
-  build_plan(p, plan, *reinterpret_cast<PlanScratch*>(gbase + Sm::ring), blockIdx.x == 0 ? p.err : nullptr);
+  build_plan(p, plan, *reinterpret_cast<PlanScratch*>(gbase + Sm::k), blockIdx.x == 0 ? p.err : nullptr);
   publish_plan(p, plan);
   cluster_sync();  // the other CTA's barriers are initialised, its scratch is done with
   tc_fence_after();
@@ -1123,9 +1090,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp < kSoftmaxWarps) {
     softmax_role<kFp8>(p, cx, plan, pair, lo, hi, tmem, gbase);
   } else if (warp == kProducerWarp) {
-    producer_role<kFp8>(p, &kmap, &vmap, &qmap, cx, plan, pair, lo, hi, tail_granule);
+    producer_role<kFp8>(p, &kmap, &vmap, &qmap, cx, plan, pair, lo, hi);
   } else if (warp == kTailWarp) {
-    tail_role<kFp8>(p, cx, plan, pair, lo, hi, tail_granule);
+    tail_role<kFp8>(p, cx, plan, pair, lo, hi);
   } else if (cx.rank == 0 && (threadIdx.x & 31) == 0) {
     mma_role<kFp8>(p, cx, plan, pair, lo, hi, tmem);
   }
