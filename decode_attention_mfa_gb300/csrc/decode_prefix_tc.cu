@@ -41,12 +41,13 @@
 // E4M3 cache: both products are 8-bit MMAs (kind::f8f6f4) on the raw codes. Q
 // enters as two E4M3 terms under a power of two per row, split in shared memory
 // when a row tile begins; P times the V scale enters as two E4M3 terms, kept
-// within [0, 2^8] by the same moving reference: with a the reference and p =
+// within 2^8 by the same moving reference: with a the reference and p =
 // 2^(logit - a), O sums p * v_scale * code and l sums p, so that any a gives
 // the same O / l, and a follows max(logit) + log2(largest V scale of the unit).
 // Two terms at twice the 16-bit rate cost the tensor cores what bf16 does.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <type_traits>
 
 #include "mfa_device.cuh"
 
@@ -69,10 +70,13 @@ constexpr int kSeqQBytes = 32768;      // one sequence's rows
 constexpr int kTmemCols = 512, kTmemO = 256, kSCols = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kTop = 8.0f;           // log2 units: P (E4M3: P * v_scale) stays below 2^8 between moves of the reference
-// Where a move leaves the largest of them: 2^0, and 2^5 for E4M3, whose small weights then lie above its smallest steps.
+// log2 units: P (E4M3: P * v_scale) stays below 2^top between moves of the reference, and a move leaves the largest of
+// them `headroom` below that. E4M3: below 2^0, held as codes of 2^8 times it (split_p2), so that a move leaves 2^5 as the
+// largest code and the small weights above the smallest steps.
 template <bool kFp8>
-__host__ __device__ constexpr float headroom() { return kFp8 ? 3.0f : kTop; }
+__host__ __device__ constexpr float top_weight() { return kFp8 ? 0.0f : 8.0f; }
+template <bool kFp8>
+__host__ __device__ constexpr float headroom() { return kFp8 ? 3.0f : 8.0f; }
 // Keys of one MMA of P V.
 template <bool kFp8>
 __host__ __device__ constexpr int key_step() { return kFp8 ? 32 : 16; }
@@ -160,6 +164,16 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
       : "memory");
   return ok != 0;
 }
+// Whether a phase is complete, without waiting for it.
+__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 // TMA load into this CTA's shared memory that completes on a barrier of the pair's leader.
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y,
                                                  uint32_t leader_bar, uint64_t cache_hint) {
@@ -208,6 +222,14 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
       "h"((uint16_t)3)
       : "memory");
+}
+
+// True in one thread of a converged warp. The compiler knows that it is one, and then issues a tcgen05 instruction behind
+// it without a loop over the threads that might be active.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+  return ok != 0;
 }
 
 struct Ctx {
@@ -626,26 +648,28 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
   const uint64_t q_desc = smem_desc_sw128(cx.base + Sm::q, 16, 1024);
   const uint64_t k_desc0 = smem_desc_sw128(cx.base + Sm::k, 16, 1024);
   const uint64_t v_desc0 = smem_desc_sw128(cx.base + Sm::v, kFp8 ? 16 : 8192, 1024);
-  auto do_s = [&]() -> bool {
+  // The tensor cores hold a few MMAs behind the one they work on, so what this thread does between two batches of them
+  // costs nothing as long as it is short: barriers are looked at in the middle of a batch, for the next one, and waited
+  // for only if that found them not yet done.
+  bool k_ready = false, pv_ready = false;
+  auto peek = [&](int i, uint32_t parity) -> bool { return mbar_test_wait(cx.bar(i), parity); };
+  // S of unit s_cnt; p_next: a P V is to follow
+  auto do_s = [&](bool p_next) -> bool {
     const uint32_t buf = s_cnt & 1, d = tmem + buf * kSCols;  // its last reader, P V of two units ago, was issued before
-    if (!cx.wait(KFull + buf, (s_cnt >> 1) & 1)) return false;
+    if (!k_ready && !cx.wait(KFull + buf, (s_cnt >> 1) & 1)) return false;
+    k_ready = false;
     tc_fence_after();
     const uint64_t k_desc = ahead(k_desc0, buf * slot_bytes<kFp8>());
-    if constexpr (kFp8) {
 #pragma unroll
-      for (int t = 0; t < 2; ++t)  // Q's terms
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            tc_mma_pair_f8(d, ahead(q_desc, t * 32768 + h * 16384 + kk * 32), ahead(k_desc, h * 8192 + kk * 32), idesc_s,
-                           (t | h | kk) != 0);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          tc_mma_pair(d, ahead(q_desc, e * 16384 + kk * 32), ahead(k_desc, e * 8192 + kk * 32), idesc_s, (e | kk) != 0);
+    for (int i = 0; i < 16; ++i) {
+      if (i == 8) pv_ready = p_next && peek(VFull + (p_cnt & 1), (p_cnt >> 1) & 1) && peek(PFull + (p_cnt & 1), (p_cnt >> 1) & 1);
+      if constexpr (kFp8) {  // Q's term i / 8, 128-dim half, 32 dims
+        const int h = (i >> 2) & 1, kk = i & 3;
+        tc_mma_pair_f8(d, ahead(q_desc, (i >> 3) * 32768 + h * 16384 + kk * 32), ahead(k_desc, h * 8192 + kk * 32), idesc_s, i != 0);
+      } else {  // 64-dim block, 16 dims
+        const int e = i >> 2, kk = i & 3;
+        tc_mma_pair(d, ahead(q_desc, e * 16384 + kk * 32), ahead(k_desc, e * 8192 + kk * 32), idesc_s, i != 0);
+      }
     }
     tc_commit_pair(cx.bar(SFull + buf));
     ++s_cnt;
@@ -661,30 +685,32 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
     constexpr int kStep = key_step<kFp8>(), kSteps = kPageSize / kStep;
     const uint32_t buf = p_cnt & 1, a = tmem + buf * kSCols, d = tmem + kTmemO;
     if (v.first && !cx.wait(OFree, (v.piece & 1) ^ 1)) return false;
-    if (!cx.wait(VFull + buf, (p_cnt >> 1) & 1)) return false;
     if (v.tail && !cx.wait_pair(TailReady + buf, tails[buf]++ & 1)) return false;
-    if (!cx.wait(PFull + buf, (p_cnt >> 1) & 1)) return false;
+    if (!pv_ready && !(cx.wait(VFull + buf, (p_cnt >> 1) & 1) && cx.wait(PFull + buf, (p_cnt >> 1) & 1))) return false;
     tc_fence_after();
     const uint64_t v_desc = ahead(v_desc0, buf * slot_bytes<kFp8>());
-    auto mma = [&](int i, int t, int kk) {  // page i, term t of P (E4M3), step kk
+    auto mma = [&](int i, int t, int kk, bool add) {  // page i, term t of P (E4M3), step kk
       if constexpr (kFp8)
-        tc_mma_pair_f8_tmem_a(d, a + t * 32 + i * 16 + kk * 8, ahead(v_desc, i * 8192 + kk * 4096), idesc_o,
-                              (i | t | kk) != 0 || !v.first);
+        tc_mma_pair_f8_tmem_a(d, a + t * 32 + i * 16 + kk * 8, ahead(v_desc, i * 8192 + kk * 4096), idesc_o, add);
       else
-        tc_mma_pair_tmem_a(d, a + i * 32 + kk * 8, ahead(v_desc, i * 16384 + kk * 2048), idesc_o, (i | kk) != 0 || !v.first);
+        tc_mma_pair_tmem_a(d, a + i * 32 + kk * 8, ahead(v_desc, i * 16384 + kk * 2048), idesc_o, add);
     };
     constexpr int kTerms = kFp8 ? 2 : 1;
     if (v.valid == kUnitKeys) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < 2; ++i) {
 #pragma unroll
         for (int t = 0; t < kTerms; ++t)
 #pragma unroll
-          for (int kk = 0; kk < kSteps; ++kk) mma(i, t, kk);
+          for (int kk = 0; kk < kSteps; ++kk) mma(i, t, kk, (i | t | kk) != 0 || !v.first);
+        if (i == 0) k_ready = peek(KFull + (s_cnt & 1), (s_cnt >> 1) & 1);
+      }
     } else {
       for (int i = 0; i * kPageSize < v.valid; ++i)
         for (int t = 0; t < kTerms; ++t)
-          for (int kk = 0; kk < min(kSteps, (v.valid - i * kPageSize + kStep - 1) / kStep); ++kk) mma(i, t, kk);
+          for (int kk = 0; kk < min(kSteps, (v.valid - i * kPageSize + kStep - 1) / kStep); ++kk)
+            mma(i, t, kk, (i | t | kk) != 0 || !v.first);
+      k_ready = false;
     }
     tc_commit_pair(cx.bar(PvDone + buf));
     ++p_cnt;
@@ -697,18 +723,22 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
   while (good && next_piece(p, s, pair, hi, q)) {
     good = kFp8 ? cx.wait_pair(QReady, pieces & 1) : cx.wait(QFull, pieces & 1);
     for (int u = q.u0; good && u < q.u1; ++u) {
-      good = do_s();
+      good = do_s(pend.valid != 0);
       if (good && pend.valid) good = do_pv(pend);
       const int valid = keys_in_unit(q, u);
       pend = Unit{valid, is_tail<kFp8>(q, valid), u == q.u0, pieces};
     }
     if (kFp8 && good) {  // the softmax warps split the next Q once they have read this O
+      pv_ready = false;
       good = do_pv(pend);
       pend.valid = 0;
     }
     ++pieces;
   }
-  if (good && pend.valid) (void)do_pv(pend);
+  if (good && pend.valid) {
+    pv_ready = false;
+    (void)do_pv(pend);
+  }
   tc_commit_pair(cx.bar(Drain));  // every MMA is done before TMEM is given back
   (void)mbar_wait(cx.bar(Drain), 0, cx.budget, nullptr, p.err);
 }
@@ -840,19 +870,32 @@ __device__ __noinline__ float split_q(uint32_t q_addr, float* red, int row, int 
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
-// Two weights (times their V scales, in [0, 2^8]) as two E4M3 terms each. The first is their f16 value rounded to the
-// three mantissa bits of E4M3, in f16 by integer arithmetic on both halves (conversions are the scarce instruction
-// here: two of them a pair instead of three); the second rounds the rest. Below 2^-6, where E4M3 has fewer bits, the
-// first conversion rounds once more: an error of 2^-10 at most, 2^-15 of the unit's largest weight.
-__device__ __forceinline__ void split_p2(float2 x, uint32_t& c1, uint32_t& c2) {
-  const __half2 h = __floats2half2_rn(x.x, x.y);
-  const uint32_t bits = (*reinterpret_cast<const uint32_t*>(&h) + 0x00400040u) & 0xFF80FF80u;
-  __half2_raw r1;
-  r1.x = (unsigned short)bits;
-  r1.y = (unsigned short)(bits >> 16);
-  const __half2 rest = __hsub2(h, *reinterpret_cast<const __half2*>(&bits));
-  c1 = __nv_cvt_halfraw2_to_fp8x2(r1, __NV_SATFINITE, __NV_E4M3);
-  c2 = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, __NV_E4M3);
+// Two weights times their V scales, y in [-1, 1], as two E4M3 terms each of 2^8 y. E4M3 has exponent bias 7 and f16 has
+// 15, so the f16 bits of y (of which the exponent's top one is 0), the sign moved behind that bit and without the low
+// seven, are the E4M3 code of 2^8 y, subnormals included: integer arithmetic on both halves gives the first term, y's
+// bits rounded, and an f16 difference without error what is left. kConvert: the second term by a conversion, else by
+// the same arithmetic. A conversion keeps the unit that also does the exponentials for 8 cycles a warp, the integer form
+// the ALU for about as long, so that neither alone is best (with three conversions a pair the softmax took 2600 cycles a
+// unit, with integers alone 3600).
+struct TermPair {
+  uint32_t hi;  // codes of the first terms in bytes 1 and 3
+  uint32_t lo;  // of the second ones: bytes 0 and 1 if converted, else 1 and 3
+};
+__device__ __forceinline__ uint32_t e4m3_bytes(uint32_t f) { return ((f + f) & 0x7FFF7FFFu) | (f & 0x80008000u); }
+template <bool kConvert>
+__device__ __forceinline__ TermPair split_p2(float2 y) {
+  TermPair t;
+  const __half2 h = __floats2half2_rn(y.x, y.y);
+  const uint32_t up = *reinterpret_cast<const uint32_t*>(&h) + 0x00400040u, first = up & 0xFF80FF80u;
+  t.hi = e4m3_bytes(up);
+  __half2 rest = __hsub2(h, *reinterpret_cast<const __half2*>(&first));
+  if constexpr (kConvert) {
+    rest = __hmul2(rest, __half2half2(__ushort_as_half(0x5C00)));  // 2^8
+    t.lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, __NV_E4M3);
+  } else {
+    t.lo = e4m3_bytes(*reinterpret_cast<const uint32_t*>(&rest) + 0x00400040u);
+  }
+  return t;
 }
 
 template <bool kFp8>
@@ -907,6 +950,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           }
           const float most = fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w)));
           lift = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
+          l += lift - lift;                     // NaN for a scale that is not finite: the integer codes would hide it
           lift = fmaxf(__log2f(lift), -90.0f);  // so that p stays far from 2^128 whatever the scales are
         }
         tc_wait_ld();
@@ -935,7 +979,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           for (int c = 0; c < 32; ++c) top[c & 3] = c < 4 ? fmaxf(-x[c].x, -x[c].y) : max3(top[c & 3], -x[c].x, -x[c].y);
         }
         float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(mul);
-        big = cols > 0 ? big + (lift - (kTop - headroom<kFp8>())) : -INFINITY;
+        big = cols > 0 ? big + (lift - (top_weight<kFp8>() - headroom<kFp8>())) : -INFINITY;
         // the barrier also lets P overwrite the columns that the other warp has read
         if (barrier_rows_or(quad, big > m + headroom<kFp8>() || u == q.u0)) {
           red[half * 128 + row] = big;
@@ -961,48 +1005,49 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
         }
         const float ref = m == -INFINITY ? 0.0f : m;  // only infinite logits so far: weights of 0
         const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          x[c] = fma2(x[c], mul_2, ref_2);
-          x[c].x = ex2_approx(x[c].x);
-          x[c].y = ex2_approx(x[c].y);
-        }
-        if (cols < 64) {
+        // weights, their sum, and P; kPart: only the first `cols` keys count
+        auto weights = [&](auto part) {
+          constexpr bool kPart = decltype(part)::value;
+          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+          uint32_t w[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            if (2 * c >= cols) x[c].x = 0.0f;
-            if (2 * c + 1 >= cols) x[c].y = 0.0f;
-          }
-        }
-        float2 sum[2] = {x[0], x[1]};
-#pragma unroll
-        for (int c = 2; c < 32; ++c) sum[c & 1] = add2(sum[c & 1], x[c]);
-        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        uint32_t w[32];
-        if constexpr (kFp8) {  // words 0-15: first terms of the 64 keys, 16-31: second ones
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + 64 * half)[c / 2];
-            float2 a = mul2(x[c], make_float2(v4.x, v4.y)), b = mul2(x[c + 1], make_float2(v4.z, v4.w));
-            if (cols < 64) {  // a stale scale may be NaN
-              if (2 * c >= cols) a.x = 0.0f;
-              if (2 * c + 1 >= cols) a.y = 0.0f;
-              if (2 * c + 2 >= cols) b.x = 0.0f;
-              if (2 * c + 3 >= cols) b.y = 0.0f;
+            x[c] = fma2(x[c], mul_2, ref_2);
+            x[c].x = ex2_approx(x[c].x);
+            x[c].y = ex2_approx(x[c].y);
+            if constexpr (kPart) {
+              if (2 * c >= cols) x[c].x = 0.0f;
+              if (2 * c + 1 >= cols) x[c].y = 0.0f;
             }
-            uint32_t a1, a2, b1, b2;
-            split_p2(a, a1, a2);
-            split_p2(b, b1, b2);
-            w[c / 2] = a1 | b1 << 16;
-            w[16 + c / 2] = a2 | b2 << 16;
+            sum[c & 1] = add2(sum[c & 1], x[c]);
+            if constexpr (!kFp8) w[c] = pack_bf16(x[c].x, x[c].y);  // the A operand is 16 bits: half a step, 2^-8, of each weight
           }
-          tmem_st16(ts + 16 * half, reinterpret_cast<const float*>(w));
-          tmem_st16(ts + 32 + 16 * half, reinterpret_cast<const float*>(w + 16));
-        } else {
+          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          if constexpr (kFp8) {  // words 0-15: first terms of the 64 keys, 16-31: second ones
 #pragma unroll
-          for (int c = 0; c < 32; ++c) w[c] = pack_bf16(x[c].x, x[c].y);  // the A operand is 16 bits: half a step, 2^-8, of each weight
-          tmem_st32(ts + 32 * half, reinterpret_cast<const float*>(w));
-        }
+            for (int c = 0; c < 32; c += 2) {
+              const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + 64 * half)[c / 2];
+              float2 a = mul2(x[c], make_float2(v4.x, v4.y)), b = mul2(x[c + 1], make_float2(v4.z, v4.w));
+              if constexpr (kPart) {  // a stale scale may be NaN
+                if (2 * c >= cols) a.x = 0.0f;
+                if (2 * c + 1 >= cols) a.y = 0.0f;
+                if (2 * c + 2 >= cols) b.x = 0.0f;
+                if (2 * c + 3 >= cols) b.y = 0.0f;
+              }
+              const TermPair ta = split_p2<true>(a), tb = split_p2<true>(b);
+              w[c / 2] = __byte_perm(ta.hi, tb.hi, 0x7531);
+              w[16 + c / 2] = __byte_perm(ta.lo, tb.lo, 0x5410);
+            }
+            tmem_st16(ts + 16 * half, reinterpret_cast<const float*>(w));
+            tmem_st16(ts + 32 + 16 * half, reinterpret_cast<const float*>(w + 16));
+          } else {
+            tmem_st32(ts + 32 * half, reinterpret_cast<const float*>(w));
+          }
+        };
+        if (cols >= 64)
+          weights(std::false_type{});
+        else
+          weights(std::true_type{});
         tc_wait_st();
       }
       tc_fence_before();
@@ -1020,7 +1065,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       barrier_rows(quad);
       l += red[(half ^ 1) * 128 + row];
       const size_t at = (size_t)(q.row + (q.own ? 0 : j)) * kHeads + (row & 63);
-      const float inv = 1.0f / l;
+      const float inv = (kFp8 ? 0x1p-8f : 1.0f) / l;  // E4M3: the codes of P stand for 2^8 of it
       float* dst = p.part_o + at * kHeadDim;
 #pragma unroll 1
       for (int c = 128 * half; c < 128 * half + 128; c += 32) {
@@ -1093,7 +1138,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     producer_role<kFp8>(p, &kmap, &vmap, &qmap, cx, plan, pair, lo, hi);
   } else if (warp == kTailWarp) {
     tail_role<kFp8>(p, cx, plan, pair, lo, hi);
-  } else if (cx.rank == 0 && (threadIdx.x & 31) == 0) {
+  } else if (cx.rank == 0 && elect_one()) {
     mma_role<kFp8>(p, cx, plan, pair, lo, hi, tmem);
   }
   __syncwarp();
