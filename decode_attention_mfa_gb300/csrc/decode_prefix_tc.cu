@@ -31,20 +31,22 @@
 // Warp roles:
 //   warps 0-7  softmax: thread = row = TMEM lane; warp w and w + 4 share 32
 //              rows, 64 keys of a unit each, and agree on the reference maximum, which moves
-//              only when a row exceeds it by 2^8 (then O is rescaled).
+//              only when weights become large (then O is rescaled).
 //   warp 8     producer (TMA, each CTA its own halves, completing on the leader's barriers).
 //   warp 9     MMA issue (one thread of the leader) and TMEM allocation.
 //   warp 10    the rows behind a sequence's last token in V, zeroed up to the
-//              end of an MMA's 16 (E4M3: 32) keys: 0 * NaN of a stale row would poison P V.
+//              end of an MMA's 16 keys: 0 * NaN of a stale row would poison P V.
+//   warps 10-13 (E4M3 cache only, instead) V codes to f16, rows behind the last token to zero.
 // Every wait is bounded (the wait budget), as in the split kernel.
 //
-// E4M3 cache: both products are 8-bit MMAs (kind::f8f6f4) on the raw codes. Q
-// enters as two E4M3 terms under a power of two per row, split in shared memory
-// when a row tile begins; P times the V scale enters as two E4M3 terms, kept
-// within 2^8 by the same moving reference: with a the reference and p =
-// 2^(logit - a), O sums p * v_scale * code and l sums p, so that any a gives
-// the same O / l, and a follows max(logit) + log2(largest V scale of the unit).
-// Two terms at twice the 16-bit rate cost the tensor cores what bf16 does.
+// E4M3 cache: S is 8-bit MMAs (kind::f8f6f4) on the raw K codes, with Q as two
+// E4M3 terms under a power of two per row, split in shared memory when a row
+// tile begins (two terms at twice the 16-bit rate cost what bf16 does). For P V
+// four more warps turn the V codes times their scales into f16, the unit's
+// scales taken relative to the power of two 2^e above their largest, and P,
+// times 2^e, is f16 as well: each is off by 2^-11, and nothing that matters
+// falls out of f16's range, where E4M3 terms of P would flush a thousand small
+// weights beside one large one.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <type_traits>
@@ -54,37 +56,38 @@
 namespace mfa {
 namespace {
 
-constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kTailWarp = 10;
-constexpr int kThreads = 352;
+constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kTailWarp = 10, kConvertWarps = 4;
+template <bool kFp8>
+__host__ __device__ constexpr int threads() { return 32 * (kTailWarp + (kFp8 ? kConvertWarps : 1)); }
 // Two K and two V slots, of even and odd units, one CTA's half of a unit each: K one page of 256 dims, V 128 dims of two
 // pages (each page's half at kHalf). A K slot is free when S of its unit is done, a V slot when P V is, which the
 // softmax warps are told anyway: the issuing thread commits twice a unit. (With a ring of 16 KB granules it waited
 // four times and committed six times a unit, and a unit took 3600 cycles instead of XXXX.)
 template <bool kFp8>
-__host__ __device__ constexpr uint32_t slot_bytes() { return kFp8 ? 16384 : 32768; }
+__host__ __device__ constexpr uint32_t slot_bytes() { return kFp8 ? 16384 : 32768; }  // as loaded
+constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;                          // V as the MMAs read it, 16 bits
 constexpr int kUnitKeys = 2 * kPageSize;
 constexpr int kScaleSlots = 4;         // E4M3: 128 K scales and 128 V scales a unit
+constexpr int kMostScale = 100;        // of 2^e: far enough from 2^127 for what is divided by it
 constexpr int kScaleBytes = 1024;
 constexpr int kQBytes = 65536;         // 128 rows x 256 dims, four 64-dim blocks of [128 rows x 128 B]
 constexpr int kSeqQBytes = 32768;      // one sequence's rows
 constexpr int kTmemCols = 512, kTmemO = 256, kSCols = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// log2 units: P (E4M3: P * v_scale) stays below 2^top between moves of the reference, and a move leaves the largest of
-// them `headroom` below that. E4M3: below 2^0, held as codes of 2^8 times it (split_p2), so that a move leaves 2^5 as the
-// largest code and the small weights above the smallest steps.
+// A move of the reference leaves the row's largest weight (E4M3: times 2^e) at 2^kMoved: of bf16, whose relative step is
+// the same everywhere, anything will do, of f16 a value that leaves room both ways. The next move comes when the sum of
+// a thread's 64 weights of a unit passes kMostSum, so that none of them passes f16's range; the sum is needed anyway,
+// and a maximum is looked for only then.
 template <bool kFp8>
-__host__ __device__ constexpr float top_weight() { return kFp8 ? 0.0f : 8.0f; }
-template <bool kFp8>
-__host__ __device__ constexpr float headroom() { return kFp8 ? 3.0f : 8.0f; }
-// Keys of one MMA of P V.
-template <bool kFp8>
-__host__ __device__ constexpr int key_step() { return kFp8 ? 32 : 16; }
+__host__ __device__ constexpr float moved_to() { return kFp8 ? 4.0f : 0.0f; }
+constexpr float kMostSum = 32768.0f;
+constexpr int kKeyStep = 16;  // keys of one MMA of P V
 static_assert(kPrefixTileSeqs * kHeads == 256, "rows of a row tile");
 
 enum Bar {
   KFull = 0,                 // [2] leader: both CTAs' halves landed
-  VFull = KFull + 2,         // [2] leader
+  VFull = KFull + 2,         // [2] leader; E4M3: one arrival per converting warp of the pair
   QFull = VFull + 2,         // bf16: leader; E4M3: both, each its own rows
   QReady,                    // E4M3, leader: Q split into terms, one arrival per softmax warp of the pair
   SFull,                     // [2] both: S of even and odd units
@@ -93,10 +96,12 @@ enum Bar {
   OFree = PvDone + 2,        // leader: O has been read, one arrival per softmax warp of the pair
   Drain,                     // leader
   ScFull,                    // [kScaleSlots] E4M3, both
-  ScEmpty = ScFull + kScaleSlots,   // [kScaleSlots] one arrival per softmax warp of the CTA
+  ScEmpty = ScFull + kScaleSlots,   // [kScaleSlots] one arrival per softmax and converting warp of the CTA
   TailFull = ScEmpty + kScaleSlots, // [2] both: this CTA's V of a partial last unit landed (by V slot)
   TailReady = TailFull + 2,         // [2] leader: its rows behind the last token are zero, one arrival a CTA
-  kBars = TailReady + 2
+  RawFull = TailReady + 2,          // [2] E4M3, both: this CTA's V codes landed
+  RawEmpty = RawFull + 2,           // [2] one arrival per converting warp of the CTA
+  kBars = RawEmpty + 2
 };
 
 // The line of work as every CTA sees it. Indices of sequences and tiles fit 16 bits (at most 1024 sequences).
@@ -119,7 +124,8 @@ template <bool kFp8>
 struct Smem {
   static constexpr uint32_t k = 0;
   static constexpr uint32_t v = k + 2 * slot_bytes<kFp8>();
-  static constexpr uint32_t q = v + 2 * slot_bytes<kFp8>();
+  static constexpr uint32_t raw = v + 2 * kVSlotBytes;  // E4M3: V codes
+  static constexpr uint32_t q = raw + (kFp8 ? 2 * slot_bytes<kFp8>() : 0);
   static constexpr uint32_t scales = q + kQBytes;
   static constexpr uint32_t plan = scales + (kFp8 ? kScaleSlots * kScaleBytes : 0);
   static constexpr uint32_t red = (plan + (uint32_t)sizeof(PlanSmem) + 15) & ~15u;  // [2][128] exchange of the row halves
@@ -128,7 +134,7 @@ struct Smem {
   static constexpr uint32_t total = misc + 8;
 };
 static_assert(Smem<false>::total + 1024 <= 227 * 1024 && Smem<true>::total + 1024 <= 227 * 1024, "shared memory");
-static_assert(4 * slot_bytes<true>() >= sizeof(PlanScratch), "the plan's scratch lies in the K and V slots");
+static_assert(2 * slot_bytes<true>() + 2 * kVSlotBytes >= sizeof(PlanScratch), "the plan's scratch lies in the K and V slots");
 
 // ---------------------------------------------------------------- cluster pair
 __device__ __forceinline__ uint32_t cta_rank() {
@@ -144,13 +150,13 @@ __device__ __forceinline__ uint32_t map_to_leader(uint32_t addr) {
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// Arrival on a barrier of the other CTA. What it announces lies in tensor memory, which the tcgen05 fences order, so no
-// release at cluster scope is needed: that one waits for all of the thread's memory operations (a unit took 3800
-// cycles with it).
+// Arrival on a barrier of the pair's leader. What it announces is read by the MMAs alone, and lies in tensor memory,
+// which the tcgen05 fences order, or in this CTA's shared memory, which the proxy fence before it has made visible to
+// them, so no release at cluster scope is needed: that one takes 1500 cycles, most of a unit's time.
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// The same behind writes to shared memory that the other CTA's MMAs read.
+// The same with that release, where it is rare.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -205,15 +211,6 @@ __device__ __forceinline__ void tc_mma_pair_f8(uint32_t d_tmem, uint64_t a_desc,
       "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
       " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// A from tensor memory: 8-bit elements 4j .. 4j + 3 of a row in column j.
-__device__ __forceinline__ void tc_mma_pair_f8_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                      uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // Arrival on the barrier at the same offset of both CTAs once every MMA issued so far is done.
@@ -293,7 +290,7 @@ __device__ __forceinline__ int pages_of_group(const PlanSmem& s, int g) {
 // own, so that no row of a shared product has a mask and nothing behind its
 // last token is ever read for it. All threads; ends with a barrier.
 __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, uint32_t* err) {
-  const int n = p.n_groups, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = p.n_groups, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kThreads = blockDim.x;
   for (int g = threadIdx.x; g < n; g += kThreads) {
     int pages = __ldcg(p.prefix_pages + g);
     if (pages < 0 || pages > p.max_pages) {
@@ -390,7 +387,7 @@ __device__ __forceinline__ int busy_pairs(const PrefixParams& p, int units) { re
 // Where the combine finds each sequence's partial results.
 __device__ void publish_plan(const PrefixParams& p, const PlanSmem& s) {
   const int n = p.n_groups, C1 = s.cost[n], C = C1 + s.own[p.B], W = busy_pairs(p, C);
-  for (int b = blockIdx.x * kThreads + threadIdx.x; b < p.B; b += gridDim.x * kThreads) {
+  for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < p.B; b += gridDim.x * blockDim.x) {
     int4 parts = make_int4(0, 0, 0, 0);
     if (s.tail[b] & kBehind) {
       const int g = last_at_most(s.b0, n + 1, b), j = b - s.b0[g], i = j / kPrefixTileSeqs;
@@ -417,28 +414,27 @@ struct Piece {
   int u0, u1;            // units
   int row;               // partial result of its first sequence
   bool own;              // a sequence's own tokens
-  long long x;           // line position behind the tile
+  int x;                 // line position behind the tile
 };
-__device__ __forceinline__ bool next_piece(const PrefixParams& p, const PlanSmem& s, int pair, long long hi, Piece& q) {
+__device__ __forceinline__ bool next_piece(const PrefixParams& p, const PlanSmem& s, int pair, int hi, Piece& q) {
   const int n = p.n_groups, C1 = s.cost[n];
   while (q.x < hi) {
-    long long first;
-    int len;
+    int first, len;
     q.own = q.x >= C1;
     if (!q.own) {
-      const int g = last_at_most(s.cost, n, (int)q.x), lead = s.lead[g] & ~kOdd;
+      const int g = last_at_most(s.cost, n, q.x), lead = s.lead[g] & ~kOdd;
       len = (s.cost[g + 1] - s.cost[g]) / tiles_of_group(s, g);
-      const int i = ((int)q.x - s.cost[g]) / len;
-      first = s.cost[g] + (long long)i * len;
+      const int i = (q.x - s.cost[g]) / len;
+      first = s.cost[g] + i * len;
       q.b = s.b0[g] + i * kPrefixTileSeqs;
       q.seqs = min(kPrefixTileSeqs, s.b0[g + 1] - q.b);
       q.keys = (len - kPrefixPieceUnits) * kUnitKeys - ((s.lead[g] & kOdd) ? kPageSize : 0);
       q.pages = p.page_table + (size_t)lead * p.max_pages;
       q.row = (pair + s.tile[g] + i) * kPrefixTileSeqs;
     } else {
-      const int b = last_at_most(s.own, p.B, (int)(q.x - C1)), tail = s.tail[b];
+      const int b = last_at_most(s.own, p.B, q.x - C1), tail = s.tail[b];
       len = s.own[b + 1] - s.own[b];
-      first = (long long)C1 + s.own[b];
+      first = C1 + s.own[b];
       q.b = b;
       q.seqs = 1;
       q.keys = (len - kPrefixPieceUnits - 1) * kUnitKeys + (tail & ~kBehind);
@@ -446,8 +442,8 @@ __device__ __forceinline__ bool next_piece(const PrefixParams& p, const PlanSmem
       if (tail & kBehind) q.pages += pages_of_group(s, last_at_most(s.b0, n + 1, b));
       q.row = p.own_row0 + pair + b;
     }
-    q.u0 = max(0, (int)(q.x - first) - kPrefixPieceUnits);
-    q.u1 = (int)min((long long)len, hi - first) - kPrefixPieceUnits;
+    q.u0 = max(0, q.x - first - kPrefixPieceUnits);
+    q.u1 = min(len, hi - first) - kPrefixPieceUnits;
     q.x = first + len;
     if (q.u0 < q.u1) return true;
   }
@@ -455,8 +451,7 @@ __device__ __forceinline__ bool next_piece(const PrefixParams& p, const PlanSmem
 }
 __device__ __forceinline__ int keys_in_unit(const Piece& q, int u) { return min(kUnitKeys, q.keys - u * kUnitKeys); }
 // A last unit whose last MMA of P V reaches behind the sequence's last token.
-template <bool kFp8>
-__device__ __forceinline__ bool is_tail(const Piece& q, int valid) { return q.own && valid % key_step<kFp8>() != 0; }
+__device__ __forceinline__ bool is_tail(const Piece& q, int valid) { return q.own && valid % kKeyStep != 0; }
 
 // ---------------------------------------------------------------- producer
 // Page ids of a tile: a window of 64 held by the warp (32 ahead of need).
@@ -488,8 +483,7 @@ struct TilePages {
 
 template <bool kFp8>
 __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                              const CUtensorMap* qmap, const Ctx& cx, const PlanSmem& s, int pair, long long lo,
-                              long long hi) {
+                              const CUtensorMap* qmap, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi) {
   using Sm = Smem<kFp8>;
   constexpr uint32_t kSlot = slot_bytes<kFp8>(), kPage = kSlot / 2;
   constexpr int kCols = kFp8 ? 128 : 64;  // columns of a copy: 128 bytes
@@ -528,21 +522,28 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
     return true;
   };
   // V of unit `n`: this CTA's 128 dims of each page. That of a tail lands on this CTA's own barrier, for the warp that
-  // zeroes its rows.
+  // zeroes its rows; E4M3: all of it does, for the warps that convert it.
   auto load_v = [&](uint32_t n, int pa, int pb, bool tail, uint64_t pol) -> bool {
-    const uint32_t slot = n & 1;
-    if (n >= 2 && !cx.wait_warp(PvDone + slot, ((n >> 1) & 1) ^ 1)) return false;
-    if (lane == 0) {
-      const uint32_t dst = cx.base + Sm::v + slot * kSlot, bytes = pb >= 0 ? kSlot : kPage;
-      if (r == 0) mbar_arrive_expect_tx(cx.bar(VFull + slot), tail ? 0 : 2 * bytes);
-      if (tail) mbar_arrive_expect_tx(cx.bar(TailFull + slot), bytes);
-      const uint32_t bar = tail ? cx.bar(TailFull + slot) : cx.leader_bar(VFull + slot);
+    const uint32_t slot = n & 1, parity = ((n >> 1) & 1) ^ 1, bytes = pb >= 0 ? kSlot : kPage;
+    uint32_t dst, bar;
+    if constexpr (kFp8) {
+      if (!cx.wait_warp(RawEmpty + slot, parity)) return false;
+      dst = cx.base + Sm::raw + slot * kSlot;
+      bar = cx.bar(RawFull + slot);
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+    } else {
+      if (n >= 2 && !cx.wait_warp(PvDone + slot, parity)) return false;
+      dst = cx.base + Sm::v + slot * kSlot;
+      bar = tail ? cx.bar(TailFull + slot) : cx.leader_bar(VFull + slot);
+      if (lane == 0 && r == 0) mbar_arrive_expect_tx(cx.bar(VFull + slot), tail ? 0 : 2 * bytes);
+      if (lane == 0 && tail) mbar_arrive_expect_tx(bar, bytes);
+      tails[slot] += tail;
+    }
+    if (lane == 0)
       for (int i = 0; i < (pb >= 0 ? 2 : 1); ++i)
 #pragma unroll
         for (int d = 0; d < 128 / kCols; ++d)
           tma_load_2d_pair(dst + i * kPage + d * 8192, vmap, r * 128 + d * kCols, (i ? pb : pa) * kPageSize, bar, pol);
-    }
-    tails[slot] += tail;
     return true;
   };
   Piece q;
@@ -581,7 +582,7 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
       ++cnt;
       va = pa;
       vb = pb;
-      vtail = is_tail<kFp8>(q, valid);
+      vtail = is_tail(q, valid);
       vpol = pol;
     }
     if (kFp8 && good) {  // E4M3: the next row tile's Q is split only behind this one's last P V
@@ -595,7 +596,8 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
   if (lane == 0) {
     for (uint32_t k = cnt > 2 ? cnt - 2 : 0; k < cnt; ++k) {
       if (r == 0) (void)mbar_wait(cx.bar(KFull + (k & 1)), (k >> 1) & 1, cx.budget, nullptr, p.err);
-      if (r == 0 && (good || k + 1 < cnt)) (void)mbar_wait(cx.bar(VFull + (k & 1)), (k >> 1) & 1, cx.budget, nullptr, p.err);
+      if ((kFp8 || r == 0) && (good || k + 1 < cnt))
+        (void)mbar_wait(cx.bar((kFp8 ? RawFull : VFull) + (k & 1)), (k >> 1) & 1, cx.budget, nullptr, p.err);
     }
     for (int i = 0; i < 2; ++i)
       if (tails[i]) (void)mbar_wait(cx.bar(TailFull + i), (tails[i] - 1) & 1, cx.budget, nullptr, p.err);
@@ -608,9 +610,7 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
 }
 
 // ---------------------------------------------------------------- rows behind the last token
-template <bool kFp8>
-__device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, long long lo, long long hi) {
-  constexpr int kStep = key_step<kFp8>(), kChunks = kFp8 ? 1 : 2;  // 128 B chunks of a V row half: 128 or 64 dims
+__device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi) {
   const int lane = threadIdx.x & 31;
   uint32_t cnt = 0, tails[2] = {0, 0};
   Piece q;
@@ -618,13 +618,13 @@ __device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& 
   while (next_piece(p, s, pair, hi, q)) {
     cnt += q.u1 - q.u0;
     const int valid = keys_in_unit(q, q.u1 - 1);
-    if (!is_tail<kFp8>(q, valid)) continue;
+    if (!is_tail(q, valid)) continue;
     const uint32_t slot = (cnt - 1) & 1;
     if (!cx.wait_warp(TailFull + slot, tails[slot] & 1)) return;
     ++tails[slot];
-    const uint32_t base = cx.base + Smem<kFp8>::v + slot * slot_bytes<kFp8>() + (valid / kPageSize) * (slot_bytes<kFp8>() / 2);
-    const int row = valid % kPageSize, words = (kStep - valid % kStep) * 8;  // 16 B words of a chunk's rows
-    for (int i = lane; i < words * kChunks; i += 32) {
+    const uint32_t base = cx.base + Smem<false>::v + slot * kVSlotBytes + (valid / kPageSize) * kVPageBytes;
+    const int row = valid % kPageSize, words = (kKeyStep - valid % kKeyStep) * 8;  // 16 B words of a 64-dim chunk's rows
+    for (int i = lane; i < words * 2; i += 32) {
       const uint32_t at = base + (i / words) * 8192 + row * 128 + (i % words) * 16;
       asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
     }
@@ -634,12 +634,103 @@ __device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& 
   }
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[4]) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+}
+
+// The exponent e of a unit: 2^e is the power of two above the largest of its 128 V scales (sc; `valid` of them count,
+// those behind are stale). All lanes of a warp.
+__device__ __forceinline__ int unit_exponent(const float* sc, int valid, int lane) {
+  float4 v = reinterpret_cast<const float4*>(sc)[lane];
+  if (4 * lane + 3 >= valid) {
+    if (4 * lane >= valid) v.x = 0.0f;
+    if (4 * lane + 1 >= valid) v.y = 0.0f;
+    if (4 * lane + 2 >= valid) v.z = 0.0f;
+    v.w = 0.0f;
+  }
+  const float most = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+  const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23) - 126;
+  return max(-kMostScale, min(kMostScale, e));
+}
+__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^-e (at most 448), from the codes: per page [64 rows x 128
+// dims] to two 64-dim chunks of [64 rows x 128 B], both with the 128-byte swizzle. Thread t takes 16 codes of row t / 8
+// and of every 16th row after it; rows behind the last token become zeros. That the scales are applied here spares the
+// softmax threads 64 values each from shared memory, whose bandwidth the MMAs need.
+__device__ void convert_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi,
+                             const uint8_t* gbase) {
+  using Sm = Smem<true>;
+  const int lane = threadIdx.x & 31, t = threadIdx.x - 32 * kTailWarp;
+  const int row0 = t >> 3, c = t & 7;  // 16-code chunk: dims [16 c, 16 c + 16)
+  const uint32_t from = row0 * 128 + ((c ^ (row0 & 7)) << 4);  // rows 16 apart share the swizzle
+  const uint32_t to = (c >> 2) * 8192 + row0 * 128;
+  const uint32_t to0 = to + (((2 * (c & 3)) ^ (row0 & 7)) << 4), to1 = to + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4);
+  uint32_t n = 0;
+  Piece q;
+  q.x = lo;
+  while (next_piece(p, s, pair, hi, q)) {
+    for (int u = q.u0; u < q.u1; ++u, ++n) {
+      const uint32_t slot = n & 1, sc_slot = n % kScaleSlots;
+      const int valid = keys_in_unit(q, u);
+      const uint32_t src = cx.base + Sm::raw + slot * slot_bytes<true>() + from, dst = cx.base + Sm::v + slot * kVSlotBytes;
+      const float* sc = reinterpret_cast<const float*>(gbase + Sm::scales + sc_slot * kScaleBytes) + kUnitKeys;
+      if (!cx.wait_warp(ScFull + sc_slot, (n / kScaleSlots) & 1)) return;
+      const float down = exp2_int(-unit_exponent(sc, valid, lane));
+      __half2 scale[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) scale[i] = __float2half2_rn(sc[(i >> 2) * kPageSize + row0 + 16 * (i & 3)] * down);
+      if (!cx.wait_warp(RawFull + slot, (n >> 1) & 1)) return;
+      if (n >= 2 && !cx.wait_warp(PvDone + slot, ((n >> 1) & 1) ^ 1)) return;
+#pragma unroll
+      for (int page = 0; page < 2; ++page) {
+        uint4 v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
+        if (valid < kUnitKeys) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (page * kPageSize + row0 + 16 * i >= valid) {
+              v[i] = make_uint4(0u, 0u, 0u, 0u);
+              scale[4 * page + i] = __float2half2_rn(0.0f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t h[2][4];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r), scale[4 * page + i]);
+            h[k >> 2][k & 3] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          st_shared_v4(dst + page * kVPageBytes + i * 2048 + to0, h[0]);
+          st_shared_v4(dst + page * kVPageBytes + i * 2048 + to1, h[1]);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(cx.bar(RawEmpty + slot));
+        mbar_arrive(cx.bar(ScEmpty + sc_slot));
+        mbar_arrive_pair(cx.leader_bar(VFull + slot));
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------- MMA issue (one thread of the leader)
 template <bool kFp8>
-__device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, long long lo, long long hi,
+__device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi,
                          uint32_t tmem) {
-  constexpr uint32_t idesc_s = idesc_f16(256, kSCols, kFp8 ? 0 : 1, 0, 0);    // A = Q, B = K, both K-major (E4M3: format 0)
-  constexpr uint32_t idesc_o = idesc_f16(256, kHeadDim, kFp8 ? 0 : 1, 0, 1);  // A = P (TMEM), B = V (dim-major)
+  constexpr uint32_t idesc_s = idesc_f16(256, kSCols, kFp8 ? 0 : 1, 0, 0);    // A = Q, B = K, both K-major (format 0: E4M3)
+  constexpr uint32_t idesc_o = idesc_f16(256, kHeadDim, kFp8 ? 0 : 1, 0, 1);  // A = P (TMEM), B = V (dim-major; format 0: f16)
   using Sm = Smem<kFp8>;
   uint32_t pieces = 0, s_cnt = 0, p_cnt = 0, tails[2] = {0, 0};
   // Descriptors of the operands' first blocks; a block `bytes` further on has bytes / 16 more in the address field, which
@@ -647,7 +738,7 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
   auto ahead = [](uint64_t desc, uint32_t bytes) -> uint64_t { return desc + (bytes >> 4); };
   const uint64_t q_desc = smem_desc_sw128(cx.base + Sm::q, 16, 1024);
   const uint64_t k_desc0 = smem_desc_sw128(cx.base + Sm::k, 16, 1024);
-  const uint64_t v_desc0 = smem_desc_sw128(cx.base + Sm::v, kFp8 ? 16 : 8192, 1024);
+  const uint64_t v_desc0 = smem_desc_sw128(cx.base + Sm::v, 8192, 1024);
   // The tensor cores hold a few MMAs behind the one they work on, so what this thread does between two batches of them
   // costs nothing as long as it is short: barriers are looked at in the middle of a batch, for the next one, and waited
   // for only if that found them not yet done.
@@ -682,34 +773,27 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
     uint32_t piece;
   };
   auto do_pv = [&](const Unit& v) -> bool {
-    constexpr int kStep = key_step<kFp8>(), kSteps = kPageSize / kStep;
+    constexpr int kSteps = kPageSize / kKeyStep;
     const uint32_t buf = p_cnt & 1, a = tmem + buf * kSCols, d = tmem + kTmemO;
     if (v.first && !cx.wait(OFree, (v.piece & 1) ^ 1)) return false;
-    if (v.tail && !cx.wait_pair(TailReady + buf, tails[buf]++ & 1)) return false;
-    if (!pv_ready && !(cx.wait(VFull + buf, (p_cnt >> 1) & 1) && cx.wait(PFull + buf, (p_cnt >> 1) & 1))) return false;
+    if (!kFp8 && v.tail && !cx.wait_pair(TailReady + buf, tails[buf]++ & 1)) return false;
+    if (!pv_ready && !(cx.wait_pair(VFull + buf, (p_cnt >> 1) & 1) && cx.wait(PFull + buf, (p_cnt >> 1) & 1))) return false;
     tc_fence_after();
-    const uint64_t v_desc = ahead(v_desc0, buf * slot_bytes<kFp8>());
-    auto mma = [&](int i, int t, int kk, bool add) {  // page i, term t of P (E4M3), step kk
-      if constexpr (kFp8)
-        tc_mma_pair_f8_tmem_a(d, a + t * 32 + i * 16 + kk * 8, ahead(v_desc, i * 8192 + kk * 4096), idesc_o, add);
-      else
-        tc_mma_pair_tmem_a(d, a + i * 32 + kk * 8, ahead(v_desc, i * 16384 + kk * 2048), idesc_o, add);
+    const uint64_t v_desc = ahead(v_desc0, buf * kVSlotBytes);
+    auto mma = [&](int i, int kk, bool add) {  // page i, step kk
+      tc_mma_pair_tmem_a(d, a + i * 64 + (kk >> 1) * 32 + (kk & 1) * 8, ahead(v_desc, i * kVPageBytes + kk * 2048), idesc_o, add);
     };
-    constexpr int kTerms = kFp8 ? 2 : 1;
     if (v.valid == kUnitKeys) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int t = 0; t < kTerms; ++t)
-#pragma unroll
-          for (int kk = 0; kk < kSteps; ++kk) mma(i, t, kk, (i | t | kk) != 0 || !v.first);
+        for (int kk = 0; kk < kSteps; ++kk) mma(i, kk, (i | kk) != 0 || !v.first);
         if (i == 0) k_ready = peek(KFull + (s_cnt & 1), (s_cnt >> 1) & 1);
       }
     } else {
       for (int i = 0; i * kPageSize < v.valid; ++i)
-        for (int t = 0; t < kTerms; ++t)
-          for (int kk = 0; kk < min(kSteps, (v.valid - i * kPageSize + kStep - 1) / kStep); ++kk)
-            mma(i, t, kk, (i | t | kk) != 0 || !v.first);
+        for (int kk = 0; kk < min(kSteps, (v.valid - i * kPageSize + kKeyStep - 1) / kKeyStep); ++kk)
+          mma(i, kk, (i | kk) != 0 || !v.first);
       k_ready = false;
     }
     tc_commit_pair(cx.bar(PvDone + buf));
@@ -726,7 +810,7 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
       good = do_s(pend.valid != 0);
       if (good && pend.valid) good = do_pv(pend);
       const int valid = keys_in_unit(q, u);
-      pend = Unit{valid, is_tail<kFp8>(q, valid), u == q.u0, pieces};
+      pend = Unit{valid, is_tail(q, valid), u == q.u0, pieces};
     }
     if (kFp8 && good) {  // the softmax warps split the next Q once they have read this O
       pv_ready = false;
@@ -751,6 +835,10 @@ __device__ __forceinline__ float ex2_approx(float x) {
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // Two fp32 operations in one instruction.
@@ -778,11 +866,6 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
 // 32 bytes at once: a whole sector of one row a thread.
 __device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
@@ -802,21 +885,12 @@ __device__ __forceinline__ bool barrier_rows_or(int quad, bool pred) {
 }
 __device__ __forceinline__ void barrier_softmax() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[4]) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-}
-
 // E4M3: the bf16 Q of this CTA's 128 rows (four 64-dim blocks of [128 rows x 128 B], 128-byte swizzle) becomes, in
 // place, two E4M3 terms of Q * 2^e ([term][128-dim half][128 rows x 128 B]): t1 rounds the scaled value, t2 the rest,
 // which is exact unless it falls below the E4M3 normal range (2^-18.8 of the row's largest |q|). 2^e is the largest
 // power of two that keeps the row within the E4M3 maximum, 448. Thread (row, half) takes 128 dims of its row. All
 // softmax threads; red: their exchange. Returns 2^-e.
-__device__ __noinline__ float split_q(uint32_t q_addr, float* red, int row, int half) {
+__device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, int half) {
   uint4 v[16];  // 8 dims each
 #pragma unroll
   for (int j = 0; j < 16; ++j)
@@ -870,42 +944,12 @@ __device__ __noinline__ float split_q(uint32_t q_addr, float* red, int row, int 
   return __uint_as_float((uint32_t)(127 - e) << 23);
 }
 
-// Two weights times their V scales, y in [-1, 1], as two E4M3 terms each of 2^8 y. E4M3 has exponent bias 7 and f16 has
-// 15, so the f16 bits of y (of which the exponent's top one is 0), the sign moved behind that bit and without the low
-// seven, are the E4M3 code of 2^8 y, subnormals included: integer arithmetic on both halves gives the first term, y's
-// bits rounded, and an f16 difference without error what is left. kConvert: the second term by a conversion, else by
-// the same arithmetic. A conversion keeps the unit that also does the exponentials for 8 cycles a warp, the integer form
-// the ALU for about as long, so that neither alone is best (with three conversions a pair the softmax took 2600 cycles a
-// unit, with integers alone 3600).
-struct TermPair {
-  uint32_t hi;  // codes of the first terms in bytes 1 and 3
-  uint32_t lo;  // of the second ones: bytes 0 and 1 if converted, else 1 and 3
-};
-__device__ __forceinline__ uint32_t e4m3_bytes(uint32_t f) { return ((f + f) & 0x7FFF7FFFu) | (f & 0x80008000u); }
-template <bool kConvert>
-__device__ __forceinline__ TermPair split_p2(float2 y) {
-  TermPair t;
-  const __half2 h = __floats2half2_rn(y.x, y.y);
-  const uint32_t up = *reinterpret_cast<const uint32_t*>(&h) + 0x00400040u, first = up & 0xFF80FF80u;
-  t.hi = e4m3_bytes(up);
-  __half2 rest = __hsub2(h, *reinterpret_cast<const __half2*>(&first));
-  if constexpr (kConvert) {
-    rest = __hmul2(rest, __half2half2(__ushort_as_half(0x5C00)));  // 2^8
-    t.lo = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, __NV_E4M3);
-  } else {
-    t.lo = e4m3_bytes(*reinterpret_cast<const uint32_t*>(&rest) + 0x00400040u);
-  }
-  return t;
-}
-
 template <bool kFp8>
-__device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, long long lo,
-                             long long hi, uint32_t tmem, uint8_t* gbase) {
+__device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi, uint32_t tmem, uint8_t* gbase) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
   const float c2 = p.scale * kLog2e;
-  const bool neg = p.scale < 0.0f;  // the smallest product then makes the largest logit
   const uint32_t p_full = cx.leader_bar(PFull), o_free = cx.leader_bar(OFree);
   float* red = reinterpret_cast<float*>(gbase + Smem<kFp8>::red);
   uint32_t cnt = 0, pieces = 0;  // units, pieces so far
@@ -936,118 +980,104 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       tc_fence_after();
       if (mine) {
         const int valid = keys_in_unit(q, u), cols = min(64, valid - 64 * half);  // this thread's keys (none: <= 0)
-        float2 x[32];
-        tmem_ld32(ts + 64 * half, reinterpret_cast<float*>(x));
-        tmem_ld32(ts + 64 * half + 32, reinterpret_cast<float*>(x) + 32);
-        float lift = 0.0f;  // E4M3: log2 of the unit's largest V scale
-        if constexpr (kFp8) {
-          float4 v4 = reinterpret_cast<const float4*>(sc + 128)[lane];
-          if (4 * lane + 3 >= valid) {  // scales behind the last key are stale
-            if (4 * lane >= valid) v4.x = 0.0f;
-            if (4 * lane + 1 >= valid) v4.y = 0.0f;
-            if (4 * lane + 2 >= valid) v4.z = 0.0f;
-            v4.w = 0.0f;
-          }
-          const float most = fmaxf(fmaxf(fabsf(v4.x), fabsf(v4.y)), fmaxf(fabsf(v4.z), fabsf(v4.w)));
-          lift = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
-          l += lift - lift;                     // NaN for a scale that is not finite: the integer codes would hide it
-          lift = fmaxf(__log2f(lift), -90.0f);  // so that p stays far from 2^128 whatever the scales are
-        }
-        tc_wait_ld();
-        if constexpr (kFp8) {  // products times the K scales
+        // This thread's products, 32 keys at a time. P of 32 keys replaces the first 16 columns of their S.
+        float2 x[16];
+        const uint32_t tx = ts + 64 * half;
+        auto load = [&](int g) {
+          tmem_ld32(tx + g, reinterpret_cast<float*>(x));
+          tc_wait_ld();
+          if constexpr (kFp8) {  // times the scales of K
 #pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float4 k4 = reinterpret_cast<const float4*>(sc + 64 * half)[c / 2];
-            x[c] = mul2(x[c], make_float2(k4.x, k4.y));
-            x[c + 1] = mul2(x[c + 1], make_float2(k4.z, k4.w));
-          }
-        }
-        if (cols < 64) {  // behind the last key: out of the maximum, and weights of 0 below
-          const float out = neg ? 3.0e38f : -3.0e38f;
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            if (2 * c >= cols) x[c].x = out;
-            if (2 * c + 1 >= cols) x[c].y = out;
-          }
-        }
-        float top[4];
-        if (!neg) {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) top[c & 3] = c < 4 ? fmaxf(x[c].x, x[c].y) : max3(top[c & 3], x[c].x, x[c].y);
-        } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c) top[c & 3] = c < 4 ? fmaxf(-x[c].x, -x[c].y) : max3(top[c & 3], -x[c].x, -x[c].y);
-        }
-        float big = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * fabsf(mul);
-        big = cols > 0 ? big + (lift - (top_weight<kFp8>() - headroom<kFp8>())) : -INFINITY;
-        // the barrier also lets P overwrite the columns that the other warp has read
-        if (barrier_rows_or(quad, big > m + headroom<kFp8>() || u == q.u0)) {
-          red[half * 128 + row] = big;
-          barrier_rows(quad);
-          const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));
-          const float alpha = u == q.u0 || m == m_new ? 1.0f : ex2_approx(m - m_new);
-          m = m_new;
-          l *= alpha;
-          if (u != q.u0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
-            // O holds the units before this one; each of the two warps scales half of its columns
-            if (!wait_pv()) return;
-            tc_fence_after();
-#pragma unroll 1
-            for (int c = 128 * half; c < 128 * half + 128; c += 32) {
-              float o[32];
-              tmem_ld32(tmem + lanes + kTmemO + c, o);
-              tc_wait_ld();
-#pragma unroll
-              for (int k = 0; k < 32; ++k) o[k] *= alpha;
-              tmem_st32(tmem + lanes + kTmemO + c, o);
+            for (int c = 0; c < 16; c += 2) {
+              const float4 k4 = *reinterpret_cast<const float4*>(sc + 64 * half + g + 2 * c);
+              x[c] = mul2(x[c], make_float2(k4.x, k4.y));
+              x[c + 1] = mul2(x[c + 1], make_float2(k4.z, k4.w));
             }
-          }
-        }
-        const float ref = m == -INFINITY ? 0.0f : m;  // only infinite logits so far: weights of 0
-        const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
-        // weights, their sum, and P; kPart: only the first `cols` keys count
-        auto weights = [&](auto part) {
-          constexpr bool kPart = decltype(part)::value;
-          float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-          uint32_t w[32];
-#pragma unroll
-          for (int c = 0; c < 32; ++c) {
-            x[c] = fma2(x[c], mul_2, ref_2);
-            x[c].x = ex2_approx(x[c].x);
-            x[c].y = ex2_approx(x[c].y);
-            if constexpr (kPart) {
-              if (2 * c >= cols) x[c].x = 0.0f;
-              if (2 * c + 1 >= cols) x[c].y = 0.0f;
-            }
-            sum[c & 1] = add2(sum[c & 1], x[c]);
-            if constexpr (!kFp8) w[c] = pack_bf16(x[c].x, x[c].y);  // the A operand is 16 bits: half a step, 2^-8, of each weight
-          }
-          l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-          if constexpr (kFp8) {  // words 0-15: first terms of the 64 keys, 16-31: second ones
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float4 v4 = reinterpret_cast<const float4*>(sc + 128 + 64 * half)[c / 2];
-              float2 a = mul2(x[c], make_float2(v4.x, v4.y)), b = mul2(x[c + 1], make_float2(v4.z, v4.w));
-              if constexpr (kPart) {  // a stale scale may be NaN
-                if (2 * c >= cols) a.x = 0.0f;
-                if (2 * c + 1 >= cols) a.y = 0.0f;
-                if (2 * c + 2 >= cols) b.x = 0.0f;
-                if (2 * c + 3 >= cols) b.y = 0.0f;
-              }
-              const TermPair ta = split_p2<true>(a), tb = split_p2<true>(b);
-              w[c / 2] = __byte_perm(ta.hi, tb.hi, 0x7531);
-              w[16 + c / 2] = __byte_perm(ta.lo, tb.lo, 0x5410);
-            }
-            tmem_st16(ts + 16 * half, reinterpret_cast<const float*>(w));
-            tmem_st16(ts + 32 + 16 * half, reinterpret_cast<const float*>(w + 16));
-          } else {
-            tmem_st32(ts + 32 * half, reinterpret_cast<const float*>(w));
           }
         };
-        if (cols >= 64)
-          weights(std::false_type{});
-        else
-          weights(std::true_type{});
+        const int e = kFp8 ? unit_exponent(sc + kUnitKeys, valid, lane) : 0;
+        const float lift = (float)e;
+        uint32_t w[32];
+        float2 sum;
+        // weights of this thread's keys, their sum, and P; kPart: only the first `cols` of the 64 count
+        auto weights = [&](auto part) {
+          constexpr bool kPart = decltype(part)::value;
+          const float ref = m == -INFINITY ? 0.0f : m - lift;  // only infinite logits so far: weights of 0
+          const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
+          sum = make_float2(0.0f, 0.0f);
+          float2 sum1 = sum;
+#pragma unroll
+          for (int g = 0; g < 64; g += 32) {
+            load(g);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float2 y = fma2(x[c], mul_2, ref_2);
+              y.x = ex2_approx(y.x);
+              y.y = ex2_approx(y.y);
+              if constexpr (kPart) {
+                if (g + 2 * c >= cols) y.x = 0.0f;
+                if (g + 2 * c + 1 >= cols) y.y = 0.0f;
+              }
+              if (c & 1)
+                sum1 = add2(sum1, y);
+              else
+                sum = add2(sum, y);
+              // the A operand is 16 bits, half a step of each weight: 2^-8 (bf16), 2^-11 (f16)
+              w[g / 2 + c] = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+            }
+          }
+          sum = add2(sum, sum1);
+        };
+        // the largest logit of this thread's keys (log2 units)
+        auto largest = [&]() -> float {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int g = 0; g < 64; g += 32) {
+            load(g);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              if (g + 2 * c < cols) top = fmaxf(top, x[c].x * mul);
+              if (g + 2 * c + 1 < cols) top = fmaxf(top, x[c].y * mul);
+            }
+          }
+          return top;
+        };
+        bool move = u == q.u0;
+#pragma unroll 1
+        for (int tries = 0; tries < 2; ++tries) {
+          if (move) {
+            const float big = largest() + (lift - moved_to<kFp8>());
+            red[half * 128 + row] = big;
+            barrier_rows(quad);
+            const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));
+            const float alpha = u == q.u0 || m == m_new ? 1.0f : ex2_approx(m - m_new);
+            m = m_new;
+            l *= alpha;
+            if (u != q.u0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+              // O holds the units before this one; each of the two warps scales half of its columns
+              if (!wait_pv()) return;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+                float o[32];
+                tmem_ld32(tmem + lanes + kTmemO + c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                tmem_st32(tmem + lanes + kTmemO + c, o);
+              }
+            }
+          }
+          if (cols >= 64)
+            weights(std::false_type{});
+          else
+            weights(std::true_type{});
+          move = barrier_rows_or(quad, sum.x + sum.y > kMostSum);
+          if (!move) break;
+        }
+        l += (sum.x + sum.y) * (kFp8 ? exp2_int(-e) : 1.0f);
+        tmem_st16(tx, reinterpret_cast<const float*>(w));
+        tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
         tc_wait_st();
       }
       tc_fence_before();
@@ -1065,7 +1095,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       barrier_rows(quad);
       l += red[(half ^ 1) * 128 + row];
       const size_t at = (size_t)(q.row + (q.own ? 0 : j)) * kHeads + (row & 63);
-      const float inv = (kFp8 ? 0x1p-8f : 1.0f) / l;  // E4M3: the codes of P stand for 2^8 of it
+      const float inv = 1.0f / l;
       float* dst = p.part_o + at * kHeadDim;
 #pragma unroll 1
       for (int c = 128 * half; c < 128 * half + 128; c += 32) {
@@ -1087,7 +1117,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
 }
 
 template <bool kFp8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
     decode_prefix_tc_kernel(const __grid_constant__ PrefixParams p, const __grid_constant__ CUtensorMap kmap,
                             const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
   using Sm = Smem<kFp8>;
@@ -1105,7 +1135,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kBars; ++i) {
       const bool of_pair = i == PFull || i == PFull + 1 || i == OFree || i == QReady;  // every softmax warp of both CTAs
       const bool of_cta = i >= ScEmpty && i < ScEmpty + kScaleSlots;                   // of this one
-      mbar_init(cx.bar(i), of_pair ? 2 * kSoftmaxWarps : of_cta ? kSoftmaxWarps : i >= TailReady ? 2 : 1);
+      const bool of_converts = kFp8 && (i == VFull || i == VFull + 1);
+      mbar_init(cx.bar(i), of_pair                             ? 2 * kSoftmaxWarps
+                           : of_cta                            ? kSoftmaxWarps + kConvertWarps
+                           : of_converts                       ? 2 * kConvertWarps
+                           : i >= RawEmpty                     ? kConvertWarps
+                           : i >= TailReady && i < RawFull     ? 2
+                                                               : 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -1130,14 +1166,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int units = plan.cost[p.n_groups] + plan.own[p.B], W = busy_pairs(p, units), pair = blockIdx.x >> 1;
-  const long long lo = pair < W ? cta_cost_lo(pair, units, W) : 0, hi = pair < W ? cta_cost_lo(pair + 1, units, W) : 0;
+  const int lo = pair < W ? (int)cta_cost_lo(pair, units, W) : 0, hi = pair < W ? (int)cta_cost_lo(pair + 1, units, W) : 0;
 
   if (warp < kSoftmaxWarps) {
     softmax_role<kFp8>(p, cx, plan, pair, lo, hi, tmem, gbase);
   } else if (warp == kProducerWarp) {
     producer_role<kFp8>(p, &kmap, &vmap, &qmap, cx, plan, pair, lo, hi);
-  } else if (warp == kTailWarp) {
-    tail_role<kFp8>(p, cx, plan, pair, lo, hi);
+  } else if (warp >= kTailWarp) {
+    if constexpr (kFp8)
+      convert_role(p, cx, plan, pair, lo, hi, gbase);
+    else
+      tail_role(p, cx, plan, pair, lo, hi);
   } else if (cx.rank == 0 && elect_one()) {
     mma_role<kFp8>(p, cx, plan, pair, lo, hi, tmem);
   }
@@ -1156,7 +1195,7 @@ cudaError_t launch_prefix(const PrefixParams& p, const CUtensorMap& kmap, const 
   static int configured[kTrackedDevices] = {};
   const cudaError_t e = ensure_dynamic_smem(decode_prefix_tc_kernel<kFp8>, smem, configured);
   if (e != cudaSuccess) return e;
-  return launch_pdl(decode_prefix_tc_kernel<kFp8>, dim3(2 * p.pairs), dim3(kThreads), smem, stream, p, kmap, vmap, qmap);
+  return launch_pdl(decode_prefix_tc_kernel<kFp8>, dim3(2 * p.pairs), dim3(threads<kFp8>()), smem, stream, p, kmap, vmap, qmap);
 }
 }  // namespace
 
