@@ -7,26 +7,32 @@
 //     S = Q K^T,  P = exp2(scale log2(e) S - m),  O = P V,  l = P 1
 // over the prefix is ordinary matrix work: 4 * 64 * 256 flops a sequence and
 // key, against 1 KB (bf16) a key for the whole group, so from about five
-// sequences on the tensor cores bound it and not memory. The tokens behind the
-// prefix are bound by memory. Both are row tiles of one line of work, so that some SMs
-// stream while others compute; the LSE combine joins a sequence's parts.
+// sequences on the tensor cores bound it and not memory. What a sequence holds
+// behind the prefix is bound by memory.
 //
-// Tile: a cluster of two CTAs works on 256 rows (four sequences of a group, two
-// a CTA; one sequence for its own tokens) against units of 128 keys (two pages)
-// with tcgen05 MMAs of cta_group::2: each CTA holds the Q rows of its
-// sequences, one of the two K pages and half of V's dimensions, and both halves
-// feed the pair's MMAs. Against one CTA with 128 rows this halves what every SM
-// reads from L2 (128 KB in 2048 tensor cycles, which L2 cannot serve to 152
-// SMs) and what the MMAs read from shared memory for B. A sequence's own tokens
-// use a quarter of the rows, but then a unit still takes the tensor cores less
-// time (2048 cycles for a pair) than HBM at its share of the bandwidth (128 KB).
-// TMEM holds S twice (2 x 128 columns; P overwrites S in place and is the A
-// operand of P V from there) and O (256 columns): all of it.
+// Row tile: up to four neighbouring sequences, 256 rows, and as its keys the
+// pages of their prefix, then the own pages of the first sequence, of the
+// second, and so on. A page is therefore seen by all the rows of the tile or by those
+// of one sequence; the others' rows skip its softmax and are left out of its P V
+// MMAs (by their mask of output lanes, so that nothing in a sequence's pages, not
+// even a NaN, reaches another's result). Own pages use a quarter of the rows, but a unit of two
+// pages still takes the tensor cores less time (2048 cycles of a pair of SMs)
+// than HBM at the pair's share of the bandwidth (128 KB).
 //
-// Work split: the row tiles, one after the other, form a line of units
-// (kPrefixPieceUnits more for every tile: its Q load and partial result); each
-// pair takes an equal range of it (stream-K) and writes a normalised partial
-// result and its LSE per row tile that it holds units of.
+// A cluster of two CTAs, each with 128 of the rows, works on units of 128 keys
+// (two pages) with tcgen05 MMAs of cta_group::2: each CTA holds one of the two
+// K pages and half of V's dimensions, and both halves feed the pair's MMAs.
+// Against one CTA with 128 rows this halves what every SM reads from L2 (128 KB
+// in 2048 tensor cycles, which L2 cannot serve to 152 SMs) and what the MMAs
+// read from shared memory for B. TMEM holds S twice (2 x 128 columns; P
+// overwrites S in place and is the A operand of P V from there) and O (256
+// columns): all of it.
+//
+// Work split: the units of all row tiles, one after the other, form a line
+// (kPrefixPieceUnits more for every tile: its Q load and partial results); each
+// pair takes an equal range of it (stream-K) and writes, per row tile that it
+// holds units of, normalised partial results and LSEs of the sequences that see any of them;
+// the LSE combine joins a sequence's parts.
 //
 // Warp roles:
 //   warps 0-7  softmax: thread = row = TMEM lane; warp w and w + 4 share 32
@@ -42,7 +48,7 @@
 // E4M3 cache: S is 8-bit MMAs (kind::f8f6f4) on the raw K codes, with Q as two
 // E4M3 terms under a power of two per row, split in shared memory when a row
 // tile begins (two terms at twice the 16-bit rate cost what bf16 does). For P V
-// four more warps turn the V codes times their scales into f16, the unit's
+// four more warps turn the V codes times their scales into f16, a page's
 // scales taken relative to the power of two 2^e above their largest, and P,
 // times 2^e, is f16 as well: each is off by 2^-11, and nothing that matters
 // falls out of f16's range, where E4M3 terms of P would flush a thousand small
@@ -67,6 +73,7 @@ template <bool kFp8>
 __host__ __device__ constexpr uint32_t slot_bytes() { return kFp8 ? 16384 : 32768; }  // as loaded
 constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;                          // V as the MMAs read it, 16 bits
 constexpr int kUnitKeys = 2 * kPageSize;
+constexpr int kSeqs = kPrefixTileSeqs;
 constexpr int kScaleSlots = 4;         // E4M3: 128 K scales and 128 V scales a unit
 constexpr int kMostScale = 100;        // of 2^e: far enough from 2^127 for what is divided by it
 constexpr int kScaleBytes = 1024;
@@ -106,18 +113,17 @@ enum Bar {
 
 // The line of work as every CTA sees it. Indices of sequences and tiles fit 16 bits (at most 1024 sequences).
 struct PlanSmem {
-  int32_t cost[kMaxBatch + 1];   // units of the prefix tiles of the groups before g; [n_groups]: of all
-  int32_t own[kMaxBatch + 1];    // units of the own tokens of the sequences before b
-  uint16_t b0[kMaxBatch + 2];    // first sequence of group g
-  uint16_t lead[kMaxBatch];      // the sequence whose table row gives the prefix pages, | kOdd; kUnshared: not shared
-  uint16_t tile[kMaxBatch + 2];  // prefix tiles of the groups before g
-  uint16_t tail[kMaxBatch];      // keys in the last unit of b's own tokens (0: it has none), | kBehind
+  int32_t cost[kMaxBatch + 1];    // units of the row tiles before t; [tiles]: of all
+  int32_t pages[kMaxBatch];       // prefix pages of tile t
+  uint32_t len[kMaxBatch];        // tokens of sequence b, | kBehind
+  uint16_t first[kMaxBatch + 2];  // first sequence of tile t; [tiles]: B
+  uint16_t lead[kMaxBatch];       // the sequence whose table row gives tile t's prefix pages
+  int32_t tiles;
 };
-constexpr uint16_t kOdd = 0x8000;       // the prefix has an odd number of pages
-constexpr uint16_t kUnshared = 0x7FFF;
-constexpr uint16_t kBehind = 0x8000;    // b's own tokens begin behind its group's prefix
+constexpr uint32_t kBehind = 0x80000000u;  // b sees its tile's prefix, its own pages begin behind it
 struct PlanScratch {
-  int32_t count[kMaxBatch], lead[kMaxBatch], pages[kMaxBatch], len[kMaxBatch], group[kMaxBatch];
+  int32_t count[kMaxBatch], lead[kMaxBatch], pages[kMaxBatch], group[kMaxBatch];
+  uint16_t b0[kMaxBatch + 2];
 };
 
 template <bool kFp8>
@@ -213,6 +219,16 @@ __device__ __forceinline__ void tc_mma_pair_f8(uint32_t d_tmem, uint64_t a_desc,
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
+// The same without the output lanes (rows) of `off`: bit i of word w stands for row 32 w + i of the pair's 256.
+__device__ __forceinline__ void tc_mma_pair_tmem_a_masked(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                          const uint32_t (&off)[8], uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]),
+      "r"(off[4]), "r"(off[5]), "r"(off[6]), "r"(off[7])
+      : "memory");
+}
 // Arrival on the barrier at the same offset of both CTAs once every MMA issued so far is done.
 __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
   asm volatile(
@@ -276,19 +292,18 @@ __device__ __forceinline__ int warp_inclusive_sum(int x, int lane) {
   }
   return x;
 }
-__device__ __forceinline__ int tiles_of_group(const PlanSmem& s, int g) {
-  return (s.b0[g + 1] - s.b0[g] + kPrefixTileSeqs - 1) / kPrefixTileSeqs;
+__device__ __forceinline__ int own_tokens(const PlanSmem& s, int b, int prefix_pages) {
+  const uint32_t len = s.len[b];
+  return (int)(len & ~kBehind) - ((len & kBehind) ? prefix_pages * kPageSize : 0);
 }
-// Pages of a shared group's prefix.
-__device__ __forceinline__ int pages_of_group(const PlanSmem& s, int g) {
-  const int units = (s.cost[g + 1] - s.cost[g]) / tiles_of_group(s, g) - kPrefixPieceUnits;
-  return 2 * units - ((s.lead[g] & kOdd) ? 1 : 0);
-}
+__device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPageSize - 1) / kPageSize; }
 
 // A group shares its prefix if at least two of its sequences hold all of it;
-// a sequence that ends inside it (or an empty slot of the batch) is read on its
-// own, so that no row of a shared product has a mask and nothing behind its
-// last token is ever read for it. All threads; ends with a barrier.
+// a sequence that ends inside it (or an empty slot of the batch) reads its own
+// table row alone, so that no row has a mask within a shared page and nothing
+// behind its last token is ever read for it. Row tiles: four neighbours at a time within a
+// shared group, and within a run of sequences that share nothing. All threads;
+// ends with a barrier.
 __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, uint32_t* err) {
   const int n = p.n_groups, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kThreads = blockDim.x;
   for (int g = threadIdx.x; g < n; g += kThreads) {
@@ -302,7 +317,7 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, u
     t.lead[g] = kMaxBatch;
   }
   for (int b = threadIdx.x; b < p.B; b += kThreads)
-    t.len[b] = clamp_len(__ldcg(p.seq_lens + b), p.max_pages * kPageSize, err);
+    s.len[b] = (uint32_t)clamp_len(__ldcg(p.seq_lens + b), p.max_pages * kPageSize, err);
   if (warp == kThreads / 32 - 1) {  // starts, made non-decreasing within [0, B]: no sequence lies in two groups
     int top = 0;
     for (int g0 = 0; g0 <= n; g0 += 32) {
@@ -317,65 +332,70 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, u
       x = max(x, top);
       if (g <= n) {
         if (x != raw) raise_error(err, MFA_DEVERR_CAPACITY);
-        s.b0[g] = (uint16_t)x;
+        t.b0[g] = (uint16_t)x;
       }
       top = __shfl_sync(0xffffffffu, x, 31);
     }
   }
   __syncthreads();
   for (int b = threadIdx.x; b < p.B; b += kThreads) {
-    int of = -1;
-    if (b >= s.b0[0] && b < s.b0[n]) {
-      const int g = last_at_most(s.b0, n + 1, b), pages = t.pages[g];
-      if (pages > 0 && t.len[b] >= pages * kPageSize) {
-        of = g;
-        atomicAdd(&t.count[g], 1);
-        atomicMin(&t.lead[g], b);
+    int of = -1;  // the group whose whole prefix b holds, | a mark where it does not
+    if (b >= t.b0[0] && b < t.b0[n]) {
+      of = last_at_most(t.b0, n + 1, b);
+      const int pages = t.pages[of];
+      if (pages > 0 && (int)s.len[b] >= pages * kPageSize) {
+        s.len[b] |= kBehind;
+        atomicAdd(&t.count[of], 1);
+        atomicMin(&t.lead[of], b);
       }
     }
     t.group[b] = of;
   }
   __syncthreads();
   if (warp == 0) {
-    int units = 0, tiles = 0;
-    for (int g0 = 0; g0 < n; g0 += 32) {
-      const int g = g0 + lane;
-      const bool shared = g < n && t.count[g] >= 2;
-      const int nt = shared ? tiles_of_group(s, g) : 0;
-      const int nu = shared ? nt * ((t.pages[g] + 1) / 2 + kPrefixPieceUnits) : 0;
-      const int x = warp_inclusive_sum(nu, lane), y = warp_inclusive_sum(nt, lane);
-      if (g < n) {
-        s.cost[g] = units + x - nu;
-        s.tile[g] = (uint16_t)(tiles + y - nt);
-        s.lead[g] = shared ? (uint16_t)(t.lead[g] | ((t.pages[g] & 1) ? kOdd : 0)) : kUnshared;
-      }
-      units += __shfl_sync(0xffffffffu, x, 31);
-      tiles += __shfl_sync(0xffffffffu, y, 31);
-    }
-    if (lane == 0) s.cost[n] = units;
-  } else if (warp == 1) {
-    int units = 0;
+    // tiles begin every four sequences from where the shared group (or the run without one) begins
+    auto key = [&](int b) { return b >= 0 && t.group[b] >= 0 && t.count[t.group[b]] >= 2 ? t.group[b] : -1; };
+    int tiles = 0, run = 0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int b = b0 + lane;
-      int rest = 0, u = 0;
-      uint16_t behind = 0;
-      if (b < p.B) {
-        const int g = t.group[b];
-        rest = t.len[b];
-        if (g >= 0 && t.count[g] >= 2) {
-          rest -= t.pages[g] * kPageSize;
-          behind = kBehind;
-        }
-        u = rest > 0 ? (rest + kUnitKeys - 1) / kUnitKeys + kPrefixPieceUnits : 0;
+      const int b = b0 + lane, g = b < p.B ? key(b) : -1;
+      int start = b < p.B && (b == 0 || key(b - 1) != g) ? b : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, start, o);
+        if (lane >= o) start = max(start, y);
+      }
+      start = max(start, run);
+      const bool begins = b < p.B && (b - start) % kSeqs == 0;
+      const uint32_t all = __ballot_sync(0xffffffffu, begins);
+      if (begins) {
+        const int i = tiles + __popc(all & ((1u << lane) - 1));
+        s.first[i] = (uint16_t)b;
+        s.pages[i] = g >= 0 ? t.pages[g] : 0;
+        s.lead[i] = g >= 0 ? (uint16_t)t.lead[g] : 0;
+      }
+      if (b < p.B && g < 0) s.len[b] &= ~kBehind;
+      tiles += __popc(all);
+      run = __shfl_sync(0xffffffffu, start, 31);
+    }
+    if (lane == 0) {
+      s.first[tiles] = (uint16_t)p.B;
+      s.tiles = tiles;
+    }
+    __syncwarp();
+    int units = 0;
+    for (int t0 = 0; t0 < tiles; t0 += 32) {
+      const int i = t0 + lane;
+      int u = 0;
+      if (i < tiles) {
+        int pages = s.pages[i];
+        for (int b = s.first[i]; b < s.first[i + 1]; ++b) pages += pages_of(own_tokens(s, b, s.pages[i]));
+        u = pages ? (pages + 1) / 2 + kPrefixPieceUnits : 0;
       }
       const int x = warp_inclusive_sum(u, lane);
-      if (b < p.B) {
-        s.own[b] = units + x - u;
-        s.tail[b] = (uint16_t)((rest > 0 ? (rest - 1) % kUnitKeys + 1 : 0) | behind);
-      }
+      if (i < tiles) s.cost[i] = units + x - u;
       units += __shfl_sync(0xffffffffu, x, 31);
     }
-    if (lane == 0) s.own[p.B] = units;
+    if (lane == 0) s.cost[tiles] = units;
   }
   fence_proxy_async_smem();  // the scratch is TMA's from here on
   __syncthreads();
@@ -384,63 +404,70 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, u
 // Pairs that have work: with fewer units than pairs, every range holds one.
 __device__ __forceinline__ int busy_pairs(const PrefixParams& p, int units) { return min(p.pairs, max(units, 1)); }
 
-// Where the combine finds each sequence's partial results.
+// Where the combine finds each sequence's partial results: of the pairs that hold prefix units, and of those that hold
+// pages of its own.
 __device__ void publish_plan(const PrefixParams& p, const PlanSmem& s) {
-  const int n = p.n_groups, C1 = s.cost[n], C = C1 + s.own[p.B], W = busy_pairs(p, C);
+  const int C = s.cost[s.tiles], W = busy_pairs(p, C);
   for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < p.B; b += gridDim.x * blockDim.x) {
+    const int t = last_at_most(s.first, s.tiles, b), j = b - s.first[t], prefix = s.pages[t];
+    int c = prefix;
+    for (int i = s.first[t]; i < b; ++i) c += pages_of(own_tokens(s, i, prefix));
+    const int own = pages_of(own_tokens(s, b, prefix));
+    auto pair_of = [&](int page) { return cta_of_cost((long long)s.cost[t] + kPrefixPieceUnits + page / 2, C, W); };
+    auto row = [&](int w) { return (w + t) * kSeqs + j; };
     int4 parts = make_int4(0, 0, 0, 0);
-    if (s.tail[b] & kBehind) {
-      const int g = last_at_most(s.b0, n + 1, b), j = b - s.b0[g], i = j / kPrefixTileSeqs;
-      const int len = (s.cost[g + 1] - s.cost[g]) / tiles_of_group(s, g);  // units of one tile
-      const long long x = s.cost[g] + (long long)i * len;
-      const int w = cta_of_cost(x + kPrefixPieceUnits, C, W);
-      parts.x = (w + s.tile[g] + i) * kPrefixTileSeqs + j % kPrefixTileSeqs;
-      parts.y = cta_of_cost(x + len - 1, C, W) - w + 1;
+    int w = -1;  // the last pair so far
+    if (s.len[b] & kBehind) {
+      const int w0 = pair_of(0);
+      w = pair_of(prefix - 1);
+      parts.x = row(w0);
+      parts.y = w - w0 + 1;
     }
-    if (s.tail[b] & ~kBehind) {
-      const int w = cta_of_cost((long long)C1 + s.own[b] + kPrefixPieceUnits, C, W);
-      parts.z = p.own_row0 + w + b;
-      parts.w = cta_of_cost((long long)C1 + s.own[b + 1] - 1, C, W) - w + 1;
+    if (own) {
+      const int w0 = max(w + 1, pair_of(c));
+      parts.z = row(w0);
+      parts.w = max(0, pair_of(c + own - 1) - w0 + 1);
     }
     p.parts[b] = parts;
   }
 }
 
-// A pair's pieces, in order: units [u0, u1) of one row tile.
+// A pair's pieces, in order: units [u0, u1) of one row tile. Page k of the tile is the prefix's for k < c[0], then
+// sequence s's for c[s] <= k < c[s + 1].
 struct Piece {
-  const int32_t* pages;  // page-table entries of the tile's keys
-  int b, seqs;           // first sequence, sequences (1 to kPrefixTileSeqs)
-  int keys;              // keys of the tile
-  int u0, u1;            // units
-  int row;               // partial result of its first sequence
-  bool own;              // a sequence's own tokens
-  int x;                 // line position behind the tile
+  int t;              // row tile
+  int b, seqs;        // first sequence, sequences (1 to kSeqs)
+  int c[kSeqs + 1];
+  uint32_t tails;     // byte s: tokens on the last own page of sequence s
+  uint32_t behind;    // bit s: sequence s sees the prefix
+  int u0, u1;         // units
+  int x;              // line position behind the tile
+  __device__ int owner(int k) const {  // kSeqs: the prefix's
+    return k < c[0] ? kSeqs : k < c[1] ? 0 : k < c[2] ? 1 : k < c[3] ? 2 : 3;
+  }
+  // tokens on page k, 0 behind the tile's last page
+  __device__ int tokens(int k) const {
+    if (k < c[0]) return kPageSize;
+    if (k >= c[kSeqs]) return 0;
+    const int s = owner(k);
+    const int end = s == 0 ? c[1] : s == 1 ? c[2] : s == 2 ? c[3] : c[4];
+    return k + 1 < end ? kPageSize : (int)((tails >> (8 * s)) & 0xFF);
+  }
 };
-__device__ __forceinline__ bool next_piece(const PrefixParams& p, const PlanSmem& s, int pair, int hi, Piece& q) {
-  const int n = p.n_groups, C1 = s.cost[n];
+__device__ __forceinline__ bool next_piece(const PlanSmem& s, int hi, Piece& q) {
   while (q.x < hi) {
-    int first, len;
-    q.own = q.x >= C1;
-    if (!q.own) {
-      const int g = last_at_most(s.cost, n, q.x), lead = s.lead[g] & ~kOdd;
-      len = (s.cost[g + 1] - s.cost[g]) / tiles_of_group(s, g);
-      const int i = (q.x - s.cost[g]) / len;
-      first = s.cost[g] + i * len;
-      q.b = s.b0[g] + i * kPrefixTileSeqs;
-      q.seqs = min(kPrefixTileSeqs, s.b0[g + 1] - q.b);
-      q.keys = (len - kPrefixPieceUnits) * kUnitKeys - ((s.lead[g] & kOdd) ? kPageSize : 0);
-      q.pages = p.page_table + (size_t)lead * p.max_pages;
-      q.row = (pair + s.tile[g] + i) * kPrefixTileSeqs;
-    } else {
-      const int b = last_at_most(s.own, p.B, q.x - C1), tail = s.tail[b];
-      len = s.own[b + 1] - s.own[b];
-      first = C1 + s.own[b];
-      q.b = b;
-      q.seqs = 1;
-      q.keys = (len - kPrefixPieceUnits - 1) * kUnitKeys + (tail & ~kBehind);
-      q.pages = p.page_table + (size_t)b * p.max_pages;
-      if (tail & kBehind) q.pages += pages_of_group(s, last_at_most(s.b0, n + 1, b));
-      q.row = p.own_row0 + pair + b;
+    const int t = last_at_most(s.cost, s.tiles, q.x), first = s.cost[t], len = s.cost[t + 1] - first;
+    q.t = t;
+    q.b = s.first[t];
+    q.seqs = s.first[t + 1] - q.b;
+    q.c[0] = s.pages[t];
+    q.tails = q.behind = 0;
+#pragma unroll
+    for (int i = 0; i < kSeqs; ++i) {
+      const int tokens = i < q.seqs ? own_tokens(s, q.b + i, q.c[0]) : 0;
+      q.c[i + 1] = q.c[i] + pages_of(tokens);
+      q.tails |= (uint32_t)(tokens > 0 ? (tokens - 1) % kPageSize + 1 : 0) << (8 * i);
+      if (i < q.seqs && (s.len[q.b + i] & kBehind)) q.behind |= 1u << i;
     }
     q.u0 = max(0, q.x - first - kPrefixPieceUnits);
     q.u1 = min(len, hi - first) - kPrefixPieceUnits;
@@ -449,34 +476,41 @@ __device__ __forceinline__ bool next_piece(const PrefixParams& p, const PlanSmem
   }
   return false;
 }
-__device__ __forceinline__ int keys_in_unit(const Piece& q, int u) { return min(kUnitKeys, q.keys - u * kUnitKeys); }
-// A last unit whose last MMA of P V reaches behind the sequence's last token.
-__device__ __forceinline__ bool is_tail(const Piece& q, int valid) { return q.own && valid % kKeyStep != 0; }
+// Whether the last MMA of P V on a page of so many tokens reaches behind them.
+__device__ __forceinline__ bool is_partial(int tokens) { return tokens % kKeyStep != 0; }
 
 // ---------------------------------------------------------------- producer
 // Page ids of a tile: a window of 64 held by the warp (32 ahead of need).
 struct TilePages {
-  const int32_t* row;
   int end, base, a, b;
-  __device__ int fetch(int pg, const PrefixParams& p) const {
-    if (pg >= end) return 0;
-    const int id = __ldg(row + pg);
+  __device__ int fetch(int k, const PrefixParams& p, const PlanSmem& s, const Piece& q) const {
+    if (k >= end) return 0;
+    const int o = q.owner(k);
+    size_t at;
+    if (o == kSeqs) {
+      at = (size_t)s.lead[q.t] * p.max_pages + k;
+    } else {
+      const int c = o == 0 ? q.c[0] : o == 1 ? q.c[1] : o == 2 ? q.c[2] : q.c[3];
+      at = (size_t)(q.b + o) * p.max_pages + (k - c) + (((q.behind >> o) & 1) ? q.c[0] : 0);
+    }
+    const int id = __ldg(p.page_table + at);
     if (id >= 0 && id < p.num_pages) return id;
     raise_error(p.err, MFA_DEVERR_PAGE);
     return 0;
   }
-  __device__ void start(int pg, const PrefixParams& p, int lane) {
-    base = pg;
-    a = fetch(base + lane, p);
-    b = fetch(base + 32 + lane, p);
+  __device__ void start(int k, const PrefixParams& p, const PlanSmem& s, const Piece& q, int lane) {
+    end = min(q.c[kSeqs], 2 * q.u1);
+    base = k;
+    a = fetch(base + lane, p, s, q);
+    b = fetch(base + 32 + lane, p, s, q);
   }
-  __device__ int get(int pg, const PrefixParams& p, int lane) {
-    while (pg >= base + 64) {
+  __device__ int get(int k, const PrefixParams& p, const PlanSmem& s, const Piece& q, int lane) {
+    while (k >= base + 64) {
       base += 32;
       a = b;
-      b = fetch(base + 32 + lane, p);
+      b = fetch(base + 32 + lane, p, s, q);
     }
-    const int i = pg - base;
+    const int i = k - base;
     return i < 32 ? __shfl_sync(0xffffffffu, a, i) : __shfl_sync(0xffffffffu, b, i - 32);
   }
 };
@@ -552,12 +586,9 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
   int va = -1, vb = -1;  // the last of them: its V is still to be loaded (V trails K by a unit, as the MMAs use them)
   bool vtail = false, good = true;
   uint64_t vpol = pol_own;
-  while (good && next_piece(p, s, pair, hi, q)) {
+  while (good && next_piece(s, hi, q)) {
     TilePages ids;
-    ids.row = q.pages;
-    ids.end = min((q.keys + kPageSize - 1) / kPageSize, 2 * q.u1);
-    ids.start(2 * q.u0, p, lane);
-    const uint64_t pol = q.own ? pol_own : pol_shared;
+    ids.start(2 * q.u0, p, s, q, lane);
     // Q may be replaced once S of every unit so far is done
     good = cnt == 0 || cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1);
     if (!good) break;
@@ -574,15 +605,15 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
     }
     ++pieces;
     for (int u = q.u0; good && u < q.u1; ++u) {
-      const int valid = keys_in_unit(q, u);
-      const int pa = ids.get(2 * u, p, lane);
-      const int pb = valid > kPageSize ? ids.get(2 * u + 1, p, lane) : -1;
+      const int pa = ids.get(2 * u, p, s, q, lane);
+      const int pb = 2 * u + 1 < q.c[kSeqs] ? ids.get(2 * u + 1, p, s, q, lane) : -1;
+      const uint64_t pol = 2 * u < q.c[0] ? pol_shared : pol_own;
       good = load_k(cnt, pa, pb, pol);
       if (good && va >= 0) good = load_v(cnt - 1, va, vb, vtail, vpol);
       ++cnt;
       va = pa;
       vb = pb;
-      vtail = is_tail(q, valid);
+      vtail = is_partial(q.tokens(2 * u)) || is_partial(q.tokens(2 * u + 1));
       vpol = pol;
     }
     if (kFp8 && good) {  // E4M3: the next row tile's Q is split only behind this one's last P V
@@ -615,22 +646,26 @@ __device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& 
   uint32_t cnt = 0, tails[2] = {0, 0};
   Piece q;
   q.x = lo;
-  while (next_piece(p, s, pair, hi, q)) {
-    cnt += q.u1 - q.u0;
-    const int valid = keys_in_unit(q, q.u1 - 1);
-    if (!is_tail(q, valid)) continue;
-    const uint32_t slot = (cnt - 1) & 1;
-    if (!cx.wait_warp(TailFull + slot, tails[slot] & 1)) return;
-    ++tails[slot];
-    const uint32_t base = cx.base + Smem<false>::v + slot * kVSlotBytes + (valid / kPageSize) * kVPageBytes;
-    const int row = valid % kPageSize, words = (kKeyStep - valid % kKeyStep) * 8;  // 16 B words of a 64-dim chunk's rows
-    for (int i = lane; i < words * 2; i += 32) {
-      const uint32_t at = base + (i / words) * 8192 + row * 128 + (i % words) * 16;
-      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+  while (next_piece(s, hi, q)) {
+    for (int u = q.u0; u < q.u1; ++u, ++cnt) {
+      const int tokens[2] = {q.tokens(2 * u), q.tokens(2 * u + 1)};
+      if (!is_partial(tokens[0]) && !is_partial(tokens[1])) continue;
+      const uint32_t slot = cnt & 1;
+      if (!cx.wait_warp(TailFull + slot, tails[slot] & 1)) return;
+      ++tails[slot];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!is_partial(tokens[i])) continue;
+        const uint32_t base = cx.base + Smem<false>::v + slot * kVSlotBytes + i * kVPageBytes + tokens[i] * 128;
+        const int words = (kKeyStep - tokens[i] % kKeyStep) * 8;  // 16 B words of a 64-dim chunk's rows
+        for (int w = lane; w < words * 2; w += 32)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(base + (w / words) * 8192 + (w % words) * 16), "r"(0)
+                       : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair(cx.leader_bar(TailReady + slot));
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive_cluster(cx.leader_bar(TailReady + slot));
   }
 }
 
@@ -643,23 +678,18 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
-// The exponent e of a unit: 2^e is the power of two above the largest of its 128 V scales (sc; `valid` of them count,
+// The exponent e of a page: 2^e is the power of two above the largest of its 64 V scales (sc; `valid` of them count,
 // those behind are stale). All lanes of a warp.
-__device__ __forceinline__ int unit_exponent(const float* sc, int valid, int lane) {
-  float4 v = reinterpret_cast<const float4*>(sc)[lane];
-  if (4 * lane + 3 >= valid) {
-    if (4 * lane >= valid) v.x = 0.0f;
-    if (4 * lane + 1 >= valid) v.y = 0.0f;
-    if (4 * lane + 2 >= valid) v.z = 0.0f;
-    v.w = 0.0f;
-  }
-  const float most = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-  const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(most)) >> 23) - 126;
+__device__ __forceinline__ int page_exponent(const float* sc, int valid, int lane) {
+  float2 v = reinterpret_cast<const float2*>(sc)[lane];
+  if (2 * lane >= valid) v.x = 0.0f;
+  if (2 * lane + 1 >= valid) v.y = 0.0f;
+  const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(v.x), fabsf(v.y)))) >> 23) - 126;
   return max(-kMostScale, min(kMostScale, e));
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^-e (at most 448), from the codes: per page [64 rows x 128
+// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^-e (at most 448, e of the page), from the codes: per page [64 rows x 128
 // dims] to two 64-dim chunks of [64 rows x 128 B], both with the 128-byte swizzle. Thread t takes 16 codes of row t / 8
 // and of every 16th row after it; rows behind the last token become zeros. That the scales are applied here spares the
 // softmax threads 64 values each from shared memory, whose bandwidth the MMAs need.
@@ -674,30 +704,31 @@ __device__ void convert_role(const PrefixParams& p, const Ctx& cx, const PlanSme
   uint32_t n = 0;
   Piece q;
   q.x = lo;
-  while (next_piece(p, s, pair, hi, q)) {
+  while (next_piece(s, hi, q)) {
     for (int u = q.u0; u < q.u1; ++u, ++n) {
       const uint32_t slot = n & 1, sc_slot = n % kScaleSlots;
-      const int valid = keys_in_unit(q, u);
       const uint32_t src = cx.base + Sm::raw + slot * slot_bytes<true>() + from, dst = cx.base + Sm::v + slot * kVSlotBytes;
       const float* sc = reinterpret_cast<const float*>(gbase + Sm::scales + sc_slot * kScaleBytes) + kUnitKeys;
       if (!cx.wait_warp(ScFull + sc_slot, (n / kScaleSlots) & 1)) return;
-      const float down = exp2_int(-unit_exponent(sc, valid, lane));
-      __half2 scale[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) scale[i] = __float2half2_rn(sc[(i >> 2) * kPageSize + row0 + 16 * (i & 3)] * down);
       if (!cx.wait_warp(RawFull + slot, (n >> 1) & 1)) return;
       if (n >= 2 && !cx.wait_warp(PvDone + slot, ((n >> 1) & 1) ^ 1)) return;
 #pragma unroll
       for (int page = 0; page < 2; ++page) {
+        const int valid = q.tokens(2 * u + page);
+        const float down = exp2_int(-page_exponent(sc + page * kPageSize, valid, lane));
         uint4 v[4];
+        __half2 scale[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
-        if (valid < kUnitKeys) {
+        for (int i = 0; i < 4; ++i) {
+          v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
+          scale[i] = __float2half2_rn(sc[page * kPageSize + row0 + 16 * i] * down);
+        }
+        if (valid < kPageSize) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            if (page * kPageSize + row0 + 16 * i >= valid) {
+            if (row0 + 16 * i >= valid) {
               v[i] = make_uint4(0u, 0u, 0u, 0u);
-              scale[4 * page + i] = __float2half2_rn(0.0f);
+              scale[i] = __float2half2_rn(0.0f);
             }
         }
 #pragma unroll
@@ -707,7 +738,7 @@ __device__ void convert_role(const PrefixParams& p, const Ctx& cx, const PlanSme
 #pragma unroll
           for (int k = 0; k < 8; ++k) {
             const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r), scale[4 * page + i]);
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r), scale[i]);
             h[k >> 2][k & 3] = *reinterpret_cast<const uint32_t*>(&y);
           }
           st_shared_v4(dst + page * kVPageBytes + i * 2048 + to0, h[0]);
@@ -766,34 +797,49 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
     ++s_cnt;
     return true;
   };
-  // P V of a unit of `valid` keys: as many MMAs as hold one
+  // P V of a unit. A page is seen by the sequences of `seen` (bits); those without O in this piece yet get theirs from
+  // its first MMA, which does not add.
   struct Unit {
-    int valid;
-    bool tail, first;
+    int tokens[2];
+    uint32_t seen[2];
+    uint32_t all;  // the sequences of the tile
+    bool pending, first;
     uint32_t piece;
   };
+  uint32_t begun = 0;  // sequences that have O in the piece of the P V issued last
   auto do_pv = [&](const Unit& v) -> bool {
     constexpr int kSteps = kPageSize / kKeyStep;
     const uint32_t buf = p_cnt & 1, a = tmem + buf * kSCols, d = tmem + kTmemO;
-    if (v.first && !cx.wait(OFree, (v.piece & 1) ^ 1)) return false;
-    if (!kFp8 && v.tail && !cx.wait_pair(TailReady + buf, tails[buf]++ & 1)) return false;
-    if (!pv_ready && !(cx.wait_pair(VFull + buf, (p_cnt >> 1) & 1) && cx.wait(PFull + buf, (p_cnt >> 1) & 1))) return false;
+    if (v.first) {
+      begun = 0;
+      if (!cx.wait(OFree, (v.piece & 1) ^ 1)) return false;
+    }
+    if (!kFp8 && (is_partial(v.tokens[0]) || is_partial(v.tokens[1])) && !cx.wait(TailReady + buf, tails[buf]++ & 1)) return false;
+    if (!pv_ready && !(cx.wait(VFull + buf, (p_cnt >> 1) & 1) && cx.wait(PFull + buf, (p_cnt >> 1) & 1))) return false;
     tc_fence_after();
     const uint64_t v_desc = ahead(v_desc0, buf * kVSlotBytes);
-    auto mma = [&](int i, int kk, bool add) {  // page i, step kk
-      tc_mma_pair_tmem_a(d, a + i * 64 + (kk >> 1) * 32 + (kk & 1) * 8, ahead(v_desc, i * kVPageBytes + kk * 2048), idesc_o, add);
-    };
-    if (v.valid == kUnitKeys) {
+    auto a_of = [&](int i, int kk) { return a + i * 64 + (kk >> 1) * 32 + (kk & 1) * 8; };  // page i, step kk
+    if (v.tokens[0] + v.tokens[1] == kUnitKeys && v.seen[0] == v.all && v.seen[1] == v.all) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int kk = 0; kk < kSteps; ++kk) mma(i, kk, (i | kk) != 0 || !v.first);
+        for (int kk = 0; kk < kSteps; ++kk)
+          tc_mma_pair_tmem_a(d, a_of(i, kk), ahead(v_desc, i * kVPageBytes + kk * 2048), idesc_o, (i | kk) != 0 || begun != 0);
         if (i == 0) k_ready = peek(KFull + (s_cnt & 1), (s_cnt >> 1) & 1);
       }
+      begun = v.all;
     } else {
-      for (int i = 0; i * kPageSize < v.valid; ++i)
-        for (int kk = 0; kk < min(kSteps, (v.valid - i * kPageSize + kKeyStep - 1) / kKeyStep); ++kk)
-          mma(i, kk, (i | kk) != 0 || !v.first);
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t seen = i ? v.seen[1] : v.seen[0];
+        const int steps = ((i ? v.tokens[1] : v.tokens[0]) + kKeyStep - 1) / kKeyStep;
+        uint32_t off[8];
+#pragma unroll
+        for (int w = 0; w < 8; ++w) off[w] = ((seen >> (w >> 1)) & 1) ? 0u : 0xFFFFFFFFu;
+        for (int kk = 0; kk < steps; ++kk)
+          tc_mma_pair_tmem_a_masked(d, a_of(i, kk), ahead(v_desc, i * kVPageBytes + kk * 2048), idesc_o, off,
+                                    kk != 0 || (begun & seen) != 0);
+        if (steps) begun |= seen;
+      }
       k_ready = false;
     }
     tc_commit_pair(cx.bar(PvDone + buf));
@@ -802,24 +848,32 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
   };
   Piece q;
   q.x = lo;
-  Unit pend{0, false, false, 0};  // the unit whose P V is still to be issued (valid = 0: none)
+  Unit pend{};  // the unit whose P V is still to be issued
   bool good = true;
-  while (good && next_piece(p, s, pair, hi, q)) {
+  while (good && next_piece(s, hi, q)) {
     good = kFp8 ? cx.wait_pair(QReady, pieces & 1) : cx.wait(QFull, pieces & 1);
     for (int u = q.u0; good && u < q.u1; ++u) {
-      good = do_s(pend.valid != 0);
-      if (good && pend.valid) good = do_pv(pend);
-      const int valid = keys_in_unit(q, u);
-      pend = Unit{valid, is_tail(q, valid), u == q.u0, pieces};
+      good = do_s(pend.pending);
+      if (good && pend.pending) good = do_pv(pend);
+      pend.pending = true;
+      pend.first = u == q.u0;
+      pend.piece = pieces;
+      pend.all = (1u << q.seqs) - 1;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = 2 * u + i, o = q.owner(k);
+        pend.tokens[i] = q.tokens(k);
+        pend.seen[i] = o == kSeqs ? q.behind : 1u << o;
+      }
     }
     if (kFp8 && good) {  // the softmax warps split the next Q once they have read this O
       pv_ready = false;
       good = do_pv(pend);
-      pend.valid = 0;
+      pend.pending = false;
     }
     ++pieces;
   }
-  if (good && pend.valid) {
+  if (good && pend.pending) {
     pv_ready = false;
     (void)do_pv(pend);
   }
@@ -958,9 +1012,15 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
   auto wait_pv = [&]() -> bool { return cx.wait_warp(PvDone + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1); };
   Piece q;
   q.x = lo;
-  while (next_piece(p, s, pair, hi, q)) {
+  while (next_piece(s, hi, q)) {
     const int j = 2 * (int)cx.rank + (quad >> 1);  // sequence of the row tile
-    const bool mine = j < q.seqs;
+    // the pages that this row sees: those below `prefix`, and own0 .. own1 - 1, of which the last holds `tail` tokens
+    const int prefix = ((q.behind >> j) & 1) ? q.c[0] : 0;
+    const int own0 = j == 0 ? q.c[0] : j == 1 ? q.c[1] : j == 2 ? q.c[2] : q.c[3];
+    const int own1 = j == 0 ? q.c[1] : j == 1 ? q.c[2] : j == 2 ? q.c[3] : q.c[4];
+    const int tail = (int)((q.tails >> (8 * j)) & 0xFF);
+    auto seen = [&](int k) { return k < prefix ? kPageSize : k < own0 || k >= own1 ? 0 : k + 1 < own1 ? kPageSize : tail; };
+    bool fresh = true;              // no key so far
     float m = -INFINITY, l = 0.0f;  // the row's reference (log2 units), and this thread's share of its denominator
     float mul = c2;                 // of the row's products: the softmax scale, and 2^-e of its Q terms
     if constexpr (kFp8) {
@@ -978,8 +1038,8 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       if (kFp8 && !cx.wait_warp(ScFull + sc_slot, (cnt / kScaleSlots) & 1)) return;
       if (!cx.wait_warp(SFull + buf, (cnt >> 1) & 1)) return;
       tc_fence_after();
-      if (mine) {
-        const int valid = keys_in_unit(q, u), cols = min(64, valid - 64 * half);  // this thread's keys (none: <= 0)
+      const int cols = seen(2 * u + half);  // this thread's keys
+      if (cols + seen(2 * u + (half ^ 1)) > 0) {
         // This thread's products, 32 keys at a time. P of 32 keys replaces the first 16 columns of their S.
         float2 x[16];
         const uint32_t tx = ts + 64 * half;
@@ -995,7 +1055,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             }
           }
         };
-        const int e = kFp8 ? unit_exponent(sc + kUnitKeys, valid, lane) : 0;
+        const int e = kFp8 ? page_exponent(sc + kUnitKeys + 64 * half, cols, lane) : 0;
         const float lift = (float)e;
         uint32_t w[32];
         float2 sum;
@@ -1042,7 +1102,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           }
           return top;
         };
-        bool move = u == q.u0;
+        bool move = fresh;
 #pragma unroll 1
         for (int tries = 0; tries < 2; ++tries) {
           if (move) {
@@ -1050,10 +1110,10 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             red[half * 128 + row] = big;
             barrier_rows(quad);
             const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));
-            const float alpha = u == q.u0 || m == m_new ? 1.0f : ex2_approx(m - m_new);
+            const float alpha = fresh || m == m_new ? 1.0f : ex2_approx(m - m_new);
             m = m_new;
             l *= alpha;
-            if (u != q.u0 && __any_sync(0xffffffffu, alpha != 1.0f)) {
+            if (!fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
               // O holds the units before this one; each of the two warps scales half of its columns
               if (!wait_pv()) return;
               tc_fence_after();
@@ -1075,6 +1135,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           move = barrier_rows_or(quad, sum.x + sum.y > kMostSum);
           if (!move) break;
         }
+        fresh = false;
         l += (sum.x + sum.y) * (kFp8 ? exp2_int(-e) : 1.0f);
         tmem_st16(tx, reinterpret_cast<const float*>(w));
         tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
@@ -1090,11 +1151,11 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     // ---- the piece's partial result: O / l and its LSE, 128 dims a thread
     if (!wait_pv()) return;
     tc_fence_after();
-    if (mine) {
+    if (!fresh) {
       red[half * 128 + row] = l;
       barrier_rows(quad);
       l += red[(half ^ 1) * 128 + row];
-      const size_t at = (size_t)(q.row + (q.own ? 0 : j)) * kHeads + (row & 63);
+      const size_t at = ((size_t)(pair + q.t) * kSeqs + j) * kHeads + (row & 63);
       const float inv = 1.0f / l;
       float* dst = p.part_o + at * kHeadDim;
 #pragma unroll 1
@@ -1165,7 +1226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
   cluster_sync();  // the other CTA's barriers are initialised, its scratch is done with
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int units = plan.cost[p.n_groups] + plan.own[p.B], W = busy_pairs(p, units), pair = blockIdx.x >> 1;
+  const int units = plan.cost[plan.tiles], W = busy_pairs(p, units), pair = blockIdx.x >> 1;
   const int lo = pair < W ? (int)cta_cost_lo(pair, units, W) : 0, hi = pair < W ? (int)cta_cost_lo(pair + 1, units, W) : 0;
 
   if (warp < kSoftmaxWarps) {

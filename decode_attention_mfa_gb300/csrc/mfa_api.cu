@@ -397,19 +397,21 @@ mfa_status_t decode_common(const void* q, const void* k_cache, const void* v_cac
 // ------------------------------------------------------------ shared prefix
 // Workspace: [header][partial O][partial LSE][parts].
 struct PrefixPlan {
-  int pairs, own_row0;
+  int pairs;
   size_t part_o, part_lse, parts, total;  // byte offsets
 };
 void fill_prefix_plan(int batch, int n_groups, int max_prefix_hint, int max_suffix_hint, int num_sms, PrefixPlan* w) {
   // one pair of CTAs per two SMs, fewer when the expected lengths are less than kUnitsPerPair units of 128 keys a pair
   constexpr long long kUnitsPerPair = 1;
-  auto units = [](long long tiles, long long tokens) { return tiles * ((tokens + 2 * kPageSize - 1) / (2 * kPageSize)); };
-  const long long work = units((batch + kPrefixTileSeqs - 1) / kPrefixTileSeqs, max_prefix_hint) + units(batch, max_suffix_hint);
+  auto pages = [](long long tokens) { return (tokens + kPageSize - 1) / kPageSize; };
+  const long long work =
+      ((batch + kPrefixTileSeqs - 1) / kPrefixTileSeqs * pages(max_prefix_hint) + batch * pages(max_suffix_hint) + 1) / 2;
   w->pairs = (int)std::max(1ll, std::min((long long)(num_sms / 2), (work + kUnitsPerPair - 1) / kUnitsPerPair));
-  // tiles of prefixes: every shared group has two sequences or more, and leaves at most one tile partly filled
-  const int tiles = std::min(batch / 2, (int)((batch + (kPrefixTileSeqs - 1ll) * n_groups) / kPrefixTileSeqs));
-  w->own_row0 = (w->pairs + tiles) * kPrefixTileSeqs;
-  const size_t rows = (size_t)w->own_row0 + w->pairs + batch;
+  // row tiles: each shared group (of two sequences or more) and each run of sequences before, between and behind them
+  // leaves at most one tile partly filled
+  const long long runs = 2ll * std::min(n_groups, batch / 2) + 1;
+  const int tiles = (int)std::min<long long>(batch, (batch + (kPrefixTileSeqs - 1) * runs) / kPrefixTileSeqs);
+  const size_t rows = (size_t)(w->pairs + tiles - 1) * kPrefixTileSeqs;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   w->part_o = kWsHeaderBytes;
   w->part_lse = w->part_o + rows * kPartialOBytes;
@@ -450,7 +452,6 @@ mfa_status_t prefix_common(const void* q, const void* k_cache, const void* v_cac
   p.v_scale = v_scale;
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-  p.own_row0 = w.own_row0;
   p.parts = reinterpret_cast<int4*>(ws + w.parts);
   p.out = static_cast<uint16_t*>(out);
   p.lse = lse;

@@ -126,9 +126,9 @@ struct DecodeParams {
   uint64_t wait_budget_ns;
 };
 
-// Shared-prefix decode. The work is a line of row tiles: of each group that shares a prefix, kPrefixTileSeqs sequences
-// against the prefix, then each sequence against what it holds behind it (all of it, where nothing is shared). Units of
-// a tile: its keys by 128, plus kPrefixPieceUnits for loading Q and writing the partial result of each piece of it.
+// Shared-prefix decode. The work is a line of row tiles: up to kPrefixTileSeqs neighbouring sequences against their
+// prefix and against the pages of each. Units of a tile: its pages by two, plus kPrefixPieceUnits for loading Q and
+// writing the partial results.
 constexpr int kPrefixTileSeqs = 4;
 constexpr int kPrefixPieceUnits = 2;
 struct PrefixParams {
@@ -138,12 +138,10 @@ struct PrefixParams {
   const int32_t* seq_lens;
   const float* k_scale;         // [num_pages][64] (null: bf16 cache)
   const float* v_scale;
-  // partial results, rows of [64 heads][256] (and [64] LSEs): row 4 (pair + i) + s for sequence s of the i-th tile of a
-  // prefix, then, from row own_row0 on, row pair + b for sequence b's own tokens
+  // partial results, rows of [64 heads][256] (and [64] LSEs): row 4 (pair + t) + s for sequence s of row tile t
   float* part_o;
   float* part_lse;
-  int own_row0;
-  int4* parts;                  // [B]: first row and number of b's partial results over its prefix (kPrefixTileSeqs apart) and of its own
+  int4* parts;                  // [B]: b's partial results, two runs of rows kPrefixTileSeqs apart: first row, number, twice
   uint16_t* out;                // [B][64][256] bf16 bits
   float* lse;                   // [B][64]
   uint32_t* err;

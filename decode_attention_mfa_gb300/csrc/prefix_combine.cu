@@ -1,5 +1,5 @@
 // prefix_combine.cu -- merges a sequence's partial results of the shared-prefix
-// kernel: those over its prefix and those over its own tokens. With O_s and
+// kernel (of the pairs of CTAs that held pages it sees). With O_s and
 // lse_s of part s, M = max_s lse_s and w_s = exp(lse_s - M):
 //     out = sum_s w_s O_s / sum_s w_s,   lse = M + ln sum_s w_s.
 //
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kThreads, 4) prefix_combine_kernel(const Prefi
     return;
   }
   auto part = [&](int i) -> size_t {  // row of part i
-    return i < at.y ? (size_t)at.x + (size_t)i * kPrefixTileSeqs : (size_t)at.z + (i - at.y);
+    return i < at.y ? (size_t)at.x + (size_t)i * kPrefixTileSeqs : (size_t)at.z + (size_t)(i - at.y) * kPrefixTileSeqs;
   };
   auto issue_round = [&](int k) {  // warp 0, one copy a lane
     const int i0 = k * kChunk, cnt = min(kChunk, n - i0);
