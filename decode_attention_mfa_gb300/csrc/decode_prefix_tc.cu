@@ -920,7 +920,24 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-// 32 bytes at once: a whole sector of one row a thread.
+// Four neighbouring lanes, each with 32 values of its row, exchange them so that lane j has values 8 j .. 8 j + 7 of all
+// four rows (row k's at v[8 k]): a store then writes whole 128 B lines instead of 32 B of as many rows as lanes (a tile's
+// result took 4 us that way).
+__device__ __forceinline__ void transpose_quad(float (&v)[32], int lane) {
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float other = __shfl_xor_sync(0xffffffffu, (lane & 2) ? v[i] : v[16 + i], 2);
+    if (lane & 2) v[i] = other; else v[16 + i] = other;
+  }
+#pragma unroll
+  for (int h = 0; h < 32; h += 16)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[h + i] : v[h + 8 + i], 1);
+      if (lane & 1) v[h + i] = other; else v[h + 8 + i] = other;
+    }
+}
+// 32 bytes at once.
 __device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
@@ -1157,7 +1174,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       l += red[(half ^ 1) * 128 + row];
       const size_t at = ((size_t)(pair + q.t) * kSeqs + j) * kHeads + (row & 63);
       const float inv = 1.0f / l;
-      float* dst = p.part_o + at * kHeadDim;
+      float* dst = p.part_o + (at - (lane & 3)) * kHeadDim + 8 * (lane & 3);
 #pragma unroll 1
       for (int c = 128 * half; c < 128 * half + 128; c += 32) {
         float o[32];
@@ -1165,8 +1182,9 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
         tc_wait_ld();
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] *= inv;
+        transpose_quad(o, lane);
 #pragma unroll
-        for (int k = 0; k < 32; k += 8) st_global_v8(dst + c + k, o + k);
+        for (int k = 0; k < 4; ++k) st_global_v8(dst + k * kHeadDim + c, o + 8 * k);
       }
       if (half == 0) p.part_lse[at] = (m + log2f(l)) * kLn2;
       barrier_rows(quad);  // red is free again
@@ -1218,6 +1236,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     tc_fence_before();
+  }
+  if (threadIdx.x == 0) {  // hints only: both may still be written
+    prefetch_l2_share(p.page_table, (size_t)p.B * p.max_pages * sizeof(int32_t), blockIdx.x, gridDim.x);
+    prefetch_l2_share(p.q, (size_t)p.B * kHeads * kHeadDim * sizeof(uint16_t), blockIdx.x, gridDim.x);
   }
   pdl_wait_prior_grid();
   pdl_launch_dependents();

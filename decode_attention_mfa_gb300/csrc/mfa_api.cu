@@ -444,6 +444,7 @@ mfa_status_t prefix_common(const void* q, const void* k_cache, const void* v_cac
     return fail(MFA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, w.total);
   char* ws = static_cast<char*>(workspace);
   PrefixParams p{};
+  p.q = static_cast<const uint16_t*>(q);
   p.group_starts = group_starts;
   p.prefix_pages = prefix_pages;
   p.page_table = page_table;

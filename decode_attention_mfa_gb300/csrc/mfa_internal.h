@@ -132,6 +132,7 @@ struct DecodeParams {
 constexpr int kPrefixTileSeqs = 4;
 constexpr int kPrefixPieceUnits = 2;
 struct PrefixParams {
+  const uint16_t* q;            // [B][64][256] bf16 bits
   const int32_t* group_starts;  // [n_groups + 1]
   const int32_t* prefix_pages;  // [n_groups]
   const int32_t* page_table;
