@@ -12,6 +12,8 @@ import os
 import re
 import threading
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmfa.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "mfa.h")
@@ -86,6 +88,8 @@ def header_functions() -> list[str]:
 def load():
     """Load libmfa.so (built by decode_attention_mfa_gb300.build); raises if absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -111,8 +115,8 @@ def _ptr(x):
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the handle of torch.cuda.current_stream(), without the Stream object (3 us of a call that takes the GPU as long)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream

@@ -130,7 +130,7 @@ struct DecodeParams {
 // prefix and against the pages of each. Units of a tile: its pages by two, plus kPrefixPieceUnits for loading Q and
 // writing the partial results.
 constexpr int kPrefixTileSeqs = 4;
-constexpr int kPrefixPieceUnits = 2;
+constexpr int kPrefixPieceUnits = 6;
 struct PrefixParams {
   const uint16_t* q;            // [B][64][256] bf16 bits
   const int32_t* group_starts;  // [n_groups + 1]
