@@ -91,6 +91,11 @@ __device__ __forceinline__ bool last_block(uint32_t* counter) {
   return s_last;
 }
 
+// Pages of len + more tokens.
+__device__ __forceinline__ int pages_held(int len, int more) {
+  return (int)(((long long)len + more + kPageSize - 1) / kPageSize);
+}
+
 __device__ __forceinline__ int checked_count(int n, int most, uint32_t* err) {
   if (n >= 0 && n <= most) return n;
   raise_error(err, MFA_DEVERR_CAPACITY);
@@ -100,7 +105,7 @@ __device__ __forceinline__ int checked_count(int n, int most, uint32_t* err) {
 __global__ void __launch_bounds__(kTableThreads) reserve_pages_kernel(const PageTableParams p) {
   __shared__ Pair s_warp[kTableWarps];
   __shared__ int s_upto[kMaxBatch];  // tokens up to and including request b
-  __shared__ int s_page[kMaxBatch];  // pages up to and including request b (served ones only)
+  __shared__ int s_page[kMaxBatch];  // pages up to and including request b
   __shared__ int s_len[kMaxBatch];
   __shared__ int s_take[kMaxBatch];  // pages taken before request b, -1: not served
   __shared__ int s_taken;
@@ -109,40 +114,34 @@ __global__ void __launch_bounds__(kTableThreads) reserve_pages_kernel(const Page
   const bool first = blockIdx.x == 0;  // device faults are reported once
   uint32_t* err = first ? p.err : nullptr;
   const long long cap = (long long)p.max_pages * kPageSize;
-  const int n_free = checked_count(__ldcg(p.n_free), p.num_pages, err);
+  const int free_raw = __ldcg(p.n_free);
+  for (int b = threadIdx.x; b < p.B; b += kTableThreads) {
+    s_take[b] = __ldcg(p.n_new + b);
+    s_len[b] = __ldcg(p.seq_lens + b);
+  }
   if (threadIdx.x == 0) s_taken = 0;
-  // tokens first (which requests fit the step's rows depends on their sum), then pages
+  const int n_free = checked_count(free_raw, p.num_pages, err);
+  // One pass for tokens and pages: which requests fit the step's rows depends on the tokens before them, but those that
+  // do not are the last ones, and no request's pages depend on a later one.
   block_scan(
       p.B, s_warp,
       [&](int b) {
-        const int n = __ldcg(p.n_new + b);
-        if (n < 0) raise_error(err, MFA_DEVERR_CAPACITY);
-        return Pair{n < 0 ? 0 : n, 0};
+        const int n = s_take[b], len = s_len[b];
+        const bool good = n >= 0 && len >= 0 && (long long)len + n <= cap;
+        if (!good) raise_error(err, MFA_DEVERR_CAPACITY);
+        return Pair{n < 0 ? 0 : n, good ? pages_held(len, n) - pages_held(len, 0) : 0};
       },
       [&](int b, Pair before, Pair own) {
-        const int len = __ldcg(p.seq_lens + b), n = __ldcg(p.n_new + b);
-        const long long end = before.a + own.a;
-        const bool fits = n >= 0 && len >= 0 && (long long)len + n <= cap && end <= p.max_new;
-        if (!fits) raise_error(err, MFA_DEVERR_CAPACITY);
+        const int n = s_take[b], len = s_len[b];
+        const long long end = before.a + own.a, pages = before.b + own.b;
+        const bool good = n >= 0 && len >= 0 && (long long)len + n <= cap, fits = end <= p.max_new;
+        if (good && !fits) raise_error(err, MFA_DEVERR_CAPACITY);
+        const bool served = good && fits && (own.b == 0 || pages <= n_free);
+        if (good && fits && !served) raise_error(err, MFA_DEVERR_NO_PAGES);
         s_upto[b] = (int)min(end, 0x7fffffffLL);
-        s_len[b] = len;
-        s_take[b] = fits ? 0 : -1;
-      });
-  __syncthreads();
-  auto pages_needed = [&](int b) -> int {
-    if (s_take[b] < 0) return 0;
-    const int n = s_upto[b] - (b ? s_upto[b - 1] : 0);
-    return (int)(((long long)s_len[b] + n + kPageSize - 1) / kPageSize - ((long long)s_len[b] + kPageSize - 1) / kPageSize);
-  };
-  block_scan(
-      p.B, s_warp, [&](int b) { return Pair{pages_needed(b), 0}; },
-      [&](int b, Pair before, Pair own) {
-        const long long upto = before.a + own.a;
-        const bool served = s_take[b] >= 0 && (own.a == 0 || upto <= n_free);
-        if (s_take[b] >= 0 && !served) raise_error(err, MFA_DEVERR_NO_PAGES);
-        s_page[b] = (int)min(upto, (long long)n_free);  // past the stack's end the last served request's sum is not needed
-        s_take[b] = served ? (int)min(before.a, (long long)n_free) : -1;
-        if (served && own.a > 0) atomicMax(&s_taken, (int)upto);
+        s_page[b] = (int)min(pages, (long long)n_free);  // behind the last served request only its order matters
+        s_take[b] = served ? (int)min(before.b, (long long)n_free) : -1;
+        if (served && own.b > 0) atomicMax(&s_taken, (int)pages);
       });
   __syncthreads();
   const int taken = s_taken;
@@ -150,27 +149,39 @@ __global__ void __launch_bounds__(kTableThreads) reserve_pages_kernel(const Page
   // the new entries of the page tables
   for (uint32_t u = t0; u < (uint32_t)taken; u += step) {
     const int i = (int)u, b = first_above(s_page, p.B, i);
-    const int held = (int)(((long long)s_len[b] + kPageSize - 1) / kPageSize);
+    const int held = pages_held(s_len[b], 0);
     const int page = __ldcg(p.free_pages + (n_free - 1 - i));
     if (page < 0 || page >= p.num_pages) raise_error(p.err, MFA_DEVERR_PAGE);
     p.page_table[(size_t)b * p.max_pages + held + (i - s_take[b])] = page;
   }
-  // the slots of the tokens; -1 for tokens that are not served and past the last one
-  for (uint32_t u = t0; u < (uint32_t)p.max_new; u += step) {
-    const int i = (int)u, b = first_above(s_upto, p.B, i);
-    long long slot = -1;
-    if (b < p.B && s_take[b] >= 0) {
-      const int pos = s_len[b] + i - (b ? s_upto[b - 1] : 0);
-      const int held = (int)(((long long)s_len[b] + kPageSize - 1) / kPageSize), pg = pos / kPageSize;
-      // a page held before the call stands in the table, a new one is read where the table's entry comes from
-      const int page = pg < held ? __ldcg(p.page_table + (size_t)b * p.max_pages + pg)
-                                 : __ldcg(p.free_pages + (n_free - 1 - (s_take[b] + pg - held)));
-      if (page >= 0 && page < p.num_pages)
-        slot = (long long)page * kPageSize + pos % kPageSize;
-      else
-        raise_error(p.err, MFA_DEVERR_PAGE);
+  // the slots of the tokens; -1 for tokens that are not served and past the last one. kAtOnce tokens a thread: their
+  // searches and page loads overlap.
+  constexpr int kAtOnce = 4;
+  for (uint32_t u0 = t0; u0 < (uint32_t)p.max_new; u0 += kAtOnce * step) {
+    int page[kAtOnce], row[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t u = u0 + k * step;
+      const int i = (int)u, b = u < (uint32_t)p.max_new ? first_above(s_upto, p.B, i) : p.B;
+      row[k] = -1;
+      page[k] = 0;
+      if (b < p.B && s_take[b] >= 0) {
+        const int pos = s_len[b] + i - (b ? s_upto[b - 1] : 0);
+        const int held = pages_held(s_len[b], 0), pg = pos / kPageSize;
+        row[k] = pos % kPageSize;
+        // a page held before the call stands in the table, a new one is read where the table's entry comes from
+        page[k] = pg < held ? __ldcg(p.page_table + (size_t)b * p.max_pages + pg)
+                            : __ldcg(p.free_pages + (n_free - 1 - (s_take[b] + pg - held)));
+      }
     }
-    p.slot_map[i] = slot;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const uint32_t u = u0 + k * step;
+      if (u >= (uint32_t)p.max_new) break;
+      const bool good = page[k] >= 0 && page[k] < p.num_pages;
+      if (!good) raise_error(p.err, MFA_DEVERR_PAGE);
+      p.slot_map[u] = row[k] >= 0 && good ? (long long)page[k] * kPageSize + row[k] : -1;
+    }
   }
   if (first)
     for (int b = threadIdx.x; b <= p.B; b += kTableThreads) p.new_starts[b] = b ? s_upto[b - 1] : 0;
@@ -192,24 +203,28 @@ __global__ void __launch_bounds__(kTableThreads) release_pages_kernel(const Page
   const bool first = blockIdx.x == 0;
   uint32_t* err = first ? p.err : nullptr;
   const long long cap = (long long)p.max_pages * kPageSize;
-  const int n_free = checked_count(__ldcg(p.n_free), p.num_pages, err);
+  const int free_raw = __ldcg(p.n_free);
+  for (int b = threadIdx.x; b < p.B; b += kTableThreads) {
+    s_len[b] = __ldcg(p.seq_lens + b);
+    s_kept[b] = __ldcg(p.finished + b);
+    s_upto[b] = p.keep_pages ? __ldcg(p.keep_pages + b) : 0;
+  }
   if (threadIdx.x == 0) s_total = 0;
+  const int n_free = checked_count(free_raw, p.num_pages, err);
   block_scan(
       p.B, s_warp,
       [&](int b) {
-        const int len = __ldcg(p.seq_lens + b);
+        const int len = s_len[b], keep = s_upto[b];
         int kept = -1, count = 0;
-        if (__ldcg(p.finished + b) != 0) {
-          const int keep = p.keep_pages ? __ldcg(p.keep_pages + b) : 0;
+        if (s_kept[b] != 0) {
           if (len < 0 || len > cap || keep < 0) {
             raise_error(err, MFA_DEVERR_CAPACITY);
           } else {
-            const int held = (int)(((long long)len + kPageSize - 1) / kPageSize);
+            const int held = pages_held(len, 0);
             kept = min(keep, held);
             count = held - kept;
           }
         }
-        s_len[b] = len;
         s_kept[b] = kept;
         return Pair{count, 0};
       },
@@ -237,10 +252,10 @@ __global__ void __launch_bounds__(kTableThreads) release_pages_kernel(const Page
   }
 }
 
-// One CTA per 2048 tokens or table entries, at most about one per SM: fewer
-// items a CTA would repeat the sums over the requests for too little work.
+// One CTA per 2048 tokens or table entries, four a thread, at most one per SM:
+// fewer items a CTA would repeat the sums over the requests for too little work.
 int table_grid(long long items) {
-  constexpr long long kItemsPerCta = 2048, kMostCtas = 152;
+  constexpr long long kItemsPerCta = 4 * kTableThreads, kMostCtas = 152;
   const long long g = (items + kItemsPerCta - 1) / kItemsPerCta;
   return (int)(g < 1 ? 1 : g > kMostCtas ? kMostCtas : g);
 }

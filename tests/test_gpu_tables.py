@@ -347,3 +347,29 @@ def test_serving_loop_captured_and_replayed():
         stream.synchronize()
     assert lens.tolist() == [0] * B and int(n_free.item()) == num_pages
     assert sorted(free.tolist()) == sorted(pages0.tolist())
+
+
+def test_append_slots_fp8_codes_of_all_kinds_of_rows():
+    """Codes and scales are those of mfa_kv_append_fp8, bit for bit, over 40,000 random rows (more than the sizes at which
+    a warp takes one row) and rows of every scale, with signed zeros, subnormals, infinities and NaN among their values."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    rows, pages = 40960, 640
+    k = torch.randn((rows, 256), generator=gen, device="cuda") * torch.exp2(torch.randint(-20, 20, (rows, 1), generator=gen, device="cuda"))
+    v = torch.randn((rows, 256), generator=gen, device="cuda") * torch.rand((rows, 256), generator=gen, device="cuda") ** 8
+    k, v = k.bfloat16(), v.bfloat16()
+    exps = torch.arange(-132, 128, device="cuda").double()  # 260 rows, one of each scale that bf16 has
+    v[:260] = (torch.randn((260, 256), generator=gen, device="cuda").double().clamp(-1, 1) * torch.exp2(exps).unsqueeze(1)).bfloat16()
+    v[300:310, ::3] = -0.0
+    v[310], v[311] = 0.0, -0.0
+    v[312, 5], v[313, 7], v[314, 9] = float("inf"), float("-inf"), float("nan")
+    v[315] = float("nan")
+    a = [torch.zeros((pages, PAGE, 256), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    s = [torch.zeros((pages, PAGE), device="cuda") for _ in range(4)]
+    ws = workspace()
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    table = torch.arange(pages, device="cuda").int().view(1, -1)
+    capi.mfa_kv_append_fp8(k, v, rows, a[0], a[1], s[0], s[1], table, lens, 1, pages, pages, ws)
+    capi.mfa_kv_append_slots_fp8(k, v, 256, 256, torch.arange(rows, device="cuda"), rows, a[2], a[3], s[2], s[3], pages, ws)
+    for i in range(2):
+        assert torch.equal(s[i].view(torch.int32), s[i + 2].view(torch.int32))
+        assert torch.equal(a[i], a[i + 2])
