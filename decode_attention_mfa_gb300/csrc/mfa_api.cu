@@ -686,6 +686,7 @@ PageTableParams make_page_table_params(const int32_t* seq_lens, int32_t* page_ta
   p.n_free = n_free;
   p.seq_lens_out = seq_lens_out;
   p.n_free_out = n_free_out;
+  p.in_place = seq_lens_out == seq_lens || n_free_out == n_free;
   p.err = static_cast<uint32_t*>(workspace);
   p.counter = reinterpret_cast<uint32_t*>(static_cast<char*>(workspace) + kTableCounterOffset);
   p.B = batch;

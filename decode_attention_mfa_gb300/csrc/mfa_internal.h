@@ -90,6 +90,7 @@ struct PageTableParams {
   uint32_t* err;
   uint32_t* counter;
   int B, max_pages, num_pages, max_new;
+  bool in_place;              // an output replaces an input: written when every CTA has read
 };
 
 struct DecodeParams {

@@ -21,50 +21,40 @@
 namespace mfa {
 namespace {
 
-constexpr int kTableThreads = 512;
+constexpr int kTableThreads = 1024;  // a thread a request
 constexpr int kTableWarps = kTableThreads / 32;
+static_assert(kTableThreads >= kMaxBatch && kTableWarps == 32, "the sums take one round, and one warp the warps' sums");
 
 struct Pair {
-  long long a, b;
+  uint32_t a, b;
 };
+// Sums that stop at 2^31 - 1 instead of wrapping: the counts are the caller's. Where a sum matters it is exact, because
+// it is compared with a bound below that first.
+__device__ __forceinline__ uint32_t add_sat(uint32_t x, uint32_t y) { return min(x + y, 0x7fffffffu); }
 
-// Exclusive prefix sums of two values per request, in request order, by the
-// whole block: f(b) gives the values of request b, g(b, before, own) receives
-// the sums before it. Returns the totals. Sums are 64-bit: the lengths are the
-// caller's and 1024 of them may pass 32 bits.
-template <typename F, typename G>
-__device__ __forceinline__ Pair block_scan(int B, Pair* s_warp, F f, G g) {
+// Sums up to and including this thread's values, and before them, in thread order, by the whole block.
+struct Sums {
+  Pair before, upto;
+};
+__device__ __forceinline__ Sums block_scan(Pair own, Pair* s_warp) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  Pair base{0, 0};
-  for (int b0 = 0; b0 < B; b0 += kTableThreads) {
-    const int b = b0 + (int)threadIdx.x;
-    Pair own{0, 0};
-    if (b < B) own = f(b);
-    Pair x = own;
+  auto scan = [lane](Pair x) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long ya = __shfl_up_sync(0xffffffffu, x.a, o), yb = __shfl_up_sync(0xffffffffu, x.b, o);
-      if (lane >= o) {
-        x.a += ya;
-        x.b += yb;
-      }
+      const uint32_t ya = __shfl_up_sync(0xffffffffu, x.a, o), yb = __shfl_up_sync(0xffffffffu, x.b, o);
+      if (lane >= o) x = Pair{add_sat(x.a, ya), add_sat(x.b, yb)};
     }
-    __syncthreads();  // the previous round's warp sums have been read
-    if (lane == 31) s_warp[warp] = x;
-    __syncthreads();
-    Pair before = base;
-    for (int w = 0; w < kTableWarps; ++w) {
-      const Pair y = s_warp[w];
-      if (w < warp) {
-        before.a += y.a;
-        before.b += y.b;
-      }
-      base.a += y.a;
-      base.b += y.b;
-    }
-    if (b < B) g(b, Pair{before.a + x.a - own.a, before.b + x.b - own.b}, own);
-  }
-  return base;
+    return x;
+  };
+  Pair x = scan(own);
+  if (lane == 31) s_warp[warp] = x;
+  __syncthreads();
+  const Pair warps = scan(s_warp[lane]);  // every warp for itself
+  Pair base{__shfl_sync(0xffffffffu, warps.a, max(warp - 1, 0)), __shfl_sync(0xffffffffu, warps.b, max(warp - 1, 0))};
+  if (warp == 0) base = Pair{0, 0};
+  Pair prev{__shfl_up_sync(0xffffffffu, x.a, 1), __shfl_up_sync(0xffffffffu, x.b, 1)};
+  if (lane == 0) prev = Pair{0, 0};
+  return Sums{{add_sat(base.a, prev.a), add_sat(base.b, prev.b)}, {add_sat(base.a, x.a), add_sat(base.b, x.b)}};
 }
 
 // First b with upto[b] > i (upto is non-decreasing); B if there is none.
@@ -82,10 +72,11 @@ __device__ __forceinline__ int first_above(const int* upto, int B, int i) {
 // counter wraps to zero for the next call.
 __device__ __forceinline__ bool last_block(uint32_t* counter) {
   __shared__ int s_last;
+  if (gridDim.x == 1) return true;  // (its threads have met since they read)
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    s_last = gridDim.x == 1 || atomicInc(counter, gridDim.x - 1) == gridDim.x - 1;
+    s_last = atomicInc(counter, gridDim.x - 1) == gridDim.x - 1;
   }
   __syncthreads();
   return s_last;
@@ -113,36 +104,28 @@ __global__ void __launch_bounds__(kTableThreads) reserve_pages_kernel(const Page
   pdl_wait_prior_grid();
   const bool first = blockIdx.x == 0;  // device faults are reported once
   uint32_t* err = first ? p.err : nullptr;
-  const long long cap = (long long)p.max_pages * kPageSize;
+  const int b = threadIdx.x;  // this thread's request
   const int free_raw = __ldcg(p.n_free);
-  for (int b = threadIdx.x; b < p.B; b += kTableThreads) {
-    s_take[b] = __ldcg(p.n_new + b);
-    s_len[b] = __ldcg(p.seq_lens + b);
-  }
-  if (threadIdx.x == 0) s_taken = 0;
+  const int n = b < p.B ? __ldcg(p.n_new + b) : 0, len = b < p.B ? __ldcg(p.seq_lens + b) : 0;
+  if (b == 0) s_taken = 0;
   const int n_free = checked_count(free_raw, p.num_pages, err);
-  // One pass for tokens and pages: which requests fit the step's rows depends on the tokens before them, but those that
-  // do not are the last ones, and no request's pages depend on a later one.
-  block_scan(
-      p.B, s_warp,
-      [&](int b) {
-        const int n = s_take[b], len = s_len[b];
-        const bool good = n >= 0 && len >= 0 && (long long)len + n <= cap;
-        if (!good) raise_error(err, MFA_DEVERR_CAPACITY);
-        return Pair{n < 0 ? 0 : n, good ? pages_held(len, n) - pages_held(len, 0) : 0};
-      },
-      [&](int b, Pair before, Pair own) {
-        const int n = s_take[b], len = s_len[b];
-        const long long end = before.a + own.a, pages = before.b + own.b;
-        const bool good = n >= 0 && len >= 0 && (long long)len + n <= cap, fits = end <= p.max_new;
-        if (good && !fits) raise_error(err, MFA_DEVERR_CAPACITY);
-        const bool served = good && fits && (own.b == 0 || pages <= n_free);
-        if (good && fits && !served) raise_error(err, MFA_DEVERR_NO_PAGES);
-        s_upto[b] = (int)min(end, 0x7fffffffLL);
-        s_page[b] = (int)min(pages, (long long)n_free);  // behind the last served request only its order matters
-        s_take[b] = served ? (int)min(before.b, (long long)n_free) : -1;
-        if (served && own.b > 0) atomicMax(&s_taken, (int)pages);
-      });
+  // One pass of sums for tokens and pages: which requests fit the step's rows depends on the tokens before them, but those
+  // that do not are the last ones, and no request's pages depend on a later one.
+  const bool good = n >= 0 && len >= 0 && (long long)len + n <= (long long)p.max_pages * kPageSize;
+  const uint32_t need = good ? (uint32_t)(pages_held(len, n) - pages_held(len, 0)) : 0u;
+  const Sums sums = block_scan(Pair{(uint32_t)max(n, 0), need}, s_warp);
+  const bool fits = sums.upto.a <= (uint32_t)p.max_new;
+  const bool served = good && fits && (need == 0 || sums.upto.b <= (uint32_t)n_free);
+  const uint32_t most = __reduce_max_sync(0xffffffffu, b < p.B && served && need > 0 ? sums.upto.b : 0u);
+  if ((b & 31) == 0) atomicMax(&s_taken, (int)most);
+  if (b < p.B) {
+    if (!good || !fits) raise_error(err, MFA_DEVERR_CAPACITY);
+    if (good && fits && !served) raise_error(err, MFA_DEVERR_NO_PAGES);
+    s_len[b] = len;
+    s_upto[b] = (int)sums.upto.a;
+    s_page[b] = (int)min(sums.upto.b, (uint32_t)n_free);  // behind the last served request only its order matters
+    s_take[b] = served ? (int)min(sums.before.b, (uint32_t)n_free) : -1;
+  }
   __syncthreads();
   const int taken = s_taken;
   const uint32_t t0 = blockIdx.x * kTableThreads + threadIdx.x, step = gridDim.x * kTableThreads;  // sums stay below 2^32
@@ -154,41 +137,28 @@ __global__ void __launch_bounds__(kTableThreads) reserve_pages_kernel(const Page
     if (page < 0 || page >= p.num_pages) raise_error(p.err, MFA_DEVERR_PAGE);
     p.page_table[(size_t)b * p.max_pages + held + (i - s_take[b])] = page;
   }
-  // the slots of the tokens; -1 for tokens that are not served and past the last one. kAtOnce tokens a thread: their
-  // searches and page loads overlap.
-  constexpr int kAtOnce = 4;
-  for (uint32_t u0 = t0; u0 < (uint32_t)p.max_new; u0 += kAtOnce * step) {
-    int page[kAtOnce], row[kAtOnce];
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const uint32_t u = u0 + k * step;
-      const int i = (int)u, b = u < (uint32_t)p.max_new ? first_above(s_upto, p.B, i) : p.B;
-      row[k] = -1;
-      page[k] = 0;
-      if (b < p.B && s_take[b] >= 0) {
-        const int pos = s_len[b] + i - (b ? s_upto[b - 1] : 0);
-        const int held = pages_held(s_len[b], 0), pg = pos / kPageSize;
-        row[k] = pos % kPageSize;
-        // a page held before the call stands in the table, a new one is read where the table's entry comes from
-        page[k] = pg < held ? __ldcg(p.page_table + (size_t)b * p.max_pages + pg)
-                            : __ldcg(p.free_pages + (n_free - 1 - (s_take[b] + pg - held)));
-      }
+  // the slots of the tokens; -1 for tokens that are not served and past the last one
+  for (uint32_t u = t0; u < (uint32_t)p.max_new; u += step) {
+    const int i = (int)u, b = first_above(s_upto, p.B, i);
+    long long slot = -1;
+    if (b < p.B && s_take[b] >= 0) {
+      const int pos = s_len[b] + i - (b ? s_upto[b - 1] : 0);
+      const int held = pages_held(s_len[b], 0), pg = pos / kPageSize;
+      // a page held before the call stands in the table, a new one is read where the table's entry comes from
+      const int page = pg < held ? __ldcg(p.page_table + (size_t)b * p.max_pages + pg)
+                                 : __ldcg(p.free_pages + (n_free - 1 - (s_take[b] + pg - held)));
+      if (page >= 0 && page < p.num_pages)
+        slot = (long long)page * kPageSize + pos % kPageSize;
+      else
+        raise_error(p.err, MFA_DEVERR_PAGE);
     }
-#pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      const uint32_t u = u0 + k * step;
-      if (u >= (uint32_t)p.max_new) break;
-      const bool good = page[k] >= 0 && page[k] < p.num_pages;
-      if (!good) raise_error(p.err, MFA_DEVERR_PAGE);
-      p.slot_map[u] = row[k] >= 0 && good ? (long long)page[k] * kPageSize + row[k] : -1;
-    }
+    p.slot_map[u] = slot;
   }
-  if (first)
-    for (int b = threadIdx.x; b <= p.B; b += kTableThreads) p.new_starts[b] = b ? s_upto[b - 1] : 0;
-  if (last_block(p.counter)) {
-    for (int b = threadIdx.x; b < p.B; b += kTableThreads)
-      p.seq_lens_out[b] = s_take[b] >= 0 ? s_len[b] + s_upto[b] - (b ? s_upto[b - 1] : 0) : s_len[b];
-    if (threadIdx.x == 0) *p.n_free_out = n_free - taken;
+  if (first && b < p.B) p.new_starts[b + 1] = s_upto[b];
+  if (first && b == 0) p.new_starts[0] = 0;
+  if (p.in_place ? last_block(p.counter) : first) {
+    if (b < p.B) p.seq_lens_out[b] = s_take[b] >= 0 ? len + n : len;
+    if (b == 0) *p.n_free_out = n_free - taken;
   }
 }
 
@@ -196,47 +166,36 @@ __global__ void __launch_bounds__(kTableThreads) release_pages_kernel(const Page
   __shared__ Pair s_warp[kTableWarps];
   __shared__ int s_upto[kMaxBatch];  // pages given back up to and including request b
   __shared__ int s_kept[kMaxBatch];  // pages request b keeps at the start of its row, -1: it is left as it is
-  __shared__ int s_len[kMaxBatch];
   __shared__ int s_total;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   const bool first = blockIdx.x == 0;
   uint32_t* err = first ? p.err : nullptr;
   const long long cap = (long long)p.max_pages * kPageSize;
+  const int b = threadIdx.x;  // this thread's request
   const int free_raw = __ldcg(p.n_free);
-  for (int b = threadIdx.x; b < p.B; b += kTableThreads) {
-    s_len[b] = __ldcg(p.seq_lens + b);
-    s_kept[b] = __ldcg(p.finished + b);
-    s_upto[b] = p.keep_pages ? __ldcg(p.keep_pages + b) : 0;
-  }
-  if (threadIdx.x == 0) s_total = 0;
+  const int len = b < p.B ? __ldcg(p.seq_lens + b) : 0;
+  const bool ended = b < p.B && __ldcg(p.finished + b) != 0;
+  const int keep = ended && p.keep_pages ? __ldcg(p.keep_pages + b) : 0;
+  if (b == 0) s_total = 0;
   const int n_free = checked_count(free_raw, p.num_pages, err);
-  block_scan(
-      p.B, s_warp,
-      [&](int b) {
-        const int len = s_len[b], keep = s_upto[b];
-        int kept = -1, count = 0;
-        if (s_kept[b] != 0) {
-          if (len < 0 || len > cap || keep < 0) {
-            raise_error(err, MFA_DEVERR_CAPACITY);
-          } else {
-            const int held = pages_held(len, 0);
-            kept = min(keep, held);
-            count = held - kept;
-          }
-        }
-        s_kept[b] = kept;
-        return Pair{count, 0};
-      },
-      [&](int b, Pair before, Pair own) {
-        const long long upto = before.a + own.a, room = p.num_pages - n_free;
-        if (own.a > 0 && upto > room) {
-          raise_error(err, MFA_DEVERR_CAPACITY);
-          s_kept[b] = -1;
-        }
-        s_upto[b] = (int)min(upto, room);
-        if (own.a > 0 && upto <= room) atomicMax(&s_total, (int)upto);
-      });
+  const bool good = ended && len >= 0 && len <= cap && keep >= 0;
+  if (ended && !good) raise_error(err, MFA_DEVERR_CAPACITY);
+  const int held = good ? pages_held(len, 0) : 0;
+  int kept = good ? min(keep, held) : -1;
+  const uint32_t count = good ? (uint32_t)(held - kept) : 0u, room = (uint32_t)(p.num_pages - n_free);
+  const Sums sums = block_scan(Pair{count, 0u}, s_warp);
+  const bool fits = count == 0 || sums.upto.a <= room;
+  const uint32_t most = __reduce_max_sync(0xffffffffu, fits && count > 0 ? sums.upto.a : 0u);
+  if ((b & 31) == 0) atomicMax(&s_total, (int)most);
+  if (b < p.B) {
+    if (!fits) {
+      raise_error(err, MFA_DEVERR_CAPACITY);
+      kept = -1;
+    }
+    s_kept[b] = kept;
+    s_upto[b] = (int)min(sums.upto.a, room);
+  }
   __syncthreads();
   const int total = s_total;
   for (uint32_t u = blockIdx.x * kTableThreads + threadIdx.x; u < (uint32_t)total; u += gridDim.x * kTableThreads) {
@@ -245,17 +204,16 @@ __global__ void __launch_bounds__(kTableThreads) release_pages_kernel(const Page
     if (page < 0 || page >= p.num_pages) raise_error(p.err, MFA_DEVERR_PAGE);
     p.free_pages[n_free + i] = page;
   }
-  if (last_block(p.counter)) {
-    for (int b = threadIdx.x; b < p.B; b += kTableThreads)
-      p.seq_lens_out[b] = s_kept[b] >= 0 ? (int)min((long long)s_len[b], (long long)s_kept[b] * kPageSize) : s_len[b];
-    if (threadIdx.x == 0) *p.n_free_out = n_free + total;
+  if (p.in_place ? last_block(p.counter) : first) {
+    if (b < p.B) p.seq_lens_out[b] = kept >= 0 ? (int)min((long long)len, (long long)kept * kPageSize) : len;
+    if (b == 0) *p.n_free_out = n_free + total;
   }
 }
 
-// One CTA per 2048 tokens or table entries, four a thread, at most one per SM:
-// fewer items a CTA would repeat the sums over the requests for too little work.
+// A thread a token or table entry, up to one CTA per SM (beyond that every CTA would repeat the sums over the requests
+// only to wait for an SM).
 int table_grid(long long items) {
-  constexpr long long kItemsPerCta = 4 * kTableThreads, kMostCtas = 152;
+  constexpr long long kItemsPerCta = kTableThreads, kMostCtas = 152;
   const long long g = (items + kItemsPerCta - 1) / kItemsPerCta;
   return (int)(g < 1 ? 1 : g > kMostCtas ? kMostCtas : g);
 }
