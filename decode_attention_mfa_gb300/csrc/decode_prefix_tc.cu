@@ -405,10 +405,10 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, u
 __device__ __forceinline__ int busy_pairs(const PrefixParams& p, int units) { return min(p.pairs, max(units, 1)); }
 
 // Where the combine finds each sequence's partial results: of the pairs that hold prefix units, and of those that hold
-// pages of its own.
-__device__ void publish_plan(const PrefixParams& p, const PlanSmem& s) {
+// pages of its own. One warp of each pair.
+__device__ void publish_plan(const PrefixParams& p, const PlanSmem& s, int pair, int lane) {
   const int C = s.cost[s.tiles], W = busy_pairs(p, C);
-  for (int b = blockIdx.x * blockDim.x + threadIdx.x; b < p.B; b += gridDim.x * blockDim.x) {
+  for (int b = 32 * pair + lane; b < p.B; b += 32 * p.pairs) {
     const int t = last_at_most(s.first, s.tiles, b), j = b - s.first[t], prefix = s.pages[t];
     int c = prefix;
     for (int i = s.first[t]; i < b; ++i) c += pages_of(own_tokens(s, i, prefix));
@@ -587,8 +587,6 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
   bool vtail = false, good = true;
   uint64_t vpol = pol_own;
   while (good && next_piece(s, hi, q)) {
-    TilePages ids;
-    ids.start(2 * q.u0, p, s, q, lane);
     // Q may be replaced once S of every unit so far is done
     good = cnt == 0 || cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1);
     if (!good) break;
@@ -604,6 +602,8 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
           tma_load_2d_pair(cx.base + Sm::q + d * 16384 + h * 8192, qmap, d * 64, (q.b + 2 * r + h) * kHeads, bar, pol_shared);
     }
     ++pieces;
+    TilePages ids;
+    ids.start(2 * q.u0, p, s, q, lane);
     for (int u = q.u0; good && u < q.u1; ++u) {
       const int pa = ids.get(2 * u, p, s, q, lane);
       const int pb = 2 * u + 1 < q.c[kSeqs] ? ids.get(2 * u + 1, p, s, q, lane) : -1;
@@ -1244,7 +1244,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   build_plan(p, plan, *reinterpret_cast<PlanScratch*>(gbase + Sm::k), blockIdx.x == 0 ? p.err : nullptr);
-  publish_plan(p, plan);
   cluster_sync();  // the other CTA's barriers are initialised, its scratch is done with
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
@@ -1260,7 +1259,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
       convert_role(p, cx, plan, pair, lo, hi, gbase);
     else
       tail_role(p, cx, plan, pair, lo, hi);
-  } else if (cx.rank == 0 && elect_one()) {
+  } else if (cx.rank == 1) {  // (its MMAs are issued by the leader)
+    publish_plan(p, plan, pair, threadIdx.x & 31);
+  } else if (elect_one()) {
     mma_role<kFp8>(p, cx, plan, pair, lo, hi, tmem);
   }
   __syncwarp();

@@ -16,7 +16,10 @@ namespace mfa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunkBytes = 32 * 1024;  // rows in shared memory a round
+// Rows in shared memory a round: with four and eight heads a CTA the parts of a batch of 32 (up to about twelve a
+// sequence) and of larger ones (about four) come in one round; four CTAs of that size share an SM.
+template <int kH>
+__host__ __device__ constexpr int chunk_bytes() { return kH >= 4 ? 48 * 1024 : 32 * 1024; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -31,6 +34,7 @@ __global__ void __launch_bounds__(kThreads, 4) prefix_combine_kernel(const Prefi
   constexpr int kDimThreads = kPerHead < 64 ? kPerHead : 64;
   constexpr int kVec = kHeadDim / (4 * kDimThreads);    // float4s a thread
   constexpr int kSubsets = kPerHead / kDimThreads;      // the parts are dealt to this many sets of threads
+  constexpr int kChunkBytes = chunk_bytes<kH>();
   constexpr int kPartBytes = kH * 1024;
   constexpr int kChunk = kChunkBytes / kPartBytes;      // parts a round
   static_assert(kDimThreads * kVec * 4 == kHeadDim && kH <= 8 && kChunk <= 32, "shape");
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 4) prefix_combine_kernel(const Prefi
 
 template <int kH>
 cudaError_t launch_kh(const PrefixParams& p, cudaStream_t stream) {
-  const size_t smem = kChunkBytes + sizeof(float) * (size_t)kH * 2 * p.pairs;
+  const size_t smem = chunk_bytes<kH>() + sizeof(float) * (size_t)kH * 2 * p.pairs;
   static int configured[kTrackedDevices] = {};
   const cudaError_t e = ensure_dynamic_smem(prefix_combine_kernel<kH>, smem, configured);
   if (e != cudaSuccess) return e;
