@@ -162,20 +162,6 @@ __device__ __forceinline__ void cluster_sync() {
 __device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
-// The same with that release, where it is rare.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 // Whether a phase is complete, without waiting for it.
 __device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -255,22 +241,6 @@ struct Ctx {
   __device__ bool wait(int i, uint32_t parity) const { return mbar_wait(bar(i), parity, budget, abort, err); }
   // the same for a whole warp, whose lanes give up together
   __device__ bool wait_warp(int i, uint32_t parity) const { return __all_sync(0xffffffffu, wait(i, parity)); }
-  // a barrier that threads of the other CTA arrive on
-  __device__ __noinline__ bool wait_pair_slow(int i, uint32_t parity) const {
-    const uint64_t t0 = globaltimer_ns();
-    while (!mbar_try_wait_cluster(bar(i), parity)) {
-      if (*abort) return false;
-      if (globaltimer_ns() - t0 > budget) {
-        raise_error(err, MFA_DEVERR_TIMEOUT);
-        *abort = 1;
-        return false;
-      }
-    }
-    return true;
-  }
-  __device__ bool wait_pair(int i, uint32_t parity) const {
-    return mbar_try_wait_cluster(bar(i), parity) || wait_pair_slow(i, parity);
-  }
 };
 
 // ---------------------------------------------------------------- plan
@@ -483,17 +453,15 @@ __device__ __forceinline__ bool is_partial(int tokens) { return tokens % kKeySte
 // Page ids of a tile: a window of 64 held by the warp (32 ahead of need).
 struct TilePages {
   int end, base, a, b;
-  __device__ int fetch(int k, const PrefixParams& p, const PlanSmem& s, const Piece& q) const {
+  __device__ int load(int k, const PrefixParams& p, const PlanSmem& s, const Piece& q) const {
     if (k >= end) return 0;
     const int o = q.owner(k);
-    size_t at;
-    if (o == kSeqs) {
-      at = (size_t)s.lead[q.t] * p.max_pages + k;
-    } else {
-      const int c = o == 0 ? q.c[0] : o == 1 ? q.c[1] : o == 2 ? q.c[2] : q.c[3];
-      at = (size_t)(q.b + o) * p.max_pages + (k - c) + (((q.behind >> o) & 1) ? q.c[0] : 0);
-    }
-    const int id = __ldg(p.page_table + at);
+    const int c = o == 0 ? q.c[0] : o == 1 ? q.c[1] : o == 2 ? q.c[2] : q.c[3];
+    const int seq = o == kSeqs ? s.lead[q.t] : q.b + o;
+    const int at = o == kSeqs ? k : k - c + (((q.behind >> o) & 1) ? q.c[0] : 0);
+    return __ldg(p.page_table + (size_t)seq * p.max_pages + at);
+  }
+  __device__ int checked(int id, const PrefixParams& p) const {
     if (id >= 0 && id < p.num_pages) return id;
     raise_error(p.err, MFA_DEVERR_PAGE);
     return 0;
@@ -501,14 +469,15 @@ struct TilePages {
   __device__ void start(int k, const PrefixParams& p, const PlanSmem& s, const Piece& q, int lane) {
     end = min(q.c[kSeqs], 2 * q.u1);
     base = k;
-    a = fetch(base + lane, p, s, q);
-    b = fetch(base + 32 + lane, p, s, q);
+    const int x = load(base + lane, p, s, q), y = load(base + 32 + lane, p, s, q);  // both on their way at once
+    a = checked(x, p);
+    b = checked(y, p);
   }
   __device__ int get(int k, const PrefixParams& p, const PlanSmem& s, const Piece& q, int lane) {
     while (k >= base + 64) {
       base += 32;
       a = b;
-      b = fetch(base + 32 + lane, p, s, q);
+      b = checked(load(base + 32 + lane, p, s, q), p);
     }
     const int i = k - base;
     return i < 32 ? __shfl_sync(0xffffffffu, a, i) : __shfl_sync(0xffffffffu, b, i - 32);
@@ -851,7 +820,7 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
   Unit pend{};  // the unit whose P V is still to be issued
   bool good = true;
   while (good && next_piece(s, hi, q)) {
-    good = kFp8 ? cx.wait_pair(QReady, pieces & 1) : cx.wait(QFull, pieces & 1);
+    good = cx.wait(kFp8 ? QReady : QFull, pieces & 1);
     for (int u = q.u0; good && u < q.u1; ++u) {
       good = do_s(pend.pending);
       if (good && pend.pending) good = do_pv(pend);
@@ -1044,7 +1013,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       if (!cx.wait_warp(QFull, pieces & 1)) return;
       mul *= split_q(cx.base + Smem<kFp8>::q, red, row, half);
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(cx.leader_bar(QReady));
+      if (lane == 0) mbar_arrive_pair(cx.leader_bar(QReady));
       barrier_rows(quad);  // red is free again
       ++pieces;
     }
@@ -1237,7 +1206,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
-  if (threadIdx.x == 0) {  // hints only: both may still be written
+  // hints only, these may still be written: what the plan, the first loads and Q need, in L2
+  {
+    auto hint = [](const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); };
+    const int i = threadIdx.x * 8;  // of 4-byte elements: a sector a thread
+    if (blockIdx.x == 0 && i < p.B) hint(p.seq_lens + i);
+    if (blockIdx.x == 0 && i < p.n_groups) hint(p.prefix_pages + i);
+    if (blockIdx.x == 0 && i <= p.n_groups) hint(p.group_starts + i);
+  }
+  if (threadIdx.x == 0) {
     prefetch_l2_share(p.page_table, (size_t)p.B * p.max_pages * sizeof(int32_t), blockIdx.x, gridDim.x);
     prefetch_l2_share(p.q, (size_t)p.B * kHeads * kHeadDim * sizeof(uint16_t), blockIdx.x, gridDim.x);
   }
