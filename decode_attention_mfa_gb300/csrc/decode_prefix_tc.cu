@@ -90,6 +90,9 @@ template <bool kFp8>
 __host__ __device__ constexpr float moved_to() { return kFp8 ? 4.0f : 0.0f; }
 constexpr float kMostSum = 32768.0f;
 constexpr int kKeyStep = 16;  // keys of one MMA of P V
+// Waits for what this CTA itself has in flight, before it leaves, do not shrink with the wait budget; and after a wait
+// that gave up, copies that no barrier of this CTA tells of get this long to land.
+constexpr uint64_t kDrainNs = 200000000ull, kSettleNs = 1000000ull;
 static_assert(kPrefixTileSeqs * kHeads == 256, "rows of a row tile");
 
 enum Bar {
@@ -595,16 +598,16 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
   // stays until the cluster's last barrier.
   if (lane == 0) {
     for (uint32_t k = cnt > 2 ? cnt - 2 : 0; k < cnt; ++k) {
-      if (r == 0) (void)mbar_wait(cx.bar(KFull + (k & 1)), (k >> 1) & 1, cx.budget, nullptr, p.err);
+      if (r == 0) (void)mbar_wait(cx.bar(KFull + (k & 1)), (k >> 1) & 1, kDrainNs, nullptr, p.err);
       if ((kFp8 || r == 0) && (good || k + 1 < cnt))
-        (void)mbar_wait(cx.bar((kFp8 ? RawFull : VFull) + (k & 1)), (k >> 1) & 1, cx.budget, nullptr, p.err);
+        (void)mbar_wait(cx.bar((kFp8 ? RawFull : VFull) + (k & 1)), (k >> 1) & 1, kDrainNs, nullptr, p.err);
     }
     for (int i = 0; i < 2; ++i)
-      if (tails[i]) (void)mbar_wait(cx.bar(TailFull + i), (tails[i] - 1) & 1, cx.budget, nullptr, p.err);
+      if (tails[i]) (void)mbar_wait(cx.bar(TailFull + i), (tails[i] - 1) & 1, kDrainNs, nullptr, p.err);
     if constexpr (kFp8)
       for (uint32_t k = cnt > (uint32_t)kScaleSlots ? cnt - kScaleSlots : 0; k < cnt; ++k)
-        (void)mbar_wait(cx.bar(ScFull + k % kScaleSlots), (k / kScaleSlots) & 1, cx.budget, nullptr, p.err);
-    if (pieces && (kFp8 || r == 0)) (void)mbar_wait(cx.bar(QFull), (pieces - 1) & 1, cx.budget, nullptr, p.err);
+        (void)mbar_wait(cx.bar(ScFull + k % kScaleSlots), (k / kScaleSlots) & 1, kDrainNs, nullptr, p.err);
+    if (pieces && (kFp8 || r == 0)) (void)mbar_wait(cx.bar(QFull), (pieces - 1) & 1, kDrainNs, nullptr, p.err);
   }
   __syncwarp();
 }
@@ -847,7 +850,7 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
     (void)do_pv(pend);
   }
   tc_commit_pair(cx.bar(Drain));  // every MMA is done before TMEM is given back
-  (void)mbar_wait(cx.bar(Drain), 0, cx.budget, nullptr, p.err);
+  (void)mbar_wait(cx.bar(Drain), 0, kDrainNs, nullptr, p.err);
 }
 
 // ---------------------------------------------------------------- softmax
@@ -993,9 +996,13 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
   const uint32_t p_full = cx.leader_bar(PFull), o_free = cx.leader_bar(OFree);
   float* red = reinterpret_cast<float*>(gbase + Smem<kFp8>::red);
   uint32_t cnt = 0, pieces = 0;  // units, pieces so far
+  // After a wait that gave up, the warp goes through the rest of its work without waiting, so that the warps that meet it
+  // at named barriers, which have no limit, do not wait for it in vain. What it computes is meaningless.
+  bool alive = true;
+  auto wait = [&](int bar, uint32_t parity) { alive = alive && cx.wait_warp(bar, parity); };
   // P V of the unit before `cnt`. S of that unit is done, and with it every MMA issued before it, P V of two units
   // earlier (the last on the same barrier) among them: the parity is exact.
-  auto wait_pv = [&]() -> bool { return cx.wait_warp(PvDone + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1); };
+  auto wait_pv = [&]() { wait(PvDone + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1); };
   Piece q;
   q.x = lo;
   while (next_piece(s, hi, q)) {
@@ -1010,7 +1017,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     float m = -INFINITY, l = 0.0f;  // the row's reference (log2 units), and this thread's share of its denominator
     float mul = c2;                 // of the row's products: the softmax scale, and 2^-e of its Q terms
     if constexpr (kFp8) {
-      if (!cx.wait_warp(QFull, pieces & 1)) return;
+      wait(QFull, pieces & 1);
       mul *= split_q(cx.base + Smem<kFp8>::q, red, row, half);
       __syncwarp();
       if (lane == 0) mbar_arrive_pair(cx.leader_bar(QReady));
@@ -1021,8 +1028,8 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       const uint32_t buf = cnt & 1, ts = tmem + lanes + buf * kSCols;
       const uint32_t sc_slot = cnt % kScaleSlots;
       const float* sc = reinterpret_cast<const float*>(gbase + Smem<kFp8>::scales + sc_slot * kScaleBytes);
-      if (kFp8 && !cx.wait_warp(ScFull + sc_slot, (cnt / kScaleSlots) & 1)) return;
-      if (!cx.wait_warp(SFull + buf, (cnt >> 1) & 1)) return;
+      if (kFp8) wait(ScFull + sc_slot, (cnt / kScaleSlots) & 1);
+      wait(SFull + buf, (cnt >> 1) & 1);
       tc_fence_after();
       const int cols = seen(2 * u + half);  // this thread's keys
       if (cols + seen(2 * u + (half ^ 1)) > 0) {
@@ -1101,7 +1108,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             l *= alpha;
             if (!fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
               // O holds the units before this one; each of the two warps scales half of its columns
-              if (!wait_pv()) return;
+              wait_pv();
               tc_fence_after();
 #pragma unroll 1
               for (int c = 128 * half; c < 128 * half + 128; c += 32) {
@@ -1135,7 +1142,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       }
     }
     // ---- the piece's partial result: O / l and its LSE, 128 dims a thread
-    if (!wait_pv()) return;
+    wait_pv();
     tc_fence_after();
     if (!fresh) {
       red[half * 128 + row] = l;
@@ -1240,6 +1247,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
     publish_plan(p, plan, pair, threadIdx.x & 31);
   } else if (elect_one()) {
     mma_role<kFp8>(p, cx, plan, pair, lo, hi, tmem);
+  }
+  __syncwarp();
+  if (*cx.abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kSettleNs) {}
   }
   __syncwarp();
   tc_fence_before();

@@ -22,6 +22,7 @@ template <int kH>
 __host__ __device__ constexpr int chunk_bytes() { return kH >= 4 ? 48 * 1024 : 32 * 1024; }
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr uint64_t kDrainNs = 200000000ull;
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
@@ -111,8 +112,9 @@ __global__ void __launch_bounds__(kThreads, 4) prefix_combine_kernel(const Prefi
       __syncthreads();  // every thread is done with the previous round's rows
       if (warp == 0) issue_round(k);
     }
-    // bounded; on expiry the error word records it, and every thread still reaches the barriers
-    (void)mbar_wait(bar, k & 1, p.wait_budget_ns, nullptr, p.err);
+    // bounded, but not by the wait budget: these are this CTA's own copies. On expiry the error word records it, and every
+    // thread still reaches the barriers.
+    (void)mbar_wait(bar, k & 1, kDrainNs, nullptr, p.err);
     const int i0 = k * kChunk, cnt = min(kChunk, n - i0);
     for (int i = sub; i < cnt; i += kSubsets) {
       const float wi = w[i0 + i];

@@ -291,3 +291,119 @@ def test_captured_and_replayed_with_new_lengths_and_groups(fp8):
         graphs[0].replay()
         stream.synchronize()
         a.check()
+
+
+@KV
+def test_nothing_of_one_sequence_reaches_another(fp8):
+    """NaN and infinities in the pages, scales and query of one sequence change no bit of the others' results, although
+    they share tiles, units and MMAs; its own results are NaN."""
+    sizes, pages = [6, 5], [5, 3]
+    lens = lens_of(sizes, pages, 200, 6)
+    lens[7] = 100  # ends inside its prefix: read on its own
+    lens[[1, 4, 8]] += 70
+    b = Batch(sizes, pages, lens, fp8, seed=11).run()
+    clean = b.out.clone(), b.lse.clone()
+    for bad in (1, 4, 7, 8):
+        own = [int(x) for x in b.table[bad, (0 if bad == 7 else pages[0 if bad < 6 else 1]):-(-int(lens[bad]) // PAGE)]]
+        if bad == 7:  # its pages are the group's: its query alone is its own
+            own = []
+        keep = [c.clone() for c in b.cache], [x.clone() for x in b.scales], b.q.clone()
+        for i, c in enumerate(b.cache):
+            if own and fp8:
+                c[own[0]] = 0x7F
+                b.scales[i][own[-1]] = float("inf") if i else float("nan")
+            elif own:
+                c[own[0]] = float("nan")
+                c[own[-1], 0] = float("inf")
+        b.q[bad, 5] = float("nan")
+        b.call()
+        capi.mfa_check_device_errors(b.ws)
+        others = [i for i in range(11) if i != bad]
+        assert torch.equal(b.out[others], clean[0][others]) and torch.equal(b.lse[others], clean[1][others]), bad
+        assert torch.isnan(b.out[bad, 5].float()).all()
+        if own:
+            assert torch.isnan(b.out[bad].float()).any(dim=1).all()
+        for c, k in zip(b.cache, keep[0]):
+            c.copy_(k)
+        for c, k in zip(b.scales, keep[1]):
+            c.copy_(k)
+        b.q.copy_(keep[2])
+    b.run()
+
+
+@KV
+def test_nan_in_the_prefix_reaches_all_who_see_it_and_no_one_else(fp8):
+    sizes, pages = [6, 5], [5, 3]
+    lens = lens_of(sizes, pages, 200, 6)
+    lens[2] = 64  # sees the first page of its group's prefix
+    b = Batch(sizes, pages, lens, fp8, seed=12).run()
+    clean = b.out.clone()
+    page = int(b.table[0, 3])
+    b.cache[1][page, 17] = 0x7F if fp8 else float("nan")
+    b.call()
+    capi.mfa_check_device_errors(b.ws)
+    hit = [0, 1, 3, 4, 5]
+    assert torch.isnan(b.out[hit].float()).all()
+    others = [i for i in range(11) if i not in hit]
+    assert torch.equal(b.out[others], clean[others])
+
+
+@KV
+def test_small_weights_beside_a_large_one(fp8):
+    """One key with most of the weight and a value of nearly nothing (as the first token of a text often has) beside
+    thousands of small weights: what these add up to is kept."""
+    n, pages = 4, 130
+    b = Batch([n], [pages], np.full(n, pages * PAGE + 40), fp8, seed=13)
+    first = int(b.table[0, 0])
+    q = b.q.float().mean(dim=(0, 1))
+    for i in range(n):
+        b.q[i] = (b.q[i].float() * 0.1 + q / q.norm() * 16).bfloat16()
+    key = q / q.norm()
+    if fp8:
+        s = key.abs().max() * 12.0 / 448
+        b.cache[0][first, 0] = (key * 12.0 / s).to(torch.float8_e4m3fn).view(torch.uint8)
+        b.scales[0][first, 0] = s
+        b.scales[1][first, 0] *= 1e-4
+    else:
+        b.cache[0][first, 0] = (key * 12.0).bfloat16()
+        b.cache[1][first, 0] *= 1e-4
+    b.call()
+    capi.mfa_check_device_errors(b.ws)
+    for i in range(n):
+        out, lse, top = b.reference(i)
+        got = b.out[i].double()
+        # the weights are rounded one by one (bf16: 2^-8 of each), so the result is off by a like part of itself
+        assert float((got - out).norm() / out.norm()) <= 2 ** -7, i
+        assert float((b.lse[i].double() - lse).abs().max()) <= LSE_ABS
+
+
+@KV
+def test_a_wait_that_gives_up_is_reported_and_the_next_call_is_whole(fp8):
+    sizes, pages = [6, 5], [40, 30]
+    b = Batch(sizes, pages, lens_of(sizes, pages, 200, 6), fp8, seed=14)
+    b.workspace()
+    try:
+        capi.mfa_set_wait_budget_ns(0)
+        b.call()
+        with pytest.raises(capi.MFAError) as e:
+            capi.mfa_check_device_errors(b.ws)
+        assert e.value.status == 7
+    finally:
+        capi.mfa_set_wait_budget_ns(2_000_000_000)
+    b.run()
+
+
+@KV
+def test_two_calls_at_once_with_workspaces_of_their_own(fp8):
+    sizes, pages = [9, 4], [33, 20]
+    a = Batch(sizes, pages, lens_of(sizes, pages, 300, 1), fp8, seed=15)
+    b = Batch(sizes, pages, lens_of(sizes, pages, 300, 2), fp8, seed=16)
+    a.workspace()
+    b.workspace()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for x, s in zip((a, b), streams):
+            x.call(stream=s)
+    torch.cuda.synchronize()
+    a.check()
+    b.check()
