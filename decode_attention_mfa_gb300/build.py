@@ -33,6 +33,7 @@ def _sources():
 
 def _deps():
     return (_sources() + glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+            + glob.glob(os.path.join(CSRC, "*.hpp"))
             + [os.path.join(ROOT, "include", "mfa.h"), os.path.abspath(__file__)])
 
 

@@ -58,6 +58,7 @@
 #include <type_traits>
 
 #include "mfa_device.cuh"
+#include "mfa_serving.hpp"
 
 namespace mfa {
 namespace {

@@ -14,6 +14,7 @@
 #include <cuda_fp8.h>
 
 #include "mfa_device.cuh"
+#include "mfa_serving.hpp"
 
 namespace mfa {
 namespace {

@@ -12,6 +12,7 @@
 #include <cudaTypedefs.h>
 
 #include "mfa_internal.h"
+#include "mfa_serving.hpp"
 
 namespace {
 

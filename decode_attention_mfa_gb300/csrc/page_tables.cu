@@ -17,6 +17,7 @@
 // The calls are bound by latency (launch, two dependent loads, the sums): the
 // step of 1000 requests with 250,000 tokens moves 2 MB.
 #include "mfa_device.cuh"
+#include "mfa_serving.hpp"
 
 namespace mfa {
 namespace {

@@ -11,6 +11,7 @@
 // or a part without a finite logit) is skipped, never scaled. Bound by latency,
 // and for large batches by reading the parts from L2.
 #include "mfa_device.cuh"
+#include "mfa_serving.hpp"
 
 namespace mfa {
 namespace {
