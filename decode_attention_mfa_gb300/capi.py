@@ -12,8 +12,6 @@ import os
 import re
 import threading
 
-import torch
-
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libmfa.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "mfa.h")
@@ -115,6 +113,7 @@ def _ptr(x):
 
 def _stream(s):
     if s is None:
+        import torch
         # the handle of torch.cuda.current_stream(), without the Stream object (3 us of a call that takes the GPU as long)
         return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):

@@ -1,4 +1,4 @@
-"""Host checks of the page-table and slot-append calls: every refusal comes before any device work, so no GPU
+"""Host checks of the page-table, slot-append and shared-prefix calls: every refusal comes before any device work, so no GPU
 is needed."""
 import ctypes
 
@@ -62,3 +62,34 @@ def test_append_slots_refusals(lib, mem, fp8):
         assert fn(*dict(good, **{key: value}).values()) == 1, (key, value)
     for ws in (None, p + 64):
         assert fn(*dict(good, ws=ws).values()) == 4
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_prefix_attention_refusals(lib, mem, fp8):
+    p = mem[1]
+    good = dict(q=p, kc=p + 512, vc=p + 1024)
+    good.update(dict(k_scale=p + 4096, v_scale=p + 4352) if fp8 else {})
+    good.update(table=p + 1536, lens=p + 2048, starts=p + 2304, pages=p + 2560, n_groups=2, out=p + 3584, lse=p + 3840,
+                scale=1 / 16, batch=4, max_pages=2, num_pages=8, prefix_hint=64, suffix_hint=64, ws=p + 5120, n=1 << 30,
+                stream=None)
+    fn = lib.mfa_decode_attention_prefix_fp8 if fp8 else lib.mfa_decode_attention_prefix
+    pointers = [k for k in good if k in ("q", "kc", "vc", "k_scale", "v_scale", "table", "lens", "starts", "pages", "out", "lse")]
+    bad = [(k, None) for k in pointers] + [(k, good[k] + 2) for k in pointers]
+    bad += [(k, good[k] + 8) for k in pointers if k in ("q", "kc", "vc", "k_scale", "v_scale", "out")]
+    bad += [("n_groups", 0), ("n_groups", 5), ("n_groups", -1), ("batch", 0), ("batch", capi.MAX_BATCH + 1), ("batch", 1),
+            ("max_pages", 0), ("max_pages", 2 ** 30), ("max_pages", 2 ** 26), ("num_pages", 0), ("prefix_hint", -1),
+            ("suffix_hint", -1)]
+    for key, value in bad:
+        assert fn(*dict(good, **{key: value}).values()) == 1, (key, value)
+    for ws in (None, p + 8):
+        assert fn(*dict(good, ws=ws).values()) == 4
+    call = capi.mfa_decode_attention_prefix_fp8 if fp8 else capi.mfa_decode_attention_prefix
+    with pytest.raises(capi.MFAError):
+        call(*dict(good, n_groups=0, stream=0).values())
+
+
+def test_prefix_workspace_refusals(lib):
+    for args in ((0, 1, 0, 0), (capi.MAX_BATCH + 1, 1, 0, 0), (4, 0, 0, 0), (4, 5, 0, 0), (4, 1, -1, 0), (4, 1, 0, -1)):
+        assert lib.mfa_decode_prefix_workspace_bytes(*args) == 0
+        with pytest.raises(capi.MFAError):
+            capi.mfa_decode_prefix_workspace_bytes(*args)
