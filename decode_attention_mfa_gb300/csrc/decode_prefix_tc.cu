@@ -12,12 +12,13 @@
 //
 // Row tile: up to four neighbouring sequences, 256 rows, and as its keys the
 // pages of their prefix, then the own pages of the first sequence, of the
-// second, and so on. A page is therefore seen by all the rows of the tile or by those
-// of one sequence; the others' rows skip its softmax and are left out of its P V
-// MMAs (by their mask of output lanes, so that nothing in a sequence's pages, not
-// even a NaN, reaches another's result). Own pages use a quarter of the rows, but a unit of two
-// pages still takes the tensor cores less time (2048 cycles of a pair of SMs)
-// than HBM at the pair's share of the bandwidth (128 KB).
+// second, and so on. A page is therefore seen by all the rows of the tile or by
+// those of one sequence; the others' rows skip its softmax and are left out of
+// its P V MMAs (by their mask of output lanes, so that nothing in a sequence's
+// pages, not even a NaN, reaches another's result). Own pages use a quarter of
+// the rows, but a unit of two pages still takes the tensor cores less time (2048
+// cycles of a pair of SMs) than HBM takes to deliver its 128 KB at the pair's
+// share of the bandwidth.
 //
 // A cluster of two CTAs, each with 128 of the rows, works on units of 128 keys
 // (two pages) with tcgen05 MMAs of cta_group::2: each CTA holds one of the two
@@ -31,18 +32,21 @@
 // Work split: the units of all row tiles, one after the other, form a line
 // (kPrefixPieceUnits more for every tile: its Q load and partial results); each
 // pair takes an equal range of it (stream-K) and writes, per row tile that it
-// holds units of, normalised partial results and LSEs of the sequences that see any of them;
-// the LSE combine joins a sequence's parts.
+// holds units of, normalised partial results and LSEs of the sequences that see
+// any of them; the combine joins a sequence's parts.
 //
 // Warp roles:
 //   warps 0-7  softmax: thread = row = TMEM lane; warp w and w + 4 share 32
-//              rows, 64 keys of a unit each, and agree on the reference maximum, which moves
-//              only when weights become large (then O is rescaled).
-//   warp 8     producer (TMA, each CTA its own halves, completing on the leader's barriers).
-//   warp 9     MMA issue (one thread of the leader) and TMEM allocation.
+//              rows, 64 keys of a unit each, and agree on the reference maximum,
+//              which moves only when weights become large (then O is rescaled).
+//   warp 8     producer (TMA, each CTA its own halves, completing on the
+//              leader's barriers).
+//   warp 9     TMEM allocation, and MMA issue (one thread of the leader's; the
+//              other CTA's leaves the combine where the parts are).
 //   warp 10    the rows behind a sequence's last token in V, zeroed up to the
 //              end of an MMA's 16 keys: 0 * NaN of a stale row would poison P V.
-//   warps 10-13 (E4M3 cache only, instead) V codes to f16, rows behind the last token to zero.
+//   warps 10-13 (E4M3 cache only, instead) V codes to f16, rows behind the last
+//              token to zero.
 // Every wait is bounded (the wait budget), as in the split kernel.
 //
 // E4M3 cache: S is 8-bit MMAs (kind::f8f6f4) on the raw K codes, with Q as two
@@ -67,9 +71,9 @@ constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kTailWarp = 10
 template <bool kFp8>
 __host__ __device__ constexpr int threads() { return 32 * (kTailWarp + (kFp8 ? kConvertWarps : 1)); }
 // Two K and two V slots, of even and odd units, one CTA's half of a unit each: K one page of 256 dims, V 128 dims of two
-// pages (each page's half at kHalf). A K slot is free when S of its unit is done, a V slot when P V is, which the
-// softmax warps are told anyway: the issuing thread commits twice a unit. (With a ring of 16 KB granules it waited
-// four times and committed six times a unit, and a unit took 3600 cycles instead of XXXX.)
+// pages. A K slot is free when S of its unit is done, a V slot when P V is, which the softmax warps are told anyway: the
+// issuing thread commits twice a unit. (With a ring of 16 KB granules it waited four times and committed six times a
+// unit, and a unit took 3600 cycles; 2650 with these slots; 2048, the tensor cores' own time, with elect_one.)
 template <bool kFp8>
 __host__ __device__ constexpr uint32_t slot_bytes() { return kFp8 ? 16384 : 32768; }  // as loaded
 constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;                          // V as the MMAs read it, 16 bits
@@ -228,7 +232,7 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
 }
 
 // True in one thread of a converged warp. The compiler knows that it is one, and then issues a tcgen05 instruction behind
-// it without a loop over the threads that might be active.
+// it without a loop over the threads that might be active (80 cycles an MMA, of which a unit has 24 or 32).
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
@@ -662,10 +666,11 @@ __device__ __forceinline__ int page_exponent(const float* sc, int valid, int lan
 }
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
-// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^-e (at most 448, e of the page), from the codes: per page [64 rows x 128
-// dims] to two 64-dim chunks of [64 rows x 128 B], both with the 128-byte swizzle. Thread t takes 16 codes of row t / 8
-// and of every 16th row after it; rows behind the last token become zeros. That the scales are applied here spares the
-// softmax threads 64 values each from shared memory, whose bandwidth the MMAs need.
+// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^-e (at most 448, e of the page; off by 2^-11 for the scale and
+// 2^-11 for the product), from the codes: per page [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both
+// with the 128-byte swizzle. Thread t takes 16 codes of row t / 8 and of every 16th row after it; rows behind the last
+// token become zeros. That the scales are applied here spares the softmax threads 64 values each from shared memory,
+// whose bandwidth the MMAs need.
 __device__ void convert_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi,
                              const uint8_t* gbase) {
   using Sm = Smem<true>;
@@ -760,7 +765,7 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
       if (i == 8) pv_ready = p_next && peek(VFull + (p_cnt & 1), (p_cnt >> 1) & 1) && peek(PFull + (p_cnt & 1), (p_cnt >> 1) & 1);
       if constexpr (kFp8) {  // Q's term i / 8, 128-dim half, 32 dims
         const int h = (i >> 2) & 1, kk = i & 3;
-        tc_mma_pair_f8(d, ahead(q_desc, (i >> 3) * 32768 + h * 16384 + kk * 32), ahead(k_desc, h * 8192 + kk * 32), idesc_s, i != 0);
+        tc_mma_pair_f8(d, ahead(q_desc, h * 32768 + (i >> 3) * 16384 + kk * 32), ahead(k_desc, h * 8192 + kk * 32), idesc_s, i != 0);
       } else {  // 64-dim block, 16 dims
         const int e = i >> 2, kk = i & 3;
         tc_mma_pair(d, ahead(q_desc, e * 16384 + kk * 32), ahead(k_desc, e * 8192 + kk * 32), idesc_s, i != 0);
@@ -916,7 +921,7 @@ __device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
                "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
                : "memory");
 }
-// Barriers of the two warps that share 32 rows, and of all softmax warps.
+// Barriers of the two warps that share 32 rows.
 __device__ __forceinline__ void barrier_rows(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
 __device__ __forceinline__ bool barrier_rows_or(int quad, bool pred) {
   uint32_t r;
@@ -927,28 +932,54 @@ __device__ __forceinline__ bool barrier_rows_or(int quad, bool pred) {
       : "memory");
   return r != 0;
 }
-__device__ __forceinline__ void barrier_softmax() { asm volatile("bar.sync 5, 256;" ::: "memory"); }
+
+// Eight bf16 values times `up` as two E4M3 terms: codes of four in a word.
+__device__ __forceinline__ void split_q8(const uint4 v, float up, uint32_t (&t1)[2], uint32_t (&t2)[2]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t a = 0, b = 0;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const float x = __uint_as_float(w[2 * i + k] << 16) * up, y = __uint_as_float(w[2 * i + k] & 0xFFFF0000u) * up;
+      const __nv_fp8x2_storage_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+      const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3);
+      const float2 d1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+      const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(x - d1.x, y - d1.y), __NV_SATFINITE, __NV_E4M3);
+      a |= (uint32_t)c1 << (16 * k);
+      b |= (uint32_t)c2 << (16 * k);
+    }
+    t1[i] = a;
+    t2[i] = b;
+  }
+}
 
 // E4M3: the bf16 Q of this CTA's 128 rows (four 64-dim blocks of [128 rows x 128 B], 128-byte swizzle) becomes, in
-// place, two E4M3 terms of Q * 2^e ([term][128-dim half][128 rows x 128 B]): t1 rounds the scaled value, t2 the rest,
-// which is exact unless it falls below the E4M3 normal range (2^-18.8 of the row's largest |q|). 2^e is the largest
-// power of two that keeps the row within the E4M3 maximum, 448. Thread (row, half) takes 128 dims of its row. All
-// softmax threads; red: their exchange. Returns 2^-e.
-__device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, int half) {
-  uint4 v[16];  // 8 dims each
-#pragma unroll
-  for (int j = 0; j < 16; ++j)
-    v[j] = ld_shared_v4(q_addr + (2 * half + (j >> 3)) * 16384 + row * 128 + (((j & 7) ^ (row & 7)) << 4));
+// place, two E4M3 terms of Q * 2^e ([128-dim half][term][128 rows x 128 B]): the first rounds the scaled value, the second
+// the rest, which is exact unless it falls below the E4M3 normal range (2^-18.8 of the row's largest |q|). 2^e is the
+// largest power of two that keeps the row within the E4M3 maximum, 448. Thread (row, half) takes the 128 dims of its
+// half, whose terms lie where they did: the second block is read whole before the terms of the first replace either.
+// All softmax threads; red: their exchange. Returns 2^-e.
+__device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, int quad, int half) {
+  const uint32_t at = q_addr + half * 32768 + row * 128;  // the first of the two blocks; the second 16 KB on
+  auto chunk = [&](int j) { return ((j ^ (row & 7)) << 4); };
+  uint4 v[8];
   float top = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+  auto largest = [&](const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
+  };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) largest(ld_shared_v4(at + chunk(j)));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = ld_shared_v4(at + 16384 + chunk(j));
+    largest(v[j]);
   }
   red[half * 128 + row] = top;
-  barrier_softmax();  // every row is in registers: the terms may overwrite it
+  barrier_rows(quad);
   top = fmaxf(red[row], red[128 + row]);
   int e = 0;
   if (top > 0.0f && top <= 3.0e38f) {
@@ -956,36 +987,24 @@ __device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, i
     e = ((bits & 0x7FFFFFu) <= 0x600000u ? 8 : 7) - ((int)((bits >> 23) & 0xFFu) - 127);  // top * 2^e in (224, 448]
     e = max(-126, min(126, e));
   }
-  const float up = __uint_as_float((uint32_t)(e + 127) << 23);
+  const float up = exp2_int(e);
+  auto store = [&](int o, const uint4& x, const uint4& y) {  // 16 dims
+    uint32_t a1[2], a2[2], b1[2], b2[2];
+    split_q8(x, up, a1, a2);
+    split_q8(y, up, b1, b2);
+    const uint32_t t1[4] = {a1[0], a1[1], b1[0], b1[1]}, t2[4] = {a2[0], a2[1], b2[0], b2[1]};
+    st_shared_v4(at + chunk(o), t1);
+    st_shared_v4(at + 16384 + chunk(o), t2);
+  };
 #pragma unroll
-  for (int o = 0; o < 8; ++o) {  // 16 dims
-    uint32_t t1[4], t2[4];
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const uint32_t w[4] = {v[2 * o + u].x, v[2 * o + u].y, v[2 * o + u].z, v[2 * o + u].w};
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint32_t a = 0, b = 0;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float x = __uint_as_float(w[2 * i + k] << 16) * up, y = __uint_as_float(w[2 * i + k] & 0xFFFF0000u) * up;
-          const __nv_fp8x2_storage_t c1 = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
-          const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3);
-          const float2 d1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
-          const __nv_fp8x2_storage_t c2 = __nv_cvt_float2_to_fp8x2(make_float2(x - d1.x, y - d1.y), __NV_SATFINITE, __NV_E4M3);
-          a |= (uint32_t)c1 << (16 * k);
-          b |= (uint32_t)c2 << (16 * k);
-        }
-        t1[2 * u + i] = a;
-        t2[2 * u + i] = b;
-      }
-    }
-    const uint32_t at = q_addr + half * 16384 + row * 128 + ((o ^ (row & 7)) << 4);
-    st_shared_v4(at, t1);
-    st_shared_v4(at + 32768, t2);
+  for (int o = 0; o < 4; ++o) {
+    const uint4 x = ld_shared_v4(at + chunk(2 * o)), y = ld_shared_v4(at + chunk(2 * o + 1));
+    store(o, x, y);
   }
+#pragma unroll
+  for (int o = 4; o < 8; ++o) store(o, v[2 * o - 8], v[2 * o - 7]);
   fence_proxy_async_smem();
-  return __uint_as_float((uint32_t)(127 - e) << 23);
+  return exp2_int(-e);
 }
 
 template <bool kFp8>
@@ -1015,11 +1034,12 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     const int tail = (int)((q.tails >> (8 * j)) & 0xFF);
     auto seen = [&](int k) { return k < prefix ? kPageSize : k < own0 || k >= own1 ? 0 : k + 1 < own1 ? kPageSize : tail; };
     bool fresh = true;              // no key so far
+    bool open = true;               // a row of the warp has no finite reference
     float m = -INFINITY, l = 0.0f;  // the row's reference (log2 units), and this thread's share of its denominator
     float mul = c2;                 // of the row's products: the softmax scale, and 2^-e of its Q terms
     if constexpr (kFp8) {
       wait(QFull, pieces & 1);
-      mul *= split_q(cx.base + Smem<kFp8>::q, red, row, half);
+      mul *= split_q(cx.base + Smem<kFp8>::q, red, row, quad, half);
       __syncwarp();
       if (lane == 0) mbar_arrive_pair(cx.leader_bar(QReady));
       barrier_rows(quad);  // red is free again
@@ -1096,7 +1116,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           }
           return top;
         };
-        bool move = fresh;
+        bool move = open;
 #pragma unroll 1
         for (int tries = 0; tries < 2; ++tries) {
           if (move) {
@@ -1106,6 +1126,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));
             const float alpha = fresh || m == m_new ? 1.0f : ex2_approx(m - m_new);
             m = m_new;
+            open = __any_sync(0xffffffffu, m == -INFINITY);  // the same in both warps of the rows
             l *= alpha;
             if (!fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
               // O holds the units before this one; each of the two warps scales half of its columns

@@ -3,8 +3,8 @@
 Tolerances, from the roundings on the way: each weight enters the second product as bf16, off by at most 2^-8 of
 itself, so an output is off by at most 2^-8 of the weighted mean of |v|, which is at most the largest |v|; the output is
 rounded to bf16, off by at most 2^-8 of itself; the fp32 sums of 256 products and the exponentials add less than 2^-12 of
-either. On an E4M3 cache the queries (2^-18.8 of the largest) and the weights (two terms: 2^-8) are held less exactly
-than that by no more than another 2^-8 of the largest |v|. The LSE is off by the logits' fp32 sums, 2^-15 of
+either. On an E4M3 cache the weights and the scaled values are f16 (2^-11 each, and 2^-11 for the scale) and the queries
+are held to 2^-18.8 of the largest: together no more than another 2^-8 of the largest |v|. The LSE is off by the logits' fp32 sums, 2^-15 of
 scale * sum |q k| (about 10 here), below 1e-3."""
 import numpy as np
 import pytest
@@ -407,3 +407,136 @@ def test_two_calls_at_once_with_workspaces_of_their_own(fp8):
     torch.cuda.synchronize()
     a.check()
     b.check()
+
+
+@KV
+def test_a_first_unit_of_infinite_logits_leaves_later_low_ones_whole(fp8):
+    """Two pages (a unit of the kernel) whose logits are all -inf come first, and then logits near -224: a reference of the
+    first unit's would send all their exponentials to zero. Queries of 1 and -1 but for one of 1024, so that two E4M3 terms
+    hold them exactly. The LSE, and with it each weight, is off by 2^-15 of scale * sum |q k|, which is below 256."""
+    n, pages = 3, 6
+    b = Batch([n], [pages], np.full(n, pages * PAGE + 30), fp8, seed=17)
+    b.q.copy_(torch.sign(b.q.float()).bfloat16())
+    b.q[:, :, 0] = 1.0
+    b.q[:, :, 1] = 1024.0
+    low = torch.from_numpy(b.table[0, :2]).long().cuda()
+    if fp8:
+        b.scales[0].fill_(2 ** -7)      # values of up to 3.5
+        b.cache[0][:, :, 1] = 0xFE      # -448
+        b.cache[0][low] = 0
+        b.cache[0][low, :, 0] = 0xB8    # -1
+        b.scales[0][low] = float("inf")
+        # 0 * inf is NaN: the other codes of these rows meet the scale as a part of the sum only
+    else:
+        b.cache[0][:, :, 1] = -3.5
+        b.cache[0][low, :, 0] = float("-inf")
+    b.call(hints=(0, 0))
+    capi.mfa_check_device_errors(b.ws)
+    for i in range(n):
+        length = int(b.lens[i]) - 2 * PAGE
+        ids = torch.from_numpy(b.table[i, 2:-(-int(b.lens[i]) // PAGE)]).long().cuda()
+        k, v = (c[ids].view(torch.float8_e4m3fn).double() * x[ids].double().unsqueeze(-1) if fp8 else c[ids].double()
+                for c, x in zip(b.cache, b.scales or [None] * 2))
+        k, v = k.reshape(-1, DIM)[:length], v.reshape(-1, DIM)[:length]
+        logits = b.q[i].double() @ k.T * SCALE
+        lse = torch.logsumexp(logits, 1)
+        out = torch.exp(logits - lse[:, None]) @ v
+        assert float(lse.max()) < -150
+        err = 256 * 2 ** -15
+        assert float((b.lse[i].double() - lse).abs().max()) <= err
+        bound = (2 ** -8 * (2 if fp8 else 1) + 2 * err) * v.abs().max() + 2 ** -8 * out.abs()
+        assert ((b.out[i].double() - out).abs() <= bound).all()
+
+
+@KV
+def test_serving_steps_over_a_shared_prefix(fp8):
+    """What a server does: a prompt is appended once, its pages are entered in the rows of all who share it, and then
+    steps of reserve, append by slots and attention are replayed from one graph; requests end, keep the shared pages and
+    give back their own. Lengths, caches and results follow the host's bookkeeping."""
+    sizes, pages, B, cols, num_pages, rows = [3, 4], [3, 2], 7, 8, 64, 7 * 24
+    b = Batch(sizes, pages, np.repeat(pages, sizes) * PAGE, fp8, seed=18, spare_cols=5)  # the prompts alone
+    i32 = dict(dtype=torch.int32, device="cuda")
+    kv = [torch.zeros((num_pages, PAGE, DIM), dtype=torch.uint8 if fp8 else torch.bfloat16, device="cuda") for _ in range(2)]
+    scales = [torch.zeros((num_pages, PAGE), device="cuda") for _ in range(2 * fp8)]
+    ids = torch.randperm(num_pages, generator=torch.Generator().manual_seed(1)).int().cuda()
+    free, n_free = ids.clone(), torch.tensor([num_pages], **i32)
+    table = torch.full((B, cols), -1, **i32)
+    lens, new, done = (torch.zeros(B, **i32) for _ in range(3))
+    starts = torch.zeros(B + 1, **i32)
+    slots = torch.zeros(max(rows, 5 * PAGE), dtype=torch.int64, device="cuda")
+    fused = torch.zeros((5 * PAGE, 2 * DIM), dtype=torch.bfloat16, device="cuda")
+    keep = torch.tensor(np.repeat(pages, sizes), **i32)
+    hints = (max(pages) * PAGE, 3 * PAGE)
+    b.workspace(hints)
+    append = capi.mfa_kv_append_slots_fp8 if fp8 else capi.mfa_kv_append_slots
+    attend = capi.mfa_decode_attention_prefix_fp8 if fp8 else capi.mfa_decode_attention_prefix
+
+    def take(most):
+        capi.mfa_reserve_pages(new, lens, table, free, n_free, B, cols, num_pages, most, starts, slots, lens, n_free, b.ws)
+        append(fused, fused[:, DIM:], 2 * DIM, 2 * DIM, slots, most, *kv, *scales, num_pages, b.ws)
+
+    def step():
+        take(rows)
+        attend(b.q, *kv, *scales, table, lens, b.d["starts"], b.d["pages"], 2, b.out, b.lse, SCALE, B, cols, num_pages,
+               *hints, b.ws, b.ws.numel())
+
+    # the prompts, for the first request of each group, and then shared with the others
+    prompt = torch.randn((5 * PAGE, 2 * DIM)).bfloat16()
+    new.copy_(torch.tensor([3 * PAGE, 0, 0, 2 * PAGE, 0, 0, 0]))
+    fused.copy_(prompt)
+    take(5 * PAGE)
+    for g, first in enumerate((0, 3)):
+        table[first:first + sizes[g], :pages[g]] = table[first, :pages[g]].clone()
+    lens.copy_(keep * PAGE)
+    held = [prompt[:3 * PAGE]] * 3 + [prompt[3 * PAGE:]] * 4
+    new.zero_()
+    torch.cuda.synchronize()
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+    rng = np.random.default_rng(3)
+    for turn in range(6):
+        count = rng.integers(0, 25, B)
+        now = torch.randn((5 * PAGE, 2 * DIM)).bfloat16()
+        with torch.cuda.stream(stream):
+            new.copy_(torch.from_numpy(count))
+            fused.copy_(now)
+            graph.replay()
+        stream.synchronize()
+        capi.mfa_check_device_errors(b.ws)
+        at = np.concatenate([[0], np.cumsum(count)])
+        held = [torch.cat([h, now[at[i]:at[i + 1]]]) for i, h in enumerate(held)]
+        assert lens.tolist() == [len(h) for h in held]
+        b.cache, b.scales, b.table, b.lens = kv, scales, table.cpu().numpy(), lens.cpu().numpy()
+        for i, h in enumerate(held):
+            pg = table[i, :-(-len(h) // PAGE)].long()
+            for c, (x, cache) in enumerate(zip((h[:, :DIM], h[:, DIM:]), kv)):
+                got = cache[pg].reshape(-1, DIM)[:len(h)]
+                if fp8:  # codes as tests of the append pin them; here: within half a step of E4M3 of the row's largest
+                    s = scales[c][pg].reshape(-1)[:len(h), None]
+                    x = x.float().cuda()
+                    top = x.abs().amax(1, keepdim=True)
+                    assert ((got.view(torch.float8_e4m3fn).float() * s - x).abs() <= 2 ** -4 * 1.01 * top).all()
+                else:
+                    assert torch.equal(got.cpu(), x)
+        b.check()
+        if turn == 3:  # two requests end and new ones take their places, behind the same prompts
+            done.zero_()
+            done[[1, 5]] = 1
+            own = [-(-len(held[i]) // PAGE) - int(keep[i]) for i in (1, 5)]
+            left = int(n_free.item())
+            with torch.cuda.stream(stream):
+                capi.mfa_release_pages(done, keep, lens, table, free, n_free, B, cols, num_pages, lens, n_free, b.ws)
+            stream.synchronize()
+            assert int(n_free.item()) == left + sum(own)
+            for i in (1, 5):
+                held[i] = held[i][:int(keep[i]) * PAGE]
+    with torch.cuda.stream(stream):  # all end; the first of each group gives the prompt back as well
+        done.fill_(1)
+        keep[0] = keep[3] = 0
+        capi.mfa_release_pages(done, keep, lens, table, free, n_free, B, cols, num_pages, lens, n_free, b.ws)
+    stream.synchronize()
+    capi.mfa_check_device_errors(b.ws)
+    assert int(n_free.item()) == num_pages and sorted(free.tolist()) == list(range(num_pages))
