@@ -668,14 +668,16 @@ __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint3
 
 // E4M3: V of a unit as P V reads it, f16 of code * scale * 2^-e (at most 448, e of the page; off by 2^-11 for the scale and
 // 2^-11 for the product), from the codes: per page [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both
-// with the 128-byte swizzle. Thread t takes 16 codes of row t / 8 and of every 16th row after it; rows behind the last
-// token become zeros. That the scales are applied here spares the softmax threads 64 values each from shared memory,
+// with the 128-byte swizzle. A thread takes 16 codes of a row and of every 16th row after it; rows behind the last token
+// become zeros. Eight neighbouring threads take half of rows r and r ^ 5, whose swizzles differ in the bits that keep
+// both the codes they read and the values they write on banks of their own. That the scales are applied here spares the softmax threads 64 values each from shared memory,
 // whose bandwidth the MMAs need.
 __device__ void convert_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi,
                              const uint8_t* gbase) {
   using Sm = Smem<true>;
   const int lane = threadIdx.x & 31, t = threadIdx.x - 32 * kTailWarp;
-  const int row0 = t >> 3, c = t & 7;  // 16-code chunk: dims [16 c, 16 c + 16)
+  const int row0 = (2 * (t >> 4)) ^ (t & 4 ? 5 : 0);
+  const int c = (t & 3) | ((t >> 1) & 4);  // 16-code chunk: dims [16 c, 16 c + 16)
   const uint32_t from = row0 * 128 + ((c ^ (row0 & 7)) << 4);  // rows 16 apart share the swizzle
   const uint32_t to = (c >> 2) * 8192 + row0 * 128;
   const uint32_t to0 = to + (((2 * (c & 3)) ^ (row0 & 7)) << 4), to1 = to + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4);
