@@ -1051,10 +1051,11 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       const uint32_t buf = cnt & 1, ts = tmem + lanes + buf * kSCols;
       const uint32_t sc_slot = cnt % kScaleSlots;
       const float* sc = reinterpret_cast<const float*>(gbase + Smem<kFp8>::scales + sc_slot * kScaleBytes);
+      const int cols = seen(2 * u + half);  // this thread's keys
       if (kFp8) wait(ScFull + sc_slot, (cnt / kScaleSlots) & 1);
+      const int e = kFp8 ? page_exponent(sc + kUnitKeys + 64 * half, cols, lane) : 0;
       wait(SFull + buf, (cnt >> 1) & 1);
       tc_fence_after();
-      const int cols = seen(2 * u + half);  // this thread's keys
       if (cols + seen(2 * u + (half ^ 1)) > 0) {
         // This thread's products, 32 keys at a time. P of 32 keys replaces the first 16 columns of their S.
         float2 x[16];
@@ -1071,7 +1072,6 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             }
           }
         };
-        const int e = kFp8 ? page_exponent(sc + kUnitKeys + 64 * half, cols, lane) : 0;
         const float lift = (float)e;
         uint32_t w[32];
         float2 sum;
