@@ -210,8 +210,9 @@ mfa_status_t mfa_release_pages(const int32_t* finished, const int32_t* keep_page
  *   slot_map: [device] int64 [n_rows], as mfa_reserve_pages writes it.
  * mfa_kv_append_slots_fp8 quantises each row as mfa_kv_append_fp8 does (the
  * same codes and scales). workspace: any workspace (only its error word is
- * used). Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers,
- * n_rows < 0, num_pages < 1, bad strides), MFA_ERR_WORKSPACE. */
+ * used), so calls may share it with any other. Host errors: MFA_ERR_INVALID_ARG
+ * (null or misaligned pointers, n_rows < 0, num_pages < 1, bad strides),
+ * MFA_ERR_WORKSPACE. */
 mfa_status_t mfa_kv_append_slots(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
                                  const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache,
                                  int num_pages, void* workspace, void* stream);
@@ -318,7 +319,8 @@ mfa_status_t mfa_query_lowrank(const void* x, const void* w_down, const void* ga
 /* Decode attention for a batch whose sequences share prefixes (bf16 cache): the
  * attention of mfa_decode_attention, with the same inputs, outputs and values,
  * in which the pages that the sequences of a group have in common are read once
- * for the group, as one matrix product over all its queries.
+ * for every four of its sequences, as one matrix product over their queries. No
+ * page of one sequence, whatever it holds, reaches the result of another.
  *   group_starts: [device] int32 [n_groups + 1], non-decreasing: group g is the
  *                 sequences group_starts[g] .. group_starts[g + 1] - 1. Sequences
  *                 in no group have no shared prefix.
@@ -350,10 +352,11 @@ mfa_status_t mfa_decode_attention_prefix(const void* q, const void* k_cache, con
 
 /* The same over an E4M3 cache with per-token fp32 scales (k_scale, v_scale
  * [num_pages][64], [device], 16-byte aligned): the attention of
- * mfa_decode_attention_fp8. Over the prefix, q enters the 8-bit products as two
- * E4M3 terms under a power of two per head, and the weights times the V scales
- * as two E4M3 terms (about 2^-8 relative). Everything else as
- * mfa_decode_attention_prefix. */
+ * mfa_decode_attention_fp8. q enters the 8-bit products with the raw K codes as
+ * two E4M3 terms under a power of two per head (2^-18.8 of its largest value);
+ * the weights and V's codes times their scales enter the second product as f16
+ * (2^-11 each, and 2^-11 for the scale; V's relative to the largest scale of
+ * its page). Everything else as mfa_decode_attention_prefix. */
 mfa_status_t mfa_decode_attention_prefix_fp8(const void* q, const void* k_cache, const void* v_cache,
                                              const float* k_scale, const float* v_scale,
                                              const int32_t* page_table, const int32_t* seq_lens,

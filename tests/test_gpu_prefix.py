@@ -540,3 +540,76 @@ def test_serving_steps_over_a_shared_prefix(fp8):
     stream.synchronize()
     capi.mfa_check_device_errors(b.ws)
     assert int(n_free.item()) == num_pages and sorted(free.tolist()) == list(range(num_pages))
+
+
+@KV
+def test_as_many_groups_as_sequences_and_empty_groups(fp8):
+    """1024 groups of one share nothing, whatever their counts of pages; groups without a sequence change nothing."""
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 200, 1024)
+    b = Batch([1] * 1024, rng.integers(0, 4, 1024), lens, fp8, seed=19)
+    b.call()
+    b.check(which=range(0, 1024, 11))
+    starts = [0, 0, 5, 5, 5, 9, 12, 12]
+    pages = [7, 3, 9, 0, 4, 2, 1]
+    lens = np.concatenate([np.full(5, 3 * PAGE + 10), np.full(4, 4 * PAGE + 70), np.full(3, 2 * PAGE), [100]])
+    Batch(None, pages, lens, fp8, seed=20, starts=starts, spare_cols=9).run()  # counts of pages within the table rows
+
+
+@KV
+def test_lengths_out_of_range_are_clamped_and_reported(fp8):
+    """A negative length is an empty sequence, one beyond its table row ends with the row; the others keep their values."""
+    b = Batch([5], [4], lens_of([5], [4], 100, 2), fp8, seed=21, spare_cols=0)
+    true = b.lens.copy()
+    full = b.table.shape[1] * PAGE
+    row = int(np.argmax(true))
+    other = (row + 1) % 5
+    b.d["lens"][other] = -5
+    b.call()
+    with pytest.raises(capi.MFAError) as e:
+        capi.mfa_check_device_errors(b.ws)
+    assert e.value.status == 6
+    b.lens[other] = 0
+    b.check()
+    b.lens = true
+    b.d["lens"].copy_(torch.from_numpy(true))
+    b.d["lens"][row] = 2 ** 31 - 1
+    for i, c in enumerate(b.cache):  # the rest of its last page counts then
+        last = int(b.table[row, -1])
+        c[last] = 0x38 if fp8 else 1.0
+        if fp8:
+            b.scales[i][last] = 1.0
+    b.call()
+    with pytest.raises(capi.MFAError) as e:
+        capi.mfa_check_device_errors(b.ws)
+    assert e.value.status == 6
+    b.lens = true.copy()
+    b.lens[row] = full
+    b.check()
+
+
+@KV
+def test_pages_at_the_far_end_of_a_large_cache(fp8):
+    """Pages whose rows lie past 2^31 elements: rows appended by slot are where the attention reads them."""
+    num_pages, n, own = 131072 + 40, 4, 70
+    sizes, pages = [n], [3]
+    b = Batch(sizes, pages, np.full(n, 3 * PAGE + own), fp8, seed=22)
+    far = torch.arange(num_pages - b.num_pages, num_pages, device="cuda")
+    kv = [torch.empty((num_pages, PAGE, DIM), dtype=c.dtype, device="cuda") for c in b.cache]
+    scales = [torch.empty((num_pages, PAGE), device="cuda") for _ in b.scales]
+    for big, c in zip(kv + scales, b.cache + b.scales):
+        big[far] = c
+    b.table = np.where(b.table >= 0, b.table + num_pages - b.num_pages, -1).astype(np.int32)
+    b.d["table"].copy_(torch.from_numpy(b.table))
+    b.cache, b.scales, b.num_pages = kv, scales, num_pages
+    b.run()
+    # one more token for each, behind its last
+    rows = torch.randn((n, DIM), device="cuda").bfloat16()
+    slots = torch.tensor([int(b.table[i, b.lens[i] // PAGE]) * PAGE + int(b.lens[i]) % PAGE for i in range(n)], device="cuda")
+    append = capi.mfa_kv_append_slots_fp8 if fp8 else capi.mfa_kv_append_slots
+    append(rows, rows, DIM, DIM, slots, n, *kv, *scales, num_pages, b.ws)
+    b.lens = b.lens + 1
+    b.d["lens"].copy_(torch.from_numpy(b.lens))
+    b.run()
+    if not fp8:
+        assert torch.equal(kv[0].view(-1, DIM)[slots], rows)
