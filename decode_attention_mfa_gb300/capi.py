@@ -106,9 +106,12 @@ def load():
 def _ptr(x):
     if x is None:
         return None
-    if isinstance(x, int):
-        return x
-    return x.data_ptr()
+    try:  # nearly always a tensor: looking for an address first costs a call of ten pointers 0.4 us
+        return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):
+            return x
+        raise
 
 
 def _stream(s):
