@@ -161,9 +161,8 @@ __device__ __forceinline__ uint32_t map_to_leader(uint32_t addr) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
   return r;
 }
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Arrival on a barrier of the pair's leader. What it announces is read by the MMAs alone, and lies in tensor memory,
 // which the tcgen05 fences order, or in this CTA's shared memory, which the proxy fence before it has made visible to
 // them, so no release at cluster scope is needed: that one takes 1500 cycles, most of a unit's time.
@@ -284,7 +283,8 @@ __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPageSize
 // ends with a barrier.
 __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, uint32_t* err) {
   const int n = p.n_groups, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kThreads = blockDim.x;
-  for (int g = threadIdx.x; g < n; g += kThreads) {
+  // (by other warps than the lengths, so that neither waits for the other's loads)
+  for (int g = (threadIdx.x + kThreads - 128) % kThreads; g < n; g += kThreads) {
     int pages = __ldcg(p.prefix_pages + g);
     if (pages < 0 || pages > p.max_pages) {
       raise_error(err, MFA_DEVERR_CAPACITY);
@@ -379,6 +379,18 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, u
   __syncthreads();
 }
 
+// a b / c, in 32 bits where the product allows it.
+__device__ __forceinline__ int share(uint32_t a, uint32_t b, uint32_t c) {
+  const unsigned long long x = (unsigned long long)a * b;
+  return (x >> 32) ? (int)(x / c) : (int)((uint32_t)x / c);
+}
+// First unit of pair w's range of the line of C units, of W pairs; and the pair whose range holds unit x.
+__device__ __forceinline__ int range_of_pair(int w, int C, int W) { return share(w, C, W); }
+__device__ __forceinline__ int pair_of_unit(int x, int C, int W) {
+  const unsigned long long y = ((unsigned long long)x + 1) * W - 1;
+  return (y >> 32) ? (int)(y / (uint32_t)C) : (int)((uint32_t)y / (uint32_t)C);
+}
+
 // Pairs that have work: with fewer units than pairs, every range holds one.
 __device__ __forceinline__ int busy_pairs(const PrefixParams& p, int units) { return min(p.pairs, max(units, 1)); }
 
@@ -391,7 +403,7 @@ __device__ void publish_plan(const PrefixParams& p, const PlanSmem& s, int pair,
     int c = prefix;
     for (int i = s.first[t]; i < b; ++i) c += pages_of(own_tokens(s, i, prefix));
     const int own = pages_of(own_tokens(s, b, prefix));
-    auto pair_of = [&](int page) { return cta_of_cost((long long)s.cost[t] + kPrefixPieceUnits + page / 2, C, W); };
+    auto pair_of = [&](int page) { return pair_of_unit(s.cost[t] + kPrefixPieceUnits + page / 2, C, W); };
     auto row = [&](int w) { return (w + t) * kSeqs + j; };
     int4 parts = make_int4(0, 0, 0, 0);
     int w = -1;  // the last pair so far
@@ -1230,6 +1242,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
     prefetch_tensormap(&vmap);
     prefetch_tensormap(&qmap);
   }
+  __syncwarp();
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + Sm::misc),
                  "n"(kTmemCols)
@@ -1237,6 +1250,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
     tc_fence_before();
   }
+  __syncwarp();
+  cluster_arrive();  // this CTA's barriers are initialised, its tensor memory is its own
   // hints only, these may still be written: what the plan, the first loads and Q need, in L2
   {
     auto hint = [](const void* at) { asm volatile("prefetch.global.L2 [%0];" ::"l"(at)); };
@@ -1252,11 +1267,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
   pdl_wait_prior_grid();
   pdl_launch_dependents();
   build_plan(p, plan, *reinterpret_cast<PlanScratch*>(gbase + Sm::k), blockIdx.x == 0 ? p.err : nullptr);
-  cluster_sync();  // the other CTA's barriers are initialised, its scratch is done with
+  cluster_wait();  // as are the other's; what it does to its own shared memory until its loads begin concerns no one else
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const int units = plan.cost[plan.tiles], W = busy_pairs(p, units), pair = blockIdx.x >> 1;
-  const int lo = pair < W ? (int)cta_cost_lo(pair, units, W) : 0, hi = pair < W ? (int)cta_cost_lo(pair + 1, units, W) : 0;
+  const int lo = pair < W ? range_of_pair(pair, units, W) : 0, hi = pair < W ? range_of_pair(pair + 1, units, W) : 0;
 
   if (warp < kSoftmaxWarps) {
     softmax_role<kFp8>(p, cx, plan, pair, lo, hi, tmem, gbase);
@@ -1279,7 +1294,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFp8>(), 1)
   }
   __syncwarp();
   tc_fence_before();
-  cluster_sync();  // no copy, MMA or arrival for either CTA is left
+  cluster_arrive();
+  cluster_wait();  // no copy, MMA or arrival for either CTA is left
   tc_fence_after();
   if (warp == kMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
