@@ -231,7 +231,8 @@ __device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
 }
 
 // True in one thread of a converged warp. The compiler knows that it is one, and then issues a tcgen05 instruction behind
-// it without a loop over the threads that might be active (80 cycles an MMA, of which a unit has 24 or 32).
+// it, or a TMA copy, without a loop over the threads that might be active (80 cycles an MMA, of which a unit has 32; the
+// eight copies of a Q took 0.6 us).
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
@@ -519,7 +520,7 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
     const uint32_t slot = n & 1;
     if (n >= 2 && !cx.wait_warp(SFull + slot, ((n >> 1) & 1) ^ 1)) return false;
     const int page = r == 0 ? pa : pb;
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t dst = cx.base + Sm::k + slot * kSlot, bar = cx.leader_bar(KFull + slot);
       if (r == 0) mbar_arrive_expect_tx(cx.bar(KFull + slot), pb >= 0 ? 2 * kSlot : kSlot);
       if (page >= 0)
@@ -530,7 +531,7 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
     if constexpr (kFp8) {  // the scales of all the unit's keys, for this CTA's rows
       const uint32_t sc_slot = n % kScaleSlots;
       if (!cx.wait_warp(ScEmpty + sc_slot, ((n / kScaleSlots) & 1) ^ 1)) return false;
-      if (lane == 0) {
+      if (elect_one()) {
         const uint32_t sc = cx.base + Sm::scales + sc_slot * kScaleBytes, sb = cx.bar(ScFull + sc_slot);
         constexpr uint32_t kPageScales = kPageSize * sizeof(float);
         mbar_arrive_expect_tx(sb, (pb >= 0 ? 4 : 2) * kPageScales);
@@ -562,11 +563,13 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
       if (lane == 0 && tail) mbar_arrive_expect_tx(bar, bytes);
       tails[slot] += tail;
     }
-    if (lane == 0)
-      for (int i = 0; i < (pb >= 0 ? 2 : 1); ++i)
+    if (elect_one())
 #pragma unroll
-        for (int d = 0; d < 128 / kCols; ++d)
-          tma_load_2d_pair(dst + i * kPage + d * 8192, vmap, r * 128 + d * kCols, (i ? pb : pa) * kPageSize, bar, pol);
+      for (int i = 0; i < 2; ++i)
+        if (i == 0 || pb >= 0)
+#pragma unroll
+          for (int d = 0; d < 128 / kCols; ++d)
+            tma_load_2d_pair(dst + i * kPage + d * 8192, vmap, r * 128 + d * kCols, (i ? pb : pa) * kPageSize, bar, pol);
     return true;
   };
   Piece q;
@@ -579,16 +582,19 @@ __device__ void producer_role(const PrefixParams& p, const CUtensorMap* kmap, co
     // Q may be replaced once S of every unit so far is done
     good = cnt == 0 || cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1);
     if (!good) break;
-    if (lane == 0) {
+    if (elect_one()) {
       const int here = min(2, max(0, q.seqs - 2 * r));  // this CTA's sequences
       if (kFp8)
         mbar_arrive_expect_tx(cx.bar(QFull), here * kSeqQBytes);
       else if (r == 0)
         mbar_arrive_expect_tx(cx.bar(QFull), q.seqs * kSeqQBytes);
       const uint32_t bar = kFp8 ? cx.bar(QFull) : cx.leader_bar(QFull);
+#pragma unroll
       for (int d = 0; d < 4; ++d)
-        for (int h = 0; h < here; ++h)
-          tma_load_2d_pair(cx.base + Sm::q + d * 16384 + h * 8192, qmap, d * 64, (q.b + 2 * r + h) * kHeads, bar, pol_shared);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (h < here)
+            tma_load_2d_pair(cx.base + Sm::q + d * 16384 + h * 8192, qmap, d * 64, (q.b + 2 * r + h) * kHeads, bar, pol_shared);
     }
     ++pieces;
     TilePages ids;
