@@ -132,7 +132,11 @@ constexpr uint32_t kBehind = 0x80000000u;  // b sees its tile's prefix, its own 
 struct PlanScratch {
   int32_t count[kMaxBatch], lead[kMaxBatch], pages[kMaxBatch], group[kMaxBatch];
   uint16_t b0[kMaxBatch + 2];
+  int32_t start[kMaxBatch];
+  int32_t last[kMaxBatch / 32], units[kMaxBatch / 32];  // of 32 sequences, of 32 row tiles
+  uint32_t begins[kMaxBatch / 32];
 };
+static_assert(kMaxBatch <= 32 * 32, "a lane for each 32 of the batch");
 
 template <bool kFp8>
 struct Smem {
@@ -331,50 +335,72 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, u
     t.group[b] = of;
   }
   __syncthreads();
-  if (warp == 0) {
-    // tiles begin every four sequences from where the shared group (or the run without one) begins
-    auto key = [&](int b) { return b >= 0 && t.group[b] >= 0 && t.count[t.group[b]] >= 2 ? t.group[b] : -1; };
-    int tiles = 0, run = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const int b = b0 + lane, g = b < p.B ? key(b) : -1;
-      int start = b < p.B && (b == 0 || key(b - 1) != g) ? b : 0;
+  // tiles begin every four sequences from where the shared group (or the run without one) begins
+  auto key = [&](int b) { return b >= 0 && t.group[b] >= 0 && t.count[t.group[b]] >= 2 ? t.group[b] : -1; };
+  // A warp takes 32 sequences, or 32 tiles, at a time; what it needs of those before is read by a lane for each 32.
+  const int chunks = (p.B + 31) / 32, warps = kThreads / 32;
+#pragma unroll 1
+  for (int c = warp; c < chunks; c += warps) {
+    const int b = 32 * c + lane;
+    int x = b < p.B && (b == 0 || key(b - 1) != key(b)) ? b : -1;  // where the run begins, if within these 32
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, start, o);
-        if (lane >= o) start = max(start, y);
-      }
-      start = max(start, run);
-      const bool begins = b < p.B && (b - start) % kSeqs == 0;
-      const uint32_t all = __ballot_sync(0xffffffffu, begins);
-      if (begins) {
-        const int i = tiles + __popc(all & ((1u << lane) - 1));
-        s.first[i] = (uint16_t)b;
-        s.pages[i] = g >= 0 ? t.pages[g] : 0;
-        s.lead[i] = g >= 0 ? (uint16_t)t.lead[g] : 0;
-      }
-      if (b < p.B && g < 0) s.len[b] &= ~kBehind;
-      tiles += __popc(all);
-      run = __shfl_sync(0xffffffffu, start, 31);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = max(x, y);
     }
-    if (lane == 0) {
-      s.first[tiles] = (uint16_t)p.B;
-      s.tiles = tiles;
+    t.start[b] = x;
+    if (lane == 31) t.last[c] = x;
+  }
+  if (chunks > 1) __syncthreads(); else __syncwarp();
+#pragma unroll 1
+  for (int c = warp; c < chunks; c += warps) {
+    const int b = 32 * c + lane;
+    const int from = max(t.start[b], __reduce_max_sync(0xffffffffu, lane < c ? t.last[lane] : -1));
+    const uint32_t begins = __ballot_sync(0xffffffffu, b < p.B && (b - from) % kSeqs == 0);
+    if (lane == 0) t.begins[c] = begins;
+  }
+  if (chunks > 1) __syncthreads(); else __syncwarp();
+#pragma unroll 1
+  for (int c = warp; c < chunks; c += warps) {
+    const int b = 32 * c + lane, g = b < p.B ? key(b) : -1;
+    const uint32_t begins = t.begins[c];
+    const int before = __reduce_add_sync(0xffffffffu, lane < c ? __popc(t.begins[lane]) : 0);
+    if ((begins >> lane) & 1) {
+      const int i = before + __popc(begins & ((1u << lane) - 1));
+      s.first[i] = (uint16_t)b;
+      s.pages[i] = g >= 0 ? t.pages[g] : 0;
+      s.lead[i] = g >= 0 ? (uint16_t)t.lead[g] : 0;
     }
-    __syncwarp();
-    int units = 0;
-    for (int t0 = 0; t0 < tiles; t0 += 32) {
-      const int i = t0 + lane;
-      int u = 0;
-      if (i < tiles) {
-        int pages = s.pages[i];
-        for (int b = s.first[i]; b < s.first[i + 1]; ++b) pages += pages_of(own_tokens(s, b, s.pages[i]));
-        u = pages ? (pages + 1) / 2 + kPrefixPieceUnits : 0;
-      }
-      const int x = warp_inclusive_sum(u, lane);
-      if (i < tiles) s.cost[i] = units + x - u;
-      units += __shfl_sync(0xffffffffu, x, 31);
+    if (b < p.B && g < 0) s.len[b] &= ~kBehind;
+    if (b == p.B - 1) {
+      s.tiles = before + __popc(begins);
+      s.first[before + __popc(begins)] = (uint16_t)p.B;
     }
-    if (lane == 0) s.cost[tiles] = units;
+  }
+  if (chunks > 1) __syncthreads(); else __syncwarp();
+  const int tiles = chunks > 1 || warp == 0 ? s.tiles : 0;
+#pragma unroll 1
+  for (int c = warp; 32 * c < tiles; c += warps) {
+    const int i = 32 * c + lane;
+    int u = 0;
+    if (i < tiles) {
+      int pages = s.pages[i];
+      for (int b = s.first[i]; b < s.first[i + 1]; ++b) pages += pages_of(own_tokens(s, b, s.pages[i]));
+      u = pages ? (pages + 1) / 2 + kPrefixPieceUnits : 0;
+    }
+    const int x = warp_inclusive_sum(u, lane);
+    if (i < tiles) s.cost[i] = x - u;
+    if (i == tiles - 1) s.cost[tiles] = x;
+    if (lane == 31) t.units[c] = x;
+  }
+  if (tiles > 32) {
+    __syncthreads();
+#pragma unroll 1
+    for (int c = warp; 32 * c < tiles; c += warps) {
+      const int i = 32 * c + lane, before = __reduce_add_sync(0xffffffffu, lane < c ? t.units[lane] : 0);
+      if (i < tiles) s.cost[i] += before;
+      if (i == tiles - 1) s.cost[tiles] += before;
+    }
   }
   fence_proxy_async_smem();  // the scratch is TMA's from here on
   __syncthreads();
