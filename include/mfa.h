@@ -180,6 +180,8 @@ mfa_status_t mfa_kv_append_fp8(const void* k_new, const void* v_new, int n_new,
  * changed. A request with a bad length or a negative keep_pages[b], and one
  * whose pages do not fit into free_pages, is left as it is
  * (MFA_DEVERR_CAPACITY); a page id outside [0, num_pages) sets MFA_DEVERR_PAGE.
+ * Pages are not counted: one that two rows give back is on the stack twice, so
+ * of the requests that share a page, the last to end gives it back.
  *
  * workspace: [device] any workspace initialised by mfa_workspace_init (only its
  * 256-byte header is used); calls that share one must not overlap on the GPU.
@@ -203,7 +205,8 @@ mfa_status_t mfa_release_pages(const int32_t* finished, const int32_t* keep_page
  * slot_map[i] of the paged cache, i.e. row slot % 64 of page slot / 64. Lengths
  * are not touched. Rows with a negative slot are skipped (padding); a slot of
  * num_pages * 64 or more is skipped and sets MFA_DEVERR_PAGE. The slots are
- * distinct.
+ * distinct; of rows that name the same slot, what it holds afterwards is not
+ * defined.
  *   k_new, v_new: [device] bf16, 16-byte aligned; k_stride, v_stride: elements
  *     from one row to the next, multiples of 8, so that K and V may be columns
  *     of one projection's output;
