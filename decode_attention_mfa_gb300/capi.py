@@ -114,11 +114,18 @@ def _ptr(x):
         raise
 
 
+_raw_stream = _device = None
+
+
 def _stream(s):
+    global _raw_stream, _device
     if s is None:
-        import torch
         # the handle of torch.cuda.current_stream(), without the Stream object (3 us of a call that takes the GPU as long)
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _raw_stream is None:
+            import torch
+            torch.cuda.init()
+            _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return _raw_stream(_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
