@@ -1148,11 +1148,12 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           }
           sum = add2(sum, sum1);
         };
-        // the largest logit of this thread's keys (log2 units)
-        auto largest = [&]() -> float {
+        // the largest logit of this thread's first `end` keys (log2 units), or of more where these give none
+        auto largest = [&](int end) -> float {
           float top = -INFINITY;
 #pragma unroll 1
           for (int g = 0; g < 64; g += 32) {
+            if (g >= end && !__any_sync(0xffffffffu, top == -INFINITY)) break;
             load(g);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
@@ -1166,7 +1167,9 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
 #pragma unroll 1
         for (int tries = 0; tries < 2; ++tries) {
           if (move) {
-            const float big = largest() + (lift - moved_to<kFp8>());
+            // Half the keys are enough for a first reference, the sum tells if not (32 sequences behind 128 pages 26.0 ->
+            // 25.6 us; on an E4M3 cache 50.4 and 50.6, so not there).
+            const float big = largest(!kFp8 && tries == 0 ? 32 : 64) + (lift - moved_to<kFp8>());
             red[half * 128 + row] = big;
             barrier_rows(quad);
             const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));

@@ -461,6 +461,39 @@ def test_a_first_unit_of_infinite_logits_leaves_later_low_ones_whole(fp8):
 
 
 @KV
+@pytest.mark.parametrize("first,count", [(0, 32), (32, 32), (0, 63)])
+def test_infinite_logits_beside_low_ones_in_a_page(first, count, fp8):
+    """Keys of one page whose logits are -inf, the others' near -224 (as above); nothing else is there to set a reference."""
+    b = Batch([2], [1], np.full(2, PAGE), fp8, seed=23)
+    b.q.copy_(torch.sign(b.q.float()).bfloat16())
+    b.q[:, :, 0] = 1.0
+    b.q[:, :, 1] = 1024.0
+    page, off = int(b.table[0, 0]), slice(first, first + count)
+    if fp8:
+        b.scales[0].fill_(2 ** -7)
+        b.cache[0][:, :, 1] = 0xFE
+        b.cache[0][page, off] = 0
+        b.cache[0][page, off, 0] = 0xB8
+        b.scales[0][page, off] = float("inf")
+    else:
+        b.cache[0][:, :, 1] = -3.5
+        b.cache[0][page, off, 0] = float("-inf")
+    b.call()
+    capi.mfa_check_device_errors(b.ws)
+    rest = [i for i in range(PAGE) if not first <= i < first + count]
+    k, v = (c[page].view(torch.float8_e4m3fn).double() * x[page].double().unsqueeze(-1) if fp8 else c[page].double()
+            for c, x in zip(b.cache, b.scales or [None] * 2))
+    for i in range(2):
+        logits = b.q[i].double() @ k[rest].T * SCALE
+        lse = torch.logsumexp(logits, 1)
+        out = torch.exp(logits - lse[:, None]) @ v[rest]
+        err = 256 * 2 ** -15
+        assert float((b.lse[i].double() - lse).abs().max()) <= err
+        bound = (2 ** -8 * (2 if fp8 else 1) + 2 * err) * v.abs().max() + 2 ** -8 * out.abs()
+        assert ((b.out[i].double() - out).abs() <= bound).all()
+
+
+@KV
 def test_serving_steps_over_a_shared_prefix(fp8):
     """What a server does: a prompt is appended once, its pages are entered in the rows of all who share it, and then
     steps of reserve, append by slots and attention are replayed from one graph; requests end, keep the shared pages and
