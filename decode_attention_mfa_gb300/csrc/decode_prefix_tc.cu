@@ -720,8 +720,8 @@ __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint3
 // 2^-11 for the product), from the codes: per page [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both
 // with the 128-byte swizzle. A thread takes 16 codes of a row and of every 16th row after it; rows behind the last token
 // become zeros. Eight neighbouring threads take half of rows r and r ^ 5, whose swizzles differ in the bits that keep
-// both the codes they read and the values they write on banks of their own. That the scales are applied here spares the softmax threads 64 values each from shared memory,
-// whose bandwidth the MMAs need.
+// both the codes they read and the values they write on banks of their own. That the scales are applied here spares the
+// softmax threads 64 values each from shared memory, whose bandwidth the MMAs need.
 __device__ void convert_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi,
                              const uint8_t* gbase) {
   using Sm = Smem<true>;
