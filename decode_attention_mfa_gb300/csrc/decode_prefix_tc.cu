@@ -152,8 +152,8 @@ struct Smem {
   static constexpr uint32_t q = raw + (kFp8 ? 2 * slot_bytes<kFp8>() : 0);
   static constexpr uint32_t scales = q + kQBytes;
   static constexpr uint32_t plan = scales + (kFp8 ? kScaleSlots * kScaleBytes : 0);
-  static constexpr uint32_t red = (plan + (uint32_t)sizeof(PlanSmem) + 15) & ~15u;  // [2][128] exchange of the row halves
-  static constexpr uint32_t bars = red + 2 * 128 * 4;
+  static constexpr uint32_t red = (plan + (uint32_t)sizeof(PlanSmem) + 15) & ~15u;  // [4][128] exchange of the row halves
+  static constexpr uint32_t bars = red + 4 * 128 * 4;
   static constexpr uint32_t misc = bars + 8 * kBars;  // TMEM base, abort flag
   static constexpr uint32_t total = misc + 8;
 };
@@ -1069,7 +1069,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
   const uint32_t lanes = (uint32_t)(32 * quad) << 16;
-  const float c2 = p.scale * kLog2e;
+  const float c2 = p.scale == 0.0f && !kFp8 ? 1e-37f : p.scale * kLog2e;  // (0 times an infinity would be NaN)
   const uint32_t p_full = cx.leader_bar(PFull), o_free = cx.leader_bar(OFree);
   float* red = reinterpret_cast<float*>(gbase + Smem<kFp8>::red);
   uint32_t cnt = 0, pieces = 0;  // units, pieces so far
@@ -1093,6 +1093,9 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     bool fresh = true;              // no key so far
     bool open = true;               // a row of the warp has no finite reference
     float m = -INFINITY, l = 0.0f;  // the row's reference (log2 units), and this thread's share of its denominator
+    // The same of the weights as P holds them, by which O is divided: a weight that has most of the sum then cancels its
+    // rounding. (Of f16 weights the difference does not matter. The LSE takes the unrounded sum.)
+    float l_p = 0.0f;
     float mul = c2;                 // of the row's products: the softmax scale, and 2^-e of its Q terms
     if constexpr (kFp8) {
       wait(QFull, pieces & 1);
@@ -1138,16 +1141,35 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             tc_wait_ld();
           }
         };
+        // Products behind the last token become infinities that give weights of 0, so that one body of code does for whole
+        // and partial units: the first pass through it takes longer to fetch than to run. (E4M3: K's scales there may be
+        // anything, so the weights are masked themselves.)
+        if (!kFp8 && cols < 64) {
+          const float none = mul > 0.0f ? -INFINITY : INFINITY;
+#pragma unroll 1
+          for (int g = 0; g < 64; g += 32) {
+            if (g + 32 <= cols) continue;
+            load(g);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              if (g + 2 * c >= cols) x[c].x = none;
+              if (g + 2 * c + 1 >= cols) x[c].y = none;
+            }
+            tmem_st32(tx + g, reinterpret_cast<const float*>(x));
+          }
+          tc_wait_st();
+        }
         const float lift = (float)e;
         uint32_t w[32];
-        float2 sum;
-        // weights of this thread's keys, their sum, and P; kPart: only the first `cols` of the 64 count
+        float2 sum, sum_p;
+        // weights of this thread's keys, their sums, and P; kPart: only the first `cols` of the 64 count
         auto weights = [&](auto part) {
           constexpr bool kPart = decltype(part)::value;
           const float ref = m == -INFINITY ? 0.0f : m - lift;  // only infinite logits so far: weights of 0
           const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
           sum = make_float2(0.0f, 0.0f);
-          float2 sum1 = sum;
+          sum_p = sum;
+          float2 sum1 = sum, sum_p1 = sum;
 #pragma unroll
           for (int g = 0; g < 64; g += 32) {
             load(g);
@@ -1165,10 +1187,19 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
               else
                 sum = add2(sum, y);
               // the A operand is 16 bits, half a step of each weight: 2^-8 (bf16), 2^-11 (f16)
-              w[g / 2 + c] = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+              const uint32_t both = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+              w[g / 2 + c] = both;
+              if constexpr (!kFp8) {
+                const float2 rounded = make_float2(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u));
+                if (c & 1)
+                  sum_p1 = add2(sum_p1, rounded);
+                else
+                  sum_p = add2(sum_p, rounded);
+              }
             }
           }
           sum = add2(sum, sum1);
+          sum_p = add2(sum_p, sum_p1);
         };
         // the largest logit of this thread's first `end` keys (log2 units), or of more where these give none
         auto largest = [&](int end) -> float {
@@ -1179,8 +1210,8 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             load(g);
 #pragma unroll
             for (int c = 0; c < 16; ++c) {
-              if (g + 2 * c < cols) top = fmaxf(top, x[c].x * mul);
-              if (g + 2 * c + 1 < cols) top = fmaxf(top, x[c].y * mul);
+              if (!kFp8 || g + 2 * c < cols) top = fmaxf(top, x[c].x * mul);
+              if (!kFp8 || g + 2 * c + 1 < cols) top = fmaxf(top, x[c].y * mul);
             }
           }
           return top;
@@ -1199,6 +1230,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             m = m_new;
             open = __any_sync(0xffffffffu, m == -INFINITY);  // the same in both warps of the rows
             l *= alpha;
+            l_p *= alpha;
             if (!fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
               // O holds the units before this one; each of the two warps scales half of its columns
               wait_pv();
@@ -1214,7 +1246,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
               }
             }
           }
-          if (cols >= 64)
+          if (!kFp8 || cols >= 64)
             weights(std::false_type{});
           else
             weights(std::true_type{});
@@ -1223,6 +1255,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
         }
         fresh = false;
         l += (sum.x + sum.y) * (kFp8 ? exp2_int(-e) : 1.0f);
+        l_p += sum_p.x + sum_p.y;
         tmem_st16(tx, reinterpret_cast<const float*>(w));
         tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
         tc_wait_st();
@@ -1239,10 +1272,12 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     tc_fence_after();
     if (!fresh) {
       red[half * 128 + row] = l;
+      if (!kFp8) red[256 + half * 128 + row] = l_p;
       barrier_rows(quad);
       l += red[(half ^ 1) * 128 + row];
+      if (!kFp8) l_p += red[256 + (half ^ 1) * 128 + row];
       const size_t at = ((size_t)(pair + q.t) * kSeqs + j) * kHeads + (row & 63);
-      const float inv = 1.0f / l;
+      const float inv = 1.0f / (kFp8 ? l : l_p);
       float* dst = p.part_o + (at - (lane & 3)) * kHeadDim + 8 * (lane & 3);
 #pragma unroll 1
       for (int c = 128 * half; c < 128 * half + 128; c += 32) {
