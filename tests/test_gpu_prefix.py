@@ -1,8 +1,9 @@
 """Shared-prefix decode attention (mfa_decode_attention_prefix*) against the definition in 64 bits.
 
 Tolerances, from the roundings on the way: each weight enters the second product as bf16, off by at most 2^-8 of
-itself, so an output is off by at most 2^-8 of the weighted mean of |v|, which is at most the largest |v|; the output is
-rounded to bf16, off by at most 2^-8 of itself; the fp32 sums of 256 products and the exponentials add less than 2^-12 of
+itself, and O is divided by the sum of what entered, so an output is off by at most 2^-8 of the weighted mean of
+|v - out|, which is at most (t^2 - out^2) / t with t the largest |v|, below t; the output is rounded to bf16, off by at
+most 2^-8 of itself; the fp32 sums of 256 products and the exponentials add less than 2^-12 of
 either. On an E4M3 cache the weights and the scaled values are f16 (2^-11 each, and 2^-11 for the scale) and the queries
 are held to 2^-18.8 of the largest: together no more than another 2^-8 of the largest |v|. The LSE is off by the logits' fp32 sums, 2^-15 of
 scale * sum |q k| (about 10 here), below 1e-3."""
