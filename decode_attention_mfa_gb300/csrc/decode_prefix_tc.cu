@@ -512,7 +512,7 @@ struct TilePages {
     const int c = o == 0 ? q.c[0] : o == 1 ? q.c[1] : o == 2 ? q.c[2] : q.c[3];
     const int seq = o == kSeqs ? s.lead[q.t] : q.b + o;
     const int at = o == kSeqs ? k : k - c + (((q.behind >> o) & 1) ? q.c[0] : 0);
-    return __ldg(p.page_table + (size_t)seq * p.max_pages + at);
+    return __ldcg(p.page_table + (size_t)seq * p.max_pages + at);
   }
   __device__ int checked(int id, const PrefixParams& p) const {
     if (id >= 0 && id < p.num_pages) return id;

@@ -305,7 +305,7 @@ struct PageIds {
   __device__ int fetch(int pg, const DecodeParams& p) const {
     int id = 0;
     if (pg < pg1) {
-      id = __ldg(row + pg);
+      id = __ldcg(row + pg);
       if (id < 0 || id >= p.num_pages) {
         raise_error(p.err, MFA_DEVERR_PAGE);
         id = 0;
@@ -353,7 +353,7 @@ struct BlockRows {
   int nb, cur, nvb;     // selected blocks, block of the last token, virtual blocks
   int vb0;              // first virtual block of the piece
   __device__ void start(const Seg& s, const DecodeParams& p) {
-    const int len = clamp_len(__ldg(p.seq_lens + s.b), p.max_pages * kPageSize, nullptr);
+    const int len = clamp_len(__ldcg(p.seq_lens + s.b), p.max_pages * kPageSize, nullptr);
     nb = selected_blocks(len, p.n_blocks, s.b, p.max_blocks, nullptr);  // errors: recorded by the prefix
     cur = (len - 1) >> 3;
     nvb = len > 0 ? nb + 1 : 0;
@@ -365,7 +365,7 @@ struct BlockRows {
   // step 1 for tile t: the block id (a load for a selected block)
   __device__ int block_id(int t, int lane) const {
     const int i = vb0 + 16 * t + lane;
-    return has(t, lane) ? (i < nb ? __ldg(bidx + i) : cur) : 0;
+    return has(t, lane) ? (i < nb ? __ldcg(bidx + i) : cur) : 0;
   }
   // step 2: the block's first position (returned in pos, -1 without a block) and a load of its page id
   __device__ int page_id(int t, int lane, int r, int& pos, const DecodeParams& p) const {
@@ -378,7 +378,7 @@ struct BlockRows {
       r = 0;
     }
     pos = 8 * r;
-    return __ldg(prow + (pos >> 6));
+    return __ldcg(prow + (pos >> 6));
   }
   // step 3: the cache row (page id * 64 + row in the page), -1 without a block
   __device__ int row(int id, int pos, const DecodeParams& p) const {
@@ -791,7 +791,7 @@ __device__ void vref_role(const DecodeParams& p, const Ctx& cx, const int* s_cos
       // block gather: the piece's virtual blocks [8 pg0, 8 pg1) -- the selected blocks, then the block of the
       // last token -- four a lane per round (block id, page id, then its 8 scales); a bad block or page id
       // (reported by the producer) is read as block 0 / page 0, as the producer reads it
-      const int len = clamp_len(__ldg(p.seq_lens + s.b), p.max_pages * kPageSize, nullptr);
+      const int len = clamp_len(__ldcg(p.seq_lens + s.b), p.max_pages * kPageSize, nullptr);
       const int nb = selected_blocks(len, p.n_blocks, s.b, p.max_blocks, nullptr);
       const int cur = (len - 1) >> 3, nvb = len > 0 ? nb + 1 : 0;
       const int vb_hi = min(8 * s.pg1, nvb);
@@ -801,12 +801,12 @@ __device__ void vref_role(const DecodeParams& p, const Ctx& cx, const int* s_cos
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int vb = vb0 + 32 * u + lane;
-          r[u] = vb < vb_hi ? (vb < nb ? __ldg(bidx + vb) : cur) : -1;
+          r[u] = vb < vb_hi ? (vb < nb ? __ldcg(bidx + vb) : cur) : -1;
           if (vb < nb && (r[u] < 0 || r[u] >= cur)) r[u] = 0;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          id[u] = r[u] >= 0 ? __ldg(row + ((8 * r[u]) >> 6)) : 0;
+          id[u] = r[u] >= 0 ? __ldcg(row + ((8 * r[u]) >> 6)) : 0;
           if (id[u] < 0 || id[u] >= p.num_pages) id[u] = 0;
         }
 #pragma unroll
@@ -815,7 +815,7 @@ __device__ void vref_role(const DecodeParams& p, const Ctx& cx, const int* s_cos
           const int vb = vb0 + 32 * u + lane;
           const int cnt = vb < nb ? 8 : len - 8 * cur;  // rows of the block that hold tokens
           const float4* sc = reinterpret_cast<const float4*>(p.v_scale + (size_t)id[u] * kPageSize + ((8 * r[u]) & 63));
-          const float4 a = __ldg(sc), b4 = __ldg(sc + 1);
+          const float4 a = __ldcg(sc), b4 = __ldcg(sc + 1);
           const float v8[8] = {a.x, a.y, a.z, a.w, b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
           for (int k = 0; k < 8; ++k)
@@ -826,13 +826,13 @@ __device__ void vref_role(const DecodeParams& p, const Ctx& cx, const int* s_cos
     for (int g = s.pg0; !kGather8 && g < s.pg1; g += 32) {
       const int pg = g + lane;
       if (pg < s.pg1) {
-        const int id = __ldg(row + pg);
+        const int id = __ldcg(row + pg);
         if (id >= 0 && id < p.num_pages) {  // a bad id is reported by the producer warps
           const int rows = min(kPageSize, s.len - pg * kPageSize);  // scales of unused rows are never read
           const float4* sc = reinterpret_cast<const float4*>(p.v_scale + (size_t)id * kPageSize);
           float4 v[16];
 #pragma unroll
-          for (int r4 = 0; r4 < 16; ++r4) v[r4] = (4 * r4 < rows) ? __ldg(sc + r4) : make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int r4 = 0; r4 < 16; ++r4) v[r4] = (4 * r4 < rows) ? __ldcg(sc + r4) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
           for (int r4 = 0; r4 < 16; ++r4) {
             if (4 * r4 + 0 < rows) mx = fmaxf(mx, v[r4].x);
@@ -1659,8 +1659,8 @@ __global__ void __launch_bounds__(Cfg<kFp8, kMtp>::kThreads)
     tc_fence_before();
   }
   if (threadIdx.x == 0) {
-    // the page table and Q are not written by the KV append: warm this CTA's
-    // share of both in L2 while the append finishes (the first page-id and Q
+    // hints only, into L2, where a later write meets them: warm this CTA's share
+    // of the page table and Q while the append finishes (the first page-id and Q
     // reads are otherwise two dependent HBM round trips at start)
     prefetch_l2_share(p.page_table, (size_t)p.B * p.max_pages * sizeof(int32_t), blockIdx.x, gridDim.x);
     prefetch_l2_share(p.q, (size_t)p.B * kHeads * kHeadDim * sizeof(uint16_t), blockIdx.x, gridDim.x);

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
   uint4 first_row = make_uint4(0u, 0u, 0u, 0u);
   if (first < 2 * p.n_new) {
     const uint16_t* src = ((first & 1) ? p.v_new : p.k_new) + ((size_t)b * p.n_new + (first >> 1)) * kHeadDim;
-    first_row = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+    first_row = __ldcg(reinterpret_cast<const uint4*>(src) + lane);
   }
   if (warp == 0) {
     const int start = p.seq_lens[b];
@@ -145,7 +145,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
                                                         : p.page_table[(size_t)b * p.max_pages + pg];
     const size_t slot = (size_t)page * kPageSize + (pos % kPageSize);
     const uint16_t* src = (is_v ? p.v_new : p.k_new) + ((size_t)b * p.n_new + t) * kHeadDim;
-    const uint4 row = (i == first) ? first_row : __ldg(reinterpret_cast<const uint4*>(src) + lane);
+    const uint4 row = (i == first) ? first_row : __ldcg(reinterpret_cast<const uint4*>(src) + lane);
     if (p.fmt == kKvE2M1) {
       uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot * (kHeadDim / 2);
       float* sc = (is_v ? p.v_scale : p.k_scale) + slot;
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_kernel(const App
     if (i < items) {
       slot[j] = __ldcg(reinterpret_cast<const long long*>(p.slot_map) + r);
       const uint16_t* src = (i & 1) ? p.v_new + r * p.v_stride : p.k_new + r * p.k_stride;
-      row[j] = __ldg(reinterpret_cast<const uint4*>(src) + lane);
+      row[j] = __ldcg(reinterpret_cast<const uint4*>(src) + lane);
     }
   }
 #pragma unroll

@@ -56,7 +56,7 @@ __device__ __forceinline__ int selected_blocks(int len, const int32_t* n_blocks,
                                                uint32_t* err) {
   if (len <= 0) return 0;
   const int lim = min((len - 1) >> 3, max_blocks);
-  const int nb = __ldg(n_blocks + b);
+  const int nb = __ldcg(n_blocks + b);
   if (nb < 0 || nb > lim) {
     raise_error(err, MFA_DEVERR_CAPACITY);
     return nb < 0 ? 0 : lim;
@@ -76,7 +76,7 @@ __device__ __forceinline__ void build_cost_prefix(const int32_t* __restrict__ se
                                                   int* s_cost, const int32_t* n_blocks = nullptr,
                                                   int max_blocks = 0) {
   for (int b = threadIdx.x; b < B; b += blockDim.x) {
-    const int len = clamp_len(__ldg(seq_lens + b), cap_tokens, err);
+    const int len = clamp_len(__ldcg(seq_lens + b), cap_tokens, err);
     s_len[b] = n_blocks ? virtual_len(len, selected_blocks(len, n_blocks, b, max_blocks, err)) : len;
   }
   __syncthreads();
@@ -124,6 +124,10 @@ __device__ __forceinline__ int seq_of_cost(const int* s_cost, int B, long long x
 // serialisation: a kernel lets the next one be scheduled early
 // (launch_dependents) and the next one runs its prologue, then waits for the
 // previous grid's completion and memory (wait) before reading its results.
+// What an earlier kernel of the stream may write (lengths, page tables, rows,
+// scales) is therefore written while later grids are already resident, and is
+// never read through the non-coherent path (ld.global.nc, __ldg), which is only
+// for data that does not change while the grid lives; __ldcg reads it from L2.
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
