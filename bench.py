@@ -187,6 +187,23 @@ def choose_copies(w: wl.Workload, lens: np.ndarray, total_steps: int) -> int:
     return int(max(2, min(cap, max(need_l2, need_drift))))
 
 
+def copy_order(cursor: int, n_steps: int, R: int) -> list:
+    """The cache copies that the steps of a timed region use; every region of a phase replays the same graphs."""
+    return [(cursor + i) % R for i in range(n_steps)]
+
+
+def steps_per_copy(R: int, warmup: int, phases) -> int:
+    """The most steps that any of the R copies takes: the warm-up's, and those of phases of (steps, regions). With
+    appends that is how many tokens a copy needs room for. A region starts where its phase does, so where R does not
+    divide its steps, some copies take one more in every region."""
+    count = np.bincount(copy_order(0, warmup, R), minlength=R)
+    cursor = warmup
+    for n_steps, regions in phases:
+        count += regions * np.bincount(copy_order(cursor, n_steps, R), minlength=R)
+        cursor += n_steps * regions
+    return int(count.max())
+
+
 def est_step_seconds(w: wl.Workload, lens) -> float:
     """Rough step time (algorithmic bytes at 5 TB/s), used only to size the timed regions."""
     L = np.asarray(lens, dtype=np.int64)
@@ -268,15 +285,16 @@ def run_ours(args, rank, world, local, workload=None, region_s=None, with_e2e=No
     B = int(lens0.size)
     est_step_s = est_step_seconds(w, lens0)
     n_reg = max(3, min(math.ceil(region_s / (args.steps * est_step_s)), max(3, MAX_HEADLINE_STEPS // args.steps)))
-    total_steps = args.warmup + args.steps * (n_reg + (1 if e2e_on else 0)) + 2
-    total_steps += max(2, min(args.steps, 512))  # the region that times the split kernel alone
+    n_ev = max(2, min(args.steps, 512))  # the region that times the split kernel alone
+    phases = [(args.steps, n_reg), (n_ev, 1)] + [(args.steps, 1)] * bool(e2e_on)
+    total_steps = args.warmup + sum(n * regions for n, regions in phases) + 2
     blocks = w.select_blocks > 0
     if blocks:  # block gather: the caller's selection, the same every step
         bidx_h, nblk_h = wl.draw_blocks(lens0, w.select_blocks, [w.seed + 1000 * rank])
     # L2 sizing by the rows a step reads (block gather: the selected ones)
     R = args.copies if args.copies > 0 else choose_copies(
         w, acc.blocks_attended(lens0, nblk_h) if blocks else lens0, total_steps)
-    headroom = math.ceil(total_steps / R) + 2
+    headroom = steps_per_copy(R, args.warmup, phases) + 2
     # inputs: seeded on the host, one copy moved to HBM, cloned R times there
     wr = wl.Workload(w.name, w.batch, w.lengths, w.kv_dtype, w.permute_pages, 0, w.seed + 1000 * rank,
                      queries=w.queries)
@@ -469,7 +487,7 @@ def run_ours(args, rank, world, local, workload=None, region_s=None, with_e2e=No
         the device ms of every region, the split-launch event times (with_events), the lengths of the
         last R steps, the wall-clock span, and the algorithmic bytes of every region."""
         nonlocal cursor
-        order = [(cursor + i) % R for i in range(n_steps)]
+        order = copy_order(cursor, n_steps, R)
         # one graph holds at least MIN_GRAPH_STEPS steps (a whole number of passes over the R copies), so
         # that graph launches are amortised; end to end, at least 16, so the copy pipeline rarely drains
         grp = R * max(1, -(-(MIN_GRAPH_STEPS if e2e_bufs is None else E2E_GRAPH_STEPS) // R))
@@ -522,7 +540,6 @@ def run_ours(args, rank, world, local, workload=None, region_s=None, with_e2e=No
     mean_len = float(np.mean([float(np.mean(L)) for L in last_lens]))
     # split-kernel device time: the same steps again, with an event pair
     # recorded around every split launch on its stream
-    n_ev = max(2, min(args.steps, 512))
     n_before = len(split_bytes)
     _, split_ms, _, _, _ = timed(n_ev, with_events=True)
     split_bytes_last = split_bytes[n_before:][-len(split_ms):]
