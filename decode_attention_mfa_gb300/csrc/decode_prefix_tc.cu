@@ -1245,6 +1245,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
                 for (int k = 0; k < 32; ++k) o[k] *= alpha;
                 tmem_st32(tmem + lanes + kTmemO + c, o);
               }
+              tc_wait_st();  // the second try may read O again
             }
           }
           if (!kFp8 || cols >= 64)
