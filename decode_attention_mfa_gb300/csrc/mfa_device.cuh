@@ -164,6 +164,8 @@ __device__ __forceinline__ bool mbar_try_wait(uint32_t bar, uint32_t parity) {
 // Wait for the phase of `bar` with the given parity to complete, for at most
 // `budget_ns`. On expiry (or when another role already gave up, `*abort` != 0)
 // it records MFA_DEVERR_TIMEOUT, raises *abort and returns false; it never traps.
+// Without a budget it gives up at the second look that finds the phase
+// incomplete, whatever the steps of the clock.
 // The polling loop is out of line: a wait whose phase has already completed
 // (the common case in a running pipeline) costs one try_wait.
 static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, uint64_t budget_ns,
@@ -172,7 +174,7 @@ static __device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity
   while (true) {
     if (mbar_try_wait(bar, parity)) return true;
     if (abort && *abort) return false;
-    if (globaltimer_ns() - t0 > budget_ns) {
+    if (globaltimer_ns() - t0 >= budget_ns) {
       raise_error(err, MFA_DEVERR_TIMEOUT);
       if (abort) *abort = 1;
       return false;
