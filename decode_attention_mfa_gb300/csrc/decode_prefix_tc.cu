@@ -58,11 +58,14 @@
 // E4M3 cache: S is 8-bit MMAs (kind::f8f6f4) on the raw K codes, with Q as two
 // E4M3 terms under a power of two per row, split in shared memory when a row
 // tile begins (two terms at twice the 16-bit rate cost what bf16 does). For P V
-// four more warps turn the V codes times their scales into f16, a page's
-// scales taken relative to the power of two 2^e above their largest, and P,
-// times 2^e, is f16 as well: each is off by 2^-11, and nothing that matters
-// falls out of f16's range, where E4M3 terms of P would flush a thousand small
-// weights beside one large one.
+// four more warps turn the V codes times their scales into f16, and P is f16 as
+// well: each is off by 2^-11, where E4M3 terms of P would flush a thousand small
+// weights beside one large one. f16 holds the codes' and the scales' exponents
+// for scales within [2^-16, 2), |v| of 0.007 to 900; of a scale outside, the
+// power of two beyond goes to its key's weight instead, and the reference follows
+// weights times that power: what neither large values without weight nor rows of
+// zeros (whose scale the append sets to 1) take from the others' bits. Weights
+// below 2^-18 of a row's largest are held to 2^-29 of it.
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <type_traits>
@@ -86,15 +89,17 @@ constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;                    
 constexpr int kUnitKeys = 2 * kPageSize;
 constexpr int kSeqs = kPrefixTileSeqs;
 constexpr int kScaleSlots = 4;         // E4M3: 128 K scales and 128 V scales a unit
-constexpr int kMostScale = 100;        // of 2^e: far enough from 2^127 for what is divided by it
+// E4M3: exponents of V's scales that f16 holds beside the codes' (V' = code * scale * 2^kScaleUp is at most 448 * 2^7 and
+// its scale at least 2^-10), and the most that a weight takes of one outside: far enough from 2^127 for their sums.
+constexpr int kLeastScale = -16, kMostScale = 0, kScaleUp = 6, kMostShift = 100;
 constexpr int kScaleBytes = 1024;
 constexpr int kQBytes = 65536;         // 128 rows x 256 dims, four 64-dim blocks of [128 rows x 128 B]
 constexpr int kSeqQBytes = 32768;      // one sequence's rows
 constexpr int kTmemCols = 512, kTmemO = 256, kSCols = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A move of the reference leaves the row's largest weight (E4M3: times 2^e) at 2^kMoved: of bf16, whose relative step is
-// the same everywhere, anything will do, of f16 a value that leaves room both ways. The next move comes when the sum of
+// A move of the reference leaves the row's largest weight at 2^moved_to: of bf16, whose relative step is the same
+// everywhere, anything will do, of f16 a value that leaves room both ways. The next move comes when the sum of
 // a thread's 64 weights of a unit passes kMostSum, so that none of them passes f16's range; the sum is needed anyway,
 // and a maximum is looked for only then.
 template <bool kFp8>
@@ -705,19 +710,21 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
 }
 
-// The exponent e of a page: 2^e is the power of two above the largest of its 64 V scales (sc; `valid` of them count,
-// those behind are stale). All lanes of a warp.
-__device__ __forceinline__ int page_exponent(const float* sc, int valid, int lane) {
-  float2 v = reinterpret_cast<const float2*>(sc)[lane];
-  if (2 * lane >= valid) v.x = 0.0f;
-  if (2 * lane + 1 >= valid) v.y = 0.0f;
-  const int e = (int)(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fabsf(v.x), fabsf(v.y)))) >> 23) - 126;
-  return max(-kMostScale, min(kMostScale, e));
-}
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+// The exponent that a key's weight takes of its V scale: what lies outside [kLeastScale, kMostScale]. A scale of zero (or
+// below the fp32 normal range) has none, its row adds nothing.
+__device__ __forceinline__ int scale_shift(float scale) {
+  const int e = (int)((__float_as_uint(scale) >> 23) & 0xFFu) - 127;
+  return e == -127 ? 0 : max(-kMostShift, min(kMostShift, e - max(kLeastScale, min(kMostScale, e))));
+}
+// Whether it may have one (zeros are taken for such, too).
+__device__ __forceinline__ bool may_shift(float scale) {
+  constexpr uint32_t kLeast = (uint32_t)(127 + kLeastScale) << 23, kSpan = (uint32_t)(kMostScale - kLeastScale + 1) << 23;
+  return (__float_as_uint(scale) & 0x7FFFFFFFu) - kLeast >= kSpan;
+}
 
-// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^-e (at most 448, e of the page; off by 2^-11 for the scale and
-// 2^-11 for the product), from the codes: per page [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both
+// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^kScaleUp without the scale's shift (off by 2^-11 for the scale
+// and 2^-11 for the product), from the codes: per page [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both
 // with the 128-byte swizzle. A thread takes 16 codes of a row and of every 16th row after it; rows behind the last token
 // become zeros. Eight neighbouring threads take half of rows r and r ^ 5, whose swizzles differ in the bits that keep
 // both the codes they read and the values they write on banks of their own. That the scales are applied here spares the
@@ -745,13 +752,13 @@ __device__ void convert_role(const PrefixParams& p, const Ctx& cx, const PlanSme
 #pragma unroll
       for (int page = 0; page < 2; ++page) {
         const int valid = q.tokens(2 * u + page);
-        const float down = exp2_int(-page_exponent(sc + page * kPageSize, valid, lane));
         uint4 v[4];
         __half2 scale[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
-          scale[i] = __float2half2_rn(sc[page * kPageSize + row0 + 16 * i] * down);
+          const float s = sc[page * kPageSize + row0 + 16 * i];
+          scale[i] = __float2half2_rn(s * exp2_int(kScaleUp - scale_shift(s)));
         }
         if (valid < kPageSize) {
 #pragma unroll
@@ -1064,6 +1071,60 @@ __device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, i
   return exp2_int(-e);
 }
 
+// E4M3: a unit whose V scales have shifts, which is rare and out of line: in the usual units' loop it cost them 9% (304
+// sequences behind 256 pages 182 -> 199 us), the threads' look for such scales alone at most 1%. P takes the shifts, the
+// denominator does not. The reference is looked for among all keys, so no second try follows and P may replace S at once.
+// tx: this thread's 64 products, sc: their K scales, 128 before their V scales. Returns the row's reference and this thread's
+// share of its denominator. Both warps of the rows; what O holds is complete.
+static __device__ __noinline__ float2 shifted_unit(uint32_t tx, uint32_t o_addr, const float* sc, int cols, float mul, float m,
+                                                   float l, bool fresh, float* red, int row, int half) {
+  const float* v_scale = sc + kUnitKeys;
+  float x[32];
+  float top = -INFINITY;
+#pragma unroll 1
+  for (int g = 0; g < 64; g += 32) {
+    tmem_ld32(tx + g, x);
+    tc_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 32; ++k)
+      if (g + k < cols) top = fmaxf(top, x[k] * sc[g + k] * mul + (float)scale_shift(v_scale[g + k]));
+  }
+  red[half * 128 + row] = top - moved_to<true>();
+  barrier_rows(row >> 5);
+  const float m_new = fmaxf(m, fmaxf(red[row], red[128 + row]));
+  const float alpha = fresh || m == m_new ? 1.0f : ex2_approx(m - m_new);
+  if (!fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
+#pragma unroll 1
+    for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+      tmem_ld32(o_addr + c, x);
+      tc_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) x[k] *= alpha;
+      tmem_st32(o_addr + c, x);
+    }
+  }
+  const float ref = m_new == -INFINITY ? 0.0f : m_new;
+  float sum = 0.0f;
+#pragma unroll 1
+  for (int g = 0; g < 64; g += 32) {
+    tmem_ld32(tx + g, x);
+    tc_wait_ld();
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 32; ++k) {
+      const float y = g + k < cols ? ex2_approx(fmaf(x[k] * sc[g + k], mul, -ref)) : 0.0f;
+      sum += y;
+      x[k] = y * exp2_int(scale_shift(v_scale[g + k]));
+    }
+#pragma unroll
+    for (int c = 0; c < 16; ++c) w[c] = pack_f16(x[2 * c], x[2 * c + 1]);
+    tmem_st16(tx + g, reinterpret_cast<const float*>(w));
+  }
+  tc_wait_st();
+  barrier_rows(row >> 5);  // red is free again
+  return make_float2(m_new, l * alpha + sum);
+}
+
 template <bool kFp8>
 __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi, uint32_t tmem, uint8_t* gbase) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -1097,7 +1158,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     // rounding (relative error of out 2.4e-3 -> 1.9e-3 for 128 sequences behind 512 pages, 1% slower). Of f16 weights the
     // difference does not matter. The LSE takes the unrounded sum.
     float l_p = 0.0f;
-    float mul = c2;                 // of the row's products: the softmax scale, and 2^-e of its Q terms
+    float mul = c2;                 // of the row's products: the softmax scale, and the power of two of its Q terms
     if constexpr (kFp8) {
       wait(QFull, pieces & 1);
       mul *= split_q(cx.base + Smem<kFp8>::q, red, row, quad, half);
@@ -1112,7 +1173,12 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       const float* sc = reinterpret_cast<const float*>(gbase + Smem<kFp8>::scales + sc_slot * kScaleBytes);
       const int cols = seen(2 * u + half);  // this thread's keys
       if (kFp8) wait(ScFull + sc_slot, (cnt / kScaleSlots) & 1);
-      const int e = kFp8 ? page_exponent(sc + kUnitKeys + 64 * half, cols, lane) : 0;
+      // E4M3: a look at two of the 64 V scales of this warp's page; the threads of the rows together see those of both.
+      bool may = false;
+      if constexpr (kFp8) {
+        const float2 v = reinterpret_cast<const float2*>(sc + kUnitKeys + 64 * half)[lane];
+        may = may_shift(2 * lane < cols ? v.x : 1.0f) | may_shift(2 * lane + 1 < cols ? v.y : 1.0f);
+      }
       wait(SFull + buf, (cnt >> 1) & 1);
       tc_fence_after();
       if (cols + seen(2 * u + (half ^ 1)) > 0) {
@@ -1160,13 +1226,12 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           }
           tc_wait_st();
         }
-        const float lift = (float)e;
         uint32_t w[32];
         float2 sum, sum_p;
         // weights of this thread's keys, their sums, and P; kPart: only the first `cols` of the 64 count
         auto weights = [&](auto part) {
           constexpr bool kPart = decltype(part)::value;
-          const float ref = m == -INFINITY ? 0.0f : m - lift;  // only infinite logits so far: weights of 0
+          const float ref = m == -INFINITY ? 0.0f : m;  // only infinite logits so far: weights of 0
           const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
           sum = make_float2(0.0f, 0.0f);
           sum_p = sum;
@@ -1217,13 +1282,14 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
           }
           return top;
         };
-        bool move = open;
+        bool move = open, shifted = false;
 #pragma unroll 1
         for (int tries = 0; tries < 2; ++tries) {
           if (move) {
+            if (kFp8 && (shifted = barrier_rows_or(quad, may))) break;
             // Half the keys are enough for a first reference, the sum tells if not (32 sequences behind 128 pages 26.0 ->
             // 25.6 us; on an E4M3 cache 50.4 and 50.6, so not there).
-            const float big = largest(!kFp8 && tries == 0 ? 32 : 64) + (lift - moved_to<kFp8>());
+            const float big = largest(!kFp8 && tries == 0 ? 32 : 64) - moved_to<kFp8>();
             red[half * 128 + row] = big;
             barrier_rows(quad);
             const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));
@@ -1252,15 +1318,24 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
             weights(std::false_type{});
           else
             weights(std::true_type{});
-          move = barrier_rows_or(quad, sum.x + sum.y > kMostSum);
+          move = barrier_rows_or(quad, sum.x + sum.y > kMostSum || may);
           if (!move) break;
         }
+        if (kFp8 && shifted) {  // nothing has been done yet
+          if (!fresh) wait_pv();
+          tc_fence_after();
+          const float2 ml = shifted_unit(tx, tmem + lanes + kTmemO, sc + 64 * half, cols, mul, m, l, fresh, red, row, half);
+          m = ml.x;
+          l = ml.y;
+          open = __any_sync(0xffffffffu, m == -INFINITY);
+        } else {
+          l += sum.x + sum.y;
+          l_p += sum_p.x + sum_p.y;
+          tmem_st16(tx, reinterpret_cast<const float*>(w));
+          tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
+          tc_wait_st();
+        }
         fresh = false;
-        l += (sum.x + sum.y) * (kFp8 ? exp2_int(-e) : 1.0f);
-        l_p += sum_p.x + sum_p.y;
-        tmem_st16(tx, reinterpret_cast<const float*>(w));
-        tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
-        tc_wait_st();
       }
       tc_fence_before();
       __syncwarp();
@@ -1279,7 +1354,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       l += red[(half ^ 1) * 128 + row];
       if (!kFp8) l_p += red[256 + (half ^ 1) * 128 + row];
       const size_t at = ((size_t)(pair + q.t) * kSeqs + j) * kHeads + (row & 63);
-      const float inv = 1.0f / (kFp8 ? l : l_p);
+      const float inv = kFp8 ? exp2_int(-kScaleUp) / l : 1.0f / l_p;
       float* dst = p.part_o + (at - (lane & 3)) * kHeadDim + 8 * (lane & 3);
 #pragma unroll 1
       for (int c = 128 * half; c < 128 * half + 128; c += 32) {

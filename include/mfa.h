@@ -358,8 +358,11 @@ mfa_status_t mfa_decode_attention_prefix(const void* q, const void* k_cache, con
  * mfa_decode_attention_fp8. q enters the 8-bit products with the raw K codes as
  * two E4M3 terms under a power of two per head (2^-18.8 of its largest value);
  * the weights and V's codes times their scales enter the second product as f16
- * (2^-11 each, and 2^-11 for the scale; V's relative to the largest scale of
- * its page). Everything else as mfa_decode_attention_prefix. */
+ * (2^-11 each, and 2^-11 for the scale). Of a V scale outside [2^-16, 2) the
+ * power of two beyond enters with the weight instead (scales from 2^-116 to
+ * 2^101); a weight below 2^-18 of the head's largest, counted with that power, is
+ * held to 2^-29 of it. Units of two pages with such scales, or zeros, take longer.
+ * Everything else as mfa_decode_attention_prefix. */
 mfa_status_t mfa_decode_attention_prefix_fp8(const void* q, const void* k_cache, const void* v_cache,
                                              const float* k_scale, const float* v_scale,
                                              const int32_t* page_table, const int32_t* seq_lens,

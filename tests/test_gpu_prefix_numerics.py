@@ -82,3 +82,96 @@ def test_a_reference_that_moves_twice_in_a_unit(fp8):
     b.call(hints=(0, 0))
     capi.mfa_check_device_errors(b.ws)
     assert not torch.isfinite(b.lse[:, 5]).any() and torch.isfinite(b.lse[:, others]).all()
+
+
+def keyed(n, pages, own, fp8, seed):
+    """A batch whose logits are set key by key, and normal ones to begin with. Returns it and set_keys(logit, power): both
+    [num_pages, 64]; K's rows become their second dimension alone, V's rows are taken times 2^power."""
+    b = Batch([n], [pages], np.full(n, pages * PAGE + own), fp8, seed=seed)
+    b.q[:, :, 1] = 1.0
+    used = ~b.unused
+
+    def set_keys(logit, power):
+        k = (logit / SCALE)[used]
+        if fp8:
+            b.cache[0][used] = 0
+            codes = b.cache[0][used]
+            codes[:, 1] = torch.where(k < 0, 0xB8, 0x38).to(torch.uint8)
+            b.cache[0][used] = codes
+            b.scales[0][used] = k.abs()
+            b.scales[1][used] = torch.ldexp(b.scales[1][used], power[used])
+        else:
+            rows = torch.zeros((int(used.sum()), DIM), device="cuda")
+            rows[:, 1] = k
+            b.cache[0][used] = rows.bfloat16()
+            b.cache[1][used] = torch.ldexp(b.cache[1][used].float(), power[used].unsqueeze(-1)).bfloat16()
+
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    shape = (b.num_pages, PAGE)
+    return b, set_keys, torch.randn(shape, generator=gen, device="cuda"), lambda lo, hi: torch.randint(
+        lo, hi + 1, shape, generator=gen, device="cuda")
+
+
+@KV
+@pytest.mark.parametrize("power", [12, 24, 60])
+def test_large_values_without_weight_leave_small_ones_whole(power, fp8):
+    """On every page one value of 2^power times the others' size at a logit of -56 (2^-81): it counts for nothing, or for all
+    there is, and the others keep their bits either way. Logits of up to 56 are single products."""
+    b, set_keys, logit, _ = keyed(3, 5, 100, fp8, 43)
+    p = torch.zeros((b.num_pages, PAGE), device="cuda", dtype=torch.int64)
+    logit[:, 5] = -56.0
+    p[:, 5] = power
+    set_keys(logit, p)
+    b.call()
+    check(b, 56 * 2 ** -15)
+
+
+@KV
+@pytest.mark.parametrize("power", [-6, -10, -14])
+def test_rows_of_zeros_beside_small_values(power, fp8):
+    """Values of nothing but zeros, whose scale is 1 as the append writes it, at logits 4 or more above the others', whose
+    values are small: the zeros add nothing, and take nothing from the others. E4M3: a weight is a multiple of 2^-24 where
+    the zeros' is 2^4, the others' largest 2^-5.8 of that (logits of 7 and 3) and, of values below 2^-16 of a scale, 2^x less:
+    their scales are at least 2^-9 (the largest of 256 normal values over 448, times exp(-1.5)) times 2^power, so x is at
+    least power + 7 where that is negative. Some 400 keys are then off by 2^-25 of 2^(4 - 5.8 + x) each, and V' of two keys
+    differ by at most 2 where x is not 0, and by 2^7 where it is: 2^(8.7 - 25 + 1.8 + 7) = 2^-7.5 at power -6, and
+    2^(8.7 - 25 + 1.8 + 1 - x) = 2^(-13.5 - x) below."""
+    b, set_keys, logit, _ = keyed(3, 5, 100, fp8, 44)
+    logit.clamp_(-3.0, 3.0)
+    logit[:, ::16] = 7.0
+    set_keys(logit, torch.full((b.num_pages, PAGE), power, device="cuda"))
+    rows = torch.zeros_like(b.unused)
+    rows[:, ::16] = True
+    rows &= ~b.unused
+    b.cache[1][rows] = 0
+    if fp8:
+        b.scales[1][rows] = 1.0
+    b.call()
+    check(b, 7 * 2 ** -15, floor=(2.0 ** -7.5 if power == -6 else 2.0 ** (-13.5 - (power + 7))) if fp8 else 0.0)
+
+
+@KV
+@pytest.mark.parametrize("lo,hi", [(-40, 20), (-110, 90)])
+def test_values_of_all_sizes_in_a_page(lo, hi, fp8):
+    """Sizes drawn key by key over a range that no 16-bit format holds; some scales are zero. The result is the large ones',
+    and the rest is off by 2^-28 of them for each of some 400 keys (a step of 2^-25 of a weight where the largest is 2^4 or
+    more, and a value twice as large)."""
+    b, set_keys, logit, draw = keyed(3, 5, 100, fp8, 45)
+    set_keys(logit, draw(lo, hi))
+    if fp8:
+        b.scales[1][:, 7::16] *= 0.0
+        b.scales[1][b.unused] = float("nan")
+    b.call()
+    check(b, 5 * 2 ** -15, floor=2.0 ** -19)
+
+
+@KV
+@pytest.mark.parametrize("lo,hi", [(-16, 0), (-40, 20)])
+def test_sizes_that_weights_make_up_for(lo, hi, fp8):
+    """The smaller the value the larger its weight, so that each of some 400 keys counts as much as any other. Logits of up to
+    28 are single products. (bf16: the weights span 2^60, which its exponents hold.)"""
+    b, set_keys, logit, draw = keyed(3, 5, 100, fp8, 46)
+    power = draw(lo, hi)
+    set_keys(logit - power * float(np.log(2.0)), power)
+    b.call()
+    check(b, 32 * 2 ** -15)
