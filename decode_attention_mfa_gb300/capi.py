@@ -114,18 +114,19 @@ def _ptr(x):
         raise
 
 
-_raw_stream = _device = None
+_lookup = None  # torch's functions for the current stream's handle and the current device; one store, for other threads
 
 
 def _stream(s):
-    global _raw_stream, _device
+    global _lookup
     if s is None:
         # the handle of torch.cuda.current_stream(), without the Stream object (3 us of a call that takes the GPU as long)
-        if _raw_stream is None:
+        lookup = _lookup
+        if lookup is None:
             import torch
             torch.cuda.init()
-            _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
-        return _raw_stream(_device())
+            lookup = _lookup = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+        return lookup[0](lookup[1]())
     if isinstance(s, int):
         return s
     return s.cuda_stream

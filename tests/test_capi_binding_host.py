@@ -1,0 +1,45 @@
+"""The binding's own steps on every call: the current stream's handle and the arguments' addresses. No GPU is needed."""
+import importlib.util
+import sys
+
+import pytest
+
+from decode_attention_mfa_gb300 import capi
+
+
+@pytest.fixture
+def fresh(monkeypatch):
+    """The binding as a program finds it before its first call, with a stand-in for torch's streams (handle 7 on device 3)."""
+    import torch
+    monkeypatch.setattr(torch.cuda, "init", lambda: None)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 3, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", {3: 7}.__getitem__, raising=False)
+    spec = importlib.util.spec_from_file_location("capi_fresh", capi.__file__)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    return module
+
+
+def test_a_first_stream_lookup_interrupted_anywhere_by_another(fresh):
+    """A second call at every instruction of the first, as another thread may make it."""
+    found = []
+
+    def trace(frame, event, arg):
+        if frame.f_code is not fresh._stream.__code__:
+            return None
+        frame.f_trace_opcodes = True
+        if event == "opcode":
+            before = fresh.__dict__.copy()
+            found.append(fresh._stream(None))
+            for name, value in before.items():  # as if it had not been made
+                fresh.__dict__[name] = value
+        return trace
+
+    old = sys.gettrace()
+    sys._getframe().f_trace_opcodes = True  # (Python 3.12 asks for it before the trace begins)
+    sys.settrace(trace)
+    try:
+        handle = fresh._stream(None)
+    finally:
+        sys.settrace(old)
+    assert handle == 7 and len(found) > 10 and set(found) == {7}
