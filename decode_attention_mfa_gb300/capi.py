@@ -125,7 +125,11 @@ def _stream(s):
         if lookup is None:
             import torch
             torch.cuda.init()
-            lookup = _lookup = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            try:
+                lookup = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            except AttributeError:  # names of torch's own; the public way gives the same handle
+                lookup = lambda device: torch.cuda.current_stream(device).cuda_stream, torch.cuda.current_device
+            _lookup = lookup
         return lookup[0](lookup[1]())
     if isinstance(s, int):
         return s

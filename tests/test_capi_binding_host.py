@@ -43,3 +43,12 @@ def test_a_first_stream_lookup_interrupted_anywhere_by_another(fresh):
     finally:
         sys.settrace(old)
     assert handle == 7 and len(found) > 10 and set(found) == {7}
+
+
+@pytest.mark.parametrize("name", ["_cuda_getCurrentRawStream", "_cuda_getDevice"])
+def test_the_stream_lookup_without_torchs_private_names(fresh, monkeypatch, name):
+    import torch
+    monkeypatch.delattr(torch._C, name)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 4)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device: type("Stream", (), {"cuda_stream": 10 + device}))
+    assert fresh._stream(None) == 14 and fresh._stream(None) == 14
