@@ -104,12 +104,12 @@ def load():
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    try:  # nearly always a tensor: looking for an address first costs a call of ten pointers 0.4 us
+    if x is None or type(x) is int:  # 15 ns of a tensor's 140; an exception for each address would be 440
+        return x
+    try:
         return x.data_ptr()
     except AttributeError:
-        if isinstance(x, int):
+        if isinstance(x, int):  # of a type of its own
             return x
         raise
 

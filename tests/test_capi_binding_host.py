@@ -52,3 +52,30 @@ def test_the_stream_lookup_without_torchs_private_names(fresh, monkeypatch, name
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 4)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device: type("Stream", (), {"cuda_stream": 10 + device}))
     assert fresh._stream(None) == 14 and fresh._stream(None) == 14
+
+
+def test_addresses_and_tensors_are_taken_without_an_exception():
+    """Addresses as integers are as usual as tensors (a row of a table, a part of a workspace): neither is found by failing."""
+    import torch
+
+    class Address(int):
+        pass
+
+    raised = []
+
+    def trace(frame, event, arg):
+        if event == "exception":
+            raised.append(arg)
+        return trace
+
+    t = torch.zeros(4)
+    old = sys.gettrace()
+    sys.settrace(trace)
+    try:
+        got = [capi._ptr(x) for x in (4096, 0, None, t)]
+    finally:
+        sys.settrace(old)
+    assert got == [4096, 0, None, t.data_ptr()] and not raised
+    assert capi._ptr(Address(8)) == 8
+    with pytest.raises(AttributeError):
+        capi._ptr("text")
