@@ -49,7 +49,7 @@ NOMINAL_HBM_GBS = 8000.0
 FALLBACK_HBM_GBS = 6800.0
 L2_BYTES = 135_528_448
 COPY_MEM_BUDGET = 100e9
-DRIFT = 0.03              # with an append, each cache copy grows by at most about this fraction of its length
+DRIFT = 0.03              # with an append, each cache copy grows by about this fraction of its length
 MAX_HEADLINE_STEPS = 20000
 MIN_GRAPH_STEPS = 32      # steps per captured graph (graph launches amortised over at least this many)
 E2E_GROUP = 16            # end to end: steps per stream synchronisation (two sets of per-step buffers)
@@ -73,7 +73,7 @@ def parse_args():
                     help="with the default workload, skip the extra workloads timed after the headline")
     ap.add_argument("--copies", type=int, default=0,
                     help="device-resident cache copies to rotate over (default: enough to defeat L2 "
-                         "and keep the per-copy length growth near 1%%; small values suit ncu captures)")
+                         "and keep the per-copy length growth near 3%%; small values suit ncu captures)")
     return ap.parse_args()
 
 

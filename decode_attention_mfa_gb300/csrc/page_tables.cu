@@ -14,9 +14,10 @@
 // Split: the sums over at most 1024 requests take well under a microsecond of a
 // CTA's time, less than a second launch or a grid-wide wait would, so every
 // CTA forms them itself and then works on its share of the tokens and pages.
-// The calls are bound by latency (launch, two dependent loads, the sums): 3.1 us
+// The calls are bound by latency (launch, two dependent loads, the sums): 3.2 us
 // for 128 requests with a token each, 5.4 us for 1000 requests with 250,000
-// tokens (2 MB), 3.3 us for the release of 63 of 1000 requests.
+// tokens (2 MB), 3.4 us for the release of 63 of 1000 requests. With outputs that
+// replace inputs the arrival of all CTAs adds 0.8 us where there are many.
 #include "mfa_device.cuh"
 #include "mfa_serving.hpp"
 

@@ -335,6 +335,9 @@ mfa_status_t mfa_query_lowrank(const void* x, const void* w_down, const void* ga
  * group's prefix (0 for an empty slot of the batch), and a group with fewer than
  * two others, are read through their own table rows alone, as by
  * mfa_decode_attention.
+ * What is gained lies in the shared pages: for batches that share nothing
+ * mfa_decode_attention is up to 7% faster, and for a few sequences with short
+ * prefixes (below eight with 16 pages) either will do.
  * max_prefix_hint, max_suffix_hint: expected maxima of 64 * prefix_pages[g] and
  * of the tokens behind the prefix; they size the grids only.
  * workspace: at least mfa_decode_prefix_workspace_bytes(batch, n_groups,
