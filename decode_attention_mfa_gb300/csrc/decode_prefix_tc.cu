@@ -49,11 +49,11 @@
 //              token to zero.
 // Every wait is bounded (the wait budget), as in the split kernel.
 //
-// Measured, combine included: 304 sequences behind 256 pages 172 to 178 us by the
-// box (1835 to 1900 TFLOP/s; cuBLAS reaches 1914 in a burst), E4M3 180 to 187; 32
-// behind 128 pages 26.2 us, of which 5 go by until the first S (plan, page ids,
-// first loads), 10 in 9 units, 2.9 in the write-out of 128 KB a CTA (an SM writes
-// 32 B a cycle) and 3.8 in the combine.
+// Measured, combine included: 304 sequences behind 256 pages 172 to 178 us from
+// card to card (1835 to 1900 TFLOP/s; cuBLAS reaches 1914 in a burst), E4M3 180 to
+// 187; 32 behind 128 pages 26.2 us, of which 5 go by until the first S (plan, page
+// ids, first loads), 10 in 9 units, 2.9 in the write-out of 128 KB a CTA (an SM
+// writes 32 B a cycle) and 3.8 in the combine.
 //
 // E4M3 cache: S is 8-bit MMAs (kind::f8f6f4) on the raw K codes, with Q as two
 // E4M3 terms under a power of two per row, split in shared memory when a row
