@@ -65,6 +65,14 @@ _SIGNATURES = {
                                          _Z, _P], _I),
     "mfa_kv_append_slots": ([_P, _P, _I64, _I64, _P, _I, _P, _P, _I, _P, _P], _I),
     "mfa_kv_append_slots_fp8": ([_P, _P, _I64, _I64, _P, _I, _P, _P, _P, _P, _I, _P, _P], _I),
+    "mfa_kv_append_slots_fp4": ([_P, _P, _I64, _I64, _P, _I, _P, _P, _P, _P, _I, _P, _P], _I),
+    "mfa_kv_read": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _P, _P], _I),
+    "mfa_kv_read_fp8": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _P, _P], _I),
+    "mfa_kv_read_fp4": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I, _I, _I, _I, _P, _P], _I),
+    "mfa_chunk_workspace_bytes": ([_I, _I], _Z),
+    "mfa_chunk_attention": ([_P, _P, _P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _P, _Z, _P], _I),
+    "mfa_chunk_attention_fp8": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _P, _Z, _P], _I),
+    "mfa_chunk_attention_fp4": ([_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F, _I, _I, _I, _I, _P, _Z, _P], _I),
     "mfa_reserve_pages": ([_P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P], _I),
     "mfa_release_pages": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P], _I),
     "mfa_check_device_errors": ([_P, _I, _P], _I),
@@ -356,6 +364,73 @@ def mfa_kv_append_slots_fp8(k_new, v_new, k_stride, v_stride, slot_map, n_rows, 
     _check(load().mfa_kv_append_slots_fp8(_ptr(k_new), _ptr(v_new), k_stride, v_stride, _ptr(slot_map), n_rows,
                                           _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), num_pages,
                                           _ptr(workspace), _stream(stream)))
+
+
+def mfa_kv_append_slots_fp4(k_new, v_new, k_stride, v_stride, slot_map, n_rows, k_cache, v_cache, k_scale, v_scale,
+                            num_pages, workspace, stream=None):
+    """The same into a 4-bit cache: uint8 [num_pages, 64, 128] (packed E2M1) with per-token fp32 scales."""
+    _check(load().mfa_kv_append_slots_fp4(_ptr(k_new), _ptr(v_new), k_stride, v_stride, _ptr(slot_map), n_rows,
+                                          _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), num_pages,
+                                          _ptr(workspace), _stream(stream)))
+
+
+def mfa_kv_read(k_cache, v_cache, page_table, first, row_starts, k_out, v_out, k_stride, v_stride, batch, max_rows,
+                max_pages, num_pages, workspace, stream=None):
+    """Positions first[b] .. of a paged cache as bf16 rows row_starts[b] .. row_starts[b + 1] of k_out and v_out; first
+    None: 0; strides in elements."""
+    _check(load().mfa_kv_read(_ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(first), _ptr(row_starts),
+                              _ptr(k_out), _ptr(v_out), k_stride, v_stride, batch, max_rows, max_pages, num_pages,
+                              _ptr(workspace), _stream(stream)))
+
+
+def mfa_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, page_table, first, row_starts, k_out, v_out, k_stride,
+                    v_stride, batch, max_rows, max_pages, num_pages, workspace, stream=None):
+    """The same of an E4M3 cache: codes times scales."""
+    _check(load().mfa_kv_read_fp8(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+                                  _ptr(first), _ptr(row_starts), _ptr(k_out), _ptr(v_out), k_stride, v_stride, batch,
+                                  max_rows, max_pages, num_pages, _ptr(workspace), _stream(stream)))
+
+
+def mfa_kv_read_fp4(k_cache, v_cache, k_scale, v_scale, page_table, first, row_starts, k_out, v_out, k_stride,
+                    v_stride, batch, max_rows, max_pages, num_pages, workspace, stream=None):
+    """The same of a 4-bit cache."""
+    _check(load().mfa_kv_read_fp4(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), _ptr(page_table),
+                                  _ptr(first), _ptr(row_starts), _ptr(k_out), _ptr(v_out), k_stride, v_stride, batch,
+                                  max_rows, max_pages, num_pages, _ptr(workspace), _stream(stream)))
+
+
+def mfa_chunk_workspace_bytes(batch: int, max_tokens: int) -> int:
+    n = load().mfa_chunk_workspace_bytes(batch, max_tokens)
+    if n == 0:
+        raise MFAError(1, "bad arguments for mfa_chunk_workspace_bytes")
+    return n
+
+
+def mfa_chunk_attention(q, k_cache, v_cache, page_table, seq_lens, q_starts, out, lse, scale, batch, max_tokens,
+                        max_pages, num_pages, workspace, workspace_bytes, stream=None):
+    """Attention of the last q_starts[b + 1] - q_starts[b] tokens of each sequence over all it holds, causal among them:
+    q, out [max_tokens, 64, 256] bf16, lse [max_tokens, 64] fp32, q_starts int32 [batch + 1]."""
+    _check(load().mfa_chunk_attention(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(page_table), _ptr(seq_lens),
+                                      _ptr(q_starts), _ptr(out), _ptr(lse), float(scale), batch, max_tokens,
+                                      max_pages, num_pages, _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def mfa_chunk_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, q_starts, out, lse, scale,
+                            batch, max_tokens, max_pages, num_pages, workspace, workspace_bytes, stream=None):
+    """The same over an E4M3 cache with per-token fp32 scales."""
+    _check(load().mfa_chunk_attention_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                          _ptr(page_table), _ptr(seq_lens), _ptr(q_starts), _ptr(out), _ptr(lse),
+                                          float(scale), batch, max_tokens, max_pages, num_pages, _ptr(workspace),
+                                          workspace_bytes, _stream(stream)))
+
+
+def mfa_chunk_attention_fp4(q, k_cache, v_cache, k_scale, v_scale, page_table, seq_lens, q_starts, out, lse, scale,
+                            batch, max_tokens, max_pages, num_pages, workspace, workspace_bytes, stream=None):
+    """The same over a 4-bit (packed E2M1) cache with per-token fp32 scales."""
+    _check(load().mfa_chunk_attention_fp4(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                                          _ptr(page_table), _ptr(seq_lens), _ptr(q_starts), _ptr(out), _ptr(lse),
+                                          float(scale), batch, max_tokens, max_pages, num_pages, _ptr(workspace),
+                                          workspace_bytes, _stream(stream)))
 
 
 def mfa_check_device_errors(workspace, clear: bool = True, stream=None):

@@ -1,0 +1,1124 @@
+// chunk_attention_tc.cu -- attention of the new tokens of every sequence (a chunk
+// of a prompt, a whole prompt, or one token) over all that its pages hold, causal
+// among the new ones. With L_b positions in the cache, of which the last n_b are
+// new, token t of them sees the first L_b - n_b + 1 + t:
+//     S = Q K^T,  P = exp2(scale log2(e) S - m),  O = P V,  l = P 1
+// for its 64 heads, which share K and V.
+//
+// Row tile: up to four neighbouring tokens of a sequence, 256 rows, and as its
+// keys the pages up to what its last token sees. 4 * 64 * 256 flops a token and
+// key against 1 KB (bf16) a key for the four tokens: matrix work, bound by the
+// tensor cores, except for tiles of one token, whose pages HBM delivers more
+// slowly than the pair of SMs that shares a tile works them off.
+//
+// A cluster of two CTAs, each with 128 of the rows, works on units of 128 keys
+// (two pages) with tcgen05 MMAs of cta_group::2: each CTA holds one of the two K
+// pages and half of V's dimensions, and both halves feed the pair's MMAs. TMEM
+// holds S twice (2 x 128 columns; P overwrites S in place and is the A operand of
+// P V from there) and O (256 columns): all of it. This is the tile of the
+// shared-prefix kernel, whose parts it uses; what differs is where tiles come
+// from, their masks, and that a prompt makes thousands of short tiles, so that
+// what happens between two of them counts:
+//   - S of a tile's first unit is issued before P V of the last tile's last one
+//     where Q is there by then: its four blocks of 64 dimensions are loaded, from
+//     L2, as the last S of the tile before has read each of them;
+//   - O of a tile is read (into registers, as bf16) while S of the next one's
+//     second unit runs, after the softmax of its first unit, and written behind
+//     the next P V.
+//
+// Work split: the units of all tiles, one after the other, form a line
+// (kChunkPieceUnits more for each tile); each pair takes an equal range of it. A
+// tile that lies whole in a range is written out; of the others, one at each end
+// of a range at most, normalised partial results go to the workspace and the
+// combine joins them. Units of the first i tiles of a sequence have a closed form,
+// so that nothing is kept for a tile.
+//
+// Masks: a row's keys end where its token does, within the last 128 + 3 keys of
+// its tile. Logits behind it become weights of zero; V's rows behind the tile's
+// last token are zeroed, and of those that only some of its tokens see, up to
+// three, values that are no numbers become zeros, which the rows that see them get
+// added at the end: 0 * NaN of a later token never reaches an earlier one.
+//
+// Warp roles:
+//   warps 0-7  softmax and output: thread = row = TMEM lane; warp w and w + 4
+//              share 32 rows, 64 keys of a unit each.
+//   warp 8     producer (TMA, each CTA its own halves, completing on the leader's
+//              barriers).
+//   warp 9     TMEM allocation, and MMA issue (one thread of the leader's; the
+//              other CTA's leaves the combine where the parts are).
+//   warp 10    V's rows behind the tile's last token and those that not all see.
+//   warps 10-13 (E4M3 and E2M1 caches, instead) V codes to f16, with the same.
+// Every wait is bounded (the wait budget), as in the split kernel.
+//
+// E4M3 and E2M1 caches: S is 8-bit MMAs (kind::f8f6f4) on the raw K codes, with Q
+// as two E4M3 terms under a power of two per row, split in shared memory when a
+// tile begins; V's codes times their scales become f16, and P is f16 as well (the
+// shared-prefix kernel says why).
+#include <cuda_fp4.h>
+#include <type_traits>
+
+#include "mfa_serving.hpp"
+#include "tc_pair.cuh"
+
+namespace mfa {
+namespace {
+
+constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kTailWarp = 10, kConvertWarps = 4;
+template <int kFmt>
+constexpr bool kQuant = kFmt != kKvBf16;
+template <int kFmt>
+__host__ __device__ constexpr int threads() { return 32 * (kTailWarp + (kQuant<kFmt> ? kConvertWarps : 1)); }
+// Two K and two V slots, of even and odd units, one CTA's half of a unit each: K one page of 256 dims, V 128 dims of two
+// pages. E2M1 codes lie in shared memory as the 4-bit operands do, 16 codes in 8 bytes and 8 unused ones behind them.
+template <int kFmt>
+__host__ __device__ constexpr uint32_t slot_bytes() { return kQuant<kFmt> ? 16384 : 32768; }
+template <int kFmt>
+__host__ __device__ constexpr uint32_t slot_tx() { return kFmt == kKvE2M1 ? 8192 : slot_bytes<kFmt>(); }  // as copied
+constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;  // V as the MMAs read it, 16 bits
+constexpr int kTokens = kChunkTileTokens;
+constexpr int kScaleSlots = 4, kScaleBytes = 1024;  // quantised: 128 K scales and 128 V scales a unit
+constexpr int kQBytes = 65536;                      // 128 rows x 256 dims, four 64-dim blocks of [128 rows x 128 B]
+constexpr int kQBlockTokenBytes = 8192;             // one token's rows of a block
+static_assert(kTokens * kHeads == 256, "rows of a tile");
+
+enum Bar {
+  KFull = 0,                 // [2] leader: both CTAs' halves landed
+  VFull = KFull + 2,         // [2] leader; quantised: one arrival per converting warp of the pair
+  QFull = VFull + 2,         // [4] bf16: leader, by 64-dim block; quantised: the first, of both, each its own rows
+  QFree = QFull + 4,         // [4] bf16, both: the last S of a piece has read the block
+  QReady = QFree + 4,        // quantised, leader: Q split into terms, one arrival per softmax warp of the pair
+  SFull,                     // [2] both: S of even and odd units
+  PFull = SFull + 2,         // [2] leader: one arrival per softmax warp of the pair
+  PvDone = PFull + 2,        // [2] both: P V of even and odd units
+  OFree = PvDone + 2,        // leader: O has been read, one arrival per softmax warp of the pair
+  Drain,                     // leader
+  ScFull,                    // [kScaleSlots] quantised, both
+  ScEmpty = ScFull + kScaleSlots,   // [kScaleSlots] one arrival per softmax and converting warp of the CTA
+  TailFull = ScEmpty + kScaleSlots, // [2] both: this CTA's V of a tile's end landed (by V slot)
+  TailReady = TailFull + 2,         // [2] leader: it has been seen to, one arrival a CTA
+  RawFull = TailReady + 2,          // [2] quantised, both: this CTA's V codes landed
+  RawEmpty = RawFull + 2,           // [2] one arrival per converting warp of the CTA
+  kBars = RawEmpty + 2
+};
+
+// The line of work as every CTA sees it.
+constexpr int kPlanChunks = kMaxBatch / 32 + 1;
+struct PlanSmem {
+  int32_t cost[kMaxBatch + 1];  // units of the sequences before b; [B]: of all
+  int32_t row[kMaxBatch + 1];   // first row of sequence b's tokens, non-decreasing within [0, max_tokens]
+  int32_t len[kMaxBatch];       // positions that its pages hold
+  int32_t last[kPlanChunks + 1], total[kPlanChunks + 1];  // of 32 sequences
+};
+
+template <int kFmt>
+struct Smem {
+  static constexpr uint32_t k = 0;
+  static constexpr uint32_t v = k + 2 * slot_bytes<kFmt>();
+  static constexpr uint32_t raw = v + 2 * kVSlotBytes;  // quantised: V codes
+  static constexpr uint32_t q = raw + (kQuant<kFmt> ? 2 * slot_bytes<kFmt>() : 0);
+  static constexpr uint32_t scales = q + kQBytes;
+  static constexpr uint32_t plan = scales + (kQuant<kFmt> ? kScaleSlots * kScaleBytes : 0);
+  static constexpr uint32_t red = (plan + (uint32_t)sizeof(PlanSmem) + 15) & ~15u;  // [4][128] exchange of the row halves
+  static constexpr uint32_t bars = red + 4 * 128 * 4;
+  static constexpr uint32_t odd = bars + 8 * kBars;  // [4] pieces with values that are no numbers (set_odd)
+  static constexpr uint32_t misc = odd + 16;         // TMEM base, abort flag
+  static constexpr uint32_t total = misc + 8;
+};
+static_assert(Smem<kKvBf16>::total + 1024 <= 227 * 1024 && Smem<kKvE4M3>::total + 1024 <= 227 * 1024, "shared memory");
+
+struct Ctx {
+  uint32_t base, bar0, odd, rank;
+  volatile int* abort;
+  uint32_t* err;
+  uint64_t budget;
+  __device__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
+  __device__ uint32_t leader_bar(int i) const { return map_to_leader(bar(i)); }
+  __device__ bool wait(int i, uint32_t parity) const { return mbar_wait(bar(i), parity, budget, abort, err); }
+  // the same for a whole warp, whose lanes give up together
+  __device__ bool wait_warp(int i, uint32_t parity) const { return __all_sync(0xffffffffu, wait(i, parity)); }
+};
+
+// Rows of a tile's end held values that are no numbers: told to both CTAs' softmax warps, by piece. They look behind the
+// piece's last P V, which waits for the arrival behind this; a fourth piece is not begun before they have. Rare.
+__device__ __noinline__ void set_odd(uint32_t odd, uint32_t piece) {
+#pragma unroll 1
+  for (uint32_t r = 0; r < 2; ++r) {
+    uint32_t at;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(odd + 4 * (piece & 3)), "r"(r));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(piece + 1) : "memory");
+  }
+  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- plan
+// Tile i of a sequence whose chunk of n tokens stands behind a others sees a + min(4 (i + 1), n) keys. Of the tiles that
+// are full, the first i take, with z = floor((a + 127) / 4),
+//     sum_{k = 1..i} ceil((a + 4 k) / 128) = sum_{k = 1..i} floor((k + z) / 32) = G(i + z) - G(z)
+// units, G(m) = sum_{k = 0..m} floor(k / 32); modulo 2^32, and the host has seen to it that the sums stay below 2^31.
+__device__ __forceinline__ uint32_t floor_sum(uint32_t m) {
+  const uint32_t q = m >> 5;
+  return 16 * q * (q - 1) + q * ((m & 31) + 1);
+}
+__device__ __forceinline__ int units_of(int keys) { return (keys + kUnitKeys - 1) / kUnitKeys; }
+__device__ __forceinline__ int full_tiles_cost(int i, int a) {
+  const uint32_t z = (uint32_t)(a + kUnitKeys - 1) >> 2;
+  return (int)(floor_sum((uint32_t)i + z) - floor_sum(z)) + i * kChunkPieceUnits;
+}
+__device__ __forceinline__ int tiles_of(int n) { return (n + kTokens - 1) / kTokens; }
+__device__ __forceinline__ int sequence_cost(int len, int n) {
+  return n > 0 ? full_tiles_cost(tiles_of(n) - 1, len - n) + units_of(len) + kChunkPieceUnits : 0;
+}
+// Tokens of b that see a key at all: the last len of them.
+__device__ __forceinline__ int seeing(const PlanSmem& s, int b) { return min(s.row[b + 1] - s.row[b], s.len[b]); }
+
+// All threads; ends with a barrier.
+__device__ void build_plan(const ChunkParams& p, PlanSmem& s, uint32_t* err) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, kThreads = blockDim.x;
+  const int starts = (p.B + 32) / 32, chunks = (p.B + 31) / 32;  // 32 at a time, a warp each
+#pragma unroll 1
+  for (int c = warp; c < starts; c += warps) {
+    const int i = 32 * c + lane, raw = i <= p.B ? __ldcg(p.q_starts + i) : 0;
+    int x = min(max(raw, 0), p.max_tokens);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x = max(x, y);
+    }
+    if (i <= p.B) {
+      if (x != raw) raise_error(err, MFA_DEVERR_CAPACITY);
+      s.row[i] = x;
+    }
+    if (lane == 31) s.last[c] = x;
+  }
+  // (from the other end of the block, so that neither waits for the other's loads)
+  for (int b = kThreads - 1 - threadIdx.x; b < p.B; b += kThreads)
+    s.len[b] = clamp_len(__ldcg(p.seq_lens + b), p.max_pages * kPageSize, err);
+  __syncthreads();
+  if (starts > 1) {
+#pragma unroll 1
+    for (int c = warp; c < starts; c += warps) {
+      const int i = 32 * c + lane, before = __reduce_max_sync(0xffffffffu, lane < c ? s.last[lane] : 0);
+      if (i <= p.B && s.row[i] < before) {
+        raise_error(err, MFA_DEVERR_CAPACITY);
+        s.row[i] = before;
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll 1
+  for (int c = warp; c < chunks; c += warps) {
+    const int b = 32 * c + lane, u = b < p.B ? sequence_cost(s.len[b], seeing(s, b)) : 0;
+    const int x = warp_inclusive_sum(u, lane);
+    if (b < p.B) s.cost[b] = x - u;
+    if (b == p.B - 1) s.cost[p.B] = x;
+    if (lane == 31) s.total[c] = x;
+  }
+  __syncthreads();
+  if (chunks > 1) {
+#pragma unroll 1
+    for (int c = warp; c < chunks; c += warps) {
+      const int b = 32 * c + lane, before = __reduce_add_sync(0xffffffffu, lane < c ? s.total[lane] : 0);
+      if (b < p.B) s.cost[b] += before;
+      if (b == p.B - 1) s.cost[p.B] += before;
+    }
+    __syncthreads();
+  }
+}
+
+// Pairs that have work: with fewer units than pairs, every range holds one.
+__device__ __forceinline__ int busy_pairs(const ChunkParams& p, int units) { return min(p.pairs, max(units, 1)); }
+
+// A pair's pieces, in order: units [u0, u1) of one row tile.
+struct Piece {
+  int b = -1, i;     // sequence, tile of it
+  int a, n, row0;    // of the sequence: positions before its chunk, tokens that see any, the first one's row
+  int row, tokens;   // of the tile: first row, tokens (1 to 4)
+  int seen0, seen;   // keys that its first and its last token see
+  int units;         // of the whole tile
+  int u0, u1;
+  int first, x;      // line positions: the tile's, and the one behind it
+  __device__ int pages() const { return (seen + kPageSize - 1) / kPageSize; }
+  __device__ int keys(int page) const { return min(max(seen - page * kPageSize, 0), kPageSize); }
+  // Whether V of unit u holds rows that not all tokens see, up to the end of an MMA's 16 keys.
+  __device__ bool ends(int u) const { return (u + 1) * kUnitKeys > seen0 && (tokens > 1 || (seen % kKeyStep) != 0); }
+  __device__ bool whole() const { return u0 == 0 && u1 == units; }
+};
+__device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem& s, int lo, int hi, Piece& q) {
+  if (q.b < 0) q.x = lo;
+  while (q.x < hi) {
+    if (q.b < 0 || q.x >= s.cost[q.b + 1]) {
+      const int b = last_at_most(s.cost, p.B, q.x);
+      q.b = b;
+      q.n = seeing(s, b);
+      q.a = s.len[b] - q.n;
+      q.row0 = s.row[b + 1] - q.n;
+      q.first = s.cost[b];
+      int i0 = 0, i1 = tiles_of(q.n) - 1;  // the last tile that begins at or before x
+      if (q.x == q.first) i1 = 0;
+      while (i0 < i1) {
+        const int mid = (i0 + i1 + 1) >> 1;
+        if (q.first + full_tiles_cost(mid, q.a) <= q.x) i0 = mid; else i1 = mid - 1;
+      }
+      q.i = i0;
+      q.first += full_tiles_cost(i0, q.a);
+    } else {
+      ++q.i;
+      q.first = q.x;
+    }
+    q.tokens = min(kTokens, q.n - kTokens * q.i);
+    q.row = q.row0 + kTokens * q.i;
+    q.seen0 = q.a + kTokens * q.i + 1;
+    q.seen = q.seen0 + q.tokens - 1;
+    q.units = units_of(q.seen);
+    q.u0 = max(0, q.x - q.first - kChunkPieceUnits);
+    q.u1 = min(q.units, hi - q.first - kChunkPieceUnits);
+    q.x = q.first + kChunkPieceUnits + q.units;
+    if (q.u0 < q.u1) return true;
+  }
+  return false;
+}
+
+// Where the combine finds the partial results of the tile that begins in this pair's range and ends behind it; and the
+// output of tokens that see no key. One warp of each pair.
+__device__ void publish_plan(const ChunkParams& p, const PlanSmem& s, int pair, int lo, int hi, int lane) {
+  const int units = s.cost[p.B], W = busy_pairs(p, units);
+  if (lane == 0) {
+    int4 part = make_int4(0, 0, 0, 0);
+    if (lo < hi) {
+      Piece q;
+      if (next_piece(p, s, hi - 1, hi, q) && q.u1 < q.units) {
+        const bool begins = lo <= q.first + kChunkPieceUnits;
+        if (begins) part = make_int4(q.row, q.tokens, pair, pair_of_unit(q.first + kChunkPieceUnits + q.units - 1, units, W) - pair + 1);
+      }
+    }
+    p.parts[pair] = part;
+  }
+  for (int b = pair; b < p.B; b += p.pairs) {
+    const int none = s.row[b + 1] - s.row[b] - seeing(s, b);
+    for (int t = 0; t < none; ++t) {
+      const size_t row = (size_t)(s.row[b] + t) * kHeads;
+      uint4* out = reinterpret_cast<uint4*>(p.out + row * kHeadDim);
+      for (int i = lane; i < kHeads * kHeadDim / 8; i += 32) out[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = lane; i < kHeads; i += 32) p.lse[row + i] = -INFINITY;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- producer
+// Page ids of a piece: a window of 64 held by the warp (32 ahead of need). Those that a piece begins with are asked for
+// when the piece before it begins.
+struct TilePages {
+  int end, base, a, b;
+  __device__ static int load(int k, int end, const ChunkParams& p, const Piece& q) {
+    return k < end ? __ldcg(p.page_table + (size_t)q.b * p.max_pages + k) : 0;
+  }
+  __device__ static int end_of(const Piece& q) { return min(q.pages(), 2 * q.u1); }
+  __device__ int checked(int id, const ChunkParams& p) const {
+    if (id >= 0 && id < p.num_pages) return id;
+    raise_error(p.err, MFA_DEVERR_PAGE);
+    return 0;
+  }
+  __device__ void start(int x, int y, const ChunkParams& p, const Piece& q) {
+    end = end_of(q);
+    base = 2 * q.u0;
+    a = checked(x, p);
+    b = checked(y, p);
+  }
+  __device__ int get(int k, const ChunkParams& p, const Piece& q, int lane) {
+    while (k >= base + 64) {
+      base += 32;
+      a = b;
+      b = checked(load(base + 32 + lane, end, p, q), p);
+    }
+    const int i = k - base;
+    return i < 32 ? __shfl_sync(0xffffffffu, a, i) : __shfl_sync(0xffffffffu, b, i - 32);
+  }
+};
+
+template <int kFmt>
+__device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
+                              const CUtensorMap* qmap, const Ctx& cx, const PlanSmem& s, int lo, int hi) {
+  using Sm = Smem<kFmt>;
+  constexpr bool kQ8 = kQuant<kFmt>;
+  constexpr uint32_t kSlot = slot_bytes<kFmt>(), kPage = kSlot / 2, kTx = slot_tx<kFmt>();
+  constexpr int kCols = kQ8 ? 128 : 64;  // columns of a copy: 128 bytes of shared memory a row
+  const int lane = threadIdx.x & 31, r = (int)cx.rank;
+  const uint64_t pol = policy_evict_normal();
+  uint32_t pieces = 0, tails[2] = {0, 0};
+  // K of unit `n` (and its scales): this CTA's page, page r of the two, on the leader's barrier, on which the leader
+  // announces the bytes of both CTAs
+  auto load_k = [&](uint32_t n, int pa, int pb) -> bool {
+    const uint32_t slot = n & 1;
+    if (n >= 2 && !cx.wait_warp(SFull + slot, ((n >> 1) & 1) ^ 1)) return false;
+    const int page = r == 0 ? pa : pb;
+    if (elect_one()) {
+      const uint32_t dst = cx.base + Sm::k + slot * kSlot, bar = cx.leader_bar(KFull + slot);
+      if (r == 0) mbar_arrive_expect_tx(cx.bar(KFull + slot), pb >= 0 ? 2 * kTx : kTx);
+      if (page >= 0)
+#pragma unroll
+        for (int d = 0; d < kHeadDim / kCols; ++d)
+          tma_load_2d_pair(dst + d * 8192, kmap, d * kCols, page * kPageSize, bar, pol);
+    }
+    if constexpr (kQ8) {  // the scales of all the unit's keys, for this CTA's rows
+      const uint32_t sc_slot = n % kScaleSlots;
+      if (!cx.wait_warp(ScEmpty + sc_slot, ((n / kScaleSlots) & 1) ^ 1)) return false;
+      if (elect_one()) {
+        const uint32_t sc = cx.base + Sm::scales + sc_slot * kScaleBytes, sb = cx.bar(ScFull + sc_slot);
+        constexpr uint32_t kPageScales = kPageSize * sizeof(float);
+        mbar_arrive_expect_tx(sb, (pb >= 0 ? 4 : 2) * kPageScales);
+        bulk_load(sc, p.k_scale + (size_t)pa * kPageSize, kPageScales, sb);
+        bulk_load(sc + 512, p.v_scale + (size_t)pa * kPageSize, kPageScales, sb);
+        if (pb >= 0) {
+          bulk_load(sc + kPageScales, p.k_scale + (size_t)pb * kPageSize, kPageScales, sb);
+          bulk_load(sc + 512 + kPageScales, p.v_scale + (size_t)pb * kPageSize, kPageScales, sb);
+        }
+      }
+    }
+    return true;
+  };
+  // V of unit `n`: this CTA's 128 dims of each page. That of a tile's end lands on this CTA's own barrier, for the warp
+  // that sees to its rows; quantised: all of it does, for the warps that convert it.
+  auto load_v = [&](uint32_t n, int pa, int pb, bool tail) -> bool {
+    const uint32_t slot = n & 1, parity = ((n >> 1) & 1) ^ 1, bytes = pb >= 0 ? kTx : kTx / 2;
+    uint32_t dst, bar;
+    if constexpr (kQ8) {
+      if (!cx.wait_warp(RawEmpty + slot, parity)) return false;
+      dst = cx.base + Sm::raw + slot * kSlot;
+      bar = cx.bar(RawFull + slot);
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+    } else {
+      if (n >= 2 && !cx.wait_warp(PvDone + slot, parity)) return false;
+      dst = cx.base + Sm::v + slot * kSlot;
+      bar = tail ? cx.bar(TailFull + slot) : cx.leader_bar(VFull + slot);
+      if (lane == 0 && r == 0) mbar_arrive_expect_tx(cx.bar(VFull + slot), tail ? 0 : 2 * bytes);
+      if (lane == 0 && tail) mbar_arrive_expect_tx(bar, bytes);
+      tails[slot] += tail;
+    }
+    if (elect_one())
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (i == 0 || pb >= 0)
+#pragma unroll
+          for (int d = 0; d < 128 / kCols; ++d)
+            tma_load_2d_pair(dst + i * kPage + d * 8192, vmap, r * 128 + d * kCols, (i ? pb : pa) * kPageSize, bar, pol);
+    return true;
+  };
+  uint32_t cnt = 0;  // units whose K has been loaded
+  // Q of a piece, this CTA's tokens of it: by block, as the piece before is done with each (quantised: with all of them)
+  auto load_q = [&](const Piece& q) -> bool {
+    const int here = min(2, max(0, q.tokens - 2 * r));
+    if (kQ8 && pieces > 0 && !cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1)) return false;
+    if (kQ8 && lane == 0) mbar_arrive_expect_tx(cx.bar(QFull), here * 4 * kQBlockTokenBytes);
+#pragma unroll 1
+    for (int d = 0; d < 4; ++d) {
+      if (!kQ8 && pieces > 0 && !cx.wait_warp(QFree + d, (pieces - 1) & 1)) return false;
+      if (elect_one()) {
+        if (!kQ8 && r == 0) mbar_arrive_expect_tx(cx.bar(QFull + d), q.tokens * kQBlockTokenBytes);
+        const uint32_t bar = kQ8 ? cx.bar(QFull) : cx.leader_bar(QFull + d);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (h < here)
+            tma_load_2d_pair(cx.base + Sm::q + d * 16384 + h * 8192, qmap, d * 64, (q.row + 2 * r + h) * kHeads, bar, pol);
+      }
+    }
+    ++pieces;
+    return true;
+  };
+  int va = -1, vb = -1;  // the last unit: its V is still to be loaded (V trails K by a unit, as the MMAs use them)
+  bool vtail = false, good = true;
+  Piece q, next;
+  bool more = next_piece(p, s, lo, hi, next);
+  int na = 0, nb = 0;
+  auto ask = [&]() {  // what the next piece begins with
+    const int end = TilePages::end_of(next);
+    na = TilePages::load(2 * next.u0 + lane, end, p, next);
+    nb = TilePages::load(2 * next.u0 + 32 + lane, end, p, next);
+  };
+  if (more) {
+    ask();
+    good = load_q(next);
+  }
+  while (good && more) {
+    q = next;
+    TilePages ids;
+    ids.start(na, nb, p, q);
+    more = next_piece(p, s, lo, hi, next);
+    if (more) {
+      ask();
+      const int here = min(2, max(0, next.tokens - 2 * r));  // its Q, into L2
+      if (here > 0 && lane == 0)
+        prefetch_l2(p.q + (size_t)(next.row + 2 * r) * kHeads * kHeadDim, here * kHeads * kHeadDim * 2);
+    }
+    for (int u = q.u0; good && u < q.u1; ++u) {
+      const int pa = ids.get(2 * u, p, q, lane);
+      const int pb = 2 * u + 1 < q.pages() ? ids.get(2 * u + 1, p, q, lane) : -1;
+      good = load_k(cnt, pa, pb);
+      if (good && va >= 0) good = load_v(cnt - 1, va, vb, vtail);
+      if (good && u == q.u0 && cnt > 0) good = load_q(q);
+      ++cnt;
+      va = pa;
+      vb = pb;
+      vtail = q.ends(u);
+    }
+  }
+  if (good && va >= 0) good = load_v(cnt - 1, va, vb, vtail);
+  // Every copy of both CTAs must land before either leaves: this CTA's barriers and the leader's tell, and the other CTA
+  // stays until the cluster's last barrier.
+  if (lane == 0) {
+    for (uint32_t k = cnt > 2 ? cnt - 2 : 0; k < cnt; ++k) {
+      if (r == 0) (void)mbar_wait(cx.bar(KFull + (k & 1)), (k >> 1) & 1, kDrainNs, nullptr, p.err);
+      if ((kQ8 || r == 0) && (good || k + 1 < cnt))
+        (void)mbar_wait(cx.bar((kQ8 ? RawFull : VFull) + (k & 1)), (k >> 1) & 1, kDrainNs, nullptr, p.err);
+    }
+    for (int i = 0; i < 2; ++i)
+      if (tails[i]) (void)mbar_wait(cx.bar(TailFull + i), (tails[i] - 1) & 1, kDrainNs, nullptr, p.err);
+    if constexpr (kQ8)
+      for (uint32_t k = cnt > (uint32_t)kScaleSlots ? cnt - kScaleSlots : 0; k < cnt; ++k)
+        (void)mbar_wait(cx.bar(ScFull + k % kScaleSlots), (k / kScaleSlots) & 1, kDrainNs, nullptr, p.err);
+    if (pieces && (kQ8 || r == 0))
+      for (int d = 0; d < (kQ8 ? 1 : 4); ++d) (void)mbar_wait(cx.bar(QFull + d), (pieces - 1) & 1, kDrainNs, nullptr, p.err);
+  }
+  __syncwarp();
+}
+
+// ---------------------------------------------------------------- V at a tile's end
+__device__ __forceinline__ bool not_number_bf16(uint32_t two) {
+  return (two & 0x7F80u) == 0x7F80u || (two & 0x7F800000u) == 0x7F800000u;
+}
+__device__ __forceinline__ bool not_number_f16(uint32_t two) {
+  return (two & 0x7C00u) == 0x7C00u || (two & 0x7C000000u) == 0x7C000000u;
+}
+// bf16 words without the halves that are no numbers.
+__device__ __forceinline__ uint32_t numbers_bf16(uint32_t two) {
+  return ((two & 0x7F80u) == 0x7F80u ? 0u : two & 0xFFFFu) | ((two & 0x7F800000u) == 0x7F800000u ? 0u : two & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint32_t numbers_f16(uint32_t two) {
+  return ((two & 0x7C00u) == 0x7C00u ? 0u : two & 0xFFFFu) | ((two & 0x7C000000u) == 0x7C000000u ? 0u : two & 0xFFFF0000u);
+}
+
+__device__ void tail_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int lo, int hi) {
+  const int lane = threadIdx.x & 31;
+  uint32_t cnt = 0, tails[2] = {0, 0}, piece = 0;
+  Piece q;
+  for (; next_piece(p, s, lo, hi, q); ++piece) {
+    for (int u = q.u0; u < q.u1; ++u, ++cnt) {
+      if (!q.ends(u)) continue;
+      const uint32_t slot = cnt & 1;
+      if (!cx.wait_warp(TailFull + slot, tails[slot] & 1)) return;
+      ++tails[slot];
+      const uint32_t unit = cx.base + Smem<kKvBf16>::v + slot * kVSlotBytes;
+      bool odd = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int first = (2 * u + i) * kPageSize, keys = q.keys(2 * u + i);
+        const uint32_t page = unit + i * kVPageBytes;
+        // rows that not all tokens see: two at a time, 16 bytes of two 64-dim chunks a lane
+        for (int row = max(0, q.seen0 - first) + (lane >> 4); row < keys; row += 2) {
+          const uint32_t at = page + ((lane >> 3) & 1) * 8192 + row * 128 + (lane & 7) * 16;
+          const uint4 v = ld_shared_v4(at);
+          if (not_number_bf16(v.x) || not_number_bf16(v.y) || not_number_bf16(v.z) || not_number_bf16(v.w)) {
+            const uint32_t w[4] = {numbers_bf16(v.x), numbers_bf16(v.y), numbers_bf16(v.z), numbers_bf16(v.w)};
+            st_shared_v4(at, w);
+            odd = true;
+          }
+        }
+        if (is_partial(keys)) {
+          const int words = (kKeyStep - keys % kKeyStep) * 8;  // 16 B words of a 64-dim chunk's rows
+          for (int w = lane; w < words * 2; w += 32)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(page + keys * 128 + (w / words) * 8192 + (w % words) * 16), "r"(0)
+                         : "memory");
+        }
+      }
+      if (odd) set_odd(cx.odd, piece);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair(cx.leader_bar(TailReady + slot));
+    }
+  }
+}
+
+// Quantised: V of a unit as P V reads it, f16 of code * scale * 2^kScaleUp without the scale's shift, from the codes: per page
+// [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both with the 128-byte swizzle. A thread takes 16 codes of
+// a row and of every 16th row after it; rows behind the tile's last token become zeros. Which rows eight neighbouring threads
+// take keeps reads and writes on banks of their own, as in the shared-prefix kernel.
+template <int kFmt>
+__device__ void convert_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int lo, int hi, const uint8_t* gbase) {
+  using Sm = Smem<kFmt>;
+  const int lane = threadIdx.x & 31, t = threadIdx.x - 32 * kTailWarp;
+  const int row0 = (2 * (t >> 4)) ^ (t & 4 ? 5 : 0);
+  const int c = (t & 3) | ((t >> 1) & 4);  // 16-code chunk: dims [16 c, 16 c + 16)
+  const uint32_t from = row0 * 128 + ((c ^ (row0 & 7)) << 4);  // rows 16 apart share the swizzle
+  const uint32_t to = (c >> 2) * 8192 + row0 * 128;
+  const uint32_t to0 = to + (((2 * (c & 3)) ^ (row0 & 7)) << 4), to1 = to + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4);
+  uint32_t n = 0, piece = 0;
+  Piece q;
+  for (; next_piece(p, s, lo, hi, q); ++piece) {
+    for (int u = q.u0; u < q.u1; ++u, ++n) {
+      const uint32_t slot = n & 1, sc_slot = n % kScaleSlots;
+      const uint32_t src = cx.base + Sm::raw + slot * slot_bytes<kFmt>() + from, dst = cx.base + Sm::v + slot * kVSlotBytes;
+      const float* sc = reinterpret_cast<const float*>(gbase + Sm::scales + sc_slot * kScaleBytes) + kUnitKeys;
+      if (!cx.wait_warp(ScFull + sc_slot, (n / kScaleSlots) & 1)) return;
+      if (!cx.wait_warp(RawFull + slot, (n >> 1) & 1)) return;
+      if (n >= 2 && !cx.wait_warp(PvDone + slot, ((n >> 1) & 1) ^ 1)) return;
+      const bool ends = q.ends(u);
+      bool odd = false;
+#pragma unroll
+      for (int page = 0; page < 2; ++page) {
+        const int valid = q.keys(2 * u + page);
+        uint4 v[4];
+        __half2 scale[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
+          const float s = sc[page * kPageSize + row0 + 16 * i];
+          scale[i] = __float2half2_rn(s * exp2_int(kScaleUp - scale_shift(s)));
+        }
+        if (valid < kPageSize) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (row0 + 16 * i >= valid) {
+              v[i] = make_uint4(0u, 0u, 0u, 0u);
+              scale[i] = __float2half2_rn(0.0f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+          uint32_t h[2][4];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            __half2_raw r;
+            if constexpr (kFmt == kKvE2M1)
+              r = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[k >> 2] >> (8 * (k & 3))), __NV_E2M1);
+            else
+              r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r), scale[i]);
+            h[k >> 2][k & 3] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          if (ends && (2 * u + page) * kPageSize + row0 + 16 * i >= q.seen0) {  // a row that not all tokens see
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              odd |= not_number_f16(h[k >> 2][k & 3]);
+              h[k >> 2][k & 3] = numbers_f16(h[k >> 2][k & 3]);
+            }
+          }
+          st_shared_v4(dst + page * kVPageBytes + i * 2048 + to0, h[0]);
+          st_shared_v4(dst + page * kVPageBytes + i * 2048 + to1, h[1]);
+        }
+      }
+      if (odd) set_odd(cx.odd, piece);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(cx.bar(RawEmpty + slot));
+        mbar_arrive(cx.bar(ScEmpty + sc_slot));
+        mbar_arrive_pair(cx.leader_bar(VFull + slot));
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- MMA issue (one thread of the leader)
+template <int kFmt>
+__device__ void mma_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int lo, int hi, uint32_t tmem) {
+  constexpr bool kQ8 = kQuant<kFmt>;
+  // A = Q, B = K, both K-major (8-bit kinds: formats 0, E4M3, and 5, E2M1); A = P (TMEM), B = V (dim-major; format 0: f16)
+  constexpr uint32_t idesc_s = idesc_f16(256, kSCols, kQ8 ? 0 : 1, 0, 0) | (kFmt == kKvE2M1 ? 5u << 10 : 0u);
+  constexpr uint32_t idesc_o = idesc_f16(256, kHeadDim, kQ8 ? 0 : 1, 0, 1);
+  using Sm = Smem<kFmt>;
+  uint32_t pieces = 0, s_cnt = 0, p_cnt = 0, tails[2] = {0, 0};
+  // Descriptors of the operands' first blocks; a block `bytes` further on has bytes / 16 more in the address field, which
+  // holds every shared address without a carry.
+  auto ahead = [](uint64_t desc, uint32_t bytes) -> uint64_t { return desc + (bytes >> 4); };
+  const uint64_t q_desc = smem_desc_sw128(cx.base + Sm::q, 16, 1024);
+  const uint64_t k_desc0 = smem_desc_sw128(cx.base + Sm::k, 16, 1024);
+  const uint64_t v_desc0 = smem_desc_sw128(cx.base + Sm::v, 8192, 1024);
+  // What this thread does between two batches of MMAs costs nothing as long as it is short: barriers are looked at in the
+  // middle of a batch, for the next one, and waited for only if that found them not yet done.
+  bool k_ready = false, pv_ready = false;
+  auto peek = [&](int i, uint32_t parity) -> bool { return mbar_test_wait(cx.bar(i), parity); };
+  auto peek_pv = [&]() -> bool { return peek(VFull + (p_cnt & 1), (p_cnt >> 1) & 1) && peek(PFull + (p_cnt & 1), (p_cnt >> 1) & 1); };
+  // S of unit s_cnt; p_next: a P V is to follow; first, last: of its piece
+  auto do_s = [&](bool p_next, bool first, bool last) -> bool {
+    const uint32_t buf = s_cnt & 1, d = tmem + buf * kSCols;  // its last reader, P V of two units ago, was issued before
+    if (!k_ready && !cx.wait(KFull + buf, (s_cnt >> 1) & 1)) return false;
+    k_ready = false;
+    tc_fence_after();
+    const uint64_t k_desc = ahead(k_desc0, buf * slot_bytes<kFmt>());
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (!kQ8 && first && !cx.wait(QFull + e, pieces & 1)) return false;
+      if (e == 2) pv_ready = p_next && peek_pv();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if constexpr (kQ8)  // Q's term e / 2, 128-dim half e % 2, 32 dims
+          tc_mma_pair_f8(d, ahead(q_desc, (e & 1) * 32768 + (e >> 1) * 16384 + kk * 32), ahead(k_desc, (e & 1) * 8192 + kk * 32), idesc_s,
+                         (e | kk) != 0);
+        else  // 64-dim block, 16 dims
+          tc_mma_pair(d, ahead(q_desc, e * 16384 + kk * 32), ahead(k_desc, e * 8192 + kk * 32), idesc_s, (e | kk) != 0);
+      }
+      if (!kQ8 && last) tc_commit_pair(cx.bar(QFree + e));
+    }
+    tc_commit_pair(cx.bar(SFull + buf));
+    ++s_cnt;
+    return true;
+  };
+  struct Unit {  // whose P V is still to be issued
+    int keys[2];
+    bool pending, first, ends;
+    uint32_t piece;
+  };
+  auto do_pv = [&](const Unit& v) -> bool {
+    constexpr int kSteps = kPageSize / kKeyStep;
+    const uint32_t buf = p_cnt & 1, a = tmem + buf * kSCols, d = tmem + kTmemO;
+    if (v.first && !cx.wait(OFree, (v.piece & 1) ^ 1)) return false;
+    if (!kQ8 && v.ends && !cx.wait(TailReady + buf, tails[buf]++ & 1)) return false;
+    if (!pv_ready && !(cx.wait(VFull + buf, (p_cnt >> 1) & 1) && cx.wait(PFull + buf, (p_cnt >> 1) & 1))) return false;
+    pv_ready = false;
+    tc_fence_after();
+    const uint64_t v_desc = ahead(v_desc0, buf * kVSlotBytes);
+    auto a_of = [&](int i, int kk) { return a + i * 64 + (kk >> 1) * 32 + (kk & 1) * 8; };  // page i, step kk
+    if (v.keys[1] == kPageSize) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int kk = 0; kk < kSteps; ++kk)
+          tc_mma_pair_tmem_a(d, a_of(i, kk), ahead(v_desc, i * kVPageBytes + kk * 2048), idesc_o, (i | kk) != 0 || !v.first);
+        if (i == 0) k_ready = peek(KFull + (s_cnt & 1), (s_cnt >> 1) & 1);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < 2; ++i) {
+        const int steps = ((i ? v.keys[1] : v.keys[0]) + kKeyStep - 1) / kKeyStep;
+#pragma unroll 1
+        for (int kk = 0; kk < steps; ++kk)
+          tc_mma_pair_tmem_a(d, a_of(i, kk), ahead(v_desc, i * kVPageBytes + kk * 2048), idesc_o, (i | kk) != 0 || !v.first);
+      }
+      k_ready = false;
+    }
+    tc_commit_pair(cx.bar(PvDone + buf));
+    ++p_cnt;
+    return true;
+  };
+  // Between two pieces: true if the next S can be issued, false if the last P V can and the next S not yet (`good` false:
+  // neither in time).
+  auto s_goes_first = [&](bool& good) -> bool {
+    const uint64_t t0 = globaltimer_ns();
+    for (bool again = false;; again = true) {
+      if (peek(QFull, pieces & 1) && peek(KFull + (s_cnt & 1), (s_cnt >> 1) & 1)) return true;
+      if (peek_pv()) return false;
+      if (*cx.abort) break;
+      if (again && globaltimer_ns() - t0 >= cx.budget) {
+        raise_error(cx.err, MFA_DEVERR_TIMEOUT);
+        *cx.abort = 1;
+        break;
+      }
+    }
+    good = false;
+    return true;
+  };
+  Piece q;
+  Unit pend{};
+  bool good = true;
+  while (good && next_piece(p, s, lo, hi, q)) {
+    for (int u = q.u0; good && u < q.u1; ++u) {
+      if (u == q.u0) {
+        // quantised: Q is split behind the last softmax, which takes longer than the last P V
+        if (pend.pending && (kQ8 || !s_goes_first(good)) && good) {
+          good = do_pv(pend);
+          pend.pending = false;
+        }
+        if (kQ8 && good) good = cx.wait(QReady, pieces & 1);
+        if (!good) break;
+      }
+      good = do_s(pend.pending, u == q.u0, u + 1 == q.u1);
+      if (good && pend.pending) good = do_pv(pend);
+      pend.pending = true;
+      pend.first = u == q.u0;
+      pend.ends = q.ends(u);
+      pend.piece = pieces;
+      pend.keys[0] = q.keys(2 * u);
+      pend.keys[1] = q.keys(2 * u + 1);
+    }
+    ++pieces;
+  }
+  if (good && pend.pending) (void)do_pv(pend);
+  tc_commit_pair(cx.bar(Drain));  // every MMA is done before TMEM is given back
+  (void)mbar_wait(cx.bar(Drain), 0, kDrainNs, nullptr, p.err);
+}
+
+// ---------------------------------------------------------------- softmax and output
+// What a piece leaves behind until its O is complete.
+struct Result {
+  Piece q;
+  RowState st;
+  uint32_t unit, piece;  // its last unit, its number
+  bool any = false;
+};
+
+// V of position k of the piece's sequence, if it is no number, else 0.
+template <int kFmt>
+__device__ float not_number(const ChunkParams& p, int b, int k, int dim) {
+  const int page = __ldcg(p.page_table + (size_t)b * p.max_pages + k / kPageSize);
+  const size_t slot = (size_t)(page >= 0 && page < p.num_pages ? page : 0) * kPageSize + k % kPageSize;
+  float v;
+  if constexpr (kFmt == kKvBf16) {
+    v = __uint_as_float((uint32_t)__ldcg(static_cast<const uint16_t*>(p.v_cache) + slot * kHeadDim + dim) << 16);
+  } else {
+    __half_raw h;
+    if constexpr (kFmt == kKvE4M3) {
+      h = __nv_cvt_fp8_to_halfraw(__ldcg(static_cast<const uint8_t*>(p.v_cache) + slot * kHeadDim + dim), __NV_E4M3);
+    } else {
+      const uint8_t two = __ldcg(static_cast<const uint8_t*>(p.v_cache) + (slot * kHeadDim + dim) / 2);
+      h = __nv_cvt_fp4_to_halfraw((__nv_fp4_storage_t)(dim & 1 ? two >> 4 : two & 15), __NV_E2M1);
+    }
+    v = __half2float(*reinterpret_cast<const __half*>(&h)) * __ldcg(p.v_scale + slot);
+  }
+  return fabsf(v) <= 3.402823466e38f ? 0.0f : v;
+}
+
+// The output of a piece whose end held values that are no numbers: O / l and, in the rows that see them, these values added
+// (a weight times one of them is one). Rare and out of line. part_row: of the partial results (null: the output itself).
+template <int kFmt>
+__device__ __noinline__ void write_odd(const ChunkParams& p, int b, int k0, int k1, uint32_t o_addr, float inv, size_t out_row,
+                                       float* part_row, bool valid, int half) {
+#pragma unroll 1
+  for (int c = 128 * half; c < 128 * half + 128; c += 16) {
+    float o[16];
+    tmem_ld16(o_addr + c, o);
+    tc_wait_ld();
+#pragma unroll 1
+    for (int k = k0; k < k1; ++k)
+#pragma unroll
+      for (int j = 0; j < 16; ++j) o[j] += not_number<kFmt>(p, b, k, c + j);
+    if (!valid) continue;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      if (part_row) part_row[c + j] = o[j] * inv;
+      else p.out[out_row * kHeadDim + c + j] = (uint16_t)(pack_bf16(o[j] * inv, 0.0f) & 0xFFFFu);
+    }
+  }
+}
+
+template <int kFmt>
+__device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi, uint32_t tmem,
+                             uint8_t* gbase) {
+  constexpr bool kQ8 = kQuant<kFmt>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int half = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
+  const int j = 2 * (int)cx.rank + (quad >> 1);  // token of the tile
+  const uint32_t lanes = (uint32_t)(32 * quad) << 16, o_addr = tmem + lanes + kTmemO;
+  const float c2 = p.scale == 0.0f && !kQ8 ? 1e-37f : p.scale * kLog2e;  // (0 times an infinity would be NaN)
+  const uint32_t p_full = cx.leader_bar(PFull), o_free = cx.leader_bar(OFree);
+  float* red = reinterpret_cast<float*>(gbase + Smem<kFmt>::red);
+  volatile uint32_t* odd = reinterpret_cast<volatile uint32_t*>(gbase + Smem<kFmt>::odd);
+  uint32_t cnt = 0, pieces = 0;  // units, pieces so far
+  // After a wait that gave up, the warp goes through the rest of its work without waiting, so that the warps that meet it
+  // at named barriers, which have no limit, do not wait for it in vain. What it computes is meaningless.
+  bool alive = true;
+  auto wait = [&](int bar, uint32_t parity) { alive = alive && cx.wait_warp(bar, parity); };
+  // P V of unit n. S of that unit is done, and with it every MMA issued before it, P V of two units earlier (the last on the
+  // same barrier) among them: the parity is exact.
+  auto wait_pv = [&](uint32_t n) { wait(PvDone + (n & 1), (n >> 1) & 1); };
+
+  // ---- O / l and its LSE, 128 dims a thread: to the output, or as a partial result
+  auto finish = [&](const Result& f) {
+    wait_pv(f.unit);
+    tc_fence_after();
+    red[half * 128 + row] = f.st.l;
+    if (!kQ8) red[256 + half * 128 + row] = f.st.l_p;
+    barrier_rows(quad);
+    const float l = f.st.l + red[(half ^ 1) * 128 + row];
+    const float l_p = kQ8 ? l : f.st.l_p + red[256 + (half ^ 1) * 128 + row];
+    // rows of a piece in which they see no key have O = 0 and no weight
+    const float inv = f.st.fresh ? 0.0f : kQ8 ? exp2_int(-kScaleUp) / l : 1.0f / l_p;
+    const float lse = (f.st.m + log2f(l)) * kLn2;
+    const bool valid = j < f.q.tokens, whole = f.q.whole();
+    const size_t out_row = (size_t)(f.q.row + j) * kHeads + (row & 63);
+    const size_t part = (size_t)(2 * pair + (f.q.u0 == 0)) * 256 + 128 * cx.rank + row;
+    if (valid && half == 0) {
+      if (whole) p.lse[out_row] = lse;
+      else p.part_lse[part] = lse;
+    }
+    bool freed = false;
+    auto free_o = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair(o_free);
+      freed = true;
+    };
+    if (odd[f.piece & 3] == f.piece + 1) {
+      // keys of this piece that not all of the tile's tokens see, up to this row's
+      const int k0 = max(f.q.seen0, f.q.u0 * kUnitKeys), k1 = min(f.q.seen0 + j, f.q.u1 * kUnitKeys);
+      write_odd<kFmt>(p, f.q.b, k0, valid ? k1 : k0, o_addr, inv, out_row, whole ? nullptr : p.part_o + part * kHeadDim, valid, half);
+    } else if (whole) {
+      // as bf16 into registers, so that O is free for the next tile's first P V before any of it is written
+      uint32_t w[64];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        float o[32];
+        tmem_ld32(o_addr + 128 * half + 32 * c, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k) w[16 * c + k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
+      }
+      free_o();
+      // four neighbouring lanes exchange theirs, so that each writes 32 B of four rows and together whole lines of them
+      if (valid) {
+        uint16_t* dst = p.out + (out_row - (lane & 3)) * kHeadDim + 128 * half + 16 * (lane & 3);
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+          float (&v)[32] = *reinterpret_cast<float (*)[32]>(w + 32 * g);
+          transpose_quad(v, lane);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint4* to = reinterpret_cast<uint4*>(dst + k * kHeadDim + 64 * g);
+            const uint32_t* from = w + 32 * g + 8 * k;
+            to[0] = make_uint4(from[0], from[1], from[2], from[3]);
+            to[1] = make_uint4(from[4], from[5], from[6], from[7]);
+          }
+        }
+      }
+    } else {
+      float* dst = p.part_o + (part - (lane & 3)) * kHeadDim + 8 * (lane & 3);
+#pragma unroll 1
+      for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+        float o[32];
+        tmem_ld32(o_addr + c, o);
+        tc_wait_ld();
+        if (!valid) continue;
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] *= inv;
+        transpose_quad(o, lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) st_global_v8(dst + k * kHeadDim + c, o + 8 * k);
+      }
+    }
+    if (!freed) free_o();
+    barrier_rows(quad);  // red is free again
+  };
+
+  Piece q;
+  Result last;
+  for (bool more = true; more;) {
+    more = next_piece(p, s, lo, hi, q);
+    const int seen = more && j < q.tokens ? q.seen0 + j : 0;  // keys that this row sees
+    auto seen_of = [&](int u, int h) { return min(max(seen - u * kUnitKeys - h * kPageSize, 0), kPageSize); };
+    RowState st;
+    float mul = c2;  // of the row's products: the softmax scale, and the power of two of its Q terms
+    if constexpr (kQ8) {
+      if (more) {
+        wait(QFull, pieces & 1);
+        mul *= split_q(cx.base + Smem<kFmt>::q, red, row, quad, half);
+        __syncwarp();
+        if (lane == 0) mbar_arrive_pair(cx.leader_bar(QReady));
+        barrier_rows(quad);  // red is free again
+      }
+      if (last.any) finish(last);  // while S of the first unit runs
+      if (!more) break;
+    }
+    int u = q.u0;
+    do {
+      if (kQ8 || more) {
+        const uint32_t buf = cnt & 1, tx = tmem + lanes + buf * kSCols + 64 * half;
+        const uint32_t sc_slot = cnt % kScaleSlots;
+        const float* sc = reinterpret_cast<const float*>(gbase + Smem<kFmt>::scales + sc_slot * kScaleBytes) + 64 * half;
+        const int cols = seen_of(u, half);  // this thread's keys
+        if (kQ8) wait(ScFull + sc_slot, (cnt / kScaleSlots) & 1);
+        // quantised: a look at two of the 64 V scales of this warp's page; the threads of the rows together see those of both.
+        bool may = false;
+        if constexpr (kQ8) {
+          const float2 v = reinterpret_cast<const float2*>(sc + kUnitKeys)[lane];
+          may = may_shift(2 * lane < cols ? v.x : 1.0f) | may_shift(2 * lane + 1 < cols ? v.y : 1.0f);
+        }
+        wait(SFull + buf, (cnt >> 1) & 1);
+        tc_fence_after();
+        if (seen_of(u, 0) > 0) {
+          softmax_unit<kQ8>(st, tx, o_addr, sc, cols, may, mul, red, row, quad, half, [&]() { wait_pv(cnt - 1); });
+        } else {  // no key of this unit: weights of zero
+          const float none[16] = {};
+          tmem_st16(tx, none);
+          tmem_st16(tx + 32, none);
+          tc_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_pair(p_full + 8 * buf);
+          if (kQ8) mbar_arrive(cx.bar(ScEmpty + sc_slot));
+        }
+        ++cnt;
+      }
+      if (!kQ8 && last.any && u == q.u0) finish(last);  // behind the first softmax of the next piece, before anything of its O
+    } while (more && ++u < q.u1);
+    last.q = q;
+    last.st = st;
+    last.unit = cnt - 1;
+    last.piece = pieces++;
+    last.any = true;
+  }
+}
+
+template <int kFmt>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
+    chunk_attention_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap kmap,
+                              const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
+  using Sm = Smem<kFmt>;
+  constexpr bool kQ8 = kQuant<kFmt>;
+  extern __shared__ __align__(1024) uint8_t dyn_smem[];
+  const uint32_t raw = smem_u32(dyn_smem);
+  const uint32_t base = (raw + 1023u) & ~1023u;
+  uint8_t* gbase = dyn_smem + (base - raw);
+  PlanSmem& plan = *reinterpret_cast<PlanSmem*>(gbase + Sm::plan);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(gbase + Sm::misc);
+  int* abort_flag = reinterpret_cast<int*>(gbase + Sm::misc + 4);
+  const int warp = threadIdx.x >> 5;
+  Ctx cx{base, base + Sm::bars, base + Sm::odd, cta_rank(), abort_flag, p.err, p.wait_budget_ns};
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kBars; ++i) {
+      const bool of_pair = i == PFull || i == PFull + 1 || i == OFree || i == QReady;  // every softmax warp of both CTAs
+      const bool of_cta = i >= ScEmpty && i < ScEmpty + kScaleSlots;                   // of this one
+      const bool of_converts = kQ8 && (i == VFull || i == VFull + 1);
+      mbar_init(cx.bar(i), of_pair                         ? 2 * kSoftmaxWarps
+                           : of_cta                        ? kSoftmaxWarps + kConvertWarps
+                           : of_converts                   ? 2 * kConvertWarps
+                           : i >= RawEmpty                 ? kConvertWarps
+                           : i >= TailReady && i < RawFull ? 2
+                                                           : 1);
+    }
+    *abort_flag = 0;
+    for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(gbase + Sm::odd)[i] = 0;
+    fence_mbar_init();
+  }
+  if (warp == kProducerWarp && (threadIdx.x & 31) == 0) {
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    prefetch_tensormap(&qmap);
+  }
+  __syncwarp();
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(base + Sm::misc),
+                 "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncwarp();
+  cluster_arrive();  // this CTA's barriers are initialised, its tensor memory is its own
+  {  // hints only, these may still be written: what the plan needs, in L2
+    const int i = threadIdx.x * 8;  // of 4-byte elements: a sector a thread
+    if (blockIdx.x == 0 && i < p.B) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.seq_lens + i));
+    if (blockIdx.x == 0 && i <= p.B) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.q_starts + i));
+  }
+  pdl_wait_prior_grid();
+  pdl_launch_dependents();
+  build_plan(p, plan, blockIdx.x == 0 ? p.err : nullptr);
+  cluster_wait();  // as are the other's; what it does to its own shared memory until its loads begin concerns no one else
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int units = plan.cost[p.B], W = busy_pairs(p, units), pair = blockIdx.x >> 1;
+  const int lo = pair < W ? range_of_pair(pair, units, W) : 0, hi = pair < W ? range_of_pair(pair + 1, units, W) : 0;
+
+  if (warp < kSoftmaxWarps) {
+    softmax_role<kFmt>(p, cx, plan, pair, lo, hi, tmem, gbase);
+  } else if (warp == kProducerWarp) {
+    producer_role<kFmt>(p, &kmap, &vmap, &qmap, cx, plan, lo, hi);
+  } else if (warp >= kTailWarp) {
+    if constexpr (kQ8)
+      convert_role<kFmt>(p, cx, plan, lo, hi, gbase);
+    else
+      tail_role(p, cx, plan, lo, hi);
+  } else if (cx.rank == 1) {  // (its MMAs are issued by the leader)
+    publish_plan(p, plan, pair, lo, hi, threadIdx.x & 31);
+  } else if (elect_one()) {
+    mma_role<kFmt>(p, cx, plan, lo, hi, tmem);
+  }
+  __syncwarp();
+  if (*cx.abort) {
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < kSettleNs) {}
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_arrive();
+  cluster_wait();  // no copy, MMA or arrival for either CTA is left
+  tc_fence_after();
+  if (warp == kMmaWarp)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kTmemCols) : "memory");
+}
+
+// ---------------------------------------------------------------- combine
+// Joins the parts of the tiles that lie in several ranges. With O_s and lse_s of part s, M = max_s lse_s and
+// w_s = exp(lse_s - M):  out = sum_s w_s O_s / sum_s w_s,  lse = M + ln sum_s w_s.  A warp a row; the first part is the
+// second partial result of its pair (a tile that begins there), the others are the first ones of the pairs behind it.
+constexpr int kCombineThreads = 256, kCombineRows = kCombineThreads / 32;
+__global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(const ChunkParams p) {
+  const int lane = threadIdx.x & 31, r = blockIdx.x * kCombineRows + (threadIdx.x >> 5);
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  const int4 at = __ldcg(p.parts + blockIdx.y);  // first row, tokens, first pair, parts
+  if (r >= at.y * kHeads) return;
+  auto part = [&](int i) -> size_t { return (size_t)(2 * (at.z + i) + (i == 0)) * 256 + r; };
+  float mx = -INFINITY;
+  for (int i = lane; i < at.w; i += 32) mx = fmaxf(mx, __ldcg(p.part_lse + part(i)));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  float den = 0.0f, acc[8] = {};
+  constexpr int kAtOnce = 4;  // parts whose loads are in flight together
+#pragma unroll 1
+  for (int i0 = 0; i0 < at.w; i0 += kAtOnce) {
+    float4 x[kAtOnce][2];
+    float w[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (i0 + k < at.w) {
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + part(i0 + k) * kHeadDim) + 2 * lane;
+        w[k] = __ldcg(p.part_lse + part(i0 + k));
+        x[k][0] = __ldcg(src);
+        x[k][1] = __ldcg(src + 1);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (i0 + k >= at.w) continue;
+      const float e = mx == -INFINITY ? 0.0f : exp2f((w[k] - mx) * kLog2e);  // (without a finite logit: 0 / 0)
+      den += e;
+      if (e == 0.0f) continue;  // of weight 0: left out, never scaled
+      const float v[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] = fmaf(e, v[c], acc[c]);
+    }
+  }
+  const float inv = 1.0f / den;
+  const size_t row = (size_t)at.x * kHeads + r;
+  uint32_t w[4];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) w[c] = pack_bf16(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+  reinterpret_cast<uint4*>(p.out + row * kHeadDim)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+  if (lane == 0) p.lse[row] = mx + log2f(den) * kLn2;
+}
+
+template <int kFmt>
+cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
+                         cudaStream_t stream) {
+  const size_t smem = Smem<kFmt>::total + 1024;
+  static int configured[kTrackedDevices] = {};
+  const cudaError_t e = ensure_dynamic_smem(chunk_attention_tc_kernel<kFmt>, smem, configured);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(chunk_attention_tc_kernel<kFmt>, dim3(2 * p.pairs), dim3(threads<kFmt>()), smem, stream, p, kmap, vmap, qmap);
+}
+}  // namespace
+
+cudaError_t launch_chunk_attention_tc(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                      const CUtensorMap& qmap, cudaStream_t stream) {
+  return p.fmt == kKvBf16   ? launch_chunk<kKvBf16>(p, kmap, vmap, qmap, stream)
+         : p.fmt == kKvE4M3 ? launch_chunk<kKvE4M3>(p, kmap, vmap, qmap, stream)
+                            : launch_chunk<kKvE2M1>(p, kmap, vmap, qmap, stream);
+}
+
+cudaError_t launch_chunk_combine(const ChunkParams& p, cudaStream_t stream) {
+  return launch_pdl(chunk_combine_kernel, dim3(256 / kCombineRows, p.pairs), dim3(kCombineThreads), 0, stream, p);
+}
+
+}  // namespace mfa

@@ -66,12 +66,10 @@
 // weights times that power: what neither large values without weight nor rows of
 // zeros (whose scale the append sets to 1) take from the others' bits. Weights
 // below 2^-18 of a row's largest are held to 2^-29 of it.
-#include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <type_traits>
 
-#include "mfa_device.cuh"
 #include "mfa_serving.hpp"
+#include "tc_pair.cuh"
 
 namespace mfa {
 namespace {
@@ -86,29 +84,11 @@ __host__ __device__ constexpr int threads() { return 32 * (kTailWarp + (kFp8 ? k
 template <bool kFp8>
 __host__ __device__ constexpr uint32_t slot_bytes() { return kFp8 ? 16384 : 32768; }  // as loaded
 constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;                          // V as the MMAs read it, 16 bits
-constexpr int kUnitKeys = 2 * kPageSize;
 constexpr int kSeqs = kPrefixTileSeqs;
 constexpr int kScaleSlots = 4;         // E4M3: 128 K scales and 128 V scales a unit
-// E4M3: exponents of V's scales that f16 holds beside the codes' (V' = code * scale * 2^kScaleUp is at most 448 * 2^7 and
-// its scale at least 2^-10), and the most that a weight takes of one outside: far enough from 2^127 for their sums.
-constexpr int kLeastScale = -16, kMostScale = 0, kScaleUp = 6, kMostShift = 100;
 constexpr int kScaleBytes = 1024;
 constexpr int kQBytes = 65536;         // 128 rows x 256 dims, four 64-dim blocks of [128 rows x 128 B]
 constexpr int kSeqQBytes = 32768;      // one sequence's rows
-constexpr int kTmemCols = 512, kTmemO = 256, kSCols = 128;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-// A move of the reference leaves the row's largest weight at 2^moved_to: of bf16, whose relative step is the same
-// everywhere, anything will do, of f16 a value that leaves room both ways. The next move comes when the sum of
-// a thread's 64 weights of a unit passes kMostSum, so that none of them passes f16's range; the sum is needed anyway,
-// and a maximum is looked for only then.
-template <bool kFp8>
-__host__ __device__ constexpr float moved_to() { return kFp8 ? 4.0f : 0.0f; }
-constexpr float kMostSum = 32768.0f;
-constexpr int kKeyStep = 16;  // keys of one MMA of P V
-// Waits for what this CTA itself has in flight, before it leaves, do not shrink with the wait budget; and after a wait
-// that gave up, copies that no barrier of this CTA tells of get this long to land.
-constexpr uint64_t kDrainNs = 200000000ull, kSettleNs = 1000000ull;
 static_assert(kPrefixTileSeqs * kHeads == 256, "rows of a row tile");
 
 enum Bar {
@@ -165,131 +145,11 @@ struct Smem {
 static_assert(Smem<false>::total + 1024 <= 227 * 1024 && Smem<true>::total + 1024 <= 227 * 1024, "shared memory");
 static_assert(2 * slot_bytes<true>() + 2 * kVSlotBytes >= sizeof(PlanScratch), "the plan's scratch lies in the K and V slots");
 
-// ---------------------------------------------------------------- cluster pair
-__device__ __forceinline__ uint32_t cta_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t map_to_leader(uint32_t addr) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(addr));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-// Arrival on a barrier of the pair's leader. What it announces is read by the MMAs alone, and lies in tensor memory,
-// which the tcgen05 fences order, or in this CTA's shared memory, which the proxy fence before it has made visible to
-// them, so no release at cluster scope is needed: that one takes 1500 cycles, most of a unit's time.
-__device__ __forceinline__ void mbar_arrive_pair(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-// Whether a phase is complete, without waiting for it.
-__device__ __forceinline__ bool mbar_test_wait(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-// TMA load into this CTA's shared memory that completes on a barrier of the pair's leader.
-__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                                 uint32_t leader_bar, uint64_t cache_hint) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(leader_bar), "l"(cache_hint)
-      : "memory");
-}
-__device__ __forceinline__ void tc_mma_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tc_mma_pair_tmem_a(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                   uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-__device__ __forceinline__ void tc_mma_pair_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// The same without the output lanes (rows) of `off`: bit i of word w stands for row 32 w + i of the pair's 256.
-__device__ __forceinline__ void tc_mma_pair_tmem_a_masked(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                          const uint32_t (&off)[8], uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8, %9, %10, %11, %12}, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(off[0]), "r"(off[1]), "r"(off[2]), "r"(off[3]),
-      "r"(off[4]), "r"(off[5]), "r"(off[6]), "r"(off[7])
-      : "memory");
-}
-// Arrival on the barrier at the same offset of both CTAs once every MMA issued so far is done.
-__device__ __forceinline__ void tc_commit_pair(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-      "h"((uint16_t)3)
-      : "memory");
-}
-
-// True in one thread of a converged warp. The compiler knows that it is one, and then issues a tcgen05 instruction behind
-// it, or a TMA copy, without a loop over the threads that might be active (80 cycles an MMA, of which a unit has 32; the
-// eight copies of a Q took 0.6 us).
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
-  return ok != 0;
-}
-
-struct Ctx {
-  uint32_t base, bar0, rank;
-  volatile int* abort;
-  uint32_t* err;
-  uint64_t budget;
-  __device__ uint32_t bar(int i) const { return bar0 + 8u * (uint32_t)i; }
-  __device__ uint32_t leader_bar(int i) const { return map_to_leader(bar(i)); }
-  __device__ bool wait(int i, uint32_t parity) const { return mbar_wait(bar(i), parity, budget, abort, err); }
-  // the same for a whole warp, whose lanes give up together
-  __device__ bool wait_warp(int i, uint32_t parity) const { return __all_sync(0xffffffffu, wait(i, parity)); }
-};
-
 // ---------------------------------------------------------------- plan
-// Largest g in [0, n) with a[g] <= x (a is non-decreasing and a[0] <= x).
-template <typename T>
-__device__ __forceinline__ int last_at_most(const T* a, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int)a[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-__device__ __forceinline__ int warp_inclusive_sum(int x, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
-  }
-  return x;
-}
 __device__ __forceinline__ int own_tokens(const PlanSmem& s, int b, int prefix_pages) {
   const uint32_t len = s.len[b];
   return (int)(len & ~kBehind) - ((len & kBehind) ? prefix_pages * kPageSize : 0);
 }
-__device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPageSize - 1) / kPageSize; }
 
 // A group shares its prefix if at least two of its sequences hold all of it;
 // a sequence that ends inside it (or an empty slot of the batch) reads its own
@@ -417,18 +277,6 @@ __device__ void build_plan(const PrefixParams& p, PlanSmem& s, PlanScratch& t, u
   __syncthreads();
 }
 
-// a b / c, in 32 bits where the product allows it.
-__device__ __forceinline__ int share(uint32_t a, uint32_t b, uint32_t c) {
-  const unsigned long long x = (unsigned long long)a * b;
-  return (x >> 32) ? (int)(x / c) : (int)((uint32_t)x / c);
-}
-// First unit of pair w's range of the line of C units, of W pairs; and the pair whose range holds unit x.
-__device__ __forceinline__ int range_of_pair(int w, int C, int W) { return share(w, C, W); }
-__device__ __forceinline__ int pair_of_unit(int x, int C, int W) {
-  const unsigned long long y = ((unsigned long long)x + 1) * W - 1;
-  return (y >> 32) ? (int)(y / (uint32_t)C) : (int)((uint32_t)y / (uint32_t)C);
-}
-
 // Pairs that have work: with fewer units than pairs, every range holds one.
 __device__ __forceinline__ int busy_pairs(const PrefixParams& p, int units) { return min(p.pairs, max(units, 1)); }
 
@@ -504,8 +352,6 @@ __device__ __forceinline__ bool next_piece(const PlanSmem& s, int hi, Piece& q) 
   }
   return false;
 }
-// Whether the last MMA of P V on a page of so many tokens reaches behind them.
-__device__ __forceinline__ bool is_partial(int tokens) { return tokens % kKeyStep != 0; }
 
 // ---------------------------------------------------------------- producer
 // Page ids of a tile: a window of 64 held by the warp (32 ahead of need).
@@ -699,28 +545,6 @@ __device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& 
       if (lane == 0) mbar_arrive_pair(cx.leader_bar(TailReady + slot));
     }
   }
-}
-
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[4]) {
-  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
-}
-
-__device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-// The exponent that a key's weight takes of its V scale: what lies outside [kLeastScale, kMostScale]. A scale of zero (or
-// below the fp32 normal range) has none, its row adds nothing.
-__device__ __forceinline__ int scale_shift(float scale) {
-  const int e = (int)((__float_as_uint(scale) >> 23) & 0xFFu) - 127;
-  return e == -127 ? 0 : max(-kMostShift, min(kMostShift, e - max(kLeastScale, min(kMostScale, e))));
-}
-// Whether it may have one (zeros are taken for such, too).
-__device__ __forceinline__ bool may_shift(float scale) {
-  constexpr uint32_t kLeast = (uint32_t)(127 + kLeastScale) << 23, kSpan = (uint32_t)(kMostScale - kLeastScale + 1) << 23;
-  return (__float_as_uint(scale) & 0x7FFFFFFFu) - kLeast >= kSpan;
 }
 
 // E4M3: V of a unit as P V reads it, f16 of code * scale * 2^kScaleUp without the scale's shift (off by 2^-11 for the scale
@@ -919,211 +743,6 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
 }
 
 // ---------------------------------------------------------------- softmax
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
-      " fma.rn.f32x2 d, a, b, c;\n mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-      " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
-      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-// Four neighbouring lanes, each with 32 values of its row, exchange them so that lane j has values 8 j .. 8 j + 7 of all
-// four rows (row k's at v[8 k]): a store then writes whole 128 B lines instead of 32 B of as many rows as lanes (a tile's
-// result took 4 us that way).
-__device__ __forceinline__ void transpose_quad(float (&v)[32], int lane) {
-#pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const float other = __shfl_xor_sync(0xffffffffu, (lane & 2) ? v[i] : v[16 + i], 2);
-    if (lane & 2) v[i] = other; else v[16 + i] = other;
-  }
-#pragma unroll
-  for (int h = 0; h < 32; h += 16)
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? v[h + i] : v[h + 8 + i], 1);
-      if (lane & 1) v[h + i] = other; else v[h + 8 + i] = other;
-    }
-}
-// 32 bytes at once.
-__device__ __forceinline__ void st_global_v8(float* dst, const float* v) {
-  asm volatile("st.global.v8.f32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "f"(v[0]), "f"(v[1]), "f"(v[2]),
-               "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
-               : "memory");
-}
-// Barriers of the two warps that share 32 rows.
-__device__ __forceinline__ void barrier_rows(int quad) { asm volatile("bar.sync %0, 64;" ::"r"(1 + quad) : "memory"); }
-__device__ __forceinline__ bool barrier_rows_or(int quad, bool pred) {
-  uint32_t r;
-  asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 q, %1, 0;\n bar.red.or.pred p, %2, 64, q;\n selp.u32 %0, 1, 0, p;\n}\n"
-      : "=r"(r)
-      : "r"((uint32_t)pred), "r"(1 + quad)
-      : "memory");
-  return r != 0;
-}
-
-// Eight bf16 values times `up` (at most 448 then) as two E4M3 terms: codes of four in a word. Between them the values are
-// f16, which holds their eight bits exactly from 2^-17 on (the second term's last step is 2^-9); in fp32 the two prompts
-// on an 8-bit cache take 0.4 us more.
-__device__ __forceinline__ void split_q8(const uint4 v, float up, uint32_t (&t1)[2], uint32_t (&t2)[2]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    uint32_t a = 0, b = 0;
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const __half2 x =
-          __floats2half2_rn(__uint_as_float(w[2 * i + k] << 16) * up, __uint_as_float(w[2 * i + k] & 0xFFFF0000u) * up);
-      const __nv_fp8x2_storage_t c1 =
-          __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3);
-      const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3);
-      const __half2 rest = __hsub2(x, *reinterpret_cast<const __half2*>(&h1));
-      const __nv_fp8x2_storage_t c2 =
-          __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&rest), __NV_SATFINITE, __NV_E4M3);
-      a |= (uint32_t)c1 << (16 * k);
-      b |= (uint32_t)c2 << (16 * k);
-    }
-    t1[i] = a;
-    t2[i] = b;
-  }
-}
-
-// E4M3: the bf16 Q of this CTA's 128 rows (four 64-dim blocks of [128 rows x 128 B], 128-byte swizzle) becomes, in
-// place, two E4M3 terms of Q * 2^e ([128-dim half][term][128 rows x 128 B]): the first rounds the scaled value, the second
-// the rest, which is exact unless it falls below the E4M3 normal range (2^-18.8 of the row's largest |q|). 2^e is the
-// largest power of two that keeps the row within the E4M3 maximum, 448. Thread (row, half) takes the 128 dims of its
-// half, whose terms lie where they did: the second block is read whole before the terms of the first replace either.
-// All softmax threads; red: their exchange. Returns 2^-e.
-__device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, int quad, int half) {
-  const uint32_t at = q_addr + half * 32768 + row * 128;  // the first of the two blocks; the second 16 KB on
-  auto chunk = [&](int j) { return ((j ^ (row & 7)) << 4); };
-  uint4 v[8];
-  float top = 0.0f;
-  auto largest = [&](const uint4& x) {
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k)
-      top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[k] << 16)), fabsf(__uint_as_float(w[k] & 0xFFFF0000u))));
-  };
-#pragma unroll
-  for (int j = 0; j < 8; ++j) largest(ld_shared_v4(at + chunk(j)));
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = ld_shared_v4(at + 16384 + chunk(j));
-    largest(v[j]);
-  }
-  red[half * 128 + row] = top;
-  barrier_rows(quad);
-  top = fmaxf(red[row], red[128 + row]);
-  int e = 0;
-  if (top > 0.0f && top <= 3.0e38f) {
-    const uint32_t bits = __float_as_uint(top);
-    e = ((bits & 0x7FFFFFu) <= 0x600000u ? 8 : 7) - ((int)((bits >> 23) & 0xFFu) - 127);  // top * 2^e in (224, 448]
-    e = max(-126, min(126, e));
-  }
-  const float up = exp2_int(e);
-  auto store = [&](int o, const uint4& x, const uint4& y) {  // 16 dims
-    uint32_t a1[2], a2[2], b1[2], b2[2];
-    split_q8(x, up, a1, a2);
-    split_q8(y, up, b1, b2);
-    const uint32_t t1[4] = {a1[0], a1[1], b1[0], b1[1]}, t2[4] = {a2[0], a2[1], b2[0], b2[1]};
-    st_shared_v4(at + chunk(o), t1);
-    st_shared_v4(at + 16384 + chunk(o), t2);
-  };
-#pragma unroll
-  for (int o = 0; o < 4; ++o) {
-    const uint4 x = ld_shared_v4(at + chunk(2 * o)), y = ld_shared_v4(at + chunk(2 * o + 1));
-    store(o, x, y);
-  }
-#pragma unroll
-  for (int o = 4; o < 8; ++o) store(o, v[2 * o - 8], v[2 * o - 7]);
-  fence_proxy_async_smem();
-  return exp2_int(-e);
-}
-
-// E4M3: a unit whose V scales have shifts, which is rare and out of line: in the usual units' loop it cost them 9% (304
-// sequences behind 256 pages 182 -> 199 us), the threads' look for such scales alone at most 1%. P takes the shifts, the
-// denominator does not. The reference is looked for among all keys, so no second try follows and P may replace S at once.
-// tx: this thread's 64 products, sc: their K scales, 128 before their V scales. Returns the row's reference and this thread's
-// share of its denominator. Both warps of the rows; what O holds is complete.
-static __device__ __noinline__ float2 shifted_unit(uint32_t tx, uint32_t o_addr, const float* sc, int cols, float mul, float m,
-                                                   float l, bool fresh, float* red, int row, int half) {
-  const float* v_scale = sc + kUnitKeys;
-  float x[32];
-  float top = -INFINITY;
-#pragma unroll 1
-  for (int g = 0; g < 64; g += 32) {
-    tmem_ld32(tx + g, x);
-    tc_wait_ld();
-#pragma unroll
-    for (int k = 0; k < 32; ++k)
-      if (g + k < cols) top = fmaxf(top, x[k] * sc[g + k] * mul + (float)scale_shift(v_scale[g + k]));
-  }
-  red[half * 128 + row] = top - moved_to<true>();
-  barrier_rows(row >> 5);
-  const float m_new = fmaxf(m, fmaxf(red[row], red[128 + row]));
-  const float alpha = fresh || m == m_new ? 1.0f : ex2_approx(m - m_new);
-  if (!fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
-#pragma unroll 1
-    for (int c = 128 * half; c < 128 * half + 128; c += 32) {
-      tmem_ld32(o_addr + c, x);
-      tc_wait_ld();
-#pragma unroll
-      for (int k = 0; k < 32; ++k) x[k] *= alpha;
-      tmem_st32(o_addr + c, x);
-    }
-  }
-  const float ref = m_new == -INFINITY ? 0.0f : m_new;
-  float sum = 0.0f;
-#pragma unroll 1
-  for (int g = 0; g < 64; g += 32) {
-    tmem_ld32(tx + g, x);
-    tc_wait_ld();
-    uint32_t w[16];
-#pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      const float y = g + k < cols ? ex2_approx(fmaf(x[k] * sc[g + k], mul, -ref)) : 0.0f;
-      sum += y;
-      x[k] = y * exp2_int(scale_shift(v_scale[g + k]));
-    }
-#pragma unroll
-    for (int c = 0; c < 16; ++c) w[c] = pack_f16(x[2 * c], x[2 * c + 1]);
-    tmem_st16(tx + g, reinterpret_cast<const float*>(w));
-  }
-  tc_wait_st();
-  barrier_rows(row >> 5);  // red is free again
-  return make_float2(m_new, l * alpha + sum);
-}
 
 template <bool kFp8>
 __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi, uint32_t tmem, uint8_t* gbase) {
@@ -1151,13 +770,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     const int own1 = j == 0 ? q.c[1] : j == 1 ? q.c[2] : j == 2 ? q.c[3] : q.c[4];
     const int tail = (int)((q.tails >> (8 * j)) & 0xFF);
     auto seen = [&](int k) { return k < prefix ? kPageSize : k < own0 || k >= own1 ? 0 : k + 1 < own1 ? kPageSize : tail; };
-    bool fresh = true;              // no key so far
-    bool open = true;               // a row of the warp has no finite reference
-    float m = -INFINITY, l = 0.0f;  // the row's reference (log2 units), and this thread's share of its denominator
-    // The same of the weights as P holds them, by which O is divided: a weight that has most of the sum then cancels its
-    // rounding (relative error of out 2.4e-3 -> 1.9e-3 for 128 sequences behind 512 pages, 1% slower). Of f16 weights the
-    // difference does not matter. The LSE takes the unrounded sum.
-    float l_p = 0.0f;
+    RowState st;
     float mul = c2;                 // of the row's products: the softmax scale, and the power of two of its Q terms
     if constexpr (kFp8) {
       wait(QFull, pieces & 1);
@@ -1182,160 +795,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       wait(SFull + buf, (cnt >> 1) & 1);
       tc_fence_after();
       if (cols + seen(2 * u + (half ^ 1)) > 0) {
-        // This thread's products, 32 keys at a time. P of 32 keys replaces the first 16 columns of their S.
-        float2 x[16];
-        const uint32_t tx = ts + 64 * half;
-        auto load = [&](int g) {
-          tmem_ld32(tx + g, reinterpret_cast<float*>(x));
-          if constexpr (kFp8) {  // times the scales of K, of which half arrive meanwhile
-            const float4* k = reinterpret_cast<const float4*>(sc + 64 * half + g);
-            float4 k4[4];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) k4[c] = k[c];
-            tc_wait_ld();
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              x[2 * c] = mul2(x[2 * c], make_float2(k4[c].x, k4[c].y));
-              x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(k4[c].z, k4[c].w));
-            }
-#pragma unroll
-            for (int c = 4; c < 8; ++c) {
-              const float4 y = k[c];
-              x[2 * c] = mul2(x[2 * c], make_float2(y.x, y.y));
-              x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(y.z, y.w));
-            }
-          } else {
-            tc_wait_ld();
-          }
-        };
-        // Products behind the last token become infinities that give weights of 0, so that one body of code does for whole
-        // and partial units, which is fetched anew in every call (4 sequences behind 16 pages 14.3 us with two bodies, 14.0
-        // with one). E4M3: K's scales there may be anything, so the weights are masked themselves.
-        if (!kFp8 && cols < 64) {
-          const float none = mul > 0.0f ? -INFINITY : INFINITY;
-#pragma unroll 1
-          for (int g = 0; g < 64; g += 32) {
-            if (g + 32 <= cols) continue;
-            load(g);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              if (g + 2 * c >= cols) x[c].x = none;
-              if (g + 2 * c + 1 >= cols) x[c].y = none;
-            }
-            tmem_st32(tx + g, reinterpret_cast<const float*>(x));
-          }
-          tc_wait_st();
-        }
-        uint32_t w[32];
-        float2 sum, sum_p;
-        // weights of this thread's keys, their sums, and P; kPart: only the first `cols` of the 64 count
-        auto weights = [&](auto part) {
-          constexpr bool kPart = decltype(part)::value;
-          const float ref = m == -INFINITY ? 0.0f : m;  // only infinite logits so far: weights of 0
-          const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
-          sum = make_float2(0.0f, 0.0f);
-          sum_p = sum;
-          float2 sum1 = sum, sum_p1 = sum;
-#pragma unroll
-          for (int g = 0; g < 64; g += 32) {
-            load(g);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              float2 y = fma2(x[c], mul_2, ref_2);
-              y.x = ex2_approx(y.x);
-              y.y = ex2_approx(y.y);
-              if constexpr (kPart) {
-                if (g + 2 * c >= cols) y.x = 0.0f;
-                if (g + 2 * c + 1 >= cols) y.y = 0.0f;
-              }
-              if (c & 1)
-                sum1 = add2(sum1, y);
-              else
-                sum = add2(sum, y);
-              // the A operand is 16 bits, half a step of each weight: 2^-8 (bf16), 2^-11 (f16)
-              const uint32_t both = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
-              w[g / 2 + c] = both;
-              if constexpr (!kFp8) {
-                const float2 rounded = make_float2(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u));
-                if (c & 1)
-                  sum_p1 = add2(sum_p1, rounded);
-                else
-                  sum_p = add2(sum_p, rounded);
-              }
-            }
-          }
-          sum = add2(sum, sum1);
-          sum_p = add2(sum_p, sum_p1);
-        };
-        // the largest logit of this thread's first `end` keys (log2 units), or of more where these give none
-        auto largest = [&](int end) -> float {
-          float top = -INFINITY;
-#pragma unroll 1
-          for (int g = 0; g < 64; g += 32) {
-            if (g >= end && !__any_sync(0xffffffffu, top == -INFINITY)) break;
-            load(g);
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-              if (!kFp8 || g + 2 * c < cols) top = fmaxf(top, x[c].x * mul);
-              if (!kFp8 || g + 2 * c + 1 < cols) top = fmaxf(top, x[c].y * mul);
-            }
-          }
-          return top;
-        };
-        bool move = open, shifted = false;
-#pragma unroll 1
-        for (int tries = 0; tries < 2; ++tries) {
-          if (move) {
-            if (kFp8 && (shifted = barrier_rows_or(quad, may))) break;
-            // Half the keys are enough for a first reference, the sum tells if not (32 sequences behind 128 pages 26.0 ->
-            // 25.6 us; on an E4M3 cache 50.4 and 50.6, so not there).
-            const float big = largest(!kFp8 && tries == 0 ? 32 : 64) - moved_to<kFp8>();
-            red[half * 128 + row] = big;
-            barrier_rows(quad);
-            const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));
-            const float alpha = fresh || m == m_new ? 1.0f : ex2_approx(m - m_new);
-            m = m_new;
-            open = __any_sync(0xffffffffu, m == -INFINITY);  // the same in both warps of the rows
-            l *= alpha;
-            l_p *= alpha;
-            if (!fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
-              // O holds the units before this one; each of the two warps scales half of its columns
-              wait_pv();
-              tc_fence_after();
-#pragma unroll 1
-              for (int c = 128 * half; c < 128 * half + 128; c += 32) {
-                float o[32];
-                tmem_ld32(tmem + lanes + kTmemO + c, o);
-                tc_wait_ld();
-#pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= alpha;
-                tmem_st32(tmem + lanes + kTmemO + c, o);
-              }
-              tc_wait_st();  // the second try may read O again
-            }
-          }
-          if (!kFp8 || cols >= 64)
-            weights(std::false_type{});
-          else
-            weights(std::true_type{});
-          move = barrier_rows_or(quad, sum.x + sum.y > kMostSum || may);
-          if (!move) break;
-        }
-        if (kFp8 && shifted) {  // nothing has been done yet
-          if (!fresh) wait_pv();
-          tc_fence_after();
-          const float2 ml = shifted_unit(tx, tmem + lanes + kTmemO, sc + 64 * half, cols, mul, m, l, fresh, red, row, half);
-          m = ml.x;
-          l = ml.y;
-          open = __any_sync(0xffffffffu, m == -INFINITY);
-        } else {
-          l += sum.x + sum.y;
-          l_p += sum_p.x + sum_p.y;
-          tmem_st16(tx, reinterpret_cast<const float*>(w));
-          tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
-          tc_wait_st();
-        }
-        fresh = false;
+        softmax_unit<kFp8>(st, ts + 64 * half, tmem + lanes + kTmemO, sc + 64 * half, cols, may, mul, red, row, quad, half, wait_pv);
       }
       tc_fence_before();
       __syncwarp();
@@ -1347,7 +807,8 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     // ---- the piece's partial result: O / l and its LSE, 128 dims a thread
     wait_pv();
     tc_fence_after();
-    if (!fresh) {
+    if (!st.fresh) {
+      float l = st.l, l_p = st.l_p;
       red[half * 128 + row] = l;
       if (!kFp8) red[256 + half * 128 + row] = l_p;
       barrier_rows(quad);
@@ -1367,7 +828,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
 #pragma unroll
         for (int k = 0; k < 4; ++k) st_global_v8(dst + k * kHeadDim + c, o + 8 * k);
       }
-      if (half == 0) p.part_lse[at] = (m + log2f(l)) * kLn2;
+      if (half == 0) p.part_lse[at] = (st.m + log2f(l)) * kLn2;
       barrier_rows(quad);  // red is free again
     }
     tc_fence_before();

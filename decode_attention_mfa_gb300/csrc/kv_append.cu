@@ -11,6 +11,7 @@
 // pages do not fix the granularity. 4-bit storage: same page, section 5.2 (KV
 // kept in 4 bits, attention computed in 8 bits), as OCP MX FP4 (E2M1) codes
 // with one fp32 scale per token (absmax / 6), two codes per byte.
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
 #include "mfa_device.cuh"
@@ -193,9 +194,11 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// quantise_row_e4m3, with the same codes and scale.
-__device__ __forceinline__ void quantise_row_e4m3_slots(const uint4 raw, uint8_t* __restrict__ dst,
-                                                        float* __restrict__ scale_out, int lane) {
+// quantise_row_e4m3 and quantise_row_e2m1, with the same codes and scales. An E2M1 code is the conversion's (nearest, a
+// tie to the even code, beyond 6 saturating, NaN to 6), which of quotients below a quarter sees no more than their sign.
+template <bool kFp4>
+__device__ __forceinline__ void quantise_row_slots(const uint4 raw, uint8_t* __restrict__ dst,
+                                                   float* __restrict__ scale_out, int lane) {
   const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
   const __nv_bfloat162* pairs = reinterpret_cast<const __nv_bfloat162*>(w);
   // the largest magnitude, a NaN left out of it as by fmaxf
@@ -203,7 +206,11 @@ __device__ __forceinline__ void quantise_row_e4m3_slots(const uint4 raw, uint8_t
   const float2 both = unpack_bf16x2(*reinterpret_cast<const uint32_t*>(&top));
   // not negative (and of NaN alone 0): ordered as integers
   const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(both.x, both.y), 0.0f))));
-  const float s = (amax > 0.0f) ? __fdiv_rn(amax, 448.0f) : 1.0f;
+  const float s = (amax > 0.0f) ? __fdiv_rn(amax, kFp4 ? 6.0f : 448.0f) : 1.0f;
+  auto convert = [](float2 q) -> uint32_t {
+    if constexpr (kFp4) return __nv_cvt_float2_to_fp4x2(q, __NV_E2M1, cudaRoundNearest);
+    else return __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+  };
   uint32_t code[4];
   if (s >= 0x1p-60f && s <= 0x1p60f) {
     const float y = -__frcp_rn(s);
@@ -214,16 +221,19 @@ __device__ __forceinline__ void quantise_row_e4m3_slots(const uint4 raw, uint8_t
       float2 q = mul2(minus_x, minus_y);
 #pragma unroll
       for (int k = 0; k < 2; ++k) q = fma2(fma2(ss, q, minus_x), minus_y, q);
-      code[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
+      code[i] = convert(q);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 x = unpack_bf16x2(w[i]);
-      code[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)), __NV_SATFINITE, __NV_E4M3);
+      code[i] = convert(make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)));
     }
   }
-  reinterpret_cast<uint2*>(dst)[lane] = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+  if constexpr (kFp4)
+    reinterpret_cast<uint32_t*>(dst)[lane] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
+  else
+    reinterpret_cast<uint2*>(dst)[lane] = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
   if (lane == 0) *scale_out = s;
 }
 
@@ -262,8 +272,11 @@ __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_kernel(const App
     }
     const bool is_v = (i0 + j) & 1;
     if (p.fmt == kKvE4M3) {
-      quantise_row_e4m3_slots(row[j], static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * kHeadDim,
-                              (is_v ? p.v_scale : p.k_scale) + slot[j], lane);
+      quantise_row_slots<false>(row[j], static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * kHeadDim,
+                                (is_v ? p.v_scale : p.k_scale) + slot[j], lane);
+    } else if (p.fmt == kKvE2M1) {
+      quantise_row_slots<true>(row[j], static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * (kHeadDim / 2),
+                               (is_v ? p.v_scale : p.k_scale) + slot[j], lane);
     } else {
       uint16_t* dst = static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * kHeadDim;
       reinterpret_cast<uint4*>(dst)[lane] = row[j];

@@ -482,6 +482,135 @@ mfa_status_t prefix_common(const void* q, const void* k_cache, const void* v_cac
   return MFA_OK;
 }
 
+// ------------------------------------------------------------ chunks
+// Workspace: [header][partial O][partial LSE][parts], two partial results of a row tile for each pair of CTAs.
+struct ChunkPlan {
+  int pairs;
+  size_t part_o, part_lse, parts, total;  // byte offsets
+};
+void fill_chunk_plan(int num_sms, ChunkPlan* w) {
+  w->pairs = std::max(1, num_sms / 2);
+  const size_t rows = (size_t)w->pairs * 2 * kChunkTileTokens;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  w->part_o = kWsHeaderBytes;
+  w->part_lse = w->part_o + rows * kPartialOBytes;
+  w->parts = w->part_lse + up(rows * kPartialLseBytes);
+  w->total = w->parts + up((size_t)w->pairs * sizeof(int4));
+}
+constexpr int kMaxChunkTokens = MFA_MAX_CHUNK_TOKENS;
+
+mfa_status_t chunk_common(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                          const float* v_scale, int fmt, const int32_t* page_table, const int32_t* seq_lens,
+                          const int32_t* q_starts, void* out, float* lse, float scale, int batch, int max_tokens,
+                          int max_pages, int num_pages, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q_starts) return fail(MFA_ERR_INVALID_ARG, "null q_starts");
+  if (!aligned(q_starts, 4)) return fail(MFA_ERR_INVALID_ARG, "misaligned q_starts");
+  if (max_tokens < 0 || max_tokens > kMaxChunkTokens)
+    return fail(MFA_ERR_INVALID_ARG, "max_tokens %d outside [0, %d]", max_tokens, kMaxChunkTokens);
+  if (fmt != kKvBf16 && (!k_scale || !v_scale)) return fail(MFA_ERR_INVALID_ARG, "null scale pointer");
+  if (fmt != kKvBf16 && (!aligned(k_scale, 16) || !aligned(v_scale, 16)))
+    return fail(MFA_ERR_INVALID_ARG, "misaligned scales (16 bytes needed)");
+  if (fmt == kKvE2M1 && (!aligned(k_cache, 32) || !aligned(v_cache, 32)))
+    return fail(MFA_ERR_INVALID_ARG, "misaligned 4-bit cache (32 bytes needed)");
+  mfa_plan_t plan;
+  mfa_status_t st = check_decode_args(q, k_cache, v_cache, page_table, seq_lens, out, lse, batch, max_pages, num_pages, 0,
+                                      workspace, (size_t)-1, 1, &plan);
+  if (st != MFA_OK) return st;
+  // every position of the line of work fits 31 bits
+  const long long tiles = (long long)max_tokens / kChunkTileTokens + batch, units = (long long)(max_pages + 1) / 2 + kChunkPieceUnits;
+  if (max_pages > (1 << 24) || tiles * units > 0x7fffffffLL)
+    return fail(MFA_ERR_INVALID_ARG, "max_tokens * max_pages too large");
+  DeviceInfo info;
+  if ((st = current_device(nullptr, &info)) != MFA_OK) return st;
+  ChunkPlan w;
+  fill_chunk_plan(info.num_sms, &w);
+  if (workspace_bytes < w.total)
+    return fail(MFA_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, w.total);
+  if (max_tokens == 0) return MFA_OK;
+  char* ws = static_cast<char*>(workspace);
+  ChunkParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.v_cache = v_cache;
+  p.q_starts = q_starts;
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  p.parts = reinterpret_cast<int4*>(ws + w.parts);
+  p.out = static_cast<uint16_t*>(out);
+  p.lse = lse;
+  p.err = reinterpret_cast<uint32_t*>(ws);
+  p.scale = scale;
+  p.B = batch;
+  p.max_tokens = max_tokens;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.pairs = w.pairs;
+  p.fmt = fmt;
+  p.wait_budget_ns = g_wait_budget_ns.load(std::memory_order_relaxed);
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  CUtensorMap kmap, vmap, qmap;
+  const uint64_t rows = (uint64_t)num_pages * kPageSize;
+  auto encode = fmt == kKvBf16 ? encode_rows_bf16 : fmt == kKvE4M3 ? encode_rows_e4m3 : encode_rows_e2m1;
+  if ((st = encode_rows_bf16(&qmap, q, (uint64_t)max_tokens * kHeads)) != MFA_OK ||
+      (st = encode(&kmap, k_cache, rows)) != MFA_OK || (st = encode(&vmap, v_cache, rows)) != MFA_OK)
+    return st;
+  cudaError_t e;
+  if (g_prof_start && (e = cudaEventRecordWithFlags(g_prof_start, s, cudaEventRecordExternal)) != cudaSuccess)
+    return cuda_fail(e, "profile event record");
+  if ((e = launch_chunk_attention_tc(p, kmap, vmap, qmap, s)) != cudaSuccess) return cuda_fail(e, "chunk attention launch");
+  if (g_prof_stop && (e = cudaEventRecordWithFlags(g_prof_stop, s, cudaEventRecordExternal)) != cudaSuccess)
+    return cuda_fail(e, "profile event record");
+  if ((e = launch_chunk_combine(p, s)) != cudaSuccess) return cuda_fail(e, "chunk combine launch");
+  return MFA_OK;
+}
+
+// ------------------------------------------------------------ reading a cache back
+mfa_status_t kv_read_common(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale, int fmt,
+                            const int32_t* page_table, const int32_t* first, const int32_t* row_starts, void* k_out,
+                            void* v_out, long long k_stride, long long v_stride, int batch, int max_rows, int max_pages,
+                            int num_pages, void* workspace, void* stream) {
+  if (!k_cache || !v_cache || !page_table || !row_starts || !k_out || !v_out)
+    return fail(MFA_ERR_INVALID_ARG, "null pointer argument");
+  if (fmt != kKvBf16 && (!k_scale || !v_scale)) return fail(MFA_ERR_INVALID_ARG, "null scale pointer");
+  if (fmt != kKvBf16 && (!aligned(k_scale, 4) || !aligned(v_scale, 4))) return fail(MFA_ERR_INVALID_ARG, "misaligned scales");
+  if (batch < 1 || batch > kMaxBatch) return fail(MFA_ERR_INVALID_ARG, "batch %d outside [1, %d]", batch, kMaxBatch);
+  if (max_rows < 0) return fail(MFA_ERR_INVALID_ARG, "negative max_rows");
+  if (max_pages < 1 || num_pages < 1) return fail(MFA_ERR_INVALID_ARG, "max_pages and num_pages must be >= 1");
+  if (k_stride < kHeadDim || v_stride < kHeadDim || k_stride % 8 || v_stride % 8)
+    return fail(MFA_ERR_INVALID_ARG, "row strides must be multiples of 8 elements, 256 at least");
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(page_table, 4) ||
+      !aligned(first, 4) || !aligned(row_starts, 4))
+    return fail(MFA_ERR_INVALID_ARG, "misaligned pointer (rows and caches need 16 bytes)");
+  if (!workspace || !aligned(workspace, 256)) return fail(MFA_ERR_WORKSPACE, "workspace missing or not 256-byte aligned");
+  const mfa_status_t st = current_device(nullptr, nullptr);
+  if (st != MFA_OK) return st;
+  if (max_rows == 0) return MFA_OK;
+  KvReadParams p{};
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.page_table = page_table;
+  p.first = first;
+  p.row_starts = row_starts;
+  p.k_out = static_cast<uint16_t*>(k_out);
+  p.v_out = static_cast<uint16_t*>(v_out);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.err = static_cast<uint32_t*>(workspace);
+  p.B = batch;
+  p.max_rows = max_rows;
+  p.max_pages = max_pages;
+  p.num_pages = num_pages;
+  p.fmt = fmt;
+  const cudaError_t e = launch_kv_read(p, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "kv_read launch");
+  return MFA_OK;
+}
+
 }  // namespace
 
 namespace mfa {
@@ -709,6 +838,72 @@ mfa_status_t mfa_kv_append_slots_fp8(const void* k_new, const void* v_new, int64
                                      float* k_scale, float* v_scale, int num_pages, void* workspace, void* stream) {
   return append_slots_common(k_new, v_new, k_stride, v_stride, slot_map, n_rows, k_cache, v_cache, k_scale, v_scale,
                              kKvE4M3, num_pages, workspace, stream);
+}
+
+mfa_status_t mfa_kv_append_slots_fp4(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                     const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache,
+                                     float* k_scale, float* v_scale, int num_pages, void* workspace, void* stream) {
+  return append_slots_common(k_new, v_new, k_stride, v_stride, slot_map, n_rows, k_cache, v_cache, k_scale, v_scale,
+                             kKvE2M1, num_pages, workspace, stream);
+}
+
+mfa_status_t mfa_kv_read(const void* k_cache, const void* v_cache, const int32_t* page_table, const int32_t* first,
+                         const int32_t* row_starts, void* k_out, void* v_out, int64_t k_stride, int64_t v_stride, int batch,
+                         int max_rows, int max_pages, int num_pages, void* workspace, void* stream) {
+  return kv_read_common(k_cache, v_cache, nullptr, nullptr, kKvBf16, page_table, first, row_starts, k_out, v_out, k_stride,
+                        v_stride, batch, max_rows, max_pages, num_pages, workspace, stream);
+}
+
+mfa_status_t mfa_kv_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* page_table, const int32_t* first, const int32_t* row_starts, void* k_out,
+                             void* v_out, int64_t k_stride, int64_t v_stride, int batch, int max_rows, int max_pages,
+                             int num_pages, void* workspace, void* stream) {
+  return kv_read_common(k_cache, v_cache, k_scale, v_scale, kKvE4M3, page_table, first, row_starts, k_out, v_out, k_stride,
+                        v_stride, batch, max_rows, max_pages, num_pages, workspace, stream);
+}
+
+mfa_status_t mfa_kv_read_fp4(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* page_table, const int32_t* first, const int32_t* row_starts, void* k_out,
+                             void* v_out, int64_t k_stride, int64_t v_stride, int batch, int max_rows, int max_pages,
+                             int num_pages, void* workspace, void* stream) {
+  return kv_read_common(k_cache, v_cache, k_scale, v_scale, kKvE2M1, page_table, first, row_starts, k_out, v_out, k_stride,
+                        v_stride, batch, max_rows, max_pages, num_pages, workspace, stream);
+}
+
+size_t mfa_chunk_workspace_bytes(int batch, int max_tokens) {
+  DeviceInfo info;
+  if (batch < 1 || batch > kMaxBatch || max_tokens < 0 || max_tokens > kMaxChunkTokens ||
+      current_device(nullptr, &info) != MFA_OK)
+    return 0;
+  ChunkPlan w;
+  fill_chunk_plan(info.num_sms, &w);
+  return w.total;
+}
+
+mfa_status_t mfa_chunk_attention(const void* q, const void* k_cache, const void* v_cache, const int32_t* page_table,
+                                 const int32_t* seq_lens, const int32_t* q_starts, void* out, float* lse, float scale,
+                                 int batch, int max_tokens, int max_pages, int num_pages, void* workspace,
+                                 size_t workspace_bytes, void* stream) {
+  return chunk_common(q, k_cache, v_cache, nullptr, nullptr, kKvBf16, page_table, seq_lens, q_starts, out, lse, scale, batch,
+                      max_tokens, max_pages, num_pages, workspace, workspace_bytes, stream);
+}
+
+mfa_status_t mfa_chunk_attention_fp8(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                     const float* v_scale, const int32_t* page_table, const int32_t* seq_lens,
+                                     const int32_t* q_starts, void* out, float* lse, float scale, int batch,
+                                     int max_tokens, int max_pages, int num_pages, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  return chunk_common(q, k_cache, v_cache, k_scale, v_scale, kKvE4M3, page_table, seq_lens, q_starts, out, lse, scale, batch,
+                      max_tokens, max_pages, num_pages, workspace, workspace_bytes, stream);
+}
+
+mfa_status_t mfa_chunk_attention_fp4(const void* q, const void* k_cache, const void* v_cache, const float* k_scale,
+                                     const float* v_scale, const int32_t* page_table, const int32_t* seq_lens,
+                                     const int32_t* q_starts, void* out, float* lse, float scale, int batch,
+                                     int max_tokens, int max_pages, int num_pages, void* workspace,
+                                     size_t workspace_bytes, void* stream) {
+  return chunk_common(q, k_cache, v_cache, k_scale, v_scale, kKvE2M1, page_table, seq_lens, q_starts, out, lse, scale, batch,
+                      max_tokens, max_pages, num_pages, workspace, workspace_bytes, stream);
 }
 
 mfa_status_t mfa_reserve_pages(const int32_t* n_new, const int32_t* seq_lens, int32_t* page_table,

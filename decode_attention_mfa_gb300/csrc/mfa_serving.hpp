@@ -1,6 +1,6 @@
 // mfa_serving.hpp -- parameter blocks and launch entry points of the operators of
-// a serving step: page tables and slots, appends by slot, and decode attention
-// over shared prefixes.
+// a serving step: page tables and slots, appends by slot, a cache read back,
+// decode attention over shared prefixes, and attention of chunks of new tokens.
 #pragma once
 
 #include "mfa_internal.h"
@@ -15,11 +15,28 @@ struct AppendSlotsParams {
   const int64_t* slot_map;  // [n_rows]
   void* k_cache;
   void* v_cache;
-  float* k_scale;  // E4M3 only
+  float* k_scale;  // E4M3 and E2M1
   float* v_scale;
   uint32_t* err;
   int n_rows, num_pages;
-  int fmt;  // kKvBf16 or kKvE4M3
+  int fmt;  // kKvBf16, kKvE4M3 or kKvE2M1
+};
+
+// Positions of a paged cache as bf16 rows: row row_starts[b] + i is position first[b] + i of sequence b.
+struct KvReadParams {
+  const void* k_cache;
+  const void* v_cache;
+  const float* k_scale;  // E4M3 and E2M1
+  const float* v_scale;
+  const int32_t* page_table;
+  const int32_t* first;       // [B] (null: 0)
+  const int32_t* row_starts;  // [B + 1]
+  uint16_t* k_out;            // row i at k_out + i * k_stride (bf16 bits)
+  uint16_t* v_out;
+  long long k_stride, v_stride;
+  uint32_t* err;
+  int B, max_rows, max_pages, num_pages;
+  int fmt;
 };
 
 // Pages taken from or given back to the stack of free page ids.
@@ -67,12 +84,42 @@ struct PrefixParams {
   uint64_t wait_budget_ns;
 };
 
+// Attention of chunks of new tokens. The work is a line of row tiles, up to kChunkTileTokens neighbouring tokens of a
+// sequence against what they see. Units of a tile: its pages by two, plus kChunkPieceUnits.
+constexpr int kChunkTileTokens = 4;
+constexpr int kChunkPieceUnits = 3;
+struct ChunkParams {
+  const uint16_t* q;         // [max_tokens][64][256] bf16 bits
+  const void* v_cache;
+  const int32_t* q_starts;   // [B + 1]
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const float* k_scale;      // [num_pages][64] (E4M3 and E2M1)
+  const float* v_scale;
+  // partial results, 256 rows of [256] (and LSEs) each: 2 pair of the tile that began before the pair's range, 2 pair + 1 of
+  // the one that ends behind it
+  float* part_o;
+  float* part_lse;
+  int4* parts;               // [pairs]: the tile that begins in the pair's range and ends behind it: first row, tokens, pair, parts
+  uint16_t* out;             // [max_tokens][64][256] bf16 bits
+  float* lse;                // [max_tokens][64]
+  uint32_t* err;
+  float scale;
+  int B, max_tokens, max_pages, num_pages, pairs;
+  int fmt;                   // kKvBf16, kKvE4M3 or kKvE2M1
+  uint64_t wait_budget_ns;
+};
+
 // Kernel launchers (each returns the launch's cudaError_t).
 cudaError_t launch_kv_append_slots(const AppendSlotsParams& p, cudaStream_t stream);
+cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream);
 cudaError_t launch_reserve_pages(const PageTableParams& p, cudaStream_t stream);
 cudaError_t launch_release_pages(const PageTableParams& p, cudaStream_t stream);
 cudaError_t launch_decode_prefix_tc(const PrefixParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
                                     const CUtensorMap& q_map, cudaStream_t stream);
 cudaError_t launch_prefix_combine(const PrefixParams& p, cudaStream_t stream);
+cudaError_t launch_chunk_attention_tc(const ChunkParams& p, const CUtensorMap& k_map, const CUtensorMap& v_map,
+                                      const CUtensorMap& q_map, cudaStream_t stream);
+cudaError_t launch_chunk_combine(const ChunkParams& p, cudaStream_t stream);
 
 }  // namespace mfa

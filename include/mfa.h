@@ -63,6 +63,7 @@ extern "C" {
 #define MFA_MAX_BATCH 1024
 #define MFA_MAX_QUERY_BATCH 256  /* batch limit of mfa_query_lowrank */
 #define MFA_MAX_QUERY_RANK 16384 /* rank limit of mfa_query_lowrank */
+#define MFA_MAX_CHUNK_TOKENS 16777216 /* max_tokens limit of mfa_chunk_attention* */
 #define MFA_MAX_QUERY_TOKENS 8   /* query tokens per sequence of the multi-token decode calls */
 
 typedef enum {
@@ -211,8 +212,9 @@ mfa_status_t mfa_release_pages(const int32_t* finished, const int32_t* keep_page
  *     from one row to the next, multiples of 8, so that K and V may be columns
  *     of one projection's output;
  *   slot_map: [device] int64 [n_rows], as mfa_reserve_pages writes it.
- * mfa_kv_append_slots_fp8 quantises each row as mfa_kv_append_fp8 does (the
- * same codes and scales). workspace: any workspace (only its error word is
+ * mfa_kv_append_slots_fp8 quantises each row as mfa_kv_append_fp8 does,
+ * mfa_kv_append_slots_fp4 as mfa_kv_append_fp4 does (the same codes and
+ * scales). workspace: any workspace (only its error word is
  * used), so calls may share it with any other. Host errors: MFA_ERR_INVALID_ARG
  * (null or misaligned pointers, n_rows < 0, num_pages < 1, bad strides),
  * MFA_ERR_WORKSPACE. */
@@ -223,6 +225,97 @@ mfa_status_t mfa_kv_append_slots_fp8(const void* k_new, const void* v_new, int64
                                      const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache,
                                      float* k_scale, float* v_scale, int num_pages,
                                      void* workspace, void* stream);
+mfa_status_t mfa_kv_append_slots_fp4(const void* k_new, const void* v_new, int64_t k_stride, int64_t v_stride,
+                                     const int64_t* slot_map, int n_rows, void* k_cache, void* v_cache,
+                                     float* k_scale, float* v_scale, int num_pages,
+                                     void* workspace, void* stream);
+
+/* Positions of a paged cache read back as bf16 rows, for a request that moves
+ * to another server or into a cache of another format: row row_starts[b] + i of
+ * K (k_out + row * k_stride, 256 bf16) and of V is position first[b] + i of
+ * sequence b, for row_starts[b] + i < row_starts[b + 1].
+ *   first:      [device] int32 [batch], null: 0. With the lengths before a step
+ *               and mfa_reserve_pages' new_starts the call reads the step's tokens;
+ *   row_starts: [device] int32 [batch + 1], non-decreasing within [0, max_rows];
+ *   k_out, v_out: [device] bf16, 16-byte aligned; k_stride, v_stride: elements
+ *               from one row to the next, multiples of 8, 256 at least.
+ * Rows outside [row_starts[0], row_starts[batch]) are left as they were. bf16
+ * rows are copied bit for bit; mfa_kv_read_fp8 and _fp4 give decode(code) *
+ * scale, rounded to fp32 and then to bf16 (a code of NaN gives NaN). What a page
+ * holds behind a sequence's last token is read like any other position. A
+ * position outside [0, max_pages * 64) sets MFA_DEVERR_CAPACITY, a page id
+ * outside [0, num_pages) MFA_DEVERR_PAGE; the row is left as it was. row_starts
+ * out of their range set MFA_DEVERR_CAPACITY; which rows are then written, of
+ * those below max_rows, is not defined.
+ * workspace: any workspace (only its error word is used). Caches, scales and
+ * page table as in mfa_decode_attention, _fp8, _fp4 (scales 4-byte aligned).
+ * Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers, batch outside
+ * [1, MFA_MAX_BATCH], max_rows < 0, max_pages < 1, num_pages < 1, bad strides),
+ * MFA_ERR_WORKSPACE. */
+mfa_status_t mfa_kv_read(const void* k_cache, const void* v_cache, const int32_t* page_table,
+                         const int32_t* first, const int32_t* row_starts,
+                         void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                         int batch, int max_rows, int max_pages, int num_pages,
+                         void* workspace, void* stream);
+mfa_status_t mfa_kv_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* page_table, const int32_t* first, const int32_t* row_starts,
+                             void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                             int batch, int max_rows, int max_pages, int num_pages,
+                             void* workspace, void* stream);
+mfa_status_t mfa_kv_read_fp4(const void* k_cache, const void* v_cache, const float* k_scale, const float* v_scale,
+                             const int32_t* page_table, const int32_t* first, const int32_t* row_starts,
+                             void* k_out, void* v_out, int64_t k_stride, int64_t v_stride,
+                             int batch, int max_rows, int max_pages, int num_pages,
+                             void* workspace, void* stream);
+
+/* Attention of chunks of new tokens over a paged cache: whole prompts, chunks of
+ * prompts behind what is cached of them, and single tokens, in one call. The
+ * step's tokens are in the cache already (mfa_kv_append_slots): of the
+ * seq_lens[b] positions that sequence b holds, the last
+ * n_b = q_starts[b + 1] - q_starts[b] are new, and token t of them, row
+ * r = q_starts[b] + t of q, attends to positions j < seq_lens[b] - n_b + 1 + t:
+ *     out[r,h,:] = softmax_j( scale * q[r,h,:] . K[b,j,:] ) . V[b,j,:]
+ *     lse[r,h]   = ln sum_j exp( scale * q[r,h,:] . K[b,j,:] )
+ * q_starts and seq_lens are what mfa_reserve_pages writes as new_starts and
+ * seq_lens_out, so that a step needs no lengths on the host.
+ *   q, out:   [device] bf16 [max_tokens][64][256], lse: [device] fp32
+ *             [max_tokens][64]. Rows outside [q_starts[0], q_starts[batch]) are
+ *             neither read nor written;
+ *   q_starts: [device] int32 [batch + 1], non-decreasing within [0, max_tokens].
+ * A token that sees no position (n_b > seq_lens[b]) gets out = 0, lse = -inf.
+ * Nothing that a token does not see reaches its results, not even a NaN or an
+ * infinity. Repeated calls give the same bits.
+ * workspace: [device] at least mfa_chunk_workspace_bytes(batch, max_tokens)
+ * bytes (about 40 MB, whatever the sizes), initialised once by
+ * mfa_workspace_init; calls that share one must not overlap on the GPU.
+ * E4M3 and E2M1 caches (mfa_chunk_attention_fp8, _fp4): q enters as the sum of
+ * two E4M3 terms under a power of two of its row (within 2^-18.8 of the row's
+ * largest |q|), V's values and the weights as f16, as in
+ * mfa_decode_attention_prefix_fp8. Scales 16-byte, 4-bit caches 32-byte aligned.
+ * Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers, batch outside
+ * [1, MFA_MAX_BATCH], max_tokens outside [0, MFA_MAX_CHUNK_TOKENS], max_pages
+ * outside [1, 2^24], num_pages < 1, (max_tokens / 4 + batch) *
+ * (max_pages / 2 + 4) above 2^31 - 1), MFA_ERR_WORKSPACE. Device errors as in
+ * mfa_decode_attention; q_starts out of their range are clamped to the largest
+ * before them (MFA_DEVERR_CAPACITY). */
+size_t mfa_chunk_workspace_bytes(int batch, int max_tokens);
+mfa_status_t mfa_chunk_attention(const void* q, const void* k_cache, const void* v_cache,
+                                 const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_starts,
+                                 void* out, float* lse, float scale,
+                                 int batch, int max_tokens, int max_pages, int num_pages,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+mfa_status_t mfa_chunk_attention_fp8(const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_starts,
+                                     void* out, float* lse, float scale,
+                                     int batch, int max_tokens, int max_pages, int num_pages,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+mfa_status_t mfa_chunk_attention_fp4(const void* q, const void* k_cache, const void* v_cache,
+                                     const float* k_scale, const float* v_scale,
+                                     const int32_t* page_table, const int32_t* seq_lens, const int32_t* q_starts,
+                                     void* out, float* lse, float scale,
+                                     int batch, int max_tokens, int max_pages, int num_pages,
+                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /* MFA decode attention over a bf16 paged cache (formula at the top of this
  * file). q, out, lse, caches, page_table, seq_lens: [device], layouts above.
