@@ -74,6 +74,8 @@ template <int kFmt>
 __host__ __device__ constexpr uint32_t slot_bytes() { return kQuant<kFmt> ? 16384 : 32768; }
 template <int kFmt>
 __host__ __device__ constexpr uint32_t slot_tx() { return kFmt == kKvE2M1 ? 8192 : slot_bytes<kFmt>(); }  // as copied
+template <int kFmt>
+using Range = std::conditional_t<kFmt == kKvE2M1, E2m1Range, E4m3Range>;
 constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;  // V as the MMAs read it, 16 bits
 constexpr int kTokens = kChunkTileTokens;
 constexpr int kScaleSlots = 4, kScaleBytes = 1024;  // quantised: 128 K scales and 128 V scales a unit
@@ -537,7 +539,29 @@ __device__ void tail_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s
   }
 }
 
-// Quantised: V of a unit as P V reads it, f16 of code * scale * 2^kScaleUp without the scale's shift, from the codes: per page
+// Of what a converting thread has stored (at0, at1: its words of row row0 of the unit), rows from `from` on, which not all
+// tokens see, without what is no number; true if there was any. Out of line: in the loop of all units it cost a fifth of their
+// time.
+__device__ __noinline__ bool clear_odd_f16(uint32_t at0, uint32_t at1, int row0, int from) {
+  bool odd = false;
+#pragma unroll 1
+  for (int i = 0; i < 8; ++i) {  // rows 16 apart, of two pages
+    if ((i >> 2) * kPageSize + row0 + 16 * (i & 3) < from) continue;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t at = (k ? at1 : at0) + (i >> 2) * kVPageBytes + (i & 3) * 2048;
+      const uint4 v = ld_shared_v4(at);
+      if (not_number_f16(v.x) || not_number_f16(v.y) || not_number_f16(v.z) || not_number_f16(v.w)) {
+        const uint32_t w[4] = {numbers_f16(v.x), numbers_f16(v.y), numbers_f16(v.z), numbers_f16(v.w)};
+        st_shared_v4(at, w);
+        odd = true;
+      }
+    }
+  }
+  return odd;
+}
+
+// Quantised: V of a unit as P V reads it, f16 of code * scale * 2^kUp without the scale's shift, from the codes: per page
 // [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both with the 128-byte swizzle. A thread takes 16 codes of
 // a row and of every 16th row after it; rows behind the tile's last token become zeros. Which rows eight neighbouring threads
 // take keeps reads and writes on banks of their own, as in the shared-prefix kernel.
@@ -560,8 +584,6 @@ __device__ void convert_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
       if (!cx.wait_warp(ScFull + sc_slot, (n / kScaleSlots) & 1)) return;
       if (!cx.wait_warp(RawFull + slot, (n >> 1) & 1)) return;
       if (n >= 2 && !cx.wait_warp(PvDone + slot, ((n >> 1) & 1) ^ 1)) return;
-      const bool ends = q.ends(u);
-      bool odd = false;
 #pragma unroll
       for (int page = 0; page < 2; ++page) {
         const int valid = q.keys(2 * u + page);
@@ -571,7 +593,7 @@ __device__ void convert_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
         for (int i = 0; i < 4; ++i) {
           v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
           const float s = sc[page * kPageSize + row0 + 16 * i];
-          scale[i] = __float2half2_rn(s * exp2_int(kScaleUp - scale_shift(s)));
+          scale[i] = __float2half2_rn(s * exp2_int(Range<kFmt>::kUp - scale_shift<Range<kFmt>>(s)));
         }
         if (valid < kPageSize) {
 #pragma unroll
@@ -595,18 +617,11 @@ __device__ void convert_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
             const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r), scale[i]);
             h[k >> 2][k & 3] = *reinterpret_cast<const uint32_t*>(&y);
           }
-          if (ends && (2 * u + page) * kPageSize + row0 + 16 * i >= q.seen0) {  // a row that not all tokens see
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              odd |= not_number_f16(h[k >> 2][k & 3]);
-              h[k >> 2][k & 3] = numbers_f16(h[k >> 2][k & 3]);
-            }
-          }
           st_shared_v4(dst + page * kVPageBytes + i * 2048 + to0, h[0]);
           st_shared_v4(dst + page * kVPageBytes + i * 2048 + to1, h[1]);
         }
       }
-      if (odd) set_odd(cx.odd, piece);
+      if (q.ends(u) && clear_odd_f16(dst + to0, dst + to1, row0, q.seen0 - u * kUnitKeys)) set_odd(cx.odd, piece);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
@@ -831,7 +846,7 @@ __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
     const float l = f.st.l + red[(half ^ 1) * 128 + row];
     const float l_p = kQ8 ? l : f.st.l_p + red[256 + (half ^ 1) * 128 + row];
     // rows of a piece in which they see no key have O = 0 and no weight
-    const float inv = f.st.fresh ? 0.0f : kQ8 ? exp2_int(-kScaleUp) / l : 1.0f / l_p;
+    const float inv = f.st.fresh ? 0.0f : kQ8 ? exp2_int(-Range<kFmt>::kUp) / l : 1.0f / l_p;
     const float lse = (f.st.m + log2f(l)) * kLn2;
     const bool valid = j < f.q.tokens, whole = f.q.whole();
     const size_t out_row = (size_t)(f.q.row + j) * kHeads + (row & 63);
@@ -929,12 +944,12 @@ __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
         bool may = false;
         if constexpr (kQ8) {
           const float2 v = reinterpret_cast<const float2*>(sc + kUnitKeys)[lane];
-          may = may_shift(2 * lane < cols ? v.x : 1.0f) | may_shift(2 * lane + 1 < cols ? v.y : 1.0f);
+          may = may_shift<Range<kFmt>>(2 * lane < cols ? v.x : 1.0f) | may_shift<Range<kFmt>>(2 * lane + 1 < cols ? v.y : 1.0f);
         }
         wait(SFull + buf, (cnt >> 1) & 1);
         tc_fence_after();
         if (seen_of(u, 0) > 0) {
-          softmax_unit<kQ8>(st, tx, o_addr, sc, cols, may, mul, red, row, quad, half, [&]() { wait_pv(cnt - 1); });
+          softmax_unit<kQ8, Range<kFmt>>(st, tx, o_addr, sc, cols, may, mul, red, row, quad, half, [&]() { wait_pv(cnt - 1); });
         } else {  // no key of this unit: weights of zero
           const float none[16] = {};
           tmem_st16(tx, none);

@@ -547,7 +547,7 @@ __device__ void tail_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& 
   }
 }
 
-// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^kScaleUp without the scale's shift (off by 2^-11 for the scale
+// E4M3: V of a unit as P V reads it, f16 of code * scale * 2^kUp without the scale's shift (off by 2^-11 for the scale
 // and 2^-11 for the product), from the codes: per page [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both
 // with the 128-byte swizzle. A thread takes 16 codes of a row and of every 16th row after it; rows behind the last token
 // become zeros. Eight neighbouring threads take half of rows r and r ^ 5, whose swizzles differ in the bits that keep
@@ -582,7 +582,7 @@ __device__ void convert_role(const PrefixParams& p, const Ctx& cx, const PlanSme
         for (int i = 0; i < 4; ++i) {
           v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
           const float s = sc[page * kPageSize + row0 + 16 * i];
-          scale[i] = __float2half2_rn(s * exp2_int(kScaleUp - scale_shift(s)));
+          scale[i] = __float2half2_rn(s * exp2_int(E4m3Range::kUp - scale_shift<E4m3Range>(s)));
         }
         if (valid < kPageSize) {
 #pragma unroll
@@ -790,12 +790,12 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       bool may = false;
       if constexpr (kFp8) {
         const float2 v = reinterpret_cast<const float2*>(sc + kUnitKeys + 64 * half)[lane];
-        may = may_shift(2 * lane < cols ? v.x : 1.0f) | may_shift(2 * lane + 1 < cols ? v.y : 1.0f);
+        may = may_shift<E4m3Range>(2 * lane < cols ? v.x : 1.0f) | may_shift<E4m3Range>(2 * lane + 1 < cols ? v.y : 1.0f);
       }
       wait(SFull + buf, (cnt >> 1) & 1);
       tc_fence_after();
       if (cols + seen(2 * u + (half ^ 1)) > 0) {
-        softmax_unit<kFp8>(st, ts + 64 * half, tmem + lanes + kTmemO, sc + 64 * half, cols, may, mul, red, row, quad, half, wait_pv);
+        softmax_unit<kFp8, E4m3Range>(st, ts + 64 * half, tmem + lanes + kTmemO, sc + 64 * half, cols, may, mul, red, row, quad, half, wait_pv);
       }
       tc_fence_before();
       __syncwarp();
@@ -815,7 +815,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       l += red[(half ^ 1) * 128 + row];
       if (!kFp8) l_p += red[256 + (half ^ 1) * 128 + row];
       const size_t at = ((size_t)(pair + q.t) * kSeqs + j) * kHeads + (row & 63);
-      const float inv = kFp8 ? exp2_int(-kScaleUp) / l : 1.0f / l_p;
+      const float inv = kFp8 ? exp2_int(-E4m3Range::kUp) / l : 1.0f / l_p;
       float* dst = p.part_o + (at - (lane & 3)) * kHeadDim + 8 * (lane & 3);
 #pragma unroll 1
       for (int c = 128 * half; c < 128 * half + 128; c += 32) {

@@ -13,9 +13,16 @@
 namespace mfa {
 
 constexpr int kUnitKeys = 2 * kPageSize;
-// E4M3: exponents of V's scales that f16 holds beside the codes' (V' = code * scale * 2^kScaleUp is at most 448 * 2^7 and
-// its scale at least 2^-10), and the most that a weight takes of one outside: far enough from 2^127 for their sums.
-constexpr int kLeastScale = -16, kMostScale = 0, kScaleUp = 6, kMostShift = 100;
+// Exponents of V's scales that f16 holds beside the codes' (V' = code * scale * 2^kUp): E4M3, V' at most 448 * 2^7 and its
+// scale at least 2^-10; E2M1, 6 * 2^13 and 2^-13.
+struct E4m3Range {
+  static constexpr int kLeast = -16, kMost = 0, kUp = 6;
+};
+struct E2m1Range {
+  static constexpr int kLeast = -16, kMost = 9, kUp = 3;
+};
+// The most that a weight takes of a scale outside: far enough from 2^127 for their sums.
+constexpr int kMostShift = 100;
 constexpr int kTmemCols = 512, kTmemO = 256, kSCols = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
@@ -178,15 +185,17 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint32_t (&w)[
 }
 
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
-// The exponent that a key's weight takes of its V scale: what lies outside [kLeastScale, kMostScale]. A scale of zero (or
-// below the fp32 normal range) has none, its row adds nothing.
+// The exponent that a key's weight takes of its V scale: what lies outside [kLeast, kMost]. A scale of zero (or below the
+// fp32 normal range) has none, its row adds nothing.
+template <typename R>
 __device__ __forceinline__ int scale_shift(float scale) {
   const int e = (int)((__float_as_uint(scale) >> 23) & 0xFFu) - 127;
-  return e == -127 ? 0 : max(-kMostShift, min(kMostShift, e - max(kLeastScale, min(kMostScale, e))));
+  return e == -127 ? 0 : max(-kMostShift, min(kMostShift, e - max(R::kLeast, min(R::kMost, e))));
 }
 // Whether it may have one (zeros are taken for such, too).
+template <typename R>
 __device__ __forceinline__ bool may_shift(float scale) {
-  constexpr uint32_t kLeast = (uint32_t)(127 + kLeastScale) << 23, kSpan = (uint32_t)(kMostScale - kLeastScale + 1) << 23;
+  constexpr uint32_t kLeast = (uint32_t)(127 + R::kLeast) << 23, kSpan = (uint32_t)(R::kMost - R::kLeast + 1) << 23;
   return (__float_as_uint(scale) & 0x7FFFFFFFu) - kLeast >= kSpan;
 }
 
@@ -347,6 +356,7 @@ __device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, i
 // denominator does not. The reference is looked for among all keys, so no second try follows and P may replace S at once.
 // tx: this thread's 64 products, sc: their K scales, 128 before their V scales. Returns the row's reference and this thread's
 // share of its denominator. Both warps of the rows; what O holds is complete.
+template <typename R>
 static __device__ __noinline__ float2 shifted_unit(uint32_t tx, uint32_t o_addr, const float* sc, int cols, float mul, float m,
                                                    float l, bool fresh, float* red, int row, int half) {
   const float* v_scale = sc + kUnitKeys;
@@ -358,7 +368,7 @@ static __device__ __noinline__ float2 shifted_unit(uint32_t tx, uint32_t o_addr,
     tc_wait_ld();
 #pragma unroll
     for (int k = 0; k < 32; ++k)
-      if (g + k < cols) top = fmaxf(top, x[k] * sc[g + k] * mul + (float)scale_shift(v_scale[g + k]));
+      if (g + k < cols) top = fmaxf(top, x[k] * sc[g + k] * mul + (float)scale_shift<R>(v_scale[g + k]));
   }
   red[half * 128 + row] = top - moved_to<true>();
   barrier_rows(row >> 5);
@@ -385,7 +395,7 @@ static __device__ __noinline__ float2 shifted_unit(uint32_t tx, uint32_t o_addr,
     for (int k = 0; k < 32; ++k) {
       const float y = g + k < cols ? ex2_approx(fmaf(x[k] * sc[g + k], mul, -ref)) : 0.0f;
       sum += y;
-      x[k] = y * exp2_int(scale_shift(v_scale[g + k]));
+      x[k] = y * exp2_int(scale_shift<R>(v_scale[g + k]));
     }
 #pragma unroll
     for (int c = 0; c < 16; ++c) w[c] = pack_f16(x[2 * c], x[2 * c + 1]);
@@ -411,7 +421,7 @@ struct RowState {
 // warps of the rows together at least one); o_addr: O's first column in its lane; sc: the K scales of its keys, 128 before
 // their V scales (E4M3); may: some V scale among the warp's may have a shift; wait_pv: O holds every unit before this one.
 // Both warps of the rows.
-template <bool kFp8, typename WaitPv>
+template <bool kFp8, typename R, typename WaitPv>
 __device__ __forceinline__ void softmax_unit(RowState& st, uint32_t tx, uint32_t o_addr, const float* sc, int cols, bool may,
                                              float mul, float* red, int row, int quad, int half, WaitPv&& wait_pv) {
   // This thread's products, 32 keys at a time. P of 32 keys replaces the first 16 columns of their S.
@@ -555,7 +565,7 @@ __device__ __forceinline__ void softmax_unit(RowState& st, uint32_t tx, uint32_t
   if (kFp8 && shifted) {  // nothing has been done yet
     if (!st.fresh) wait_pv();
     tc_fence_after();
-    const float2 ml = shifted_unit(tx, o_addr, sc, cols, mul, st.m, st.l, st.fresh, red, row, half);
+    const float2 ml = shifted_unit<R>(tx, o_addr, sc, cols, mul, st.m, st.l, st.fresh, red, row, half);
     st.m = ml.x;
     st.l = ml.y;
     st.open = __any_sync(0xffffffffu, st.m == -INFINITY);
