@@ -63,11 +63,14 @@
 namespace mfa {
 namespace {
 
-constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kTailWarp = 10, kConvertWarps = 4;
+constexpr int kSoftmaxWarps = 8, kProducerWarp = 8, kMmaWarp = 9, kValueWarp = 10, kValueWarps = 4;
 template <int kFmt>
 constexpr bool kQuant = kFmt != kKvBf16;
 template <int kFmt>
-__host__ __device__ constexpr int threads() { return 32 * (kTailWarp + (kQuant<kFmt> ? kConvertWarps : 1)); }
+__host__ __device__ constexpr int threads() { return 32 * (kValueWarp + (kQuant<kFmt> ? kValueWarps : 1)); }
+// Warps that write the output: the softmax warps on a bf16 cache, on a quantised one the value warps.
+template <int kFmt>
+__host__ __device__ constexpr int output_warps() { return kQuant<kFmt> ? kValueWarps : kSoftmaxWarps; }
 // Two K and two V slots, of even and odd units, one CTA's half of a unit each: K one page of 256 dims, V 128 dims of two
 // pages. E2M1 codes lie in shared memory as the 4-bit operands do, 16 codes in 8 bytes and 8 unused ones behind them.
 template <int kFmt>
@@ -83,6 +86,13 @@ constexpr int kQBytes = 65536;                      // 128 rows x 256 dims, four
 constexpr int kQBlockTokenBytes = 8192;             // one token's rows of a block
 static_assert(kTokens * kHeads == 256, "rows of a tile");
 
+// The rows' sums of a piece, for its output: a softmax warp is at most two pieces ahead of it (S of a third follows P V of the
+// second, which waits for the first one's O to be read).
+constexpr int kStats = 4;
+struct RowStats {
+  float l[2][128], m[128];  // [half of the keys][row]
+};
+
 enum Bar {
   KFull = 0,                 // [2] leader: both CTAs' halves landed
   VFull = KFull + 2,         // [2] leader; quantised: one arrival per converting warp of the pair
@@ -92,8 +102,9 @@ enum Bar {
   SFull,                     // [2] both: S of even and odd units
   PFull = SFull + 2,         // [2] leader: one arrival per softmax warp of the pair
   PvDone = PFull + 2,        // [2] both: P V of even and odd units
-  OFree = PvDone + 2,        // leader: O has been read, one arrival per softmax warp of the pair
-  Drain,                     // leader
+  OFree = PvDone + 2,        // leader: O has been read, one arrival per output warp of the pair
+  StFull,                    // [kStats] quantised, both: the rows' sums of a piece, one arrival per softmax warp of the CTA
+  Drain = StFull + kStats,   // leader
   ScFull,                    // [kScaleSlots] quantised, both
   ScEmpty = ScFull + kScaleSlots,   // [kScaleSlots] one arrival per softmax and converting warp of the CTA
   TailFull = ScEmpty + kScaleSlots, // [2] both: this CTA's V of a tile's end landed (by V slot)
@@ -120,8 +131,9 @@ struct Smem {
   static constexpr uint32_t q = raw + (kQuant<kFmt> ? 2 * slot_bytes<kFmt>() : 0);
   static constexpr uint32_t scales = q + kQBytes;
   static constexpr uint32_t plan = scales + (kQuant<kFmt> ? kScaleSlots * kScaleBytes : 0);
-  static constexpr uint32_t red = (plan + (uint32_t)sizeof(PlanSmem) + 15) & ~15u;  // [4][128] exchange of the row halves
-  static constexpr uint32_t bars = red + 4 * 128 * 4;
+  static constexpr uint32_t red = (plan + (uint32_t)sizeof(PlanSmem) + 15) & ~15u;  // [8][128] exchange of the row halves
+  static constexpr uint32_t stats = red + 8 * 128 * 4;
+  static constexpr uint32_t bars = stats + (kQuant<kFmt> ? kStats * sizeof(RowStats) : 0);
   static constexpr uint32_t odd = bars + 8 * kBars;  // [4] pieces with values that are no numbers (set_odd)
   static constexpr uint32_t misc = odd + 16;         // TMEM base, abort flag
   static constexpr uint32_t total = misc + 8;
@@ -175,7 +187,7 @@ __device__ __forceinline__ int seeing(const PlanSmem& s, int b) { return min(s.r
 
 // All threads; ends with a barrier.
 __device__ void build_plan(const ChunkParams& p, PlanSmem& s, uint32_t* err) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, kThreads = blockDim.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kThreads = blockDim.x, warps = blockDim.x >> 5;
   const int starts = (p.B + 32) / 32, chunks = (p.B + 31) / 32;  // 32 at a time, a warp each
 #pragma unroll 1
   for (int c = warp; c < starts; c += warps) {
@@ -436,10 +448,7 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
     na = TilePages::load(2 * next.u0 + lane, end, p, next);
     nb = TilePages::load(2 * next.u0 + 32 + lane, end, p, next);
   };
-  if (more) {
-    ask();
-    good = load_q(next);
-  }
+  if (more) ask();
   while (good && more) {
     q = next;
     TilePages ids;
@@ -456,7 +465,7 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
       const int pb = 2 * u + 1 < q.pages() ? ids.get(2 * u + 1, p, q, lane) : -1;
       good = load_k(cnt, pa, pb);
       if (good && va >= 0) good = load_v(cnt - 1, va, vb, vtail);
-      if (good && u == q.u0 && cnt > 0) good = load_q(q);
+      if (good && u == q.u0) good = load_q(q);
       ++cnt;
       va = pa;
       vb = pb;
@@ -498,45 +507,32 @@ __device__ __forceinline__ uint32_t numbers_f16(uint32_t two) {
   return ((two & 0x7C00u) == 0x7C00u ? 0u : two & 0xFFFFu) | ((two & 0x7C000000u) == 0x7C000000u ? 0u : two & 0xFFFF0000u);
 }
 
-__device__ void tail_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int lo, int hi) {
-  const int lane = threadIdx.x & 31;
-  uint32_t cnt = 0, tails[2] = {0, 0}, piece = 0;
-  Piece q;
-  for (; next_piece(p, s, lo, hi, q); ++piece) {
-    for (int u = q.u0; u < q.u1; ++u, ++cnt) {
-      if (!q.ends(u)) continue;
-      const uint32_t slot = cnt & 1;
-      if (!cx.wait_warp(TailFull + slot, tails[slot] & 1)) return;
-      ++tails[slot];
-      const uint32_t unit = cx.base + Smem<kKvBf16>::v + slot * kVSlotBytes;
-      bool odd = false;
+// bf16: V of a unit at a tile's end, once it has landed: of rows that not all tokens see values that are no numbers become
+// zeros, and rows behind the last one up to the end of an MMA's 16 keys do. One warp; true if there was such a value.
+__device__ bool clear_tail(uint32_t unit, const Piece& q, int u, int lane) {
+  bool odd = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int first = (2 * u + i) * kPageSize, keys = q.keys(2 * u + i);
-        const uint32_t page = unit + i * kVPageBytes;
-        // rows that not all tokens see: two at a time, 16 bytes of two 64-dim chunks a lane
-        for (int row = max(0, q.seen0 - first) + (lane >> 4); row < keys; row += 2) {
-          const uint32_t at = page + ((lane >> 3) & 1) * 8192 + row * 128 + (lane & 7) * 16;
-          const uint4 v = ld_shared_v4(at);
-          if (not_number_bf16(v.x) || not_number_bf16(v.y) || not_number_bf16(v.z) || not_number_bf16(v.w)) {
-            const uint32_t w[4] = {numbers_bf16(v.x), numbers_bf16(v.y), numbers_bf16(v.z), numbers_bf16(v.w)};
-            st_shared_v4(at, w);
-            odd = true;
-          }
-        }
-        if (is_partial(keys)) {
-          const int words = (kKeyStep - keys % kKeyStep) * 8;  // 16 B words of a 64-dim chunk's rows
-          for (int w = lane; w < words * 2; w += 32)
-            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(page + keys * 128 + (w / words) * 8192 + (w % words) * 16), "r"(0)
-                         : "memory");
-        }
+  for (int i = 0; i < 2; ++i) {
+    const int first = (2 * u + i) * kPageSize, keys = q.keys(2 * u + i);
+    const uint32_t page = unit + i * kVPageBytes;
+    // two rows at a time, 16 bytes of two 64-dim chunks a lane
+    for (int row = max(0, q.seen0 - first) + (lane >> 4); row < keys; row += 2) {
+      const uint32_t at = page + ((lane >> 3) & 1) * 8192 + row * 128 + (lane & 7) * 16;
+      const uint4 v = ld_shared_v4(at);
+      if (not_number_bf16(v.x) || not_number_bf16(v.y) || not_number_bf16(v.z) || not_number_bf16(v.w)) {
+        const uint32_t w[4] = {numbers_bf16(v.x), numbers_bf16(v.y), numbers_bf16(v.z), numbers_bf16(v.w)};
+        st_shared_v4(at, w);
+        odd = true;
       }
-      if (odd) set_odd(cx.odd, piece);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair(cx.leader_bar(TailReady + slot));
+    }
+    if (is_partial(keys)) {
+      const int words = (kKeyStep - keys % kKeyStep) * 8;  // 16 B words of a 64-dim chunk's rows
+      for (int w = lane; w < words * 2; w += 32)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(page + keys * 128 + (w / words) * 8192 + (w % words) * 16), "r"(0)
+                     : "memory");
     }
   }
+  return odd;
 }
 
 // Of what a converting thread has stored (at0, at1: its words of row row0 of the unit), rows from `from` on, which not all
@@ -565,70 +561,57 @@ __device__ __noinline__ bool clear_odd_f16(uint32_t at0, uint32_t at1, int row0,
 // [64 rows x 128 dims] to two 64-dim chunks of [64 rows x 128 B], both with the 128-byte swizzle. A thread takes 16 codes of
 // a row and of every 16th row after it; rows behind the tile's last token become zeros. Which rows eight neighbouring threads
 // take keeps reads and writes on banks of their own, as in the shared-prefix kernel.
+struct Converter {
+  int row0;
+  uint32_t from, to0, to1;
+  __device__ explicit Converter(int t) {
+    row0 = (2 * (t >> 4)) ^ (t & 4 ? 5 : 0);
+    const int c = (t & 3) | ((t >> 1) & 4);  // 16-code chunk: dims [16 c, 16 c + 16)
+    from = row0 * 128 + ((c ^ (row0 & 7)) << 4);  // rows 16 apart share the swizzle
+    const uint32_t to = (c >> 2) * 8192 + row0 * 128;
+    to0 = to + (((2 * (c & 3)) ^ (row0 & 7)) << 4);
+    to1 = to + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4);
+  }
+};
 template <int kFmt>
-__device__ void convert_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int lo, int hi, const uint8_t* gbase) {
-  using Sm = Smem<kFmt>;
-  const int lane = threadIdx.x & 31, t = threadIdx.x - 32 * kTailWarp;
-  const int row0 = (2 * (t >> 4)) ^ (t & 4 ? 5 : 0);
-  const int c = (t & 3) | ((t >> 1) & 4);  // 16-code chunk: dims [16 c, 16 c + 16)
-  const uint32_t from = row0 * 128 + ((c ^ (row0 & 7)) << 4);  // rows 16 apart share the swizzle
-  const uint32_t to = (c >> 2) * 8192 + row0 * 128;
-  const uint32_t to0 = to + (((2 * (c & 3)) ^ (row0 & 7)) << 4), to1 = to + (((2 * (c & 3) + 1) ^ (row0 & 7)) << 4);
-  uint32_t n = 0, piece = 0;
-  Piece q;
-  for (; next_piece(p, s, lo, hi, q); ++piece) {
-    for (int u = q.u0; u < q.u1; ++u, ++n) {
-      const uint32_t slot = n & 1, sc_slot = n % kScaleSlots;
-      const uint32_t src = cx.base + Sm::raw + slot * slot_bytes<kFmt>() + from, dst = cx.base + Sm::v + slot * kVSlotBytes;
-      const float* sc = reinterpret_cast<const float*>(gbase + Sm::scales + sc_slot * kScaleBytes) + kUnitKeys;
-      if (!cx.wait_warp(ScFull + sc_slot, (n / kScaleSlots) & 1)) return;
-      if (!cx.wait_warp(RawFull + slot, (n >> 1) & 1)) return;
-      if (n >= 2 && !cx.wait_warp(PvDone + slot, ((n >> 1) & 1) ^ 1)) return;
+__device__ __forceinline__ void convert_unit(const Converter& at, uint32_t src, uint32_t dst, const float* sc, const Piece& q, int u) {
+  const int row0 = at.row0;
+  src += at.from;
 #pragma unroll
-      for (int page = 0; page < 2; ++page) {
-        const int valid = q.keys(2 * u + page);
-        uint4 v[4];
-        __half2 scale[4];
+  for (int page = 0; page < 2; ++page) {
+    const int valid = q.keys(2 * u + page);
+    uint4 v[4];
+    __half2 scale[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
-          const float s = sc[page * kPageSize + row0 + 16 * i];
-          scale[i] = __float2half2_rn(s * exp2_int(Range<kFmt>::kUp - scale_shift<Range<kFmt>>(s)));
+    for (int i = 0; i < 4; ++i) {
+      v[i] = ld_shared_v4(src + page * 8192 + i * 2048);
+      const float s = sc[page * kPageSize + row0 + 16 * i];
+      scale[i] = __float2half2_rn(s * exp2_int(Range<kFmt>::kUp - scale_shift<Range<kFmt>>(s)));
+    }
+    if (valid < kPageSize) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (row0 + 16 * i >= valid) {
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          scale[i] = __float2half2_rn(0.0f);
         }
-        if (valid < kPageSize) {
+    }
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (row0 + 16 * i >= valid) {
-              v[i] = make_uint4(0u, 0u, 0u, 0u);
-              scale[i] = __float2half2_rn(0.0f);
-            }
-        }
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t h[2][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-          uint32_t h[2][4];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            __half2_raw r;
-            if constexpr (kFmt == kKvE2M1)
-              r = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[k >> 2] >> (8 * (k & 3))), __NV_E2M1);
-            else
-              r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
-            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r), scale[i]);
-            h[k >> 2][k & 3] = *reinterpret_cast<const uint32_t*>(&y);
-          }
-          st_shared_v4(dst + page * kVPageBytes + i * 2048 + to0, h[0]);
-          st_shared_v4(dst + page * kVPageBytes + i * 2048 + to1, h[1]);
-        }
+      for (int k = 0; k < 8; ++k) {
+        __half2_raw r;
+        if constexpr (kFmt == kKvE2M1)
+          r = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(w[k >> 2] >> (8 * (k & 3))), __NV_E2M1);
+        else
+          r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(w[k >> 1] >> (16 * (k & 1))), __NV_E4M3);
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&r), scale[i]);
+        h[k >> 2][k & 3] = *reinterpret_cast<const uint32_t*>(&y);
       }
-      if (q.ends(u) && clear_odd_f16(dst + to0, dst + to1, row0, q.seen0 - u * kUnitKeys)) set_odd(cx.odd, piece);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(cx.bar(RawEmpty + slot));
-        mbar_arrive(cx.bar(ScEmpty + sc_slot));
-        mbar_arrive_pair(cx.leader_bar(VFull + slot));
-      }
+      st_shared_v4(dst + page * kVPageBytes + i * 2048 + at.to0, h[0]);
+      st_shared_v4(dst + page * kVPageBytes + i * 2048 + at.to1, h[1]);
     }
   }
 }
@@ -762,15 +745,7 @@ __device__ void mma_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s,
   (void)mbar_wait(cx.bar(Drain), 0, kDrainNs, nullptr, p.err);
 }
 
-// ---------------------------------------------------------------- softmax and output
-// What a piece leaves behind until its O is complete.
-struct Result {
-  Piece q;
-  RowState st;
-  uint32_t unit, piece;  // its last unit, its number
-  bool any = false;
-};
-
+// ---------------------------------------------------------------- V and output
 // V of position k of the piece's sequence, if it is no number, else 0.
 template <int kFmt>
 __device__ float not_number(const ChunkParams& p, int b, int k, int dim) {
@@ -796,9 +771,9 @@ __device__ float not_number(const ChunkParams& p, int b, int k, int dim) {
 // (a weight times one of them is one). Rare and out of line. part_row: of the partial results (null: the output itself).
 template <int kFmt>
 __device__ __noinline__ void write_odd(const ChunkParams& p, int b, int k0, int k1, uint32_t o_addr, float inv, size_t out_row,
-                                       float* part_row, bool valid, int half) {
+                                       float* part_row, int d0, int dims, bool valid) {
 #pragma unroll 1
-  for (int c = 128 * half; c < 128 * half + 128; c += 16) {
+  for (int c = d0; c < d0 + dims; c += 16) {
     float o[16];
     tmem_ld16(o_addr + c, o);
     tc_wait_ld();
@@ -815,19 +790,288 @@ __device__ __noinline__ void write_odd(const ChunkParams& p, int b, int k0, int 
   }
 }
 
+// O of a piece over its rows' sums, and their LSE: to the output, or as a partial result. Thread = row, kDims dims from d0 on;
+// l, l_p: the sum of the row's weights, and of those that entered O.
+template <int kFmt, int kDims>
+__device__ __forceinline__ void write_piece(const ChunkParams& p, const Ctx& cx, const Piece& q, float l, float l_p, float m, int pair,
+                                            uint32_t o_addr, uint32_t o_free, int row, int d0, bool odd) {
+  const int lane = threadIdx.x & 31, j = 2 * (int)cx.rank + (row >> 6);  // token of the tile
+  const bool valid = j < q.tokens, whole = q.whole();
+  // rows that see no key of the piece have O = 0 and no weight
+  const float inv = q.seen0 + j <= q.u0 * kUnitKeys ? 0.0f : kQuant<kFmt> ? exp2_int(-Range<kFmt>::kUp) / l_p : 1.0f / l_p;
+  const size_t out_row = (size_t)(q.row + j) * kHeads + (row & 63);
+  const size_t part = (size_t)(2 * pair + (q.u0 == 0)) * 256 + 128 * cx.rank + row;
+  if (valid && d0 == 0) {
+    const float lse = (m + log2f(l)) * kLn2;
+    if (whole) p.lse[out_row] = lse;
+    else p.part_lse[part] = lse;
+  }
+  auto free_o = [&]() {  // for the next piece's first P V
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive_pair(o_free);
+  };
+  if (odd) {
+    // keys of this piece that not all of the tile's tokens see, up to this row's
+    const int k0 = max(q.seen0, q.u0 * kUnitKeys), k1 = min(q.seen0 + j, q.u1 * kUnitKeys);
+    write_odd<kFmt>(p, q.b, k0, valid ? k1 : k0, o_addr, inv, out_row, whole ? nullptr : p.part_o + part * kHeadDim, d0, kDims, valid);
+  }
+  if (odd || !valid) {
+    free_o();
+    return;
+  }
+  // Four neighbouring lanes exchange theirs, so that each writes a part of four rows and together whole lines of them.
+  if (whole) {
+    // As bf16 into registers as far as they go, so that O is free before much is written. Words of 64 dims in the order in which
+    // the lanes' 16 bytes lie beside each other.
+    constexpr int kHeld = kDims > 128 ? 64 : kDims;  // (128 of 256 spill)
+    uint16_t* dst = p.out + (out_row - (lane & 3)) * kHeadDim + d0 + 8 * (lane & 3);
+#pragma unroll 1
+    for (int d = 0; d < kDims; d += kHeld) {
+      float w[kHeld / 64][32];
+#pragma unroll
+      for (int c = 0; c < kHeld / 32; ++c) {
+        float o[32];
+        tmem_ld32(o_addr + d0 + d + 32 * c, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 16; ++k)
+          w[c >> 1][8 * (k >> 2) + 4 * (c & 1) + (k & 3)] = __uint_as_float(pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv));
+      }
+      if (d + kHeld == kDims) free_o();
+#pragma unroll
+      for (int c = 0; c < kHeld / 64; ++c) {
+        transpose_quad(w[c], lane);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float4* to = reinterpret_cast<float4*>(dst + k * kHeadDim + d + 64 * c);
+          to[0] = make_float4(w[c][8 * k], w[c][8 * k + 1], w[c][8 * k + 2], w[c][8 * k + 3]);
+          to[4] = make_float4(w[c][8 * k + 4], w[c][8 * k + 5], w[c][8 * k + 6], w[c][8 * k + 7]);
+        }
+      }
+    }
+  } else {
+    float* dst = p.part_o + (part - (lane & 3)) * kHeadDim + 8 * (lane & 3);
+#pragma unroll 1
+    for (int c = d0; c < d0 + kDims; c += 32) {
+      float o[32];
+      tmem_ld32(o_addr + c, o);
+      tc_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 32; ++k) o[k] *= inv;
+      transpose_quad(o, lane);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) st_global_v8(dst + k * kHeadDim + c, o + 8 * k);
+    }
+    free_o();
+  }
+}
+
+// bf16: V at the end of every tile.
+__device__ void tail_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int lo, int hi) {
+  const int lane = threadIdx.x & 31;
+  uint32_t n = 0, tails[2] = {0, 0}, piece = 0;
+  Piece q;
+  for (; next_piece(p, s, lo, hi, q); ++piece) {
+    for (int u = q.u0; u < q.u1; ++u, ++n) {
+      if (!q.ends(u)) continue;
+      const uint32_t slot = n & 1;
+      if (!cx.wait_warp(TailFull + slot, tails[slot] & 1)) return;
+      ++tails[slot];
+      if (clear_tail(cx.base + Smem<kKvBf16>::v + slot * kVSlotBytes, q, u, lane)) set_odd(cx.odd, piece);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair(cx.leader_bar(TailReady + slot));
+    }
+  }
+}
+
+// Quantised: V of every unit as P V needs it and, behind that of the next piece's first unit, the output of a piece.
+template <int kFmt>
+__device__ void value_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi, uint32_t tmem,
+                           uint8_t* gbase) {
+  using Sm = Smem<kFmt>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 32 * (warp & 3) + lane;
+  const uint32_t o_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kTmemO, o_free = cx.leader_bar(OFree);
+  const RowStats* stats = reinterpret_cast<const RowStats*>(gbase + Sm::stats);
+  volatile const uint32_t* odd = reinterpret_cast<volatile const uint32_t*>(gbase + Sm::odd);
+  const Converter at(threadIdx.x - 32 * kValueWarp);
+  uint32_t n = 0, piece = 0;
+  Piece q, last;
+  for (bool more = true; more; ++piece) {
+    more = next_piece(p, s, lo, hi, q);
+    int u = q.u0;
+    do {
+      if (more) {
+        const uint32_t slot = n & 1, sc_slot = n % kScaleSlots, dst = cx.base + Sm::v + slot * kVSlotBytes;
+        const float* sc = reinterpret_cast<const float*>(gbase + Sm::scales + sc_slot * kScaleBytes) + kUnitKeys;
+        if (!cx.wait_warp(ScFull + sc_slot, (n / kScaleSlots) & 1)) return;
+        if (!cx.wait_warp(RawFull + slot, (n >> 1) & 1)) return;
+        if (n >= 2 && !cx.wait_warp(PvDone + slot, ((n >> 1) & 1) ^ 1)) return;
+        convert_unit<kFmt>(at, cx.base + Sm::raw + slot * slot_bytes<kFmt>(), dst, sc, q, u);
+        if (q.ends(u) && clear_odd_f16(dst + at.to0, dst + at.to1, at.row0, q.seen0 - u * kUnitKeys)) set_odd(cx.odd, piece);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(cx.bar(RawEmpty + slot));
+          mbar_arrive(cx.bar(ScEmpty + sc_slot));
+          mbar_arrive_pair(cx.leader_bar(VFull + slot));
+        }
+        ++n;
+      }
+      if (piece > 0 && u == q.u0) {
+        const uint32_t done = piece - 1, unit = n - (more ? 2 : 1);  // the piece before, its last unit
+        // the sums tell that S of that unit is done, and so every P V of two units earlier: the parity is exact
+        if (!cx.wait_warp(StFull + (done & (kStats - 1)), (done / kStats) & 1)) return;
+        if (!cx.wait_warp(PvDone + (unit & 1), (unit >> 1) & 1)) return;
+        tc_fence_after();
+        const RowStats& st = stats[done & (kStats - 1)];
+        const float l = st.l[0][row] + st.l[1][row];
+        write_piece<kFmt, kHeadDim>(p, cx, last, l, l, st.m[row], pair, o_addr, o_free, row, 0, odd[done & 3] == done + 1);
+      }
+    } while (more && ++u < q.u1);
+    last = q;
+  }
+}
+
+// ---------------------------------------------------------------- softmax
+// The weights of one unit, S in tensor memory replaced by P. tx: this thread's 64 products, of which `cols` count (the two
+// warps of the rows together at least one; `whole`: all 128); o_addr: O's first column in its lane; sc: the K scales of its
+// keys, 128 before their V scales (quantised); may: some V scale among the warp's may have a shift; wait_pv: O holds every
+// unit before this one. Both warps of the rows. A whole unit of rows that have a reference takes the first way, in which the
+// products come 32 at a time and no maximum is looked for, unless its weights are too large; the other way holds all 64 in
+// registers between the maximum and the weights, so that masks and references take no second trip to tensor memory.
+template <bool kQ8, typename R, typename WaitPv>
+__device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uint32_t o_addr, const float* sc, int cols, bool whole,
+                                                  bool may, float mul, float* red, bool& turn, int row, int quad, int half, WaitPv&& wait_pv) {
+  // 32 products; P of 32 keys replaces the first 16 columns of their S
+  auto load = [&](int g, float2 (&x)[16]) {
+    tmem_ld32(tx + g, reinterpret_cast<float*>(x));
+    if constexpr (kQ8) {  // times the scales of K, of which half arrive meanwhile
+      const float4* k = reinterpret_cast<const float4*>(sc + g);
+      float4 k4[4];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) k4[c] = k[c];
+      tc_wait_ld();
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        x[2 * c] = mul2(x[2 * c], make_float2(k4[c].x, k4[c].y));
+        x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(k4[c].z, k4[c].w));
+      }
+#pragma unroll
+      for (int c = 4; c < 8; ++c) {
+        const float4 y = k[c];
+        x[2 * c] = mul2(x[2 * c], make_float2(y.x, y.y));
+        x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(y.z, y.w));
+      }
+    } else {
+      tc_wait_ld();
+    }
+  };
+  float2 sum[2], sum_p[2];
+  auto clear = [&]() { sum[0] = sum[1] = sum_p[0] = sum_p[1] = make_float2(0.0f, 0.0f); };
+  // the weights of keys 2 c, 2 c + 1 into the sums, and as the A operand: 16 bits, half a step of each weight is 2^-8 (bf16)
+  // or 2^-11 (f16)
+  auto weigh = [&](float2 y, int c) -> uint32_t {
+    y.x = ex2_approx(y.x);
+    y.y = ex2_approx(y.y);
+    sum[c & 1] = add2(sum[c & 1], y);
+    const uint32_t both = kQ8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+    if constexpr (!kQ8)
+      sum_p[c & 1] = add2(sum_p[c & 1], make_float2(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u)));
+    return both;
+  };
+  uint32_t w[32];
+  bool done = false;
+  if (whole && !st.open) {
+    const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-st.m, -st.m);
+    clear();
+#pragma unroll
+    for (int g = 0; g < 64; g += 32) {
+      float2 x[16];
+      load(g, x);
+#pragma unroll
+      for (int c = 0; c < 16; ++c) w[g / 2 + c] = weigh(fma2(x[c], mul_2, ref_2), c);
+    }
+    const float2 all = add2(sum[0], sum[1]);
+    done = !barrier_rows_or(quad, all.x + all.y > kMostSum || may);
+  }
+  if (!done) {
+    if (kQ8 && barrier_rows_or(quad, may)) {
+      if (!st.fresh) wait_pv();
+      tc_fence_after();
+      const float2 ml = shifted_unit<R>(tx, o_addr, sc, cols, mul, st.m, st.l, st.fresh, red + 4 * 128, row, half);
+      st.m = ml.x;
+      st.l = ml.y;
+      st.open = __any_sync(0xffffffffu, st.m == -INFINITY);
+      st.fresh = false;
+      return;
+    }
+    float2 y[32];
+    load(0, *reinterpret_cast<float2 (*)[16]>(y));
+    load(32, *reinterpret_cast<float2 (*)[16]>(y + 16));
+    float top = -INFINITY;
+#pragma unroll
+    for (int c = 0; c < 32; ++c) {
+      y[c] = mul2(y[c], make_float2(mul, mul));
+      if (2 * c >= cols) y[c].x = -INFINITY;
+      if (2 * c + 1 >= cols) y[c].y = -INFINITY;
+      top = fmaxf(top, fmaxf(y[c].x, y[c].y));
+    }
+    const float big = top - moved_to<kQ8>();
+    float* mine = red + (turn ? 256 : 0);  // two turns: who is two exchanges ahead has seen the other read
+    turn = !turn;
+    mine[half * 128 + row] = big;
+    barrier_rows(quad);
+    const float most = fmaxf(big, mine[(half ^ 1) * 128 + row]);
+    // 64 weights up to 2^9 add up to kMostSum
+    const float m_new = st.open || most > st.m + (9.0f - moved_to<kQ8>()) ? fmaxf(st.m, most) : st.m;
+    const float alpha = st.fresh || st.m == m_new ? 1.0f : ex2_approx(st.m - m_new);
+    st.m = m_new;
+    st.open = __any_sync(0xffffffffu, st.m == -INFINITY);  // the same in both warps of the rows
+    st.l *= alpha;
+    st.l_p *= alpha;
+    const float ref = st.m == -INFINITY ? 0.0f : st.m;  // only infinite logits so far: weights of 0
+    clear();
+#pragma unroll
+    for (int c = 0; c < 32; ++c) w[c] = weigh(add2(y[c], make_float2(-ref, -ref)), c);
+    if (!st.fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
+      // O holds the units before this one; each of the two warps scales half of its columns
+      wait_pv();
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+        float o[32];
+        tmem_ld32(o_addr + c, o);
+        tc_wait_ld();
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] *= alpha;
+        tmem_st32(o_addr + c, o);
+      }
+    }
+  }
+  st.l += sum[0].x + sum[1].x + sum[0].y + sum[1].y;
+  st.l_p += sum_p[0].x + sum_p[1].x + sum_p[0].y + sum_p[1].y;
+  tmem_st16(tx, reinterpret_cast<const float*>(w));
+  tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
+  tc_wait_st();
+  st.fresh = false;
+}
+
 template <int kFmt>
 __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi, uint32_t tmem,
                              uint8_t* gbase) {
   constexpr bool kQ8 = kQuant<kFmt>;
+  using Sm = Smem<kFmt>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int half = warp >> 2, quad = warp & 3, row = 32 * quad + lane;
   const int j = 2 * (int)cx.rank + (quad >> 1);  // token of the tile
   const uint32_t lanes = (uint32_t)(32 * quad) << 16, o_addr = tmem + lanes + kTmemO;
   const float c2 = p.scale == 0.0f && !kQ8 ? 1e-37f : p.scale * kLog2e;  // (0 times an infinity would be NaN)
   const uint32_t p_full = cx.leader_bar(PFull), o_free = cx.leader_bar(OFree);
-  float* red = reinterpret_cast<float*>(gbase + Smem<kFmt>::red);
-  volatile uint32_t* odd = reinterpret_cast<volatile uint32_t*>(gbase + Smem<kFmt>::odd);
+  float* red = reinterpret_cast<float*>(gbase + Sm::red);
   uint32_t cnt = 0, pieces = 0;  // units, pieces so far
+  bool turn = false;             // of the exchanges between the two warps of the rows
   // After a wait that gave up, the warp goes through the rest of its work without waiting, so that the warps that meet it
   // at named barriers, which have no limit, do not wait for it in vain. What it computes is meaningless.
   bool alive = true;
@@ -835,110 +1079,28 @@ __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
   // P V of unit n. S of that unit is done, and with it every MMA issued before it, P V of two units earlier (the last on the
   // same barrier) among them: the parity is exact.
   auto wait_pv = [&](uint32_t n) { wait(PvDone + (n & 1), (n >> 1) & 1); };
-
-  // ---- O / l and its LSE, 128 dims a thread: to the output, or as a partial result
-  auto finish = [&](const Result& f) {
-    wait_pv(f.unit);
-    tc_fence_after();
-    red[half * 128 + row] = f.st.l;
-    if (!kQ8) red[256 + half * 128 + row] = f.st.l_p;
-    barrier_rows(quad);
-    const float l = f.st.l + red[(half ^ 1) * 128 + row];
-    const float l_p = kQ8 ? l : f.st.l_p + red[256 + (half ^ 1) * 128 + row];
-    // rows of a piece in which they see no key have O = 0 and no weight
-    const float inv = f.st.fresh ? 0.0f : kQ8 ? exp2_int(-Range<kFmt>::kUp) / l : 1.0f / l_p;
-    const float lse = (f.st.m + log2f(l)) * kLn2;
-    const bool valid = j < f.q.tokens, whole = f.q.whole();
-    const size_t out_row = (size_t)(f.q.row + j) * kHeads + (row & 63);
-    const size_t part = (size_t)(2 * pair + (f.q.u0 == 0)) * 256 + 128 * cx.rank + row;
-    if (valid && half == 0) {
-      if (whole) p.lse[out_row] = lse;
-      else p.part_lse[part] = lse;
-    }
-    bool freed = false;
-    auto free_o = [&]() {
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_pair(o_free);
-      freed = true;
-    };
-    if (odd[f.piece & 3] == f.piece + 1) {
-      // keys of this piece that not all of the tile's tokens see, up to this row's
-      const int k0 = max(f.q.seen0, f.q.u0 * kUnitKeys), k1 = min(f.q.seen0 + j, f.q.u1 * kUnitKeys);
-      write_odd<kFmt>(p, f.q.b, k0, valid ? k1 : k0, o_addr, inv, out_row, whole ? nullptr : p.part_o + part * kHeadDim, valid, half);
-    } else if (whole) {
-      // as bf16 into registers, so that O is free for the next tile's first P V before any of it is written
-      uint32_t w[64];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        float o[32];
-        tmem_ld32(o_addr + 128 * half + 32 * c, o);
-        tc_wait_ld();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) w[16 * c + k] = pack_bf16(o[2 * k] * inv, o[2 * k + 1] * inv);
-      }
-      free_o();
-      // four neighbouring lanes exchange theirs, so that each writes 32 B of four rows and together whole lines of them
-      if (valid) {
-        uint16_t* dst = p.out + (out_row - (lane & 3)) * kHeadDim + 128 * half + 16 * (lane & 3);
-#pragma unroll
-        for (int g = 0; g < 2; ++g) {
-          float (&v)[32] = *reinterpret_cast<float (*)[32]>(w + 32 * g);
-          transpose_quad(v, lane);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            uint4* to = reinterpret_cast<uint4*>(dst + k * kHeadDim + 64 * g);
-            const uint32_t* from = w + 32 * g + 8 * k;
-            to[0] = make_uint4(from[0], from[1], from[2], from[3]);
-            to[1] = make_uint4(from[4], from[5], from[6], from[7]);
-          }
-        }
-      }
-    } else {
-      float* dst = p.part_o + (part - (lane & 3)) * kHeadDim + 8 * (lane & 3);
-#pragma unroll 1
-      for (int c = 128 * half; c < 128 * half + 128; c += 32) {
-        float o[32];
-        tmem_ld32(o_addr + c, o);
-        tc_wait_ld();
-        if (!valid) continue;
-#pragma unroll
-        for (int k = 0; k < 32; ++k) o[k] *= inv;
-        transpose_quad(o, lane);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) st_global_v8(dst + k * kHeadDim + c, o + 8 * k);
-      }
-    }
-    if (!freed) free_o();
-    barrier_rows(quad);  // red is free again
-  };
-
-  Piece q;
-  Result last;
-  for (bool more = true; more;) {
+  Piece q, last;
+  RowState st, last_st;
+  for (bool more = true; more; ++pieces) {
     more = next_piece(p, s, lo, hi, q);
+    if (kQ8 && !more) break;
     const int seen = more && j < q.tokens ? q.seen0 + j : 0;  // keys that this row sees
-    auto seen_of = [&](int u, int h) { return min(max(seen - u * kUnitKeys - h * kPageSize, 0), kPageSize); };
-    RowState st;
+    st = RowState();
     float mul = c2;  // of the row's products: the softmax scale, and the power of two of its Q terms
     if constexpr (kQ8) {
-      if (more) {
-        wait(QFull, pieces & 1);
-        mul *= split_q(cx.base + Smem<kFmt>::q, red, row, quad, half);
-        __syncwarp();
-        if (lane == 0) mbar_arrive_pair(cx.leader_bar(QReady));
-        barrier_rows(quad);  // red is free again
-      }
-      if (last.any) finish(last);  // while S of the first unit runs
-      if (!more) break;
+      wait(QFull, pieces & 1);
+      mul *= split_q(cx.base + Sm::q, red + 4 * 128, row, quad, half);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_pair(cx.leader_bar(QReady));
+      barrier_rows(quad);  // red is free again
     }
     int u = q.u0;
     do {
-      if (kQ8 || more) {
+      if (more) {
         const uint32_t buf = cnt & 1, tx = tmem + lanes + buf * kSCols + 64 * half;
         const uint32_t sc_slot = cnt % kScaleSlots;
-        const float* sc = reinterpret_cast<const float*>(gbase + Smem<kFmt>::scales + sc_slot * kScaleBytes) + 64 * half;
-        const int cols = seen_of(u, half);  // this thread's keys
+        const float* sc = reinterpret_cast<const float*>(gbase + Sm::scales + sc_slot * kScaleBytes) + 64 * half;
+        const int cols = min(max(seen - u * kUnitKeys - half * kPageSize, 0), kPageSize);  // this thread's keys
         if (kQ8) wait(ScFull + sc_slot, (cnt / kScaleSlots) & 1);
         // quantised: a look at two of the 64 V scales of this warp's page; the threads of the rows together see those of both.
         bool may = false;
@@ -948,8 +1110,9 @@ __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
         }
         wait(SFull + buf, (cnt >> 1) & 1);
         tc_fence_after();
-        if (seen_of(u, 0) > 0) {
-          softmax_unit<kQ8, Range<kFmt>>(st, tx, o_addr, sc, cols, may, mul, red, row, quad, half, [&]() { wait_pv(cnt - 1); });
+        if (seen > u * kUnitKeys) {
+          softmax_tile_unit<kQ8, Range<kFmt>>(st, tx, o_addr, sc, cols, seen >= (u + 1) * kUnitKeys, may, mul, red, turn, row, quad, half,
+                                              [&]() { wait_pv(cnt - 1); });
         } else {  // no key of this unit: weights of zero
           const float none[16] = {};
           tmem_st16(tx, none);
@@ -964,13 +1127,29 @@ __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
         }
         ++cnt;
       }
-      if (!kQ8 && last.any && u == q.u0) finish(last);  // behind the first softmax of the next piece, before anything of its O
+      if (!kQ8 && pieces > 0 && u == q.u0) {  // the output of the piece before
+        wait_pv(cnt - (more ? 2 : 1));
+        tc_fence_after();
+        red[(4 + half) * 128 + row] = last_st.l;
+        red[(6 + half) * 128 + row] = last_st.l_p;
+        barrier_rows(quad);
+        const uint32_t done = pieces - 1;
+        const bool odd = reinterpret_cast<volatile const uint32_t*>(gbase + Sm::odd)[done & 3] == done + 1;
+        write_piece<kFmt, 128>(p, cx, last, last_st.l + red[(4 + (half ^ 1)) * 128 + row], last_st.l_p + red[(6 + (half ^ 1)) * 128 + row],
+                               last_st.m, pair, o_addr, o_free, row, 128 * half, odd);
+        barrier_rows(quad);  // red is free again
+      }
     } while (more && ++u < q.u1);
-    last.q = q;
-    last.st = st;
-    last.unit = cnt - 1;
-    last.piece = pieces++;
-    last.any = true;
+    if constexpr (kQ8) {
+      RowStats& to = reinterpret_cast<RowStats*>(gbase + Sm::stats)[pieces & (kStats - 1)];
+      to.l[half][row] = st.l;
+      if (half == 0) to.m[row] = st.m;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(cx.bar(StFull + (pieces & (kStats - 1))));
+    } else {
+      last = q;
+      last_st = st;
+    }
   }
 }
 
@@ -992,13 +1171,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kBars; ++i) {
-      const bool of_pair = i == PFull || i == PFull + 1 || i == OFree || i == QReady;  // every softmax warp of both CTAs
-      const bool of_cta = i >= ScEmpty && i < ScEmpty + kScaleSlots;                   // of this one
-      const bool of_converts = kQ8 && (i == VFull || i == VFull + 1);
+      const bool of_pair = i == PFull || i == PFull + 1 || i == QReady;  // every softmax warp of both CTAs
+      const bool of_cta = i >= ScEmpty && i < ScEmpty + kScaleSlots;     // and value warp of this one
+      const bool of_values = kQ8 && (i == VFull || i == VFull + 1);
       mbar_init(cx.bar(i), of_pair                         ? 2 * kSoftmaxWarps
-                           : of_cta                        ? kSoftmaxWarps + kConvertWarps
-                           : of_converts                   ? 2 * kConvertWarps
-                           : i >= RawEmpty                 ? kConvertWarps
+                           : of_cta                        ? kSoftmaxWarps + kValueWarps
+                           : of_values                     ? 2 * kValueWarps
+                           : i == OFree                    ? 2 * output_warps<kFmt>()
+                           : i >= StFull && i < Drain      ? kSoftmaxWarps
+                           : i >= RawEmpty                 ? kValueWarps
                            : i >= TailReady && i < RawFull ? 2
                                                            : 1);
     }
@@ -1039,9 +1220,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
     softmax_role<kFmt>(p, cx, plan, pair, lo, hi, tmem, gbase);
   } else if (warp == kProducerWarp) {
     producer_role<kFmt>(p, &kmap, &vmap, &qmap, cx, plan, lo, hi);
-  } else if (warp >= kTailWarp) {
+  } else if (warp >= kValueWarp) {
     if constexpr (kQ8)
-      convert_role<kFmt>(p, cx, plan, lo, hi, gbase);
+      value_role<kFmt>(p, cx, plan, pair, lo, hi, tmem, gbase);
     else
       tail_role(p, cx, plan, lo, hi);
   } else if (cx.rank == 1) {  // (its MMAs are issued by the leader)
