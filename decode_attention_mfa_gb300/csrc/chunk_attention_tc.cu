@@ -83,7 +83,6 @@ constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;  // V as the MMAs r
 constexpr int kTokens = kChunkTileTokens;
 constexpr int kScaleSlots = 4, kScaleBytes = 1024;  // quantised: 128 K scales and 128 V scales a unit
 constexpr int kQBytes = 65536;                      // 128 rows x 256 dims, four 64-dim blocks of [128 rows x 128 B]
-constexpr int kQBlockTokenBytes = 8192;             // one token's rows of a block
 static_assert(kTokens * kHeads == 256, "rows of a tile");
 
 // The rows' sums of a piece, for its output: a softmax warp is at most two pieces ahead of it (S of a third follows P V of the
@@ -151,6 +150,16 @@ struct Ctx {
   // the same for a whole warp, whose lanes give up together
   __device__ bool wait_warp(int i, uint32_t parity) const { return __all_sync(0xffffffffu, wait(i, parity)); }
 };
+
+// TMA load into this CTA's shared memory that completes on a barrier of the pair's leader.
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t leader_bar,
+                                                 uint64_t cache_hint) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(leader_bar), "l"(cache_hint)
+      : "memory");
+}
 
 // Rows of a tile's end held values that are no numbers: told to both CTAs' softmax warps, by piece. They look behind the
 // piece's last P V, which waits for the arrival behind this; a fourth piece is not begun before they have. Rare.
@@ -292,21 +301,29 @@ __device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem&
   return false;
 }
 
-// Where the combine finds the partial results of the tile that begins in this pair's range and ends behind it; and the
-// output of tokens that see no key. One warp of each pair.
-__device__ void publish_plan(const ChunkParams& p, const PlanSmem& s, int pair, int lo, int hi, int lane) {
+// Where the combine finds the partial results: for every pair in whose range a tile begins that ends behind it, in order,
+// then entries without tokens. One warp of the first pair.
+__device__ void publish_parts(const ChunkParams& p, const PlanSmem& s, int lane) {
   const int units = s.cost[p.B], W = busy_pairs(p, units);
-  if (lane == 0) {
+  int found = 0;
+  for (int w0 = 0; w0 < W; w0 += 32) {
+    const int w = w0 + lane;
     int4 part = make_int4(0, 0, 0, 0);
-    if (lo < hi) {
+    if (w < W && units > 0) {
+      const int lo = range_of_pair(w, units, W), hi = range_of_pair(w + 1, units, W);
       Piece q;
-      if (next_piece(p, s, hi - 1, hi, q) && q.u1 < q.units) {
-        const bool begins = lo <= q.first + kChunkPieceUnits;
-        if (begins) part = make_int4(q.row, q.tokens, pair, pair_of_unit(q.first + kChunkPieceUnits + q.units - 1, units, W) - pair + 1);
-      }
+      if (next_piece(p, s, hi - 1, hi, q) && q.u1 < q.units && lo <= q.first + kChunkPieceUnits)
+        part = make_int4(q.row, q.tokens, w, pair_of_unit(q.first + kChunkPieceUnits + q.units - 1, units, W) - w + 1);
     }
-    p.parts[pair] = part;
+    const uint32_t some = __ballot_sync(0xffffffffu, part.y > 0);
+    if (part.y > 0) p.parts[found + __popc(some & ((1u << lane) - 1))] = part;
+    found += __popc(some);
   }
+  for (int i = found + lane; i < p.pairs; i += 32) p.parts[i] = make_int4(0, 0, 0, 0);
+}
+
+// The output of tokens that see no key. One warp of each pair.
+__device__ void write_unseeing(const ChunkParams& p, const PlanSmem& s, int pair, int lane) {
   for (int b = pair; b < p.B; b += p.pairs) {
     const int none = s.row[b + 1] - s.row[b] - seeing(s, b);
     for (int t = 0; t < none; ++t) {
@@ -355,7 +372,6 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
   using Sm = Smem<kFmt>;
   constexpr bool kQ8 = kQuant<kFmt>;
   constexpr uint32_t kSlot = slot_bytes<kFmt>(), kPage = kSlot / 2, kTx = slot_tx<kFmt>();
-  constexpr int kCols = kQ8 ? 128 : 64;  // columns of a copy: 128 bytes of shared memory a row
   const int lane = threadIdx.x & 31, r = (int)cx.rank;
   const uint64_t pol = policy_evict_normal();
   uint32_t pieces = 0, tails[2] = {0, 0};
@@ -368,10 +384,7 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
     if (elect_one()) {
       const uint32_t dst = cx.base + Sm::k + slot * kSlot, bar = cx.leader_bar(KFull + slot);
       if (r == 0) mbar_arrive_expect_tx(cx.bar(KFull + slot), pb >= 0 ? 2 * kTx : kTx);
-      if (page >= 0)
-#pragma unroll
-        for (int d = 0; d < kHeadDim / kCols; ++d)
-          tma_load_2d_pair(dst + d * 8192, kmap, d * kCols, page * kPageSize, bar, pol);
+      if (page >= 0) tma_load_3d_pair(dst, kmap, 0, page * kPageSize, 0, bar, pol);
     }
     if constexpr (kQ8) {  // the scales of all the unit's keys, for this CTA's rows
       const uint32_t sc_slot = n % kScaleSlots;
@@ -408,31 +421,26 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
       if (lane == 0 && tail) mbar_arrive_expect_tx(bar, bytes);
       tails[slot] += tail;
     }
-    if (elect_one())
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (i == 0 || pb >= 0)
-#pragma unroll
-          for (int d = 0; d < 128 / kCols; ++d)
-            tma_load_2d_pair(dst + i * kPage + d * 8192, vmap, r * 128 + d * kCols, (i ? pb : pa) * kPageSize, bar, pol);
+    if (elect_one()) {
+      constexpr int kBlocks = kQ8 ? 1 : 2;  // of 128 dims
+      tma_load_3d_pair(dst, vmap, 0, pa * kPageSize, r * kBlocks, bar, pol);
+      if (pb >= 0) tma_load_3d_pair(dst + kPage, vmap, 0, pb * kPageSize, r * kBlocks, bar, pol);
+    }
     return true;
   };
   uint32_t cnt = 0;  // units whose K has been loaded
-  // Q of a piece, this CTA's tokens of it: by block, as the piece before is done with each (quantised: with all of them)
+  // Q of a piece, the rows of this CTA's two tokens (of a tile's end, whatever lies behind its last one): by block, as the
+  // piece before is done with each (quantised: with all of them)
   auto load_q = [&](const Piece& q) -> bool {
-    const int here = min(2, max(0, q.tokens - 2 * r));
     if (kQ8 && pieces > 0 && !cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1)) return false;
-    if (kQ8 && lane == 0) mbar_arrive_expect_tx(cx.bar(QFull), here * 4 * kQBlockTokenBytes);
+    if (kQ8 && lane == 0) mbar_arrive_expect_tx(cx.bar(QFull), kQBytes);
+    const int y = (q.row + 2 * r) * kHeads;
 #pragma unroll 1
     for (int d = 0; d < 4; ++d) {
       if (!kQ8 && pieces > 0 && !cx.wait_warp(QFree + d, (pieces - 1) & 1)) return false;
       if (elect_one()) {
-        if (!kQ8 && r == 0) mbar_arrive_expect_tx(cx.bar(QFull + d), q.tokens * kQBlockTokenBytes);
-        const uint32_t bar = kQ8 ? cx.bar(QFull) : cx.leader_bar(QFull + d);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (h < here)
-            tma_load_2d_pair(cx.base + Sm::q + d * 16384 + h * 8192, qmap, d * 64, (q.row + 2 * r + h) * kHeads, bar, pol);
+        if (!kQ8 && r == 0) mbar_arrive_expect_tx(cx.bar(QFull + d), 2 * kQBytes / 4);
+        tma_load_3d_pair(cx.base + Sm::q + d * (kQBytes / 4), qmap, 0, y, d, kQ8 ? cx.bar(QFull) : cx.leader_bar(QFull + d), pol);
       }
     }
     ++pieces;
@@ -1226,7 +1234,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
     else
       tail_role(p, cx, plan, lo, hi);
   } else if (cx.rank == 1) {  // (its MMAs are issued by the leader)
-    publish_plan(p, plan, pair, lo, hi, threadIdx.x & 31);
+    if (pair == 0) publish_parts(p, plan, threadIdx.x & 31);
+    write_unseeing(p, plan, pair, threadIdx.x & 31);
   } else if (elect_one()) {
     mma_role<kFmt>(p, cx, plan, lo, hi, tmem);
   }
@@ -1246,53 +1255,65 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
 
 // ---------------------------------------------------------------- combine
 // Joins the parts of the tiles that lie in several ranges. With O_s and lse_s of part s, M = max_s lse_s and
-// w_s = exp(lse_s - M):  out = sum_s w_s O_s / sum_s w_s,  lse = M + ln sum_s w_s.  A warp a row; the first part is the
-// second partial result of its pair (a tile that begins there), the others are the first ones of the pairs behind it.
+// w_s = exp(lse_s - M):  out = sum_s w_s O_s / sum_s w_s,  lse = M + ln sum_s w_s.  A warp a row, four parts at a time, with a
+// running M. The first part is the second partial result of its pair (a tile that begins there), the others are the first ones
+// of the pairs behind it. Bound by latency: the list of tiles, then the parts of a row (its rows on one line of groups of eight,
+// which the blocks share; a grid with a block for every group of every pair took a call without parts 2.5 us longer).
 constexpr int kCombineThreads = 256, kCombineRows = kCombineThreads / 32;
+constexpr int kCombineGroups = kChunkTileTokens * kHeads / kCombineRows;  // of a tile
 __global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(const ChunkParams p) {
-  const int lane = threadIdx.x & 31, r = blockIdx.x * kCombineRows + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
-  const int4 at = __ldcg(p.parts + blockIdx.y);  // first row, tokens, first pair, parts
-  if (r >= at.y * kHeads) return;
-  auto part = [&](int i) -> size_t { return (size_t)(2 * (at.z + i) + (i == 0)) * 256 + r; };
-  float mx = -INFINITY;
-  for (int i = lane; i < at.w; i += 32) mx = fmaxf(mx, __ldcg(p.part_lse + part(i)));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  float den = 0.0f, acc[8] = {};
-  constexpr int kAtOnce = 4;  // parts whose loads are in flight together
 #pragma unroll 1
-  for (int i0 = 0; i0 < at.w; i0 += kAtOnce) {
-    float4 x[kAtOnce][2];
-    float w[kAtOnce];
+  for (int g = blockIdx.x; g < p.pairs * kCombineGroups; g += gridDim.x) {
+    const int4 at = __ldcg(p.parts + g / kCombineGroups);  // first row, tokens, first pair, parts
+    if (at.y == 0) return;  // nor has any behind it
+    const int r = (g % kCombineGroups) * kCombineRows + (threadIdx.x >> 5);
+    if (r >= at.y * kHeads) continue;
+    auto part = [&](int i) -> size_t { return (size_t)(2 * (at.z + i) + (i == 0)) * 256 + r; };
+    float mx = -INFINITY, den = 0.0f, acc[8] = {};
+    constexpr int kAtOnce = 4;  // parts whose loads are in flight together
+#pragma unroll 1
+    for (int i0 = 0; i0 < at.w; i0 += kAtOnce) {
+      float4 x[kAtOnce][2];
+      float z[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      if (i0 + k < at.w) {
-        const float4* src = reinterpret_cast<const float4*>(p.part_o + part(i0 + k) * kHeadDim) + 2 * lane;
-        w[k] = __ldcg(p.part_lse + part(i0 + k));
-        x[k][0] = __ldcg(src);
-        x[k][1] = __ldcg(src + 1);
+      for (int k = 0; k < kAtOnce; ++k) {
+        z[k] = -INFINITY;
+        if (i0 + k < at.w) {
+          const float4* src = reinterpret_cast<const float4*>(p.part_o + part(i0 + k) * kHeadDim) + 2 * lane;
+          z[k] = __ldcg(p.part_lse + part(i0 + k));
+          x[k][0] = __ldcg(src);
+          x[k][1] = __ldcg(src + 1);
+        }
+      }
+      const float before = mx;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) mx = fmaxf(mx, z[k]);
+      const float base = mx == -INFINITY ? 0.0f : mx;  // (no finite logit so far: weights of 0)
+      const float old = exp2f((before - base) * kLog2e);
+      den *= old;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) acc[c] = old == 0.0f ? 0.0f : acc[c] * old;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const float w = exp2f((z[k] - base) * kLog2e);
+        den += w;
+        if (w == 0.0f) continue;  // of weight 0 (or no part): left out, never scaled
+        const float v[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
+#pragma unroll
+        for (int c = 0; c < 8; ++c) acc[c] = fmaf(w, v[c], acc[c]);
       }
     }
+    const float inv = 1.0f / den;
+    const size_t row = (size_t)at.x * kHeads + r;
+    uint32_t w[4];
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) {
-      if (i0 + k >= at.w) continue;
-      const float e = mx == -INFINITY ? 0.0f : exp2f((w[k] - mx) * kLog2e);  // (without a finite logit: 0 / 0)
-      den += e;
-      if (e == 0.0f) continue;  // of weight 0: left out, never scaled
-      const float v[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
-#pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] = fmaf(e, v[c], acc[c]);
-    }
+    for (int c = 0; c < 4; ++c) w[c] = pack_bf16(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+    reinterpret_cast<uint4*>(p.out + row * kHeadDim)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
+    if (lane == 0) p.lse[row] = mx + log2f(den) * kLn2;
   }
-  const float inv = 1.0f / den;
-  const size_t row = (size_t)at.x * kHeads + r;
-  uint32_t w[4];
-#pragma unroll
-  for (int c = 0; c < 4; ++c) w[c] = pack_bf16(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-  reinterpret_cast<uint4*>(p.out + row * kHeadDim)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-  if (lane == 0) p.lse[row] = mx + log2f(den) * kLn2;
 }
 
 template <int kFmt>
@@ -1314,7 +1335,7 @@ cudaError_t launch_chunk_attention_tc(const ChunkParams& p, const CUtensorMap& k
 }
 
 cudaError_t launch_chunk_combine(const ChunkParams& p, cudaStream_t stream) {
-  return launch_pdl(chunk_combine_kernel, dim3(256 / kCombineRows, p.pairs), dim3(kCombineThreads), 0, stream, p);
+  return launch_pdl(chunk_combine_kernel, dim3(8 * p.pairs), dim3(kCombineThreads), 0, stream, p);
 }
 
 }  // namespace mfa

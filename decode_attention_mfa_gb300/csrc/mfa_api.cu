@@ -198,6 +198,28 @@ mfa_status_t encode_blocks_e4m3(CUtensorMap* map, const void* base, uint64_t row
   return MFA_OK;
 }
 
+// Rows of 256 elements viewed as 3-D -- x = the elements of a 128-byte column block (E2M1: of 128 codes), y = row, z = column
+// block -- and read in boxes of `box_rows` rows x `zbox` column blocks, which land one block after the other, each as
+// [box_rows x 128 B] with the 128-byte swizzle: a whole page, or a tile's queries, in one copy.
+mfa_status_t encode_row_blocks(CUtensorMap* map, const void* base, uint64_t rows, int fmt, uint32_t box_rows, uint32_t zbox) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc;
+  mfa_status_t st = get_encoder(&enc);
+  if (st != MFA_OK) return st;
+  const CUtensorMapDataType type = fmt == kKvBf16   ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                   : fmt == kKvE4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                                    : CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B;
+  const cuuint32_t x = fmt == kKvBf16 ? 64 : 128;
+  const cuuint64_t row_bytes = fmt == kKvBf16 ? kHeadDim * 2 : fmt == kKvE4M3 ? kHeadDim : kHeadDim / 2;
+  const cuuint64_t dims[3] = {x, (cuuint64_t)rows, (cuuint64_t)kHeadDim / x};
+  const cuuint64_t strides[2] = {row_bytes, row_bytes * x / kHeadDim};
+  const cuuint32_t box[3] = {x, box_rows, zbox};
+  const cuuint32_t elem[3] = {1, 1, 1};
+  const CUresult r = enc(map, type, 3, const_cast<void*>(base), dims, strides, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(MFA_ERR_CUDA, "cuTensorMapEncodeTiled (column blocks) failed (%d)", (int)r);
+  return MFA_OK;
+}
+
 // 2-D byte tensor [rows][256] (E4M3 codes) read in [64 rows x 128 bytes]
 // boxes with the 128-byte swizzle.
 mfa_status_t encode_rows_e4m3(CUtensorMap* map, const void* base, uint64_t rows) {
@@ -553,9 +575,10 @@ mfa_status_t chunk_common(const void* q, const void* k_cache, const void* v_cach
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   CUtensorMap kmap, vmap, qmap;
   const uint64_t rows = (uint64_t)num_pages * kPageSize;
-  auto encode = fmt == kKvBf16 ? encode_rows_bf16 : fmt == kKvE4M3 ? encode_rows_e4m3 : encode_rows_e2m1;
-  if ((st = encode_rows_bf16(&qmap, q, (uint64_t)max_tokens * kHeads)) != MFA_OK ||
-      (st = encode(&kmap, k_cache, rows)) != MFA_OK || (st = encode(&vmap, v_cache, rows)) != MFA_OK)
+  const uint32_t blocks = fmt == kKvBf16 ? 4 : 2;  // of a K row; a CTA takes half of those of V
+  if ((st = encode_row_blocks(&qmap, q, (uint64_t)max_tokens * kHeads, kKvBf16, 2 * kHeads, 1)) != MFA_OK ||
+      (st = encode_row_blocks(&kmap, k_cache, rows, fmt, kPageSize, blocks)) != MFA_OK ||
+      (st = encode_row_blocks(&vmap, v_cache, rows, fmt, kPageSize, blocks / 2)) != MFA_OK)
     return st;
   cudaError_t e;
   if (g_prof_start && (e = cudaEventRecordWithFlags(g_prof_start, s, cudaEventRecordExternal)) != cudaSuccess)

@@ -100,7 +100,7 @@ struct ChunkParams {
   // the one that ends behind it
   float* part_o;
   float* part_lse;
-  int4* parts;               // [pairs]: the tile that begins in the pair's range and ends behind it: first row, tokens, pair, parts
+  int4* parts;               // [pairs]: tiles that lie in several ranges: first row, tokens (0 behind the last), first pair, parts
   uint16_t* out;             // [max_tokens][64][256] bf16 bits
   float* lse;                // [max_tokens][64]
   uint32_t* err;
