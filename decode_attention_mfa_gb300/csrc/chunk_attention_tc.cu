@@ -943,6 +943,49 @@ __device__ void value_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& 
 }
 
 // ---------------------------------------------------------------- softmax
+// Quantised: the bf16 Q of this CTA's 128 rows (four 64-dim blocks of [128 rows x 128 B], 128-byte swizzle) becomes, in place,
+// two E4M3 terms of Q * 2^e ([128-dim half][term][128 rows x 128 B]): the first rounds the scaled value, the second the rest,
+// which is exact unless it falls below the E4M3 normal range (2^-18.8 of the row's largest |q|). 2^e is the largest power of
+// two that keeps the row within the E4M3 maximum, 448 (2^126 at most). Thread (row, half) takes the 128 dims of its half, whose
+// terms lie where they did. All softmax threads; red: their exchange. Returns 2^-e, NaN for a row with a value that is no number.
+__device__ __forceinline__ float split_queries(uint32_t q_addr, float* red, int row, int quad, int half) {
+  const uint32_t at = q_addr + half * 32768 + row * 128;  // the first of the two blocks; the second 16 KB on
+  auto chunk = [&](int j) { return (j ^ (row & 7)) << 4; };
+  uint4 v[8];
+  uint32_t tops = 0;  // the largest magnitudes of even and odd dims, as bits: what is no number is larger than any
+  auto largest = [&](const uint4& x) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tops = __vmaxu2(tops, w[k] & 0x7FFF7FFFu);
+  };
+#pragma unroll
+  for (int j = 0; j < 8; ++j) largest(ld_shared_v4(at + chunk(j)));
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = ld_shared_v4(at + 16384 + chunk(j));
+    largest(v[j]);
+  }
+  red[half * 128 + row] = __uint_as_float(max(tops << 16, tops & 0xFFFF0000u));
+  barrier_rows(quad);
+  const uint32_t top = max(__float_as_uint(red[row]), __float_as_uint(red[128 + row]));
+  int e = 0;
+  if (top != 0 && top < 0x7F800000u) e = ((top & 0x7FFFFFu) <= 0x600000u ? 8 : 7) - ((int)(top >> 23) - 127);  // in (224, 448]
+  e = max(-120, min(126, e));
+  const float up = exp2_int(e);
+#pragma unroll
+  for (int o = 0; o < 8; ++o) {  // 16 dims; those of the second block have been read
+    const uint4 x = o < 4 ? ld_shared_v4(at + chunk(2 * o)) : v[2 * o - 8], y = o < 4 ? ld_shared_v4(at + chunk(2 * o + 1)) : v[2 * o - 7];
+    uint32_t a1[2], a2[2], b1[2], b2[2];
+    split_q8(x, up, a1, a2);
+    split_q8(y, up, b1, b2);
+    const uint32_t t1[4] = {a1[0], a1[1], b1[0], b1[1]}, t2[4] = {a2[0], a2[1], b2[0], b2[1]};
+    st_shared_v4(at + chunk(o), t1);
+    st_shared_v4(at + 16384 + chunk(o), t2);
+  }
+  fence_proxy_async_smem();
+  return top < 0x7F800000u ? exp2_int(-e) : __uint_as_float(0x7FFFFFFFu);
+}
+
 // The weights of one unit, S in tensor memory replaced by P. tx: this thread's 64 products, of which `cols` count (the two
 // warps of the rows together at least one; `whole`: all 128); o_addr: O's first column in its lane; sc: the K scales of its
 // keys, 128 before their V scales (quantised); may: some V scale among the warp's may have a shift; wait_pv: O holds every
@@ -1097,7 +1140,7 @@ __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
     float mul = c2;  // of the row's products: the softmax scale, and the power of two of its Q terms
     if constexpr (kQ8) {
       wait(QFull, pieces & 1);
-      mul *= split_q(cx.base + Sm::q, red + 4 * 128, row, quad, half);
+      mul *= split_queries(cx.base + Sm::q, red + 4 * 128, row, quad, half);
       __syncwarp();
       if (lane == 0) mbar_arrive_pair(cx.leader_bar(QReady));
       barrier_rows(quad);  // red is free again

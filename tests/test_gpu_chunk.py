@@ -283,15 +283,28 @@ def test_a_value_that_is_no_number_reaches_every_token_that_sees_it(new, held, a
     assert torch.isfinite(s.lse).all()
 
 
-def test_query_rows_do_not_meet():
+@KV
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_query_rows_do_not_meet(kv, what):
     """A query that is no number makes its own rows so and no others."""
-    s = Step([9], [100], seed=18)
-    s.q[4, 7, 3] = float("nan")
+    s = Step([9], [100], kv, seed=18)
+    s.q[4, 7, 3] = what
     s.call()
     bad = torch.zeros((9, HEADS), dtype=torch.bool, device="cuda")
     bad[4, 7] = True
     assert torch.isnan(s.out[bad]).all() and torch.isfinite(s.out[~bad]).all()
     assert torch.isnan(s.lse[bad]).all() and torch.isfinite(s.lse[~bad]).all()
+
+
+@KV
+@pytest.mark.parametrize("power", [-133, -126, -110, -60, -9, 9, 40, 100])
+def test_query_norms(kv, power):
+    """Queries from the smallest bf16 numbers to the largest, the scale undoing their power where fp32 holds it: 100 elements of a
+    row are 2^-10 of the others, so that both terms of a quantised cache's queries count."""
+    s = Step([6], [300], kv, seed=28, pad=0)
+    s.q[:, :, :100] *= 2.0 ** -10
+    s.q.copy_((s.q.double() * 2.0 ** power).bfloat16())
+    s.run(scale=SCALE * 2.0 ** min(max(-power, -100), 120))
 
 
 @KV
