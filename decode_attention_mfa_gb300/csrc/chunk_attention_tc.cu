@@ -27,7 +27,7 @@
 //     the next P V.
 //
 // Work split: the units of all tiles, one after the other, form a line
-// (kChunkPieceUnits more for each tile); each pair takes an equal range of it. A
+// (a few more for each tile); each pair takes an equal range of it. A
 // tile that lies whole in a range is written out; of the others, one at each end
 // of a range at most, normalised partial results go to the workspace and the
 // combine joins them. Units of the first i tiles of a sequence have a closed form,
@@ -183,13 +183,13 @@ __device__ __forceinline__ uint32_t floor_sum(uint32_t m) {
   return 16 * q * (q - 1) + q * ((m & 31) + 1);
 }
 __device__ __forceinline__ int units_of(int keys) { return (keys + kUnitKeys - 1) / kUnitKeys; }
-__device__ __forceinline__ int full_tiles_cost(int i, int a) {
+__device__ __forceinline__ int full_tiles_cost(int i, int a, int piece_units) {
   const uint32_t z = (uint32_t)(a + kUnitKeys - 1) >> 2;
-  return (int)(floor_sum((uint32_t)i + z) - floor_sum(z)) + i * kChunkPieceUnits;
+  return (int)(floor_sum((uint32_t)i + z) - floor_sum(z)) + i * piece_units;
 }
 __device__ __forceinline__ int tiles_of(int n) { return (n + kTokens - 1) / kTokens; }
-__device__ __forceinline__ int sequence_cost(int len, int n) {
-  return n > 0 ? full_tiles_cost(tiles_of(n) - 1, len - n) + units_of(len) + kChunkPieceUnits : 0;
+__device__ __forceinline__ int sequence_cost(int len, int n, int piece_units) {
+  return n > 0 ? full_tiles_cost(tiles_of(n) - 1, len - n, piece_units) + units_of(len) + piece_units : 0;
 }
 // Tokens of b that see a key at all: the last len of them.
 __device__ __forceinline__ int seeing(const PlanSmem& s, int b) { return min(s.row[b + 1] - s.row[b], s.len[b]); }
@@ -230,7 +230,7 @@ __device__ void build_plan(const ChunkParams& p, PlanSmem& s, uint32_t* err) {
   }
 #pragma unroll 1
   for (int c = warp; c < chunks; c += warps) {
-    const int b = 32 * c + lane, u = b < p.B ? sequence_cost(s.len[b], seeing(s, b)) : 0;
+    const int b = 32 * c + lane, u = b < p.B ? sequence_cost(s.len[b], seeing(s, b), p.piece_units) : 0;
     const int x = warp_inclusive_sum(u, lane);
     if (b < p.B) s.cost[b] = x - u;
     if (b == p.B - 1) s.cost[p.B] = x;
@@ -280,10 +280,10 @@ __device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem&
       if (q.x == q.first) i1 = 0;
       while (i0 < i1) {
         const int mid = (i0 + i1 + 1) >> 1;
-        if (q.first + full_tiles_cost(mid, q.a) <= q.x) i0 = mid; else i1 = mid - 1;
+        if (q.first + full_tiles_cost(mid, q.a, p.piece_units) <= q.x) i0 = mid; else i1 = mid - 1;
       }
       q.i = i0;
-      q.first += full_tiles_cost(i0, q.a);
+      q.first += full_tiles_cost(i0, q.a, p.piece_units);
     } else {
       ++q.i;
       q.first = q.x;
@@ -293,9 +293,9 @@ __device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem&
     q.seen0 = q.a + kTokens * q.i + 1;
     q.seen = q.seen0 + q.tokens - 1;
     q.units = units_of(q.seen);
-    q.u0 = max(0, q.x - q.first - kChunkPieceUnits);
-    q.u1 = min(q.units, hi - q.first - kChunkPieceUnits);
-    q.x = q.first + kChunkPieceUnits + q.units;
+    q.u0 = max(0, q.x - q.first - p.piece_units);
+    q.u1 = min(q.units, hi - q.first - p.piece_units);
+    q.x = q.first + p.piece_units + q.units;
     if (q.u0 < q.u1) return true;
   }
   return false;
@@ -312,8 +312,8 @@ __device__ void publish_parts(const ChunkParams& p, const PlanSmem& s, int lane)
     if (w < W && units > 0) {
       const int lo = range_of_pair(w, units, W), hi = range_of_pair(w + 1, units, W);
       Piece q;
-      if (next_piece(p, s, hi - 1, hi, q) && q.u1 < q.units && lo <= q.first + kChunkPieceUnits)
-        part = make_int4(q.row, q.tokens, w, pair_of_unit(q.first + kChunkPieceUnits + q.units - 1, units, W) - w + 1);
+      if (next_piece(p, s, hi - 1, hi, q) && q.u1 < q.units && lo <= q.first + p.piece_units)
+        part = make_int4(q.row, q.tokens, w, pair_of_unit(q.first + p.piece_units + q.units - 1, units, W) - w + 1);
     }
     const uint32_t some = __ballot_sync(0xffffffffu, part.y > 0);
     if (part.y > 0) p.parts[found + __popc(some & ((1u << lane) - 1))] = part;

@@ -539,7 +539,7 @@ mfa_status_t chunk_common(const void* q, const void* k_cache, const void* v_cach
                                       workspace, (size_t)-1, 1, &plan);
   if (st != MFA_OK) return st;
   // every position of the line of work fits 31 bits
-  const long long tiles = (long long)max_tokens / kChunkTileTokens + batch, units = (long long)(max_pages + 1) / 2 + kChunkPieceUnits;
+  const long long tiles = (long long)max_tokens / kChunkTileTokens + batch, units = (long long)(max_pages + 1) / 2 + kChunkPieceUnitsQuantised;
   if (max_pages > (1 << 24) || tiles * units > 0x7fffffffLL)
     return fail(MFA_ERR_INVALID_ARG, "max_tokens * max_pages too large");
   DeviceInfo info;
@@ -570,6 +570,7 @@ mfa_status_t chunk_common(const void* q, const void* k_cache, const void* v_cach
   p.max_pages = max_pages;
   p.num_pages = num_pages;
   p.pairs = w.pairs;
+  p.piece_units = fmt == kKvBf16 ? kChunkPieceUnits : kChunkPieceUnitsQuantised;
   p.fmt = fmt;
   p.wait_budget_ns = g_wait_budget_ns.load(std::memory_order_relaxed);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

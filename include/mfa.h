@@ -295,7 +295,7 @@ mfa_status_t mfa_kv_read_fp4(const void* k_cache, const void* v_cache, const flo
  * Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers, batch outside
  * [1, MFA_MAX_BATCH], max_tokens outside [0, MFA_MAX_CHUNK_TOKENS], max_pages
  * outside [1, 2^24], num_pages < 1, (max_tokens / 4 + batch) *
- * (max_pages / 2 + 4) above 2^31 - 1), MFA_ERR_WORKSPACE. Device errors as in
+ * ((max_pages + 1) / 2 + 4) above 2^31 - 1), MFA_ERR_WORKSPACE. Device errors as in
  * mfa_decode_attention; q_starts out of their range are clamped to the largest
  * before them (MFA_DEVERR_CAPACITY). */
 size_t mfa_chunk_workspace_bytes(int batch, int max_tokens);
