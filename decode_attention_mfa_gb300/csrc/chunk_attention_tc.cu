@@ -194,19 +194,41 @@ __device__ __forceinline__ int sequence_cost(int len, int n, int piece_units) {
 // Tokens of b that see a key at all: the last len of them.
 __device__ __forceinline__ int seeing(const PlanSmem& s, int b) { return min(s.row[b + 1] - s.row[b], s.len[b]); }
 
+__device__ __forceinline__ int running_max(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x = max(x, y);
+  }
+  return x;
+}
+
 // All threads; ends with a barrier.
 __device__ void build_plan(const ChunkParams& p, PlanSmem& s, uint32_t* err) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, kThreads = blockDim.x, warps = blockDim.x >> 5;
+  if (p.B < 32) {  // one warp, without a barrier between the steps
+    if (warp == 0) {
+      const int raw = lane <= p.B ? __ldcg(p.q_starts + lane) : 0, raw_len = lane < p.B ? __ldcg(p.seq_lens + lane) : 0;
+      const int len = clamp_len(raw_len, p.max_pages * kPageSize, err);
+      const int x = running_max(min(max(raw, 0), p.max_tokens), lane);
+      if (lane <= p.B && x != raw) raise_error(err, MFA_DEVERR_CAPACITY);
+      const int next = __shfl_down_sync(0xffffffffu, x, 1);
+      const int u = lane < p.B ? sequence_cost(len, min(next - x, len), p.piece_units) : 0;
+      const int before = warp_inclusive_sum(u, lane) - u;
+      if (lane < p.B) s.len[lane] = len;
+      if (lane <= p.B) {
+        s.row[lane] = x;
+        s.cost[lane] = before;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   const int starts = (p.B + 32) / 32, chunks = (p.B + 31) / 32;  // 32 at a time, a warp each
 #pragma unroll 1
   for (int c = warp; c < starts; c += warps) {
     const int i = 32 * c + lane, raw = i <= p.B ? __ldcg(p.q_starts + i) : 0;
-    int x = min(max(raw, 0), p.max_tokens);
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x = max(x, y);
-    }
+    const int x = running_max(min(max(raw, 0), p.max_tokens), lane);
     if (i <= p.B) {
       if (x != raw) raise_error(err, MFA_DEVERR_CAPACITY);
       s.row[i] = x;
@@ -456,7 +478,10 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
     na = TilePages::load(2 * next.u0 + lane, end, p, next);
     nb = TilePages::load(2 * next.u0 + 32 + lane, end, p, next);
   };
-  if (more) ask();
+  if (more) {
+    ask();
+    if (kQ8) good = load_q(next);  // (first, as it is split; bf16: K first, 0.1 us of a short call)
+  }
   while (good && more) {
     q = next;
     TilePages ids;
@@ -473,7 +498,7 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
       const int pb = 2 * u + 1 < q.pages() ? ids.get(2 * u + 1, p, q, lane) : -1;
       good = load_k(cnt, pa, pb);
       if (good && va >= 0) good = load_v(cnt - 1, va, vb, vtail);
-      if (good && u == q.u0) good = load_q(q);
+      if (good && u == q.u0 && (!kQ8 || cnt > 0)) good = load_q(q);
       ++cnt;
       va = pa;
       vb = pb;
