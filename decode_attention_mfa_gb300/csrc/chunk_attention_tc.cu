@@ -151,16 +151,6 @@ struct Ctx {
   __device__ bool wait_warp(int i, uint32_t parity) const { return __all_sync(0xffffffffu, wait(i, parity)); }
 };
 
-// TMA load into this CTA's shared memory that completes on a barrier of the pair's leader.
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t leader_bar,
-                                                 uint64_t cache_hint) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(leader_bar), "l"(cache_hint)
-      : "memory");
-}
-
 // Rows of a tile's end held values that are no numbers: told to both CTAs' softmax warps, by piece. They look behind the
 // piece's last P V, which waits for the arrival behind this; a fourth piece is not begun before they have. Rare.
 __device__ __noinline__ void set_odd(uint32_t odd, uint32_t piece) {
@@ -1073,16 +1063,6 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
     done = !barrier_rows_or(quad, all.x + all.y > kMostSum || may);
   }
   if (!done) {
-    if (kQ8 && barrier_rows_or(quad, may)) {
-      if (!st.fresh) wait_pv();
-      tc_fence_after();
-      const float2 ml = shifted_unit<R>(tx, o_addr, sc, cols, mul, st.m, st.l, st.fresh, red + 4 * 128, row, half);
-      st.m = ml.x;
-      st.l = ml.y;
-      st.open = __any_sync(0xffffffffu, st.m == -INFINITY);
-      st.fresh = false;
-      return;
-    }
     float2 y[32];
     load(0, *reinterpret_cast<float2 (*)[16]>(y));
     load(32, *reinterpret_cast<float2 (*)[16]>(y + 16));
@@ -1098,7 +1078,19 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
     float* mine = red + (turn ? 256 : 0);  // two turns: who is two exchanges ahead has seen the other read
     turn = !turn;
     mine[half * 128 + row] = big;
-    barrier_rows(quad);
+    bool shifted = false;
+    if constexpr (kQ8) shifted = barrier_rows_or(quad, may);
+    else barrier_rows(quad);
+    if (kQ8 && shifted) {  // nothing has been done yet
+      if (!st.fresh) wait_pv();
+      tc_fence_after();
+      const float2 ml = shifted_unit<R>(tx, o_addr, sc, cols, mul, st.m, st.l, st.fresh, red + 4 * 128, row, half);
+      st.m = ml.x;
+      st.l = ml.y;
+      st.open = __any_sync(0xffffffffu, st.m == -INFINITY);
+      st.fresh = false;
+      return;
+    }
     const float most = fmaxf(big, mine[(half ^ 1) * 128 + row]);
     // 64 weights up to 2^9 add up to kMostSum
     const float m_new = st.open || most > st.m + (9.0f - moved_to<kQ8>()) ? fmaxf(st.m, most) : st.m;
