@@ -446,7 +446,8 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
   auto load_q = [&](const Piece& q) -> bool {
     if (kQ8 && pieces > 0 && !cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1)) return false;
     if (kQ8 && lane == 0) mbar_arrive_expect_tx(cx.bar(QFull), kQBytes);
-    const int y = (q.row + 2 * r) * kHeads;
+    // (rows past the tensor's end, for a CTA without a token, come as zeros and from nowhere)
+    const int y = (2 * r < q.tokens ? q.row + 2 * r : p.max_tokens) * kHeads;
 #pragma unroll 1
     for (int d = 0; d < 4; ++d) {
       if (!kQ8 && pieces > 0 && !cx.wait_warp(QFree + d, (pieces - 1) & 1)) return false;
