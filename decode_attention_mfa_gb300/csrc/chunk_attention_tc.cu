@@ -441,19 +441,22 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
     return true;
   };
   uint32_t cnt = 0;  // units whose K has been loaded
-  // Q of a piece, the rows of this CTA's two tokens (of a tile's end, whatever lies behind its last one): by block, as the
+  // Q of a piece, the rows of this CTA's two tokens: by block, as the
   // piece before is done with each (quantised: with all of them)
   auto load_q = [&](const Piece& q) -> bool {
     if (kQ8 && pieces > 0 && !cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1)) return false;
     if (kQ8 && lane == 0) mbar_arrive_expect_tx(cx.bar(QFull), kQBytes);
-    // (rows past the tensor's end, for a CTA without a token, come as zeros and from nowhere)
-    const int y = (2 * r < q.tokens ? q.row + 2 * r : p.max_tokens) * kHeads;
+    // (rows past the tensor's end, in a missing token's place, come as zeros and from nowhere)
+    const int y0 = (2 * r < q.tokens ? q.row + 2 * r : p.max_tokens) * kHeads;
+    const int y1 = (2 * r + 1 < q.tokens ? q.row + 2 * r + 1 : p.max_tokens) * kHeads;
 #pragma unroll 1
     for (int d = 0; d < 4; ++d) {
       if (!kQ8 && pieces > 0 && !cx.wait_warp(QFree + d, (pieces - 1) & 1)) return false;
       if (elect_one()) {
         if (!kQ8 && r == 0) mbar_arrive_expect_tx(cx.bar(QFull + d), 2 * kQBytes / 4);
-        tma_load_3d_pair(cx.base + Sm::q + d * (kQBytes / 4), qmap, 0, y, d, kQ8 ? cx.bar(QFull) : cx.leader_bar(QFull + d), pol);
+        const uint32_t dst = cx.base + Sm::q + d * (kQBytes / 4), bar = kQ8 ? cx.bar(QFull) : cx.leader_bar(QFull + d);
+        tma_load_3d_pair(dst, qmap, 0, y0, d, bar, pol);
+        tma_load_3d_pair(dst + kQBytes / 8, qmap, 0, y1, d, bar, pol);
       }
     }
     ++pieces;

@@ -577,7 +577,7 @@ mfa_status_t chunk_common(const void* q, const void* k_cache, const void* v_cach
   CUtensorMap kmap, vmap, qmap;
   const uint64_t rows = (uint64_t)num_pages * kPageSize;
   const uint32_t blocks = fmt == kKvBf16 ? 4 : 2;  // of a K row; a CTA takes half of those of V
-  if ((st = encode_row_blocks(&qmap, q, (uint64_t)max_tokens * kHeads, kKvBf16, 2 * kHeads, 1)) != MFA_OK ||
+  if ((st = encode_row_blocks(&qmap, q, (uint64_t)max_tokens * kHeads, kKvBf16, kHeads, 1)) != MFA_OK ||
       (st = encode_row_blocks(&kmap, k_cache, rows, fmt, kPageSize, blocks)) != MFA_OK ||
       (st = encode_row_blocks(&vmap, v_cache, rows, fmt, kPageSize, blocks / 2)) != MFA_OK)
     return st;
