@@ -20,18 +20,21 @@
 // from, their masks, and that a prompt makes thousands of short tiles, so that
 // what happens between two of them counts:
 //   - S of a tile's first unit is issued before P V of the last tile's last one
-//     where Q is there by then: its four blocks of 64 dimensions are loaded, from
-//     L2, as the last S of the tile before has read each of them;
-//   - O of a tile is read (into registers, as bf16) while S of the next one's
-//     second unit runs, after the softmax of its first unit, and written behind
-//     the next P V.
+//     where Q is there by then: its four blocks of 64 dimensions are loaded as the
+//     last S of the tile before has read each of them;
+//   - O of a tile is read into registers as bf16, and free for the next tile,
+//     before any of it is written; on a bf16 cache by the softmax warps behind the
+//     first unit of the next tile (by four warps of their own, which leave the
+//     others 128 registers, 16 prompts of 512 tokens took 188 us instead of 163),
+//     on a quantised one by the warps that convert V (by the softmax warps, which
+//     split Q at that time, 307 us instead of 223).
 //
-// Work split: the units of all tiles, one after the other, form a line
-// (a few more for each tile); each pair takes an equal range of it. A
-// tile that lies whole in a range is written out; of the others, one at each end
-// of a range at most, normalised partial results go to the workspace and the
-// combine joins them. Units of the first i tiles of a sequence have a closed form,
-// so that nothing is kept for a tile.
+// Work split: the units of all tiles, one after the other, form a line (a few
+// more for each tile); each pair takes an equal range of it. A tile that lies
+// whole in a range is written out; of the others, one at each end of a range at
+// most, normalised partial results go to the workspace and the combine joins
+// them. Units of the first i tiles of a sequence have a closed form, so that
+// nothing is kept for a tile.
 //
 // Masks: a row's keys end where its token does, within the last 128 + 3 keys of
 // its tile. Logits behind it become weights of zero; V's rows behind the tile's
@@ -40,20 +43,31 @@
 // added at the end: 0 * NaN of a later token never reaches an earlier one.
 //
 // Warp roles:
-//   warps 0-7  softmax and output: thread = row = TMEM lane; warp w and w + 4
+//   warps 0-7  softmax (and output): thread = row = TMEM lane; warp w and w + 4
 //              share 32 rows, 64 keys of a unit each.
 //   warp 8     producer (TMA, each CTA its own halves, completing on the leader's
 //              barriers).
 //   warp 9     TMEM allocation, and MMA issue (one thread of the leader's; the
-//              other CTA's leaves the combine where the parts are).
+//              first pair's other one leaves the combine where the parts are).
 //   warp 10    V's rows behind the tile's last token and those that not all see.
-//   warps 10-13 (E4M3 and E2M1 caches, instead) V codes to f16, with the same.
+//   warps 10-13 (E4M3 and E2M1 caches, instead) V codes to f16, with the same, and
+//              the output.
 // Every wait is bounded (the wait budget), as in the split kernel.
 //
 // E4M3 and E2M1 caches: S is 8-bit MMAs (kind::f8f6f4) on the raw K codes, with Q
 // as two E4M3 terms under a power of two per row, split in shared memory when a
 // tile begins; V's codes times their scales become f16, and P is f16 as well (the
 // shared-prefix kernel says why).
+//
+// Measured, combine included: 2048 tokens behind 63488 in 4.56 ms (1900 TFLOP/s;
+// cuBLAS reaches 1896 in a burst, 1707 for seconds), the tensor cores 97% busy; 304
+// behind 16080 in 170 us, E4M3 180, E2M1 176. A unit takes the 2050 cycles of its
+// MMAs; what is lost between two tiles is 0.4 us for long tiles, and 2.6 us for the
+// tiles of 2.5 units that 512-token prompts have (16 of them 163 us: a chain of Q
+// and K from L2, 2 us each under load, the softmax of two units and the output),
+// on quantised caches 3 us (Q waits for the last S, and its split takes 1.7). 23
+// tokens behind 900 take 17 us: plan 1.2, page ids and first loads 1.5, a unit 3,
+// 128 KB of fp32 partial results a CTA 2.7, combine 4, two launches.
 #include <cuda_fp4.h>
 #include <type_traits>
 
@@ -1321,8 +1335,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
 // Joins the parts of the tiles that lie in several ranges. With O_s and lse_s of part s, M = max_s lse_s and
 // w_s = exp(lse_s - M):  out = sum_s w_s O_s / sum_s w_s,  lse = M + ln sum_s w_s.  A warp a row, four parts at a time, with a
 // running M. The first part is the second partial result of its pair (a tile that begins there), the others are the first ones
-// of the pairs behind it. Bound by latency: the list of tiles, then the parts of a row (its rows on one line of groups of eight,
-// which the blocks share; a grid with a block for every group of every pair took a call without parts 2.5 us longer).
+// of the pairs behind it. Bound by latency: the list of tiles, then the parts of a row (groups of eight rows on one line, which the
+// blocks share; a grid with a block for every group of every pair took a call without parts 2.5 us longer).
 constexpr int kCombineThreads = 256, kCombineRows = kCombineThreads / 32;
 constexpr int kCombineGroups = kChunkTileTokens * kHeads / kCombineRows;  // of a tile
 __global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(const ChunkParams p) {

@@ -167,13 +167,13 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendParams 
 // Quotients x / s, two at a time, as IEEE division rounds them: Markstein's
 // method (P. Markstein, "Computation of elementary functions on the IBM RISC
 // System/6000 processor", 1990). With y the rounded reciprocal of s, q = x y is
-// corrected twice by its exact remainder, q -= (q s - x) y: the first correction
-// leaves less than an ulp, the second the rounded quotient. The remainders are
-// exact while nothing underflows, which s in [2^-60, 2^60] and quotients above
-// 2^-10 (smaller ones are code 0 whatever their last bits) ensure. Written in -x
-// and -y, which also keeps the sign of a zero. Two instructions and a half a
-// value; with divisions the call took 33.6 us for 65,000 tokens, then 23.1, and 19.3 with
-// the maximum in bf16 pairs.
+// corrected by its exact remainder, q -= (q s - x) y. For any s that takes two
+// such steps; for the scales of a row, absmax / 6 or / 448 rounded, and its bf16
+// values one gives the rounded quotient (tests/test_quantiser_host.py goes through
+// all of their mantissas). The remainders are exact while nothing underflows, which
+// s in [2^-60, 2^60] and quotients above 2^-10 (smaller ones are code 0 whatever
+// their last bits) ensure. Written in -x and -y, which also keeps the sign of a
+// zero. With divisions the call took 33.6 us for 65,000 tokens to E4M3.
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   float2 d;
   asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
@@ -194,56 +194,75 @@ __device__ __forceinline__ float2 unpack_bf16x2(uint32_t w) {
   return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
 }
 
-// quantise_row_e4m3 and quantise_row_e2m1, with the same codes and scales. An E2M1 code is the conversion's (nearest, a
-// tie to the even code, beyond 6 saturating, NaN to 6), which of quotients below a quarter sees no more than their sign.
-template <bool kFp4>
-__device__ __forceinline__ void quantise_row_slots(const uint4 raw, uint8_t* __restrict__ dst,
-                                                   float* __restrict__ scale_out, int lane) {
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  const __nv_bfloat162* pairs = reinterpret_cast<const __nv_bfloat162*>(w);
+// quantise_row_e4m3 and quantise_row_e2m1, with the same codes and scales, by kLanes lanes: lane l has elements 8 l to 8 l + 7, and
+// of 16 lanes those 128 further on. An E2M1 code is the conversion's (nearest, a tie to the even code, beyond 6 saturating, NaN
+// to 6).
+template <bool kFp4, int kLanes>
+__device__ __forceinline__ void quantise_row_slots(const uint4 (&raw)[32 / kLanes], uint8_t* __restrict__ dst,
+                                                   float* __restrict__ scale_out, int l) {
+  constexpr int kPairs = 4 * (32 / kLanes);
+  uint32_t w[kPairs];
+#pragma unroll
+  for (int h = 0; h < 32 / kLanes; ++h) {
+    w[4 * h] = raw[h].x;
+    w[4 * h + 1] = raw[h].y;
+    w[4 * h + 2] = raw[h].z;
+    w[4 * h + 3] = raw[h].w;
+  }
   // the largest magnitude, a NaN left out of it as by fmaxf
-  const __nv_bfloat162 top = __hmax2(__hmax2(__habs2(pairs[0]), __habs2(pairs[1])), __hmax2(__habs2(pairs[2]), __habs2(pairs[3])));
+  const __nv_bfloat162* pairs = reinterpret_cast<const __nv_bfloat162*>(w);
+  __nv_bfloat162 top = __habs2(pairs[0]);
+#pragma unroll
+  for (int i = 1; i < kPairs; ++i) top = __hmax2(top, __habs2(pairs[i]));
   const float2 both = unpack_bf16x2(*reinterpret_cast<const uint32_t*>(&top));
-  // not negative (and of NaN alone 0): ordered as integers
-  const float amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(fmaxf(both.x, both.y), 0.0f))));
+  float amax = fmaxf(fmaxf(both.x, both.y), 0.0f);
+  if constexpr (kLanes == 32) {
+    // not negative (and of NaN alone 0): ordered as integers
+    amax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(amax)));
+  } else {
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  }
   const float s = (amax > 0.0f) ? __fdiv_rn(amax, kFp4 ? 6.0f : 448.0f) : 1.0f;
   auto convert = [](float2 q) -> uint32_t {
     if constexpr (kFp4) return __nv_cvt_float2_to_fp4x2(q, __NV_E2M1, cudaRoundNearest);
     else return __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
   };
-  uint32_t code[4];
+  uint32_t code[kPairs];
   if (s >= 0x1p-60f && s <= 0x1p60f) {
     const float y = -__frcp_rn(s);
     const float2 minus_y = make_float2(y, y), ss = make_float2(s, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       const float2 minus_x = unpack_bf16x2(w[i] ^ 0x80008000u);
-      float2 q = mul2(minus_x, minus_y);
-#pragma unroll
-      for (int k = 0; k < 2; ++k) q = fma2(fma2(ss, q, minus_x), minus_y, q);
-      code[i] = convert(q);
+      const float2 q = mul2(minus_x, minus_y);
+      code[i] = convert(fma2(fma2(ss, q, minus_x), minus_y, q));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kPairs; ++i) {
       const float2 x = unpack_bf16x2(w[i]);
       code[i] = convert(make_float2(__fdiv_rn(x.x, s), __fdiv_rn(x.y, s)));
     }
   }
-  if constexpr (kFp4)
-    reinterpret_cast<uint32_t*>(dst)[lane] = code[0] | code[1] << 8 | code[2] << 16 | code[3] << 24;
-  else
-    reinterpret_cast<uint2*>(dst)[lane] = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
-  if (lane == 0) *scale_out = s;
+#pragma unroll
+  for (int h = 0; h < 32 / kLanes; ++h) {
+    const uint32_t* c = code + 4 * h;
+    if constexpr (kFp4)
+      reinterpret_cast<uint32_t*>(dst)[kLanes * h + l] = c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24;
+    else
+      reinterpret_cast<uint2*>(dst)[kLanes * h + l] = make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+  }
+  if (l == 0) *scale_out = s;
 }
 
-// Rows scattered to the slots of a slot map: one warp per row of K or of V, kRows
-// such items a warp, all of whose loads are in flight before the first store. No
-// row depends on another, so the call is bound by latency for a decode step's
-// rows and by memory bandwidth for a prefill's (read 1 KB, write 1 KB or 520 B a
-// token): 128 rows 1.2 us, 16384 rows 3.7 us (9 TB/s, L2 among it), 65536 rows to
-// E4M3 19.2 us (5.3 TB/s).
+// Rows scattered to the slots of a slot map. No row depends on another, so the
+// call is bound by latency for a decode step's rows and by memory bandwidth for a
+// prefill's (read 1 KB, write 1 KB, 520 or 264 B a token): 128 rows 1.2 us, 16384
+// rows 3.7 us (9 TB/s, L2 among it), 65536 rows to E4M3 18.2 us (5.6
+// TB/s), to E2M1 18.1 us (4.7 TB/s).
 constexpr int kSlotThreads = 256;
+// bf16: a warp a row of K or of V, kRows such items a warp, all of whose loads are in flight before the first store.
 template <int kRows>
 __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_kernel(const AppendSlotsParams p) {
   const int lane = threadIdx.x & 31;
@@ -270,34 +289,59 @@ __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_kernel(const App
       if (lane == 0) raise_error(p.err, MFA_DEVERR_PAGE);
       continue;
     }
-    const bool is_v = (i0 + j) & 1;
-    if (p.fmt == kKvE4M3) {
-      quantise_row_slots<false>(row[j], static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * kHeadDim,
-                                (is_v ? p.v_scale : p.k_scale) + slot[j], lane);
-    } else if (p.fmt == kKvE2M1) {
-      quantise_row_slots<true>(row[j], static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * (kHeadDim / 2),
-                               (is_v ? p.v_scale : p.k_scale) + slot[j], lane);
-    } else {
-      uint16_t* dst = static_cast<uint16_t*>(is_v ? p.v_cache : p.k_cache) + slot[j] * kHeadDim;
-      reinterpret_cast<uint4*>(dst)[lane] = row[j];
-    }
+    uint16_t* dst = static_cast<uint16_t*>((i0 + j) & 1 ? p.v_cache : p.k_cache) + slot[j] * kHeadDim;
+    reinterpret_cast<uint4*>(dst)[lane] = row[j];
   }
 }
+// Quantised: kLanes lanes a row of K or of V. With half a warp, what there is to do for a row (its maximum, its scale and the
+// scale's reciprocal) takes half the instructions.
+template <bool kFp4, int kLanes>
+__global__ void __launch_bounds__(kSlotThreads) kv_append_slots_quantised_kernel(const AppendSlotsParams p) {
+  const int l = threadIdx.x & (kLanes - 1);
+  const long long item = (long long)blockIdx.x * (kSlotThreads / kLanes) + threadIdx.x / kLanes, r = item >> 1;
+  const bool is_v = item & 1;
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  uint4 row[32 / kLanes] = {};
+  long long slot = -1;
+  if (r < p.n_rows) {
+    slot = __ldcg(reinterpret_cast<const long long*>(p.slot_map) + r);
+    const uint4* src = reinterpret_cast<const uint4*>(is_v ? p.v_new + r * p.v_stride : p.k_new + r * p.k_stride);
+#pragma unroll
+    for (int h = 0; h < 32 / kLanes; ++h) row[h] = __ldcg(src + kLanes * h + l);
+  }
+  if (slot >= (long long)p.num_pages * kPageSize) {
+    if (l == 0) raise_error(p.err, MFA_DEVERR_PAGE);
+    slot = -1;
+  }
+  if (slot < 0) return;  // a padded row, of the warp's K and V alike
+  quantise_row_slots<kFp4, kLanes>(row, static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot * (kFp4 ? kHeadDim / 2 : kHeadDim),
+                                   (is_v ? p.v_scale : p.k_scale) + slot, l);
+}
 
+unsigned slot_blocks(long long warps) { return (unsigned)((warps + kSlotThreads / 32 - 1) / (kSlotThreads / 32)); }
 template <int kRows>
 cudaError_t launch_slots(const AppendSlotsParams& p, cudaStream_t stream) {
-  const long long warps = (2ll * p.n_rows + kRows - 1) / kRows;
-  const unsigned grid = (unsigned)((warps + kSlotThreads / 32 - 1) / (kSlotThreads / 32));
-  return launch_pdl(kv_append_slots_kernel<kRows>, dim3(grid), dim3(kSlotThreads), 0, stream, p);
+  const unsigned blocks = slot_blocks((2ll * p.n_rows + kRows - 1) / kRows);
+  return launch_pdl(kv_append_slots_kernel<kRows>, dim3(blocks), dim3(kSlotThreads), 0, stream, p);
+}
+template <bool kFp4, int kLanes>
+cudaError_t launch_slots_quantised(const AppendSlotsParams& p, cudaStream_t stream) {
+  const unsigned blocks = slot_blocks((2ll * p.n_rows * kLanes + 31) / 32);
+  return launch_pdl(kv_append_slots_quantised_kernel<kFp4, kLanes>, dim3(blocks), dim3(kSlotThreads), 0, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append_slots(const AppendSlotsParams& p, cudaStream_t stream) {
-  // Two items a warp halve the blocks that many rows take to launch, one is the shorter wait for few rows: 16384 rows,
-  // bf16 / E4M3, 4.6 / 6.2 us with one and 3.5 / 5.4 with two; 4096 rows 1.8 / 2.4 and 2.1 / 2.9.
-  constexpr int kManyRows = 8192;
-  return p.n_rows < kManyRows ? launch_slots<1>(p, stream) : launch_slots<2>(p, stream);
+  // bf16: two items a warp halve the blocks that many rows take to launch, one is the shorter wait for few rows: 16384 rows 4.6
+  // us with one and 3.5 with two; 4096 rows 1.8 and 2.1. Quantised, E4M3: 65536 rows 20.5 us with a warp a row and 18.2 with half
+  // a warp, 8192 rows 3.9 and 3.1, 128 rows 1.55 and 1.75; a warp for four rows or eight 18.4 and 20.0.
+  constexpr int kManyRows = 8192, kManyQuantised = 2048;
+  if (p.fmt == kKvBf16) return p.n_rows >= kManyRows ? launch_slots<2>(p, stream) : launch_slots<1>(p, stream);
+  const bool many = p.n_rows >= kManyQuantised;
+  if (p.fmt == kKvE4M3) return many ? launch_slots_quantised<false, 16>(p, stream) : launch_slots_quantised<false, 32>(p, stream);
+  return many ? launch_slots_quantised<true, 16>(p, stream) : launch_slots_quantised<true, 32>(p, stream);
 }
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {

@@ -282,8 +282,9 @@ mfa_status_t mfa_kv_read_fp4(const void* k_cache, const void* v_cache, const flo
  *             [max_tokens][64]. Rows outside [q_starts[0], q_starts[batch]) are
  *             neither read nor written;
  *   q_starts: [device] int32 [batch + 1], non-decreasing within [0, max_tokens].
- * A token that sees no position (n_b > seq_lens[b]) gets out = 0, lse = -inf.
- * Nothing that a token does not see reaches its results, not even a NaN or an
+ * A token that sees no position (n_b > seq_lens[b]) gets out = 0, lse = -inf; so
+ * the rows of a request that mfa_reserve_pages left as it was are written, but
+ * hold attention of its last positions, or these. Nothing that a token does not see reaches its results, not even a NaN or an
  * infinity. Repeated calls give the same bits.
  * workspace: [device] at least mfa_chunk_workspace_bytes(batch, max_tokens)
  * bytes (about 40 MB, whatever the sizes), initialised once by
@@ -291,7 +292,9 @@ mfa_status_t mfa_kv_read_fp4(const void* k_cache, const void* v_cache, const flo
  * E4M3 and E2M1 caches (mfa_chunk_attention_fp8, _fp4): q enters as the sum of
  * two E4M3 terms under a power of two of its row (within 2^-18.8 of the row's
  * largest |q|), V's values and the weights as f16, as in
- * mfa_decode_attention_prefix_fp8. Scales 16-byte, 4-bit caches 32-byte aligned.
+ * mfa_decode_attention_prefix_fp8. A batch of one token each is faster with
+ * mfa_decode_attention, _fp8, _fp4, from three or four tokens each on this call
+ * is faster than mfa_decode_attention_mtp. Scales 16-byte, 4-bit caches 32-byte aligned.
  * Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers, batch outside
  * [1, MFA_MAX_BATCH], max_tokens outside [0, MFA_MAX_CHUNK_TOKENS], max_pages
  * outside [1, 2^24], num_pages < 1, (max_tokens / 4 + batch) *
