@@ -327,25 +327,37 @@ __device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem&
   return false;
 }
 
-// Where the combine finds the partial results: for every pair in whose range a tile begins that ends behind it, in order,
-// then entries without tokens. One warp of the first pair.
+// Groups of eight warps that the combine takes for a tile: of one and two parts a warp takes two rows, of up to four one, of more
+// half a row.
+__device__ __forceinline__ int combine_groups(int tokens, int parts) {
+  return tokens * kHeads / 8 * 2 / (parts <= 2 ? 4 : parts <= 4 ? 2 : 1);
+}
+
+// Where the combine finds the partial results: for every pair in whose range a tile begins that ends behind it, in order, then
+// entries without tokens, the first of them with the number of all groups. One warp of the first pair.
 __device__ void publish_parts(const ChunkParams& p, const PlanSmem& s, int lane) {
   const int units = s.cost[p.B], W = busy_pairs(p, units);
-  int found = 0;
+  int found = 0, groups = 0;
   for (int w0 = 0; w0 < W; w0 += 32) {
     const int w = w0 + lane;
-    int4 part = make_int4(0, 0, 0, 0);
+    int row = 0, tokens = 0, parts = 0;
     if (w < W && units > 0) {
       const int lo = range_of_pair(w, units, W), hi = range_of_pair(w + 1, units, W);
       Piece q;
-      if (next_piece(p, s, hi - 1, hi, q) && q.u1 < q.units && lo <= q.first + p.piece_units)
-        part = make_int4(q.row, q.tokens, w, pair_of_unit(q.first + p.piece_units + q.units - 1, units, W) - w + 1);
+      if (next_piece(p, s, hi - 1, hi, q) && q.u1 < q.units && lo <= q.first + p.piece_units) {
+        row = q.row;
+        tokens = q.tokens;
+        parts = pair_of_unit(q.first + p.piece_units + q.units - 1, units, W) - w + 1;
+      }
     }
-    const uint32_t some = __ballot_sync(0xffffffffu, part.y > 0);
-    if (part.y > 0) p.parts[found + __popc(some & ((1u << lane) - 1))] = part;
+    const uint32_t some = __ballot_sync(0xffffffffu, tokens > 0);
+    const int mine = tokens > 0 ? combine_groups(tokens, parts) : 0, upto = warp_inclusive_sum(mine, lane);
+    if (tokens > 0)
+      p.parts[found + __popc(some & ((1u << lane) - 1))] = make_int4(row, tokens | parts << 8, w, groups + upto - mine);
     found += __popc(some);
+    groups += __shfl_sync(0xffffffffu, upto, 31);
   }
-  for (int i = found + lane; i < p.pairs; i += 32) p.parts[i] = make_int4(0, 0, 0, 0);
+  for (int i = found + lane; i <= p.pairs; i += 32) p.parts[i] = make_int4(0, 0, 0, i == found ? groups : 0x7fffffff);
 }
 
 // The output of tokens that see no key. One warp of each pair.
@@ -1333,64 +1345,121 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
 
 // ---------------------------------------------------------------- combine
 // Joins the parts of the tiles that lie in several ranges. With O_s and lse_s of part s, M = max_s lse_s and
-// w_s = exp(lse_s - M):  out = sum_s w_s O_s / sum_s w_s,  lse = M + ln sum_s w_s.  A warp a row, four parts at a time, with a
-// running M. The first part is the second partial result of its pair (a tile that begins there), the others are the first ones
-// of the pairs behind it. Bound by latency: the list of tiles, then the parts of a row (groups of eight rows on one line, which the
-// blocks share; a grid with a block for every group of every pair took a call without parts 2.5 us longer).
-constexpr int kCombineThreads = 256, kCombineRows = kCombineThreads / 32;
-constexpr int kCombineGroups = kChunkTileTokens * kHeads / kCombineRows;  // of a tile
-__global__ void __launch_bounds__(kCombineThreads) chunk_combine_kernel(const ChunkParams p) {
-  const int lane = threadIdx.x & 31;
-  pdl_launch_dependents();
-  pdl_wait_prior_grid();
+// w_s = exp(lse_s - M):  out = sum_s w_s O_s / sum_s w_s,  lse = M + ln sum_s w_s.  A warp takes half a row, eight parts at a time,
+// with a running M, or, of tiles with up to four and two parts, one or two rows: eight loads of 16 bytes in flight a lane. The first part is the second partial result of its pair (a tile that begins there), the others are the first ones of the
+// pairs behind it. Bound by latency: the list of tiles, then the parts, of groups on one line that the blocks share. Three blocks an SM are there at once; with more a call without parts took 1 us longer, and with four parts of a
+// row at a time 23 tokens behind 900 took 1.7 us longer.
+constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32, kCombineBlocksPerPair = 6;
+static_assert(kCombineWarps == 8, "combine_groups");
+// kRows rows from r on of a tile whose first row is `first` and whose first part is pair `pair`'s; kHalves halves of them from
+// `half` on, kParts parts at a time; dims 4 lane .. 4 lane + 3 of a half.
+template <int kRows, int kHalves, int kParts>
+__device__ __forceinline__ void combine_rows(const ChunkParams& p, int first, int pair, int parts, int r, int half, int lane) {
+  static_assert(kRows * kHalves * kParts == 8, "loads in flight");
+  float mx[kRows], den[kRows], acc[kRows][kHalves][4];
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    mx[j] = -INFINITY;
+    den[j] = 0.0f;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[j][h][c] = 0.0f;
+  }
 #pragma unroll 1
-  for (int g = blockIdx.x; g < p.pairs * kCombineGroups; g += gridDim.x) {
-    const int4 at = __ldcg(p.parts + g / kCombineGroups);  // first row, tokens, first pair, parts
-    if (at.y == 0) return;  // nor has any behind it
-    const int r = (g % kCombineGroups) * kCombineRows + (threadIdx.x >> 5);
-    if (r >= at.y * kHeads) continue;
-    auto part = [&](int i) -> size_t { return (size_t)(2 * (at.z + i) + (i == 0)) * 256 + r; };
-    float mx = -INFINITY, den = 0.0f, acc[8] = {};
-    constexpr int kAtOnce = 4;  // parts whose loads are in flight together
-#pragma unroll 1
-    for (int i0 = 0; i0 < at.w; i0 += kAtOnce) {
-      float4 x[kAtOnce][2];
-      float z[kAtOnce];
+  for (int i0 = 0; i0 < parts; i0 += kParts) {
+    float4 x[kRows][kHalves][kParts];
+    float z[kRows][kParts];
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        z[k] = -INFINITY;
-        if (i0 + k < at.w) {
-          const float4* src = reinterpret_cast<const float4*>(p.part_o + part(i0 + k) * kHeadDim) + 2 * lane;
-          z[k] = __ldcg(p.part_lse + part(i0 + k));
-          x[k][0] = __ldcg(src);
-          x[k][1] = __ldcg(src + 1);
-        }
-      }
-      const float before = mx;
+    for (int k = 0; k < kParts; ++k) {
+      const int i = min(i0 + k, parts - 1);  // (behind the last part: the last one, without weight)
+      const size_t part = (size_t)(2 * (pair + i) + (i == 0)) * 256 + r;
 #pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) mx = fmaxf(mx, z[k]);
-      const float base = mx == -INFINITY ? 0.0f : mx;  // (no finite logit so far: weights of 0)
-      const float old = exp2f((before - base) * kLog2e);
-      den *= old;
+      for (int j = 0; j < kRows; ++j) {
+        z[j][k] = __ldcg(p.part_lse + part + j);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] = old == 0.0f ? 0.0f : acc[c] * old;
-#pragma unroll
-      for (int k = 0; k < kAtOnce; ++k) {
-        const float w = exp2f((z[k] - base) * kLog2e);
-        den += w;
-        if (w == 0.0f) continue;  // of weight 0 (or no part): left out, never scaled
-        const float v[8] = {x[k][0].x, x[k][0].y, x[k][0].z, x[k][0].w, x[k][1].x, x[k][1].y, x[k][1].z, x[k][1].w};
-#pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = fmaf(w, v[c], acc[c]);
+        for (int h = 0; h < kHalves; ++h)
+          x[j][h][k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + (part + j) * kHeadDim) + 32 * (half + h) + lane);
       }
     }
-    const float inv = 1.0f / den;
-    const size_t row = (size_t)at.x * kHeads + r;
-    uint32_t w[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c) w[c] = pack_bf16(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-    reinterpret_cast<uint4*>(p.out + row * kHeadDim)[lane] = make_uint4(w[0], w[1], w[2], w[3]);
-    if (lane == 0) p.lse[row] = mx + log2f(den) * kLn2;
+    for (int j = 0; j < kRows; ++j) {
+      const float before = mx[j];
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        if (i0 + k >= parts) z[j][k] = -INFINITY;
+        mx[j] = fmaxf(mx[j], z[j][k]);
+      }
+      const float base = mx[j] == -INFINITY ? 0.0f : mx[j];  // (no finite logit so far: weights of 0)
+      const float old = exp2f((before - base) * kLog2e);
+      den[j] *= old;
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[j][h][c] = old == 0.0f ? 0.0f : acc[j][h][c] * old;
+#pragma unroll
+      for (int k = 0; k < kParts; ++k) {
+        const float w = exp2f((z[j][k] - base) * kLog2e);
+        den[j] += w;
+        if (w != 0.0f) {  // of weight 0 (or no part): left out, never scaled
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            acc[j][h][0] = fmaf(w, x[j][h][k].x, acc[j][h][0]);
+            acc[j][h][1] = fmaf(w, x[j][h][k].y, acc[j][h][1]);
+            acc[j][h][2] = fmaf(w, x[j][h][k].z, acc[j][h][2]);
+            acc[j][h][3] = fmaf(w, x[j][h][k].w, acc[j][h][3]);
+          }
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const float inv = 1.0f / den[j];
+    const size_t row = (size_t)first * kHeads + r + j;
+#pragma unroll
+    for (int h = 0; h < kHalves; ++h)
+      reinterpret_cast<uint2*>(p.out + row * kHeadDim)[32 * (half + h) + lane] =
+          make_uint2(pack_bf16(acc[j][h][0] * inv, acc[j][h][1] * inv), pack_bf16(acc[j][h][2] * inv, acc[j][h][3] * inv));
+    if (half == 0 && lane == 0) p.lse[row] = mx[j] + log2f(den[j]) * kLn2;
+  }
+}
+__global__ void __launch_bounds__(kCombineThreads, 3) chunk_combine_kernel(const ChunkParams p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  // The list by one warp of a block: by all of them, their requests for the same lines take the call 1.4 us.
+  static_assert((kChunkMaxPairs + 1) % 32 == 0, "lanes");
+  __shared__ int4 list[kChunkMaxPairs + 1];
+  __shared__ int s_groups;
+  if (warp == 0) {
+    constexpr int kHeld = (kChunkMaxPairs + 32) / 32;
+    int4 e[kHeld];
+    int groups = 0x7fffffff;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k)
+      e[k] = 32 * k + lane <= p.pairs ? __ldcg(p.parts + 32 * k + lane) : make_int4(0, 0, 0, 0x7fffffff);
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      list[32 * k + lane] = e[k];
+      if (e[k].y == 0) groups = min(groups, e[k].w);
+    }
+    groups = __reduce_min_sync(0xffffffffu, groups);
+    if (lane == 0) s_groups = groups;
+  }
+  __syncthreads();
+  int i = 0;  // the tile of group g
+#pragma unroll 1
+  for (int g = blockIdx.x; g < s_groups; g += gridDim.x) {
+    while (g >= list[i + 1].w) ++i;
+    const int4 at = list[i];  // first row, tokens | parts << 8, first pair, first group
+    const int first = at.x, parts = at.y >> 8, item = (g - at.w) * kCombineWarps + warp;
+    if (parts <= 2)
+      combine_rows<2, 2, 2>(p, first, at.z, parts, 2 * item, 0, lane);
+    else if (parts <= 4)
+      combine_rows<1, 2, 4>(p, first, at.z, parts, item, 0, lane);
+    else
+      combine_rows<1, 1, 8>(p, first, at.z, parts, item >> 1, item & 1, lane);
   }
 }
 
@@ -1413,7 +1482,7 @@ cudaError_t launch_chunk_attention_tc(const ChunkParams& p, const CUtensorMap& k
 }
 
 cudaError_t launch_chunk_combine(const ChunkParams& p, cudaStream_t stream) {
-  return launch_pdl(chunk_combine_kernel, dim3(8 * p.pairs), dim3(kCombineThreads), 0, stream, p);
+  return launch_pdl(chunk_combine_kernel, dim3(kCombineBlocksPerPair * p.pairs), dim3(kCombineThreads), 0, stream, p);
 }
 
 }  // namespace mfa

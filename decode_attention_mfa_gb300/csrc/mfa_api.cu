@@ -511,13 +511,13 @@ struct ChunkPlan {
   size_t part_o, part_lse, parts, total;  // byte offsets
 };
 void fill_chunk_plan(int num_sms, ChunkPlan* w) {
-  w->pairs = std::max(1, num_sms / 2);
+  w->pairs = std::max(1, std::min(num_sms / 2, kChunkMaxPairs));
   const size_t rows = (size_t)w->pairs * 2 * kChunkTileTokens;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   w->part_o = kWsHeaderBytes;
   w->part_lse = w->part_o + rows * kPartialOBytes;
   w->parts = w->part_lse + up(rows * kPartialLseBytes);
-  w->total = w->parts + up((size_t)w->pairs * sizeof(int4));
+  w->total = w->parts + up((size_t)(w->pairs + 1) * sizeof(int4));
 }
 constexpr int kMaxChunkTokens = MFA_MAX_CHUNK_TOKENS;
 

@@ -88,7 +88,7 @@ struct PrefixParams {
 // sequence against what they see. Units of a tile: its pages by two, and what goes by between two tiles, for which quantised
 // caches split Q: with 1, 2, 3, 4, 6 of them steps that mix long and short tiles took 40.3, 39.9, 39.1, 42.4, 47.2 us on a bf16
 // cache, and 1303, 1087, 935, 840, 870 us on a 4-bit one.
-constexpr int kChunkTileTokens = 4;
+constexpr int kChunkTileTokens = 4, kChunkMaxPairs = 95;
 constexpr int kChunkPieceUnits = 3, kChunkPieceUnitsQuantised = 4;
 struct ChunkParams {
   const uint16_t* q;         // [max_tokens][64][256] bf16 bits
@@ -102,7 +102,9 @@ struct ChunkParams {
   // the one that ends behind it
   float* part_o;
   float* part_lse;
-  int4* parts;               // [pairs]: tiles that lie in several ranges: first row, tokens (0 behind the last), first pair, parts
+  // [pairs + 1]: tiles that lie in several ranges: first row, tokens | parts << 8 (0 behind the last), first pair, first of the
+  // combine's groups
+  int4* parts;
   uint16_t* out;             // [max_tokens][64][256] bf16 bits
   float* lse;                // [max_tokens][64]
   uint32_t* err;
