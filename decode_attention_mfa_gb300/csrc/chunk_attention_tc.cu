@@ -66,8 +66,8 @@
 // tiles of 2.5 units that 512-token prompts have (16 of them 163 us: a chain of Q
 // and K from L2, 2 us each under load, the softmax of two units and the output),
 // on quantised caches 3 us (Q waits for the last S, and its split takes 1.7). 23
-// tokens behind 900 take 17 us: plan 1.2, page ids and first loads 1.5, a unit 3,
-// 128 KB of fp32 partial results a CTA 2.7, combine 4, two launches.
+// tokens behind 900 take 15 us: plan 1.2, first tile, page ids and loads 1.9, a unit
+// 2.9, 128 KB of fp32 partial results a CTA 2.8, combine 2.5, two launches.
 #include <cuda_fp4.h>
 #include <type_traits>
 
@@ -467,8 +467,7 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
     return true;
   };
   uint32_t cnt = 0;  // units whose K has been loaded
-  // Q of a piece, the rows of this CTA's two tokens: by block, as the
-  // piece before is done with each (quantised: with all of them)
+  // Q of a piece, the rows of this CTA's two tokens: by block, as the piece before is done with each (quantised: with all)
   auto load_q = [&](const Piece& q) -> bool {
     if (kQ8 && pieces > 0 && !cx.wait_warp(SFull + ((cnt - 1) & 1), ((cnt - 1) >> 1) & 1)) return false;
     if (kQ8 && lane == 0) mbar_arrive_expect_tx(cx.bar(QFull), kQBytes);

@@ -41,7 +41,7 @@ template <int kFmt, int kRows>
 __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p) {
   __shared__ int s_start[kMaxBatch + 1];
   const int lane = threadIdx.x & 31;
-  const int r0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kRows;
+  const long long r0 = ((long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * kRows;
   pdl_launch_dependents();
   pdl_wait_prior_grid();
   for (int b = threadIdx.x; b <= p.B; b += kThreads) s_start[b] = __ldcg(p.row_starts + b);
@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(kThreads) kv_read_kernel(const KvReadParams p)
   // lane j looks row r0 + j up: its slot, or -1
   long long slot = -1;
   if (lane < kRows && r0 + lane < p.max_rows && r0 + lane >= s_start[0] && r0 + lane < s_start[p.B]) {
-    const int r = r0 + lane;
+    const int r = (int)(r0 + lane);
     int lo = 0, hi = p.B - 1;  // the last sequence that begins at or before r: those behind it with no rows begin later
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
