@@ -1344,10 +1344,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
 
 // ---------------------------------------------------------------- combine
 // Joins the parts of the tiles that lie in several ranges. With O_s and lse_s of part s, M = max_s lse_s and
-// w_s = exp(lse_s - M):  out = sum_s w_s O_s / sum_s w_s,  lse = M + ln sum_s w_s.  A warp takes half a row, eight parts at a time,
-// with a running M, or, of tiles with up to four and two parts, one or two rows: eight loads of 16 bytes in flight a lane. The first part is the second partial result of its pair (a tile that begins there), the others are the first ones of the
-// pairs behind it. Bound by latency: the list of tiles, then the parts, of groups on one line that the blocks share. Three blocks an SM are there at once; with more a call without parts took 1 us longer, and with four parts of a
-// row at a time 23 tokens behind 900 took 1.7 us longer.
+// w_s = exp(lse_s - M):  out = sum_s w_s O_s / sum_s w_s,  lse = M + ln sum_s w_s.  A warp takes half a row, eight parts at a
+// time, with a running M, or, of tiles with up to four and two parts, one or two rows: eight loads of 16 bytes in flight a
+// lane. The first part is the second partial result of its pair (a tile that begins there), the others are the first ones of
+// the pairs behind it. Bound by latency: the list of tiles, then the parts, of groups on one line that the blocks share. Three
+// blocks an SM are there at once; with more a call without parts took 1 us longer, and with four parts of a row at a time 23
+// tokens behind 900 took 1.7 us longer.
 constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32, kCombineBlocksPerPair = 6;
 static_assert(kCombineWarps == 8, "combine_groups");
 // kRows rows from r on of a tile whose first row is `first` and whose first part is pair `pair`'s; kHalves halves of them from
