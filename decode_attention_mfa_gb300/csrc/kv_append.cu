@@ -11,6 +11,7 @@
 // pages do not fix the granularity. 4-bit storage: same page, section 5.2 (KV
 // kept in 4 bits, attention computed in 8 bits), as OCP MX FP4 (E2M1) codes
 // with one fp32 scale per token (absmax / 6), two codes per byte.
+#include <algorithm>
 #include <cuda_fp4.h>
 #include <cuda_fp8.h>
 
@@ -223,7 +224,11 @@ __device__ __forceinline__ void quantise_row_slots(const uint4 (&raw)[32 / kLane
 #pragma unroll
     for (int o = kLanes / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
   }
-  const float s = (amax > 0.0f) ? __fdiv_rn(amax, kFp4 ? 6.0f : 448.0f) : 1.0f;
+  // absmax over 6 or 448 in the same way, 1 / 6 and 1 / 448 being known (bf16's 128 mantissas are in that test too)
+  constexpr float kMost = kFp4 ? 6.0f : 448.0f, kInverse = 1.0f / kMost;
+  const float q0 = amax * kInverse;
+  float s = fmaf(fmaf(-kMost, q0, amax), kInverse, q0);
+  if (!(amax >= 0x1p-100f && amax <= 0x1p100f)) s = (amax > 0.0f) ? __fdiv_rn(amax, kMost) : 1.0f;
   auto convert = [](float2 q) -> uint32_t {
     if constexpr (kFp4) return __nv_cvt_float2_to_fp4x2(q, __NV_E2M1, cudaRoundNearest);
     else return __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
@@ -259,8 +264,8 @@ __device__ __forceinline__ void quantise_row_slots(const uint4 (&raw)[32 / kLane
 // Rows scattered to the slots of a slot map. No row depends on another, so the
 // call is bound by latency for a decode step's rows and by memory bandwidth for a
 // prefill's (read 1 KB, write 1 KB, 520 or 264 B a token): 128 rows 1.2 us, 16384
-// rows 3.7 us (9 TB/s, L2 among it), 65536 rows to E4M3 18.2 us (5.6
-// TB/s), to E2M1 18.1 us (4.7 TB/s).
+// rows 3.7 us (9 TB/s, L2 among it), 65536 rows to E4M3 17.5 us (5.8
+// TB/s), to E2M1 16.0 us (5.3 TB/s).
 constexpr int kSlotThreads = 256;
 // bf16: a warp a row of K or of V, kRows such items a warp, all of whose loads are in flight before the first store.
 template <int kRows>
@@ -293,8 +298,10 @@ __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_kernel(const App
     reinterpret_cast<uint4*>(dst)[lane] = row[j];
   }
 }
+template <bool kFp4>
+__device__ __forceinline__ constexpr int code_row_bytes() { return kFp4 ? kHeadDim / 2 : kHeadDim; }
 // Quantised: kLanes lanes a row of K or of V. With half a warp, what there is to do for a row (its maximum, its scale and the
-// scale's reciprocal) takes half the instructions.
+// scale's reciprocal) takes half the instructions; the halves of a warp then take K and V of one row.
 template <bool kFp4, int kLanes>
 __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_quantised_kernel(const AppendSlotsParams p) {
   const int l = threadIdx.x & (kLanes - 1);
@@ -315,8 +322,49 @@ __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_quantised_kernel
     slot = -1;
   }
   if (slot < 0) return;  // a padded row, of the warp's K and V alike
-  quantise_row_slots<kFp4, kLanes>(row, static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot * (kFp4 ? kHeadDim / 2 : kHeadDim),
+  quantise_row_slots<kFp4, kLanes>(row, static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) + slot * code_row_bytes<kFp4>(),
                                    (is_v ? p.v_scale : p.k_scale) + slot, l);
+}
+// The same with half a warp a row for very many rows: the blocks that are there at once go through all of them, each warp with
+// its next row's loads in flight while it works on one. With a block for every 8 rows the memory waits for that work (65536
+// rows to E2M1 17.7 us instead of 16.0). Five blocks an SM: with three, four and six E2M1 took 19.9, 16.5 and 18.9 us.
+constexpr int kStreamBlocksPerSm = 5, kStreamBlocks = 152 * kStreamBlocksPerSm, kStreamRows = kSlotThreads / 32;
+template <bool kFp4>
+__global__ void __launch_bounds__(kSlotThreads, kStreamBlocksPerSm) kv_append_slots_stream_kernel(const AppendSlotsParams p) {
+  constexpr int kLanes = 16;
+  const int l = threadIdx.x & (kLanes - 1);
+  const bool is_v = threadIdx.x & kLanes;
+  const uint32_t rows = p.n_rows, step = gridDim.x * kStreamRows;
+  uint32_t r = blockIdx.x * kStreamRows + threadIdx.x / 32;
+  uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
+  float* scales = is_v ? p.v_scale : p.k_scale;
+  const long long end = (long long)p.num_pages * kPageSize, stride = (is_v ? p.v_stride : p.k_stride) / 8;  // in uint4
+  const uint4* src = reinterpret_cast<const uint4*>(is_v ? p.v_new : p.k_new) + r * stride + l;
+  const long long* at = reinterpret_cast<const long long*>(p.slot_map) + r;
+  pdl_launch_dependents();
+  pdl_wait_prior_grid();
+  if (r >= rows) return;
+  uint4 next[2] = {__ldcg(src), __ldcg(src + kLanes)};
+  long long next_slot = __ldcg(at);
+#pragma unroll 1
+  for (bool more = true; more;) {  // (of the warp)
+    const uint4 row[2] = {next[0], next[1]};
+    const long long slot = next_slot;
+    more = rows - r > step;
+    if (more) {
+      r += step;
+      src += step * stride;
+      at += step;
+      next[0] = __ldcg(src);
+      next[1] = __ldcg(src + kLanes);
+      next_slot = __ldcg(at);
+    }
+    if (slot >= end) {
+      if (l == 0) raise_error(p.err, MFA_DEVERR_PAGE);
+    } else if (slot >= 0) {  // else a padded row
+      quantise_row_slots<kFp4, kLanes>(row, cache + slot * code_row_bytes<kFp4>(), scales + slot, l);
+    }
+  }
 }
 
 unsigned slot_blocks(long long warps) { return (unsigned)((warps + kSlotThreads / 32 - 1) / (kSlotThreads / 32)); }
@@ -325,23 +373,28 @@ cudaError_t launch_slots(const AppendSlotsParams& p, cudaStream_t stream) {
   const unsigned blocks = slot_blocks((2ll * p.n_rows + kRows - 1) / kRows);
   return launch_pdl(kv_append_slots_kernel<kRows>, dim3(blocks), dim3(kSlotThreads), 0, stream, p);
 }
-template <bool kFp4, int kLanes>
+template <bool kFp4>
 cudaError_t launch_slots_quantised(const AppendSlotsParams& p, cudaStream_t stream) {
-  const unsigned blocks = slot_blocks((2ll * p.n_rows * kLanes + 31) / 32);
-  return launch_pdl(kv_append_slots_quantised_kernel<kFp4, kLanes>, dim3(blocks), dim3(kSlotThreads), 0, stream, p);
+  // a warp a row, half a warp, and with the loop, E4M3: 128 rows 1.55, 1.75 and 1.6 us, 4096 rows 2.7, 2.6 and 2.6, 8192 rows
+  // 3.9, 3.1 and 3.4, 65536 rows 20.5, 18.0 and 17.6
+  constexpr int kManyRows = 2048, kVeryManyRows = 16384;
+  if (p.n_rows < kManyRows)
+    return launch_pdl(kv_append_slots_quantised_kernel<kFp4, 32>, dim3(slot_blocks(2ll * p.n_rows)), dim3(kSlotThreads), 0, stream, p);
+  if (p.n_rows < kVeryManyRows)
+    return launch_pdl(kv_append_slots_quantised_kernel<kFp4, 16>, dim3(slot_blocks(p.n_rows)), dim3(kSlotThreads), 0, stream, p);
+  const unsigned blocks = std::min((unsigned)kStreamBlocks, (unsigned)(((long long)p.n_rows + kStreamRows - 1) / kStreamRows));
+  return launch_pdl(kv_append_slots_stream_kernel<kFp4>, dim3(blocks), dim3(kSlotThreads), 0, stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_kv_append_slots(const AppendSlotsParams& p, cudaStream_t stream) {
-  // bf16: two items a warp halve the blocks that many rows take to launch, one is the shorter wait for few rows: 16384 rows 4.6
-  // us with one and 3.5 with two; 4096 rows 1.8 and 2.1. Quantised, E4M3: 65536 rows 20.5 us with a warp a row and 18.2 with half
-  // a warp, 8192 rows 3.9 and 3.1, 128 rows 1.55 and 1.75; a warp for four rows or eight 18.4 and 20.0.
-  constexpr int kManyRows = 8192, kManyQuantised = 2048;
-  if (p.fmt == kKvBf16) return p.n_rows >= kManyRows ? launch_slots<2>(p, stream) : launch_slots<1>(p, stream);
-  const bool many = p.n_rows >= kManyQuantised;
-  if (p.fmt == kKvE4M3) return many ? launch_slots_quantised<false, 16>(p, stream) : launch_slots_quantised<false, 32>(p, stream);
-  return many ? launch_slots_quantised<true, 16>(p, stream) : launch_slots_quantised<true, 32>(p, stream);
+  if (p.fmt == kKvE4M3) return launch_slots_quantised<false>(p, stream);
+  if (p.fmt == kKvE2M1) return launch_slots_quantised<true>(p, stream);
+  // Two items a warp halve the blocks that many rows take to launch, one is the shorter wait for few rows: 16384 rows 4.6
+  // us with one and 3.5 with two; 4096 rows 1.8 and 2.1.
+  constexpr int kManyRows = 8192;
+  return p.n_rows >= kManyRows ? launch_slots<2>(p, stream) : launch_slots<1>(p, stream);
 }
 
 cudaError_t launch_kv_append(const AppendParams& p, cudaStream_t stream) {

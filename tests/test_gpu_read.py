@@ -101,6 +101,42 @@ def test_append_slots_fp4_bad_slot():
     assert (kc.view(-1, DIM // 2)[1:] == 5).all() and (vc.view(-1, DIM // 2)[1:] == 5).all()
 
 
+@pytest.mark.parametrize("n", [2047, 2048, 6081, 16383, 16384, 18239, 18241, 30000])  # all ways, with whole and ragged loops
+@pytest.mark.parametrize("kv", ["fp8", "fp4"])
+def test_append_slots_many_rows(kv, n):
+    """Codes and scales of rows of every kind, in a shuffled pool and beside skipped and bad slots, are those of the other append."""
+    rows = torch.randn((n, DIM), generator=torch.Generator().manual_seed(n)).bfloat16()
+    odd = special_rows()[:15]
+    rows[: 15 * 130: 130], rows[-15:] = odd, odd
+    both = torch.stack([rows, rows.flip(0)], 1).cuda()
+    k, v = both[:, 0], both[:, 1]
+    pages, width = -(-n // PAGE) + 2, DIM if kv == "fp8" else DIM // 2
+    rng = np.random.default_rng(n)
+    slots = rng.permutation(pages * PAGE)[:n]
+    given = np.where(rng.random(n) < 0.1, -1, slots)
+    given[n - 7] = pages * PAGE  # one that the pool does not have
+    pools = lambda: ([torch.full((pages, PAGE, width), 0x55, dtype=torch.uint8, device="cuda") for _ in range(2)]  # noqa: E731
+                     + [torch.full((pages, PAGE), -3.0, device="cuda") for _ in range(2)])
+    got, want = pools(), pools()
+    ws = workspace()
+    call = capi.mfa_kv_append_slots_fp8 if kv == "fp8" else capi.mfa_kv_append_slots_fp4
+    call(k, v, k.stride(0), v.stride(0), torch.from_numpy(given).cuda(), n, *got, pages, ws)
+    with pytest.raises(capi.MFAError) as e:
+        capi.mfa_check_device_errors(ws)
+    assert e.value.status == 5
+    lens, table = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.arange(pages, dtype=torch.int32, device="cuda")
+    other = capi.mfa_kv_append_fp8 if kv == "fp8" else capi.mfa_kv_append_fp4
+    other(k.contiguous(), v.contiguous(), n, *want, table, lens, 1, pages, pages, ws)
+    written = (given >= 0) & (given < pages * PAGE)
+    at, kept = torch.from_numpy(slots[written]).cuda(), torch.from_numpy(written).cuda()
+    rest = torch.ones(pages * PAGE, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    for a, b in zip(got, want):
+        a, b = a.reshape(pages * PAGE, -1), b.reshape(pages * PAGE, -1)
+        assert torch.equal(a[at].view(torch.uint8), b[:n][kept].view(torch.uint8))
+        assert (a[rest] == (0x55 if a.dtype == torch.uint8 else -3.0)).all()
+
+
 # ---------------------------------------------------------------- read back
 def read_plain(s, first, starts, i):
     """(values in 64 bits, flat slots) of the rows of cache i."""

@@ -1,6 +1,6 @@
 """Quotients of the slot appends' quantisers, by whole-number arithmetic: with y the rounded reciprocal of s and q = x y rounded,
 q - (q s - x) y is the rounded quotient x / s for every scale that the append forms (s = absmax / 6 or / 448, rounded) and every
-bf16 x up to absmax, so that one correction is enough there; for any s two are needed."""
+bf16 x up to absmax, so that one correction is enough there; for any s two are needed. The same for these scales themselves."""
 import pytest
 
 
@@ -50,3 +50,13 @@ def test_one_correction_gives_the_rounded_quotient(most, steps):
                 want = rn(x << 60, s[0])
                 want = (want[0], want[1] - 60 - s[1] - j)
                 assert q == want, (a, x, j)
+
+
+@pytest.mark.parametrize("most", [6, 448])
+def test_one_correction_gives_the_scale(most):
+    """absmax / 6 and / 448 from their rounded reciprocals, for every bf16 mantissa."""
+    y = rn(1, most)
+    for a in range(128, 256):
+        q = fma((a, 0), y, (0, 0))
+        left = fma((-most, 0), q, (a, 0))
+        assert fma(left, y, q) == rn(a, most), a
