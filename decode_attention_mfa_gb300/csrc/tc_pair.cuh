@@ -285,13 +285,15 @@ __device__ __forceinline__ bool barrier_rows_or(int quad, bool pred) {
 // on an 8-bit cache take 0.4 us more.
 __device__ __forceinline__ void split_q8(const uint4 v, float up, uint32_t (&t1)[2], uint32_t (&t2)[2]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  const __nv_bfloat162 up_2 = __float2bfloat162_rn(up);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t a = 0, b = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const __half2 x =
-          __floats2half2_rn(__uint_as_float(w[2 * i + k] << 16) * up, __uint_as_float(w[2 * i + k] & 0xFFFF0000u) * up);
+      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * i + k]), up_2);  // exact
+      const uint32_t bits = *reinterpret_cast<const uint32_t*>(&y);
+      const __half2 x = __floats2half2_rn(__uint_as_float(bits << 16), __uint_as_float(bits & 0xFFFF0000u));
       const __nv_fp8x2_storage_t c1 =
           __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3);
       const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3);
