@@ -515,8 +515,11 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
     for (int u = q.u0; good && u < q.u1; ++u) {
       const int pa = ids.get(2 * u, p, q, lane);
       const int pb = 2 * u + 1 < q.pages() ? ids.get(2 * u + 1, p, q, lane) : -1;
-      good = load_k(cnt, pa, pb);
-      if (good && va >= 0) good = load_v(cnt - 1, va, vb, vtail);
+      // quantised: V's codes of two units earlier are converted before the MMAs are done with K of that unit, bf16: it is the other
+      // way round
+      if (kQ8 && va >= 0) good = load_v(cnt - 1, va, vb, vtail);
+      good = good && load_k(cnt, pa, pb);
+      if (!kQ8 && good && va >= 0) good = load_v(cnt - 1, va, vb, vtail);
       if (good && u == q.u0 && (!kQ8 || cnt > 0)) good = load_q(q);
       ++cnt;
       va = pa;
