@@ -1033,6 +1033,12 @@ __device__ __forceinline__ float split_queries(uint32_t q_addr, float* red, int 
   return top < 0x7F800000u ? exp2_int(-e) : __uint_as_float(0x7FFFFFFFu);
 }
 
+// The next move of a row's reference comes when the sum of a thread's 64 weights of a unit passes this, and in units that the
+// careful way below takes for another reason, when a weight passes the 64th part. A move takes a unit 2000 cycles longer. f16:
+// as in the shared-prefix kernel; bf16 has room for more, but O is weights times V, and V up to 2^97 is to fit.
+template <bool kQ8>
+__host__ __device__ constexpr int most_sum_log2() { return kQ8 ? 15 : 30; }
+
 // The weights of one unit, S in tensor memory replaced by P. tx: this thread's 64 products, of which `cols` count (the two
 // warps of the rows together at least one; `whole`: all 128); o_addr: O's first column in its lane; sc: the K scales of its
 // keys, 128 before their V scales (quantised); may: some V scale among the warp's may have a shift; wait_pv: O holds every
@@ -1080,7 +1086,7 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
     return both;
   };
   uint32_t w[32];
-  bool done = false;
+  bool done = false, over = false;
   if (whole && !st.open) {
     const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-st.m, -st.m);
     clear();
@@ -1092,7 +1098,8 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
       for (int c = 0; c < 16; ++c) w[g / 2 + c] = weigh(fma2(x[c], mul_2, ref_2), c);
     }
     const float2 all = add2(sum[0], sum[1]);
-    done = !barrier_rows_or(quad, all.x + all.y > kMostSum || may);
+    done = !barrier_rows_or(quad, all.x + all.y > exp2_int(most_sum_log2<kQ8>()) || may);
+    over = !done;
   }
   if (!done) {
     float2 y[32];
@@ -1124,8 +1131,8 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
       return;
     }
     const float most = fmaxf(big, mine[(half ^ 1) * 128 + row]);
-    // 64 weights up to 2^9 add up to kMostSum
-    const float m_new = st.open || most > st.m + (9.0f - moved_to<kQ8>()) ? fmaxf(st.m, most) : st.m;
+    // where one row moves, all do
+    const float m_new = st.open || over || most > st.m + (most_sum_log2<kQ8>() - 6 - moved_to<kQ8>()) ? fmaxf(st.m, most) : st.m;
     const float alpha = st.fresh || st.m == m_new ? 1.0f : ex2_approx(st.m - m_new);
     st.m = m_new;
     st.open = __any_sync(0xffffffffu, st.m == -INFINITY);  // the same in both warps of the rows
