@@ -1033,9 +1033,12 @@ __device__ __forceinline__ float split_queries(uint32_t q_addr, float* red, int 
   return top < 0x7F800000u ? exp2_int(-e) : __uint_as_float(0x7FFFFFFFu);
 }
 
-// The next move of a row's reference comes when the sum of a thread's 64 weights of a unit passes this, and in units that the
-// careful way below takes for another reason, when a weight passes the 64th part. A move takes a unit 2000 cycles longer. f16:
-// as in the shared-prefix kernel; bf16 has room for more, but O is weights times V, and V up to 2^97 is to fit.
+// A row's reference is its largest logit when it is set, so that its weights then are at most 1. It moves when the sum of a
+// thread's 64 weights of a unit passes this, and in units that the careful way below takes for another reason, when a weight
+// passes the 64th part. A move takes a unit 2000 cycles longer. bf16 has room for more, but O is weights times V, and V up to
+// 2^97 is to fit. f16 ends at 2^16, and below 2^-14 its step stays 2^-24: N such weights, beside a sum of 1 at least, are off
+// by N 2^-25 together if all round the same way (65536: half a bf16 step of the output). With references lower by 4, as the
+// shared-prefix kernel has them, 304 tokens behind 16080 with logits of twice the spread took 207 us instead of 191.
 template <bool kQ8>
 __host__ __device__ constexpr int most_sum_log2() { return kQ8 ? 15 : 30; }
 
@@ -1113,7 +1116,7 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
       if (2 * c + 1 >= cols) y[c].y = -INFINITY;
       top = fmaxf(top, fmaxf(y[c].x, y[c].y));
     }
-    const float big = top - moved_to<kQ8>();
+    const float big = top;
     float* mine = red + (turn ? 256 : 0);  // two turns: who is two exchanges ahead has seen the other read
     turn = !turn;
     mine[half * 128 + row] = big;
@@ -1132,7 +1135,7 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
     }
     const float most = fmaxf(big, mine[(half ^ 1) * 128 + row]);
     // where one row moves, all do
-    const float m_new = st.open || over || most > st.m + (most_sum_log2<kQ8>() - 6 - moved_to<kQ8>()) ? fmaxf(st.m, most) : st.m;
+    const float m_new = st.open || over || most > st.m + (most_sum_log2<kQ8>() - 6) ? fmaxf(st.m, most) : st.m;
     const float alpha = st.fresh || st.m == m_new ? 1.0f : ex2_approx(st.m - m_new);
     st.m = m_new;
     st.open = __any_sync(0xffffffffu, st.m == -INFINITY);  // the same in both warps of the rows

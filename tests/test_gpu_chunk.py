@@ -229,6 +229,54 @@ def test_rising_and_falling_logits(kv):
         s.run()
 
 
+def _with_logits(s, b, logits, values_of=None):
+    """Keys of sequence b that give every head the logits (to what the cache holds of them); values_of: their value rows."""
+    s.q[:] = 0.0
+    s.q[..., 0] = 16.0
+    for i, x in enumerate((logits, values_of)):
+        if x is None:
+            continue
+        rows = torch.zeros((len(x), DIM), device="cuda")
+        rows[:, 0 if i == 0 else slice(None)] = x if i == 0 else x.unsqueeze(1)
+        at = torch.tensor([s.row(b, j) for j in range(len(x))], device="cuda")
+        if s.kv == "bf16":
+            s.cache[i].view(-1, DIM)[at] = rows.bfloat16()
+        else:
+            code, scale = to_codes(rows, s.kv)
+            s.cache[i].view(-1, code.shape[1])[at] = torch.where((scale > 0).unsqueeze(1), code, torch.zeros_like(code))
+            s.scales[i].view(-1)[at] = torch.where(scale > 0, scale, torch.ones_like(scale))
+
+
+@KV
+@pytest.mark.parametrize("step", [-30.0, -3.0, 2.0, 5.0, 9.0, 11.0, 16.0, 18.0, 25.0, 60.0])
+def test_logits_by_steps(step, kv):
+    """Every 128 positions the logits rise or fall by `step`: references move within all ranges that weights have, or not at all."""
+    s = Step([9], [1000], kv, seed=21)
+    n = int(s.lens[0])
+    noise = torch.randn(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    _with_logits(s, 0, noise + step * (torch.arange(n, device="cuda") // 128))
+    s.run()
+
+
+@KV
+@pytest.mark.parametrize("below", [9.0, 13.5, 15.45, 16.2])
+def test_one_key_and_many_equal_ones_far_below(below, kv):
+    """One key of weight 1 and 40000 of weight 2^-below, all rounded the same way."""
+    s = Step([1], [40000], kv, seed=22)
+    n = int(s.lens[0])
+    logits = torch.full((n,), -below * np.log(2.0), device="cuda")
+    logits[100] = 0.0
+    v = torch.ones(n, device="cuda")
+    v[100] = -1.0
+    _with_logits(s, 0, logits, v)
+    s.run()
+    out, _, _, _ = s.reference(0)
+    # the output's half step; weights, and values on a quantised cache, by half a step each (bf16 2^-8, f16 2^-11) of a mean of
+    # values of 1, below 2^-14 by 2^-25 each instead; a sum of 1 at least
+    half = 2 ** -8 if kv == "bf16" else 2 ** -11
+    assert float((s.out[int(s.starts[0])].double() - out[0]).abs().max()) <= 2 ** -8 * float(out.abs().max()) + 2 * half + 2 * n * 2 ** -25
+
+
 @pytest.mark.parametrize("kv", ["fp8", "fp4"])
 def test_value_scales_far_apart(kv):
     """V scales from 2^-40 to 2^20 beside each other: large values without weight, small ones with all of it."""
