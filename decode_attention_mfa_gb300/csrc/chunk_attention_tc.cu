@@ -1108,13 +1108,21 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
     float2 y[32];
     load(0, *reinterpret_cast<float2 (*)[16]>(y));
     load(32, *reinterpret_cast<float2 (*)[16]>(y + 16));
-    float top = -INFINITY;
+    // all 64 count: the largest product, which times a positive factor stays the largest; else each by itself
+    float top = -INFINITY, factor = 1.0f;
+    if (cols == kPageSize && mul > 0.0f) {
 #pragma unroll
-    for (int c = 0; c < 32; ++c) {
-      y[c] = mul2(y[c], make_float2(mul, mul));
-      if (2 * c >= cols) y[c].x = -INFINITY;
-      if (2 * c + 1 >= cols) y[c].y = -INFINITY;
-      top = fmaxf(top, fmaxf(y[c].x, y[c].y));
+      for (int c = 0; c < 32; ++c) top = fmaxf(top, fmaxf(y[c].x, y[c].y));
+      top *= mul;
+      factor = mul;
+    } else {
+#pragma unroll
+      for (int c = 0; c < 32; ++c) {
+        y[c] = mul2(y[c], make_float2(mul, mul));
+        if (2 * c >= cols) y[c].x = -INFINITY;
+        if (2 * c + 1 >= cols) y[c].y = -INFINITY;
+        top = fmaxf(top, fmaxf(y[c].x, y[c].y));
+      }
     }
     const float big = top;
     float* mine = red + (turn ? 256 : 0);  // two turns: who is two exchanges ahead has seen the other read
@@ -1144,7 +1152,7 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
     const float ref = st.m == -INFINITY ? 0.0f : st.m;  // only infinite logits so far: weights of 0
     clear();
 #pragma unroll
-    for (int c = 0; c < 32; ++c) w[c] = weigh(add2(y[c], make_float2(-ref, -ref)), c);
+    for (int c = 0; c < 32; ++c) w[c] = weigh(fma2(y[c], make_float2(factor, factor), make_float2(-ref, -ref)), c);
     if (!st.fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
       // O holds the units before this one; each of the two warps scales half of its columns
       wait_pv();
