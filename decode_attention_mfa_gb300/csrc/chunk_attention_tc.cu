@@ -69,6 +69,7 @@
 // tokens behind 900 take 15 us: plan 1.2, first tile, page ids and loads 1.9, a unit
 // 2.9, 128 KB of fp32 partial results a CTA 2.8, combine 2.5, two launches.
 #include <cuda_fp4.h>
+#include <algorithm>
 #include <type_traits>
 
 #include "mfa_serving.hpp"
@@ -129,11 +130,15 @@ enum Bar {
 
 // The line of work as every CTA sees it.
 constexpr int kPlanChunks = kMaxBatch / 32 + 1;
+struct LineRange {
+  int from, to;
+};
 struct PlanSmem {
   int32_t cost[kMaxBatch + 1];  // units of the sequences before b; [B]: of all
   int32_t row[kMaxBatch + 1];   // first row of sequence b's tokens, non-decreasing within [0, max_tokens]
   int32_t len[kMaxBatch];       // positions that its pages hold
   int32_t last[kPlanChunks + 1], total[kPlanChunks + 1];  // of 32 sequences
+  LineRange rest;                                         // what the pair does last, if it is not empty
 };
 
 template <int kFmt>
@@ -277,7 +282,11 @@ __device__ void build_plan(const ChunkParams& p, PlanSmem& s, uint32_t* err) {
 // Pairs that have work: with fewer units than pairs, every range holds one.
 __device__ __forceinline__ int busy_pairs(const ChunkParams& p, int units) { return min(p.pairs, max(units, 1)); }
 
-// A pair's pieces, in order: units [u0, u1) of one row tile.
+// A pair's pieces, in order: units [u0, u1) of one row tile. The rest of a tile that begins before the pair's range comes first,
+// or, where the pages are more than L2 holds, last (kTurn): then all pairs begin with tiles' beginnings and go through a
+// sequence's pages at about the same time, and HBM delivers them once for all of these. bf16, for seconds: 1024 tokens each
+// behind 100000 and 90000 1600 -> 1870 TFLOP/s, 2048 behind 129024 1660 -> 1890, 8 chunks of 512 behind 32000 1720 -> 2050 in a
+// burst; 2048 behind 63488, whose pages L2 holds, 1885 and 1890.
 struct Piece {
   int b = -1, i;     // sequence, tile of it
   int a, n, row0;    // of the sequence: positions before its chunk, tokens that see any, the first one's row
@@ -286,15 +295,25 @@ struct Piece {
   int units;         // of the whole tile
   int u0, u1;
   int first, x;      // line positions: the tile's, and the one behind it
+  bool last = false; // it is of what comes last
   __device__ int pages() const { return (seen + kPageSize - 1) / kPageSize; }
   __device__ int keys(int page) const { return min(max(seen - page * kPageSize, 0), kPageSize); }
   // Whether V of unit u holds rows that not all tokens see, up to the end of an MMA's 16 keys.
   __device__ bool ends(int u) const { return (u + 1) * kUnitKeys > seen0 && (tokens > 1 || (seen % kKeyStep) != 0); }
   __device__ bool whole() const { return u0 == 0 && u1 == units; }
 };
-__device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem& s, int lo, int hi, Piece& q) {
-  if (q.b < 0) q.x = lo;
-  while (q.x < hi) {
+template <bool kTurn>
+__device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem& s, LineRange range, Piece& q) {
+  if (q.b < 0) q.x = range.from;
+  for (;;) {
+    if (kTurn && q.last) range = s.rest;
+    if (q.x >= range.to) {
+      if (!kTurn || q.last || s.rest.from >= s.rest.to) return false;
+      q.last = true;
+      q.x = s.rest.from;
+      q.b = -1;
+      range = s.rest;
+    }
     if (q.b < 0 || q.x >= s.cost[q.b + 1]) {
       const int b = last_at_most(s.cost, p.B, q.x);
       q.b = b;
@@ -320,11 +339,20 @@ __device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem&
     q.seen = q.seen0 + q.tokens - 1;
     q.units = units_of(q.seen);
     q.u0 = max(0, q.x - q.first - p.piece_units);
-    q.u1 = min(q.units, hi - q.first - p.piece_units);
+    q.u1 = min(q.units, range.to - q.first - p.piece_units);
     q.x = q.first + p.piece_units + q.units;
     if (q.u0 < q.u1) return true;
   }
-  return false;
+}
+
+// Where a pair's range begins: at its first tile's beginning, if the rest of a tile before that is to come last.
+static __device__ __noinline__ int begin_of(const ChunkParams& p, const PlanSmem& s, int lo, int hi) {
+  Piece q;
+  if (!next_piece<false>(p, s, LineRange{lo, hi}, q) || q.u0 == 0 || q.x >= hi) return lo;
+  // units that the sequences hold together, if all are like this one, which is to have more than two tiles
+  const int cost = s.cost[q.b + 1] - s.cost[q.b];
+  const bool more = cost > 2 * (q.units + p.piece_units) && (float)q.units * (float)s.cost[p.B] > (float)p.l2_units * (float)cost;
+  return more ? q.x : lo;
 }
 
 // Groups of eight warps that the combine takes for a tile: of one and two parts a warp takes two rows, of up to four one, of more
@@ -344,7 +372,7 @@ __device__ void publish_parts(const ChunkParams& p, const PlanSmem& s, int lane)
     if (w < W && units > 0) {
       const int lo = range_of_pair(w, units, W), hi = range_of_pair(w + 1, units, W);
       Piece q;
-      if (next_piece(p, s, hi - 1, hi, q) && q.u1 < q.units && lo <= q.first + p.piece_units) {
+      if (next_piece<false>(p, s, LineRange{hi - 1, hi}, q) && q.u1 < q.units && lo <= q.first + p.piece_units) {
         row = q.row;
         tokens = q.tokens;
         parts = pair_of_unit(q.first + p.piece_units + q.units - 1, units, W) - w + 1;
@@ -404,9 +432,9 @@ struct TilePages {
   }
 };
 
-template <int kFmt>
+template <int kFmt, bool kTurn>
 __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, const CUtensorMap* vmap,
-                              const CUtensorMap* qmap, const Ctx& cx, const PlanSmem& s, int lo, int hi) {
+                              const CUtensorMap* qmap, const Ctx& cx, const PlanSmem& s, LineRange range) {
   using Sm = Smem<kFmt>;
   constexpr bool kQ8 = kQuant<kFmt>;
   constexpr uint32_t kSlot = slot_bytes<kFmt>(), kPage = kSlot / 2, kTx = slot_tx<kFmt>();
@@ -490,7 +518,7 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
   int va = -1, vb = -1;  // the last unit: its V is still to be loaded (V trails K by a unit, as the MMAs use them)
   bool vtail = false, good = true;
   Piece q, next;
-  bool more = next_piece(p, s, lo, hi, next);
+  bool more = next_piece<kTurn>(p, s, range, next);
   int na = 0, nb = 0;
   auto ask = [&]() {  // what the next piece begins with
     const int end = TilePages::end_of(next);
@@ -505,7 +533,7 @@ __device__ void producer_role(const ChunkParams& p, const CUtensorMap* kmap, con
     q = next;
     TilePages ids;
     ids.start(na, nb, p, q);
-    more = next_piece(p, s, lo, hi, next);
+    more = next_piece<kTurn>(p, s, range, next);
     if (more) {
       ask();
       const int here = min(2, max(0, next.tokens - 2 * r));  // its Q, into L2
@@ -672,8 +700,8 @@ __device__ __forceinline__ void convert_unit(const Converter& at, uint32_t src, 
 }
 
 // ---------------------------------------------------------------- MMA issue (one thread of the leader)
-template <int kFmt>
-__device__ void mma_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int lo, int hi, uint32_t tmem) {
+template <int kFmt, bool kTurn>
+__device__ void mma_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, LineRange range, uint32_t tmem) {
   constexpr bool kQ8 = kQuant<kFmt>;
   // A = Q, B = K, both K-major (8-bit kinds: formats 0, E4M3, and 5, E2M1); A = P (TMEM), B = V (dim-major; format 0: f16)
   constexpr uint32_t idesc_s = idesc_f16(256, kSCols, kQ8 ? 0 : 1, 0, 0) | (kFmt == kKvE2M1 ? 5u << 10 : 0u);
@@ -773,7 +801,7 @@ __device__ void mma_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s,
   Piece q;
   Unit pend{};
   bool good = true;
-  while (good && next_piece(p, s, lo, hi, q)) {
+  while (good && next_piece<kTurn>(p, s, range, q)) {
     for (int u = q.u0; good && u < q.u1; ++u) {
       if (u == q.u0) {
         // quantised: Q is split behind the last softmax, which takes longer than the last P V
@@ -923,11 +951,12 @@ __device__ __forceinline__ void write_piece(const ChunkParams& p, const Ctx& cx,
 }
 
 // bf16: V at the end of every tile.
-__device__ void tail_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int lo, int hi) {
+template <bool kTurn>
+__device__ void tail_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, LineRange range) {
   const int lane = threadIdx.x & 31;
   uint32_t n = 0, tails[2] = {0, 0}, piece = 0;
   Piece q;
-  for (; next_piece(p, s, lo, hi, q); ++piece) {
+  for (; next_piece<kTurn>(p, s, range, q); ++piece) {
     for (int u = q.u0; u < q.u1; ++u, ++n) {
       if (!q.ends(u)) continue;
       const uint32_t slot = n & 1;
@@ -942,8 +971,8 @@ __device__ void tail_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s
 }
 
 // Quantised: V of every unit as P V needs it and, behind that of the next piece's first unit, the output of a piece.
-template <int kFmt>
-__device__ void value_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi, uint32_t tmem,
+template <int kFmt, bool kTurn>
+__device__ void value_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int pair, LineRange range, uint32_t tmem,
                            uint8_t* gbase) {
   using Sm = Smem<kFmt>;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = 32 * (warp & 3) + lane;
@@ -954,7 +983,7 @@ __device__ void value_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& 
   uint32_t n = 0, piece = 0;
   Piece q, last;
   for (bool more = true; more; ++piece) {
-    more = next_piece(p, s, lo, hi, q);
+    more = next_piece<kTurn>(p, s, range, q);
     int u = q.u0;
     do {
       if (more) {
@@ -1176,8 +1205,8 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
   st.fresh = false;
 }
 
-template <int kFmt>
-__device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int pair, int lo, int hi, uint32_t tmem,
+template <int kFmt, bool kTurn>
+__device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s, int pair, LineRange range, uint32_t tmem,
                              uint8_t* gbase) {
   constexpr bool kQ8 = kQuant<kFmt>;
   using Sm = Smem<kFmt>;
@@ -1200,7 +1229,7 @@ __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
   Piece q, last;
   RowState st, last_st;
   for (bool more = true; more; ++pieces) {
-    more = next_piece(p, s, lo, hi, q);
+    more = next_piece<kTurn>(p, s, range, q);
     if (kQ8 && !more) break;
     const int seen = more && j < q.tokens ? q.seen0 + j : 0;  // keys that this row sees
     st = RowState();
@@ -1271,7 +1300,7 @@ __device__ void softmax_role(const ChunkParams& p, const Ctx& cx, const PlanSmem
   }
 }
 
-template <int kFmt>
+template <int kFmt, bool kTurn>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
     chunk_attention_tc_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap kmap,
                               const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap qmap) {
@@ -1302,6 +1331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
                                                            : 1);
     }
     *abort_flag = 0;
+    plan.rest = {0, 0};
     for (int i = 0; i < 4; ++i) reinterpret_cast<uint32_t*>(gbase + Sm::odd)[i] = 0;
     fence_mbar_init();
   }
@@ -1333,21 +1363,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
   const uint32_t tmem = *tmem_slot;
   const int units = plan.cost[p.B], W = busy_pairs(p, units), pair = blockIdx.x >> 1;
   const int lo = pair < W ? range_of_pair(pair, units, W) : 0, hi = pair < W ? range_of_pair(pair + 1, units, W) : 0;
+  LineRange range{lo, hi};
+  if (kTurn && units > p.l2_units) {
+    if (lo < hi) range.from = begin_of(p, plan, lo, hi);
+    __syncthreads();
+    if (threadIdx.x == 0) plan.rest = {lo, range.from};
+    __syncthreads();
+  }
 
   if (warp < kSoftmaxWarps) {
-    softmax_role<kFmt>(p, cx, plan, pair, lo, hi, tmem, gbase);
+    softmax_role<kFmt, kTurn>(p, cx, plan, pair, range, tmem, gbase);
   } else if (warp == kProducerWarp) {
-    producer_role<kFmt>(p, &kmap, &vmap, &qmap, cx, plan, lo, hi);
+    producer_role<kFmt, kTurn>(p, &kmap, &vmap, &qmap, cx, plan, range);
   } else if (warp >= kValueWarp) {
     if constexpr (kQ8)
-      value_role<kFmt>(p, cx, plan, pair, lo, hi, tmem, gbase);
+      value_role<kFmt, kTurn>(p, cx, plan, pair, range, tmem, gbase);
     else
-      tail_role(p, cx, plan, lo, hi);
+      tail_role<kTurn>(p, cx, plan, range);
   } else if (cx.rank == 1) {  // (its MMAs are issued by the leader)
     if (pair == 0) publish_parts(p, plan, threadIdx.x & 31);
     write_unseeing(p, plan, pair, threadIdx.x & 31);
   } else if (elect_one()) {
-    mma_role<kFmt>(p, cx, plan, lo, hi, tmem);
+    mma_role<kFmt, kTurn>(p, cx, plan, range, tmem);
   }
   __syncwarp();
   if (*cx.abort) {
@@ -1485,14 +1522,22 @@ __global__ void __launch_bounds__(kCombineThreads, 3) chunk_combine_kernel(const
   }
 }
 
-template <int kFmt>
+template <int kFmt, bool kTurn>
 cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                          cudaStream_t stream) {
   const size_t smem = Smem<kFmt>::total + 1024;
   static int configured[kTrackedDevices] = {};
-  const cudaError_t e = ensure_dynamic_smem(chunk_attention_tc_kernel<kFmt>, smem, configured);
+  const cudaError_t e = ensure_dynamic_smem(chunk_attention_tc_kernel<kFmt, kTurn>, smem, configured);
   if (e != cudaSuccess) return e;
-  return launch_pdl(chunk_attention_tc_kernel<kFmt>, dim3(2 * p.pairs), dim3(threads<kFmt>()), smem, stream, p, kmap, vmap, qmap);
+  return launch_pdl(chunk_attention_tc_kernel<kFmt, kTurn>, dim3(2 * p.pairs), dim3(threads<kFmt>()), smem, stream, p, kmap, vmap, qmap);
+}
+template <int kFmt>
+cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
+                         cudaStream_t stream) {
+  // Pieces that may turn cost 1 to 2% of a short prompt's or few tiles' time (16 of 512 tokens 160.7 -> 164.0 us, 304 tokens
+  // behind 16080 168.3 -> 169.6), so where all pages fit L2 there is a kernel without.
+  const bool turn = 0.5 * std::min((long long)p.B * p.max_pages, (long long)p.num_pages) > p.l2_units;
+  return turn ? launch_chunk<kFmt, true>(p, kmap, vmap, qmap, stream) : launch_chunk<kFmt, false>(p, kmap, vmap, qmap, stream);
 }
 }  // namespace
 

@@ -571,6 +571,8 @@ mfa_status_t chunk_common(const void* q, const void* k_cache, const void* v_cach
   p.num_pages = num_pages;
   p.pairs = w.pairs;
   p.piece_units = fmt == kKvBf16 ? kChunkPieceUnits : kChunkPieceUnitsQuantised;
+  const int row_bytes = fmt == kKvBf16 ? 2 * kHeadDim : fmt == kKvE4M3 ? kHeadDim : kHeadDim / 2;
+  p.l2_units = (int)(kChunkL2Bytes / (4 * kPageSize * row_bytes));  // K and V of two pages
   p.fmt = fmt;
   p.wait_budget_ns = g_wait_budget_ns.load(std::memory_order_relaxed);
   const cudaStream_t s = static_cast<cudaStream_t>(stream);

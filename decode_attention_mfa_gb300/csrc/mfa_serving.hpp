@@ -90,6 +90,8 @@ struct PrefixParams {
 // cache, and 1303, 1087, 935, 840, 870 us on a 4-bit one.
 constexpr int kChunkTileTokens = 4, kChunkMaxPairs = 95;
 constexpr int kChunkPieceUnits = 3, kChunkPieceUnitsQuantised = 4;
+// What L2's 129 MB hold: lines that both dies read are in both halves.
+constexpr long long kChunkL2Bytes = 80ll << 20;
 struct ChunkParams {
   const uint16_t* q;         // [max_tokens][64][256] bf16 bits
   const void* v_cache;
@@ -111,6 +113,7 @@ struct ChunkParams {
   float scale;
   int B, max_tokens, max_pages, num_pages, pairs;
   int piece_units;           // of a tile besides its pages'
+  int l2_units;              // units whose K and V L2 holds
   int fmt;                   // kKvBf16, kKvE4M3 or kKvE2M1
   uint64_t wait_budget_ns;
 };

@@ -160,6 +160,16 @@ def test_long_context(new, held, kv):
 
 
 @KV
+def test_more_pages_than_l2_holds(kv):
+    """Sequences of many, few and single tiles whose pages are more than L2 holds: pairs leave a tile's rest for last."""
+    s = Step([9, 1, 30, 61, 4, 17, 2, 9, 40, 0, 5, 12, 3, 700], [30000 + 777 * (i % 5) for i in range(13)] + [9000], kv, seed=8, pad=2)
+    s.run()
+    out, lse = s.out.clone(), s.lse.clone()
+    s.call()
+    assert torch.equal(out, s.out) and torch.equal(lse, s.lse)
+
+
+@KV
 def test_ragged_batch(kv):
     rng = np.random.default_rng(5)
     new = np.where(rng.random(70) < 0.5, 1, rng.integers(0, 90, 70))
