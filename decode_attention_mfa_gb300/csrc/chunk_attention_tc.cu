@@ -1062,12 +1062,14 @@ __device__ __forceinline__ float split_queries(uint32_t q_addr, float* red, int 
   return top < 0x7F800000u ? exp2_int(-e) : __uint_as_float(0x7FFFFFFFu);
 }
 
-// A row's reference is its largest logit when it is set, so that its weights then are at most 1. It moves when the sum of a
+// A row's reference is set so that its largest weight then is 2^moved_to: 1, and 16 on quantised caches. It moves when the sum of a
 // thread's 64 weights of a unit passes this, and in units that the careful way below takes for another reason, when a weight
 // passes the 64th part. A move takes a unit 2000 cycles longer. bf16 has room for more, but O is weights times V, and V up to
-// 2^97 is to fit. f16 ends at 2^16, and below 2^-14 its step stays 2^-24: N such weights, beside a sum of 1 at least, are off
-// by N 2^-25 together if all round the same way (65536: half a bf16 step of the output). With references lower by 4, as the
-// shared-prefix kernel has them, 304 tokens behind 16080 with logits of twice the spread took 207 us instead of 191.
+// 2^97 is to fit. f16 ends at 2^16, and below 2^-14 its step stays 2^-24: weights below 2^-18 of the row's largest are held to
+// 2^-29 of it, as in the shared-prefix kernel, so that N of them that all round the same way are off by N 2^-29 together (262144:
+// 2^-11). With references at the largest logit that would be N 2^-25, and below 2^-25 nothing would be left of them in O (304
+// tokens behind 16080 on E4M3 174 us instead of 174.5, with logits of twice and four times the spread 187 and 224 instead of 201
+// and 235).
 template <bool kQ8>
 __host__ __device__ constexpr int most_sum_log2() { return kQ8 ? 15 : 30; }
 
@@ -1172,7 +1174,7 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
     }
     const float most = fmaxf(big, mine[(half ^ 1) * 128 + row]);
     // where one row moves, all do
-    const float m_new = st.open || over || most > st.m + (most_sum_log2<kQ8>() - 6) ? fmaxf(st.m, most) : st.m;
+    const float m_new = st.open || over || most > st.m + (most_sum_log2<kQ8>() - 6) ? fmaxf(st.m, most - moved_to<kQ8>()) : st.m;
     const float alpha = st.fresh || st.m == m_new ? 1.0f : ex2_approx(st.m - m_new);
     st.m = m_new;
     st.open = __any_sync(0xffffffffu, st.m == -INFINITY);  // the same in both warps of the rows
