@@ -828,6 +828,24 @@ __device__ void mma_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s,
   (void)mbar_wait(cx.bar(Drain), 0, kDrainNs, nullptr, p.err);
 }
 
+// ---------------------------------------------------------------- references
+// A row's reference is set so that its largest weight then is 2^set_at. It moves when the sum of a thread's weights passes
+// 2^most_sum_log2: of the 64 of a unit on a quantised cache, of all so far on a bf16 cache. And in units that the careful way
+// below takes for another reason, when a weight passes the 64th part. A move takes a unit 2000 cycles longer.
+// P as f16 ends at 2^16, and below 2^-14 its step stays 2^-24: weights below 2^-18 of the row's largest are held to 2^-29 of it,
+// as in the shared-prefix kernel, so that N of them that all round the same way are off by N 2^-29 together (262144: 2^-11). With
+// references at the largest logit that would be N 2^-25, and below 2^-25 nothing would be left of them in O (304 tokens behind
+// 16080 on E4M3 174 us instead of 174.5, with logits of twice and four times the spread 187 and 224 instead of 201 and 235).
+// P as bf16 has the same relative step everywhere, so its weights are small enough that a row's never have a sum above 1: two
+// threads have 2^-3 each, the last unit, which is not whole, once more, and units at the limit whose weights are no larger than
+// 2^-30 64 of these each (2^21 units, the most that memory holds, 2^-3 together). O is then never larger than the largest V, and
+// no finite V gives an infinite output; values below 2^-88 have products at fp32's lower end and may lose bits. (With weights of
+// up to 2^30 a unit, values of 2^90 came out infinite behind 200 units of such weights; the times are the same.)
+template <bool kQ8>
+__host__ __device__ constexpr int set_at() { return kQ8 ? (int)moved_to<true>() : -30; }
+template <bool kQ8>
+__host__ __device__ constexpr int most_sum_log2() { return kQ8 ? 15 : -3; }
+
 // ---------------------------------------------------------------- V and output
 // V of position k of the piece's sequence, if it is no number, else 0.
 template <int kFmt>
@@ -885,7 +903,8 @@ __device__ __forceinline__ void write_piece(const ChunkParams& p, const Ctx& cx,
   const size_t out_row = (size_t)(q.row + j) * kHeads + (row & 63);
   const size_t part = (size_t)(2 * pair + (q.u0 == 0)) * 256 + 128 * cx.rank + row;
   if (valid && d0 == 0) {
-    const float lse = (m + log2f(l)) * kLn2;
+    constexpr int kSet = kQuant<kFmt> ? 0 : set_at<false>();  // taken off both first, so that neither is far from their sum
+    const float lse = ((m + kSet) + log2f(l * exp2_int(-kSet))) * kLn2;
     if (whole) p.lse[out_row] = lse;
     else p.part_lse[part] = lse;
   }
@@ -1062,17 +1081,6 @@ __device__ __forceinline__ float split_queries(uint32_t q_addr, float* red, int 
   return top < 0x7F800000u ? exp2_int(-e) : __uint_as_float(0x7FFFFFFFu);
 }
 
-// A row's reference is set so that its largest weight then is 2^moved_to: 1, and 16 on quantised caches. It moves when the sum of a
-// thread's 64 weights of a unit passes this, and in units that the careful way below takes for another reason, when a weight
-// passes the 64th part. A move takes a unit 2000 cycles longer. bf16 has room for more, but O is weights times V, and V up to
-// 2^97 is to fit. f16 ends at 2^16, and below 2^-14 its step stays 2^-24: weights below 2^-18 of the row's largest are held to
-// 2^-29 of it, as in the shared-prefix kernel, so that N of them that all round the same way are off by N 2^-29 together (262144:
-// 2^-11). With references at the largest logit that would be N 2^-25, and below 2^-25 nothing would be left of them in O (304
-// tokens behind 16080 on E4M3 174 us instead of 174.5, with logits of twice and four times the spread 187 and 224 instead of 201
-// and 235).
-template <bool kQ8>
-__host__ __device__ constexpr int most_sum_log2() { return kQ8 ? 15 : 30; }
-
 // The weights of one unit, S in tensor memory replaced by P. tx: this thread's 64 products, of which `cols` count (the two
 // warps of the rows together at least one; `whole`: all 128); o_addr: O's first column in its lane; sc: the K scales of its
 // keys, 128 before their V scales (quantised); may: some V scale among the warp's may have a shift; wait_pv: O holds every
@@ -1132,7 +1140,9 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
       for (int c = 0; c < 16; ++c) w[g / 2 + c] = weigh(fma2(x[c], mul_2, ref_2), c);
     }
     const float2 all = add2(sum[0], sum[1]);
-    done = !barrier_rows_or(quad, all.x + all.y > exp2_int(most_sum_log2<kQ8>()) || may);
+    float total = all.x + all.y;
+    if constexpr (!kQ8) total += st.l;
+    done = !barrier_rows_or(quad, total > exp2_int(most_sum_log2<kQ8>()) || may);
     over = !done;
   }
   if (!done) {
@@ -1174,7 +1184,7 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
     }
     const float most = fmaxf(big, mine[(half ^ 1) * 128 + row]);
     // where one row moves, all do
-    const float m_new = st.open || over || most > st.m + (most_sum_log2<kQ8>() - 6) ? fmaxf(st.m, most - moved_to<kQ8>()) : st.m;
+    const float m_new = st.open || over || most > st.m + (most_sum_log2<kQ8>() - 6) ? fmaxf(st.m, most - set_at<kQ8>()) : st.m;
     const float alpha = st.fresh || st.m == m_new ? 1.0f : ex2_approx(st.m - m_new);
     st.m = m_new;
     st.open = __any_sync(0xffffffffu, st.m == -INFINITY);  // the same in both warps of the rows
@@ -1412,6 +1422,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(threads<kFmt>(), 1)
 // tokens behind 900 took 1.7 us longer.
 constexpr int kCombineThreads = 256, kCombineWarps = kCombineThreads / 32, kCombineBlocksPerPair = 6;
 static_assert(kCombineWarps == 8, "combine_groups");
+// Of the part with the largest LSE: the weights of all have a sum of at most 1, and what they join is no larger than the parts.
+constexpr float kPartWeight = 1.0f / 128;
+static_assert(kChunkMaxPairs + 1 <= 128, "parts of a tile");
 // kRows rows from r on of a tile whose first row is `first` and whose first part is pair `pair`'s; kHalves halves of them from
 // `half` on, kParts parts at a time; dims 4 lane .. 4 lane + 3 of a half.
 template <int kRows, int kHalves, int kParts>
@@ -1460,7 +1473,7 @@ __device__ __forceinline__ void combine_rows(const ChunkParams& p, int first, in
         for (int c = 0; c < 4; ++c) acc[j][h][c] = old == 0.0f ? 0.0f : acc[j][h][c] * old;
 #pragma unroll
       for (int k = 0; k < kParts; ++k) {
-        const float w = exp2f((z[j][k] - base) * kLog2e);
+        const float w = exp2f((z[j][k] - base) * kLog2e) * kPartWeight;
         den[j] += w;
         if (w != 0.0f) {  // of weight 0 (or no part): left out, never scaled
 #pragma unroll
@@ -1482,7 +1495,7 @@ __device__ __forceinline__ void combine_rows(const ChunkParams& p, int first, in
     for (int h = 0; h < kHalves; ++h)
       reinterpret_cast<uint2*>(p.out + row * kHeadDim)[32 * (half + h) + lane] =
           make_uint2(pack_bf16(acc[j][h][0] * inv, acc[j][h][1] * inv), pack_bf16(acc[j][h][2] * inv, acc[j][h][3] * inv));
-    if (half == 0 && lane == 0) p.lse[row] = mx[j] + log2f(den[j]) * kLn2;
+    if (half == 0 && lane == 0) p.lse[row] = mx[j] + log2f(den[j] / kPartWeight) * kLn2;
   }
 }
 __global__ void __launch_bounds__(kCombineThreads, 3) chunk_combine_kernel(const ChunkParams p) {

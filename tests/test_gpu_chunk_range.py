@@ -44,3 +44,40 @@ def test_many_small_weights_beside_a_large_one(below, at, kv):
 @pytest.mark.parametrize("new,held", [(1, 262143), (3, 131072), (2, 200001)])
 def test_long_contexts(new, held, kv):
     Step([new], [held], kv, seed=held).run()
+
+
+# ---------------------------------------------------------------- values of any size
+@pytest.mark.parametrize("power", [-90, -40, 40, 90, 110, 127])
+@pytest.mark.parametrize("rise", [0.0, 9.0, 14.0, 16.5, 30.0, -30.0])
+@pytest.mark.parametrize("new,held", [(5, 40000), (70, 300), (304, 30000)])
+def test_values_of_any_size(new, held, rise, power):
+    """Values up to the largest bf16, behind logits that are 2^(rise / ln 2) larger from the second unit of 128 keys on, so that
+    weights grow as far as they may before the reference moves, and then stay there: no finite value gives an infinite output."""
+    s = Step([new], [held], seed=32)
+    n = int(s.lens[0])
+    logits = torch.full((n,), rise, device="cuda")
+    logits[:128] = 0.0
+    v = torch.full((n,), 1.9921875 * 2.0 ** power, device="cuda")  # 2^127: the largest bf16
+    if held != 300:
+        v[::3] *= -1.0
+    _with_logits(s, 0, logits, v)
+    s.call()
+    if new > 70:  # the reference takes 64 heads of each token that it is asked for
+        s.starts[0], s.new[0] = new - 4, 4
+        s.out[:new - 4] = 7.0
+        s.lse[:new - 4] = 7.0
+    s.check()
+
+
+@pytest.mark.parametrize("sigma", [1.0, 4.0])
+def test_large_values_and_logits_of_any_spread(sigma):
+    s = Step([40, 1], [20000, 20000], seed=33, q_scale=sigma)
+    s.cache[1] *= 2.0 ** 124
+    s.call()
+    capi.mfa_check_device_errors(s.ws)
+    for b in range(2):
+        out, lse, top, _ = s.reference(b)
+        got, got_lse = (x[s.starts[b]:s.starts[b + 1]].double() for x in (s.out, s.lse))
+        # besides the weights' and the output's rounding, the logits' fp32 sums: 2^-15 of scale * sum |q k|, about 10 sigma
+        assert ((got - out).abs() <= 2 ** -8 * (top + out.abs()) + 2 * 10 * sigma * 2 ** -15 * top).all(), b
+        assert float((got_lse - lse).abs().max()) <= 1e-3 * sigma, b
