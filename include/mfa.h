@@ -293,9 +293,12 @@ mfa_status_t mfa_kv_read_fp4(const void* k_cache, const void* v_cache, const flo
  * E4M3 and E2M1 caches (mfa_chunk_attention_fp8, _fp4): q enters as the sum of
  * two E4M3 terms under a power of two of its row (within 2^-18.8 of the row's
  * largest |q|), V's values and the weights as f16, as in
- * mfa_decode_attention_prefix_fp8. A batch of one token each is faster with
- * mfa_decode_attention, _fp8, _fp4, from three or four tokens each on this call
- * is faster than mfa_decode_attention_mtp. Scales 16-byte, 4-bit caches 32-byte aligned.
+ * mfa_decode_attention_prefix_fp8: of a V scale outside [2^-16, 2) (E2M1:
+ * [2^-16, 2^10)) the power of two beyond enters with the weight instead, from
+ * 2^-116 to 2^101 (E2M1: 2^110); larger ones may give infinities or NaN.
+ * A batch of one token each is faster with mfa_decode_attention, _fp8, _fp4, from
+ * three or four tokens each on this call is faster than mfa_decode_attention_mtp.
+ * Scales 16-byte, 4-bit caches 32-byte aligned.
  * Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers, batch outside
  * [1, MFA_MAX_BATCH], max_tokens outside [0, MFA_MAX_CHUNK_TOKENS], max_pages
  * outside [1, 2^24], num_pages < 1, (max_tokens / 4 + batch) *

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from decode_attention_mfa_gb300 import capi
-from test_gpu_chunk import KV, Step, _with_logits
+from test_gpu_chunk import KV, Step, _with_logits, values
 
 pytestmark = pytest.mark.gpu
 LN2 = float(np.log(2.0))
@@ -81,3 +81,30 @@ def test_large_values_and_logits_of_any_spread(sigma):
         # besides the weights' and the output's rounding, the logits' fp32 sums: 2^-15 of scale * sum |q k|, about 10 sigma
         assert ((got - out).abs() <= 2 ** -8 * (top + out.abs()) + 2 * 10 * sigma * 2 ** -15 * top).all(), b
         assert float((got_lse - lse).abs().max()) <= 1e-3 * sigma, b
+
+
+@pytest.mark.parametrize("kv,power", [("fp8", 100), ("fp8", 101), ("fp8", 104), ("fp8", 112), ("fp4", 100), ("fp4", 110), ("fp4", 112), ("fp4", 115)])
+@pytest.mark.parametrize("new,held,at", [(7, 121, 125), (3, 0, 2), (4, 0, 0), (6, 125, 128), (40, 300, 50), (2, 5000, 5001)])
+def test_value_scales_at_the_end_of_their_range(new, held, at, kv, power):
+    """One position's V scale is the largest that the weights can take, 2^101 (E2M1 2^110), or above: the tokens that see it get
+    the attention, or no number where f16 does not hold a value above, and never a finite output without it; the others do not
+    notice it."""
+    s = Step([new], [held], kv, seed=34)
+    s.call()
+    clean = s.out.clone()
+    s.scales[1].view(-1)[s.row(0, at)] = 2.0 ** power
+    s.call()
+    capi.mfa_check_device_errors(s.ws)
+    out, _, top, limit = s.reference(0)
+    sees = limit > at
+    assert sees.any() and torch.equal(s.out[~sees], clean[~sees])
+    got = s.out.double()[sees]
+    # as f16: the codes times the scale less the 2^100 that the weight takes at most, times 2^6 (E2M1 2^3)
+    code = values(s.cache[1].view(-1, s.cache[1].shape[-1])[s.row(0, at)], torch.ones((), device="cuda"), kv)
+    held_as = code * torch.tensor(2.0 ** (power - 100 + (6 if kv == "fp8" else 3)), device="cuda").half().double()
+    fits = held_as.abs() < 65520
+    assert fits.all() or power > (101 if kv == "fp8" else 110)
+    # weights, values and their scales as f16, another 2^-8 of the largest value (that position's)
+    bound = 2 ** -8 * (2 * top[sees] + out[sees].abs()) + 2 ** -12 * top[sees]
+    assert ((got - out[sees]).abs() <= bound)[..., fits].all()
+    assert not torch.isfinite(got[..., ~fits]).any()
