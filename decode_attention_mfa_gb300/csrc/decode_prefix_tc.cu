@@ -748,7 +748,8 @@ __device__ void mma_role(const PrefixParams& p, const Ctx& cx, const PlanSmem& s
 // the rest, which is exact unless it falls below the E4M3 normal range (2^-18.8 of the row's largest |q|). 2^e is the
 // largest power of two that keeps the row within the E4M3 maximum, 448. Thread (row, half) takes the 128 dims of its
 // half, whose terms lie where they did: the second block is read whole before the terms of the first replace either.
-// All softmax threads; red: their exchange. Returns 2^-e.
+// All softmax threads; red: their exchange. Returns 2^-e, NaN for a row with an infinity (which E4M3 would hold as 448; a NaN
+// stays one in the terms).
 __device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, int quad, int half) {
   const uint32_t at = q_addr + half * 32768 + row * 128;  // the first of the two blocks; the second 16 KB on
   auto chunk = [&](int j) { return ((j ^ (row & 7)) << 4); };
@@ -771,7 +772,7 @@ __device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, i
   barrier_rows(quad);
   top = fmaxf(red[row], red[128 + row]);
   int e = 0;
-  if (top > 0.0f && top <= 3.0e38f) {
+  if (top > 0.0f && top < INFINITY) {
     const uint32_t bits = __float_as_uint(top);
     e = ((bits & 0x7FFFFFu) <= 0x600000u ? 8 : 7) - ((int)((bits >> 23) & 0xFFu) - 127);  // top * 2^e in (224, 448]
     e = max(-126, min(126, e));
@@ -793,7 +794,7 @@ __device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, i
 #pragma unroll
   for (int o = 4; o < 8; ++o) store(o, v[2 * o - 8], v[2 * o - 7]);
   fence_proxy_async_smem();
-  return exp2_int(-e);
+  return top < INFINITY ? exp2_int(-e) : __uint_as_float(0x7FFFFFFFu);
 }
 
 // The weights of one unit, S in tensor memory replaced by P. tx: this thread's 64 products, of which `cols` count (the two
