@@ -326,9 +326,9 @@ __global__ void __launch_bounds__(kSlotThreads) kv_append_slots_quantised_kernel
                                    (is_v ? p.v_scale : p.k_scale) + slot, l);
 }
 // The same with half a warp a row for very many rows: the blocks that are there at once go through all of them, each warp with
-// its next row's loads in flight while it works on one. With a block for every 8 rows the memory waits for that work (65536
-// rows to E2M1 17.7 us instead of 16.0). Five blocks an SM: with three, four and six E2M1 took 19.9, 16.5 and 18.9 us.
-constexpr int kStreamBlocksPerSm = 5, kStreamBlocks = 152 * kStreamBlocksPerSm, kStreamRows = kSlotThreads / 32;
+// its next row's loads in flight while it works on one. With a block for every 8 rows the memory waits for that work. Five
+// blocks an SM: with three, four and six, 65536 rows to E2M1 took 19.9, 16.5 and 18.9 us instead of 16.0.
+constexpr int kStreamBlocksPerSm = 5, kStreamRows = kSlotThreads / 32;
 template <bool kFp4>
 __global__ void __launch_bounds__(kSlotThreads, kStreamBlocksPerSm) kv_append_slots_stream_kernel(const AppendSlotsParams p) {
   constexpr int kLanes = 16;
@@ -376,13 +376,16 @@ cudaError_t launch_slots(const AppendSlotsParams& p, cudaStream_t stream) {
 template <bool kFp4>
 cudaError_t launch_slots_quantised(const AppendSlotsParams& p, cudaStream_t stream) {
   // a warp a row, half a warp, and with the loop, E4M3: 128 rows 1.55, 1.75 and 1.6 us, 4096 rows 2.7, 2.6 and 2.6, 8192 rows
-  // 3.9, 3.1 and 3.4, 65536 rows 20.5, 18.0 and 17.6
+  // 3.9, 3.1 and 3.4. Half a warp and the loop, from graphs: 8192 rows 2.8 and 3.1 (E2M1 3.0 and 3.3), 12160 rows 3.51 and 3.54
+  // (3.72 and 3.77), 16384 rows 4.24 and 4.24 (4.56 and 4.55), 24320 rows 5.8 and 5.8 (6.27 and 6.13), 65536 rows 15.7 and 14.6
+  // (15.5 and 14.7), 200000 rows 48.2 and 46.7 (48.0 and 43.4). (The loop gains at 4096 to 6080 rows too, 0.1 to 0.4 us, where all
+  // rows are in its first turn, and loses where few are in its second.)
   constexpr int kManyRows = 2048, kVeryManyRows = 16384;
   if (p.n_rows < kManyRows)
     return launch_pdl(kv_append_slots_quantised_kernel<kFp4, 32>, dim3(slot_blocks(2ll * p.n_rows)), dim3(kSlotThreads), 0, stream, p);
   if (p.n_rows < kVeryManyRows)
     return launch_pdl(kv_append_slots_quantised_kernel<kFp4, 16>, dim3(slot_blocks(p.n_rows)), dim3(kSlotThreads), 0, stream, p);
-  const unsigned blocks = std::min((unsigned)kStreamBlocks, (unsigned)(((long long)p.n_rows + kStreamRows - 1) / kStreamRows));
+  const unsigned blocks = std::min((unsigned)(kStreamBlocksPerSm * p.num_sms), (unsigned)(((long long)p.n_rows + kStreamRows - 1) / kStreamRows));
   return launch_pdl(kv_append_slots_stream_kernel<kFp4>, dim3(blocks), dim3(kSlotThreads), 0, stream, p);
 }
 

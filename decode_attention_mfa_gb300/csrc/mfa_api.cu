@@ -789,7 +789,8 @@ mfa_status_t append_slots_common(const void* k_new, const void* v_new, long long
     return fail(MFA_ERR_INVALID_ARG, "misaligned pointer (rows and caches need 16 bytes, the slot map 8)");
   if (!workspace || !aligned(workspace, 256))
     return fail(MFA_ERR_WORKSPACE, "workspace missing or not 256-byte aligned");
-  const mfa_status_t st = current_device(nullptr, nullptr);
+  DeviceInfo info;
+  const mfa_status_t st = current_device(nullptr, &info);
   if (st != MFA_OK) return st;
   if (n_rows == 0) return MFA_OK;
   AppendSlotsParams p{};
@@ -805,6 +806,7 @@ mfa_status_t append_slots_common(const void* k_new, const void* v_new, long long
   p.err = static_cast<uint32_t*>(workspace);
   p.n_rows = n_rows;
   p.num_pages = num_pages;
+  p.num_sms = info.num_sms;
   p.fmt = fmt;
   const cudaError_t e = launch_kv_append_slots(p, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "kv_append_slots launch");

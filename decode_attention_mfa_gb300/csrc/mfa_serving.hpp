@@ -18,7 +18,7 @@ struct AppendSlotsParams {
   float* k_scale;  // E4M3 and E2M1
   float* v_scale;
   uint32_t* err;
-  int n_rows, num_pages;
+  int n_rows, num_pages, num_sms;
   int fmt;  // kKvBf16, kKvE4M3 or kKvE2M1
 };
 
