@@ -1552,8 +1552,10 @@ cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& kmap, const CU
 template <int kFmt>
 cudaError_t launch_chunk(const ChunkParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, const CUtensorMap& qmap,
                          cudaStream_t stream) {
-  // Pieces that may turn cost 1 to 2% of a short prompt's or few tiles' time (16 of 512 tokens 160.7 -> 164.0 us, 304 tokens
-  // behind 16080 168.3 -> 169.6), so where all pages fit L2 there is a kernel without.
+  // Pieces that may turn cost a short prompt or few tiles 1 to 2% even where none does (16 of 512 tokens 160.0 -> 163.9 us, E4M3
+  // 233.5 -> 235.5, E2M1 233.4 -> 238.1; 304 tokens behind 16080 168.3 -> 169.6), so there is a kernel without, for calls whose
+  // pages fit L2 whatever their lengths. The host knows capacities alone: tables and a pool as small as that are a small server's
+  // or a test's, and one whose pool fills the card has the other kernel in every step. Half a unit a page.
   const bool turn = 0.5 * std::min((long long)p.B * p.max_pages, (long long)p.num_pages) > p.l2_units;
   return turn ? launch_chunk<kFmt, true>(p, kmap, vmap, qmap, stream) : launch_chunk<kFmt, false>(p, kmap, vmap, qmap, stream);
 }
