@@ -72,6 +72,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "chunk_plan.hpp"
 #include "mfa_serving.hpp"
 #include "tc_pair.cuh"
 
@@ -95,7 +96,6 @@ __host__ __device__ constexpr uint32_t slot_tx() { return kFmt == kKvE2M1 ? 8192
 template <int kFmt>
 using Range = std::conditional_t<kFmt == kKvE2M1, E2m1Range, E4m3Range>;
 constexpr uint32_t kVSlotBytes = 32768, kVPageBytes = 16384;  // V as the MMAs read it, 16 bits
-constexpr int kTokens = kChunkTileTokens;
 constexpr int kScaleSlots = 4, kScaleBytes = 1024;  // quantised: 128 K scales and 128 V scales a unit
 constexpr int kQBytes = 65536;                      // 128 rows x 256 dims, four 64-dim blocks of [128 rows x 128 B]
 static_assert(kTokens * kHeads == 256, "rows of a tile");
@@ -126,19 +126,6 @@ enum Bar {
   RawFull = TailReady + 2,          // [2] quantised, both: this CTA's V codes landed
   RawEmpty = RawFull + 2,           // [2] one arrival per converting warp of the CTA
   kBars = RawEmpty + 2
-};
-
-// The line of work as every CTA sees it.
-constexpr int kPlanChunks = kMaxBatch / 32 + 1;
-struct LineRange {
-  int from, to;
-};
-struct PlanSmem {
-  int32_t cost[kMaxBatch + 1];  // units of the sequences before b; [B]: of all
-  int32_t row[kMaxBatch + 1];   // first row of sequence b's tokens, non-decreasing within [0, max_tokens]
-  int32_t len[kMaxBatch];       // positions that its pages hold
-  int32_t last[kPlanChunks + 1], total[kPlanChunks + 1];  // of 32 sequences
-  LineRange rest;                                         // what the pair does last, if it is not empty
 };
 
 template <int kFmt>
@@ -183,26 +170,6 @@ __device__ __noinline__ void set_odd(uint32_t odd, uint32_t piece) {
 }
 
 // ---------------------------------------------------------------- plan
-// Tile i of a sequence whose chunk of n tokens stands behind a others sees a + min(4 (i + 1), n) keys. Of the tiles that
-// are full, the first i take, with z = floor((a + 127) / 4),
-//     sum_{k = 1..i} ceil((a + 4 k) / 128) = sum_{k = 1..i} floor((k + z) / 32) = G(i + z) - G(z)
-// units, G(m) = sum_{k = 0..m} floor(k / 32); modulo 2^32, and the host has seen to it that the sums stay below 2^31.
-__device__ __forceinline__ uint32_t floor_sum(uint32_t m) {
-  const uint32_t q = m >> 5;
-  return 16 * q * (q - 1) + q * ((m & 31) + 1);
-}
-__device__ __forceinline__ int units_of(int keys) { return (keys + kUnitKeys - 1) / kUnitKeys; }
-__device__ __forceinline__ int full_tiles_cost(int i, int a, int piece_units) {
-  const uint32_t z = (uint32_t)(a + kUnitKeys - 1) >> 2;
-  return (int)(floor_sum((uint32_t)i + z) - floor_sum(z)) + i * piece_units;
-}
-__device__ __forceinline__ int tiles_of(int n) { return (n + kTokens - 1) / kTokens; }
-__device__ __forceinline__ int sequence_cost(int len, int n, int piece_units) {
-  return n > 0 ? full_tiles_cost(tiles_of(n) - 1, len - n, piece_units) + units_of(len) + piece_units : 0;
-}
-// Tokens of b that see a key at all: the last len of them.
-__device__ __forceinline__ int seeing(const PlanSmem& s, int b) { return min(s.row[b + 1] - s.row[b], s.len[b]); }
-
 __device__ __forceinline__ int running_max(int x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -279,82 +246,6 @@ __device__ void build_plan(const ChunkParams& p, PlanSmem& s, uint32_t* err) {
   }
 }
 
-// Pairs that have work: with fewer units than pairs, every range holds one.
-__device__ __forceinline__ int busy_pairs(const ChunkParams& p, int units) { return min(p.pairs, max(units, 1)); }
-
-// A pair's pieces, in order: units [u0, u1) of one row tile. The rest of a tile that begins before the pair's range comes first,
-// or, where the pages are more than L2 holds, last (kTurn): then all pairs begin with tiles' beginnings and go through a
-// sequence's pages at about the same time, and HBM delivers them once for all of these. bf16, for seconds: 1024 tokens each
-// behind 100000 and 90000 1600 -> 1870 TFLOP/s, 2048 behind 129024 1660 -> 1890, 8 chunks of 512 behind 32000 1720 -> 2050 in a
-// burst; 2048 behind 63488, whose pages L2 holds, 1885 and 1890.
-struct Piece {
-  int b = -1, i;     // sequence, tile of it
-  int a, n, row0;    // of the sequence: positions before its chunk, tokens that see any, the first one's row
-  int row, tokens;   // of the tile: first row, tokens (1 to 4)
-  int seen0, seen;   // keys that its first and its last token see
-  int units;         // of the whole tile
-  int u0, u1;
-  int first, x;      // line positions: the tile's, and the one behind it
-  bool last = false; // it is of what comes last
-  __device__ int pages() const { return (seen + kPageSize - 1) / kPageSize; }
-  __device__ int keys(int page) const { return min(max(seen - page * kPageSize, 0), kPageSize); }
-  // Whether V of unit u holds rows that not all tokens see, up to the end of an MMA's 16 keys.
-  __device__ bool ends(int u) const { return (u + 1) * kUnitKeys > seen0 && (tokens > 1 || (seen % kKeyStep) != 0); }
-  __device__ bool whole() const { return u0 == 0 && u1 == units; }
-};
-template <bool kTurn>
-__device__ __forceinline__ bool next_piece(const ChunkParams& p, const PlanSmem& s, LineRange range, Piece& q) {
-  if (q.b < 0) q.x = range.from;
-  for (;;) {
-    if (kTurn && q.last) range = s.rest;
-    if (q.x >= range.to) {
-      if (!kTurn || q.last || s.rest.from >= s.rest.to) return false;
-      q.last = true;
-      q.x = s.rest.from;
-      q.b = -1;
-      range = s.rest;
-    }
-    if (q.b < 0 || q.x >= s.cost[q.b + 1]) {
-      const int b = last_at_most(s.cost, p.B, q.x);
-      q.b = b;
-      q.n = seeing(s, b);
-      q.a = s.len[b] - q.n;
-      q.row0 = s.row[b + 1] - q.n;
-      q.first = s.cost[b];
-      int i0 = 0, i1 = tiles_of(q.n) - 1;  // the last tile that begins at or before x
-      if (q.x == q.first) i1 = 0;
-      while (i0 < i1) {
-        const int mid = (i0 + i1 + 1) >> 1;
-        if (q.first + full_tiles_cost(mid, q.a, p.piece_units) <= q.x) i0 = mid; else i1 = mid - 1;
-      }
-      q.i = i0;
-      q.first += full_tiles_cost(i0, q.a, p.piece_units);
-    } else {
-      ++q.i;
-      q.first = q.x;
-    }
-    q.tokens = min(kTokens, q.n - kTokens * q.i);
-    q.row = q.row0 + kTokens * q.i;
-    q.seen0 = q.a + kTokens * q.i + 1;
-    q.seen = q.seen0 + q.tokens - 1;
-    q.units = units_of(q.seen);
-    q.u0 = max(0, q.x - q.first - p.piece_units);
-    q.u1 = min(q.units, range.to - q.first - p.piece_units);
-    q.x = q.first + p.piece_units + q.units;
-    if (q.u0 < q.u1) return true;
-  }
-}
-
-// Where a pair's range begins: at its first tile's beginning, if the rest of a tile before that is to come last.
-static __device__ __noinline__ int begin_of(const ChunkParams& p, const PlanSmem& s, int lo, int hi) {
-  Piece q;
-  if (!next_piece<false>(p, s, LineRange{lo, hi}, q) || q.u0 == 0 || q.x >= hi) return lo;
-  // units that the sequences hold together, if all are like this one, which is to have more than two tiles
-  const int cost = s.cost[q.b + 1] - s.cost[q.b];
-  const bool more = cost > 2 * (q.units + p.piece_units) && (float)q.units * (float)s.cost[p.B] > (float)p.l2_units * (float)cost;
-  return more ? q.x : lo;
-}
-
 // Groups of eight warps that the combine takes for a tile: of one and two parts a warp takes two rows, of up to four one, of more
 // half a row.
 __device__ __forceinline__ int combine_groups(int tokens, int parts) {
@@ -369,14 +260,10 @@ __device__ void publish_parts(const ChunkParams& p, const PlanSmem& s, int lane)
   for (int w0 = 0; w0 < W; w0 += 32) {
     const int w = w0 + lane;
     int row = 0, tokens = 0, parts = 0;
-    if (w < W && units > 0) {
-      const int lo = range_of_pair(w, units, W), hi = range_of_pair(w + 1, units, W);
-      Piece q;
-      if (next_piece<false>(p, s, LineRange{hi - 1, hi}, q) && q.u1 < q.units && lo <= q.first + p.piece_units) {
-        row = q.row;
-        tokens = q.tokens;
-        parts = pair_of_unit(q.first + p.piece_units + q.units - 1, units, W) - w + 1;
-      }
+    Piece q;
+    if (w < W && units > 0 && (parts = parts_from(p, s, w, units, W, q)) > 0) {
+      row = q.row;
+      tokens = q.tokens;
     }
     const uint32_t some = __ballot_sync(0xffffffffu, tokens > 0);
     const int mine = tokens > 0 ? combine_groups(tokens, parts) : 0, upto = warp_inclusive_sum(mine, lane);
@@ -904,7 +791,7 @@ __device__ __forceinline__ void write_piece(const ChunkParams& p, const Ctx& cx,
   // rows that see no key of the piece have O = 0 and no weight
   const float inv = q.seen0 + j <= q.u0 * kUnitKeys ? 0.0f : kQuant<kFmt> ? exp2_int(-Range<kFmt>::kUp) / l_p : 1.0f / l_p;
   const size_t out_row = (size_t)(q.row + j) * kHeads + (row & 63);
-  const size_t part = (size_t)(2 * pair + (q.u0 == 0)) * 256 + 128 * cx.rank + row;
+  const size_t part = (size_t)part_slot(pair, q.u0 == 0) * 256 + 128 * cx.rank + row;
   if (valid && d0 == 0) {
     constexpr int kSet = kQuant<kFmt> ? 0 : set_at<false>();  // taken off both first, so that neither is far from their sum
     const float lse = ((m + kSet) + log2f(l * exp2_int(-kSet))) * kLn2;
@@ -1450,7 +1337,7 @@ __device__ __forceinline__ void combine_rows(const ChunkParams& p, int first, in
 #pragma unroll
     for (int k = 0; k < kParts; ++k) {
       const int i = min(i0 + k, parts - 1);  // (behind the last part: the last one, without weight)
-      const size_t part = (size_t)(2 * (pair + i) + (i == 0)) * 256 + r;
+      const size_t part = (size_t)part_slot(pair + i, i == 0) * 256 + r;
 #pragma unroll
       for (int j = 0; j < kRows; ++j) {
         z[j][k] = __ldcg(p.part_lse + part + j);

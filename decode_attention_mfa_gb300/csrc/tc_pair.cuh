@@ -9,10 +9,10 @@
 #include <cuda_fp8.h>
 
 #include "mfa_device.cuh"
+#include "work_line.hpp"
 
 namespace mfa {
 
-constexpr int kUnitKeys = 2 * kPageSize;
 // Exponents of V's scales that f16 holds beside the codes' (V' = code * scale * 2^kUp): E4M3, V' at most 448 * 2^7 and its
 // scale at least 2^-10; E2M1, 6 * 2^13 and 2^-13.
 struct E4m3Range {
@@ -33,7 +33,6 @@ constexpr float kLn2 = 0.6931471805599453f;
 template <bool kFp8>
 __host__ __device__ constexpr float moved_to() { return kFp8 ? 4.0f : 0.0f; }
 constexpr float kMostSum = 32768.0f;
-constexpr int kKeyStep = 16;  // keys of one MMA of P V
 // Waits for what this CTA itself has in flight, before it leaves, do not shrink with the wait budget; and after a wait
 // that gave up, copies that no barrier of this CTA tells of get this long to land.
 constexpr uint64_t kDrainNs = 200000000ull, kSettleNs = 1000000ull;
@@ -147,16 +146,6 @@ struct Ctx {
   __device__ bool wait_warp(int i, uint32_t parity) const { return __all_sync(0xffffffffu, wait(i, parity)); }
 };
 
-// Largest g in [0, n) with a[g] <= x (a is non-decreasing and a[0] <= x).
-template <typename T>
-__device__ __forceinline__ int last_at_most(const T* a, int n, int x) {
-  int lo = 0, hi = n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((int)a[mid] <= x) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
 __device__ __forceinline__ int warp_inclusive_sum(int x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -167,18 +156,6 @@ __device__ __forceinline__ int warp_inclusive_sum(int x, int lane) {
 }
 
 __device__ __forceinline__ int pages_of(int tokens) { return (tokens + kPageSize - 1) / kPageSize; }
-
-// a b / c, in 32 bits where the product allows it.
-__device__ __forceinline__ int share(uint32_t a, uint32_t b, uint32_t c) {
-  const unsigned long long x = (unsigned long long)a * b;
-  return (x >> 32) ? (int)(x / c) : (int)((uint32_t)x / c);
-}
-// First unit of pair w's range of the line of C units, of W pairs; and the pair whose range holds unit x.
-__device__ __forceinline__ int range_of_pair(int w, int C, int W) { return share(w, C, W); }
-__device__ __forceinline__ int pair_of_unit(int x, int C, int W) {
-  const unsigned long long y = ((unsigned long long)x + 1) * W - 1;
-  return (y >> 32) ? (int)(y / (uint32_t)C) : (int)((uint32_t)y / (uint32_t)C);
-}
 
 // Whether the last MMA of P V on a page of so many tokens reaches behind them.
 __device__ __forceinline__ bool is_partial(int tokens) { return tokens % kKeyStep != 0; }
