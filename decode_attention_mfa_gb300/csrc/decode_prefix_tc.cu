@@ -780,8 +780,8 @@ __device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, i
   const float up = exp2_int(e);
   auto store = [&](int o, const uint4& x, const uint4& y) {  // 16 dims
     uint32_t a1[2], a2[2], b1[2], b2[2];
-    split_q8(x, up, a1, a2);
-    split_q8(y, up, b1, b2);
+    split_q8<false>(x, up, a1, a2);
+    split_q8<false>(y, up, b1, b2);
     const uint32_t t1[4] = {a1[0], a1[1], b1[0], b1[1]}, t2[4] = {a2[0], a2[1], b2[0], b2[1]};
     st_shared_v4(at + chunk(o), t1);
     st_shared_v4(at + 16384 + chunk(o), t2);
@@ -795,168 +795,6 @@ __device__ __forceinline__ float split_q(uint32_t q_addr, float* red, int row, i
   for (int o = 4; o < 8; ++o) store(o, v[2 * o - 8], v[2 * o - 7]);
   fence_proxy_async_smem();
   return top < INFINITY ? exp2_int(-e) : __uint_as_float(0x7FFFFFFFu);
-}
-
-// The weights of one unit, S in tensor memory replaced by P. tx: this thread's 64 products, of which `cols` count (the two
-// warps of the rows together at least one); o_addr: O's first column in its lane; sc: the K scales of its keys, 128 before
-// their V scales (E4M3); may: some V scale among the warp's may have a shift; wait_pv: O holds every unit before this one.
-// Both warps of the rows.
-template <bool kFp8, typename R, typename WaitPv>
-__device__ __forceinline__ void softmax_unit(RowState& st, uint32_t tx, uint32_t o_addr, const float* sc, int cols, bool may,
-                                             float mul, float* red, int row, int quad, int half, WaitPv&& wait_pv) {
-  // This thread's products, 32 keys at a time. P of 32 keys replaces the first 16 columns of their S.
-  float2 x[16];
-  auto load = [&](int g) {
-    tmem_ld32(tx + g, reinterpret_cast<float*>(x));
-    if constexpr (kFp8) {  // times the scales of K, of which half arrive meanwhile
-      const float4* k = reinterpret_cast<const float4*>(sc + g);
-      float4 k4[4];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) k4[c] = k[c];
-      tc_wait_ld();
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        x[2 * c] = mul2(x[2 * c], make_float2(k4[c].x, k4[c].y));
-        x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(k4[c].z, k4[c].w));
-      }
-#pragma unroll
-      for (int c = 4; c < 8; ++c) {
-        const float4 y = k[c];
-        x[2 * c] = mul2(x[2 * c], make_float2(y.x, y.y));
-        x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(y.z, y.w));
-      }
-    } else {
-      tc_wait_ld();
-    }
-  };
-  // Products behind the last token become infinities that give weights of 0, so that one body of code does for whole
-  // and partial units, which is fetched anew in every call (4 sequences behind 16 pages 14.3 us with two bodies, 14.0
-  // with one). E4M3: K's scales there may be anything, so the weights are masked themselves.
-  if (!kFp8 && cols < 64) {
-    const float none = mul > 0.0f ? -INFINITY : INFINITY;
-#pragma unroll 1
-    for (int g = 0; g < 64; g += 32) {
-      if (g + 32 <= cols) continue;
-      load(g);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        if (g + 2 * c >= cols) x[c].x = none;
-        if (g + 2 * c + 1 >= cols) x[c].y = none;
-      }
-      tmem_st32(tx + g, reinterpret_cast<const float*>(x));
-    }
-    tc_wait_st();
-  }
-  uint32_t w[32];
-  float2 sum, sum_p;
-  // weights of this thread's keys, their sums, and P; kPart: only the first `cols` of the 64 count
-  auto weights = [&](auto part) {
-    constexpr bool kPart = decltype(part)::value;
-    const float ref = st.m == -INFINITY ? 0.0f : st.m;  // only infinite logits so far: weights of 0
-    const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
-    sum = make_float2(0.0f, 0.0f);
-    sum_p = sum;
-    float2 sum1 = sum, sum_p1 = sum;
-#pragma unroll
-    for (int g = 0; g < 64; g += 32) {
-      load(g);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        float2 y = fma2(x[c], mul_2, ref_2);
-        y.x = ex2_approx(y.x);
-        y.y = ex2_approx(y.y);
-        if constexpr (kPart) {
-          if (g + 2 * c >= cols) y.x = 0.0f;
-          if (g + 2 * c + 1 >= cols) y.y = 0.0f;
-        }
-        if (c & 1)
-          sum1 = add2(sum1, y);
-        else
-          sum = add2(sum, y);
-        // the A operand is 16 bits, half a step of each weight: 2^-8 (bf16), 2^-11 (f16)
-        const uint32_t both = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
-        w[g / 2 + c] = both;
-        if constexpr (!kFp8) {
-          const float2 rounded = make_float2(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u));
-          if (c & 1)
-            sum_p1 = add2(sum_p1, rounded);
-          else
-            sum_p = add2(sum_p, rounded);
-        }
-      }
-    }
-    sum = add2(sum, sum1);
-    sum_p = add2(sum_p, sum_p1);
-  };
-  // the largest logit of this thread's first `end` keys (log2 units), or of more where these give none
-  auto largest = [&](int end) -> float {
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int g = 0; g < 64; g += 32) {
-      if (g >= end && !__any_sync(0xffffffffu, top == -INFINITY)) break;
-      load(g);
-#pragma unroll
-      for (int c = 0; c < 16; ++c) {
-        if (!kFp8 || g + 2 * c < cols) top = fmaxf(top, x[c].x * mul);
-        if (!kFp8 || g + 2 * c + 1 < cols) top = fmaxf(top, x[c].y * mul);
-      }
-    }
-    return top;
-  };
-  bool move = st.open, shifted = false;
-#pragma unroll 1
-  for (int tries = 0; tries < 2; ++tries) {
-    if (move) {
-      if (kFp8 && (shifted = barrier_rows_or(quad, may))) break;
-      // Half the keys are enough for a first reference, the sum tells if not (32 sequences behind 128 pages 26.0 ->
-      // 25.6 us; on an E4M3 cache 50.4 and 50.6, so not there).
-      const float big = largest(!kFp8 && tries == 0 ? 32 : 64) - moved_to<kFp8>();
-      red[half * 128 + row] = big;
-      barrier_rows(quad);
-      const float m_new = fmaxf(st.m, fmaxf(big, red[(half ^ 1) * 128 + row]));
-      const float alpha = st.fresh || st.m == m_new ? 1.0f : ex2_approx(st.m - m_new);
-      st.m = m_new;
-      st.open = __any_sync(0xffffffffu, st.m == -INFINITY);  // the same in both warps of the rows
-      st.l *= alpha;
-      st.l_p *= alpha;
-      if (!st.fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
-        // O holds the units before this one; each of the two warps scales half of its columns
-        wait_pv();
-        tc_fence_after();
-#pragma unroll 1
-        for (int c = 128 * half; c < 128 * half + 128; c += 32) {
-          float o[32];
-          tmem_ld32(o_addr + c, o);
-          tc_wait_ld();
-#pragma unroll
-          for (int k = 0; k < 32; ++k) o[k] *= alpha;
-          tmem_st32(o_addr + c, o);
-        }
-        tc_wait_st();  // the second try may read O again
-      }
-    }
-    if (!kFp8 || cols >= 64)
-      weights(std::false_type{});
-    else
-      weights(std::true_type{});
-    move = barrier_rows_or(quad, sum.x + sum.y > kMostSum || may);
-    if (!move) break;
-  }
-  if (kFp8 && shifted) {  // nothing has been done yet
-    if (!st.fresh) wait_pv();
-    tc_fence_after();
-    const float2 ml = shifted_unit<R>(tx, o_addr, sc, cols, mul, st.m, st.l, st.fresh, red, row, half);
-    st.m = ml.x;
-    st.l = ml.y;
-    st.open = __any_sync(0xffffffffu, st.m == -INFINITY);
-  } else {
-    st.l += sum.x + sum.y;
-    st.l_p += sum_p.x + sum_p.y;
-    tmem_st16(tx, reinterpret_cast<const float*>(w));
-    tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
-    tc_wait_st();
-  }
-  st.fresh = false;
 }
 
 template <bool kFp8>
@@ -985,7 +823,13 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     const int own1 = j == 0 ? q.c[1] : j == 1 ? q.c[2] : j == 2 ? q.c[3] : q.c[4];
     const int tail = (int)((q.tails >> (8 * j)) & 0xFF);
     auto seen = [&](int k) { return k < prefix ? kPageSize : k < own0 || k >= own1 ? 0 : k + 1 < own1 ? kPageSize : tail; };
-    RowState st;
+    bool fresh = true;              // no key so far
+    bool open = true;               // a row of the warp has no finite reference
+    float m = -INFINITY, l = 0.0f;  // the row's reference (log2 units), and this thread's share of its denominator
+    // The same of the weights as P holds them, by which O is divided: a weight that has most of the sum then cancels its
+    // rounding (relative error of out 2.4e-3 -> 1.9e-3 for 128 sequences behind 512 pages, 1% slower). Of f16 weights the
+    // difference does not matter. The LSE takes the unrounded sum.
+    float l_p = 0.0f;
     float mul = c2;                 // of the row's products: the softmax scale, and the power of two of its Q terms
     if constexpr (kFp8) {
       wait(QFull, pieces & 1);
@@ -1010,7 +854,160 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
       wait(SFull + buf, (cnt >> 1) & 1);
       tc_fence_after();
       if (cols + seen(2 * u + (half ^ 1)) > 0) {
-        softmax_unit<kFp8, E4m3Range>(st, ts + 64 * half, tmem + lanes + kTmemO, sc + 64 * half, cols, may, mul, red, row, quad, half, wait_pv);
+        // This thread's products, 32 keys at a time. P of 32 keys replaces the first 16 columns of their S.
+        float2 x[16];
+        const uint32_t tx = ts + 64 * half;
+        auto load = [&](int g) {
+          tmem_ld32(tx + g, reinterpret_cast<float*>(x));
+          if constexpr (kFp8) {  // times the scales of K, of which half arrive meanwhile
+            const float4* k = reinterpret_cast<const float4*>(sc + 64 * half + g);
+            float4 k4[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) k4[c] = k[c];
+            tc_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              x[2 * c] = mul2(x[2 * c], make_float2(k4[c].x, k4[c].y));
+              x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(k4[c].z, k4[c].w));
+            }
+#pragma unroll
+            for (int c = 4; c < 8; ++c) {
+              const float4 y = k[c];
+              x[2 * c] = mul2(x[2 * c], make_float2(y.x, y.y));
+              x[2 * c + 1] = mul2(x[2 * c + 1], make_float2(y.z, y.w));
+            }
+          } else {
+            tc_wait_ld();
+          }
+        };
+        // Products behind the last token become infinities that give weights of 0, so that one body of code does for whole
+        // and partial units, which is fetched anew in every call (4 sequences behind 16 pages 14.3 us with two bodies, 14.0
+        // with one). E4M3: K's scales there may be anything, so the weights are masked themselves.
+        if (!kFp8 && cols < 64) {
+          const float none = mul > 0.0f ? -INFINITY : INFINITY;
+#pragma unroll 1
+          for (int g = 0; g < 64; g += 32) {
+            if (g + 32 <= cols) continue;
+            load(g);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              if (g + 2 * c >= cols) x[c].x = none;
+              if (g + 2 * c + 1 >= cols) x[c].y = none;
+            }
+            tmem_st32(tx + g, reinterpret_cast<const float*>(x));
+          }
+          tc_wait_st();
+        }
+        uint32_t w[32];
+        float2 sum, sum_p;
+        // weights of this thread's keys, their sums, and P; kPart: only the first `cols` of the 64 count
+        auto weights = [&](auto part) {
+          constexpr bool kPart = decltype(part)::value;
+          const float ref = m == -INFINITY ? 0.0f : m;  // only infinite logits so far: weights of 0
+          const float2 mul_2 = make_float2(mul, mul), ref_2 = make_float2(-ref, -ref);
+          sum = make_float2(0.0f, 0.0f);
+          sum_p = sum;
+          float2 sum1 = sum, sum_p1 = sum;
+#pragma unroll
+          for (int g = 0; g < 64; g += 32) {
+            load(g);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              float2 y = fma2(x[c], mul_2, ref_2);
+              y.x = ex2_approx(y.x);
+              y.y = ex2_approx(y.y);
+              if constexpr (kPart) {
+                if (g + 2 * c >= cols) y.x = 0.0f;
+                if (g + 2 * c + 1 >= cols) y.y = 0.0f;
+              }
+              if (c & 1)
+                sum1 = add2(sum1, y);
+              else
+                sum = add2(sum, y);
+              // the A operand is 16 bits, half a step of each weight: 2^-8 (bf16), 2^-11 (f16)
+              const uint32_t both = kFp8 ? pack_f16(y.x, y.y) : pack_bf16(y.x, y.y);
+              w[g / 2 + c] = both;
+              if constexpr (!kFp8) {
+                const float2 rounded = make_float2(__uint_as_float(both << 16), __uint_as_float(both & 0xFFFF0000u));
+                if (c & 1)
+                  sum_p1 = add2(sum_p1, rounded);
+                else
+                  sum_p = add2(sum_p, rounded);
+              }
+            }
+          }
+          sum = add2(sum, sum1);
+          sum_p = add2(sum_p, sum_p1);
+        };
+        // the largest logit of this thread's first `end` keys (log2 units), or of more where these give none
+        auto largest = [&](int end) -> float {
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int g = 0; g < 64; g += 32) {
+            if (g >= end && !__any_sync(0xffffffffu, top == -INFINITY)) break;
+            load(g);
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+              if (!kFp8 || g + 2 * c < cols) top = fmaxf(top, x[c].x * mul);
+              if (!kFp8 || g + 2 * c + 1 < cols) top = fmaxf(top, x[c].y * mul);
+            }
+          }
+          return top;
+        };
+        bool move = open, shifted = false;
+#pragma unroll 1
+        for (int tries = 0; tries < 2; ++tries) {
+          if (move) {
+            if (kFp8 && (shifted = barrier_rows_or(quad, may))) break;
+            // Half the keys are enough for a first reference, the sum tells if not (32 sequences behind 128 pages 26.0 ->
+            // 25.6 us; on an E4M3 cache 50.4 and 50.6, so not there).
+            const float big = largest(!kFp8 && tries == 0 ? 32 : 64) - moved_to<kFp8>();
+            red[half * 128 + row] = big;
+            barrier_rows(quad);
+            const float m_new = fmaxf(m, fmaxf(big, red[(half ^ 1) * 128 + row]));
+            const float alpha = fresh || m == m_new ? 1.0f : ex2_approx(m - m_new);
+            m = m_new;
+            open = __any_sync(0xffffffffu, m == -INFINITY);  // the same in both warps of the rows
+            l *= alpha;
+            l_p *= alpha;
+            if (!fresh && __any_sync(0xffffffffu, alpha != 1.0f)) {
+              // O holds the units before this one; each of the two warps scales half of its columns
+              wait_pv();
+              tc_fence_after();
+#pragma unroll 1
+              for (int c = 128 * half; c < 128 * half + 128; c += 32) {
+                float o[32];
+                tmem_ld32(tmem + lanes + kTmemO + c, o);
+                tc_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= alpha;
+                tmem_st32(tmem + lanes + kTmemO + c, o);
+              }
+              tc_wait_st();  // the second try may read O again
+            }
+          }
+          if (!kFp8 || cols >= 64)
+            weights(std::false_type{});
+          else
+            weights(std::true_type{});
+          move = barrier_rows_or(quad, sum.x + sum.y > kMostSum || may);
+          if (!move) break;
+        }
+        if (kFp8 && shifted) {  // nothing has been done yet
+          if (!fresh) wait_pv();
+          tc_fence_after();
+          const float2 ml = shifted_unit<E4m3Range>(tx, tmem + lanes + kTmemO, sc + 64 * half, cols, mul, m, l, fresh, red, row, half);
+          m = ml.x;
+          l = ml.y;
+          open = __any_sync(0xffffffffu, m == -INFINITY);
+        } else {
+          l += sum.x + sum.y;
+          l_p += sum_p.x + sum_p.y;
+          tmem_st16(tx, reinterpret_cast<const float*>(w));
+          tmem_st16(tx + 32, reinterpret_cast<const float*>(w + 16));
+          tc_wait_st();
+        }
+        fresh = false;
       }
       tc_fence_before();
       __syncwarp();
@@ -1022,8 +1019,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
     // ---- the piece's partial result: O / l and its LSE, 128 dims a thread
     wait_pv();
     tc_fence_after();
-    if (!st.fresh) {
-      float l = st.l, l_p = st.l_p;
+    if (!fresh) {
       red[half * 128 + row] = l;
       if (!kFp8) red[256 + half * 128 + row] = l_p;
       barrier_rows(quad);
@@ -1043,7 +1039,7 @@ __device__ void softmax_role(const PrefixParams& p, const Ctx& cx, const PlanSme
 #pragma unroll
         for (int k = 0; k < 4; ++k) st_global_v8(dst + k * kHeadDim + c, o + 8 * k);
       }
-      if (half == 0) p.part_lse[at] = (st.m + log2f(l)) * kLn2;
+      if (half == 0) p.part_lse[at] = (m + log2f(l)) * kLn2;
       barrier_rows(quad);  // red is free again
     }
     tc_fence_before();

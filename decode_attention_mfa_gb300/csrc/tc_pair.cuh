@@ -260,6 +260,10 @@ __device__ __forceinline__ bool barrier_rows_or(int quad, bool pred) {
 // Eight bf16 values times `up` (at most 448 then) as two E4M3 terms: codes of four in a word. Between them the values are
 // f16, which holds their eight bits exactly from 2^-17 on (the second term's last step is 2^-9); in fp32 the two prompts
 // on an 8-bit cache take 0.4 us more.
+// kPairs: the product, which is exact, as bf16 pairs, one operation of ten less; the chunk kernel gains 0.5% by it (two prompts of
+// 4096 672.7 -> 669.4 us), the shared-prefix kernel loses 0.4 to 3% (128 sequences behind 512 pages 182.4 -> 188.4), whose loops the
+// compiler then lays out otherwise.
+template <bool kPairs>
 __device__ __forceinline__ void split_q8(const uint4 v, float up, uint32_t (&t1)[2], uint32_t (&t2)[2]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
   const __nv_bfloat162 up_2 = __float2bfloat162_rn(up);
@@ -268,9 +272,14 @@ __device__ __forceinline__ void split_q8(const uint4 v, float up, uint32_t (&t1)
     uint32_t a = 0, b = 0;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * i + k]), up_2);  // exact
-      const uint32_t bits = *reinterpret_cast<const uint32_t*>(&y);
-      const __half2 x = __floats2half2_rn(__uint_as_float(bits << 16), __uint_as_float(bits & 0xFFFF0000u));
+      __half2 x;
+      if constexpr (kPairs) {
+        const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w[2 * i + k]), up_2);
+        const uint32_t bits = *reinterpret_cast<const uint32_t*>(&y);
+        x = __floats2half2_rn(__uint_as_float(bits << 16), __uint_as_float(bits & 0xFFFF0000u));
+      } else {
+        x = __floats2half2_rn(__uint_as_float(w[2 * i + k] << 16) * up, __uint_as_float(w[2 * i + k] & 0xFFFF0000u) * up);
+      }
       const __nv_fp8x2_storage_t c1 =
           __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&x), __NV_SATFINITE, __NV_E4M3);
       const __half2_raw h1 = __nv_cvt_fp8x2_to_halfraw2(c1, __NV_E4M3);
@@ -339,16 +348,5 @@ static __device__ __noinline__ float2 shifted_unit(uint32_t tx, uint32_t o_addr,
   barrier_rows(row >> 5);  // red is free again
   return make_float2(m_new, l * alpha + sum);
 }
-
-// A row's state over the units of its keys: the reference (log2 units), and this thread's share of the denominator.
-struct RowState {
-  bool fresh = true;  // no key so far
-  bool open = true;   // a row of the warp has no finite reference
-  float m = -INFINITY, l = 0.0f;
-  // The same of the weights as P holds them, by which O is divided: a weight that has most of the sum then cancels its
-  // rounding (relative error of out 2.4e-3 -> 1.9e-3 for 128 sequences behind 512 pages, 1% slower). Of f16 weights the
-  // difference does not matter. The LSE takes the unrounded sum.
-  float l_p = 0.0f;
-};
 
 }  // namespace mfa
