@@ -59,15 +59,13 @@
 // tile begins; V's codes times their scales become f16, and P is f16 as well (the
 // shared-prefix kernel says why).
 //
-// Measured, combine included: 2048 tokens behind 63488 in 4.56 ms (1900 TFLOP/s;
-// cuBLAS reaches 1896 in a burst, 1707 for seconds), the tensor cores 97% busy; 304
-// behind 16080 in 165 us, E4M3 175, E2M1 167. A unit takes the 2050 cycles of its
-// MMAs; what is lost between two tiles is 0.4 us for long tiles, and 2.6 us for the
-// tiles of 2.5 units that 512-token prompts have (16 of them 163 us: a chain of Q
-// and K from L2, 2 us each under load, the softmax of two units and the output),
-// on quantised caches 3 us (Q waits for the last S, and its split takes 1.6). 23
-// tokens behind 900 take 15 us: plan 1.2, first tile, page ids and loads 1.9, a unit
-// 2.9, 128 KB of fp32 partial results a CTA 2.8, combine 2.5, two launches.
+// Measured, combine included: 2048 tokens behind 63488 in 4.65 ms called back to back (1860 TFLOP/s; cuBLAS reaches 1896 in a
+// burst, 1707 for seconds), the tensor cores 98% busy; 304 behind 16080 in 165 us, E4M3 174, E2M1 168 (replayed from graphs, as
+// the following). A unit takes the 2050 cycles of its MMAs; what is lost between two tiles is 0.4 us for long tiles, and 2.6 us for
+// the tiles of 2.5 units that 512-token prompts have (16 of them 161 us: a chain of Q and K from L2, 2 us each under load, the
+// softmax of two units and the output), on quantised caches 3 us (Q waits for the last S, and its split takes 1.6; 220 and 223
+// us). 23 tokens behind 900 take 15 us: plan 1.2, first tile, page ids and loads 1.9, a unit 2.9, 128 KB of fp32 partial results
+// a CTA 2.8, combine 2.5, two launches.
 #include <cuda_fp4.h>
 #include <algorithm>
 #include <type_traits>

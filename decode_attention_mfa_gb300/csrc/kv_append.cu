@@ -376,10 +376,10 @@ cudaError_t launch_slots(const AppendSlotsParams& p, cudaStream_t stream) {
 template <bool kFp4>
 cudaError_t launch_slots_quantised(const AppendSlotsParams& p, cudaStream_t stream) {
   // a warp a row, half a warp, and with the loop, E4M3: 128 rows 1.55, 1.75 and 1.6 us, 4096 rows 2.7, 2.6 and 2.6, 8192 rows
-  // 3.9, 3.1 and 3.4. Half a warp and the loop, from graphs: 8192 rows 2.8 and 3.1 (E2M1 3.0 and 3.3), 12160 rows 3.51 and 3.54
-  // (3.72 and 3.77), 16384 rows 4.24 and 4.24 (4.56 and 4.55), 24320 rows 5.8 and 5.8 (6.27 and 6.13), 65536 rows 15.7 and 14.6
-  // (15.5 and 14.7), 200000 rows 48.2 and 46.7 (48.0 and 43.4). (The loop gains at 4096 to 6080 rows too, 0.1 to 0.4 us, where all
-  // rows are in its first turn, and loses where few are in its second.)
+  // 3.9, 3.1 and 3.4. Half a warp and the loop, replayed on the same rows, part of which L2 then holds: 8192 rows 2.8 and 3.1
+  // (E2M1 3.0 and 3.3), 12160 rows 3.51 and 3.54 (3.72 and 3.77), 16384 rows 4.24 and 4.24 (4.56 and 4.55), 24320 rows 5.8 and
+  // 5.8 (6.27 and 6.13), 65536 rows 15.7 and 14.6 (15.5 and 14.7), 200000 rows 48.2 and 46.7 (48.0 and 43.4). The loop gains at
+  // 4096 to 6080 rows too, 0.1 to 0.4 us, where all rows are in its first turn, and loses where few are in its second.
   constexpr int kManyRows = 2048, kVeryManyRows = 16384;
   if (p.n_rows < kManyRows)
     return launch_pdl(kv_append_slots_quantised_kernel<kFp4, 32>, dim3(slot_blocks(2ll * p.n_rows)), dim3(kSlotThreads), 0, stream, p);

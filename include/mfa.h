@@ -296,8 +296,9 @@ mfa_status_t mfa_kv_read_fp4(const void* k_cache, const void* v_cache, const flo
  * mfa_decode_attention_prefix_fp8: of a V scale outside [2^-16, 2) (E2M1:
  * [2^-16, 2^10)) the power of two beyond enters with the weight instead, from
  * 2^-116 to 2^101 (E2M1: 2^110); larger ones may give infinities or NaN.
- * A batch of one token each is faster with mfa_decode_attention, _fp8, _fp4, from
- * three or four tokens each on this call is faster than mfa_decode_attention_mtp.
+ * A batch of one token each is faster with mfa_decode_attention, _fp8, _fp4 (by 1
+ * to 15%), of two about as fast with mfa_decode_attention_mtp on a bf16 cache;
+ * from three tokens each on, on quantised caches from two, this call is faster.
  * Scales 16-byte, 4-bit caches 32-byte aligned.
  * Host errors: MFA_ERR_INVALID_ARG (null or misaligned pointers, batch outside
  * [1, MFA_MAX_BATCH], max_tokens outside [0, MFA_MAX_CHUNK_TOKENS], max_pages
