@@ -721,13 +721,14 @@ __device__ void mma_role(const ChunkParams& p, const Ctx& cx, const PlanSmem& s,
 // as in the shared-prefix kernel, so that N of them that all round the same way are off by N 2^-29 together (262144: 2^-11). With
 // references at the largest logit that would be N 2^-25, and below 2^-25 nothing would be left of them in O (304 tokens behind
 // 16080 on E4M3 174 us instead of 174.5, with logits of twice and four times the spread 187 and 224 instead of 201 and 235).
-// P as bf16 has the same relative step everywhere, so its weights are small enough that a row's never have a sum above 1: two
-// threads have 2^-3 each, the last unit, which is not whole, once more, and units at the limit whose weights are no larger than
-// 2^-30 64 of these each (2^21 units, the most that memory holds, 2^-3 together). O is then never larger than the largest V, and
-// no finite V gives an infinite output; values below 2^-88 have products at fp32's lower end and may lose bits. (With weights of
-// up to 2^30 a unit, values of 2^90 came out infinite behind 200 units of such weights; the times are the same.)
+// P as bf16 has the same relative step everywhere, so its weights are small enough that a row's never have a sum above 1: each of
+// its two threads has 2^-3 behind a whole unit, 2^-2 behind the last one, and where it has more than 2^-4 when others move its
+// reference does too. O is then never larger than the largest V, and no finite V gives an infinite output. (With references at the
+// largest logit, moved by units of 2^30, values of 2^90 came out infinite behind 200 such units; the times are the same.) What it
+// takes from fp32's lower end: values of V below 2^-110 lose bits. Set at 2^-30, below 2^-104; at 2^-18, with which rows move
+// more often, below 2^-116, but two prompts of 4096 with logits of five times the spread took 680 us instead of 620.
 template <bool kQ8>
-__host__ __device__ constexpr int set_at() { return kQ8 ? (int)moved_to<true>() : -30; }
+__host__ __device__ constexpr int set_at() { return kQ8 ? (int)moved_to<true>() : -24; }
 template <bool kQ8>
 __host__ __device__ constexpr int most_sum_log2() { return kQ8 ? 15 : -3; }
 
@@ -1064,10 +1065,11 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
         top = fmaxf(top, fmaxf(y[c].x, y[c].y));
       }
     }
-    const float big = top;
+    float ask = top - set_at<kQ8>();  // for the row's reference
+    if constexpr (!kQ8) ask = fmaxf(ask, st.l > 0x1p-4f ? st.m + 8.0f : -INFINITY);
     float* mine = red + (turn ? 256 : 0);  // two turns: who is two exchanges ahead has seen the other read
     turn = !turn;
-    mine[half * 128 + row] = big;
+    mine[half * 128 + row] = ask;
     bool shifted = false;
     if constexpr (kQ8) shifted = barrier_rows_or(quad, may);
     else barrier_rows(quad);
@@ -1081,9 +1083,9 @@ __device__ __forceinline__ void softmax_tile_unit(RowState& st, uint32_t tx, uin
       st.fresh = false;
       return;
     }
-    const float most = fmaxf(big, mine[(half ^ 1) * 128 + row]);
+    ask = fmaxf(ask, mine[(half ^ 1) * 128 + row]);
     // where one row moves, all do
-    const float m_new = st.open || over || most > st.m + (most_sum_log2<kQ8>() - 6) ? fmaxf(st.m, most - set_at<kQ8>()) : st.m;
+    const float m_new = st.open || over || ask > st.m + (most_sum_log2<kQ8>() - 6 - set_at<kQ8>()) ? fmaxf(st.m, ask) : st.m;
     const float alpha = st.fresh || st.m == m_new ? 1.0f : ex2_approx(st.m - m_new);
     st.m = m_new;
     st.open = __any_sync(0xffffffffu, st.m == -INFINITY);  // the same in both warps of the rows

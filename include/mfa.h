@@ -286,7 +286,7 @@ mfa_status_t mfa_kv_read_fp4(const void* k_cache, const void* v_cache, const flo
  * the rows of a request that mfa_reserve_pages left as it was are written, but
  * hold attention of its last positions, or these. Nothing that a token does not see reaches its results, not even a NaN or an
  * infinity. Repeated calls give the same bits. On a bf16 cache no finite V gives an
- * infinite output; values of V below 2^-88 may lose bits.
+ * infinite output; values of V below 2^-110 may lose bits.
  * workspace: [device] at least mfa_chunk_workspace_bytes(batch, max_tokens)
  * bytes (about 40 MB, whatever the sizes), initialised once by
  * mfa_workspace_init; calls that share one must not overlap on the GPU.

@@ -47,7 +47,7 @@ def test_long_contexts(new, held, kv):
 
 
 # ---------------------------------------------------------------- values of any size
-@pytest.mark.parametrize("power", [-90, -40, 40, 90, 110, 127])
+@pytest.mark.parametrize("power", [-108, -90, -40, 40, 90, 110, 127])
 @pytest.mark.parametrize("rise", [0.0, 9.0, 14.0, 16.5, 30.0, -30.0])
 @pytest.mark.parametrize("new,held", [(5, 40000), (70, 300), (304, 30000)])
 def test_values_of_any_size(new, held, rise, power):
@@ -67,6 +67,27 @@ def test_values_of_any_size(new, held, rise, power):
         s.out[:new - 4] = 7.0
         s.lse[:new - 4] = 7.0
     s.check()
+
+
+@pytest.mark.parametrize("steps", [1, 7, 90])
+def test_sums_near_what_moves_a_reference(steps):
+    """Weights that grow by 2^20 in all, in steps between whole units: each unit's sum, and what the units before it left, is near
+    what moves the reference (a weight of 2^-9 each), behind it again, and much smaller ones follow to the end."""
+    s = Step([9, 304], [60000, 9000], seed=35)
+    for b in range(2):
+        n = int(s.lens[b])
+        unit = torch.arange(n, device="cuda") // 128
+        logits = LN2 * (20.0 * (unit.clamp(max=steps) / steps) - 45.0 * (unit > 2 * steps))
+        logits += 0.3 * torch.randn(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(steps))
+        _with_logits(s, b, logits)
+    s.cache[1] *= 2.0 ** 124
+    s.call()
+    s.check(which=[0])
+    s.starts[1], s.new[1] = int(s.starts[2]) - 4, 4
+    out, lse, top, _ = s.reference(1)
+    got, got_lse = s.out[s.starts[1]:s.starts[2]].double(), s.lse[s.starts[1]:s.starts[2]].double()
+    assert ((got - out).abs() <= 2 ** -8 * (top + out.abs()) + 2 ** -12 * top).all()
+    assert float((got_lse - lse).abs().max()) <= 1e-3
 
 
 @pytest.mark.parametrize("sigma", [1.0, 4.0])
