@@ -59,7 +59,7 @@
 // tile begins; V's codes times their scales become f16, and P is f16 as well (the
 // shared-prefix kernel says why).
 //
-// Measured, combine included: 2048 tokens behind 63488 in 4.65 ms called back to back (1860 TFLOP/s; cuBLAS reaches 1896 in a
+// Measured, combine included: 2048 tokens behind 63488 in 4.65 to 4.7 ms called back to back (1840 to 1860 TFLOP/s; cuBLAS reaches 1896 in a
 // burst, 1707 for seconds), the tensor cores 98% busy; 304 behind 16080 in 165 us, E4M3 174, E2M1 168 (replayed from graphs, as
 // the following). A unit takes the 2050 cycles of its MMAs; what is lost between two tiles is 0.4 us for long tiles, and 2.6 us for
 // the tiles of 2.5 units that 512-token prompts have (16 of them 161 us: a chain of Q and K from L2, 2 us each under load, the
